@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(_PKG, "libgar.so")
 
 GAR_OK, GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_EOVERFLOW, GAR_ECUDA = 0, -1, -2, -3, -4, -5
 GAR_F32, GAR_BF16 = 0, 1
+GAR_F8E4M3, GAR_F8E5M2 = 0, 1
 GAR_SUM, GAR_AVG = 0, 1
 GAR_MAX_WORKERS = 64
 
@@ -91,6 +92,16 @@ _SIGNATURES = {
     "gar_nmse_noalloc": (C.c_int, [_vp, _vp, _i64, _vp, _vp]),
     "gar_nmse_sums": (C.c_int, [_vp, _vp, _i64, _vp, _vp, C.c_size_t, _vp]),
     "gar_nmse_combine": (C.c_int, [_vp, _i32, _vp, _vp]),
+    "gar_fp8_scale_bytes": (_i64, [_i64, _i64]),
+    "gar_fp8_quantize": (C.c_int, [_vp, _i32, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp]),
+    "gar_fp8_matmul": (C.c_int, [_vp, _i64, _vp, _i32, _vp, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64,
+                                 _i32, _vp]),
+    "gar_distill_loss": (C.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i32, C.c_float, _vp, _vp, _vp, _vp, _i64,
+                                   _vp]),
+    "gar_distill_grad": (C.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i32, C.c_float, _vp, _vp, _vp, _i64, _vp]),
+    "gar_balance_workspace_bytes": (C.c_size_t, [_i32]),
+    "gar_balance_loss": (C.c_int, [_pp, _i32, _i64, _i32, _i64, _i32, _i32, _pp, C.c_float, _pp, _vp, _vp, _pp, _i64,
+                                   _vp, C.c_size_t, _vp]),
 }
 
 
@@ -359,6 +370,7 @@ def gar_fused_allreduce_range(src, dst, plan: FusionPlan, d_mM, op: int = GAR_AV
 
 
 GAR_STATUS_NONFINITE = 1
+GAR_STATUS_TIMEOUT = 2
 
 
 def gar_checksum(words, d_out, stream=None):
@@ -612,6 +624,174 @@ def gar_nmse_noalloc(x, x_hat, d_out, stream=None):
     _call("gar_nmse_noalloc", _dev(x), _dev(x_hat), x.numel(), _dev(d_out), _stream(stream))
 
 
+# ------------------------------------- a worker's products and losses: 8-bit
+def fp8_matrix(rows: int, cols: int, dtype=None, device="cuda"):
+    """(codes, scales) of a rows x cols block-scaled 8-bit matrix, uninitialised:
+    codes are a [rows, cols] view (torch.float8_e4m3fn unless ``dtype`` is
+    float8_e5m2) whose rows start on 16 bytes, scales uint8 [ceil(cols / 512),
+    rows, 4]."""
+    import torch
+
+    ld = (cols + 15) // 16 * 16
+    codes = torch.empty((rows, ld), dtype=torch.uint8, device=device).view(dtype or torch.float8_e4m3fn)[:, :cols]
+    return codes, torch.empty(((cols + 511) // 512, rows, 4), dtype=torch.uint8, device=device)
+
+
+def _matrix(t, name, shape=None):
+    """(pointer, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise GarError(GAR_EINVAL, f"{name} has shape {tuple(t.shape)}, not {shape or 'two dimensions'}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise GarError(GAR_EINVAL, f"{name}: the elements of a row are not contiguous")
+    # the stride of a single row means nothing: any that the library accepts will do
+    return _dev(t), t.stride(0) if rows > 1 else (max(cols, 1) + 15) // 16 * 16
+
+
+def _vector(t, name, dtype, n):
+    if t.dtype != dtype:
+        raise GarError(GAR_EDTYPE, f"{name} is {t.dtype}, not {dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise GarError(GAR_EINVAL, f"{name} is not a contiguous tensor of {n} elements")
+    return _dev(t)
+
+
+def _fp8_code(t, name) -> int:
+    import torch
+
+    if t.dtype == torch.float8_e4m3fn:
+        return GAR_F8E4M3
+    if t.dtype == torch.float8_e5m2:
+        return GAR_F8E5M2
+    raise GarError(GAR_EDTYPE, f"{name} is {t.dtype}, not float8_e4m3fn or float8_e5m2")
+
+
+def gar_fp8_scale_bytes(rows: int, cols: int) -> int:
+    return int(load().gar_fp8_scale_bytes(rows, cols))
+
+
+def gar_fp8_quantize(x, q, scale, qt=None, scale_t=None, square: bool = False, stream=None):
+    """Codes and scales of x [rows, cols] (fp32 or bf16): q [rows, cols] with
+    ``scale``, and/or qt [cols, rows], the transpose's, with ``scale_t`` (see
+    fp8_matrix; either pair may be None).  square: 128 x 128 blocks instead of
+    128 along the summed axis."""
+    import torch
+
+    rows, cols = x.shape
+    xp, ldx = _matrix(x, "x")
+    fmt, args = None, []
+    for name, codes, s, shape in (("q", q, scale, (rows, cols)), ("qt", qt, scale_t, (cols, rows))):
+        if codes is None:
+            args += [None, 0, None]
+            continue
+        f = _fp8_code(codes, name)
+        if fmt is not None and f != fmt:
+            raise GarError(GAR_EDTYPE, "q and qt have different formats")
+        fmt = f
+        ptr, ld = _matrix(codes, name, shape)
+        args += [ptr, ld, None if s is None else
+                 _vector(s, f"scales of {name}", torch.uint8, (shape[1] + 511) // 512 * shape[0] * 4)]
+    _call("gar_fp8_quantize", xp, _dtype_code(x), rows, cols, ldx, fmt or 0, int(bool(square)), *args, _stream(stream))
+
+
+def gar_fp8_matmul(a, a_scale, b, b_scale, d, c=None, stream=None):
+    """d = a b^T (+ c): a [M, K] and b [N, K] codes with their scales, d [M, N]
+    fp32 or bf16, c of d's type (it may be d)."""
+    import torch
+
+    (M, K), N = a.shape, b.shape[0]
+    ap, lda = _matrix(a, "a")
+    bp, ldb = _matrix(b, "b", (N, K))
+    dp, ldd = _matrix(d, "d", (M, N))
+    words = (K + 511) // 512 * 4
+    asp = _vector(a_scale, "scales of a", torch.uint8, words * M)
+    bsp = _vector(b_scale, "scales of b", torch.uint8, words * N)
+    cp, ldc = None, 0
+    if c is not None:
+        if c.dtype != d.dtype:
+            raise GarError(GAR_EDTYPE, f"c is {c.dtype}, d {d.dtype}")
+        cp, ldc = _matrix(c, "c", (M, N))
+    _call("gar_fp8_matmul", ap, lda, asp, _fp8_code(a, "a"), bp, ldb, bsp, _fp8_code(b, "b"), M, N, K, cp, ldc, dp, ldd,
+          _dtype_code(d), _stream(stream))
+
+
+def _distill_args(z, index, teacher, tau, weight, dz):
+    import torch
+
+    rows, vocab = z.shape
+    k = index.shape[-1]
+    zp, ldz = _matrix(z, "z")
+    dzp, lddz = None, 0
+    if dz is not None:
+        if dz.dtype != z.dtype:
+            raise GarError(GAR_EDTYPE, f"dz is {dz.dtype}, z {z.dtype}")
+        dzp, lddz = _matrix(dz, "dz", (rows, vocab))
+    head = [zp, _dtype_code(z), rows, vocab, ldz, _vector(index, "index", torch.int32, rows * k),
+            _vector(teacher, "teacher", torch.float32, rows * k), k, float(tau),
+            None if weight is None else _vector(weight, "weight", torch.float32, rows)]
+    return rows, head, dzp, lddz
+
+
+def gar_distill_loss(z, index, teacher, tau: float, loss, lse, dz=None, weight=None, stream=None):
+    """Distillation loss of student logits z [rows, vocab] against the teacher's
+    top logits (index, teacher [rows, k]) at temperature tau: loss and lse
+    [rows], and the gradient dz (z's type; may be z) under the rows' weights."""
+    import torch
+
+    rows, head, dzp, lddz = _distill_args(z, index, teacher, tau, weight, dz)
+    _call("gar_distill_loss", *head, _vector(loss, "loss", torch.float32, rows), _vector(lse, "lse", torch.float32, rows),
+          dzp, lddz, _stream(stream))
+
+
+def gar_distill_grad(z, index, teacher, tau: float, lse, dz, weight=None, stream=None):
+    """The gradient of gar_distill_loss alone, from its lse."""
+    import torch
+
+    rows, head, dzp, lddz = _distill_args(z, index, teacher, tau, weight, dz)
+    _call("gar_distill_grad", *head, _vector(lse, "lse", torch.float32, rows), dzp, lddz, _stream(stream))
+
+
+def gar_balance_workspace_bytes(P: int) -> int:
+    return int(load().gar_balance_workspace_bytes(P))
+
+
+def gar_balance_loss(z, k: int, alpha: float, choice, counts, loss, workspace, dz=None, valid=None, stream=None):
+    """A router's choices, counts and balance loss over P workers.  z[w]
+    [tokens, experts] logits, choice[w] [tokens, k] int32 out, counts [P,
+    experts] int32 out, loss one fp32 out, dz[w] of z's type out (may be z[w]),
+    valid[w] [tokens] uint8 or bool.  Lists or PtrTables; a list's tensors are
+    checked one by one, a PtrTable's by its first."""
+    import torch
+
+    zt, ct, dt, vt = [pointer_table(t) if t is not None else None for t in (z, choice, dz, valid)]
+    P, (tokens, experts) = len(zt), zt.first.shape
+    _, ldz = _matrix(zt.first, "z[0]")
+    code = _dtype_code(zt.first)
+    lddz = 0
+    for name, given, t, dtype, shape in (("z", z, zt, zt.first.dtype, (tokens, experts)),
+                                         ("choice", choice, ct, torch.int32, (tokens, k)),
+                                         ("dz", dz, dt, zt.first.dtype, (tokens, experts)),
+                                         ("valid", valid, vt, None, (tokens,))):
+        if t is None:
+            continue
+        if len(t) != P:
+            raise GarError(GAR_EINVAL, f"{name} has {len(t)} tensors, z {P}")
+        for x in t.tensors[:1] if isinstance(given, PtrTable) else t.tensors:
+            if tuple(x.shape) != shape or (x.stride() != t.first.stride() and tokens > 1):
+                raise GarError(GAR_EINVAL, f"{name} has a tensor of shape {tuple(x.shape)}, not {shape}, or strides that differ")
+            if x.dtype != dtype if dtype is not None else x.element_size() != 1:
+                raise GarError(GAR_EDTYPE, f"{name} is {x.dtype}")
+            if name in ("choice", "valid") and not x.is_contiguous():
+                raise GarError(GAR_EINVAL, f"{name} is not contiguous")
+    if dt is not None:
+        _, lddz = _matrix(dt.first, "dz[0]")
+    _call("gar_balance_loss", zt.array, P, tokens, experts, ldz, code, k, vt.array if vt is not None else None,
+          float(alpha), ct.array, _vector(counts, "counts", torch.int32, P * experts),
+          _vector(loss, "loss", torch.float32, 1), dt.array if dt is not None else None, lddz, _dev(workspace),
+          workspace.numel() * workspace.element_size(), _stream(stream))
+
+
 __all__ = [n for n in dir() if n.startswith(("gar_", "GAR_"))] + ["GarError", "FusionPlan", "PtrTable", "load",
                                                                     "pointer_table", "fused_pointer_tables", "thc_plan_tables",
+                                                                    "fp8_matrix",
                                                                     "Timeline", "timeline"]

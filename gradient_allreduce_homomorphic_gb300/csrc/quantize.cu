@@ -1,0 +1,272 @@
+// quantize.cu -- block-scaled 8-bit floating point: gar_fp8_quantize.
+//
+// A block of 128 values (128 consecutive ones along the axis that a product
+// will sum over, or a 128 x 128 square) shares the power-of-two scale 2^k,
+// k the smallest integer with amax <= FMAX 2^k (amax over the block's finite
+// values, FMAX = 448 for e4m3, 57344 for e5m2; both are 1.75 times a power of
+// two, so k follows from amax's exponent and one comparison of its
+// significand).  Codes are x 2^-k rounded to nearest even: the product with a
+// power of two is exact, so this is the only rounding.  A power of two rather
+// than amax / FMAX costs at most one binade of the format's 15 (e4m3) or 30
+// (e5m2) and nothing in relative precision above its subnormals, and it is
+// the scale type that the tensor core applies by itself.
+#include "common.cuh"
+#include "fp8.cuh"
+
+namespace gar {
+namespace {
+
+constexpr int kTile = 128;  // rows and columns of one CTA's tile
+constexpr int kThreads = 256;
+
+struct QuantizeParams {
+    const void *x;
+    int64_t rows, cols, ldx;
+    uint8_t *q, *qt;          // either may be NULL
+    int64_t ldq, ldqt;
+    uint8_t *scale, *scale_t;
+    int64_t tiles_c;
+    int32_t emax;  // 8 (e4m3) or 15 (e5m2): FMAX = 1.75 * 2^emax
+    int32_t square, vec;
+};
+
+// |v|'s bits, 0 for NaN and infinities.
+__device__ __forceinline__ uint32_t finite_abs(float v) {
+    const uint32_t a = __float_as_uint(v) & 0x7FFFFFFFu;
+    return a < 0x7F800000u ? a : 0u;
+}
+// Biased exponent of the scale from amax's bits: the addition carries into the
+// exponent exactly where the significand is above 1.75.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax, int emax) {
+    const int e = static_cast<int>((amax + 0x1FFFFFu) >> 23) - emax;
+    return static_cast<uint32_t>(e < 1 ? 1 : e);
+}
+// 2^(127 - byte), exact: byte is at most 247.
+__device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+template <bool kE5M2>
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    if (kE5M2) {
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    } else {
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    }
+    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// One CTA per 128 x 128 tile, x read once for both orders.  Each half-warp
+// owns 8 consecutive rows and each of its lanes 8 consecutive columns, so a
+// row's maximum is a shuffle over 16 lanes, a column's is a maximum over the
+// thread's 8 rows and then over the 16 half-warps through shared memory, and
+// a thread's 8 codes of a column are 8 consecutive bytes of the transposed
+// tile.  The transposed tile goes through shared memory; its 8-byte groups
+// are exchanged (group h of column c sits at h ^ (c / 8)) so that neither the
+// stores nor the loads conflict.
+template <typename T, bool kE5M2>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constant__ QuantizeParams p) {
+    __shared__ uint32_t colmax[16][kTile];
+    __shared__ __align__(16) uint8_t tile[kTile * kTile];
+    __shared__ uint32_t wmax[kThreads / 32];
+    const int tid = threadIdx.x, half = tid >> 4, hl = tid & 15;
+    const int64_t tr = blockIdx.x / p.tiles_c, tc = blockIdx.x % p.tiles_c;
+    const int64_t row0 = tr * kTile + half * 8, col0 = tc * kTile + hl * 8;
+    const T *x = static_cast<const T *>(p.x);
+    float v[8][8];
+    const int64_t left = p.cols - col0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = row0 + i;
+        const T *src = x + r * p.ldx + col0;
+        if (p.vec && r < p.rows && left >= 8) {
+            if (sizeof(T) == 2) {
+                const uint4 g = ld16(src);
+                v[i][0] = bf16_lo(g.x), v[i][1] = bf16_hi(g.x), v[i][2] = bf16_lo(g.y), v[i][3] = bf16_hi(g.y);
+                v[i][4] = bf16_lo(g.z), v[i][5] = bf16_hi(g.z), v[i][6] = bf16_lo(g.w), v[i][7] = bf16_hi(g.w);
+            } else {
+                const uint4 g = ld16(src), h = ld16(src + 4);
+                v[i][0] = __uint_as_float(g.x), v[i][1] = __uint_as_float(g.y);
+                v[i][2] = __uint_as_float(g.z), v[i][3] = __uint_as_float(g.w);
+                v[i][4] = __uint_as_float(h.x), v[i][5] = __uint_as_float(h.y);
+                v[i][6] = __uint_as_float(h.z), v[i][7] = __uint_as_float(h.w);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = r < p.rows && j < left ? load_f32(src + j) : 0.0f;
+        }
+    }
+    uint32_t rmax[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, finite_abs(v[i][j]));
+        rmax[i] = m;
+    }
+    uint32_t cbyte[8], rbyte[8];
+    if (p.square) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, rmax[i]);
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if ((tid & 31) == 0) wmax[tid >> 5] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) m = max(m, wmax[w]);
+        const uint32_t b = scale_byte(m, p.emax);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rbyte[i] = cbyte[i] = b;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t m = rmax[i];
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            rbyte[i] = scale_byte(m, p.emax);
+        }
+        if (p.qt) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = max(m, finite_abs(v[i][j]));
+                colmax[half][hl * 8 + j] = m;
+            }
+            __syncthreads();
+            if (tid < kTile) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int h = 0; h < 16; ++h) m = max(m, colmax[h][tid]);
+                colmax[0][tid] = m;  // only this thread reads or writes this column here
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) cbyte[j] = scale_byte(colmax[0][hl * 8 + j], p.emax);
+        }
+    }
+    // an infinity times zero makes it a NaN, whose code is the format's NaN
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = __fmaf_rn(v[i][j], 0.0f, v[i][j]);
+
+    if (p.q) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = row0 + i;
+            const float f = inverse_scale(rbyte[i]);
+            uint2 w;
+            w.x = pack4<kE5M2>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f);
+            w.y = pack4<kE5M2>(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f);
+            if (r < p.rows) {
+                uint8_t *dst = p.q + r * p.ldq + col0;
+                if (left >= 8) {
+                    *reinterpret_cast<uint2 *>(dst) = w;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < left) dst[j] = static_cast<uint8_t>((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+                }
+                if (hl == 0) store_scale(p.scale, p.rows, r, tc, p.tiles_c, rbyte[i]);
+            }
+        }
+    }
+    if (p.qt) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float f = inverse_scale(cbyte[j]);
+            uint2 w;
+            w.x = pack4<kE5M2>(v[0][j] * f, v[1][j] * f, v[2][j] * f, v[3][j] * f);
+            w.y = pack4<kE5M2>(v[4][j] * f, v[5][j] * f, v[6][j] * f, v[7][j] * f);
+            *reinterpret_cast<uint2 *>(&tile[(hl * 8 + j) * kTile + ((half ^ hl) << 3)]) = w;
+        }
+        const int64_t tiles_r = (p.rows + kTile - 1) / kTile;
+        if (half == 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < left) store_scale(p.scale_t, p.cols, col0 + j, tr, tiles_r, cbyte[j]);
+        }
+        __syncthreads();
+        const int part = tid & 7;  // 16 bytes of a column: row groups 2 part and 2 part + 1
+        const int64_t r = tr * kTile + part * 16;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int c = k * 32 + (tid >> 3);
+            const int64_t cg = tc * kTile + c;
+            const int f = c >> 3;
+            uint4 g = *reinterpret_cast<const uint4 *>(&tile[c * kTile + (((2 * part) ^ (f & ~1)) << 3)]);
+            if (f & 1) g = make_uint4(g.z, g.w, g.x, g.y);
+            if (cg >= p.cols || r >= p.rows) continue;
+            uint8_t *dst = p.qt + cg * p.ldqt + r;
+            if (r + 16 <= p.rows) {
+                *reinterpret_cast<uint4 *>(dst) = g;
+            } else {
+                const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                for (int b = 0; b < 16; ++b)
+                    if (r + b < p.rows) dst[b] = static_cast<uint8_t>(w[b >> 2] >> (8 * (b & 3)));
+            }
+        }
+    }
+}
+
+template <typename T>
+void launch(const QuantizeParams &p, unsigned blocks, cudaStream_t stream) {
+    if (p.emax == 15)
+        quantize_kernel<T, true><<<blocks, kThreads, 0, stream>>>(p);
+    else
+        quantize_kernel<T, false><<<blocks, kThreads, 0, stream>>>(p);
+}
+
+int check_codes(const char *name, const void *q, int64_t ld, int64_t cols, const void *scale) {
+    if (!scale) return fail(GAR_EINVAL, "%s is given without its scales", name);
+    if (ld < cols) return fail(GAR_EINVAL, "%s: row stride %lld < %lld columns", name, static_cast<long long>(ld),
+                               static_cast<long long>(cols));
+    if (!aligned(q, 16) || ld % 16 || !aligned(scale, 4))
+        return fail(GAR_EALIGN, "%s: codes and their row stride need 16-byte alignment, scales 4-byte", name);
+    return GAR_OK;
+}
+
+}  // namespace
+}  // namespace gar
+
+using namespace gar;
+
+extern "C" int64_t gar_fp8_scale_bytes(int64_t rows, int64_t cols) {
+    return rows < 0 || cols < 0 ? 0 : ceil_div(cols, 512) * rows * 4;
+}
+
+extern "C" int gar_fp8_quantize(const void *x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, int32_t format,
+                                int32_t square, uint8_t *q, int64_t ldq, uint8_t *scale, uint8_t *qt, int64_t ldqt,
+                                uint8_t *scale_t, gar_stream_t stream_) {
+    if (rows < 0 || cols < 0 || rows > 0x7FFFFFFF || cols > 0x7FFFFFFF)
+        return fail(GAR_EINVAL, "rows=%lld cols=%lld", static_cast<long long>(rows), static_cast<long long>(cols));
+    if (elem_bytes(dtype) < 0) return fail(GAR_EDTYPE, "unknown dtype %d", dtype);
+    if (format != GAR_F8E4M3 && format != GAR_F8E5M2) return fail(GAR_EDTYPE, "unknown 8-bit format %d", format);
+    if (!q && !qt) return fail(GAR_EINVAL, "neither q nor qt is given");
+    if (rows == 0 || cols == 0) return GAR_OK;
+    if (!x || ldx < cols) return fail(GAR_EINVAL, "x is NULL or its row stride is below its columns");
+    if (!aligned(x, elem_bytes(dtype))) return fail(GAR_EALIGN, "x is misaligned");
+    if (q)
+        if (int rc = check_codes("q", q, ldq, cols, scale)) return rc;
+    if (qt)
+        if (int rc = check_codes("qt", qt, ldqt, rows, scale_t)) return rc;
+    const int64_t tiles_r = ceil_div(rows, kTile), tiles_c = ceil_div(cols, kTile);
+    if (tiles_r * tiles_c > 0x7FFFFFFF) return fail(GAR_EINVAL, "the matrix has too many tiles");
+    QuantizeParams p{};
+    p.x = x, p.rows = rows, p.cols = cols, p.ldx = ldx;
+    p.q = q, p.ldq = ldq, p.scale = scale, p.qt = qt, p.ldqt = ldqt, p.scale_t = scale_t;
+    p.tiles_c = tiles_c;
+    p.emax = format == GAR_F8E5M2 ? 15 : 8;
+    p.square = square ? 1 : 0;
+    p.vec = aligned(x, 16) && (ldx * elem_bytes(dtype)) % 16 == 0;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const unsigned blocks = static_cast<unsigned>(tiles_r * tiles_c);
+    if (dtype == GAR_F32)
+        launch<float>(p, blocks, stream);
+    else
+        launch<uint16_t>(p, blocks, stream);
+    return check_launch("quantize_kernel");
+}

@@ -74,9 +74,14 @@ typedef enum {
 
 typedef enum { GAR_F32 = 0, GAR_BF16 = 1 } gar_dtype;
 
+/* 8-bit floating-point formats of codes: 4 exponent and 3 significand bits
+ * (largest value 448, no infinities) or 5 and 2 (57344). */
+typedef enum { GAR_F8E4M3 = 0, GAR_F8E5M2 = 1 } gar_f8_format;
+
 /* Bits of the device status word (gar_sync_status). */
 typedef enum {
-    GAR_STATUS_NONFINITE = 1 /* a THC range pass saw a NaN or an infinite input */
+    GAR_STATUS_NONFINITE = 1, /* a THC range pass saw a NaN or an infinite input */
+    GAR_STATUS_TIMEOUT = 2    /* a wait inside gar_fp8_matmul ran out: its result is not valid */
 } gar_device_status;
 typedef enum { GAR_SUM = 0, GAR_AVG = 1 } gar_op;
 
@@ -649,6 +654,126 @@ int gar_nmse_combine(const double *d_pairs, int32_t n, double *d_out, gar_stream
  * at zero); calls that overlap on the GPU, e.g. on two streams, race.
  * Errors: GAR_EINVAL (null, N < 0), GAR_EALIGN, GAR_ECUDA. */
 int gar_nmse_noalloc(const float *x, const float *x_hat, int64_t N, double *d_out,
+                     gar_stream_t stream);
+
+/* ===================================================================== */
+/* What a worker computes before its gradients are averaged: 8-bit        */
+/* products, distillation, the router's balance loss.  No counterpart in  */
+/* the pages; formulas stand with each call.                              */
+/* ===================================================================== */
+
+/* Block-scaled 8-bit matrices.  A matrix of `rows` rows and `cols` columns is
+ * held as codes (one byte each, row stride ld bytes) and scale bytes: 128
+ * consecutive columns of a row are a block, and the value of a code in a block
+ * with scale byte s is code * 2^(s - 127), 1 <= s <= 254.  The scale byte of
+ * block j of row r is at ((j / 4) * rows + r) * 4 + j % 4; blocks of the last
+ * group of four that do not exist hold 1.  Codes are 16-byte aligned with ld a
+ * multiple of 16, scales 4-byte aligned. */
+
+/* Bytes of the scales of a rows x cols matrix: ceil(cols / 512) * rows * 4. */
+int64_t gar_fp8_scale_bytes(int64_t rows, int64_t cols);
+
+/* gar_fp8_quantize -- 8-bit codes and scales of x, in either or both orders,
+ * reading x once.  The scale of a block is the smallest power of two 2^k with
+ * amax <= FMAX 2^k (amax over the block's finite values, FMAX 448 or 57344;
+ * k >= -126), a code x 2^-k rounded to nearest even.  NaN and infinities
+ * become the code NaN (0x7F).
+ *   x            device, rows x cols fp32 or bf16 (dtype), row stride ldx
+ *   format       gar_f8_format
+ *   square       0: blocks of 128 along the summed axis of each order (q: of a
+ *                row's columns; qt: of a column's rows); else 128 x 128 squares,
+ *                one scale for both orders
+ *   q, scale     codes of x [rows, cols] (row stride ldq) and their scales, or
+ *                both NULL
+ *   qt, scale_t  codes of the transpose [cols, rows] (row stride ldqt) and
+ *                their scales, or both NULL
+ * Outputs must not overlap x or one another.  Bytes of a row of codes past its
+ * last column are not written.
+ * Errors: GAR_EINVAL (sizes, strides, NULL), GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA. */
+int gar_fp8_quantize(const void *x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, int32_t format,
+                     int32_t square, uint8_t *q, int64_t ldq, uint8_t *scale, uint8_t *qt, int64_t ldqt,
+                     uint8_t *scale_t, gar_stream_t stream);
+
+/* gar_fp8_matmul -- d = a b^T (+ c) of block-scaled 8-bit matrices: a [M, K],
+ * b [N, K], d [M, N], each with its own format.  Products are exact, sums and
+ * scales in fp32, one rounding to d's type.  With x and w quantized in both
+ * orders this gives a linear layer's forward product (x, w), its input
+ * gradient (dy, w's transpose) and its weight gradient (dy's transpose, x's
+ * transpose, c = d to accumulate).
+ *   c            device, [M, N] of d's type, added to the product; NULL: none;
+ *                may be d itself (same row stride)
+ *   d            device, fp32 or bf16 (dtype), row stride ldd
+ * A code NaN makes its row (of a) or column (of b) of d NaN.  A scale byte of
+ * 255 counts as NaN.  The result does not depend on timing.  With K = 0, d is
+ * c or 0.
+ * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA; on the device
+ * GAR_STATUS_TIMEOUT (a wait inside the kernel ran out of its two seconds). */
+int gar_fp8_matmul(const uint8_t *a, int64_t lda, const uint8_t *a_scale, int32_t a_format, const uint8_t *b,
+                   int64_t ldb, const uint8_t *b_scale, int32_t b_format, int64_t M, int64_t N, int64_t K,
+                   const void *c, int64_t ldc, void *d, int64_t ldd, int32_t dtype, gar_stream_t stream);
+
+/* gar_distill_loss -- cross entropy of a student against a teacher's top
+ * logits, less the teacher's entropy, and its gradient.  For each row,
+ *   p    = softmax of teacher / tau over the row's present entries
+ *   lse  = log sum_v exp(z_v / tau)
+ *   loss = sum_j p_j (log p_j + lse - z_{index_j} / tau)
+ *   dz_v = weight / tau * (exp(z_v / tau - lse) - sum of p_j with index_j = v)
+ * An entry is present if its index lies in [0, vocab) and its logit is above
+ * -inf; an index may occur more than once.  A row of weight 0 or without an
+ * entry has loss 0, lse 0 and gradient 0, and its z is not read.  A student
+ * logit of -inf has probability 0 (loss +inf where the teacher gives it any).
+ *   z            device, rows x vocab fp32 or bf16 (dtype), row stride ldz
+ *   index        device, [rows, k] int32, 1 <= k <= 1024
+ *   teacher      device, [rows, k] fp32 logits
+ *   weight       device, [rows] fp32: the gradient of the total loss with
+ *                respect to each row's (tau^2 / rows for the mean scaled by
+ *                tau^2); NULL: 1
+ *   loss, lse    device, out, [rows] fp32
+ *   dz           device, out, of z's type, row stride lddz; NULL: loss only;
+ *                may be z itself (same row stride)
+ * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA. */
+int gar_distill_loss(const void *z, int32_t dtype, int64_t rows, int64_t vocab, int64_t ldz, const int32_t *index,
+                     const float *teacher, int32_t k, float tau, const float *weight, float *loss, float *lse,
+                     void *dz, int64_t lddz, gar_stream_t stream);
+
+/* gar_distill_grad -- the gradient alone, from the lse that gar_distill_loss
+ * wrote for the same rows.  A row that was without weight then must be without
+ * weight now.  Arguments and errors as there. */
+int gar_distill_grad(const void *z, int32_t dtype, int64_t rows, int64_t vocab, int64_t ldz, const int32_t *index,
+                     const float *teacher, int32_t k, float tau, const float *weight, const float *lse, void *dz,
+                     int64_t lddz, gar_stream_t stream);
+
+/* Bytes of device workspace gar_balance_loss needs. */
+size_t gar_balance_workspace_bytes(int32_t P);
+
+/* gar_balance_loss -- top-k choices, per-expert counts and balance loss of a
+ * router over the tokens of P workers, with its gradient.  Each token that
+ * counts (valid, some logit above -inf) chooses its k largest logits (equal
+ * ones: the lowest expert first; NaN and -inf are never chosen, missing choices
+ * are -1).  With c_e the choices of expert e over all workers, N the tokens
+ * that count and p = softmax(z) of each,
+ *   loss   = alpha E sum_e (c_e / (k N)) (sum_t p_te / N)
+ *   dz_te  = alpha E / (k N^2) p_te (c_e - sum_j p_tj c_j)
+ * (alpha for a balanced router; 0 with no token).  This is the gradient of the
+ * loss over all workers' tokens: where worker gradients are averaged rather
+ * than summed, pass P alpha.
+ *   z            host array of P device pointers, tokens x experts fp32 or bf16
+ *                (dtype), row stride ldz
+ *   experts, k   1 <= k <= min(32, experts), experts <= 1024
+ *   valid        host array of P device pointers, [tokens] bytes (0: the token
+ *                is padding); NULL: every token is valid
+ *   choice       host array of P device pointers, out, [tokens, k] int32, in
+ *                falling order of logit (padding: -1)
+ *   counts       device, out, [P, experts] int32
+ *   loss         device, out, one fp32
+ *   dz           host array of P device pointers, out, of z's type, row stride
+ *                lddz (padding: 0); NULL: no gradient; an entry may be that z
+ *   d_workspace  device, gar_balance_workspace_bytes(P) bytes, 8-byte aligned,
+ *                not shared with a concurrent call
+ * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA. */
+int gar_balance_loss(const void *const *z, int32_t P, int64_t tokens, int32_t experts, int64_t ldz, int32_t dtype,
+                     int32_t k, const uint8_t *const *valid, float alpha, int32_t *const *choice, int32_t *counts,
+                     float *loss, void *const *dz, int64_t lddz, void *d_workspace, size_t workspace_bytes,
                      gar_stream_t stream);
 
 #ifdef __cplusplus
