@@ -72,6 +72,29 @@ __device__ __forceinline__ void store_out(const MatmulParams &p, int64_t m, int6
         static_cast<float *>(p.d)[i] = v;
 }
 
+// One lane's scale words of kAtoms tiles of 128 rows (w[a][q]: row 128 a + 32 q
+// + lane) to the order that the copy to tensor memory takes.
+template <int kAtoms>
+__device__ __forceinline__ void stage_scales(uint32_t dst, const uint32_t (&w)[kAtoms][4]) {
+#pragma unroll
+    for (int a = 0; a < kAtoms; ++a)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512 * a), "r"(w[a][0]), "r"(w[a][1]), "r"(w[a][2]),
+                     "r"(w[a][3])
+                     : "memory");
+    fence_async_shared();
+}
+
+// After a wait ran out: the copies into the last `issued` stages before stage
+// s (of the pass whose empty parity is turn) have to land before the CTA ends.
+__device__ __noinline__ void mbar_drain(uint32_t full, uint32_t stages, int issued, uint32_t s, uint32_t turn) {
+    for (; issued > 0; --issued) {
+        if (s == 0) s = stages, turn ^= 1;
+        --s;
+        int given_up = 0;
+        mbar_wait(full + 8 * s, turn ^ 1, &given_up);
+    }
+}
+
 template <int TM>
 __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant__ CUtensorMap map_n,
                                                           const __grid_constant__ CUtensorMap map_m,
@@ -103,78 +126,78 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const uint32_t sf_cols = tmem + TM;  // scale columns: kScaleBufs x (4 + 4 kAtomsB)
-    bool ok = true;
 
     if (warp == 0 && lane == 0) {
         tma_prefetch_map(&map_n);
         tma_prefetch_map(&map_m);
+        uint32_t s = 0, turn = 1;  // the first turn finds every stage free
         int issued = 0;
-        for (int c = c0; c < c1; ++c, ++issued) {
-            const int s = issued % S::kStages, turn = issued / S::kStages;
-            if (turn > 0 && !(ok = mbar_wait(empty + 8 * s, (turn - 1) & 1))) break;
+        bool ok = true;
+        for (int c = c0; c < c1; ++c) {
+            if (!(ok = mbar_wait(empty + 8 * s, turn, &failed))) break;
             const uint32_t dst = base + s * S::kStage;
             mbar_expect_tx(full + 8 * s, S::kStage);
             tma_load_2d(dst, &map_n, full + 8 * s, c * kKC, static_cast<int32_t>(n0));
             tma_load_2d(dst + S::kBytesA, &map_m, full + 8 * s, c * kKC, static_cast<int32_t>(m0));
+            issued = issued < S::kStages ? issued + 1 : S::kStages;
+            if (++s == S::kStages) s = 0, turn ^= 1;
         }
-        if (!ok)  // leave no copy in flight
-            for (int i = issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i)
-                mbar_wait(full + 8 * (i % S::kStages), (i / S::kStages) & 1);
-    } else if (warp == 1 && lane == 0) {
-        int i = 0, g = -1;
-        for (int c = c0; c < c1 && ok; ++c, ++i) {
-            const int s = i % S::kStages;
+        if (!ok) mbar_drain(full, S::kStages, issued, s, turn);
+    } else if (warp == 1) {
+        const uint64_t desc = smem_desc(base, 16, 1024, 2);
+        uint32_t s = 0, turn = 0, groups = 0, g = 0;
+        for (int c = c0; c < c1; ++c) {
             if (c == c0 || (c & 3) == 0) {
-                ++g;
-                const int b = g % kScaleBufs;
-                if (!(ok = mbar_wait(sf_full + 8 * b, (g / kScaleBufs) & 1))) break;
+                g = groups++;
+                const uint32_t b = g % kScaleBufs;
+                mbar_wait(sf_full + 8 * b, (g / kScaleBufs) & 1, &failed);
                 tc_fence_after();
-                const uint32_t src = scales + b * S::kScaleBuf, col = sf_cols + b * 4 * (1 + S::kAtomsB);
-                for (int a = 0; a < 1 + S::kAtomsB; ++a) tc_copy_scales<1>(col + 4 * a, src + 512 * a);
+                if (elect_one())
+                    for (int a = 0; a < 1 + S::kAtomsB; ++a)
+                        tc_copy_scales<1>(sf_cols + (b * (1 + S::kAtomsB) + a) * 4, scales + b * S::kScaleBuf + 512 * a);
+                __syncwarp();
             }
-            if (!(ok = mbar_wait(full + 8 * s, (i / S::kStages) & 1))) break;
+            mbar_wait(full + 8 * s, turn, &failed);
             tc_fence_after();
-            const uint32_t src = base + s * S::kStage;
-            const uint32_t col = sf_cols + (g % kScaleBufs) * 4 * (1 + S::kAtomsB);
-            const uint32_t idesc = p.idesc | mxf8_scale_byte(c & 3);
+            if (elect_one()) {
+                const uint64_t d = desc + s * (S::kStage >> 4);
+                const uint32_t col = sf_cols + (g % kScaleBufs) * 4 * (1 + S::kAtomsB);
+                const uint32_t idesc = p.idesc | mxf8_scale_byte(c & 3);
 #pragma unroll
-            for (int k = 0; k < kKC / 32; ++k)
-                tc_mma_mxf8<1>(tmem, smem_desc(src + 32 * k, 16, 1024, 2), smem_desc(src + S::kBytesA + 32 * k, 16, 1024, 2),
-                               idesc, col, col + 4, i > 0 || k > 0);
-            tc_commit(empty + 8 * s);
-            if ((c & 3) == 3 || c == c1 - 1) tc_commit(sf_empty + 8 * (g % kScaleBufs));
-        }
-        tc_commit(done);
-    } else if (warp == 2) {
-        int g = 0;
-        for (int j = c0 >> 2; c0 < c1 && j <= (c1 - 1) >> 2; ++j, ++g) {
-            const int b = g % kScaleBufs, turn = g / kScaleBufs;
-            if (turn > 0 && !(ok = mbar_wait(sf_empty + 8 * b, (turn - 1) & 1))) break;
-            const uint32_t dst = scales + b * S::kScaleBuf + lane * 16;
-#pragma unroll
-            for (int a = 0; a < 1 + S::kAtomsB; ++a) {
-                const uint32_t *src = a == 0 ? p.sb + static_cast<int64_t>(j) * p.N : p.sa + static_cast<int64_t>(j) * p.M;
-                const int64_t r0 = a == 0 ? n0 : m0 + (a - 1) * 128, rows = a == 0 ? p.N : p.M;
-                uint32_t w[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int64_t r = r0 + 32 * q + lane;
-                    w[q] = r < rows ? __ldg(src + r) : 0x01010101u;
-                }
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512 * a), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                             "r"(w[3])
-                             : "memory");
+                for (int k = 0; k < kKC / 32; ++k)
+                    tc_mma_mxf8<1>(tmem, d + 2 * k, d + (S::kBytesA >> 4) + 2 * k, idesc, col, col + 4, c > c0 || k > 0);
+                tc_commit(empty + 8 * s);
+                if ((c & 3) == 3 || c == c1 - 1) tc_commit(sf_empty + 8 * (g % kScaleBufs));
             }
-            fence_async_shared();
+            __syncwarp();
+            if (++s == S::kStages) s = 0, turn ^= 1;
+        }
+        if (elect_one()) tc_commit(done);
+        __syncwarp();
+    } else if (warp == 2) {
+        uint32_t g = 0;
+        for (int j = c0 >> 2; c0 < c1 && j <= (c1 - 1) >> 2; ++j, ++g) {
+            const uint32_t *sn = p.sb + static_cast<int64_t>(j) * p.N, *sm = p.sa + static_cast<int64_t>(j) * p.M;
+            uint32_t w[1 + S::kAtomsB][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t nr = n0 + 32 * q + lane, mr = m0 + 32 * q + lane;
+                w[0][q] = nr < p.N ? ldg_early(sn + nr) : 0x01010101u;
+#pragma unroll
+                for (int a = 0; a < S::kAtomsB; ++a) w[1 + a][q] = mr + 128 * a < p.M ? ldg_early(sm + mr + 128 * a) : 0x01010101u;
+            }
+            const uint32_t b = g % kScaleBufs;
+            mbar_wait(sf_empty + 8 * b, (g / kScaleBufs + 1) & 1, &failed);
+            __syncwarp();
+            stage_scales<1 + S::kAtomsB>(scales + b * S::kScaleBuf + lane * 16, w);
             __syncwarp();
             if (lane == 0) mbar_arrive(sf_full + 8 * b);
         }
     }
     if (warp >= 4) {
-        ok = mbar_wait(done, 0);
+        mbar_wait(done, 0, &failed);
         tc_fence_after();
     }
-    if (!ok) failed = 1;
     __syncwarp();
     const int quarter = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -233,6 +256,270 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
     __syncthreads();
     if (threadIdx.x == 0 && failed && p.status) atomicOr(p.status, static_cast<unsigned int>(GAR_STATUS_TIMEOUT));
     if (warp == 1) tmem_free<1>(tmem, S::kColumns);
+}
+
+// ---------------------------------------------------------------- CTA pairs
+// Large products: persistent pairs of CTAs (cta_group::2), each pair computing
+// tiles of 256 columns by TM rows of D.  A CTA holds 128 of the tile's columns
+// (its tensor-memory lanes) and loads, besides its own 128 rows of b, half of
+// the tile's TM rows of a, which both tensor cores then share: at TM = 256,
+// 32 KB of operands per CTA and 128 k instead of 48, so shared memory is
+// written and read at 64 bytes a clock each rather than 96.
+//
+// Two accumulators alternate, so the epilogue of a tile overlaps the products
+// of the next.  Tensor memory has 512 columns and the scales take 24 of them:
+// up to TM = 224 the accumulators lie side by side; at TM = 256 they overlap
+// by 32 columns (0..255 and 224..479), which the epilogue reads first and then
+// lets the next tile's products start.  TM is chosen so that the tiles fill
+// the SMs' last wave (pair_rows below).
+//
+// With an fp32 result, k is cut into segments of at most 8192 whose sums are
+// added in fp32: the tensor core's additions round toward zero, so its error
+// grows with the number of k it adds (measured against 64 bits: 2.6e-7 of the
+// result at 2048, 8e-7 at 8192).
+constexpr int kPairThreads = 384;  // warps 0-2 as above, 3 scale copies, 4-11 epilogue
+constexpr int kPairStages = 6;
+constexpr int kPairScaleBuf = 512 * 3;
+constexpr int kPairScaleBufs = 4;  // in shared memory; tensor memory has two
+constexpr int kPairScaleCols = 480;
+constexpr int kSegment = 64;  // chunks of 128 k
+
+struct PairParams {
+    MatmulParams mm;
+    int64_t tiles_m, tiles;
+    int32_t rows;  // TM
+    int32_t segments, seg_chunks;
+};
+
+__host__ __device__ constexpr int pair_stage(int rows) { return (128 + rows / 2) * kKC; }
+constexpr int pair_smem(int rows) { return 1024 + kPairStages * pair_stage(rows) + kPairScaleBufs * kPairScaleBuf; }
+
+// Tiles in the order they are handed out: runs of 8 tiles of rows by all tiles
+// of columns, so that the pairs working at one time share operands in L2.
+__device__ __forceinline__ void pair_tile(const PairParams &p, int64_t t, int64_t &m0, int64_t &n0) {
+    const int64_t per = 8 * static_cast<int64_t>(p.mm.tiles_n), g = t / per, in = t % per;
+    const int64_t rows = p.tiles_m - g * 8 < 8 ? p.tiles_m - g * 8 : 8;
+    m0 = (g * 8 + in % rows) * p.rows;
+    n0 = in / rows * 256;
+}
+
+// 32 accumulator columns to rows m .. of column n of D, c added where given.
+template <typename T>
+__device__ __forceinline__ void store32(const float (&v)[32], T *d, int64_t ldd, const T *c, int64_t ldc, int count) {
+    if (c) {
+        float x[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = j < count ? load_f32(c + j * ldc) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < count) store_f32(d + j * ldd, v[j] + x[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < count) store_f32(d + j * ldd, v[j]);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    matmul_pair_kernel(const __grid_constant__ CUtensorMap map_n, const __grid_constant__ CUtensorMap map_m,
+                       const __grid_constant__ PairParams pp) {
+    const MatmulParams &p = pp.mm;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kPairStages + 2 * kPairScaleBufs + 8];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int failed;
+    const uint32_t stage = pair_stage(pp.rows);
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t scales = base + kPairStages * stage;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kPairStages, sf_full = empty + 8 * kPairStages,
+                   sf_empty = sf_full + 8 * kPairScaleBufs, acc_full = sf_empty + 8 * kPairScaleBufs,
+                   drained = acc_full + 16, sf_ready = drained + 16, sf_done = sf_ready + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_cta_rank();
+    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const bool overlap = pp.rows == 256;
+    const uint32_t acc1 = overlap ? 224 : pp.rows;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * kPairStages; ++i) mbar_init(full + 8 * i, 1);
+        for (int i = 0; i < kPairScaleBufs; ++i) {
+            mbar_init(sf_full + 8 * i, 2);  // one staging warp of each CTA
+            mbar_init(sf_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(drained + 8 * i, 16);  // eight epilogue warps of each CTA
+            mbar_init(sf_ready + 8 * i, 1);
+            mbar_init(sf_done + 8 * i, 1);
+        }
+        failed = 0;
+        mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc<2>(smem_u32(&tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&map_n);
+        tma_prefetch_map(&map_m);
+        const uint32_t lead_full = cluster_map(full, 0);
+        uint32_t s = 0, turn = 1;  // the first turn finds every stage free
+        int issued = 0;
+        bool ok = true;
+        for (int64_t t = first; t < pp.tiles && ok; t += step) {
+            int64_t m0, n0;
+            pair_tile(pp, t, m0, n0);
+            const int32_t yn = static_cast<int32_t>(n0 + 128 * rank), ym = static_cast<int32_t>(m0 + pp.rows / 2 * rank);
+            for (int c = 0; c < p.chunks; ++c) {
+                if (!(ok = mbar_wait(empty + 8 * s, turn, &failed))) break;
+                const uint32_t dst = base + s * stage;
+                if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * stage);
+                tma_load_2d_pair(dst, &map_n, lead_full + 8 * s, c * kKC, yn);
+                tma_load_2d_pair(dst + 128 * kKC, &map_m, lead_full + 8 * s, c * kKC, ym);
+                issued = issued < kPairStages ? issued + 1 : kPairStages;
+                if (++s == kPairStages) s = 0, turn ^= 1;
+            }
+        }
+        // both CTAs' copies count on the first one's barriers; the other waits at the cluster barrier below
+        if (!ok && rank == 0) mbar_drain(full, kPairStages, issued, s, turn);
+    } else if (warp == 1 && rank == 0) {
+        // Issue of the products.  This thread's time per chunk bounds the kernel (512 clocks of products at TM = 256),
+        // and a look at an mbarrier takes about a hundred: the next chunk's is looked at before this one's products
+        // are issued, and the scale copies have a warp of their own.
+        uint64_t d = smem_desc(base, 16, 1024, 2);
+        const uint64_t d_step = stage >> 4;
+        uint32_t s = 0, turn = 0, seq = 0, g = 0;
+        const uint32_t lag = overlap ? 1 : 2;
+        bool ready = false;
+        for (int64_t t = first; t < pp.tiles; t += step) {
+            for (int c0 = 0; c0 < p.chunks; c0 += pp.seg_chunks, ++seq) {
+                const int c1 = min(p.chunks, c0 + pp.seg_chunks);
+                const uint32_t acc = tmem + (seq & 1 ? acc1 : 0);
+                if (seq >= lag) mbar_wait_cluster(drained + 8 * ((seq - lag) & 1), ((seq - lag) >> 1) & 1, &failed);
+                for (int c = c0; c < c1; ++c) {
+                    const bool first_of_word = (c & 3) == 0, last_of_word = (c & 3) == 3 || c == p.chunks - 1;
+                    if (first_of_word) mbar_wait(sf_ready + 8 * (g & 1), (g >> 1) & 1, &failed);
+                    if (!ready) mbar_wait(full + 8 * s, turn, &failed);
+                    tc_fence_after();
+                    const uint32_t next = s + 1 == kPairStages ? 0 : s + 1;
+                    ready = mbar_test(full + 8 * next, next ? turn : turn ^ 1);
+                    if (elect_one()) {
+                        const uint32_t col = tmem + kPairScaleCols + (g & 1) * 12;
+                        const uint32_t idesc = p.idesc | mxf8_scale_byte(c & 3);
+#pragma unroll
+                        for (int k = 0; k < kKC / 32; ++k)
+                            tc_mma_mxf8<2>(acc, d + 2 * k, d + ((128 * kKC) >> 4) + 2 * k, idesc, col, col + 4, c > c0 || k > 0);
+                        tc_commit_pair(empty + 8 * s);
+                        if (last_of_word) tc_commit_pair(sf_done + 8 * (g & 1));
+                        if (c == c1 - 1) tc_commit_pair(acc_full + 8 * (seq & 1));
+                    }
+                    __syncwarp();
+                    g += last_of_word;
+                    s = next;
+                    if (s == 0) turn ^= 1, d = smem_desc(base, 16, 1024, 2);
+                    else d += d_step;
+                }
+            }
+        }
+    } else if (warp == 3 && rank == 0) {
+        // Scale words from shared memory (four buffers, filled by the staging warps of both CTAs) to tensor memory
+        // (two, freed by the products that read them).
+        const int64_t words = (p.chunks + 3) >> 2;
+        uint32_t g = 0;
+        for (int64_t t = first; t < pp.tiles; t += step)
+            for (int64_t j = 0; j < words; ++j, ++g) {
+                const uint32_t b = g % kPairScaleBufs;
+                mbar_wait_cluster(sf_full + 8 * b, (g / kPairScaleBufs) & 1, &failed);
+                mbar_wait(sf_done + 8 * (g & 1), ((g >> 1) + 1) & 1, &failed);
+                tc_fence_after();
+                if (elect_one()) {
+                    for (int a = 0; a < 3; ++a)
+                        tc_copy_scales<2>(tmem + kPairScaleCols + (g & 1) * 12 + 4 * a, scales + b * kPairScaleBuf + 512 * a);
+                    tc_commit_pair(sf_empty + 8 * b);
+                    tc_commit_pair(sf_ready + 8 * (g & 1));
+                }
+                __syncwarp();
+            }
+    } else if (warp == 2) {
+        uint32_t g = 0;
+        const uint32_t lead_sf = cluster_map(sf_full, 0);
+        for (int64_t t = first; t < pp.tiles; t += step) {
+            int64_t m0, n0;
+            pair_tile(pp, t, m0, n0);
+            const int64_t nr = n0 + 128 * rank + lane, mr = m0 + lane;
+            for (int j = 0; j <= (p.chunks - 1) >> 2; ++j, ++g) {
+                const uint32_t *sn = p.sb + static_cast<int64_t>(j) * p.N, *sm = p.sa + static_cast<int64_t>(j) * p.M;
+                uint32_t w[3][4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    w[0][q] = nr + 32 * q < p.N ? ldg_early(sn + nr + 32 * q) : 0x01010101u;
+                    w[1][q] = mr + 32 * q < p.M ? ldg_early(sm + mr + 32 * q) : 0x01010101u;
+                    w[2][q] = mr + 128 + 32 * q < p.M ? ldg_early(sm + mr + 128 + 32 * q) : 0x01010101u;
+                }
+                const uint32_t b = g % kPairScaleBufs;
+                mbar_wait(sf_empty + 8 * b, (g / kPairScaleBufs + 1) & 1, &failed);
+                __syncwarp();
+                stage_scales<3>(scales + b * kPairScaleBuf + lane * 16, w);
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(lead_sf + 8 * b);
+            }
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t lead_drained = cluster_map(drained, 0);
+        const int batches = pp.rows / 32;
+        uint32_t seq = 0;
+        for (int64_t t = first; t < pp.tiles; t += step) {
+            int64_t m0, n0;
+            pair_tile(pp, t, m0, n0);
+            const int64_t n = n0 + 128 * rank + quarter * 32 + lane, mleft = p.M - m0;
+            for (int seg = 0; seg < pp.segments; ++seg, ++seq) {
+                const uint32_t buf = seq & 1;
+                mbar_wait(acc_full + 8 * buf, (seq >> 1) & 1, &failed);
+                __syncwarp();
+                tc_fence_after();
+                // The halves take alternate batches of 32 columns.  Where the accumulators overlap, the half that
+                // holds the shared batch (7 of buffer 0, 0 of buffer 1) starts with it and the other has none.
+                const int start = overlap && buf == 0 && half == 1 ? 7 : half;
+                bool told = overlap && half == static_cast<int>(buf);
+                if (told) {
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
+                }
+#pragma unroll 1
+                for (int i = half; i < batches; i += 2) {
+                    int j = start == half ? i : (i == half ? 7 : i - 2);
+                    float v[32];
+                    tc_load32(v, lanes + (buf ? acc1 : 0) + j * 32);
+                    tc_wait_ld();
+                    if (!told && (overlap || i + 2 >= batches)) {
+                        told = true;
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
+                    }
+                    const int64_t m = m0 + j * 32;
+                    const int64_t left = mleft - j * 32;
+                    if (n >= p.N || left <= 0) continue;
+                    T *d = static_cast<T *>(p.d) + m * p.ldd + n;
+                    const T *c = seg > 0 ? d : p.c ? static_cast<const T *>(p.c) + m * p.ldc + n : nullptr;
+                    const int64_t ldc = seg > 0 ? p.ldd : p.ldc;
+                    store32<T>(v, d, p.ldd, c, ldc, left < 32 ? static_cast<int>(left) : 32);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();
+    if (threadIdx.x == 0 && failed && p.status) atomicOr(p.status, static_cast<unsigned int>(GAR_STATUS_TIMEOUT));
+    if (warp == 1) tmem_free<2>(tmem, 512);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -307,6 +594,67 @@ int launch(MatmulParams &p, const uint8_t *a, int64_t lda, const uint8_t *b, int
     return check_launch("matmul_kernel");
 }
 
+// The rows of a pair's tiles: the count that finishes soonest.  A chunk of 128
+// k takes the tensor cores 2 TM clocks and its operands, at the 70 bytes a
+// clock that an SM gets from L2 when all load, (128 + TM / 2) 128 / 70; a wave
+// adds its prologue, more where the accumulators overlap.
+int pair_rows(int64_t M, int64_t tiles_n, int64_t chunks, int pairs) {
+    int best = 256;
+    int64_t least = INT64_MAX;
+    for (int rows = 256; rows >= 128; rows -= 32) {
+        const int64_t waves = ceil_div(ceil_div(M, int64_t{rows}) * tiles_n, int64_t{pairs});
+        const int64_t load = (128 + rows / 2) * 128 / 70, mma = 2 * rows;
+        const int64_t cost = waves * (chunks * (mma > load ? mma : load) + (rows == 256 ? 2500 : 500));
+        if (cost < least) least = cost, best = rows;
+    }
+    return best;
+}
+
+template <typename T>
+int launch_pair(MatmulParams &mm, const uint8_t *a, int64_t lda, const uint8_t *b, int64_t ldb, int64_t K,
+                cudaStream_t stream) {
+    static std::atomic<int> pairs_of[64];  // resident pairs per device, 0: not looked up yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return fail(GAR_ECUDA, "no current device");
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = pair_smem(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int pairs = pairs_of[dev & 63].load(std::memory_order_relaxed);
+    if (pairs == 0) {
+        cfg.gridDim = dim3(2);
+        cudaError_t e = cudaFuncSetAttribute(matmul_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, pair_smem(256));
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&pairs, matmul_pair_kernel<T>, &cfg);
+        if (e != cudaSuccess || pairs < 1) return fail(GAR_ECUDA, "matmul_pair_kernel: %s", cudaGetErrorString(e));
+        pairs_of[dev & 63].store(pairs, std::memory_order_relaxed);
+    }
+    PairParams p{};
+    mm.tiles_n = static_cast<int32_t>(ceil_div(mm.N, int64_t{256}));
+    p.rows = pair_rows(mm.M, mm.tiles_n, mm.chunks, pairs);
+    mm.idesc |= mxf8_idesc(0, 0, 256, static_cast<uint32_t>(p.rows));
+    p.mm = mm;
+    p.tiles_m = ceil_div(mm.M, int64_t{p.rows});
+    p.tiles = p.tiles_m * mm.tiles_n;
+    p.segments = sizeof(T) == 2 ? 1 : static_cast<int32_t>(ceil_div(mm.chunks, kSegment));
+    // whole scale words per segment
+    p.seg_chunks = static_cast<int32_t>(ceil_div(ceil_div(mm.chunks, p.segments), 4) * 4);
+    p.segments = static_cast<int32_t>(ceil_div(mm.chunks, p.seg_chunks));
+    CUtensorMap map_n{}, map_m{};
+    if (int rc = encode(&map_n, b, mm.N, K, ldb, 128)) return rc;
+    if (int rc = encode(&map_m, a, mm.M, K, lda, p.rows / 2)) return rc;
+    cfg.dynamicSmemBytes = pair_smem(p.rows);
+    cfg.gridDim = dim3(2 * static_cast<unsigned>(p.tiles < pairs ? p.tiles : pairs));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, matmul_pair_kernel<T>, map_n, map_m, p);
+    if (e != cudaSuccess) return fail(GAR_ECUDA, "matmul_pair_kernel: %s", cudaGetErrorString(e));
+    return check_launch("matmul_pair_kernel");
+}
+
 int check_operand(const char *name, const uint8_t *q, int64_t ld, int64_t K, const uint8_t *scale, int32_t format) {
     if (format != GAR_F8E4M3 && format != GAR_F8E5M2) return fail(GAR_EDTYPE, "%s: unknown 8-bit format %d", name, format);
     if (K == 0) return GAR_OK;
@@ -342,6 +690,8 @@ extern "C" int gar_fp8_matmul(const uint8_t *a, int64_t lda, const uint8_t *a_sc
     p.d = d, p.ldd = ldd, p.c = c, p.ldc = ldc, p.bf16 = dtype == GAR_BF16;
     p.status = device_status();
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (K > 0 && ceil_div(M, int64_t{256}) * ceil_div(N, int64_t{256}) >= sm_count() / 2)
+        return p.bf16 ? launch_pair<uint16_t>(p, a, lda, b, ldb, K, stream) : launch_pair<float>(p, a, lda, b, ldb, K, stream);
     if (M <= 32) return launch<32>(p, a, lda, b, ldb, K, stream);
     if (M <= 64) return launch<64>(p, a, lda, b, ldb, K, stream);
     if (ceil_div(M, int64_t{256}) * ceil_div(N, int64_t{kTN}) < sm_count())

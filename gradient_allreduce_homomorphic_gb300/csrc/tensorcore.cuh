@@ -37,21 +37,53 @@ __device__ __forceinline__ uint64_t global_ns() {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
-// Wait for the phase of the given parity to complete; false after kWaitNs
-// (the caller then gives up its work, in order, and reports it).
+// Without waiting: whether the phase of the given parity is complete.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Wait for the phase of the given parity to complete, for kWaitNs at most:
+// then *failed (shared memory) is set, after which no wait of the CTA waits any
+// longer and the kernel runs to its end with a result that is not valid.  The
+// caller's control flow does not depend on the outcome, so that a loop around
+// it stays uniform across its warp; only what must not go on (the issue of
+// copies) looks at the returned value.
 constexpr uint64_t kWaitNs = 2000000000ull;
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *failed) {
     const uint64_t t0 = global_ns();
-    while (global_ns() - t0 < kWaitNs)
+    while (!*failed && global_ns() - t0 < kWaitNs)
         for (int i = 0; i < 64; ++i)
             if (mbar_try(bar, parity)) return true;
+    if (mbar_test(bar, parity)) return true;
+    *failed = 1;
     return false;
 }
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int *failed) {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < 16; ++i)
         if (mbar_try(bar, parity)) return true;
-    return mbar_wait_slow(bar, parity);
+    return mbar_wait_slow(bar, parity, failed);
+}
+
+// The same across a cluster: arrive on the barrier at a mapped address, and
+// wait with cluster scope for such arrivals on an own barrier.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t mapped) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
+}
+__device__ __forceinline__ void mbar_wait_cluster(uint32_t bar, uint32_t parity, int *failed) {
+    mbar_wait(bar, parity, failed);
+    asm volatile(  // the phase is complete: this returns at once, with the wider scope
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(parity)
+        : "memory");
 }
 
 // One 2-D tile of a tensor map (x: innermost, a multiple of 16 bytes) into
@@ -60,6 +92,13 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+// For a CTA pair: the bytes counted on an mbarrier of either CTA (mapped address).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, uint32_t mapped_bar, int32_t x, int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(mapped_bar), "r"(x), "r"(y)
         : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
@@ -92,6 +131,13 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 // All products issued before it done: one arrival on the mbarrier.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// The same for products of a CTA pair: an arrival on both CTAs' barriers.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"(static_cast<uint16_t>(3))
+                 : "memory");
 }
 
 // Shared-memory matrix descriptor (start address, leading and stride byte
@@ -147,6 +193,21 @@ __device__ __forceinline__ void tc_load32(float (&v)[32], uint32_t taddr) {
         : "r"(taddr));
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// True in one lane of a converged warp.  Chosen this way, and with the loops
+// around it run by the whole warp, the compiler knows the operands of the
+// tensor-core instructions to be uniform.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// A read-only load that stays where it is written, ahead of a wait.
+__device__ __forceinline__ uint32_t ldg_early(const uint32_t *p) {
+    uint32_t v;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 
 // ------------------------------------------------------------------ clusters
 __device__ __forceinline__ uint32_t cluster_cta_rank() {
