@@ -7,15 +7,28 @@
 //   loss = sum_j p_j (log p_j + lse - z_{i_j} / tau)
 //   dz_v = w / tau (exp(z_v / tau - lse) - sum_{j: i_j = v} p_j)
 // An entry is present if its index lies in [0, V) and its logit is above -inf.
-// Everything is computed in fp32 and rounded once, when dz is stored.
+// Everything is computed in fp32 and rounded once, when dz is stored.  Powers
+// are taken as 2^((z - m) c), c = log2(e) / tau: the difference from the row's
+// maximum m is formed first, so a row of equal values, however large, stays
+// exact, and the product's rounding is relative to a small number.  A maximum
+// of -inf is replaced by 0 in the difference, which makes the powers 0.
+//
+// Bound by HBM: a row is read once and, with dz, written once.  Rows of at
+// least kStreamBytes go through shared memory (distill_stream_kernel); shorter
+// ones take one small CTA each, whose second and third reads hit L1 and L2
+// (distill_row_kernel).
+#include <atomic>
+
 #include "common.cuh"
 #include "fp8.cuh"
+#include "tensorcore.cuh"
 
 namespace gar {
 namespace {
 
-constexpr int kThreads = 512;
 constexpr int kMaxTop = 1024;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
 
 struct DistillParams {
     const void *z;
@@ -28,38 +41,72 @@ struct DistillParams {
     float *loss, *lse;         // gar_distill_loss
     const float *lse_in;       // gar_distill_grad
     void *dz;                  // NULL: no gradient
+    int32_t stages, stage_bytes, slots, log_cluster;  // distill_stream_kernel
+    unsigned int *status;
 };
 
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// A maximum and the sum of 2^((z - maximum) c) over the values seen.
+struct MaxSum {
+    float m, s;
+};
+__device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b, float c) {
+    const float m = fmaxf(a.m, b.m), r = finite_or_0(m);
+    return {m, a.s * pow2((a.m - r) * c) + b.s * pow2((b.m - r) * c)};
+}
 __device__ __forceinline__ float warp_max(float v) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(v));
+    return m;
+}
+template <int kWidth>
+__device__ __forceinline__ float lane_sum(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    for (int o = kWidth / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
+__device__ __forceinline__ float warp_sum(float v) { return lane_sum<32>(v); }
+// The merge of kWidth lanes' pairs (each held by 32 / kWidth lanes).
+template <int kWidth>
+__device__ __forceinline__ MaxSum merge_lanes(MaxSum a, float c) {
+    const float m = warp_max(a.m);
+    return {m, lane_sum<kWidth>(a.s * pow2((a.m - finite_or_0(m)) * c))};
 }
 
-// The block's sum (or maximum), the same value in every thread.
+// Where the gradient of a student logit z comes from: the row's maximum and
+// log2 of its sum (loss), or its saved lse (grad).
+template <bool kSaved>
+struct Softmax {
+    float ref, sub, c;  // probability 2^((z - ref) c - sub), or exp(z c - sub)
+    __device__ __forceinline__ float operator()(float z) const {
+        return kSaved ? pow2(fmaf(z, c, -sub) * kLog2e) : pow2(fmaf(z - ref, c, -sub));
+    }
+};
+
+// ---------------------------------------------------------------- short rows
+constexpr int kRowThreads = 128;
+
 template <bool kMax>
 __device__ __forceinline__ float block_reduce(float v, float *scratch) {
     v = kMax ? warp_max(v) : warp_sum(v);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = scratch[threadIdx.x & (kThreads / 32 - 1)];
+    v = scratch[0];
 #pragma unroll
-    for (int o = kThreads / 64; o > 0; o >>= 1) {
-        const float u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        v = kMax ? fmaxf(v, u) : v + u;
-    }
+    for (int i = 1; i < kRowThreads / 32; ++i) v = kMax ? fmaxf(v, scratch[i]) : v + scratch[i];
     return v;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const __grid_constant__ DistillParams p) {
-    __shared__ float scratch[kThreads / 32];
+template <typename T, bool kSaved>
+__global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_constant__ DistillParams p) {
+    __shared__ float scratch[kRowThreads / 32];
     __shared__ float top_p[kMaxTop], top_z[kMaxTop];
     __shared__ int32_t top_i[kMaxTop];
     const int64_t row = blockIdx.x;
@@ -69,66 +116,63 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const __grid_constant
     const int tid = threadIdx.x;
 
     float tmax = -INFINITY;
-    for (int j = tid; j < p.k; j += kThreads) {
+    for (int j = tid; j < p.k; j += kRowThreads) {
         const int32_t i = p.index[row * p.k + j];
         const float t = p.teacher[row * p.k + j] * p.inv_tau;
         const bool on = i >= 0 && i < p.vocab && !(t == -INFINITY);
         top_i[j] = on ? i : -1;
         top_p[j] = t;
+        top_z[j] = on ? load_f32(z + i) : 0.0f;
         if (on) tmax = fmaxf(tmax, t);
     }
     tmax = block_reduce<true>(tmax, scratch);
     float tsum = 0.0f;
-    for (int j = tid; j < p.k; j += kThreads) {
-        const float e = top_i[j] >= 0 ? expf(top_p[j] - tmax) : 0.0f;
-        tsum += e;
-    }
+    for (int j = tid; j < p.k; j += kRowThreads)
+        if (top_i[j] >= 0) tsum += expf(top_p[j] - tmax);
     tsum = block_reduce<false>(tsum, scratch);
-    const bool live = w != 0.0f && tsum != 0.0f;
-    if (!live) {  // nothing to learn in this row: z is not read
+    if (w == 0.0f || tsum == 0.0f) {  // nothing to learn in this row
         if (dz)
-            for (int v = tid; v < p.vocab; v += kThreads) store_f32(dz + v, 0.0f);
-        if (tid == 0 && p.loss) p.loss[row] = 0.0f;
-        if (tid == 0 && p.lse) p.lse[row] = 0.0f;
+            for (int v = tid; v < p.vocab; v += kRowThreads) store_f32(dz + v, 0.0f);
+        if (!kSaved && tid == 0) p.loss[row] = 0.0f, p.lse[row] = 0.0f;
         return;
     }
-    const float log_tsum = logf(tsum);
-    float lse;
-    if (p.lse_in) {
-        lse = p.lse_in[row];
+    const float log_tsum = logf(tsum), c = kLog2e * p.inv_tau;
+    Softmax<kSaved> q;
+    bool empty = false;
+    if (kSaved) {
+        q.ref = 0.0f, q.c = p.inv_tau, q.sub = p.lse_in[row];
+        empty = q.sub == -INFINITY;
     } else {
         float m = -INFINITY;
-        for (int v = tid; v < p.vocab; v += kThreads) m = fmaxf(m, load_f32(z + v));
+        for (int v = tid; v < p.vocab; v += kRowThreads) m = fmaxf(m, load_f32(z + v));
         m = block_reduce<true>(m, scratch);
+        const float r = finite_or_0(m);
         float s = 0.0f;
-        for (int v = tid; v < p.vocab; v += kThreads) s += expf((load_f32(z + v) - m) * p.inv_tau);
+        for (int v = tid; v < p.vocab; v += kRowThreads) s += pow2((load_f32(z + v) - r) * c);
         s = block_reduce<false>(s, scratch);
-        lse = m == -INFINITY ? -INFINITY : m * p.inv_tau + logf(s);
+        empty = m == -INFINITY && s == 0.0f;
+        q.ref = r, q.c = c, q.sub = log2f(s);
     }
     float part = 0.0f;
-    for (int j = tid; j < p.k; j += kThreads) {
+    for (int j = tid; j < p.k; j += kRowThreads) {
         float pj = 0.0f;
         if (top_i[j] >= 0) {
             const float logp = top_p[j] - tmax - log_tsum;
             pj = expf(logp);
-            const float zj = load_f32(z + top_i[j]) * p.inv_tau;
-            top_z[j] = zj;
-            if (pj > 0.0f) part += lse == -INFINITY ? INFINITY : pj * (logp + lse - zj);
-            else if (pj != pj) part = pj;
+            if (!(pj == 0.0f)) part += pj * (logp - (top_z[j] - q.ref) * p.inv_tau);
         }
         top_p[j] = pj;
     }
     part = block_reduce<false>(part, scratch);
-    if (tid == 0 && p.loss) p.loss[row] = part;
-    if (tid == 0 && p.lse) p.lse[row] = lse;
+    if (!kSaved && tid == 0) {
+        p.loss[row] = empty ? INFINITY : part + q.sub * kLn2;
+        p.lse[row] = empty ? -INFINITY : q.ref * p.inv_tau + q.sub * kLn2;
+    }
     if (!dz) return;
     const float g = w * p.inv_tau;
-    for (int v = tid; v < p.vocab; v += kThreads) {
-        const float q = lse == -INFINITY ? 0.0f : expf(load_f32(z + v) * p.inv_tau - lse);
-        store_f32(dz + v, g * q);
-    }
+    for (int v = tid; v < p.vocab; v += kRowThreads) store_f32(dz + v, empty ? 0.0f : g * q(load_f32(z + v)));
     __syncthreads();
-    for (int j = tid; j < p.k; j += kThreads) {
+    for (int j = tid; j < p.k; j += kRowThreads) {
         const int32_t i = top_i[j];
         if (i < 0) continue;
         float sum = 0.0f;
@@ -138,10 +182,410 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const __grid_constant
                 if (o < j) first = false;
                 sum += top_p[o];
             }
-        if (!first) continue;
-        const float q = lse == -INFINITY ? 0.0f : expf(top_z[j] - lse);
-        store_f32(dz + i, g * (q - sum));
+        if (first) store_f32(dz + i, g * ((empty ? 0.0f : q(top_z[j])) - sum));
     }
+}
+
+// ----------------------------------------------------------------- long rows
+// A cluster of K CTAs takes a row at a time, each CTA a K-th of its 16-byte
+// vectors.  Sixteen warps pass over the present row in shared memory: once for
+// the maximum and the sum of powers, exchanged between the CTAs as one pair
+// each, once for the gradient.  Behind them one warp copies the CTA's part of
+// the coming rows to shared memory (bulk copies, two or more stages), and
+// kPrepare warps take turns preparing the coming rows' teacher entries (slots),
+// a chain of dependent loads and reductions of some microseconds a row.  The
+// elements before a row's first 16-byte boundary and after its last one (a
+// vocabulary of odd size) are taken from global memory by the cluster's first
+// CTA.
+//
+// With more than one CTA a row (kLag) the gradient pass runs a row behind the
+// first pass, so that a pair that comes late, for its CTA's copy took longer,
+// holds no one up.  The elements of dz at the entries are written over the
+// softmax's once a barrier has followed that row's gradient pass; the barrier
+// is the one in the next row's reduction.
+constexpr int kMain = 512, kMainWarps = kMain / 32, kPrepare = 3;
+constexpr int kStreamThreads = kMain + 32 + 32 * kPrepare;
+constexpr int kMaxStages = 8, kMaxSlots = 8, kMaxCluster = 8;
+constexpr int kMeets = 4;  // exchanges that may be under way: this row's, the last one's, and two a faster CTA may be at
+
+// A slot's row.  The slot's entries follow it in dynamic shared memory: their
+// indices (-1: absent), probabilities, and the student's logits at those that
+// this CTA's part holds (at all of them in the first CTA, for the loss).
+struct Header {
+    float weight, cross;  // cross: sum of p_j (log p_j - (z_j - zref) / tau)
+    float zref;
+    int32_t live, repeated;
+};
+
+template <typename T>
+struct Row {  // one row's split into head, vectors and tail
+    int32_t head, vectors, v0, v1;  // this CTA: vectors v0 .. v1
+    __device__ __forceinline__ Row(const T *z, int32_t vocab, int32_t rank, int32_t log_cluster) {
+        constexpr int32_t n = 16 / sizeof(T);
+        const int32_t off = static_cast<int32_t>((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / static_cast<int32_t>(sizeof(T));
+        head = off < vocab ? off : vocab;
+        vectors = (vocab - head) / n;
+        v0 = (vectors * rank) >> log_cluster;  // below 2^31: there are fewer than 2^28 vectors, and 8 ranks
+        v1 = (vectors * (rank + 1)) >> log_cluster;
+    }
+    // Element of the i-th place outside the vectors, which are the first CTA's; -1 past the last.
+    __device__ __forceinline__ int32_t edge(int32_t i, int32_t vocab, int32_t rank) const {
+        const int32_t at = i < head ? i : i + vectors * static_cast<int32_t>(16 / sizeof(T));
+        return rank == 0 && at < vocab ? at : -1;
+    }
+    __device__ __forceinline__ bool holds(int32_t i, int32_t rank) const {
+        constexpr int32_t n = 16 / sizeof(T);
+        const int32_t v = i - head;
+        if (v < 0 || v >= vectors * n) return rank == 0;
+        return v >= v0 * n && v < v1 * n;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4 &g, float (&x)[16 / sizeof(T)]) {
+    if constexpr (sizeof(T) == 2) {
+        x[0] = bf16_lo(g.x), x[1] = bf16_hi(g.x), x[2] = bf16_lo(g.y), x[3] = bf16_hi(g.y);
+        x[4] = bf16_lo(g.z), x[5] = bf16_hi(g.z), x[6] = bf16_lo(g.w), x[7] = bf16_hi(g.w);
+    } else {
+        x[0] = __uint_as_float(g.x), x[1] = __uint_as_float(g.y);
+        x[2] = __uint_as_float(g.z), x[3] = __uint_as_float(g.w);
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&x)[16 / sizeof(T)]) {
+    if constexpr (sizeof(T) == 2)
+        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    else
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+
+__device__ __forceinline__ void bar_main() { asm volatile("bar.sync 1, %0;" ::"n"(kMain) : "memory"); }
+
+template <typename T, bool kSaved, bool kLag>
+__global__ void __launch_bounds__(kStreamThreads, kLag ? 1 : 2) distill_stream_kernel(const __grid_constant__ DistillParams p) {
+    constexpr int n = 16 / sizeof(T);
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kMaxSlots + kMeets];
+    __shared__ Header header[kMaxSlots];
+    __shared__ MaxSum partial[2][kMainWarps];
+    __shared__ __align__(8) MaxSum pairs[kMeets][kMaxCluster];
+    __shared__ int failed;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t K = 1u << p.log_cluster, rank = blockIdx.x & (K - 1);
+    const int64_t first = blockIdx.x >> p.log_cluster, step = gridDim.x >> p.log_cluster;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages, slot_full = empty + 8 * kMaxStages,
+                   slot_empty = slot_full + 8 * kMaxSlots, met = slot_empty + 8 * kMaxSlots;
+    const uint32_t S = p.stages, E = p.slots;
+    // dynamic shared memory: the stages, the slots, each preparing warp's table for finding repeated indices
+    const int entries = (p.k + 3) & ~3;
+    uint8_t *slots = smem + S * p.stage_bytes;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, kMainWarps);
+        }
+        for (int i = 0; i < kMaxSlots; ++i) {
+            mbar_init(slot_full + 8 * i, 1);
+            mbar_init(slot_empty + 8 * i, kMainWarps);
+        }
+        for (int i = 0; i < kMeets; ++i) mbar_init(met + 8 * i, 1);
+        failed = 0;
+        mbar_init_fence();
+    }
+    __syncthreads();
+    if (kLag) cluster_barrier();
+
+    if (warp == kMainWarps) {
+        if (lane == 0) {
+            uint32_t s = 0, turn = 1, issued = 0;
+            bool ok = true;
+            for (int64_t row = first; row < p.rows; row += step) {
+                const T *z = static_cast<const T *>(p.z) + row * p.ldz;
+                const Row<T> part(z, p.vocab, rank, p.log_cluster);
+                const uint32_t bytes = static_cast<uint32_t>((part.v1 - part.v0) * 16);
+                if (!(ok = mbar_wait(empty + 8 * s, turn, &failed))) break;
+                mbar_expect_tx(full + 8 * s, bytes);
+                if (bytes > 0)
+                    asm volatile(
+                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                            smem_u32(smem + s * p.stage_bytes)),
+                        "l"(__cvta_generic_to_global(z + part.head + part.v0 * n)), "r"(bytes), "r"(full + 8 * s)
+                        : "memory");
+                issued = issued < S ? issued + 1 : S;
+                if (++s == S) s = 0, turn ^= 1;
+            }
+            if (!ok)  // leave no copy in flight
+                for (; issued > 0; --issued) {
+                    if (s == 0) s = S, turn ^= 1;
+                    --s;
+                    int given_up = 0;
+                    mbar_wait(full + 8 * s, turn ^ 1, &given_up);
+                }
+        }
+    } else if (warp > kMainWarps) {
+        const uint32_t mine = warp - kMainWarps - 1;
+        uint32_t buckets = 32, shift = 27;  // a bucket is the top bits of the index times an odd constant
+        while (buckets < 2 * static_cast<uint32_t>(p.k)) buckets *= 2, --shift;
+        uint32_t *table = reinterpret_cast<uint32_t *>(slots + E * 12 * entries) + mine * buckets;
+        uint32_t e = mine % E, turn = 1 ^ (mine / E & 1);
+        for (int64_t row = first + mine * step; row < p.rows; row += kPrepare * step) {
+            const T *z = static_cast<const T *>(p.z) + row * p.ldz;
+            const Row<T> part(z, p.vocab, rank, p.log_cluster);
+            mbar_wait(slot_empty + 8 * e, turn, &failed);
+            __syncwarp();
+            int32_t *top_i = reinterpret_cast<int32_t *>(slots + e * 12 * entries);
+            float *top_p = reinterpret_cast<float *>(top_i + entries), *top_z = top_p + entries;
+            const float w = p.weight ? p.weight[row] : 1.0f;
+            float tmax = -INFINITY, tsum = 0.0f, zref = -INFINITY;
+            constexpr int kAtOnce = 4;  // entries of a lane whose loads are in flight together
+            for (int j0 = lane; j0 < p.k; j0 += 32 * kAtOnce) {
+                int32_t at[kAtOnce];
+                float t[kAtOnce], zj[kAtOnce];
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
+                    const int j = j0 + 32 * u;
+                    at[u] = j < p.k ? p.index[row * p.k + j] : -1;
+                    t[u] = j < p.k ? p.teacher[row * p.k + j] * p.inv_tau : -INFINITY;
+                }
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
+                    if (at[u] < 0 || at[u] >= p.vocab || t[u] == -INFINITY) at[u] = -1;
+                    zj[u] = at[u] >= 0 && ((!kSaved && rank == 0) || part.holds(at[u], rank)) ? load_f32(z + at[u]) : 0.0f;
+                }
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
+                    const int j = j0 + 32 * u;
+                    if (j >= p.k) continue;
+                    top_i[j] = at[u];
+                    top_p[j] = t[u];
+                    top_z[j] = zj[u];
+                    if (at[u] >= 0) tmax = fmaxf(tmax, t[u]), zref = fmaxf(zref, zj[u]);
+                }
+            }
+            tmax = warp_max(tmax);
+            zref = finite_or_0(warp_max(zref));
+            for (uint32_t j = lane; j < buckets; j += 32) table[j] = 0xFFFFFFFFu;
+            for (int j = lane; j < p.k; j += 32)
+                if (top_i[j] >= 0) tsum += expf(top_p[j] - tmax);
+            tsum = warp_sum(tsum);
+            const bool live = w != 0.0f && tsum != 0.0f;  // NaN: live, and it spreads
+            float cross = 0.0f;
+            bool twice = false;
+            __syncwarp();
+            if (live) {
+                const float log_tsum = logf(tsum);
+                for (int j = lane; j < p.k; j += 32) {
+                    const int32_t i = top_i[j];
+                    float pj = 0.0f;
+                    if (i >= 0) {
+                        const float logp = top_p[j] - tmax - log_tsum;
+                        pj = expf(logp);
+                        if (!(pj == 0.0f)) cross += pj * (logp - (top_z[j] - zref) * p.inv_tau);
+                        uint32_t at = (static_cast<uint32_t>(i) * 0x9E3779B1u) >> shift;
+                        while (true) {  // ends: at most half of the buckets are taken
+                            const uint32_t was = atomicCAS(table + at, 0xFFFFFFFFu, static_cast<uint32_t>(i));
+                            if (was == 0xFFFFFFFFu) break;
+                            if (was == static_cast<uint32_t>(i)) {
+                                twice = true;
+                                break;
+                            }
+                            at = (at + 1) & (buckets - 1);
+                        }
+                    }
+                    top_p[j] = pj;
+                }
+                cross = warp_sum(cross);
+                twice = __any_sync(0xFFFFFFFFu, twice);
+            }
+            if (lane == 0) header[e] = {w, cross, zref, live, twice};
+            __syncwarp();
+            if (lane == 0) mbar_arrive(slot_full + 8 * e);
+            for (int i = 0; i < kPrepare; ++i)
+                if (++e == E) e = 0, turn ^= 1;
+        }
+    } else {
+        const float c = kLog2e * p.inv_tau;
+        struct Place {
+            int64_t row;  // -1: none
+            uint32_t s, e, meet;
+        };
+        struct Done {
+            int64_t row;
+            uint32_t e;
+            float ref, sub, g;
+        };
+
+        // The row's maximum and sum over this CTA's part, the same in every thread.
+        const auto reduce_part = [&](const Place &at) {
+            const T *z = static_cast<const T *>(p.z) + at.row * p.ldz;
+            const Row<T> part(z, p.vocab, rank, p.log_cluster);
+            const uint4 *v = reinterpret_cast<const uint4 *>(smem + at.s * p.stage_bytes);
+            const int count = part.v1 - part.v0;
+            MaxSum a{-INFINITY, 0.0f};
+            const int odd = part.edge(threadIdx.x, p.vocab, rank);
+            if (odd >= 0) a.m = load_f32(z + odd), a.s = pow2((a.m - finite_or_0(a.m)) * c);
+#pragma unroll 2
+            for (int i = threadIdx.x; i < count; i += kMain) {
+                float x[n];
+                unpack<T>(v[i], x);
+                float m = a.m;
+#pragma unroll
+                for (int j = 0; j < n; ++j) m = fmaxf(m, x[j]);
+                const float r = finite_or_0(m);
+                float t = 0.0f;
+#pragma unroll
+                for (int j = 0; j < n; ++j) t += pow2((x[j] - r) * c);
+                a.s = fmaf(a.s, pow2((a.m - r) * c), t);
+                a.m = m;
+            }
+            return merge_lanes<32>(a, c);
+        };
+
+        // Loss, lse and the gradient's softmax over this CTA's part.
+        const auto finish = [&](const Place &at, MaxSum a) {
+            Done r{at.row, at.e, 0.0f, 0.0f, 0.0f};
+            const T *z = static_cast<const T *>(p.z) + at.row * p.ldz;
+            T *dz = p.dz ? static_cast<T *>(p.dz) + at.row * p.lddz : nullptr;
+            const Row<T> part(z, p.vocab, rank, p.log_cluster);
+            const Header &h = header[at.e];
+            if (h.live) {
+                bool none;
+                if (kSaved) {
+                    r.sub = p.lse_in[at.row];
+                    none = r.sub == -INFINITY;
+                } else {
+                    if (kLag) {
+                        const uint32_t meet = at.meet % kMeets;
+                        mbar_wait(met + 8 * meet, (at.meet / kMeets) & 1, &failed);
+                        a = pairs[meet][0];
+                        for (uint32_t i = 1; i < K; ++i) a = merge(a, pairs[meet][i], c);
+                    }
+                    none = a.m == -INFINITY && a.s == 0.0f;
+                    r.ref = finite_or_0(a.m), r.sub = log2f(a.s);
+                    if (rank == 0 && threadIdx.x == 0) {
+                        p.loss[at.row] = none ? INFINITY : h.cross + (r.ref - h.zref) * p.inv_tau + r.sub * kLn2;
+                        p.lse[at.row] = none ? -INFINITY : r.ref * p.inv_tau + r.sub * kLn2;
+                    }
+                }
+                if (none)
+                    r.ref = r.sub = 0.0f;  // probabilities 0 by g = 0
+                else
+                    r.g = h.weight * p.inv_tau;
+            } else if (!kSaved && rank == 0 && threadIdx.x == 0) {
+                p.loss[at.row] = 0.0f, p.lse[at.row] = 0.0f;
+            }
+            if (!dz) return r;
+            const Softmax<kSaved> q{r.ref, r.sub, kSaved ? p.inv_tau : c};
+            const uint4 *v = reinterpret_cast<const uint4 *>(smem + at.s * p.stage_bytes);
+            T *out = dz + part.head + part.v0 * n;
+            const int count = part.v1 - part.v0;
+            const bool wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+            const bool zero = r.g == 0.0f;  // whatever z holds
+            const int odd = part.edge(threadIdx.x, p.vocab, rank);
+            if (odd >= 0) store_f32(dz + odd, zero ? 0.0f : r.g * q(load_f32(z + odd)));
+#pragma unroll 2
+            for (int i = threadIdx.x; i < count; i += kMain) {
+                float x[n];
+                unpack<T>(v[i], x);
+#pragma unroll
+                for (int j = 0; j < n; ++j) x[j] = zero ? 0.0f : r.g * q(x[j]);
+                if (wide) {
+                    st16(out + i * n, pack<T>(x));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < n; ++j) store_f32(out + i * n + j, x[j]);
+                }
+            }
+            return r;
+        };
+
+        // dz at the entries that this CTA's part holds; then the slot is free.
+        const auto entries_of = [&](const Done &r) {
+            const Header &h = header[r.e];
+            if (p.dz && h.live) {
+                const T *z = static_cast<const T *>(p.z) + r.row * p.ldz;
+                T *dz = static_cast<T *>(p.dz) + r.row * p.lddz;
+                const Row<T> part(z, p.vocab, rank, p.log_cluster);
+                const Softmax<kSaved> q{r.ref, r.sub, kSaved ? p.inv_tau : c};
+                const int32_t *top_i = reinterpret_cast<const int32_t *>(slots + r.e * 12 * entries);
+                const float *top_p = reinterpret_cast<const float *>(top_i + entries), *top_z = top_p + entries;
+                for (int j = threadIdx.x; j < p.k; j += kMain) {
+                    const int32_t i = top_i[j];
+                    if (i < 0 || !part.holds(i, rank)) continue;
+                    float sum = top_p[j];
+                    if (h.repeated) {
+                        sum = 0.0f;
+                        bool earlier = false;
+                        for (int o = 0; o < p.k; ++o)
+                            if (top_i[o] == i) {
+                                earlier |= o < j;
+                                sum += top_p[o];
+                            }
+                        if (earlier) continue;
+                    }
+                    const float first = r.g == 0.0f ? 0.0f : r.g * q(top_z[j]);
+                    store_f32(dz + i, fmaf(-(h.weight * p.inv_tau), sum, first));
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(slot_empty + 8 * r.e);
+        };
+
+        uint32_t s = 0, turn = 0, e = 0, eturn = 0, meet = 0, buf = 0;
+        Place last{-1, 0, 0, 0};
+        Done done{-1, 0, 0.0f, 0.0f, 0.0f};
+        const auto finish_and_release = [&](const Place &at, MaxSum a) {
+            done = finish(at, a);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + 8 * at.s);
+        };
+        for (int64_t row = first; row < p.rows; row += step) {
+            const Place at{row, s, e, meet};
+            mbar_wait(slot_full + 8 * e, eturn, &failed);
+            mbar_wait(full + 8 * s, turn, &failed);
+            const bool pass = !kSaved && header[e].live;
+            MaxSum a{-INFINITY, 0.0f};
+            if (pass) {
+                a = reduce_part(at);
+                if (lane == 0) partial[buf][warp] = a;
+            }
+            bar_main();
+            if (pass) {
+                a = merge_lanes<kMainWarps>(partial[buf][lane & (kMainWarps - 1)], c);
+                if (kLag) {
+                    const uint32_t bar = met + 8 * (meet % kMeets);
+                    if (threadIdx.x == 0) mbar_expect_tx(bar, 8 * K);
+                    if (threadIdx.x < K)
+                        asm volatile(
+                            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                                cluster_map(smem_u32(&pairs[meet % kMeets][rank]), threadIdx.x)),
+                            "f"(a.m), "f"(a.s), "r"(cluster_map(bar, threadIdx.x))
+                            : "memory");
+                }
+                ++meet;
+            }
+            buf ^= 1;
+            if (done.row >= 0) entries_of(done);
+            if (kLag) {
+                if (last.row >= 0) finish_and_release(last, a);
+                last = at;
+            } else {
+                finish_and_release(at, a);
+            }
+            if (++s == S) s = 0, turn ^= 1;
+            if (++e == E) e = 0, eturn ^= 1;
+        }
+        if (kLag && last.row >= 0) {
+            bar_main();
+            if (done.row >= 0) entries_of(done);
+            finish_and_release(last, {});
+        }
+        bar_main();
+        if (done.row >= 0) entries_of(done);
+    }
+    __syncthreads();
+    if (kLag) cluster_barrier();  // no CTA leaves while another may write its pair
+    if (threadIdx.x == 0 && failed && p.status) atomicOr(p.status, static_cast<unsigned int>(GAR_STATUS_TIMEOUT));
 }
 
 int check(const void *z, int32_t dtype, int64_t rows, int64_t vocab, int64_t ldz, const int32_t *index,
@@ -160,14 +604,89 @@ int check(const void *z, int32_t dtype, int64_t rows, int64_t vocab, int64_t ldz
     return GAR_OK;
 }
 
-int run(const DistillParams &p, int32_t dtype, cudaStream_t stream) {
+constexpr int64_t kStreamBytes = 16384;
+constexpr int kSharedBytes = 220 * 1024;  // of a CTA that has the SM to itself, static shared memory taken off
+
+template <typename T, bool kSaved, bool kLag>
+int launch_stream(const DistillParams &p, int64_t rows_at_once, size_t shared, cudaStream_t stream) {
+    const auto kernel = distill_stream_kernel<T, kSaved, kLag>;
+    // Clusters of 1 << i CTAs that the device holds at one time (its SMs come in groups, so it is fewer than its SMs
+    // would make; one more would run after all others), 0: not looked up yet.
+    static std::atomic<int> resident[64][4];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return fail(GAR_ECUDA, "no current device");
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kStreamThreads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kLag ? 1u << p.log_cluster : 1u;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    std::atomic<int> &known = resident[dev & 63][p.log_cluster];
+    int clusters = known.load(std::memory_order_relaxed);
+    if (clusters == 0) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
+        clusters = 1;
+        if (e == cudaSuccess && kLag) {
+            cfg.gridDim = dim3(1u << p.log_cluster);
+            cfg.dynamicSmemBytes = kSharedBytes;
+            e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+            cfg.dynamicSmemBytes = shared;
+        }
+        if (e != cudaSuccess || clusters < 1) return fail(GAR_ECUDA, "distill_stream_kernel: %s", cudaGetErrorString(e));
+        known.store(clusters, std::memory_order_relaxed);
+    }
+    if (!kLag || clusters > rows_at_once) clusters = static_cast<int>(rows_at_once);
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters) << p.log_cluster);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (e != cudaSuccess) return fail(GAR_ECUDA, "distill_stream_kernel: %s", cudaGetErrorString(e));
+    return check_launch("distill_stream_kernel");
+}
+
+template <typename T, bool kSaved>
+int launch(DistillParams &p, cudaStream_t stream) {
+    const int64_t bytes = static_cast<int64_t>(p.vocab) * sizeof(T);
+    const int slot = 12 * ((p.k + 3) & ~3);
+    int tables = 32;
+    while (tables < 2 * p.k) tables *= 2;
+    tables *= 4 * kPrepare;
+    // Slots: eight up to 24 KB, else four (three rows' entries are in use where the gradient lags).
+    p.slots = slot * kMaxSlots <= 24576 ? kMaxSlots : 4;
+    const int fixed = p.slots * slot + tables;
+    // The fewest CTAs a row whose parts fit the stages (two, or three where the gradient lags a row), and more while
+    // there are SMs without a row.
+    const auto part = [&](int K) { return (ceil_div(bytes / 16, K) + 1) * 16; };
+    const auto fits = [&](int K, int room) { return (K > 1 && !kSaved ? 3 : 2) * part(K) + fixed <= room; };
+    int K = 1;
+    while (K < kMaxCluster && !fits(K, kSharedBytes)) K *= 2;
+    while (K < kMaxCluster && p.rows * K * 2 <= sm_count() && part(K) >= 8192) K *= 2;
+    if (bytes < kStreamBytes || !fits(K, kSharedBytes)) {
+        distill_row_kernel<T, kSaved><<<static_cast<unsigned>(p.rows), kRowThreads, 0, stream>>>(p);
+        return check_launch("distill_row_kernel");
+    }
+    p.log_cluster = K == 8 ? 3 : K / 2;
+    p.stage_bytes = static_cast<int32_t>(part(K));
+    const bool lag = K > 1 && !kSaved;
+    // two CTAs an SM where two find room for their stages: one's barriers hide behind the other's passes
+    const bool two = !lag && fits(K, kSharedBytes / 2 - 2048);
+    const int room = (two ? kSharedBytes / 2 - 2048 : kSharedBytes) - fixed;
+    p.stages = room / p.stage_bytes < kMaxStages ? room / p.stage_bytes : kMaxStages;
+    p.status = device_status();
+    int64_t at_once = static_cast<int64_t>(sm_count()) * (two ? 2 : 1) / K;
+    if (at_once > p.rows) at_once = p.rows;
+    const size_t shared = static_cast<size_t>(p.stages) * p.stage_bytes + fixed;
+    if constexpr (!kSaved)
+        if (lag) return launch_stream<T, false, true>(p, at_once, shared, stream);
+    return launch_stream<T, kSaved, false>(p, at_once, shared, stream);
+}
+
+int run(DistillParams &p, int32_t dtype, cudaStream_t stream) {
     if (p.rows == 0) return GAR_OK;
-    const unsigned blocks = static_cast<unsigned>(p.rows);
-    if (dtype == GAR_F32)
-        distill_kernel<float><<<blocks, kThreads, 0, stream>>>(p);
-    else
-        distill_kernel<uint16_t><<<blocks, kThreads, 0, stream>>>(p);
-    return check_launch("distill_kernel");
+    if (dtype == GAR_F32) return p.lse_in ? launch<float, true>(p, stream) : launch<float, false>(p, stream);
+    return p.lse_in ? launch<uint16_t, true>(p, stream) : launch<uint16_t, false>(p, stream);
 }
 
 }  // namespace

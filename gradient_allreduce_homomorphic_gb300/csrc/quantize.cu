@@ -30,11 +30,6 @@ struct QuantizeParams {
     int32_t square, vec;
 };
 
-// |v|'s bits, 0 for NaN and infinities.
-__device__ __forceinline__ uint32_t finite_abs(float v) {
-    const uint32_t a = __float_as_uint(v) & 0x7FFFFFFFu;
-    return a < 0x7F800000u ? a : 0u;
-}
 // Biased exponent of the scale from amax's bits: the addition carries into the
 // exponent exactly where the significand is above 1.75.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax, int emax) {
@@ -57,6 +52,91 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
+// A thread's 8 rows x 8 columns of x as they are stored, and what both orders
+// need of them.  bf16 values stay packed (32 registers rather than 64): their
+// absolute values compare as unsigned 16-bit integers, two at a time.
+template <typename T>
+struct Patch;
+
+template <>
+struct Patch<uint16_t> {
+    static constexpr uint32_t kInf = 0x7F80u;  // bits of an infinity's absolute value, in 16-bit halves
+    uint32_t w[8][4];
+    __device__ __forceinline__ void load(int i, const uint16_t *src) {
+        const uint4 g = ld16(src);
+        w[i][0] = g.x, w[i][1] = g.y, w[i][2] = g.z, w[i][3] = g.w;
+    }
+    __device__ __forceinline__ void load_some(int i, const uint16_t *src, int64_t left) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = 2 * j < left ? src[2 * j] : 0, hi = 2 * j + 1 < left ? src[2 * j + 1] : 0;
+            w[i][j] = lo | (hi << 16);
+        }
+    }
+    __device__ __forceinline__ float value(int i, int j) const {
+        return j & 1 ? bf16_hi(w[i][j >> 1]) : bf16_lo(w[i][j >> 1]);
+    }
+    // Largest absolute values, as fp32 bits: of row i, and of every column (cmax).
+    template <bool kSanitize>
+    __device__ __forceinline__ uint32_t absw(int i, int j) const {
+        uint32_t a = w[i][j] & 0x7FFF7FFFu;
+        if (kSanitize) {
+            if ((a & 0xFFFFu) >= kInf) a &= 0xFFFF0000u;
+            if ((a >> 16) >= kInf) a &= 0xFFFFu;
+        }
+        return a;
+    }
+    template <bool kSanitize>
+    __device__ __forceinline__ void maxima(uint32_t (&rmax)[8], uint32_t (&cmax)[8]) const {
+        uint32_t c[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a = absw<kSanitize>(i, j);
+                m = __vmaxu2(m, a);
+                c[j] = __vmaxu2(c[j], a);
+            }
+            rmax[i] = max(m << 16, m & 0xFFFF0000u);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cmax[2 * j] = c[j] << 16, cmax[2 * j + 1] = c[j] & 0xFFFF0000u;
+    }
+};
+
+template <>
+struct Patch<float> {
+    uint32_t w[8][8];
+    __device__ __forceinline__ void load(int i, const float *src) {
+        const uint4 g = ld16(src), h = ld16(src + 4);
+        w[i][0] = g.x, w[i][1] = g.y, w[i][2] = g.z, w[i][3] = g.w;
+        w[i][4] = h.x, w[i][5] = h.y, w[i][6] = h.z, w[i][7] = h.w;
+    }
+    __device__ __forceinline__ void load_some(int i, const float *src, int64_t left) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[i][j] = j < left ? __float_as_uint(src[j]) : 0u;
+    }
+    __device__ __forceinline__ float value(int i, int j) const { return __uint_as_float(w[i][j]); }
+    template <bool kSanitize>
+    __device__ __forceinline__ void maxima(uint32_t (&rmax)[8], uint32_t (&cmax)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cmax[j] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t a = w[i][j] & 0x7FFFFFFFu;
+                if (kSanitize && a >= 0x7F800000u) a = 0;
+                m = max(m, a);
+                cmax[j] = max(cmax[j], a);
+            }
+            rmax[i] = m;
+        }
+    }
+};
+
 // One CTA per 128 x 128 tile, x read once for both orders.  Each half-warp
 // owns 8 consecutive rows and each of its lanes 8 consecutive columns, so a
 // row's maximum is a shuffle over 16 lanes, a column's is a maximum over the
@@ -64,61 +144,58 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
 // a thread's 8 codes of a column are 8 consecutive bytes of the transposed
 // tile.  The transposed tile goes through shared memory; its 8-byte groups
 // are exchanged (group h of column c sits at h ^ (c / 8)) so that neither the
-// stores nor the loads conflict.
+// stores nor the loads conflict.  A tile with a NaN or an infinity (one vote
+// per tile tells) takes its maxima again without them.
 template <typename T, bool kE5M2>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constant__ QuantizeParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) quantize_kernel(const __grid_constant__ QuantizeParams p) {
     __shared__ uint32_t colmax[16][kTile];
     __shared__ __align__(16) uint8_t tile[kTile * kTile];
-    __shared__ uint32_t wmax[kThreads / 32];
     const int tid = threadIdx.x, half = tid >> 4, hl = tid & 15;
     const int64_t tr = blockIdx.x / p.tiles_c, tc = blockIdx.x % p.tiles_c;
     const int64_t row0 = tr * kTile + half * 8, col0 = tc * kTile + hl * 8;
-    const T *x = static_cast<const T *>(p.x);
-    float v[8][8];
+    const T *x = static_cast<const T *>(p.x) + row0 * p.ldx + col0;
+    Patch<T> v;
     const int64_t left = p.cols - col0;
+    if (p.vec && row0 + 8 <= p.rows && left >= 8) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t r = row0 + i;
-        const T *src = x + r * p.ldx + col0;
-        if (p.vec && r < p.rows && left >= 8) {
-            if (sizeof(T) == 2) {
-                const uint4 g = ld16(src);
-                v[i][0] = bf16_lo(g.x), v[i][1] = bf16_hi(g.x), v[i][2] = bf16_lo(g.y), v[i][3] = bf16_hi(g.y);
-                v[i][4] = bf16_lo(g.z), v[i][5] = bf16_hi(g.z), v[i][6] = bf16_lo(g.w), v[i][7] = bf16_hi(g.w);
-            } else {
-                const uint4 g = ld16(src), h = ld16(src + 4);
-                v[i][0] = __uint_as_float(g.x), v[i][1] = __uint_as_float(g.y);
-                v[i][2] = __uint_as_float(g.z), v[i][3] = __uint_as_float(g.w);
-                v[i][4] = __uint_as_float(h.x), v[i][5] = __uint_as_float(h.y);
-                v[i][6] = __uint_as_float(h.z), v[i][7] = __uint_as_float(h.w);
-            }
-        } else {
+        for (int i = 0; i < 8; ++i) v.load(i, x + i * p.ldx);
+    } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = r < p.rows && j < left ? load_f32(src + j) : 0.0f;
-        }
+        for (int i = 0; i < 8; ++i) v.load_some(i, x + i * p.ldx, row0 + i < p.rows ? left : 0);
     }
-    uint32_t rmax[8];
+    uint32_t rmax[8], cmax[8];
+    v.template maxima<false>(rmax, cmax);
+    uint32_t most = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, finite_abs(v[i][j]));
-        rmax[i] = m;
-    }
+    for (int i = 0; i < 8; ++i) most = max(most, rmax[i]);
+    const bool bad = __syncthreads_or(most >= 0x7F800000u);
+    if (bad) v.template maxima<true>(rmax, cmax);
     uint32_t cbyte[8], rbyte[8];
     if (p.square) {
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = max(m, rmax[i]);
         m = __reduce_max_sync(0xFFFFFFFFu, m);
-        if ((tid & 31) == 0) wmax[tid >> 5] = m;
+        if ((tid & 31) == 0) colmax[0][tid >> 5] = m;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) m = max(m, wmax[w]);
+        for (int w = 0; w < kThreads / 32; ++w) m = max(m, colmax[0][w]);
         const uint32_t b = scale_byte(m, p.emax);
 #pragma unroll
         for (int i = 0; i < 8; ++i) rbyte[i] = cbyte[i] = b;
     } else {
+        if (p.qt) {
+#pragma unroll
+            for (int j = 0; j < 8; j += 4)
+                *reinterpret_cast<uint4 *>(&colmax[half][hl * 8 + j]) = make_uint4(cmax[j], cmax[j + 1], cmax[j + 2], cmax[j + 3]);
+            __syncthreads();
+            if (tid < kTile) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int h = 0; h < 16; ++h) m = max(m, colmax[h][tid]);
+                colmax[0][tid] = m;  // only this thread reads or writes this column here
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             uint32_t m = rmax[i];
@@ -127,39 +204,41 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
             rbyte[i] = scale_byte(m, p.emax);
         }
         if (p.qt) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m = max(m, finite_abs(v[i][j]));
-                colmax[half][hl * 8 + j] = m;
-            }
-            __syncthreads();
-            if (tid < kTile) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int h = 0; h < 16; ++h) m = max(m, colmax[h][tid]);
-                colmax[0][tid] = m;  // only this thread reads or writes this column here
-            }
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < 8; ++j) cbyte[j] = scale_byte(colmax[0][hl * 8 + j], p.emax);
         }
     }
-    // an infinity times zero makes it a NaN, whose code is the format's NaN
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = __fmaf_rn(v[i][j], 0.0f, v[i][j]);
+    // the value times a power of two; a NaN or (times zero) an infinity becomes the code NaN
+    const auto scaled = [&](int i, int j, float f) {
+        const float y = v.value(i, j);
+        return bad ? __fmaf_rn(y, 0.0f, y * f) : y * f;
+    };
 
+    if (p.qt) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float f = inverse_scale(cbyte[j]);
+            uint2 w;
+            w.x = pack4<kE5M2>(scaled(0, j, f), scaled(1, j, f), scaled(2, j, f), scaled(3, j, f));
+            w.y = pack4<kE5M2>(scaled(4, j, f), scaled(5, j, f), scaled(6, j, f), scaled(7, j, f));
+            *reinterpret_cast<uint2 *>(&tile[(hl * 8 + j) * kTile + ((half ^ hl) << 3)]) = w;
+        }
+        const int64_t tiles_r = (p.rows + kTile - 1) / kTile;
+        if (half == 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < left) store_scale(p.scale_t, p.cols, col0 + j, tr, tiles_r, cbyte[j]);
+        }
+    }
     if (p.q) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t r = row0 + i;
             const float f = inverse_scale(rbyte[i]);
             uint2 w;
-            w.x = pack4<kE5M2>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f);
-            w.y = pack4<kE5M2>(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f);
+            w.x = pack4<kE5M2>(scaled(i, 0, f), scaled(i, 1, f), scaled(i, 2, f), scaled(i, 3, f));
+            w.y = pack4<kE5M2>(scaled(i, 4, f), scaled(i, 5, f), scaled(i, 6, f), scaled(i, 7, f));
             if (r < p.rows) {
                 uint8_t *dst = p.q + r * p.ldq + col0;
                 if (left >= 8) {
@@ -174,20 +253,6 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
         }
     }
     if (p.qt) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float f = inverse_scale(cbyte[j]);
-            uint2 w;
-            w.x = pack4<kE5M2>(v[0][j] * f, v[1][j] * f, v[2][j] * f, v[3][j] * f);
-            w.y = pack4<kE5M2>(v[4][j] * f, v[5][j] * f, v[6][j] * f, v[7][j] * f);
-            *reinterpret_cast<uint2 *>(&tile[(hl * 8 + j) * kTile + ((half ^ hl) << 3)]) = w;
-        }
-        const int64_t tiles_r = (p.rows + kTile - 1) / kTile;
-        if (half == 0) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < left) store_scale(p.scale_t, p.cols, col0 + j, tr, tiles_r, cbyte[j]);
-        }
         __syncthreads();
         const int part = tid & 7;  // 16 bytes of a column: row groups 2 part and 2 part + 1
         const int64_t r = tr * kTile + part * 16;

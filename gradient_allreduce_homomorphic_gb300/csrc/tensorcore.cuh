@@ -56,7 +56,7 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 // it stays uniform across its warp; only what must not go on (the issue of
 // copies) looks at the returned value.
 constexpr uint64_t kWaitNs = 2000000000ull;
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *failed) {
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *failed) {
     const uint64_t t0 = global_ns();
     while (!*failed && global_ns() - t0 < kWaitNs)
         for (int i = 0; i < 64; ++i)

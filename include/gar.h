@@ -720,7 +720,7 @@ int gar_fp8_matmul(const uint8_t *a, int64_t lda, const uint8_t *a_scale, int32_
  *   dz_v = weight / tau * (exp(z_v / tau - lse) - sum of p_j with index_j = v)
  * An entry is present if its index lies in [0, vocab) and its logit is above
  * -inf; an index may occur more than once.  A row of weight 0 or without an
- * entry has loss 0, lse 0 and gradient 0, and its z is not read.  A student
+ * entry has loss 0, lse 0 and gradient 0, whatever its z.  A student
  * logit of -inf has probability 0 (loss +inf where the teacher gives it any).
  *   z            device, rows x vocab fp32 or bf16 (dtype), row stride ldz
  *   index        device, [rows, k] int32, 1 <= k <= 1024
