@@ -12,17 +12,27 @@
 // not matter), a second the gradient and d_t.  sum_e p_te = 1, so c may be
 // shifted by any constant; the mean k N / E is taken off, which removes the
 // cancellation of c_e - d_t for a router near balance.
+//
+// A token is held by L lanes of a warp, V of its logits each, in runs of 16
+// bytes that neighbouring lanes hold in turn.  A warp works on 32 / L tokens at
+// a time: with V = 32 most instructions serve several tokens and a warp has 4
+// KB of loads in flight; with V = 8 few tokens spread over more warps.  Bound by HBM for many experts (z is read twice, the second
+// time in part from L2), by the selection's instructions for many choices.
+#include <algorithm>
+
 #include "common.cuh"
 #include "fp8.cuh"
 
 namespace gar {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kMaxExperts = 1024;
-constexpr int kPerLane = kMaxExperts / 32;
 constexpr int kMaxChoices = 32;
 constexpr int kMaxBlocks = 4096;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kOneThreads = 512;           // the one-CTA kernel
+constexpr int kOneCounts = 4096;           // its counts: workers x experts
+constexpr float kLog2e = 1.44269504088896340736f;
 
 struct BalanceParams {
     const void *z[GAR_MAX_WORKERS];
@@ -31,168 +41,493 @@ struct BalanceParams {
     const uint8_t *valid[GAR_MAX_WORKERS];
     int64_t tokens, ldz, lddz;
     int32_t P, experts, k, has_valid, has_grad;
+    int32_t wide, dwide; // whether rows of z, of dz may be accessed 16 bytes at a time
     float alpha;
-    int32_t *counts;      // [P, experts]
-    int32_t *n_tokens;    // workspace: tokens that count, per worker
-    double *partial;      // workspace: sum of d_t per CTA
+    int32_t *counts;     // [P, experts]
+    uint32_t *seen;      // workspace: tokens that count; CTAs done
+    float *partial;      // workspace: sum of d_t per CTA
     float *loss;
 };
 
-// A token's logits: lane l holds experts l, l + 32, ...; -inf past the end.
-template <typename T>
-__device__ __forceinline__ void load_token(const BalanceParams &p, int w, int64_t t, int lane, int per, float *v) {
-    const T *z = static_cast<const T *>(p.z[w]) + t * p.ldz;
-    for (int i = 0; i < per; ++i) {
-        const int e = i * 32 + lane;
-        v[i] = e < p.experts ? load_f32(z + e) : -INFINITY;
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+// The lanes that share a lane's token.
+template <int L>
+__device__ __forceinline__ uint32_t group_mask(int lane) {
+    return L == 32 ? 0xFFFFFFFFu : ((1u << (L & 31)) - 1u) << (lane & ~(L - 1));
+}
+
+// Expert of a lane's i-th value, the values being of type T.
+template <typename T, int L>
+__device__ __forceinline__ int expert(int sub, int i) {
+    constexpr int kRun = 16 / sizeof(T);
+    return i / kRun * (kRun * L) + sub * kRun + i % kRun;
+}
+
+// A lane's logits of one token; -inf past the last expert.
+template <typename T, int L, int V>
+__device__ __forceinline__ void load_token(const T *z, int sub, int experts, bool wide, float (&v)[V]) {
+    constexpr int kRun = 16 / sizeof(T);
+#pragma unroll
+    for (int r = 0; r < V; r += kRun) {
+        const int e0 = expert<T, L>(sub, r);
+        if (wide && e0 + kRun <= experts) {
+            const uint4 g = *reinterpret_cast<const uint4 *>(z + e0);
+            if constexpr (sizeof(T) == 2) {
+                v[r] = bf16_lo(g.x), v[r + 1] = bf16_hi(g.x), v[r + 2] = bf16_lo(g.y), v[r + 3] = bf16_hi(g.y);
+                v[r + 4] = bf16_lo(g.z), v[r + 5] = bf16_hi(g.z), v[r + 6] = bf16_lo(g.w), v[r + 7] = bf16_hi(g.w);
+            } else {
+                v[r] = __uint_as_float(g.x), v[r + 1] = __uint_as_float(g.y);
+                v[r + 2] = __uint_as_float(g.z), v[r + 3] = __uint_as_float(g.w);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) v[r + j] = e0 + j < experts ? load_f32(z + e0 + j) : -INFINITY;
+        }
+    }
+}
+template <typename T, int L, int V>
+__device__ __forceinline__ void store_token(T *dz, int sub, int experts, bool wide, const float (&v)[V]) {
+    constexpr int kRun = 16 / sizeof(T);
+#pragma unroll
+    for (int r = 0; r < V; r += kRun) {
+        const int e0 = expert<T, L>(sub, r);
+        if (wide && e0 + kRun <= experts) {
+            uint4 g;
+            if constexpr (sizeof(T) == 2)
+                g = make_uint4(pack_bf16x2(v[r], v[r + 1]), pack_bf16x2(v[r + 2], v[r + 3]), pack_bf16x2(v[r + 4], v[r + 5]),
+                               pack_bf16x2(v[r + 6], v[r + 7]));
+            else
+                g = make_uint4(__float_as_uint(v[r]), __float_as_uint(v[r + 1]), __float_as_uint(v[r + 2]), __float_as_uint(v[r + 3]));
+            st16(dz + e0, g);  // streaming: z, which is read again, is worth more in L2
+        } else {
+#pragma unroll
+            for (int j = 0; j < kRun; ++j)
+                if (e0 + j < experts) store_f32(dz + e0 + j, v[r + j]);
+        }
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) balance_count_kernel(const __grid_constant__ BalanceParams p) {
+// A NaN compares false and is passed over by fmaxf, so it is never chosen.
+
+// A token's choices by k rounds of: the group's largest value, its lowest
+// expert, that value taken out.  v is used up.  About 3 V + 2 log2 L + 15
+// instructions a round for 32 / L tokens.
+template <typename T, int L, int V>
+__device__ __forceinline__ void choose_by_rounds(float (&v)[V], int sub, int lane, int k, bool live, int32_t *out, int32_t *cnt) {
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
+    for (int c = 0; c < k; ++c) {
+        const float best = group_max<L>(m);
+        const bool some = best > -INFINITY;
+        uint32_t at = 0xFFFFFFFFu;
+        if (some && m == best) {
+#pragma unroll
+            for (int i = V - 1; i >= 0; --i)
+                if (v[i] == best) at = expert<T, L>(sub, i);
+        }
+        uint32_t lowest = at;
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) lowest = min(lowest, __shfl_xor_sync(0xFFFFFFFFu, lowest, o));
+        if (some && at == lowest) {
+            m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (expert<T, L>(sub, i) == static_cast<int>(at)) v[i] = -INFINITY;
+                m = fmaxf(m, v[i]);
+            }
+            out[c] = static_cast<int32_t>(at);
+            atomicAdd(cnt + at, 1);
+        }
+        if (!some && live && sub == 0) out[c] = -1;
+    }
+}
+
+// The same in fewer instructions where a token takes eight lanes or more: the
+// k-th largest of its 4 L maxima of 8 values bounds the k-th largest value from
+// below, so the few values that reach it (k and a half in the mean, for k = 8
+// of 256) hold the choices; they are listed in shared memory and each is
+// ranked against the others.  Tokens with more of them than the list holds
+// (many equal values), or with fewer such maxima than choices, are reported
+// for choose_by_rounds.
+constexpr int kList = 32;
+// Order of choice as an integer: larger value first, then the lower expert.
+__device__ __forceinline__ uint64_t choice_key(float v, uint32_t e) {
+    uint32_t u = __float_as_uint(v + 0.0f);  // one zero
+    u ^= u >> 31 ? 0xFFFFFFFFu : 0x80000000u;
+    return static_cast<uint64_t>(u) << 32 | (0xFFFFFFFFu - e);
+}
+template <typename T, int L>
+__device__ __forceinline__ bool choose_by_bound(const float (&v)[32], const T *z, int sub, int lane, int k, bool live, int32_t *out,
+                                                int32_t *cnt, uint64_t *list) {
+    float g[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        g[j] = v[8 * j];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) g[j] = fmaxf(g[j], v[8 * j + i]);
+    }
+    float bound = 0.0f;
+    for (int c = 0; c < k; ++c) {
+        bound = group_max<L>(fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3])));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (g[j] == bound) g[j] = -INFINITY;
+    }
+    uint32_t mask = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (v[i] >= bound) mask |= 1u << i;
+    const int n = __popc(mask);
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, upto, o, L);
+        if (sub >= o) upto += u;
+    }
+    const int total = __shfl_sync(0xFFFFFFFFu, upto, L - 1, L);
+    const bool good = live && bound > -INFINITY && total <= kList;
+    list += lane / L * kList;
+    if (good) {
+        int at = upto - n;
+        while (mask) {
+            const int i = __ffs(mask) - 1;
+            mask &= mask - 1;
+            const int e = expert<T, L>(sub, i);
+            list[at++] = choice_key(load_f32(z + e), e);
+        }
+    }
+    __syncwarp();
+    if (good) {
+        for (int own = sub; own < total; own += L) {
+            const uint64_t mine = list[own];
+            int rank = 0;
+            for (int j = 0; j < total; ++j) rank += list[j] > mine;
+            if (rank < k) {
+                const int e = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(mine));
+                out[rank] = e;
+                atomicAdd(cnt + e, 1);
+            }
+        }
+    }
+    __syncwarp();
+    return good;
+}
+
+// Choices of the tokens of one warp; adds to cnt (shared memory) and returns,
+// in each lane that leads a group, whether its token counts.
+template <typename T, int L, int V>
+__device__ __forceinline__ bool choose(const BalanceParams &p, int w, int64_t t, int sub, int lane, int32_t *cnt, uint64_t *list) {
+    const bool here = t < p.tokens, live = here && (!p.has_valid || p.valid[w][t] != 0);
+    int32_t *out = here ? p.choice[w] + t * p.k : nullptr;
+    const T *z = static_cast<const T *>(p.z[w]) + (live ? t : 0) * p.ldz;
+    float v[V];
+    if (live) {
+        load_token<T, L, V>(z, sub, p.experts, p.wide, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = -INFINITY;
+        for (int c = sub; here && c < p.k; c += L) out[c] = -1;
+    }
+    bool some = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) some |= v[i] > -INFINITY;
+    some = (__ballot_sync(0xFFFFFFFFu, some) & group_mask<L>(lane)) != 0;
+    if constexpr (L >= 8 && V == 32) {
+        bool good = !live;
+        if (p.k > 2) good |= choose_by_bound<T, L>(v, z, sub, lane, p.k, live, out, cnt, list);
+        if (__any_sync(0xFFFFFFFFu, !good)) {
+            if (good) {  // done: nothing left to choose
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = -INFINITY;
+            }
+            choose_by_rounds<T, L, V>(v, sub, lane, p.k, live && !good, out, cnt);
+        }
+    } else {
+        choose_by_rounds<T, L, V>(v, sub, lane, p.k, live, out, cnt);
+    }
+    return some && sub == 0;
+}
+
+// Gradient of one warp's tokens; returns d_t in each lane that leads a group.
+template <typename T, int L, int V>
+__device__ __forceinline__ float gradient(const BalanceParams &p, int w, int64_t t, int sub, const float (&c)[V], float coef) {
+    const bool here = t < p.tokens;
+    bool live = here && (!p.has_valid || p.valid[w][t] != 0);
+    float v[V];
+    if (live) {
+        load_token<T, L, V>(static_cast<const T *>(p.z[w]) + t * p.ldz, sub, p.experts, p.wide, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = -INFINITY;
+    }
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
+    m = group_max<L>(m);
+    live = live && m > -INFINITY;
+    const float r = live ? m : 0.0f;
+    float s = 0.0f, d = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float x;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"((v[i] - r) * kLog2e));
+        v[i] = x;
+        s += x;
+        d = fmaf(x, c[i], d);
+    }
+    s = group_sum<L>(s);
+    d = group_sum<L>(d);
+    d = live ? d / s : 0.0f;
+    const float f = live ? coef / s : 0.0f;
+    if (here && p.has_grad) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = live ? f * v[i] * (c[i] - d) : 0.0f;
+        store_token<T, L, V>(static_cast<T *>(p.dz[w]) + t * p.lddz, sub, p.experts, p.dwide, v);
+    }
+    return sub == 0 ? d : 0.0f;
+}
+
+// A CTA's sum of integers, the same value in every thread.
+template <int kN>
+__device__ __forceinline__ int64_t cta_count(int64_t v, int64_t *scratch) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = scratch[threadIdx.x & (kN / 32 - 1)];
+#pragma unroll
+    for (int o = kN / 64; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// alpha E / (k N^2), and the loss from the sum of d_t in which c_e lacked its
+// mean (choices / E).  In fp32: GB300 has few fp64 units, and one division on
+// them takes longer than a launch's other arithmetic.
+__device__ __forceinline__ float loss_scale(const BalanceParams &p, int64_t n) {
+    const float f = static_cast<float>(n);
+    return n > 0 ? p.alpha * static_cast<float>(p.experts) / static_cast<float>(p.k) / f / f : 0.0f;
+}
+__device__ __forceinline__ float loss_of(const BalanceParams &p, float sum, int64_t n, int64_t choices) {
+    return loss_scale(p, n) * (sum + static_cast<float>(choices) / static_cast<float>(p.experts) * static_cast<float>(n));
+}
+// c_e less its mean: the integer E c_e - choices, rounded once, over E.
+__device__ __forceinline__ float centred(int32_t count, int64_t choices, int experts) {
+    return __fdividef(static_cast<float>(static_cast<int64_t>(count) * experts - choices), static_cast<float>(experts));
+}
+
+// Three launches, the second and third of which may begin before the one ahead
+// of them ends (programmatic dependent launch) and wait before they use what
+// it wrote.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__global__ void __launch_bounds__(kThreads) balance_zero_kernel(int32_t *counts, int n, uint32_t *seen) {
+    const int i = blockIdx.x * kThreads + threadIdx.x;
+    if (i < n) counts[i] = 0;
+    if (i < 2) seen[i] = 0;
+    let_next_start();
+}
+
+template <typename T, int L, int V>
+__global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_constant__ BalanceParams p) {
     __shared__ int32_t cnt[kMaxExperts];
-    __shared__ int32_t seen;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = blockIdx.y;
-    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) cnt[e] = 0;
+    __shared__ uint64_t list[L >= 8 && V == 32 ? kWarps : 1][32 / L * kList];
+    __shared__ uint32_t seen;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = blockIdx.y, sub = lane & (L - 1);
+    for (int e = threadIdx.x; e < p.experts; e += kThreads) cnt[e] = 0;
     if (threadIdx.x == 0) seen = 0;
     __syncthreads();
-    const int per = (p.experts + 31) / 32;
-    float v[kPerLane];
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.tokens;
-         t += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const bool valid = !p.has_valid || p.valid[w][t] != 0;
-        int32_t *out = p.choice[w] + t * p.k;
-        if (!valid) {
-            if (lane < p.k) out[lane] = -1;
-            continue;
-        }
-        load_token<T>(p, w, t, lane, per, v);
-        bool some = false;
-        for (int i = 0; i < per; ++i) some |= !(v[i] == -INFINITY);
-        some = __any_sync(0xFFFFFFFFu, some);
-        if (some && lane == 0) atomicAdd(&seen, 1);
-        for (int c = 0; c < p.k; ++c) {
-            float best = -INFINITY;
-            int at = 0x7FFFFFFF;
-            for (int i = 0; i < per; ++i)
-                if (v[i] > best) best = v[i], at = i * 32 + lane;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const float u = __shfl_xor_sync(0xFFFFFFFFu, best, o);
-                const int a = __shfl_xor_sync(0xFFFFFFFFu, at, o);
-                if (u > best || (u == best && a < at)) best = u, at = a;
-            }
-            const bool found = at != 0x7FFFFFFF;
-            if (lane == 0) {
-                out[c] = found ? at : -1;
-                if (found) atomicAdd(&cnt[at], 1);
-            }
-            if (found && (at & 31) == lane) v[at >> 5] = -INFINITY;
-        }
-    }
+    constexpr int kPerWarp = 32 / L;
+    uint32_t mine = 0;
+    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kPerWarp; t0 < p.tokens;
+         t0 += static_cast<int64_t>(gridDim.x) * kWarps * kPerWarp)
+        mine += choose<T, L, V>(p, w, t0 + lane / L, sub, lane, cnt, list[L >= 8 && V == 32 ? warp : 0]);
+    mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+    if (lane == 0 && mine) atomicAdd(&seen, mine);
     __syncthreads();
-    for (int e = threadIdx.x; e < p.experts; e += blockDim.x)
+    let_next_start();
+    wait_for_previous();
+    for (int e = threadIdx.x; e < p.experts; e += kThreads)
         if (cnt[e]) atomicAdd(&p.counts[w * p.experts + e], cnt[e]);
-    if (threadIdx.x == 0 && seen) atomicAdd(&p.n_tokens[w], seen);
+    if (threadIdx.x == 0 && seen) atomicAdd(p.seen, seen);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) balance_grad_kernel(const __grid_constant__ BalanceParams p) {
-    __shared__ float c[kMaxExperts];
-    __shared__ double wsum[kWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = blockIdx.y;
-    int64_t n = 0;
-    for (int i = 0; i < p.P; ++i) n += p.n_tokens[i];
-    int64_t all = 0;  // choices made: k N, or fewer where a token had fewer experts to choose from
-    for (int e = 0; e < p.experts; ++e)
-        for (int i = 0; i < p.P; ++i) all += p.counts[i * p.experts + e];
-    const double mean = static_cast<double>(all) / p.experts;
-    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) {
-        int64_t s = 0;
+template <typename T, int L, int V>
+__global__ void __launch_bounds__(kThreads) balance_grad_kernel(const __grid_constant__ BalanceParams p) {
+    __shared__ int32_t all[kMaxExperts];
+    __shared__ float dsum[kWarps];
+    __shared__ int64_t isum[kWarps];
+    __shared__ float coef;
+    __shared__ bool last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = blockIdx.y, sub = lane & (L - 1);
+    wait_for_previous();
+    const int64_t n = *p.seen;
+    if (threadIdx.x == 0) coef = loss_scale(p, n);
+    int64_t choices = 0;
+    for (int e = threadIdx.x; e < p.experts; e += kThreads) {
+        int32_t s = 0;
         for (int i = 0; i < p.P; ++i) s += p.counts[i * p.experts + e];
-        c[e] = static_cast<float>(static_cast<double>(s) - mean);
+        all[e] = s;
+        choices += s;
     }
-    __syncthreads();
-    const int per = (p.experts + 31) / 32;
-    const double coef = n > 0 ? static_cast<double>(p.alpha) * p.experts / (static_cast<double>(p.k) * n * n) : 0.0;
-    const float fcoef = static_cast<float>(coef);
-    float v[kPerLane];
-    double sum = 0.0;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.tokens;
-         t += static_cast<int64_t>(gridDim.x) * kWarps) {
-        T *dz = p.has_grad ? static_cast<T *>(p.dz[w]) + t * p.lddz : nullptr;
-        bool live = !p.has_valid || p.valid[w][t] != 0;
-        float m = -INFINITY;
-        if (live) {
-            load_token<T>(p, w, t, lane, per, v);
-            bool some = false;
-            for (int i = 0; i < per; ++i) m = fmaxf(m, v[i]), some |= !(v[i] == -INFINITY);
+    choices = cta_count<kThreads>(choices, isum);
+    float c[V];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            live = __any_sync(0xFFFFFFFFu, some);
-        }
-        if (!live) {
-            if (dz)
-                for (int e = lane; e < p.experts; e += 32) store_f32(dz + e, 0.0f);
-            continue;
-        }
-        float s = 0.0f, d = 0.0f;
-        for (int i = 0; i < per; ++i) {
-            const int e = i * 32 + lane;
-            v[i] = expf(v[i] - m);
-            s += v[i];
-            if (e < p.experts) d += v[i] * c[e];
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-            d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-        }
-        d /= s;
-        sum += d;
-        const float f = fcoef / s;
-        if (dz)
-            for (int i = 0; i < per; ++i) {
-                const int e = i * 32 + lane;
-                if (e < p.experts) store_f32(dz + e, f * v[i] * (c[e] - d));
-            }
+    for (int i = 0; i < V; ++i) {
+        const int e = expert<T, L>(sub, i);
+        c[i] = e < p.experts ? centred(all[e], choices, p.experts) : 0.0f;
     }
-    if (lane == 0) wsum[warp] = sum;
+    constexpr int kPerWarp = 32 / L;
+    float sum = 0.0f;
+    // backwards: what the counting pass read last is still in L2
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps * kPerWarp;
+    const int64_t own = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kPerWarp;
+    for (int64_t t0 = own + (p.tokens - 1 - own) / stride * stride; own < p.tokens && t0 >= 0; t0 -= stride)
+        sum += gradient<T, L, V>(p, w, t0 + lane / L, sub, c, coef);
+    sum = group_sum<32>(sum);
+    if (lane == 0) dsum[warp] = sum;
     __syncthreads();
+    const uint32_t blocks = gridDim.x * gridDim.y;
     if (threadIdx.x == 0) {
-        double s = 0.0;
-        for (int i = 0; i < kWarps; ++i) s += wsum[i];
+        float s = 0.0f;
+        for (int i = 0; i < kWarps; ++i) s += dsum[i];
         p.partial[blockIdx.y * gridDim.x + blockIdx.x] = s;
+        __threadfence();
+        last = atomicAdd(p.seen + 1, 1u) == blocks - 1;
+    }
+    __syncthreads();
+    if (last) {  // the sums of all CTAs, in their order
+        __threadfence();
+        float s = 0.0f;
+        for (uint32_t i = threadIdx.x; i < blocks; i += kThreads) s += __ldcg(p.partial + i);
+        s = group_sum<32>(s);
+        if (lane == 0) dsum[warp] = s;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int i = 1; i < kWarps; ++i) s += dsum[i];
+            *p.loss = loss_of(p, s, n, choices);
+        }
     }
 }
 
-__global__ void balance_loss_kernel(const __grid_constant__ BalanceParams p, int blocks) {
-    __shared__ double acc[256];
-    int64_t n = 0, all = 0;
-    for (int i = 0; i < p.P; ++i) n += p.n_tokens[i];
-    for (int i = 0; i < p.P * p.experts; ++i) all += p.counts[i];
-    double s = 0.0;
-    for (int i = threadIdx.x; i < blocks; i += 256) s += p.partial[i];
-    acc[threadIdx.x] = s;
+// Few tokens: everything in one CTA, whose barriers cost less than launches.
+template <typename T, int L, int V>
+__global__ void __launch_bounds__(kOneThreads) balance_one_kernel(const __grid_constant__ BalanceParams p) {
+    constexpr int kOneWarps = kOneThreads / 32;
+    __shared__ int32_t cnt[kOneCounts];
+    __shared__ int32_t all[kMaxExperts];
+    __shared__ float dsum[kOneWarps];
+    __shared__ int64_t isum[kOneWarps];
+    __shared__ float coef;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (L - 1);
+    for (int e = threadIdx.x; e < p.P * p.experts; e += kOneThreads) cnt[e] = 0;
+    __syncthreads();
+    constexpr int kPerWarp = 32 / L;
+    const int chunks = static_cast<int>((p.tokens + kPerWarp - 1) / kPerWarp), items = chunks * p.P;
+    int64_t n = 0;
+    for (int i = warp; i < items; i += kOneWarps) {
+        const int w = i / chunks;
+        n += choose<T, L, V>(p, w, static_cast<int64_t>(i - w * chunks) * kPerWarp + lane / L, sub, lane, cnt + w * p.experts, nullptr);
+    }
+    n = cta_count<kOneThreads>(n, isum);
+    if (threadIdx.x == 0) coef = loss_scale(p, n);
+    int64_t choices = 0;
+    for (int e = threadIdx.x; e < p.experts; e += kOneThreads) {
+        int32_t s = 0;
+        for (int i = 0; i < p.P; ++i) s += cnt[i * p.experts + e];
+        all[e] = s;
+        choices += s;
+    }
+    for (int e = threadIdx.x; e < p.P * p.experts; e += kOneThreads) p.counts[e] = cnt[e];
+    choices = cta_count<kOneThreads>(choices, isum);
+    float c[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = expert<T, L>(sub, i);
+        c[i] = e < p.experts ? centred(all[e], choices, p.experts) : 0.0f;
+    }
+    float sum = 0.0f;
+    for (int i = warp; i < items; i += kOneWarps) {
+        const int w = i / chunks;
+        sum += gradient<T, L, V>(p, w, static_cast<int64_t>(i - w * chunks) * kPerWarp + lane / L, sub, c, coef);
+    }
+    sum = group_sum<32>(sum);
+    if (lane == 0) dsum[warp] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
-        double t = 0.0;
-        for (int i = 0; i < 256; ++i) t += acc[i];
-        const double mean = static_cast<double>(all) / p.experts;
-        const double coef = n > 0 ? static_cast<double>(p.alpha) * p.experts / (static_cast<double>(p.k) * n * n) : 0.0;
-        *p.loss = static_cast<float>(coef * (t + mean * static_cast<double>(n)));
+        float s = 0.0f;
+        for (int i = 0; i < kOneWarps; ++i) s += dsum[i];
+        *p.loss = loss_of(p, s, n, choices);
     }
+}
+
+template <typename T, int L, int V>
+int launch(const BalanceParams &p, cudaStream_t stream) {
+    // One CTA up to four tokens a lane group: measured level with three launches at about eight.
+    if constexpr (V == 8)
+        if (p.tokens * p.P * L <= kOneThreads * 4 && p.P * p.experts <= kOneCounts) {
+            balance_one_kernel<T, L, V><<<1, kOneThreads, 0, stream>>>(p);
+            return check_launch("balance_one_kernel");
+        }
+    const int n = p.P * p.experts;
+    balance_zero_kernel<<<(n + kThreads - 1) / kThreads, kThreads, 0, stream>>>(p.counts, n, p.seen);
+    if (int rc = check_launch("balance_zero_kernel")) return rc;
+    // as many CTAs as the SMs hold (registers), for each begins with the totals of all counts
+    const auto blocks = [&](int per_sm) {
+        const int64_t work = ceil_div(p.tokens, int64_t{kWarps} * (32 / L));
+        const int64_t most = std::min(ceil_div(static_cast<int64_t>(sm_count()) * per_sm, p.P), int64_t{kMaxBlocks} / p.P);
+        return static_cast<unsigned>(std::max(std::min(work, most), int64_t{1}));
+    };
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks(V == 32 ? 3 : 6), static_cast<unsigned>(p.P));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, balance_count_kernel<T, L, V>, p);
+    if (e != cudaSuccess) return fail(GAR_ECUDA, "balance_count_kernel: %s", cudaGetErrorString(e));
+    if (int rc = check_launch("balance_count_kernel")) return rc;
+    cfg.gridDim = dim3(blocks(V == 32 ? 2 : 4), static_cast<unsigned>(p.P));
+    e = cudaLaunchKernelEx(&cfg, balance_grad_kernel<T, L, V>, p);
+    if (e != cudaSuccess) return fail(GAR_ECUDA, "balance_grad_kernel: %s", cudaGetErrorString(e));
+    return check_launch("balance_grad_kernel");
 }
 
 template <typename T>
-int launch(const BalanceParams &p, int blocks, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(p.P));
-    balance_count_kernel<T><<<grid, kWarps * 32, 0, stream>>>(p);
-    if (int rc = check_launch("balance_count_kernel")) return rc;
-    balance_grad_kernel<T><<<grid, kWarps * 32, 0, stream>>>(p);
-    if (int rc = check_launch("balance_grad_kernel")) return rc;
-    balance_loss_kernel<<<1, 256, 0, stream>>>(p, blocks * p.P);
-    return check_launch("balance_loss_kernel");
+int dispatch(const BalanceParams &p, cudaStream_t stream) {
+    // 32 logits a lane once that leaves every SM sixteen warps
+    const bool many = p.tokens * p.P * p.experts >= static_cast<int64_t>(sm_count()) * 16 * 32 * 32;
+    if (p.experts <= 8) return launch<T, 1, 8>(p, stream);
+    if (p.experts <= 16) return many ? launch<T, 1, 16>(p, stream) : launch<T, 2, 8>(p, stream);
+    if (p.experts <= 32) return many ? launch<T, 1, 32>(p, stream) : launch<T, 4, 8>(p, stream);
+    if (p.experts <= 64) return many ? launch<T, 2, 32>(p, stream) : launch<T, 8, 8>(p, stream);
+    if (p.experts <= 128) return many ? launch<T, 4, 32>(p, stream) : launch<T, 16, 8>(p, stream);
+    if (p.experts <= 256) return many ? launch<T, 8, 32>(p, stream) : launch<T, 32, 8>(p, stream);
+    if (p.experts <= 512) return launch<T, 16, 32>(p, stream);
+    return launch<T, 32, 32>(p, stream);
+}
+
+// Whether every row of every worker starts on 16 bytes.
+bool wide_rows(const void *const *rows, int P, int64_t ld, int elem) {
+    bool good = ld * elem % 16 == 0;
+    for (int i = 0; i < P; ++i) good = good && aligned(rows[i], 16);
+    return good;
 }
 
 }  // namespace
@@ -201,7 +536,7 @@ int launch(const BalanceParams &p, int blocks, cudaStream_t stream) {
 using namespace gar;
 
 extern "C" size_t gar_balance_workspace_bytes(int32_t P) {
-    return P < 1 || P > GAR_MAX_WORKERS ? 0 : static_cast<size_t>(kMaxBlocks) * 8 + GAR_MAX_WORKERS * 4;
+    return P < 1 || P > GAR_MAX_WORKERS ? 0 : static_cast<size_t>(kMaxBlocks) * 4 + 8;
 }
 
 extern "C" int gar_balance_loss(const void *const *z, int32_t P, int64_t tokens, int32_t experts, int64_t ldz,
@@ -233,17 +568,12 @@ extern "C" int gar_balance_loss(const void *const *z, int32_t P, int64_t tokens,
     p.tokens = tokens, p.ldz = ldz, p.lddz = lddz;
     p.P = P, p.experts = experts, p.k = k, p.has_valid = valid != nullptr, p.has_grad = dz != nullptr;
     p.alpha = alpha, p.counts = counts, p.loss = loss;
-    p.partial = static_cast<double *>(d_workspace);
-    p.n_tokens = reinterpret_cast<int32_t *>(p.partial + kMaxBlocks);
+    p.partial = static_cast<float *>(d_workspace);
+    p.seen = reinterpret_cast<uint32_t *>(p.partial + kMaxBlocks);
+    if (tokens > 0) {
+        p.wide = wide_rows(p.z, P, ldz, elem_bytes(dtype));
+        p.dwide = dz && wide_rows(p.dz, P, lddz, elem_bytes(dtype));
+    }
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    cudaError_t e = cudaMemsetAsync(counts, 0, sizeof(int32_t) * P * experts, stream);
-    if (e == cudaSuccess) e = cudaMemsetAsync(p.n_tokens, 0, sizeof(int32_t) * GAR_MAX_WORKERS, stream);
-    if (e != cudaSuccess) return fail(GAR_ECUDA, "gar_balance_loss: %s", cudaGetErrorString(e));
-    int64_t blocks = ceil_div(tokens, kWarps);
-    const int64_t cap = ceil_div(static_cast<int64_t>(sm_count()) * 8, P);
-    if (blocks > cap) blocks = cap;
-    if (blocks > kMaxBlocks / P) blocks = kMaxBlocks / P;
-    if (blocks < 1) blocks = 1;
-    return dtype == GAR_F32 ? launch<float>(p, static_cast<int>(blocks), stream)
-                            : launch<uint16_t>(p, static_cast<int>(blocks), stream);
+    return dtype == GAR_F32 ? dispatch<float>(p, stream) : dispatch<uint16_t>(p, stream);
 }
