@@ -39,6 +39,7 @@ class gar_seg(C.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_bound = {}  # entry point -> its ctypes function, once the library is loaded
 
 _vp, _pp = C.c_void_p, C.POINTER(C.c_void_p)
 _i32, _i64, _u64 = C.c_int32, C.c_int64, C.c_uint64
@@ -119,6 +120,7 @@ def load(path: str = LIB_PATH):
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
+                _bound[name] = fn
             _lib = lib
     return _lib
 
@@ -201,19 +203,37 @@ def _call(name, *args):
     token = None
     if _timeline is not None and args and isinstance(args[-1], _StreamArg):
         token = _timeline.begin(name, args[-1].value)
-    rc = getattr(load(), name)(*args)
+    rc = (_bound.get(name) or getattr(load(), name))(*args)
     if token is not None:
         _timeline.end(token)
     if rc != GAR_OK:
         raise GarError(rc, load().gar_last_error().decode(errors="replace"))
 
 
-def _stream(stream):
+_current_stream = None  # () -> handle of the current stream of the current device
+
+
+def _find_current_stream():
+    """The current stream's handle without building torch's stream object
+    (3 us of a call's host time) where this torch can say it directly."""
     import torch
 
+    global _current_stream
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    else:
+        torch.cuda.init()
+        _current_stream = lambda: raw(device())  # noqa: E731
+    return _current_stream
+
+
+def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return _StreamArg(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        handle = (_current_stream or _find_current_stream())()
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return handle if _timeline is None else _StreamArg(handle)
 
 
 def _dev(t):
@@ -637,15 +657,37 @@ def fp8_matrix(rows: int, cols: int, dtype=None, device="cuda"):
     return codes, torch.empty(((cols + 511) // 512, rows, 4), dtype=torch.uint8, device=device)
 
 
-def _matrix(t, name, shape=None):
-    """(pointer, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise GarError(GAR_EINVAL, f"{name} has shape {tuple(t.shape)}, not {shape or 'two dimensions'}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+# torch's types by what the library calls them; filled on first use, so that the package imports without torch
+_FLOATS, _FP8S, _INT32, _FLOAT32, _UINT8 = {}, {}, None, None, None
+
+
+def _types():
+    import torch
+
+    global _INT32, _FLOAT32, _UINT8
+    _INT32, _FLOAT32, _UINT8 = torch.int32, torch.float32, torch.uint8
+    _FP8S.update({torch.float8_e4m3fn: GAR_F8E4M3, torch.float8_e5m2: GAR_F8E5M2})
+    _FLOATS.update({torch.float32: GAR_F32, torch.bfloat16: GAR_BF16})
+
+
+def _code(t, table, name):
+    if not _FLOATS:
+        _types()
+    code = table.get(t.dtype)
+    if code is None:
+        raise GarError(GAR_EDTYPE, f"{name} is {t.dtype}, not one of {', '.join(map(str, table))}")
+    return code
+
+
+def _matrix(t, name, rows, cols):
+    """(pointer, row stride) of a rows x cols CUDA tensor whose rows are contiguous."""
+    if t.shape != (rows, cols):
+        raise GarError(GAR_EINVAL, f"{name} has shape {tuple(t.shape)}, not {(rows, cols)}")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise GarError(GAR_EINVAL, f"{name}: the elements of a row are not contiguous")
-    # the stride of a single row means nothing: any that the library accepts will do
-    return _dev(t), t.stride(0) if rows > 1 else (max(cols, 1) + 15) // 16 * 16
+    # the stride of a single row means nothing: one that the library accepts
+    return _dev(t), ld if rows > 1 else (cols + 15) // 16 * 16
 
 
 def _vector(t, name, dtype, n):
@@ -656,14 +698,10 @@ def _vector(t, name, dtype, n):
     return _dev(t)
 
 
-def _fp8_code(t, name) -> int:
-    import torch
-
-    if t.dtype == torch.float8_e4m3fn:
-        return GAR_F8E4M3
-    if t.dtype == torch.float8_e5m2:
-        return GAR_F8E5M2
-    raise GarError(GAR_EDTYPE, f"{name} is {t.dtype}, not float8_e4m3fn or float8_e5m2")
+def _two_dims(t, name):
+    if t.dim() != 2:
+        raise GarError(GAR_EINVAL, f"{name} has {t.dim()} dimensions, not two")
+    return t.shape
 
 
 def gar_fp8_scale_bytes(rows: int, cols: int) -> int:
@@ -675,60 +713,61 @@ def gar_fp8_quantize(x, q, scale, qt=None, scale_t=None, square: bool = False, s
     ``scale``, and/or qt [cols, rows], the transpose's, with ``scale_t`` (see
     fp8_matrix; either pair may be None).  square: 128 x 128 blocks instead of
     128 along the summed axis."""
-    import torch
-
-    rows, cols = x.shape
-    xp, ldx = _matrix(x, "x")
-    fmt, args = None, []
-    for name, codes, s, shape in (("q", q, scale, (rows, cols)), ("qt", qt, scale_t, (cols, rows))):
-        if codes is None:
-            args += [None, 0, None]
-            continue
-        f = _fp8_code(codes, name)
+    dtype = _code(x, _FLOATS, "x")
+    rows, cols = _two_dims(x, "x")
+    fmt = qp = sp = qtp = stp = None
+    ldq = ldqt = 0
+    if q is not None:
+        fmt = _code(q, _FP8S, "q")
+    if qt is not None:
+        f = _code(qt, _FP8S, "qt")
         if fmt is not None and f != fmt:
             raise GarError(GAR_EDTYPE, "q and qt have different formats")
         fmt = f
-        ptr, ld = _matrix(codes, name, shape)
-        args += [ptr, ld, None if s is None else
-                 _vector(s, f"scales of {name}", torch.uint8, (shape[1] + 511) // 512 * shape[0] * 4)]
-    _call("gar_fp8_quantize", xp, _dtype_code(x), rows, cols, ldx, fmt or 0, int(bool(square)), *args, _stream(stream))
+    xp, ldx = _matrix(x, "x", rows, cols)
+    if q is not None:
+        qp, ldq = _matrix(q, "q", rows, cols)
+        sp = _vector(scale, "scale", _UINT8, (cols + 511) // 512 * rows * 4) if scale is not None else None
+    if qt is not None:
+        qtp, ldqt = _matrix(qt, "qt", cols, rows)
+        stp = _vector(scale_t, "scale_t", _UINT8, (rows + 511) // 512 * cols * 4) if scale_t is not None else None
+    _call("gar_fp8_quantize", xp, dtype, rows, cols, ldx, fmt or 0, 1 if square else 0, qp, ldq, sp, qtp, ldqt, stp,
+          _stream(stream))
 
 
 def gar_fp8_matmul(a, a_scale, b, b_scale, d, c=None, stream=None):
     """d = a b^T (+ c): a [M, K] and b [N, K] codes with their scales, d [M, N]
     fp32 or bf16, c of d's type (it may be d)."""
-    import torch
-
-    (M, K), N = a.shape, b.shape[0]
-    ap, lda = _matrix(a, "a")
-    bp, ldb = _matrix(b, "b", (N, K))
-    dp, ldd = _matrix(d, "d", (M, N))
+    fmt_a, fmt_b, dtype = _code(a, _FP8S, "a"), _code(b, _FP8S, "b"), _code(d, _FLOATS, "d")
+    M, K = _two_dims(a, "a")
+    N = _two_dims(b, "b")[0]
+    ap, lda = _matrix(a, "a", M, K)
+    bp, ldb = _matrix(b, "b", N, K)
+    dp, ldd = _matrix(d, "d", M, N)
     words = (K + 511) // 512 * 4
-    asp = _vector(a_scale, "scales of a", torch.uint8, words * M)
-    bsp = _vector(b_scale, "scales of b", torch.uint8, words * N)
+    asp = _vector(a_scale, "a_scale", _UINT8, words * M)
+    bsp = _vector(b_scale, "b_scale", _UINT8, words * N)
     cp, ldc = None, 0
     if c is not None:
         if c.dtype != d.dtype:
             raise GarError(GAR_EDTYPE, f"c is {c.dtype}, d {d.dtype}")
-        cp, ldc = _matrix(c, "c", (M, N))
-    _call("gar_fp8_matmul", ap, lda, asp, _fp8_code(a, "a"), bp, ldb, bsp, _fp8_code(b, "b"), M, N, K, cp, ldc, dp, ldd,
-          _dtype_code(d), _stream(stream))
+        cp, ldc = _matrix(c, "c", M, N)
+    _call("gar_fp8_matmul", ap, lda, asp, fmt_a, bp, ldb, bsp, fmt_b, M, N, K, cp, ldc, dp, ldd, dtype, _stream(stream))
 
 
 def _distill_args(z, index, teacher, tau, weight, dz):
-    import torch
-
-    rows, vocab = z.shape
-    k = index.shape[-1]
-    zp, ldz = _matrix(z, "z")
+    dtype = _code(z, _FLOATS, "z")
+    rows, vocab = _two_dims(z, "z")
+    k = index.shape[-1] if index.dim() else 0
+    zp, ldz = _matrix(z, "z", rows, vocab)
     dzp, lddz = None, 0
     if dz is not None:
         if dz.dtype != z.dtype:
             raise GarError(GAR_EDTYPE, f"dz is {dz.dtype}, z {z.dtype}")
-        dzp, lddz = _matrix(dz, "dz", (rows, vocab))
-    head = [zp, _dtype_code(z), rows, vocab, ldz, _vector(index, "index", torch.int32, rows * k),
-            _vector(teacher, "teacher", torch.float32, rows * k), k, float(tau),
-            None if weight is None else _vector(weight, "weight", torch.float32, rows)]
+        dzp, lddz = _matrix(dz, "dz", rows, vocab)
+    head = (zp, dtype, rows, vocab, ldz, _vector(index, "index", _INT32, rows * k),
+            _vector(teacher, "teacher", _FLOAT32, rows * k), k, tau,
+            None if weight is None else _vector(weight, "weight", _FLOAT32, rows))
     return rows, head, dzp, lddz
 
 
@@ -736,58 +775,58 @@ def gar_distill_loss(z, index, teacher, tau: float, loss, lse, dz=None, weight=N
     """Distillation loss of student logits z [rows, vocab] against the teacher's
     top logits (index, teacher [rows, k]) at temperature tau: loss and lse
     [rows], and the gradient dz (z's type; may be z) under the rows' weights."""
-    import torch
-
     rows, head, dzp, lddz = _distill_args(z, index, teacher, tau, weight, dz)
-    _call("gar_distill_loss", *head, _vector(loss, "loss", torch.float32, rows), _vector(lse, "lse", torch.float32, rows),
-          dzp, lddz, _stream(stream))
+    _call("gar_distill_loss", *head, _vector(loss, "loss", _FLOAT32, rows), _vector(lse, "lse", _FLOAT32, rows), dzp, lddz,
+          _stream(stream))
 
 
 def gar_distill_grad(z, index, teacher, tau: float, lse, dz, weight=None, stream=None):
     """The gradient of gar_distill_loss alone, from its lse."""
-    import torch
-
     rows, head, dzp, lddz = _distill_args(z, index, teacher, tau, weight, dz)
-    _call("gar_distill_grad", *head, _vector(lse, "lse", torch.float32, rows), dzp, lddz, _stream(stream))
+    _call("gar_distill_grad", *head, _vector(lse, "lse", _FLOAT32, rows), dzp, lddz, _stream(stream))
 
 
 def gar_balance_workspace_bytes(P: int) -> int:
     return int(load().gar_balance_workspace_bytes(P))
 
 
+def _workers(given, name, P, shape, dtype):
+    """(pointer array, row stride) of one tensor per worker, each of the given
+    shape and type and all of one row stride.  A PtrTable's tensors were put
+    together before: its first is looked at."""
+    tensors = given.tensors if isinstance(given, PtrTable) else given
+    if len(tensors) != P:
+        raise GarError(GAR_EINVAL, f"{name} has {len(tensors)} tensors, not {P}")
+    first = tensors[0].stride()
+    if len(first) != len(shape) or (first[-1] != 1 and shape[-1] > 1):
+        raise GarError(GAR_EINVAL, f"{name}: a tensor is not of shape {shape} with contiguous rows")
+    ptrs = []
+    for t in tensors[:1] if isinstance(given, PtrTable) else tensors:
+        if t.shape != shape or (t.stride() != first and shape[0] > 1):
+            raise GarError(GAR_EINVAL, f"{name} has a tensor of shape {tuple(t.shape)}, not {shape}, or of another stride")
+        if t.dtype != dtype and not (dtype is _UINT8 and t.element_size() == 1):
+            raise GarError(GAR_EDTYPE, f"{name} is {t.dtype}, not {dtype}")
+        ptrs.append(_dev(t))
+    array = given.array if isinstance(given, PtrTable) else (C.c_void_p * P)(*ptrs)
+    return array, first[0] if shape[0] > 1 or len(shape) == 1 else max(shape[-1], 1)
+
+
 def gar_balance_loss(z, k: int, alpha: float, choice, counts, loss, workspace, dz=None, valid=None, stream=None):
     """A router's choices, counts and balance loss over P workers.  z[w]
     [tokens, experts] logits, choice[w] [tokens, k] int32 out, counts [P,
     experts] int32 out, loss one fp32 out, dz[w] of z's type out (may be z[w]),
-    valid[w] [tokens] uint8 or bool.  Lists or PtrTables; a list's tensors are
-    checked one by one, a PtrTable's by its first."""
-    import torch
-
-    zt, ct, dt, vt = [pointer_table(t) if t is not None else None for t in (z, choice, dz, valid)]
-    P, (tokens, experts) = len(zt), zt.first.shape
-    _, ldz = _matrix(zt.first, "z[0]")
-    code = _dtype_code(zt.first)
-    lddz = 0
-    for name, given, t, dtype, shape in (("z", z, zt, zt.first.dtype, (tokens, experts)),
-                                         ("choice", choice, ct, torch.int32, (tokens, k)),
-                                         ("dz", dz, dt, zt.first.dtype, (tokens, experts)),
-                                         ("valid", valid, vt, None, (tokens,))):
-        if t is None:
-            continue
-        if len(t) != P:
-            raise GarError(GAR_EINVAL, f"{name} has {len(t)} tensors, z {P}")
-        for x in t.tensors[:1] if isinstance(given, PtrTable) else t.tensors:
-            if tuple(x.shape) != shape or (x.stride() != t.first.stride() and tokens > 1):
-                raise GarError(GAR_EINVAL, f"{name} has a tensor of shape {tuple(x.shape)}, not {shape}, or strides that differ")
-            if x.dtype != dtype if dtype is not None else x.element_size() != 1:
-                raise GarError(GAR_EDTYPE, f"{name} is {x.dtype}")
-            if name in ("choice", "valid") and not x.is_contiguous():
-                raise GarError(GAR_EINVAL, f"{name} is not contiguous")
-    if dt is not None:
-        _, lddz = _matrix(dt.first, "dz[0]")
-    _call("gar_balance_loss", zt.array, P, tokens, experts, ldz, code, k, vt.array if vt is not None else None,
-          float(alpha), ct.array, _vector(counts, "counts", torch.int32, P * experts),
-          _vector(loss, "loss", torch.float32, 1), dt.array if dt is not None else None, lddz, _dev(workspace),
+    valid[w] [tokens] uint8 or bool.  Lists or PtrTables."""
+    first = z.first if isinstance(z, PtrTable) else z[0]
+    dtype = _code(first, _FLOATS, "z")
+    P, (tokens, experts) = len(z), _two_dims(first, "z[0]")
+    za, ldz = _workers(z, "z", P, (tokens, experts), first.dtype)
+    ca, ldc = _workers(choice, "choice", P, (tokens, k), _INT32)
+    da, lddz = _workers(dz, "dz", P, (tokens, experts), first.dtype) if dz is not None else (None, 0)
+    va, step = _workers(valid, "valid", P, (tokens,), _UINT8) if valid is not None else (None, 1)
+    if (ldc != k and tokens > 1) or (step != 1 and tokens > 1):
+        raise GarError(GAR_EINVAL, "choice and valid have to be contiguous")
+    _call("gar_balance_loss", za, P, tokens, experts, ldz, dtype, k, va, alpha, ca,
+          _vector(counts, "counts", _INT32, P * experts), _vector(loss, "loss", _FLOAT32, 1), da, lddz, _dev(workspace),
           workspace.numel() * workspace.element_size(), _stream(stream))
 
 

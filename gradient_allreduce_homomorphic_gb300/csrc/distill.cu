@@ -37,7 +37,7 @@ struct DistillParams {
     const int32_t *index;
     const float *teacher;
     const float *weight;  // NULL: 1
-    float inv_tau;
+    float inv_tau, inv_tau_rest;  // 1 / tau, and what its rounding left
     float *loss, *lse;         // gar_distill_loss
     const float *lse_in;       // gar_distill_grad
     void *dz;                  // NULL: no gradient
@@ -79,6 +79,23 @@ __device__ __forceinline__ MaxSum merge_lanes(MaxSum a, float c) {
     return {m, lane_sum<kWidth>(a.s * pow2((a.m - finite_or_0(m)) * c))};
 }
 
+// exp((t - tmax) / tau) of a teacher's entry, and its exponent.  The difference
+// and the product keep what their rounding leaves (the sum of two floats is
+// exact as a pair, [K]; a product by fma), for a teacher's spread over tens of
+// units would cost its small probabilities four bits otherwise; entries are few.
+//   [K] Knuth, The Art of Computer Programming vol. 2, 4.2.2: two-sum.
+struct Entry {
+    float power, exponent;
+};
+__device__ __forceinline__ Entry entry_power(const DistillParams &p, float t, float tmax) {
+    const float d = t - tmax, x = d * p.inv_tau;
+    if (x < -200.0f) return {0.0f, x};  // 0 in fp32; a mask's lowest value would overflow below
+    const float b = d - t, lost = (t - (d - b)) + (-tmax - b);
+    const float rest = fmaf(d, p.inv_tau_rest, fmaf(lost, p.inv_tau, fmaf(d, p.inv_tau, -x)));
+    const float e = expf(x);
+    return {fmaf(e, rest, e), x + rest};
+}
+
 // Where the gradient of a student logit z comes from: the row's maximum and
 // log2 of its sum (loss), or its saved lse (grad).
 template <bool kSaved>
@@ -118,7 +135,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_c
     float tmax = -INFINITY;
     for (int j = tid; j < p.k; j += kRowThreads) {
         const int32_t i = p.index[row * p.k + j];
-        const float t = p.teacher[row * p.k + j] * p.inv_tau;
+        const float t = p.teacher[row * p.k + j];
         const bool on = i >= 0 && i < p.vocab && !(t == -INFINITY);
         top_i[j] = on ? i : -1;
         top_p[j] = t;
@@ -128,7 +145,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_c
     tmax = block_reduce<true>(tmax, scratch);
     float tsum = 0.0f;
     for (int j = tid; j < p.k; j += kRowThreads)
-        if (top_i[j] >= 0) tsum += expf(top_p[j] - tmax);
+        if (top_i[j] >= 0) tsum += entry_power(p, top_p[j], tmax).power;
     tsum = block_reduce<false>(tsum, scratch);
     if (w == 0.0f || tsum == 0.0f) {  // nothing to learn in this row
         if (dz)
@@ -157,9 +174,9 @@ __global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_c
     for (int j = tid; j < p.k; j += kRowThreads) {
         float pj = 0.0f;
         if (top_i[j] >= 0) {
-            const float logp = top_p[j] - tmax - log_tsum;
-            pj = expf(logp);
-            if (!(pj == 0.0f)) part += pj * (logp - (top_z[j] - q.ref) * p.inv_tau);
+            const Entry t = entry_power(p, top_p[j], tmax);
+            pj = t.power / tsum;
+            if (!(pj == 0.0f)) part += pj * (t.exponent - log_tsum - (top_z[j] - q.ref) * p.inv_tau);
         }
         top_p[j] = pj;
     }
@@ -345,7 +362,7 @@ __global__ void __launch_bounds__(kStreamThreads, kLag ? 1 : 2) distill_stream_k
                 for (int u = 0; u < kAtOnce; ++u) {
                     const int j = j0 + 32 * u;
                     at[u] = j < p.k ? p.index[row * p.k + j] : -1;
-                    t[u] = j < p.k ? p.teacher[row * p.k + j] * p.inv_tau : -INFINITY;
+                    t[u] = j < p.k ? p.teacher[row * p.k + j] : -INFINITY;
                 }
 #pragma unroll
                 for (int u = 0; u < kAtOnce; ++u) {
@@ -366,7 +383,7 @@ __global__ void __launch_bounds__(kStreamThreads, kLag ? 1 : 2) distill_stream_k
             zref = finite_or_0(warp_max(zref));
             for (uint32_t j = lane; j < buckets; j += 32) table[j] = 0xFFFFFFFFu;
             for (int j = lane; j < p.k; j += 32)
-                if (top_i[j] >= 0) tsum += expf(top_p[j] - tmax);
+                if (top_i[j] >= 0) tsum += entry_power(p, top_p[j], tmax).power;
             tsum = warp_sum(tsum);
             const bool live = w != 0.0f && tsum != 0.0f;  // NaN: live, and it spreads
             float cross = 0.0f;
@@ -378,9 +395,9 @@ __global__ void __launch_bounds__(kStreamThreads, kLag ? 1 : 2) distill_stream_k
                     const int32_t i = top_i[j];
                     float pj = 0.0f;
                     if (i >= 0) {
-                        const float logp = top_p[j] - tmax - log_tsum;
-                        pj = expf(logp);
-                        if (!(pj == 0.0f)) cross += pj * (logp - (top_z[j] - zref) * p.inv_tau);
+                        const Entry t = entry_power(p, top_p[j], tmax);
+                        pj = t.power / tsum;
+                        if (!(pj == 0.0f)) cross += pj * (t.exponent - log_tsum - (top_z[j] - zref) * p.inv_tau);
                         uint32_t at = (static_cast<uint32_t>(i) * 0x9E3779B1u) >> shift;
                         while (true) {  // ends: at most half of the buckets are taken
                             const uint32_t was = atomicCAS(table + at, 0xFFFFFFFFu, static_cast<uint32_t>(i));
@@ -702,7 +719,9 @@ extern "C" int gar_distill_loss(const void *z, int32_t dtype, int64_t rows, int6
     if (!aligned(loss, 4) || !aligned(lse, 4) || !aligned(weight, 4)) return fail(GAR_EALIGN, "misaligned pointer");
     DistillParams p{};
     p.z = z, p.rows = rows, p.ldz = ldz, p.lddz = lddz, p.vocab = static_cast<int32_t>(vocab), p.k = k;
-    p.index = index, p.teacher = teacher, p.weight = weight, p.inv_tau = 1.0f / tau;
+    p.index = index, p.teacher = teacher, p.weight = weight;
+    p.inv_tau = 1.0f / tau;
+    p.inv_tau_rest = static_cast<float>(1.0 / static_cast<double>(tau) - static_cast<double>(p.inv_tau));
     p.loss = loss, p.lse = lse, p.dz = dz;
     return run(p, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -715,7 +734,9 @@ extern "C" int gar_distill_grad(const void *z, int32_t dtype, int64_t rows, int6
     if (!aligned(lse, 4) || !aligned(weight, 4)) return fail(GAR_EALIGN, "misaligned pointer");
     DistillParams p{};
     p.z = z, p.rows = rows, p.ldz = ldz, p.lddz = lddz, p.vocab = static_cast<int32_t>(vocab), p.k = k;
-    p.index = index, p.teacher = teacher, p.weight = weight, p.inv_tau = 1.0f / tau;
+    p.index = index, p.teacher = teacher, p.weight = weight;
+    p.inv_tau = 1.0f / tau;
+    p.inv_tau_rest = static_cast<float>(1.0 / static_cast<double>(tau) - static_cast<double>(p.inv_tau));
     p.lse_in = lse, p.dz = dz;
     return run(p, dtype, reinterpret_cast<cudaStream_t>(stream));
 }

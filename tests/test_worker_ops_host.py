@@ -1,0 +1,146 @@
+"""Argument checks of the operators that a worker runs before its gradients are
+averaged (no GPU needed, no kernel launched): statuses at the C boundary, the
+binding's own checks of shapes and types."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+import worker_ref as ref
+
+
+@pytest.fixture(scope="module")
+def gar():
+    from gradient_allreduce_homomorphic_gb300 import build
+
+    build.build()
+    import gradient_allreduce_homomorphic_gb300 as g
+
+    g.load()
+    return g
+
+
+V = C.c_void_p
+A, B, D, S, T, U, W = (V(0x10000 * (i + 1)) for i in range(7))
+NULL = V(0)
+
+
+def test_quantize_refusals(gar):
+    f = gar.load().gar_fp8_quantize
+
+    def call(x=A, dtype=0, rows=10, cols=100, ldx=100, fmt=0, square=0, q=B, ldq=112, s=S, qt=D, ldqt=16, st=T):
+        return f(x, dtype, rows, cols, ldx, fmt, square, q, ldq, s, qt, ldqt, st, NULL)
+
+    assert call(rows=-1) == call(cols=-1) == call(cols=1 << 31) == gar.GAR_EINVAL
+    assert call(dtype=2) == call(fmt=2) == gar.GAR_EDTYPE
+    assert call(q=NULL, qt=NULL) == call(x=NULL) == call(ldx=99) == gar.GAR_EINVAL
+    assert call(s=NULL) == call(st=NULL) == call(ldq=96) == call(ldqt=0) == gar.GAR_EINVAL
+    assert call(ldq=101) == call(q=V(0x10008)) == call(qt=V(0x10001)) == call(s=V(0x10002)) == gar.GAR_EALIGN
+    assert call(x=V(0x10002)) == call(x=V(0x10001), dtype=1) == gar.GAR_EALIGN
+    assert call(rows=0) == call(cols=0, ldx=0) == gar.GAR_OK
+    assert "scales" in gar.gar_last_error() or gar.gar_last_error()
+
+
+def test_matmul_refusals(gar):
+    f = gar.load().gar_fp8_matmul
+
+    def call(a=A, lda=64, sa=S, fa=0, b=B, ldb=64, sb=T, fb=1, M=4, N=5, K=50, c=NULL, ldc=0, d=D, ldd=5, dtype=0):
+        return f(a, lda, sa, fa, b, ldb, sb, fb, M, N, K, c, ldc, d, ldd, dtype, NULL)
+
+    assert call(M=-1) == call(N=-1) == call(K=-1) == call(M=1 << 31) == gar.GAR_EINVAL
+    assert call(dtype=7) == call(fa=2) == call(fb=-1) == gar.GAR_EDTYPE
+    assert call(a=NULL) == call(sb=NULL) == call(lda=48) == call(d=NULL) == call(ldd=4) == gar.GAR_EINVAL
+    assert call(c=U, ldc=4) == call(c=D, ldc=6, ldd=5) == gar.GAR_EINVAL
+    assert call(a=V(0x10008)) == call(ldb=72) == call(sa=V(0x10001)) == call(d=V(0x10002)) == gar.GAR_EALIGN
+    assert call(M=0) == call(N=0) == gar.GAR_OK
+
+
+def test_distill_refusals(gar):
+    lib = gar.load()
+
+    def loss(z=A, dtype=0, rows=3, vocab=10, ldz=10, i=B, t=D, k=2, tau=1.0, w=NULL, loss=S, lse=T, dz=NULL, lddz=0):
+        return lib.gar_distill_loss(z, dtype, rows, vocab, ldz, i, t, k, tau, w, loss, lse, dz, lddz, NULL)
+
+    assert loss(rows=-1) == loss(vocab=0) == loss(k=0) == loss(k=1025) == loss(ldz=9) == gar.GAR_EINVAL
+    assert loss(tau=0.0) == loss(tau=-1.0) == loss(tau=float("nan")) == loss(tau=float("inf")) == gar.GAR_EINVAL
+    assert loss(z=NULL) == loss(i=NULL) == loss(t=NULL) == loss(loss=NULL) == loss(lse=NULL) == gar.GAR_EINVAL
+    assert loss(dz=U, lddz=9) == loss(dz=A, lddz=12) == gar.GAR_EINVAL
+    assert loss(dtype=3) == gar.GAR_EDTYPE
+    assert loss(z=V(0x10002)) == loss(i=V(0x10001)) == loss(w=V(0x10002)) == loss(dz=V(0x10002), lddz=10) == gar.GAR_EALIGN
+    assert loss(rows=0) == gar.GAR_OK
+
+    def grad(lse=T, dz=U, lddz=10):
+        return lib.gar_distill_grad(A, 0, 3, 10, 10, B, D, 2, 1.0, NULL, lse, dz, lddz, NULL)
+
+    assert grad(lse=NULL) == grad(dz=NULL) == grad(lddz=9) == gar.GAR_EINVAL
+    assert grad(lse=V(0x10001)) == gar.GAR_EALIGN
+
+
+def test_balance_refusals(gar):
+    lib = gar.load()
+    two = (V * 2)(0x10000, 0x20000)
+
+    def call(z=two, P=2, tokens=3, experts=8, ldz=8, dtype=0, k=2, valid=None, alpha=0.1, choice=two, counts=B, loss=D, dz=None,
+             lddz=0, ws=S, nbytes=1 << 16):
+        return lib.gar_balance_loss(z, P, tokens, experts, ldz, dtype, k, valid, alpha, choice, counts, loss, dz, lddz, ws, nbytes,
+                                    NULL)
+
+    assert call(P=0) == call(P=65) == call(tokens=-1) == call(tokens=1 << 40) == gar.GAR_EINVAL
+    assert call(experts=0) == call(experts=1025) == call(k=0) == call(k=9) == call(experts=64, k=33, ldz=64) == gar.GAR_EINVAL
+    assert call(alpha=float("nan")) == call(ldz=7) == call(dz=two, lddz=7) == gar.GAR_EINVAL
+    assert call(z=None) == call(choice=None) == call(counts=NULL) == call(loss=NULL) == call(ws=NULL) == gar.GAR_EINVAL
+    assert call(nbytes=8) == call(z=(V * 2)(0x10000, 0)) == call(valid=(V * 2)(0x10000, 0)) == gar.GAR_EINVAL
+    assert call(dz=two, lddz=9) == gar.GAR_EINVAL  # in place with another stride
+    assert call(dtype=4) == gar.GAR_EDTYPE
+    assert call(counts=V(0x10002)) == call(z=(V * 2)(0x10000, 0x20002)) == call(ws=V(0x10004)) == gar.GAR_EALIGN
+
+
+def test_sizes(gar):
+    assert gar.gar_fp8_scale_bytes(3, 1) == 12 and gar.gar_fp8_scale_bytes(3, 512) == 12
+    assert gar.gar_fp8_scale_bytes(3, 513) == 24 and gar.gar_fp8_scale_bytes(0, 5) == 0 and gar.gar_fp8_scale_bytes(-1, 5) == 0
+    assert 0 < gar.gar_balance_workspace_bytes(8) <= 1 << 16 and gar.gar_balance_workspace_bytes(0) == 0
+
+
+def test_binding_checks(gar):
+    torch = pytest.importorskip("torch")
+    q, s = gar.fp8_matrix(4, 100, device="cpu")
+    r, t = gar.fp8_matrix(5, 100, torch.float8_e5m2, device="cpu")
+    assert q.shape == (4, 100) and q.stride(0) == 112 and s.shape == (1, 4, 4)
+    d = torch.zeros((4, 5))
+
+    def status(f, *a, **k):
+        with pytest.raises(gar.GarError) as e:
+            f(*a, **k)
+        return e.value.status
+
+    x = torch.zeros((4, 100))
+    assert status(gar.gar_fp8_quantize, x.double(), q, s) == gar.GAR_EDTYPE
+    assert status(gar.gar_fp8_quantize, x, x, s) == gar.GAR_EDTYPE
+    assert status(gar.gar_fp8_quantize, x.t(), q, s) == gar.GAR_EINVAL
+    assert status(gar.gar_fp8_quantize, x, q, s) == gar.GAR_EINVAL  # not on a CUDA device
+    assert status(gar.gar_fp8_matmul, q, s, r, t, d) == gar.GAR_EINVAL
+    assert status(gar.gar_fp8_matmul, q, s, r, t, torch.zeros((5, 4))) == gar.GAR_EINVAL
+    assert status(gar.gar_fp8_matmul, q, s, x, t, d) == gar.GAR_EDTYPE
+    z, i, e, v = torch.zeros((3, 10)), torch.zeros((3, 2), dtype=torch.int32), torch.zeros((3, 2)), torch.zeros(3)
+    assert status(gar.gar_distill_loss, z, i, e, 1.0, v, v) == gar.GAR_EINVAL
+    assert status(gar.gar_distill_loss, z.half(), i, e, 1.0, v, v) == gar.GAR_EDTYPE
+    c = torch.zeros((1, 10), dtype=torch.int32)
+    w = torch.zeros(1 << 16, dtype=torch.uint8)
+    assert status(gar.gar_balance_loss, [z], 2, 0.1, [i], c, v[:1], w) == gar.GAR_EINVAL
+    assert status(gar.gar_balance_loss, [z.half()], 2, 0.1, [i], c, v[:1], w) == gar.GAR_EDTYPE
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_reference_grid_is_the_format(fmt):
+    """The plain form's rounding against every code of the format, and midway between neighbours."""
+    torch = pytest.importorskip("torch")
+    t = torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2
+    v = torch.arange(256, dtype=torch.uint8).view(t).double().numpy()
+    v = np.unique(v[np.isfinite(v)])
+    np.testing.assert_array_equal(ref.round_to_format(v, fmt), v)
+    mid = (v[1:] + v[:-1]) / 2
+    got = ref.round_to_format(mid, fmt)
+    assert all(g in (a, b) for g, a, b in zip(got, v[:-1], v[1:]))
+    np.testing.assert_array_equal(got, torch.from_numpy(mid).to(t).double().numpy())
+    near = np.nextafter(mid, np.inf)
+    np.testing.assert_array_equal(ref.round_to_format(near, fmt), v[1:])
