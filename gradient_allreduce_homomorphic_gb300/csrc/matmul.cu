@@ -32,7 +32,7 @@ namespace {
 constexpr int kTN = 128;     // tile rows in tensor memory: columns of D
 constexpr int kKC = 128;     // k per chunk: one scale block, one swizzled line
 constexpr int kThreads = 256;
-constexpr int kScaleBufs = 2;
+constexpr int kScaleBufs = 4;   // of scale words, one for each 512 k, in shared memory; tensor memory has two
 
 struct MatmulParams {
     const uint32_t *sa, *sb;  // scale words [ceil(K / 512)][rows]
@@ -72,16 +72,15 @@ __device__ __forceinline__ void store_out(const MatmulParams &p, int64_t m, int6
         static_cast<float *>(p.d)[i] = v;
 }
 
-// One lane's scale words of kAtoms tiles of 128 rows (w[a][q]: row 128 a + 32 q
-// + lane) to the order that the copy to tensor memory takes.
-template <int kAtoms>
-__device__ __forceinline__ void stage_scales(uint32_t dst, const uint32_t (&w)[kAtoms][4]) {
+// The scale words of 128 rows r0 .. of a matrix (its words of one group of four
+// blocks at src) to the order that the copy to tensor memory takes, by one warp;
+// zero (2^-127, of rows of zeros) past the last row.
+__device__ __forceinline__ void copy_scales_async(uint32_t dst, const uint32_t *src, int64_t r0, int64_t rows, int lane) {
 #pragma unroll
-    for (int a = 0; a < kAtoms; ++a)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512 * a), "r"(w[a][0]), "r"(w[a][1]), "r"(w[a][2]),
-                     "r"(w[a][3])
-                     : "memory");
-    fence_async_shared();
+    for (int q = 0; q < 4; ++q) {
+        const int64_t r = r0 + 32 * q + lane;
+        copy4_async(dst + lane * 16 + q * 4, src + (r < rows ? r : 0), r < rows);
+    }
 }
 
 // After a wait ran out: the copies into the last `issued` stages before stage
@@ -116,7 +115,8 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
     const int c1 = static_cast<int>(static_cast<int64_t>(p.chunks) * (rank + 1) / p.splits);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2 * S::kStages + 2 * kScaleBufs + 1; ++i) mbar_init(full + 8 * i, 1);
+        for (int i = 0; i < 2 * S::kStages + 2 * kScaleBufs + 1; ++i)
+            mbar_init(full + 8 * i, i >= 2 * S::kStages && i < 2 * S::kStages + kScaleBufs ? 32 : 1);  // sf_full: a warp's copies
         failed = 0;
         mbar_init_fence();
     }
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
                 g = groups++;
                 const uint32_t b = g % kScaleBufs;
                 mbar_wait(sf_full + 8 * b, (g / kScaleBufs) & 1, &failed);
-                tc_fence_after();
+                fence_async_shared();
                 if (elect_one())
                     for (int a = 0; a < 1 + S::kAtomsB; ++a)
                         tc_copy_scales<1>(sf_cols + (b * (1 + S::kAtomsB) + a) * 4, scales + b * S::kScaleBuf + 512 * a);
@@ -175,23 +175,15 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
         if (elect_one()) tc_commit(done);
         __syncwarp();
     } else if (warp == 2) {
-        uint32_t g = 0;
-        for (int j = c0 >> 2; c0 < c1 && j <= (c1 - 1) >> 2; ++j, ++g) {
-            const uint32_t *sn = p.sb + static_cast<int64_t>(j) * p.N, *sm = p.sa + static_cast<int64_t>(j) * p.M;
-            uint32_t w[1 + S::kAtomsB][4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t nr = n0 + 32 * q + lane, mr = m0 + 32 * q + lane;
-                w[0][q] = nr < p.N ? ldg_early(sn + nr) : 0x01010101u;
-#pragma unroll
-                for (int a = 0; a < S::kAtomsB; ++a) w[1 + a][q] = mr + 128 * a < p.M ? ldg_early(sm + mr + 128 * a) : 0x01010101u;
-            }
-            const uint32_t b = g % kScaleBufs;
+        const int j0 = c0 >> 2, groups = c0 < c1 ? ((c1 - 1) >> 2) - j0 + 1 : 0;
+        for (int g = 0; g < groups; ++g) {
+            const uint32_t b = g % kScaleBufs, dst = scales + b * S::kScaleBuf;
             mbar_wait(sf_empty + 8 * b, (g / kScaleBufs + 1) & 1, &failed);
-            __syncwarp();
-            stage_scales<1 + S::kAtomsB>(scales + b * S::kScaleBuf + lane * 16, w);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sf_full + 8 * b);
+            copy_scales_async(dst, p.sb + static_cast<int64_t>(j0 + g) * p.N, n0, p.N, lane);
+#pragma unroll
+            for (int a = 0; a < S::kAtomsB; ++a)
+                copy_scales_async(dst + 512 * (1 + a), p.sa + static_cast<int64_t>(j0 + g) * p.M, m0 + 128 * a, p.M, lane);
+            copy_async_arrive(sf_full + 8 * b);
         }
     }
     if (warp >= 4) {
@@ -277,10 +269,10 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
 // added in fp32: the tensor core's additions round toward zero, so its error
 // grows with the number of k it adds (measured against 64 bits: 2.6e-7 of the
 // result at 2048, 8e-7 at 8192).
-constexpr int kPairThreads = 384;  // warps 0-2 as above, 3 scale copies, 4-11 epilogue
+constexpr int kPairThreads = 384;  // warps 0-3 and 4-11 epilogue
 constexpr int kPairStages = 6;
 constexpr int kPairScaleBuf = 512 * 3;
-constexpr int kPairScaleBufs = 4;  // in shared memory; tensor memory has two
+constexpr int kPairScaleBufs = 8;
 constexpr int kPairScaleCols = 480;
 constexpr int kSegment = 64;  // chunks of 128 k
 
@@ -326,7 +318,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                        const __grid_constant__ PairParams pp) {
     const MatmulParams &p = pp.mm;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kPairStages + 2 * kPairScaleBufs + 8];
+    __shared__ __align__(8) uint64_t bars[2 * kPairStages + 3 * kPairScaleBufs + 4];
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
     const uint32_t stage = pair_stage(pp.rows);
@@ -334,7 +326,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t scales = base + kPairStages * stage;
     const uint32_t full = smem_u32(bars), empty = full + 8 * kPairStages, sf_full = empty + 8 * kPairStages,
                    sf_empty = sf_full + 8 * kPairScaleBufs, acc_full = sf_empty + 8 * kPairScaleBufs,
-                   drained = acc_full + 16, sf_ready = drained + 16, sf_done = sf_ready + 16;
+                   drained = acc_full + 16, sf_here = drained + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_cta_rank();
     const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
@@ -344,14 +336,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * kPairStages; ++i) mbar_init(full + 8 * i, 1);
         for (int i = 0; i < kPairScaleBufs; ++i) {
-            mbar_init(sf_full + 8 * i, 2);  // one staging warp of each CTA
+            mbar_init(sf_here + 8 * i, 32);  // a warp's copies
+            mbar_init(sf_full + 8 * i, 2);   // a word from each CTA
             mbar_init(sf_empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
             mbar_init(drained + 8 * i, 16);  // eight epilogue warps of each CTA
-            mbar_init(sf_ready + 8 * i, 1);
-            mbar_init(sf_done + 8 * i, 1);
         }
         failed = 0;
         mbar_init_fence();
@@ -387,14 +378,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // both CTAs' copies count on the first one's barriers; the other waits at the cluster barrier below
         if (!ok && rank == 0) mbar_drain(full, kPairStages, issued, s, turn);
     } else if (warp == 1 && rank == 0) {
-        // Issue of the products.  This thread's time per chunk bounds the kernel (512 clocks of products at TM = 256),
-        // and a look at an mbarrier takes about a hundred: the next chunk's is looked at before this one's products
-        // are issued, and the scale copies have a warp of their own.
+        // Issue of scale copies and products, by one thread: the tensor core takes them in the order of issue, so a
+        // copy needs no barrier before the products that use it.  The thread's time per chunk must stay below the
+        // products' (512 clocks at TM = 256) and a look at an mbarrier takes about a hundred, so what comes next is
+        // looked at before the present products are issued, and waited for only if it was not there.
         uint64_t d = smem_desc(base, 16, 1024, 2);
         const uint64_t d_step = stage >> 4;
         uint32_t s = 0, turn = 0, seq = 0, g = 0;
         const uint32_t lag = overlap ? 1 : 2;
-        bool ready = false;
+        bool ready = false, sf_ready = false;
         for (int64_t t = first; t < pp.tiles; t += step) {
             for (int c0 = 0; c0 < p.chunks; c0 += pp.seg_chunks, ++seq) {
                 const int c1 = min(p.chunks, c0 + pp.seg_chunks);
@@ -402,19 +394,31 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (seq >= lag) mbar_wait_cluster(drained + 8 * ((seq - lag) & 1), ((seq - lag) >> 1) & 1, &failed);
                 for (int c = c0; c < c1; ++c) {
                     const bool first_of_word = (c & 3) == 0, last_of_word = (c & 3) == 3 || c == p.chunks - 1;
-                    if (first_of_word) mbar_wait(sf_ready + 8 * (g & 1), (g >> 1) & 1, &failed);
+                    const uint32_t col = tmem + kPairScaleCols + (g & 1) * 12;
+                    if (first_of_word && !sf_ready) {
+                        // scale group g: shared buffer g % 8, tensor-memory buffer g % 2, free once group g - 2 is done
+                        mbar_wait_cluster(sf_full + 8 * (g % kPairScaleBufs), (g / kPairScaleBufs) & 1, &failed);
+                        if (g >= 2) mbar_wait(sf_empty + 8 * ((g - 2) % kPairScaleBufs), ((g - 2) / kPairScaleBufs) & 1, &failed);
+                    }
                     if (!ready) mbar_wait(full + 8 * s, turn, &failed);
                     tc_fence_after();
                     const uint32_t next = s + 1 == kPairStages ? 0 : s + 1;
                     ready = mbar_test(full + 8 * next, next ? turn : turn ^ 1);
+                    if (last_of_word) {
+                        const uint32_t n = g + 1;
+                        sf_ready = mbar_test_cluster(sf_full + 8 * (n % kPairScaleBufs), (n / kPairScaleBufs) & 1) &
+                                   (n < 2 || mbar_test(sf_empty + 8 * ((n - 2) % kPairScaleBufs), ((n - 2) / kPairScaleBufs) & 1));
+                    }
                     if (elect_one()) {
-                        const uint32_t col = tmem + kPairScaleCols + (g & 1) * 12;
+                        if (first_of_word)
+                            for (int a = 0; a < 3; ++a)
+                                tc_copy_scales<2>(col + 4 * a, scales + (g % kPairScaleBufs) * kPairScaleBuf + 512 * a);
                         const uint32_t idesc = p.idesc | mxf8_scale_byte(c & 3);
 #pragma unroll
                         for (int k = 0; k < kKC / 32; ++k)
                             tc_mma_mxf8<2>(acc, d + 2 * k, d + ((128 * kKC) >> 4) + 2 * k, idesc, col, col + 4, c > c0 || k > 0);
                         tc_commit_pair(empty + 8 * s);
-                        if (last_of_word) tc_commit_pair(sf_done + 8 * (g & 1));
+                        if (last_of_word) tc_commit_pair(sf_empty + 8 * (g % kPairScaleBufs));
                         if (c == c1 - 1) tc_commit_pair(acc_full + 8 * (seq & 1));
                     }
                     __syncwarp();
@@ -425,49 +429,36 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
             }
         }
-    } else if (warp == 3 && rank == 0) {
-        // Scale words from shared memory (four buffers, filled by the staging warps of both CTAs) to tensor memory
-        // (two, freed by the products that read them).
-        const int64_t words = (p.chunks + 3) >> 2;
-        uint32_t g = 0;
-        for (int64_t t = first; t < pp.tiles; t += step)
-            for (int64_t j = 0; j < words; ++j, ++g) {
-                const uint32_t b = g % kPairScaleBufs;
-                mbar_wait_cluster(sf_full + 8 * b, (g / kPairScaleBufs) & 1, &failed);
-                mbar_wait(sf_done + 8 * (g & 1), ((g >> 1) + 1) & 1, &failed);
-                tc_fence_after();
-                if (elect_one()) {
-                    for (int a = 0; a < 3; ++a)
-                        tc_copy_scales<2>(tmem + kPairScaleCols + (g & 1) * 12 + 4 * a, scales + b * kPairScaleBuf + 512 * a);
-                    tc_commit_pair(sf_empty + 8 * b);
-                    tc_commit_pair(sf_ready + 8 * (g & 1));
-                }
-                __syncwarp();
-            }
     } else if (warp == 2) {
+        const int words = (p.chunks + 3) >> 2;
         uint32_t g = 0;
-        const uint32_t lead_sf = cluster_map(sf_full, 0);
         for (int64_t t = first; t < pp.tiles; t += step) {
             int64_t m0, n0;
             pair_tile(pp, t, m0, n0);
-            const int64_t nr = n0 + 128 * rank + lane, mr = m0 + lane;
-            for (int j = 0; j <= (p.chunks - 1) >> 2; ++j, ++g) {
+            for (int j = 0; j < words; ++j, ++g) {
+                const uint32_t b = g % kPairScaleBufs, dst = scales + b * kPairScaleBuf;
                 const uint32_t *sn = p.sb + static_cast<int64_t>(j) * p.N, *sm = p.sa + static_cast<int64_t>(j) * p.M;
-                uint32_t w[3][4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    w[0][q] = nr + 32 * q < p.N ? ldg_early(sn + nr + 32 * q) : 0x01010101u;
-                    w[1][q] = mr + 32 * q < p.M ? ldg_early(sm + mr + 32 * q) : 0x01010101u;
-                    w[2][q] = mr + 128 + 32 * q < p.M ? ldg_early(sm + mr + 128 + 32 * q) : 0x01010101u;
-                }
-                const uint32_t b = g % kPairScaleBufs;
                 mbar_wait(sf_empty + 8 * b, (g / kPairScaleBufs + 1) & 1, &failed);
-                __syncwarp();
-                stage_scales<3>(scales + b * kPairScaleBuf + lane * 16, w);
+                copy_scales_async(dst, sn, n0 + 128 * rank, p.N, lane);
+                copy_scales_async(dst + 512, sm, m0, p.M, lane);
+                copy_scales_async(dst + 1024, sm, m0 + 128, p.M, lane);
+                copy_async_arrive(sf_here + 8 * b);
+            }
+        }
+    } else if (warp == 3) {
+        // Passes on to the pair's first CTA that a group of scales is here.  Not the copying warp's work: a release to
+        // the cluster waits for the thread's own copies under way.
+        const uint32_t lead_sf = cluster_map(sf_full, 0);
+        const uint32_t words = (p.chunks + 3) >> 2;
+        uint32_t g = 0;
+        for (int64_t t = first; t < pp.tiles; t += step)
+            for (uint32_t j = 0; j < words; ++j, ++g) {
+                const uint32_t b = g % kPairScaleBufs;
+                mbar_wait(sf_here + 8 * b, (g / kPairScaleBufs) & 1, &failed);
+                fence_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(lead_sf + 8 * b);
             }
-        }
     } else if (warp >= 4) {
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);

@@ -77,13 +77,19 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int *fa
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t mapped) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
 }
-__device__ __forceinline__ void mbar_wait_cluster(uint32_t bar, uint32_t parity, int *failed) {
-    mbar_wait(bar, parity, failed);
-    asm volatile(  // the phase is complete: this returns at once, with the wider scope
+__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar),
-        "r"(parity)
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
         : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void mbar_wait_cluster(uint32_t bar, uint32_t parity, int *failed) {
+    if (mbar_wait(bar, parity, failed)) mbar_test_cluster(bar, parity);  // complete: again, with the wider scope
 }
 
 // One 2-D tile of a tensor map (x: innermost, a multiple of 16 bytes) into
@@ -202,11 +208,14 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
 }
-// A read-only load that stays where it is written, ahead of a wait.
-__device__ __forceinline__ uint32_t ldg_early(const uint32_t *p) {
-    uint32_t v;
-    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
+// 4 bytes to shared memory without passing through a register; zero where !valid
+// (src is then any readable address).
+__device__ __forceinline__ void copy4_async(uint32_t dst, const uint32_t *src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+// One arrival on the mbarrier (whose count includes it) once the thread's copies so far have landed.
+__device__ __forceinline__ void copy_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // ------------------------------------------------------------------ clusters
