@@ -22,6 +22,7 @@
 
 #include "common.cuh"
 #include "fp8.cuh"
+#include "launch.cuh"
 
 namespace gar {
 namespace {
@@ -328,17 +329,14 @@ __device__ __forceinline__ float centred(int32_t count, int64_t choices, int exp
     return __fdividef(static_cast<float>(static_cast<int64_t>(count) * experts - choices), static_cast<float>(experts));
 }
 
-// Three launches, the second and third of which may begin before the one ahead
-// of them ends (programmatic dependent launch) and wait before they use what
-// it wrote.
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
+// Three launches.  The counting kernel reads z before it waits for the zeroing
+// one, which lets it begin only once the kernels ahead of both are done.
 __global__ void __launch_bounds__(kThreads) balance_zero_kernel(int32_t *counts, int n, uint32_t *seen) {
+    after_previous();
+    let_next_begin();
     const int i = blockIdx.x * kThreads + threadIdx.x;
     if (i < n) counts[i] = 0;
     if (i < 2) seen[i] = 0;
-    let_next_start();
 }
 
 template <typename T, int L, int V>
@@ -358,8 +356,8 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_co
     mine = __reduce_add_sync(0xFFFFFFFFu, mine);
     if (lane == 0 && mine) atomicAdd(&seen, mine);
     __syncthreads();
-    let_next_start();
-    wait_for_previous();
+    let_next_begin();
+    after_previous();
     for (int e = threadIdx.x; e < p.experts; e += kThreads)
         if (cnt[e]) atomicAdd(&p.counts[w * p.experts + e], cnt[e]);
     if (threadIdx.x == 0 && seen) atomicAdd(p.seen, seen);
@@ -373,7 +371,8 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(const __grid_con
     __shared__ float coef;
     __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = blockIdx.y, sub = lane & (L - 1);
-    wait_for_previous();
+    let_next_begin();
+    after_previous();
     const int64_t n = *p.seen;
     if (threadIdx.x == 0) coef = loss_scale(p, n);
     int64_t choices = 0;
@@ -435,6 +434,8 @@ __global__ void __launch_bounds__(kOneThreads) balance_one_kernel(const __grid_c
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (L - 1);
     for (int e = threadIdx.x; e < p.P * p.experts; e += kOneThreads) cnt[e] = 0;
     __syncthreads();
+    let_next_begin();
+    after_previous();
     constexpr int kPerWarp = 32 / L;
     const int chunks = static_cast<int>((p.tokens + kPerWarp - 1) / kPerWarp), items = chunks * p.P;
     int64_t n = 0;
@@ -479,34 +480,22 @@ int launch(const BalanceParams &p, cudaStream_t stream) {
     // One CTA up to four tokens a lane group: measured level with three launches at about eight.
     if constexpr (V == 8)
         if (p.tokens * p.P * L <= kOneThreads * 4 && p.P * p.experts <= kOneCounts) {
-            balance_one_kernel<T, L, V><<<1, kOneThreads, 0, stream>>>(p);
-            return check_launch("balance_one_kernel");
+            return launch_early("balance_one_kernel", balance_one_kernel<T, L, V>, dim3(1), kOneThreads, 0, 1, stream, p);
         }
     const int n = p.P * p.experts;
-    balance_zero_kernel<<<(n + kThreads - 1) / kThreads, kThreads, 0, stream>>>(p.counts, n, p.seen);
-    if (int rc = check_launch("balance_zero_kernel")) return rc;
+    const auto zero = launch_early("balance_zero_kernel", balance_zero_kernel, dim3(static_cast<unsigned>(ceil_div(n, kThreads))), kThreads, 0, 1,
+                                   stream, p.counts, n, p.seen);
+    if (zero) return zero;
     // as many CTAs as the SMs hold (registers), for each begins with the totals of all counts
     const auto blocks = [&](int per_sm) {
         const int64_t work = ceil_div(p.tokens, int64_t{kWarps} * (32 / L));
         const int64_t most = std::min(ceil_div(static_cast<int64_t>(sm_count()) * per_sm, p.P), int64_t{kMaxBlocks} / p.P);
         return static_cast<unsigned>(std::max(std::min(work, most), int64_t{1}));
     };
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks(V == 32 ? 3 : 6), static_cast<unsigned>(p.P));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, balance_count_kernel<T, L, V>, p);
-    if (e != cudaSuccess) return fail(GAR_ECUDA, "balance_count_kernel: %s", cudaGetErrorString(e));
-    if (int rc = check_launch("balance_count_kernel")) return rc;
-    cfg.gridDim = dim3(blocks(V == 32 ? 2 : 4), static_cast<unsigned>(p.P));
-    e = cudaLaunchKernelEx(&cfg, balance_grad_kernel<T, L, V>, p);
-    if (e != cudaSuccess) return fail(GAR_ECUDA, "balance_grad_kernel: %s", cudaGetErrorString(e));
-    return check_launch("balance_grad_kernel");
+    const unsigned P = static_cast<unsigned>(p.P);
+    if (int rc = launch_early("balance_count_kernel", balance_count_kernel<T, L, V>, dim3(blocks(V == 32 ? 3 : 6), P), kThreads, 0, 1, stream, p))
+        return rc;
+    return launch_early("balance_grad_kernel", balance_grad_kernel<T, L, V>, dim3(blocks(V == 32 ? 2 : 4), P), kThreads, 0, 1, stream, p);
 }
 
 template <typename T>

@@ -21,6 +21,7 @@
 
 #include "common.cuh"
 #include "fp8.cuh"
+#include "launch.cuh"
 #include "tensorcore.cuh"
 
 namespace gar {
@@ -129,6 +130,8 @@ __global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_c
     const int64_t row = blockIdx.x;
     const T *z = static_cast<const T *>(p.z) + row * p.ldz;
     T *dz = p.dz ? static_cast<T *>(p.dz) + row * p.lddz : nullptr;
+    let_next_begin();
+    after_previous();
     const float w = p.weight ? p.weight[row] : 1.0f;
     const int tid = threadIdx.x;
 
@@ -311,6 +314,8 @@ __global__ void __launch_bounds__(kStreamThreads, kLag ? 1 : 2) distill_stream_k
     }
     __syncthreads();
     if (kLag) cluster_barrier();
+    let_next_begin();
+    after_previous();
 
     if (warp == kMainWarps) {
         if (lane == 0) {
@@ -632,35 +637,31 @@ int launch_stream(const DistillParams &p, int64_t rows_at_once, size_t shared, c
     static std::atomic<int> resident[64][4];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(GAR_ECUDA, "no current device");
-    cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(kStreamThreads);
-    cfg.dynamicSmemBytes = shared;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kLag ? 1u << p.log_cluster : 1u;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    const unsigned cluster = kLag ? 1u << p.log_cluster : 1u;
     std::atomic<int> &known = resident[dev & 63][p.log_cluster];
     int clusters = known.load(std::memory_order_relaxed);
     if (clusters == 0) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
         clusters = 1;
         if (e == cudaSuccess && kLag) {
-            cfg.gridDim = dim3(1u << p.log_cluster);
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(cluster);
+            cfg.blockDim = dim3(kStreamThreads);
             cfg.dynamicSmemBytes = kSharedBytes;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = cluster;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
             e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
-            cfg.dynamicSmemBytes = shared;
         }
         if (e != cudaSuccess || clusters < 1) return fail(GAR_ECUDA, "distill_stream_kernel: %s", cudaGetErrorString(e));
         known.store(clusters, std::memory_order_relaxed);
     }
     if (!kLag || clusters > rows_at_once) clusters = static_cast<int>(rows_at_once);
-    cfg.gridDim = dim3(static_cast<unsigned>(clusters) << p.log_cluster);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
-    if (e != cudaSuccess) return fail(GAR_ECUDA, "distill_stream_kernel: %s", cudaGetErrorString(e));
-    return check_launch("distill_stream_kernel");
+    return launch_early("distill_stream_kernel", kernel, dim3(static_cast<unsigned>(clusters) << p.log_cluster), kStreamThreads, shared,
+                        cluster, stream, p);
 }
 
 template <typename T, bool kSaved>
@@ -681,8 +682,8 @@ int launch(DistillParams &p, cudaStream_t stream) {
     while (K < kMaxCluster && !fits(K, kSharedBytes)) K *= 2;
     while (K < kMaxCluster && p.rows * K * 2 <= sm_count() && part(K) >= 8192) K *= 2;
     if (bytes < kStreamBytes || !fits(K, kSharedBytes)) {
-        distill_row_kernel<T, kSaved><<<static_cast<unsigned>(p.rows), kRowThreads, 0, stream>>>(p);
-        return check_launch("distill_row_kernel");
+        return launch_early("distill_row_kernel", distill_row_kernel<T, kSaved>, dim3(static_cast<unsigned>(p.rows)), kRowThreads, 0, 1,
+                            stream, p);
     }
     p.log_cluster = K == 8 ? 3 : K / 2;
     p.stage_bytes = static_cast<int32_t>(part(K));

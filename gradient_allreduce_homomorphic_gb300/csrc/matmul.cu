@@ -24,6 +24,7 @@
 #include <atomic>
 
 #include "fp8.cuh"
+#include "launch.cuh"
 #include "tensorcore.cuh"
 
 namespace gar {
@@ -114,6 +115,7 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
     const int c0 = static_cast<int>(static_cast<int64_t>(p.chunks) * rank / p.splits);
     const int c1 = static_cast<int>(static_cast<int64_t>(p.chunks) * (rank + 1) / p.splits);
 
+    let_next_begin();
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * S::kStages + 2 * kScaleBufs + 1; ++i)
             mbar_init(full + 8 * i, i >= 2 * S::kStages && i < 2 * S::kStages + kScaleBufs ? 32 : 1);  // sf_full: a warp's copies
@@ -124,6 +126,7 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    after_previous();
     const uint32_t tmem = tmem_slot;
     const uint32_t sf_cols = tmem + TM;  // scale columns: kScaleBufs x (4 + 4 kAtomsB)
 
@@ -333,6 +336,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const bool overlap = pp.rows == 256;
     const uint32_t acc1 = overlap ? 224 : pp.rows;
 
+    let_next_begin();
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * kPairStages; ++i) mbar_init(full + 8 * i, 1);
         for (int i = 0; i < kPairScaleBufs; ++i) {
@@ -352,6 +356,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_barrier();
     tc_fence_after();
+    after_previous();
     const uint32_t tmem = tmem_slot;
 
     if (warp == 0 && lane == 0) {
@@ -568,21 +573,9 @@ int launch(MatmulParams &p, const uint8_t *a, int64_t lda, const uint8_t *b, int
     p.splits = 1;
     while (p.splits < 8 && tiles * p.splits * 2 <= sm_count() && p.chunks >= p.splits * 4) p.splits *= 2;
     if (tiles * p.splits > 0x7FFFFFFF) return fail(GAR_EINVAL, "the product has too many tiles");
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.splits));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     p.idesc = p.idesc | mxf8_idesc(0, 0, kTN, TM);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, matmul_kernel<TM>, map_n, map_m, p);
-    if (e != cudaSuccess) return fail(GAR_ECUDA, "matmul_kernel: %s", cudaGetErrorString(e));
-    return check_launch("matmul_kernel");
+    return launch_early("matmul_kernel", matmul_kernel<TM>, dim3(static_cast<unsigned>(tiles * p.splits)), kThreads, S::kSmem,
+                        static_cast<unsigned>(p.splits), stream, map_n, map_m, p);
 }
 
 // The rows of a pair's tiles: the count that finishes soonest.  A chunk of 128
@@ -607,19 +600,18 @@ int launch_pair(MatmulParams &mm, const uint8_t *a, int64_t lda, const uint8_t *
     static std::atomic<int> pairs_of[64];  // resident pairs per device, 0: not looked up yet
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(GAR_ECUDA, "no current device");
-    cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = pair_smem(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     int pairs = pairs_of[dev & 63].load(std::memory_order_relaxed);
     if (pairs == 0) {
+        cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kPairThreads);
+        cfg.dynamicSmemBytes = pair_smem(256);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
         cudaError_t e = cudaFuncSetAttribute(matmul_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, pair_smem(256));
         if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&pairs, matmul_pair_kernel<T>, &cfg);
         if (e != cudaSuccess || pairs < 1) return fail(GAR_ECUDA, "matmul_pair_kernel: %s", cudaGetErrorString(e));
@@ -639,11 +631,8 @@ int launch_pair(MatmulParams &mm, const uint8_t *a, int64_t lda, const uint8_t *
     CUtensorMap map_n{}, map_m{};
     if (int rc = encode(&map_n, b, mm.N, K, ldb, 128)) return rc;
     if (int rc = encode(&map_m, a, mm.M, K, lda, p.rows / 2)) return rc;
-    cfg.dynamicSmemBytes = pair_smem(p.rows);
-    cfg.gridDim = dim3(2 * static_cast<unsigned>(p.tiles < pairs ? p.tiles : pairs));
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, matmul_pair_kernel<T>, map_n, map_m, p);
-    if (e != cudaSuccess) return fail(GAR_ECUDA, "matmul_pair_kernel: %s", cudaGetErrorString(e));
-    return check_launch("matmul_pair_kernel");
+    return launch_early("matmul_pair_kernel", matmul_pair_kernel<T>, dim3(2 * static_cast<unsigned>(p.tiles < pairs ? p.tiles : pairs)),
+                        kPairThreads, pair_smem(p.rows), 2, stream, map_n, map_m, p);
 }
 
 int check_operand(const char *name, const uint8_t *q, int64_t ld, int64_t K, const uint8_t *scale, int32_t format) {

@@ -12,6 +12,7 @@
 // the scale type that the tensor core applies by itself.
 #include "common.cuh"
 #include "fp8.cuh"
+#include "launch.cuh"
 
 namespace gar {
 namespace {
@@ -154,6 +155,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) quantize_ker
     const int64_t tr = blockIdx.x / p.tiles_c, tc = blockIdx.x % p.tiles_c;
     const int64_t row0 = tr * kTile + half * 8, col0 = tc * kTile + hl * 8;
     const T *x = static_cast<const T *>(p.x) + row0 * p.ldx + col0;
+    let_next_begin();
+    after_previous();
     Patch<T> v;
     const int64_t left = p.cols - col0;
     if (p.vec && row0 + 8 <= p.rows && left >= 8) {
@@ -278,11 +281,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) quantize_ker
 }
 
 template <typename T>
-void launch(const QuantizeParams &p, unsigned blocks, cudaStream_t stream) {
-    if (p.emax == 15)
-        quantize_kernel<T, true><<<blocks, kThreads, 0, stream>>>(p);
-    else
-        quantize_kernel<T, false><<<blocks, kThreads, 0, stream>>>(p);
+int launch(const QuantizeParams &p, unsigned blocks, cudaStream_t stream) {
+    const auto kernel = p.emax == 15 ? quantize_kernel<T, true> : quantize_kernel<T, false>;
+    return launch_early("quantize_kernel", kernel, dim3(blocks), kThreads, 0, 1, stream, p);
 }
 
 int check_codes(const char *name, const void *q, int64_t ld, int64_t cols, const void *scale) {
@@ -329,9 +330,5 @@ extern "C" int gar_fp8_quantize(const void *x, int32_t dtype, int64_t rows, int6
     p.vec = aligned(x, 16) && (ldx * elem_bytes(dtype)) % 16 == 0;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const unsigned blocks = static_cast<unsigned>(tiles_r * tiles_c);
-    if (dtype == GAR_F32)
-        launch<float>(p, blocks, stream);
-    else
-        launch<uint16_t>(p, blocks, stream);
-    return check_launch("quantize_kernel");
+    return dtype == GAR_F32 ? launch<float>(p, blocks, stream) : launch<uint16_t>(p, blocks, stream);
 }
