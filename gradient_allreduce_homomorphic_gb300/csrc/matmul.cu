@@ -21,6 +21,7 @@
 // store.  A grid with fewer tiles than SMs splits k over a cluster of up to 8
 // CTAs, whose partial tiles are added through distributed shared memory in
 // rank order, so the result does not depend on timing.
+#include <algorithm>
 #include <atomic>
 
 #include "fp8.cuh"
@@ -43,7 +44,6 @@ struct MatmulParams {
     void *d;
     const void *c;
     int64_t ldd, ldc;
-    int32_t bf16;
     int32_t tiles_n;
     int32_t splits;           // CTAs of a cluster along k
     unsigned int *status;
@@ -54,23 +54,64 @@ struct Shape {
     static constexpr int kBytesA = kTN * kKC;  // D's columns: the operand b
     static constexpr int kBytesB = TM * kKC;
     static constexpr int kStage = kBytesA + kBytesB;
-    static constexpr int kStages = TM == 256 ? 4 : TM == 128 ? 6 : 8;
-    static constexpr int kAtomsB = TM > 128 ? 2 : 1;
-    static constexpr int kScaleBuf = 512 * (1 + kAtomsB);
-    static constexpr int kColumns = TM == 256 ? 512 : TM == 128 ? 256 : TM == 64 ? 128 : 64;
+    static constexpr int kResident = TM == 128 ? 1 : 2;  // CTAs an SM has shared memory for
+    static constexpr int kStages = TM == 128 ? 6 : TM == 64 ? 4 : 5;
+    static constexpr int kScaleBuf = 512 * 2;            // 128 rows of each operand
+    static constexpr int kColumns = TM == 128 ? 256 : TM == 64 ? 128 : 64;
     static constexpr int kSmem = 1024 + kStages * kStage + kScaleBufs * kScaleBuf;
 };
 
-__device__ __forceinline__ float load_out(const MatmulParams &p, int64_t m, int64_t n) {
-    const int64_t i = m * p.ldc + n;
-    return p.bf16 ? bf16_one(static_cast<const uint16_t *>(p.c)[i]) : static_cast<const float *>(p.c)[i];
+// 32 accumulator columns to rows m .. of column n of D, c added where given.
+template <typename T>
+__device__ __forceinline__ void store32(const float (&v)[32], T *d, int64_t ldd, const T *c, int64_t ldc, int count) {
+    if (c) {
+        float x[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = j < count ? load_f32(c + j * ldc) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < count) store_f32(d + j * ldd, v[j] + x[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < count) store_f32(d + j * ldd, v[j]);
+    }
 }
-__device__ __forceinline__ void store_out(const MatmulParams &p, int64_t m, int64_t n, float v) {
-    const int64_t i = m * p.ldd + n;
-    if (p.bf16)
-        static_cast<uint16_t *>(p.d)[i] = to_bf16(v);
-    else
-        static_cast<float *>(p.d)[i] = v;
+
+// The sum of kSplits CTAs' partial tiles [m][128], in rank order, to rows m .. of
+// D: this CTA's share of the tile's `rows` rows.  A thread has 32 loads of
+// distributed shared memory under way.
+template <int kSplits, typename T>
+__device__ __forceinline__ void add_partials(const MatmulParams &p, uint32_t base, int rank, int64_t m0, int64_t n0, int rows) {
+    constexpr int kRows = 8 / kSplits;  // of a warp at a time
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t from[kSplits];
+#pragma unroll
+    for (int r = 0; r < kSplits; ++r) from[r] = cluster_map(base, r) + lane * 4;
+    T *d = static_cast<T *>(p.d) + m0 * p.ldd + n0 + lane;
+    const T *c = static_cast<const T *>(p.c) + m0 * p.ldc + n0 + lane;
+    for (int j0 = (rank * (kThreads / 32) + warp) * kRows; j0 < rows; j0 += kSplits * (kThreads / 32) * kRows) {
+        float v[kRows][4][kSplits];
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < kSplits; ++r)  // past the last row it reads what it will not use
+                    v[j][i][r] = cluster_load(from[r] + ((j0 + j < rows ? j0 + j : 0) * kTN + 32 * i) * 4);
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float x = v[j][i][0];
+#pragma unroll
+                for (int r = 1; r < kSplits; ++r) x += v[j][i][r];
+                if (j0 + j < rows && n0 + lane + 32 * i < p.N) {
+                    if (p.c) x += load_f32(c + (j0 + j) * p.ldc + 32 * i);
+                    store_f32(d + (j0 + j) * p.ldd + 32 * i, x);
+                }
+            }
+    }
 }
 
 // The scale words of 128 rows r0 .. of a matrix (its words of one group of four
@@ -95,7 +136,7 @@ __device__ __noinline__ void mbar_drain(uint32_t full, uint32_t stages, int issu
     }
 }
 
-template <int TM>
+template <typename T, int TM>
 __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant__ CUtensorMap map_n,
                                                           const __grid_constant__ CUtensorMap map_m,
                                                           const __grid_constant__ MatmulParams p) {
@@ -128,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
     tc_fence_after();
     after_previous();
     const uint32_t tmem = tmem_slot;
-    const uint32_t sf_cols = tmem + TM;  // scale columns: kScaleBufs x (4 + 4 kAtomsB)
+    const uint32_t sf_cols = tmem + TM;  // scale columns: kScaleBufs x (4 + 4)
 
     if (warp == 0 && lane == 0) {
         tma_prefetch_map(&map_n);
@@ -156,15 +197,14 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
                 mbar_wait(sf_full + 8 * b, (g / kScaleBufs) & 1, &failed);
                 fence_async_shared();
                 if (elect_one())
-                    for (int a = 0; a < 1 + S::kAtomsB; ++a)
-                        tc_copy_scales<1>(sf_cols + (b * (1 + S::kAtomsB) + a) * 4, scales + b * S::kScaleBuf + 512 * a);
+                    for (int a = 0; a < 2; ++a) tc_copy_scales<1>(sf_cols + (2 * b + a) * 4, scales + b * S::kScaleBuf + 512 * a);
                 __syncwarp();
             }
             mbar_wait(full + 8 * s, turn, &failed);
             tc_fence_after();
             if (elect_one()) {
                 const uint64_t d = desc + s * (S::kStage >> 4);
-                const uint32_t col = sf_cols + (g % kScaleBufs) * 4 * (1 + S::kAtomsB);
+                const uint32_t col = sf_cols + (g % kScaleBufs) * 8;
                 const uint32_t idesc = p.idesc | mxf8_scale_byte(c & 3);
 #pragma unroll
                 for (int k = 0; k < kKC / 32; ++k)
@@ -183,9 +223,7 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
             const uint32_t b = g % kScaleBufs, dst = scales + b * S::kScaleBuf;
             mbar_wait(sf_empty + 8 * b, (g / kScaleBufs + 1) & 1, &failed);
             copy_scales_async(dst, p.sb + static_cast<int64_t>(j0 + g) * p.N, n0, p.N, lane);
-#pragma unroll
-            for (int a = 0; a < S::kAtomsB; ++a)
-                copy_scales_async(dst + 512 * (1 + a), p.sa + static_cast<int64_t>(j0 + g) * p.M, m0 + 128 * a, p.M, lane);
+            copy_scales_async(dst + 512, p.sa + static_cast<int64_t>(j0 + g) * p.M, m0, p.M, lane);
             copy_async_arrive(sf_full + 8 * b);
         }
     }
@@ -197,54 +235,33 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
     const int quarter = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const int64_t n = n0 + quarter * 32 + lane;
-    const int64_t mleft = p.M - m0;
-    if (p.splits == 1) {
-        if (warp >= 4) {
+    const int rows = static_cast<int>(p.M - m0 < TM ? p.M - m0 : TM);
+    if (warp >= 4) {
 #pragma unroll 1
-            for (int j0 = 0; j0 < TM && j0 < mleft; j0 += 32) {
-                float v[32];
-                tc_load32(v, lanes + j0);
-                tc_wait_ld();
-                if (c0 == c1)
+        for (int j0 = 0; j0 < rows; j0 += 32) {
+            float v[32];
+            tc_load32(v, lanes + j0);
+            tc_wait_ld();
+            if (c0 == c1)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                if (n < p.N)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j0 + j < mleft) {
-                            float x = v[j];
-                            if (p.c) x += load_out(p, m0 + j0 + j, n);
-                            store_out(p, m0 + j0 + j, n, x);
-                        }
-            }
-        }
-    } else {
-        // every load of the stages has been consumed: they hold the partial tile [m][n] now
-        if (warp >= 4) {
-#pragma unroll 1
-            for (int j0 = 0; j0 < TM && j0 < mleft; j0 += 32) {
-                float v[32];
-                tc_load32(v, lanes + j0);
-                tc_wait_ld();
+                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+            if (p.splits > 1) {  // every copy into the stages has been used: they hold the partial tile [m][n] now
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((j0 + j) * kTN + quarter * 32 + lane) * 4),
-                                 "f"(c0 == c1 ? 0.0f : v[j])
-                                 : "memory");
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((j0 + j) * kTN + quarter * 32 + lane) * 4), "f"(v[j]) : "memory");
+            } else if (n < p.N) {
+                T *d = static_cast<T *>(p.d) + (m0 + j0) * p.ldd + n;
+                const T *c = p.c ? static_cast<const T *>(p.c) + (m0 + j0) * p.ldc + n : nullptr;
+                store32<T>(v, d, p.ldd, c, p.ldc, rows - j0 < 32 ? rows - j0 : 32);
             }
         }
+    }
+    if (p.splits > 1) {
+        __syncwarp();
         cluster_barrier();
-        for (int j = rank * (kThreads / kTN) + static_cast<int>(threadIdx.x) / kTN; j < TM && j < mleft;
-             j += p.splits * (kThreads / kTN)) {
-            const int col = static_cast<int>(threadIdx.x) % kTN;
-            const uint32_t at = base + (j * kTN + col) * 4;
-            float x = 0.0f;
-            for (int r = 0; r < p.splits; ++r) x += cluster_load(cluster_map(at, r));
-            if (n0 + col < p.N) {
-                if (p.c) x += load_out(p, m0 + j, n0 + col);
-                store_out(p, m0 + j, n0 + col, x);
-            }
-        }
+        if (p.splits == 2) add_partials<2, T>(p, base, rank, m0, n0, rows);
+        if (p.splits == 4) add_partials<4, T>(p, base, rank, m0, n0, rows);
+        if (p.splits == 8) add_partials<8, T>(p, base, rank, m0, n0, rows);
         cluster_barrier();  // no CTA leaves while another reads its shared memory
     }
     tc_fence_before();
@@ -296,23 +313,6 @@ __device__ __forceinline__ void pair_tile(const PairParams &p, int64_t t, int64_
     const int64_t rows = p.tiles_m - g * 8 < 8 ? p.tiles_m - g * 8 : 8;
     m0 = (g * 8 + in % rows) * p.rows;
     n0 = in / rows * 256;
-}
-
-// 32 accumulator columns to rows m .. of column n of D, c added where given.
-template <typename T>
-__device__ __forceinline__ void store32(const float (&v)[32], T *d, int64_t ldd, const T *c, int64_t ldc, int count) {
-    if (c) {
-        float x[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = j < count ? load_f32(c + j * ldc) : 0.0f;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < count) store_f32(d + j * ldd, v[j] + x[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < count) store_f32(d + j * ldd, v[j]);
-    }
 }
 
 template <typename T>
@@ -550,57 +550,99 @@ int encode(CUtensorMap *map, const uint8_t *q, int64_t rows, int64_t K, int64_t 
     return GAR_OK;
 }
 
-template <int TM>
-int launch(MatmulParams &p, const uint8_t *a, int64_t lda, const uint8_t *b, int64_t ldb, int64_t K, cudaStream_t stream) {
+// Clusters of `splits` CTAs that the device holds at one time (its SMs come in
+// groups, so it is fewer than its SMs would make; one more would run after all
+// others); looked up once.  < 1: an error, reported.
+template <typename T, int TM>
+int resident_clusters(int splits) {
     using S = Shape<TM>;
-    static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
+    static std::atomic<int> known[64][4];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(GAR_ECUDA, "no current device");
-    const uint64_t bit = 1ull << (dev & 63);
-    if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(matmul_kernel<TM>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-        if (e != cudaSuccess) return fail(GAR_ECUDA, "matmul_kernel: %s", cudaGetErrorString(e));
-        ready.fetch_or(bit, std::memory_order_relaxed);
+    std::atomic<int> &slot = known[dev & 63][splits == 8 ? 3 : splits / 2];
+    int n = slot.load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(splits));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = S::kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        cudaError_t e = cudaFuncSetAttribute(matmul_kernel<T, TM>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, matmul_kernel<T, TM>, &cfg);
+        if (e != cudaSuccess || n < 1) return fail(GAR_ECUDA, "matmul_kernel: %s", cudaGetErrorString(e));
+        slot.store(n, std::memory_order_relaxed);
     }
+    return n;
+}
+
+// A product by CTAs of TM rows: its tiles, the CTAs that split k of each and
+// what it takes, in ns, by measurements at M of 16 to 2048, N of 128 to 4096
+// and K of 512 to 8192: 3.9 us, 0.33 for a chunk, 1.4 for the exchange of
+// partial tiles, and a wave more as often as the CTAs exceed the SMs.  So k is
+// split from 12 chunks on, down to four a CTA, as far as all clusters run at
+// one time.
+struct Plan {
+    int64_t tiles, ns;
+    int splits;
+};
+template <typename T, int TM>
+int plan(const MatmulParams &p, Plan *out) {
+    out->tiles = ceil_div(p.N, int64_t{kTN}) * ceil_div(p.M, int64_t{TM});
+    out->splits = 1;
+    int resident = resident_clusters<T, TM>(1);
+    if (resident < 1) return resident;
+    const int64_t waves = ceil_div(out->tiles, int64_t{resident});
+    for (int splits = 2; p.chunks >= 12 && splits <= 8 && p.chunks >= 4 * splits; splits *= 2) {
+        const int n = resident_clusters<T, TM>(splits);
+        if (n < 1) return n;
+        if (out->tiles <= n / Shape<TM>::kResident) out->splits = splits;
+    }
+    out->ns = 3900 + 330 * ceil_div(p.chunks, int64_t{out->splits}) + (out->splits > 1 ? 1400 : 0) + (waves - 1) * (1500 + 330 * p.chunks);
+    return GAR_OK;
+}
+
+template <typename T, int TM>
+int launch(MatmulParams &p, const Plan &how, const uint8_t *a, int64_t lda, const uint8_t *b, int64_t ldb, int64_t K, cudaStream_t stream) {
+    using S = Shape<TM>;
     CUtensorMap map_n{}, map_m{};
     if (K > 0) {
         if (int rc = encode(&map_n, b, p.N, K, ldb, kTN)) return rc;
         if (int rc = encode(&map_m, a, p.M, K, lda, TM)) return rc;
     }
-    p.tiles_n = static_cast<int32_t>(ceil_div(p.N, kTN));
-    const int64_t tiles = p.tiles_n * ceil_div(p.M, int64_t{TM});
-    // split k while the cluster's CTAs still find SMs and have two chunks each
-    p.splits = 1;
-    while (p.splits < 8 && tiles * p.splits * 2 <= sm_count() && p.chunks >= p.splits * 4) p.splits *= 2;
-    if (tiles * p.splits > 0x7FFFFFFF) return fail(GAR_EINVAL, "the product has too many tiles");
+    p.tiles_n = static_cast<int32_t>(ceil_div(p.N, int64_t{kTN}));
+    p.splits = how.splits;
+    if (how.tiles * how.splits > 0x7FFFFFFF) return fail(GAR_EINVAL, "the product has too many tiles");
     p.idesc = p.idesc | mxf8_idesc(0, 0, kTN, TM);
-    return launch_early("matmul_kernel", matmul_kernel<TM>, dim3(static_cast<unsigned>(tiles * p.splits)), kThreads, S::kSmem,
+    return launch_early("matmul_kernel", matmul_kernel<T, TM>, dim3(static_cast<unsigned>(how.tiles * how.splits)), kThreads, S::kSmem,
                         static_cast<unsigned>(p.splits), stream, map_n, map_m, p);
 }
 
-// The rows of a pair's tiles: the count that finishes soonest.  A chunk of 128
-// k takes the tensor cores 2 TM clocks and its operands, at the 70 bytes a
-// clock that an SM gets from L2 when all load, (128 + TM / 2) 128 / 70; a wave
-// adds its prologue, more where the accumulators overlap.
+// The rows of a pair's tiles: the count that finishes soonest.  In clocks, as
+// measured at K = 2048 and 8192 for 192, 224 and 256 rows: a chunk of 128 k
+// takes 2 TM + 28, but no less than the issuing thread's 516; a tile begins 500
+// after its predecessor's last chunk, 2600 where the accumulators overlap.
+int64_t pair_clocks(int rows, int64_t M, int64_t tiles_n, int64_t chunks, int pairs) {
+    const int64_t waves = ceil_div(ceil_div(M, int64_t{rows}) * tiles_n, int64_t{pairs});
+    return waves * (chunks * std::max(2 * rows + 28, 516) + (rows == 256 ? 2600 : 500));
+}
 int pair_rows(int64_t M, int64_t tiles_n, int64_t chunks, int pairs) {
     int best = 256;
-    int64_t least = INT64_MAX;
-    for (int rows = 256; rows >= 128; rows -= 32) {
-        const int64_t waves = ceil_div(ceil_div(M, int64_t{rows}) * tiles_n, int64_t{pairs});
-        const int64_t load = (128 + rows / 2) * 128 / 70, mma = 2 * rows;
-        const int64_t cost = waves * (chunks * (mma > load ? mma : load) + (rows == 256 ? 2500 : 500));
-        if (cost < least) least = cost, best = rows;
-    }
+    for (int rows = 224; rows >= 128; rows -= 32)
+        if (pair_clocks(rows, M, tiles_n, chunks, pairs) < pair_clocks(best, M, tiles_n, chunks, pairs)) best = rows;
     return best;
 }
 
 template <typename T>
-int launch_pair(MatmulParams &mm, const uint8_t *a, int64_t lda, const uint8_t *b, int64_t ldb, int64_t K,
-                cudaStream_t stream) {
-    static std::atomic<int> pairs_of[64];  // resident pairs per device, 0: not looked up yet
+int resident_pairs() {
+    static std::atomic<int> known[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(GAR_ECUDA, "no current device");
-    int pairs = pairs_of[dev & 63].load(std::memory_order_relaxed);
+    int pairs = known[dev & 63].load(std::memory_order_relaxed);
     if (pairs == 0) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(2);
@@ -615,8 +657,14 @@ int launch_pair(MatmulParams &mm, const uint8_t *a, int64_t lda, const uint8_t *
         cudaError_t e = cudaFuncSetAttribute(matmul_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, pair_smem(256));
         if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&pairs, matmul_pair_kernel<T>, &cfg);
         if (e != cudaSuccess || pairs < 1) return fail(GAR_ECUDA, "matmul_pair_kernel: %s", cudaGetErrorString(e));
-        pairs_of[dev & 63].store(pairs, std::memory_order_relaxed);
+        known[dev & 63].store(pairs, std::memory_order_relaxed);
     }
+    return pairs;
+}
+
+template <typename T>
+int launch_pair(MatmulParams &mm, int pairs, const uint8_t *a, int64_t lda, const uint8_t *b, int64_t ldb, int64_t K,
+                cudaStream_t stream) {
     PairParams p{};
     mm.tiles_n = static_cast<int32_t>(ceil_div(mm.N, int64_t{256}));
     p.rows = pair_rows(mm.M, mm.tiles_n, mm.chunks, pairs);
@@ -633,6 +681,29 @@ int launch_pair(MatmulParams &mm, const uint8_t *a, int64_t lda, const uint8_t *
     if (int rc = encode(&map_m, a, mm.M, K, lda, p.rows / 2)) return rc;
     return launch_early("matmul_pair_kernel", matmul_pair_kernel<T>, dim3(2 * static_cast<unsigned>(p.tiles < pairs ? p.tiles : pairs)),
                         kPairThreads, pair_smem(p.rows), 2, stream, map_n, map_m, p);
+}
+
+// Small products by single CTAs, large ones by pairs: whichever the measurements
+// behind plan() and pair_clocks() say is sooner done (a pair's kernel takes 5.8 us
+// beside its tiles).
+template <typename T, int TM>
+int choose_for(MatmulParams &p, const uint8_t *a, int64_t lda, const uint8_t *b, int64_t ldb, int64_t K, cudaStream_t stream) {
+    Plan how;
+    if (int rc = plan<T, TM>(p, &how)) return rc;
+    if (K > 0) {
+        const int pairs = resident_pairs<T>();
+        if (pairs < 1) return pairs;
+        const int64_t tiles_n = ceil_div(p.N, int64_t{256});
+        const int64_t clocks = pair_clocks(pair_rows(p.M, tiles_n, p.chunks, pairs), p.M, tiles_n, p.chunks, pairs);
+        if (5800 + clocks * 10 / 19 < how.ns) return launch_pair<T>(p, pairs, a, lda, b, ldb, K, stream);
+    }
+    return launch<T, TM>(p, how, a, lda, b, ldb, K, stream);
+}
+template <typename T>
+int choose(MatmulParams &p, const uint8_t *a, int64_t lda, const uint8_t *b, int64_t ldb, int64_t K, cudaStream_t stream) {
+    if (p.M <= 32) return choose_for<T, 32>(p, a, lda, b, ldb, K, stream);
+    if (p.M <= 64) return choose_for<T, 64>(p, a, lda, b, ldb, K, stream);
+    return choose_for<T, 128>(p, a, lda, b, ldb, K, stream);
 }
 
 int check_operand(const char *name, const uint8_t *q, int64_t ld, int64_t K, const uint8_t *scale, int32_t format) {
@@ -667,14 +738,8 @@ extern "C" int gar_fp8_matmul(const uint8_t *a, int64_t lda, const uint8_t *a_sc
     p.sa = reinterpret_cast<const uint32_t *>(a_scale), p.sb = reinterpret_cast<const uint32_t *>(b_scale);
     p.M = M, p.N = N, p.chunks = static_cast<int32_t>(ceil_div(K, int64_t{kKC}));
     p.idesc = mxf8_idesc(b_format == GAR_F8E5M2, a_format == GAR_F8E5M2, 0, 0);  // the tile is transposed
-    p.d = d, p.ldd = ldd, p.c = c, p.ldc = ldc, p.bf16 = dtype == GAR_BF16;
+    p.d = d, p.ldd = ldd, p.c = c, p.ldc = ldc;
     p.status = device_status();
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    if (K > 0 && ceil_div(M, int64_t{256}) * ceil_div(N, int64_t{256}) >= sm_count() / 2)
-        return p.bf16 ? launch_pair<uint16_t>(p, a, lda, b, ldb, K, stream) : launch_pair<float>(p, a, lda, b, ldb, K, stream);
-    if (M <= 32) return launch<32>(p, a, lda, b, ldb, K, stream);
-    if (M <= 64) return launch<64>(p, a, lda, b, ldb, K, stream);
-    if (ceil_div(M, int64_t{256}) * ceil_div(N, int64_t{kTN}) < sm_count())
-        return launch<128>(p, a, lda, b, ldb, K, stream);
-    return launch<256>(p, a, lda, b, ldb, K, stream);
+    return dtype == GAR_BF16 ? choose<uint16_t>(p, a, lda, b, ldb, K, stream) : choose<float>(p, a, lda, b, ldb, K, stream);
 }
