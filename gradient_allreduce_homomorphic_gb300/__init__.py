@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 import threading
 from dataclasses import dataclass
 
@@ -101,7 +102,7 @@ _SIGNATURES = {
                                    _vp]),
     "gar_distill_grad": (C.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i32, C.c_float, _vp, _vp, _vp, _i64, _vp]),
     "gar_balance_workspace_bytes": (C.c_size_t, [_i32]),
-    "gar_balance_loss": (C.c_int, [_pp, _i32, _i64, _i32, _i64, _i32, _i32, _pp, C.c_float, _pp, _vp, _vp, _pp, _i64,
+    "gar_balance_loss": (C.c_int, [_vp, _i32, _i64, _i32, _i64, _i32, _i32, _vp, C.c_float, _vp, _vp, _vp, _vp, _i64,
                                    _vp, C.c_size_t, _vp]),
 }
 
@@ -790,25 +791,32 @@ def gar_balance_workspace_bytes(P: int) -> int:
     return int(load().gar_balance_workspace_bytes(P))
 
 
+def _worker_fits(t, name, shape, stride, dtype):
+    """Whether one worker's tensor is as asked; what _workers' quick comparison turned down may still be."""
+    if not t.is_cuda:
+        _dev(t)
+    if t.dtype != dtype and not (dtype is _UINT8 and t.element_size() == 1):
+        raise GarError(GAR_EDTYPE, f"{name} is {t.dtype}, not {dtype}")
+    if t.shape != shape or (t.stride() != stride and shape[0] > 1):
+        raise GarError(GAR_EINVAL, f"{name} has a tensor of shape {tuple(t.shape)}, not {shape}, or of another stride")
+
+
 def _workers(given, name, P, shape, dtype):
-    """(pointer array, row stride) of one tensor per worker, each of the given
-    shape and type and all of one row stride.  A PtrTable's tensors were put
-    together before: its first is looked at."""
-    tensors = given.tensors if isinstance(given, PtrTable) else given
+    """(pointers, row stride) of one tensor per worker, each of the given shape
+    and type and all of one row stride.  A PtrTable's tensors were put together
+    before: its first is looked at."""
+    table = isinstance(given, PtrTable)
+    tensors = given.tensors if table else given
     if len(tensors) != P:
         raise GarError(GAR_EINVAL, f"{name} has {len(tensors)} tensors, not {P}")
-    first = tensors[0].stride()
-    if len(first) != len(shape) or (first[-1] != 1 and shape[-1] > 1):
-        raise GarError(GAR_EINVAL, f"{name}: a tensor is not of shape {shape} with contiguous rows")
-    ptrs = []
-    for t in tensors[:1] if isinstance(given, PtrTable) else tensors:
-        if t.shape != shape or (t.stride() != first and shape[0] > 1):
-            raise GarError(GAR_EINVAL, f"{name} has a tensor of shape {tuple(t.shape)}, not {shape}, or of another stride")
-        if t.dtype != dtype and not (dtype is _UINT8 and t.element_size() == 1):
-            raise GarError(GAR_EDTYPE, f"{name} is {t.dtype}, not {dtype}")
-        ptrs.append(_dev(t))
-    array = given.array if isinstance(given, PtrTable) else (C.c_void_p * P)(*ptrs)
-    return array, first[0] if shape[0] > 1 or len(shape) == 1 else max(shape[-1], 1)
+    stride, ptrs = tensors[0].stride(), []
+    for t in tensors[:1] if table else tensors:
+        if t.dtype is not dtype or t.shape != shape or not t.is_cuda or t.stride() != stride:
+            _worker_fits(t, name, shape, stride, dtype)
+        ptrs.append(t.data_ptr())
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise GarError(GAR_EINVAL, f"{name}: the elements of a row are not contiguous")
+    return given.array if table else struct.pack(f"{P}Q", *ptrs), stride[0] if shape[0] > 1 else max(shape[-1], 1)
 
 
 def gar_balance_loss(z, k: int, alpha: float, choice, counts, loss, workspace, dz=None, valid=None, stream=None):
@@ -822,9 +830,9 @@ def gar_balance_loss(z, k: int, alpha: float, choice, counts, loss, workspace, d
     za, ldz = _workers(z, "z", P, (tokens, experts), first.dtype)
     ca, ldc = _workers(choice, "choice", P, (tokens, k), _INT32)
     da, lddz = _workers(dz, "dz", P, (tokens, experts), first.dtype) if dz is not None else (None, 0)
-    va, step = _workers(valid, "valid", P, (tokens,), _UINT8) if valid is not None else (None, 1)
-    if (ldc != k and tokens > 1) or (step != 1 and tokens > 1):
-        raise GarError(GAR_EINVAL, "choice and valid have to be contiguous")
+    va = _workers(valid, "valid", P, (tokens,), _UINT8)[0] if valid is not None else None
+    if ldc != k:
+        raise GarError(GAR_EINVAL, "choice has to be contiguous")
     _call("gar_balance_loss", za, P, tokens, experts, ldz, dtype, k, va, alpha, ca,
           _vector(counts, "counts", _INT32, P * experts), _vector(loss, "loss", _FLOAT32, 1), da, lddz, _dev(workspace),
           workspace.numel() * workspace.element_size(), _stream(stream))

@@ -19,10 +19,12 @@
 // KB of loads in flight; with V = 8 few tokens spread over more warps.  Bound by HBM for many experts (z is read twice, the second
 // time in part from L2), by the selection's instructions for many choices.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "fp8.cuh"
 #include "launch.cuh"
+#include "tensorcore.cuh"
 
 namespace gar {
 namespace {
@@ -31,7 +33,7 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 32;
 constexpr int kMaxBlocks = 4096;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kOneThreads = 512;           // the one-CTA kernel
+constexpr int kOneThreads = 512;           // a CTA of the one-cluster kernel
 constexpr int kOneCounts = 4096;           // its counts: workers x experts
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -45,7 +47,7 @@ struct BalanceParams {
     int32_t wide, dwide; // whether rows of z, of dz may be accessed 16 bytes at a time
     float alpha;
     int32_t *counts;     // [P, experts]
-    uint32_t *seen;      // workspace: tokens that count; CTAs done
+    uint32_t *seen;      // workspace: CTAs done; each worker's tokens that count
     float *partial;      // workspace: sum of d_t per CTA
     float *loss;
 };
@@ -301,16 +303,16 @@ __device__ __forceinline__ float gradient(const BalanceParams &p, int w, int64_t
 }
 
 // A CTA's sum of integers, the same value in every thread.
-template <int kN>
 __device__ __forceinline__ int64_t cta_count(int64_t v, int64_t *scratch) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    if (lane == 0) scratch[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = scratch[threadIdx.x & (kN / 32 - 1)];
+    v = lane < static_cast<int>(blockDim.x >> 5) ? scratch[lane] : 0;
 #pragma unroll
-    for (int o = kN / 64; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
 
@@ -329,17 +331,21 @@ __device__ __forceinline__ float centred(int32_t count, int64_t choices, int exp
     return __fdividef(static_cast<float>(static_cast<int64_t>(count) * experts - choices), static_cast<float>(experts));
 }
 
-// Three launches.  The counting kernel reads z before it waits for the zeroing
-// one, which lets it begin only once the kernels ahead of both are done.
-__global__ void __launch_bounds__(kThreads) balance_zero_kernel(int32_t *counts, int n, uint32_t *seen) {
+// Two or three launches.  With kTogether, blockIdx.y's CTAs are one cluster,
+// which adds its counts in distributed shared memory and stores a worker's whole
+// counts; else the counts are zeroed by a kernel ahead and added with atomics
+// (integers: their order does not matter).  The counting kernel reads z before
+// it waits for the zeroing one, which lets it begin only once the kernels ahead
+// of both are done.
+__global__ void __launch_bounds__(kThreads) balance_zero_kernel(int32_t *counts, int n, uint32_t *seen, int workers) {
     after_previous();
     let_next_begin();
     const int i = blockIdx.x * kThreads + threadIdx.x;
     if (i < n) counts[i] = 0;
-    if (i < 2) seen[i] = 0;
+    if (i <= workers) seen[i] = 0;
 }
 
-template <typename T, int L, int V>
+template <typename T, int L, int V, bool kTogether>
 __global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_constant__ BalanceParams p) {
     __shared__ int32_t cnt[kMaxExperts];
     __shared__ uint64_t list[L >= 8 && V == 32 ? kWarps : 1][32 / L * kList];
@@ -348,6 +354,10 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_co
     for (int e = threadIdx.x; e < p.experts; e += kThreads) cnt[e] = 0;
     if (threadIdx.x == 0) seen = 0;
     __syncthreads();
+    if (kTogether) {
+        let_next_begin();
+        after_previous();
+    }
     constexpr int kPerWarp = 32 / L;
     uint32_t mine = 0;
     for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kPerWarp; t0 < p.tokens;
@@ -356,11 +366,28 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_co
     mine = __reduce_add_sync(0xFFFFFFFFu, mine);
     if (lane == 0 && mine) atomicAdd(&seen, mine);
     __syncthreads();
-    let_next_begin();
-    after_previous();
-    for (int e = threadIdx.x; e < p.experts; e += kThreads)
-        if (cnt[e]) atomicAdd(&p.counts[w * p.experts + e], cnt[e]);
-    if (threadIdx.x == 0 && seen) atomicAdd(p.seen, seen);
+    if (kTogether) {
+        const int C = gridDim.x;
+        cluster_barrier();
+        for (int e = blockIdx.x * kThreads + threadIdx.x; e < p.experts; e += C * kThreads) {
+            int32_t sum = 0;
+            for (int r = 0; r < C; ++r) sum += cluster_load_int(cluster_map(smem_u32(cnt + e), r));
+            p.counts[w * p.experts + e] = sum;
+        }
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            uint32_t sum = 0;
+            for (int r = 0; r < C; ++r) sum += cluster_load_int(cluster_map(smem_u32(&seen), r));
+            p.seen[1 + w] = sum;
+            if (w == 0) p.seen[0] = 0;
+        }
+        cluster_barrier();  // no CTA leaves while another reads its shared memory
+    } else {
+        let_next_begin();
+        after_previous();
+        for (int e = threadIdx.x; e < p.experts; e += kThreads)
+            if (cnt[e]) atomicAdd(&p.counts[w * p.experts + e], cnt[e]);
+        if (threadIdx.x == 0 && seen) atomicAdd(p.seen + 1 + w, seen);
+    }
 }
 
 template <typename T, int L, int V>
@@ -373,7 +400,8 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(const __grid_con
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = blockIdx.y, sub = lane & (L - 1);
     let_next_begin();
     after_previous();
-    const int64_t n = *p.seen;
+    int64_t n = 0;
+    for (int i = 0; i < p.P; ++i) n += p.seen[1 + i];
     if (threadIdx.x == 0) coef = loss_scale(p, n);
     int64_t choices = 0;
     for (int e = threadIdx.x; e < p.experts; e += kThreads) {
@@ -382,7 +410,7 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(const __grid_con
         all[e] = s;
         choices += s;
     }
-    choices = cta_count<kThreads>(choices, isum);
+    choices = cta_count(choices, isum);
     float c[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -405,7 +433,7 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(const __grid_con
         for (int i = 0; i < kWarps; ++i) s += dsum[i];
         p.partial[blockIdx.y * gridDim.x + blockIdx.x] = s;
         __threadfence();
-        last = atomicAdd(p.seen + 1, 1u) == blocks - 1;
+        last = atomicAdd(p.seen, 1u) == blocks - 1;
     }
     __syncthreads();
     if (last) {  // the sums of all CTAs, in their order
@@ -422,46 +450,64 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(const __grid_con
     }
 }
 
-// Few tokens: everything in one CTA, whose barriers cost less than launches.
+// Few tokens: everything in one cluster of up to 16 CTAs (one launch, and its
+// barriers, cost less than three launches).  The CTAs' counts and sums meet in
+// distributed shared memory; every CTA adds them in rank order.
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(kOneThreads) balance_one_kernel(const __grid_constant__ BalanceParams p) {
-    constexpr int kOneWarps = kOneThreads / 32;
+    constexpr int threads = kOneThreads, warps = threads / 32;
     __shared__ int32_t cnt[kOneCounts];
     __shared__ int32_t all[kMaxExperts];
-    __shared__ float dsum[kOneWarps];
-    __shared__ int64_t isum[kOneWarps];
+    __shared__ float dsum[kOneThreads / 32];
+    __shared__ int64_t isum[kOneThreads / 32];
     __shared__ float coef;
+    __shared__ int32_t seen;
+    __shared__ float total;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (L - 1);
-    for (int e = threadIdx.x; e < p.P * p.experts; e += kOneThreads) cnt[e] = 0;
+    const int C = gridDim.x, rank = blockIdx.x, P = p.P, E = p.experts;
+    for (int e = threadIdx.x; e < P * E; e += threads) cnt[e] = 0;
     __syncthreads();
     let_next_begin();
     after_previous();
     constexpr int kPerWarp = 32 / L;
-    const int chunks = static_cast<int>((p.tokens + kPerWarp - 1) / kPerWarp), items = chunks * p.P;
+    const int chunks = static_cast<int>((p.tokens + kPerWarp - 1) / kPerWarp), items = chunks * P;
     int64_t n = 0;
-    for (int i = warp; i < items; i += kOneWarps) {
+    for (int i = warp * C + rank; i < items; i += warps * C) {
         const int w = i / chunks;
-        n += choose<T, L, V>(p, w, static_cast<int64_t>(i - w * chunks) * kPerWarp + lane / L, sub, lane, cnt + w * p.experts, nullptr);
+        n += choose<T, L, V>(p, w, static_cast<int64_t>(i - w * chunks) * kPerWarp + lane / L, sub, lane, cnt + w * E, nullptr);
     }
-    n = cta_count<kOneThreads>(n, isum);
+    n = cta_count(n, isum);
+    if (C > 1) {
+        if (threadIdx.x == 0) seen = static_cast<int32_t>(n);
+        cluster_barrier();
+        n = 0;
+        for (int r = 0; r < C; ++r) n += cluster_load_int(cluster_map(smem_u32(&seen), r));
+    }
     if (threadIdx.x == 0) coef = loss_scale(p, n);
     int64_t choices = 0;
-    for (int e = threadIdx.x; e < p.experts; e += kOneThreads) {
+    for (int e = threadIdx.x; e < E; e += threads) {
         int32_t s = 0;
-        for (int i = 0; i < p.P; ++i) s += cnt[i * p.experts + e];
+        for (int i = 0; i < P; ++i) {
+            int32_t of_worker = cnt[i * E + e];
+            if (C > 1) {
+                of_worker = 0;
+                for (int r = 0; r < C; ++r) of_worker += cluster_load_int(cluster_map(smem_u32(cnt + i * E + e), r));
+            }
+            if (rank == 0) p.counts[i * E + e] = of_worker;
+            s += of_worker;
+        }
         all[e] = s;
         choices += s;
     }
-    for (int e = threadIdx.x; e < p.P * p.experts; e += kOneThreads) p.counts[e] = cnt[e];
-    choices = cta_count<kOneThreads>(choices, isum);
+    choices = cta_count(choices, isum);
     float c[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = expert<T, L>(sub, i);
-        c[i] = e < p.experts ? centred(all[e], choices, p.experts) : 0.0f;
+        c[i] = e < E ? centred(all[e], choices, E) : 0.0f;
     }
     float sum = 0.0f;
-    for (int i = warp; i < items; i += kOneWarps) {
+    for (int i = warp * C + rank; i < items; i += warps * C) {
         const int w = i / chunks;
         sum += gradient<T, L, V>(p, w, static_cast<int64_t>(i - w * chunks) * kPerWarp + lane / L, sub, c, coef);
     }
@@ -469,32 +515,91 @@ __global__ void __launch_bounds__(kOneThreads) balance_one_kernel(const __grid_c
     if (lane == 0) dsum[warp] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
-        float s = 0.0f;
-        for (int i = 0; i < kOneWarps; ++i) s += dsum[i];
-        *p.loss = loss_of(p, s, n, choices);
+        sum = 0.0f;
+        for (int i = 0; i < warps; ++i) sum += dsum[i];
+        total = sum;
     }
+    if (C > 1) {
+        __syncthreads();
+        cluster_barrier();
+        if (rank == 0 && threadIdx.x == 0) {
+            sum = 0.0f;
+            for (int r = 0; r < C; ++r) sum += cluster_load(cluster_map(smem_u32(&total), r));
+        }
+        cluster_barrier();  // no CTA leaves while another reads its shared memory
+    }
+    if (rank == 0 && threadIdx.x == 0) *p.loss = loss_of(p, sum, n, choices);
+}
+
+// Whether clusters of 16 CTAs of a kernel (above the portable size) can be had
+// on this device; known: a static array of the caller, 1: yes, 2: no, 0: not
+// looked up yet.
+template <typename Kernel>
+bool wide_clusters(Kernel kernel, unsigned threads, std::atomic<int> *known) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    int have = known[dev & 63].load(std::memory_order_relaxed);
+    if (have == 0) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(threads);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 16;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        const bool good = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                          cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0;
+        if (!good) cudaGetLastError();  // not an error of this call: clusters of eight do
+        have = good ? 1 : 2;
+        known[dev & 63].store(have, std::memory_order_relaxed);
+    }
+    return have == 1;
 }
 
 template <typename T, int L, int V>
 int launch(const BalanceParams &p, cudaStream_t stream) {
-    // One CTA up to four tokens a lane group: measured level with three launches at about eight.
-    if constexpr (V == 8)
-        if (p.tokens * p.P * L <= kOneThreads * 4 && p.P * p.experts <= kOneCounts) {
-            return launch_early("balance_one_kernel", balance_one_kernel<T, L, V>, dim3(1), kOneThreads, 0, 1, stream, p);
+    const unsigned P = static_cast<unsigned>(p.P);
+    bool together = false;
+    unsigned ctas = 1;
+    if constexpr (V == 8) {
+        // One launch of one cluster up to two passes of its 256 warps; two launches, of a cluster a worker, up to four
+        // passes of its 128 warps; else three over the whole device.  (8000 tokens of 60 experts, GPU time: 20, 14.5
+        // and 13.5 us; but a launch takes the host 3 us.)
+        const int64_t items = ceil_div(p.tokens, int64_t{32 / L});  // of a worker
+        if (items * p.P <= 16 * 16 * 2 && p.P * p.experts <= kOneCounts) {
+            const auto kernel = balance_one_kernel<T, L, V>;
+            static std::atomic<int> known[64];
+            while (ctas < 16 && items * p.P > static_cast<int64_t>(ctas) * 16 * 2) ctas *= 2;
+            if (ctas == 16 && !wide_clusters(kernel, kOneThreads, known)) ctas = 8;
+            return launch_early("balance_one_kernel", kernel, dim3(ctas), kOneThreads, 0, ctas, stream, p);
         }
-    const int n = p.P * p.experts;
-    const auto zero = launch_early("balance_zero_kernel", balance_zero_kernel, dim3(static_cast<unsigned>(ceil_div(n, kThreads))), kThreads, 0, 1,
-                                   stream, p.counts, n, p.seen);
-    if (zero) return zero;
+        if (items <= 16 * kWarps * 4) {
+            const auto kernel = balance_count_kernel<T, L, V, true>;
+            static std::atomic<int> known[64];
+            while (ctas < 16 && items > static_cast<int64_t>(ctas) * kWarps) ctas *= 2;
+            if (ctas == 16 && !wide_clusters(kernel, kThreads, known)) ctas = 8;
+            if (int rc = launch_early("balance_count_kernel", kernel, dim3(ctas, P), kThreads, 0, ctas, stream, p)) return rc;
+            together = true;
+        }
+    }
     // as many CTAs as the SMs hold (registers), for each begins with the totals of all counts
     const auto blocks = [&](int per_sm) {
         const int64_t work = ceil_div(p.tokens, int64_t{kWarps} * (32 / L));
         const int64_t most = std::min(ceil_div(static_cast<int64_t>(sm_count()) * per_sm, p.P), int64_t{kMaxBlocks} / p.P);
         return static_cast<unsigned>(std::max(std::min(work, most), int64_t{1}));
     };
-    const unsigned P = static_cast<unsigned>(p.P);
-    if (int rc = launch_early("balance_count_kernel", balance_count_kernel<T, L, V>, dim3(blocks(V == 32 ? 3 : 6), P), kThreads, 0, 1, stream, p))
-        return rc;
+    if (!together) {
+        const int n = p.P * p.experts;
+        if (int rc = launch_early("balance_zero_kernel", balance_zero_kernel, dim3(static_cast<unsigned>(ceil_div(std::max(n, p.P + 1), kThreads))),
+                                  kThreads, 0, 1, stream, p.counts, n, p.seen, p.P))
+            return rc;
+        if (int rc = launch_early("balance_count_kernel", balance_count_kernel<T, L, V, false>, dim3(blocks(V == 32 ? 3 : 6), P), kThreads, 0,
+                                  1, stream, p))
+            return rc;
+    }
     return launch_early("balance_grad_kernel", balance_grad_kernel<T, L, V>, dim3(blocks(V == 32 ? 2 : 4), P), kThreads, 0, 1, stream, p);
 }
 
@@ -525,7 +630,7 @@ bool wide_rows(const void *const *rows, int P, int64_t ld, int elem) {
 using namespace gar;
 
 extern "C" size_t gar_balance_workspace_bytes(int32_t P) {
-    return P < 1 || P > GAR_MAX_WORKERS ? 0 : static_cast<size_t>(kMaxBlocks) * 4 + 8;
+    return P < 1 || P > GAR_MAX_WORKERS ? 0 : static_cast<size_t>(kMaxBlocks) * 4 + (GAR_MAX_WORKERS + 1) * 4;
 }
 
 extern "C" int gar_balance_loss(const void *const *z, int32_t P, int64_t tokens, int32_t experts, int64_t ldz,

@@ -138,6 +138,55 @@ struct Patch<float> {
     }
 };
 
+// The codes of one tile, both orders.  kBad: the tile has NaN or infinities;
+// fma(y, 0, y f) is y f for finite y and NaN else, whose code is the format's NaN.
+template <typename T, bool kE5M2, bool kBad>
+__device__ __forceinline__ void emit(const QuantizeParams &p, const Patch<T> &v, const uint32_t (&rbyte)[8], const uint32_t (&cbyte)[8],
+                                     uint8_t *tile, int64_t tr, int64_t tc, int64_t row0, int64_t col0, int64_t left) {
+    const int tid = threadIdx.x, half = tid >> 4, hl = tid & 15;
+    const auto scaled = [&](int i, int j, float f) {
+        const float y = v.value(i, j);
+        return kBad ? __fmaf_rn(y, 0.0f, y * f) : y * f;
+    };
+    if (p.qt) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float f = inverse_scale(cbyte[j]);
+            uint2 w;
+            w.x = pack4<kE5M2>(scaled(0, j, f), scaled(1, j, f), scaled(2, j, f), scaled(3, j, f));
+            w.y = pack4<kE5M2>(scaled(4, j, f), scaled(5, j, f), scaled(6, j, f), scaled(7, j, f));
+            *reinterpret_cast<uint2 *>(&tile[(hl * 8 + j) * kTile + ((half ^ hl) << 3)]) = w;
+        }
+        const int64_t tiles_r = (p.rows + kTile - 1) / kTile;
+        if (half == 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < left) store_scale(p.scale_t, p.cols, col0 + j, tr, tiles_r, cbyte[j]);
+        }
+    }
+    if (p.q) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = row0 + i;
+            const float f = inverse_scale(rbyte[i]);
+            uint2 w;
+            w.x = pack4<kE5M2>(scaled(i, 0, f), scaled(i, 1, f), scaled(i, 2, f), scaled(i, 3, f));
+            w.y = pack4<kE5M2>(scaled(i, 4, f), scaled(i, 5, f), scaled(i, 6, f), scaled(i, 7, f));
+            if (r < p.rows) {
+                uint8_t *dst = p.q + r * p.ldq + col0;
+                if (left >= 8) {
+                    *reinterpret_cast<uint2 *>(dst) = w;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < left) dst[j] = static_cast<uint8_t>((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+                }
+                if (hl == 0) store_scale(p.scale, p.rows, r, tc, p.tiles_c, rbyte[i]);
+            }
+        }
+    }
+}
+
 // One CTA per 128 x 128 tile, x read once for both orders.  Each half-warp
 // owns 8 consecutive rows and each of its lanes 8 consecutive columns, so a
 // row's maximum is a shuffle over 16 lanes, a column's is a maximum over the
@@ -212,49 +261,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) quantize_ker
             for (int j = 0; j < 8; ++j) cbyte[j] = scale_byte(colmax[0][hl * 8 + j], p.emax);
         }
     }
-    // the value times a power of two; a NaN or (times zero) an infinity becomes the code NaN
-    const auto scaled = [&](int i, int j, float f) {
-        const float y = v.value(i, j);
-        return bad ? __fmaf_rn(y, 0.0f, y * f) : y * f;
-    };
-
-    if (p.qt) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float f = inverse_scale(cbyte[j]);
-            uint2 w;
-            w.x = pack4<kE5M2>(scaled(0, j, f), scaled(1, j, f), scaled(2, j, f), scaled(3, j, f));
-            w.y = pack4<kE5M2>(scaled(4, j, f), scaled(5, j, f), scaled(6, j, f), scaled(7, j, f));
-            *reinterpret_cast<uint2 *>(&tile[(hl * 8 + j) * kTile + ((half ^ hl) << 3)]) = w;
-        }
-        const int64_t tiles_r = (p.rows + kTile - 1) / kTile;
-        if (half == 0) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < left) store_scale(p.scale_t, p.cols, col0 + j, tr, tiles_r, cbyte[j]);
-        }
-    }
-    if (p.q) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t r = row0 + i;
-            const float f = inverse_scale(rbyte[i]);
-            uint2 w;
-            w.x = pack4<kE5M2>(scaled(i, 0, f), scaled(i, 1, f), scaled(i, 2, f), scaled(i, 3, f));
-            w.y = pack4<kE5M2>(scaled(i, 4, f), scaled(i, 5, f), scaled(i, 6, f), scaled(i, 7, f));
-            if (r < p.rows) {
-                uint8_t *dst = p.q + r * p.ldq + col0;
-                if (left >= 8) {
-                    *reinterpret_cast<uint2 *>(dst) = w;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < left) dst[j] = static_cast<uint8_t>((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
-                }
-                if (hl == 0) store_scale(p.scale, p.rows, r, tc, p.tiles_c, rbyte[i]);
-            }
-        }
-    }
+    if (bad)
+        emit<T, kE5M2, true>(p, v, rbyte, cbyte, tile, tr, tc, row0, col0, left);
+    else
+        emit<T, kE5M2, false>(p, v, rbyte, cbyte, tile, tr, tc, row0, col0, left);
     if (p.qt) {
         __syncthreads();
         const int part = tid & 7;  // 16 bytes of a column: row groups 2 part and 2 part + 1

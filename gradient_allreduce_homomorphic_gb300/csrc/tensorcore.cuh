@@ -238,4 +238,10 @@ __device__ __forceinline__ float cluster_load(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ int cluster_load_int(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 }  // namespace gar
