@@ -157,7 +157,7 @@ __device__ __forceinline__ void choose_by_rounds(float (&v)[V], int sub, int lan
     }
 }
 
-// The same in fewer instructions where a token takes eight lanes or more: the
+// The same in fewer instructions where a token takes four lanes or more: the
 // k-th largest of its 4 L maxima of 8 values bounds the k-th largest value from
 // below, so the few values that reach it (k and a half in the mean, for k = 8
 // of 256) hold the choices; they are listed in shared memory and each is
@@ -213,13 +213,23 @@ __device__ __forceinline__ bool choose_by_bound(const float (&v)[32], const T *z
     }
     __syncwarp();
     if (good) {
-        for (int own = sub; own < total; own += L) {
-            const uint64_t mine = list[own];
-            int rank = 0;
-            for (int j = 0; j < total; ++j) rank += list[j] > mine;
-            if (rank < k) {
-                const int e = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(mine));
-                out[rank] = e;
+        for (int own = sub; own < total; own += 2 * L) {  // two of the list at a time in each lane
+            const bool second = own + L < total;
+            const uint64_t a = list[own], b = list[second ? own + L : own];
+            int rank_a = 0, rank_b = 0;
+            for (int j = 0; j < total; ++j) {
+                const uint64_t x = list[j];
+                rank_a += x > a;
+                rank_b += x > b;
+            }
+            if (rank_a < k) {
+                const uint32_t e = 0xFFFFFFFFu - static_cast<uint32_t>(a);
+                out[rank_a] = static_cast<int32_t>(e);
+                atomicAdd(cnt + e, 1);
+            }
+            if (second && rank_b < k) {
+                const uint32_t e = 0xFFFFFFFFu - static_cast<uint32_t>(b);
+                out[rank_b] = static_cast<int32_t>(e);
                 atomicAdd(cnt + e, 1);
             }
         }
@@ -243,11 +253,11 @@ __device__ __forceinline__ bool choose(const BalanceParams &p, int w, int64_t t,
         for (int i = 0; i < V; ++i) v[i] = -INFINITY;
         for (int c = sub; here && c < p.k; c += L) out[c] = -1;
     }
-    bool some = false;
+    float m = v[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) some |= v[i] > -INFINITY;
-    some = (__ballot_sync(0xFFFFFFFFu, some) & group_mask<L>(lane)) != 0;
-    if constexpr (L >= 8 && V == 32) {
+    for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
+    const bool some = (__ballot_sync(0xFFFFFFFFu, m > -INFINITY) & group_mask<L>(lane)) != 0;
+    if constexpr (L >= 4 && V == 32) {
         bool good = !live;
         if (p.k > 2) good |= choose_by_bound<T, L>(v, z, sub, lane, p.k, live, out, cnt, list);
         if (__any_sync(0xFFFFFFFFu, !good)) {
@@ -293,10 +303,14 @@ __device__ __forceinline__ float gradient(const BalanceParams &p, int w, int64_t
     s = group_sum<L>(s);
     d = group_sum<L>(d);
     d = live ? d / s : 0.0f;
-    const float f = live ? coef / s : 0.0f;
+    const float f = live ? coef / s : 0.0f, fd = f * d;
     if (here && p.has_grad) {
+        if (!live) {  // powers of nothing, or of NaN alone
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = live ? f * v[i] * (c[i] - d) : 0.0f;
+            for (int i = 0; i < V; ++i) v[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] *= fmaf(f, c[i], -fd);
         store_token<T, L, V>(static_cast<T *>(p.dz[w]) + t * p.lddz, sub, p.experts, p.dwide, v);
     }
     return sub == 0 ? d : 0.0f;
@@ -348,7 +362,7 @@ __global__ void __launch_bounds__(kThreads) balance_zero_kernel(int32_t *counts,
 template <typename T, int L, int V, bool kTogether>
 __global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_constant__ BalanceParams p) {
     __shared__ int32_t cnt[kMaxExperts];
-    __shared__ uint64_t list[L >= 8 && V == 32 ? kWarps : 1][32 / L * kList];
+    __shared__ uint64_t list[L >= 4 && V == 32 ? kWarps : 1][32 / L * kList];
     __shared__ uint32_t seen;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = blockIdx.y, sub = lane & (L - 1);
     for (int e = threadIdx.x; e < p.experts; e += kThreads) cnt[e] = 0;
@@ -362,7 +376,7 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_co
     uint32_t mine = 0;
     for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kPerWarp; t0 < p.tokens;
          t0 += static_cast<int64_t>(gridDim.x) * kWarps * kPerWarp)
-        mine += choose<T, L, V>(p, w, t0 + lane / L, sub, lane, cnt, list[L >= 8 && V == 32 ? warp : 0]);
+        mine += choose<T, L, V>(p, w, t0 + lane / L, sub, lane, cnt, list[L >= 4 && V == 32 ? warp : 0]);
     mine = __reduce_add_sync(0xFFFFFFFFu, mine);
     if (lane == 0 && mine) atomicAdd(&seen, mine);
     __syncthreads();
