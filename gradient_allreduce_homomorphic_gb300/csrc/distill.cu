@@ -30,6 +30,9 @@ namespace {
 constexpr int kMaxTop = 1024;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
+// bf16 rows with |m c| up to this take (z - m) c as one fma of z, c and the rounded m c, which adds 2^-16 to an exponent
+// at most (2^-17 from rounding m c, as much from rounding the fma): a fraction 1.1e-5 of a probability.
+constexpr float kPlain = 256.0f;
 
 struct DistillParams {
     const void *z;
@@ -208,25 +211,30 @@ __global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_c
 
 // ----------------------------------------------------------------- long rows
 // A cluster of K CTAs takes a row at a time, each CTA a K-th of its 16-byte
-// vectors.  Sixteen warps pass over the present row in shared memory: once for
-// the maximum and the sum of powers, exchanged between the CTAs as one pair
-// each, once for the gradient.  Behind them one warp copies the CTA's part of
-// the coming rows to shared memory (bulk copies, two or more stages), and
-// kPrepare warps take turns preparing the coming rows' teacher entries (slots),
-// a chain of dependent loads and reductions of some microseconds a row.  The
-// elements before a row's first 16-byte boundary and after its last one (a
-// vocabulary of odd size) are taken from global memory by the cluster's first
-// CTA.
-//
-// With more than one CTA a row (kLag) the gradient pass runs a row behind the
-// first pass, so that a pair that comes late, for its CTA's copy took longer,
-// holds no one up.  The elements of dz at the entries are written over the
-// softmax's once a barrier has followed that row's gradient pass; the barrier
-// is the one in the next row's reduction.
-constexpr int kMain = 512, kMainWarps = kMain / 32, kPrepare = 3;
-constexpr int kStreamThreads = kMain + 32 + 32 * kPrepare;
+// vectors, in shared memory, as a pipeline of warps:
+//   one warp copies the CTA's part of the coming rows there (bulk copies, up to
+//   eight stages);
+//   kPrepare warps take turns preparing the coming rows' teacher entries
+//   (slots), a chain of dependent loads and reductions of microseconds a row;
+//   the first group passes over a row for the maximum and the sum of powers,
+//   which its CTAs send one another as one pair each;
+//   the second group, a row or more behind, takes the pairs and passes over the
+//   row again for the gradient, then writes dz at the entries.
+// So copies, reductions and exchanges of some rows hide behind the passes over
+// others.  The elements before a row's first 16-byte boundary and after its last
+// one (a vocabulary of odd size) are the cluster's first CTA's; they come with the
+// teacher entries.  The loss alone leaves the second group one warp; the gradient
+// alone, from a saved lse, needs no first group and no cluster.
+enum { kFused, kLossOnly, kGradOnly };
+constexpr int first_warps(int mode) { return mode == kGradOnly ? 0 : 8; }  // as many with the gradient as without: the same loss
+constexpr int second_warps(int mode) { return mode == kFused ? 8 : mode == kLossOnly ? 1 : 16; }
+constexpr int kPrepare = 3;
+constexpr int stream_threads(int mode) { return 32 * (first_warps(mode) + second_warps(mode) + 1 + kPrepare); }
 constexpr int kMaxStages = 8, kMaxSlots = 8, kMaxCluster = 8;
-constexpr int kMeets = 4;  // exchanges that may be under way: this row's, the last one's, and two a faster CTA may be at
+// Exchanges under way.  A CTA's first group is at most kMaxStages rows ahead of its second; to send row i + n it has
+// seen its second group finish row i + n - kMaxStages, for which every CTA's first group sent that row and its second
+// group finished one kMaxStages before: the pair of row i has been read if n = 2 kMaxStages.
+constexpr int kMeets = 2 * kMaxStages;
 
 // A slot's row.  The slot's entries follow it in dynamic shared memory: their
 // indices (-1: absent), probabilities, and the student's logits at those that
@@ -235,6 +243,7 @@ struct Header {
     float weight, cross;  // cross: sum of p_j (log p_j - (z_j - zref) / tau)
     float zref;
     int32_t live, repeated;
+    float edge[16];  // the first CTA's logits outside the vectors (up to 14), in order
 };
 
 template <typename T>
@@ -245,7 +254,7 @@ struct Row {  // one row's split into head, vectors and tail
         const int32_t off = static_cast<int32_t>((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / static_cast<int32_t>(sizeof(T));
         head = off < vocab ? off : vocab;
         vectors = (vocab - head) / n;
-        v0 = (vectors * rank) >> log_cluster;  // below 2^31: there are fewer than 2^28 vectors, and 8 ranks
+        v0 = (vectors * rank) >> log_cluster;  // a row that is taken this way has fewer than 2^16 vectors
         v1 = (vectors * (rank + 1)) >> log_cluster;
     }
     // Element of the i-th place outside the vectors, which are the first CTA's; -1 past the last.
@@ -260,6 +269,14 @@ struct Row {  // one row's split into head, vectors and tail
         return v >= v0 * n && v < v1 * n;
     }
 };
+
+// `bytes` (a multiple of 16) to shared memory, counted on the mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    if (bytes > 0)
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                     "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+                     : "memory");
+}
 
 template <typename T>
 __device__ __forceinline__ void unpack(const uint4 &g, float (&x)[16 / sizeof(T)]) {
@@ -279,15 +296,41 @@ __device__ __forceinline__ uint4 pack(const float (&x)[16 / sizeof(T)]) {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
 }
 
-__device__ __forceinline__ void bar_main() { asm volatile("bar.sync 1, %0;" ::"n"(kMain) : "memory"); }
+template <int n>
+__device__ __forceinline__ float tree_max(const float (&x)[n]) {
+    float m[n / 2];
+#pragma unroll
+    for (int j = 0; j < n / 2; ++j) m[j] = fmaxf(x[j], x[j + n / 2]);
+    if constexpr (n == 2)
+        return m[0];
+    else
+        return tree_max(m);
+}
+template <int n>
+__device__ __forceinline__ float tree_sum(const float (&x)[n]) {
+    float m[n / 2];
+#pragma unroll
+    for (int j = 0; j < n / 2; ++j) m[j] = x[j] + x[j + n / 2];
+    if constexpr (n == 2)
+        return m[0];
+    else
+        return tree_sum(m);
+}
 
-template <typename T, bool kSaved, bool kLag>
-__global__ void __launch_bounds__(kStreamThreads, kLag ? 1 : 2) distill_stream_kernel(const __grid_constant__ DistillParams p) {
+template <int kThreads>
+__device__ __forceinline__ void bar_group(int id) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
+}
+
+template <typename T, int kMode>
+__global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kernel(const __grid_constant__ DistillParams p) {
     constexpr int n = 16 / sizeof(T);
+    constexpr bool kSaved = kMode == kGradOnly;
+    constexpr int kFirst = first_warps(kMode), kSecond = second_warps(kMode), kMainWarps = kFirst + kSecond;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kMaxSlots + kMeets];
     __shared__ Header header[kMaxSlots];
-    __shared__ MaxSum partial[2][kMainWarps];
+    __shared__ MaxSum partial[2][16];
     __shared__ __align__(8) MaxSum pairs[kMeets][kMaxCluster];
     __shared__ int failed;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -302,7 +345,7 @@ __global__ void __launch_bounds__(kStreamThreads, kLag ? 1 : 2) distill_stream_k
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, kMainWarps);
+            mbar_init(empty + 8 * i, kMode == kLossOnly ? kFirst : kMainWarps);
         }
         for (int i = 0; i < kMaxSlots; ++i) {
             mbar_init(slot_full + 8 * i, 1);
@@ -313,7 +356,8 @@ __global__ void __launch_bounds__(kStreamThreads, kLag ? 1 : 2) distill_stream_k
         mbar_init_fence();
     }
     __syncthreads();
-    if (kLag) cluster_barrier();
+    const bool exchange = !kSaved && K > 1;
+    if (exchange) cluster_barrier();
     let_next_begin();
     after_previous();
 
@@ -327,12 +371,7 @@ __global__ void __launch_bounds__(kStreamThreads, kLag ? 1 : 2) distill_stream_k
                 const uint32_t bytes = static_cast<uint32_t>((part.v1 - part.v0) * 16);
                 if (!(ok = mbar_wait(empty + 8 * s, turn, &failed))) break;
                 mbar_expect_tx(full + 8 * s, bytes);
-                if (bytes > 0)
-                    asm volatile(
-                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                            smem_u32(smem + s * p.stage_bytes)),
-                        "l"(__cvta_generic_to_global(z + part.head + part.v0 * n)), "r"(bytes), "r"(full + 8 * s)
-                        : "memory");
+                bulk_load(smem_u32(smem + s * p.stage_bytes), z + part.head + part.v0 * n, bytes, full + 8 * s);
                 issued = issued < S ? issued + 1 : S;
                 if (++s == S) s = 0, turn ^= 1;
             }
@@ -358,6 +397,8 @@ __global__ void __launch_bounds__(kStreamThreads, kLag ? 1 : 2) distill_stream_k
             int32_t *top_i = reinterpret_cast<int32_t *>(slots + e * 12 * entries);
             float *top_p = reinterpret_cast<float *>(top_i + entries), *top_z = top_p + entries;
             const float w = p.weight ? p.weight[row] : 1.0f;
+            const int odd = lane < 16 ? part.edge(lane, p.vocab, rank) : -1;
+            const float z_odd = odd >= 0 ? load_f32(z + odd) : 0.0f;
             float tmax = -INFINITY, tsum = 0.0f, zref = -INFINITY;
             constexpr int kAtOnce = 4;  // entries of a lane whose loads are in flight together
             for (int j0 = lane; j0 < p.k; j0 += 32 * kAtOnce) {
@@ -419,194 +460,191 @@ __global__ void __launch_bounds__(kStreamThreads, kLag ? 1 : 2) distill_stream_k
                 cross = warp_sum(cross);
                 twice = __any_sync(0xFFFFFFFFu, twice);
             }
-            if (lane == 0) header[e] = {w, cross, zref, live, twice};
+            Header &h = header[e];
+            if (lane < 16) h.edge[lane] = z_odd;
+            if (lane == 0) h.weight = w, h.cross = cross, h.zref = zref, h.live = live, h.repeated = twice;
             __syncwarp();
             if (lane == 0) mbar_arrive(slot_full + 8 * e);
             for (int i = 0; i < kPrepare; ++i)
                 if (++e == E) e = 0, turn ^= 1;
         }
-    } else {
+    } else if (warp < kFirst) {
         const float c = kLog2e * p.inv_tau;
-        struct Place {
-            int64_t row;  // -1: none
-            uint32_t s, e, meet;
-        };
-        struct Done {
-            int64_t row;
-            uint32_t e;
-            float ref, sub, g;
-        };
-
-        // The row's maximum and sum over this CTA's part, the same in every thread.
-        const auto reduce_part = [&](const Place &at) {
-            const T *z = static_cast<const T *>(p.z) + at.row * p.ldz;
-            const Row<T> part(z, p.vocab, rank, p.log_cluster);
-            const uint4 *v = reinterpret_cast<const uint4 *>(smem + at.s * p.stage_bytes);
-            const int count = part.v1 - part.v0;
-            MaxSum a{-INFINITY, 0.0f};
-            const int odd = part.edge(threadIdx.x, p.vocab, rank);
-            if (odd >= 0) a.m = load_f32(z + odd), a.s = pow2((a.m - finite_or_0(a.m)) * c);
-#pragma unroll 2
-            for (int i = threadIdx.x; i < count; i += kMain) {
-                float x[n];
-                unpack<T>(v[i], x);
-                float m = a.m;
-#pragma unroll
-                for (int j = 0; j < n; ++j) m = fmaxf(m, x[j]);
-                const float r = finite_or_0(m);
-                float t = 0.0f;
-#pragma unroll
-                for (int j = 0; j < n; ++j) t += pow2((x[j] - r) * c);
-                a.s = fmaf(a.s, pow2((a.m - r) * c), t);
-                a.m = m;
-            }
-            return merge_lanes<32>(a, c);
-        };
-
-        // Loss, lse and the gradient's softmax over this CTA's part.
-        const auto finish = [&](const Place &at, MaxSum a) {
-            Done r{at.row, at.e, 0.0f, 0.0f, 0.0f};
-            const T *z = static_cast<const T *>(p.z) + at.row * p.ldz;
-            T *dz = p.dz ? static_cast<T *>(p.dz) + at.row * p.lddz : nullptr;
-            const Row<T> part(z, p.vocab, rank, p.log_cluster);
-            const Header &h = header[at.e];
-            if (h.live) {
-                bool none;
-                if (kSaved) {
-                    r.sub = p.lse_in[at.row];
-                    none = r.sub == -INFINITY;
-                } else {
-                    if (kLag) {
-                        const uint32_t meet = at.meet % kMeets;
-                        mbar_wait(met + 8 * meet, (at.meet / kMeets) & 1, &failed);
-                        a = pairs[meet][0];
-                        for (uint32_t i = 1; i < K; ++i) a = merge(a, pairs[meet][i], c);
-                    }
-                    none = a.m == -INFINITY && a.s == 0.0f;
-                    r.ref = finite_or_0(a.m), r.sub = log2f(a.s);
-                    if (rank == 0 && threadIdx.x == 0) {
-                        p.loss[at.row] = none ? INFINITY : h.cross + (r.ref - h.zref) * p.inv_tau + r.sub * kLn2;
-                        p.lse[at.row] = none ? -INFINITY : r.ref * p.inv_tau + r.sub * kLn2;
-                    }
-                }
-                if (none)
-                    r.ref = r.sub = 0.0f;  // probabilities 0 by g = 0
-                else
-                    r.g = h.weight * p.inv_tau;
-            } else if (!kSaved && rank == 0 && threadIdx.x == 0) {
-                p.loss[at.row] = 0.0f, p.lse[at.row] = 0.0f;
-            }
-            if (!dz) return r;
-            const Softmax<kSaved> q{r.ref, r.sub, kSaved ? p.inv_tau : c};
-            const uint4 *v = reinterpret_cast<const uint4 *>(smem + at.s * p.stage_bytes);
-            T *out = dz + part.head + part.v0 * n;
-            const int count = part.v1 - part.v0;
-            const bool wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-            const bool zero = r.g == 0.0f;  // whatever z holds
-            const int odd = part.edge(threadIdx.x, p.vocab, rank);
-            if (odd >= 0) store_f32(dz + odd, zero ? 0.0f : r.g * q(load_f32(z + odd)));
-#pragma unroll 2
-            for (int i = threadIdx.x; i < count; i += kMain) {
-                float x[n];
-                unpack<T>(v[i], x);
-#pragma unroll
-                for (int j = 0; j < n; ++j) x[j] = zero ? 0.0f : r.g * q(x[j]);
-                if (wide) {
-                    st16(out + i * n, pack<T>(x));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < n; ++j) store_f32(out + i * n + j, x[j]);
-                }
-            }
-            return r;
-        };
-
-        // dz at the entries that this CTA's part holds; then the slot is free.
-        const auto entries_of = [&](const Done &r) {
-            const Header &h = header[r.e];
-            if (p.dz && h.live) {
-                const T *z = static_cast<const T *>(p.z) + r.row * p.ldz;
-                T *dz = static_cast<T *>(p.dz) + r.row * p.lddz;
-                const Row<T> part(z, p.vocab, rank, p.log_cluster);
-                const Softmax<kSaved> q{r.ref, r.sub, kSaved ? p.inv_tau : c};
-                const int32_t *top_i = reinterpret_cast<const int32_t *>(slots + r.e * 12 * entries);
-                const float *top_p = reinterpret_cast<const float *>(top_i + entries), *top_z = top_p + entries;
-                for (int j = threadIdx.x; j < p.k; j += kMain) {
-                    const int32_t i = top_i[j];
-                    if (i < 0 || !part.holds(i, rank)) continue;
-                    float sum = top_p[j];
-                    if (h.repeated) {
-                        sum = 0.0f;
-                        bool earlier = false;
-                        for (int o = 0; o < p.k; ++o)
-                            if (top_i[o] == i) {
-                                earlier |= o < j;
-                                sum += top_p[o];
-                            }
-                        if (earlier) continue;
-                    }
-                    const float first = r.g == 0.0f ? 0.0f : r.g * q(top_z[j]);
-                    store_f32(dz + i, fmaf(-(h.weight * p.inv_tau), sum, first));
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(slot_empty + 8 * r.e);
-        };
-
-        uint32_t s = 0, turn = 0, e = 0, eturn = 0, meet = 0, buf = 0;
-        Place last{-1, 0, 0, 0};
-        Done done{-1, 0, 0.0f, 0.0f, 0.0f};
-        const auto finish_and_release = [&](const Place &at, MaxSum a) {
-            done = finish(at, a);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + 8 * at.s);
-        };
+        constexpr int kThreads = 32 * (kFirst > 0 ? kFirst : 1);
+        uint32_t s = 0, turn = 0, e = 0, eturn = 0, meet = 0;
         for (int64_t row = first; row < p.rows; row += step) {
-            const Place at{row, s, e, meet};
+            const T *z = static_cast<const T *>(p.z) + row * p.ldz;
+            const Row<T> part(z, p.vocab, rank, p.log_cluster);
+            const uint4 *v = reinterpret_cast<const uint4 *>(smem + s * p.stage_bytes);
+            const int count = part.v1 - part.v0, odd = part.edge(threadIdx.x, p.vocab, rank);
             mbar_wait(slot_full + 8 * e, eturn, &failed);
+            const bool live = header[e].live;
             mbar_wait(full + 8 * s, turn, &failed);
-            const bool pass = !kSaved && header[e].live;
             MaxSum a{-INFINITY, 0.0f};
-            if (pass) {
-                a = reduce_part(at);
-                if (lane == 0) partial[buf][warp] = a;
+            if (live) {
+                if (odd >= 0) a.m = header[e].edge[threadIdx.x], a.s = pow2((a.m - finite_or_0(a.m)) * c);
+                // two vectors at a time: a thread's maximum, powers and sum are chains of dependent instructions
+                for (int i = threadIdx.x; i < count; i += 2 * kThreads) {
+                    float x[2][n];
+                    unpack<T>(v[i], x[0]);
+                    unpack<T>(v[i + kThreads < count ? i + kThreads : i], x[1]);
+                    const float kept = i + kThreads < count ? 1.0f : 0.0f;  // of the second one's powers
+                    const float m = fmaxf(a.m, fmaxf(tree_max(x[0]), tree_max(x[1]))), r = finite_or_0(m);
+                    if (m > a.m) {  // a new maximum: seldom, after the first values
+                        a.s *= pow2((a.m - r) * c);
+                        a.m = m;
+                    }
+                    if (sizeof(T) == 2 && fabsf(r * c) <= kPlain) {
+                        const float rc = r * c;
+#pragma unroll
+                        for (int j = 0; j < n; ++j) x[0][j] = pow2(fmaf(x[0][j], c, -rc)), x[1][j] = pow2(fmaf(x[1][j], c, -rc));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < n; ++j) x[0][j] = pow2((x[0][j] - r) * c), x[1][j] = pow2((x[1][j] - r) * c);
+                    }
+                    a.s += fmaf(kept, tree_sum(x[1]), tree_sum(x[0]));
+                }
             }
-            bar_main();
-            if (pass) {
-                a = merge_lanes<kMainWarps>(partial[buf][lane & (kMainWarps - 1)], c);
-                if (kLag) {
-                    const uint32_t bar = met + 8 * (meet % kMeets);
-                    if (threadIdx.x == 0) mbar_expect_tx(bar, 8 * K);
-                    if (threadIdx.x < K)
-                        asm volatile(
-                            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
-                                cluster_map(smem_u32(&pairs[meet % kMeets][rank]), threadIdx.x)),
-                            "f"(a.m), "f"(a.s), "r"(cluster_map(bar, threadIdx.x))
-                            : "memory");
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(empty + 8 * s);
+                mbar_arrive(slot_empty + 8 * e);
+            }
+            if (live) {
+                a = merge_lanes<32>(a, c);
+                if (lane == 0) partial[meet & 1][warp] = a;
+                bar_group<kThreads>(1);
+                if (warp == 0) {
+                    const uint32_t at = meet % kMeets, bar = met + 8 * at;
+                    a = merge_lanes<(kFirst > 0 ? kFirst : 1)>(partial[meet & 1][lane & (kFirst > 0 ? kFirst - 1 : 0)], c);
+                    if (K == 1) {
+                        if (lane == 0) {
+                            pairs[at][0] = a;
+                            mbar_arrive(bar);
+                        }
+                    } else {
+                        if (lane == 0) mbar_expect_tx(bar, 8 * K);
+                        __syncwarp();
+                        if (lane < static_cast<int>(K))
+                            asm volatile(
+                                "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                                    cluster_map(smem_u32(&pairs[at][rank]), lane)),
+                                "f"(a.m), "f"(a.s), "r"(cluster_map(bar, lane))
+                                : "memory");
+                    }
                 }
                 ++meet;
-            }
-            buf ^= 1;
-            if (done.row >= 0) entries_of(done);
-            if (kLag) {
-                if (last.row >= 0) finish_and_release(last, a);
-                last = at;
-            } else {
-                finish_and_release(at, a);
             }
             if (++s == S) s = 0, turn ^= 1;
             if (++e == E) e = 0, eturn ^= 1;
         }
-        if (kLag && last.row >= 0) {
-            bar_main();
-            if (done.row >= 0) entries_of(done);
-            finish_and_release(last, {});
+    } else {
+        const float c = kLog2e * p.inv_tau;
+        constexpr int kThreads = 32 * kSecond;
+        const int tid = threadIdx.x - 32 * kFirst;
+        uint32_t s = 0, turn = 0, e = 0, eturn = 0, meet = 0;
+        for (int64_t row = first; row < p.rows; row += step) {
+            const T *z = static_cast<const T *>(p.z) + row * p.ldz;
+            T *dz = kMode == kLossOnly ? nullptr : static_cast<T *>(p.dz) + row * p.lddz;
+            const Row<T> part(z, p.vocab, rank, p.log_cluster);
+            mbar_wait(slot_full + 8 * e, eturn, &failed);
+            const Header &h = header[e];
+            if (kMode != kLossOnly) mbar_wait(full + 8 * s, turn, &failed);
+            Softmax<kSaved> q{0.0f, 0.0f, kSaved ? p.inv_tau : c};
+            float g = 0.0f;
+            if (h.live) {
+                bool none;
+                if (kSaved) {
+                    q.sub = p.lse_in[row];
+                    none = q.sub == -INFINITY;
+                } else {
+                    const uint32_t at = meet % kMeets;
+                    mbar_wait(met + 8 * at, (meet / kMeets) & 1, &failed);
+                    ++meet;
+                    MaxSum a = pairs[at][0];
+                    for (uint32_t i = 1; i < K; ++i) a = merge(a, pairs[at][i], c);
+                    none = a.m == -INFINITY && a.s == 0.0f;
+                    q.ref = finite_or_0(a.m), q.sub = log2f(a.s);
+                    if (rank == 0 && tid == 0) {
+                        p.loss[row] = none ? INFINITY : h.cross + (q.ref - h.zref) * p.inv_tau + q.sub * kLn2;
+                        p.lse[row] = none ? -INFINITY : q.ref * p.inv_tau + q.sub * kLn2;
+                    }
+                }
+                if (none)
+                    q.ref = q.sub = 0.0f;  // probabilities 0 by g = 0
+                else
+                    g = h.weight * p.inv_tau;
+            } else if (!kSaved && rank == 0 && tid == 0) {
+                p.loss[row] = 0.0f, p.lse[row] = 0.0f;
+            }
+            if (kMode != kLossOnly) {
+                const uint4 *v = reinterpret_cast<const uint4 *>(smem + s * p.stage_bytes);
+                T *out = dz + part.head + part.v0 * n;
+                const int count = part.v1 - part.v0, odd = part.edge(tid, p.vocab, rank);
+                const bool wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+                const bool zero = g == 0.0f;  // whatever z holds
+                if (odd >= 0) store_f32(dz + odd, zero ? 0.0f : g * q(h.edge[tid]));
+                if (wide && zero) {
+                    for (int i = tid; i < count; i += kThreads) st16(out + i * n, make_uint4(0, 0, 0, 0));
+                } else if (sizeof(T) == 2 && !kSaved && wide && g > 0.0f && fabsf(q.ref * c) <= kPlain) {
+                    const float sub = fmaf(q.ref, c, q.sub) - log2f(g);  // g too goes into the exponent
+#pragma unroll 4
+                    for (int i = tid; i < count; i += kThreads) {
+                        float x[n];
+                        unpack<T>(v[i], x);
+#pragma unroll
+                        for (int j = 0; j < n; ++j) x[j] = pow2(fmaf(x[j], c, -sub));
+                        st16(out + i * n, pack<T>(x));
+                    }
+                } else if (wide) {
+#pragma unroll 4
+                    for (int i = tid; i < count; i += kThreads) {
+                        float x[n];
+                        unpack<T>(v[i], x);
+#pragma unroll
+                        for (int j = 0; j < n; ++j) x[j] = g * q(x[j]);
+                        st16(out + i * n, pack<T>(x));
+                    }
+                } else {
+                    for (int i = tid; i < count; i += kThreads) {
+                        float x[n];
+                        unpack<T>(v[i], x);
+#pragma unroll
+                        for (int j = 0; j < n; ++j) store_f32(out + i * n + j, zero ? 0.0f : g * q(x[j]));
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + 8 * s);
+                if (h.live) {  // dz at the entries that this CTA's part holds, over what the pass stored there
+                    bar_group<kThreads>(2);
+                    const int32_t *top_i = reinterpret_cast<const int32_t *>(slots + e * 12 * entries);
+                    const float *top_p = reinterpret_cast<const float *>(top_i + entries), *top_z = top_p + entries;
+                    for (int j = tid; j < p.k; j += kThreads) {
+                        const int32_t i = top_i[j];
+                        if (i < 0 || !part.holds(i, rank)) continue;
+                        float sum = top_p[j];
+                        if (h.repeated) {
+                            sum = 0.0f;
+                            bool earlier = false;
+                            for (int o = 0; o < p.k; ++o)
+                                if (top_i[o] == i) {
+                                    earlier |= o < j;
+                                    sum += top_p[o];
+                                }
+                            if (earlier) continue;
+                        }
+                        store_f32(dz + i, fmaf(-(h.weight * p.inv_tau), sum, zero ? 0.0f : g * q(top_z[j])));
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(slot_empty + 8 * e);
+            if (++s == S) s = 0, turn ^= 1;
+            if (++e == E) e = 0, eturn ^= 1;
         }
-        bar_main();
-        if (done.row >= 0) entries_of(done);
     }
     __syncthreads();
-    if (kLag) cluster_barrier();  // no CTA leaves while another may write its pair
+    if (exchange) cluster_barrier();  // no CTA leaves while another may write its pair
     if (threadIdx.x == 0 && failed && p.status) atomicOr(p.status, static_cast<unsigned int>(GAR_STATUS_TIMEOUT));
 }
 
@@ -629,24 +667,24 @@ int check(const void *z, int32_t dtype, int64_t rows, int64_t vocab, int64_t ldz
 constexpr int64_t kStreamBytes = 16384;
 constexpr int kSharedBytes = 220 * 1024;  // of a CTA that has the SM to itself, static shared memory taken off
 
-template <typename T, bool kSaved, bool kLag>
+template <typename T, int kMode>
 int launch_stream(const DistillParams &p, int64_t rows_at_once, size_t shared, cudaStream_t stream) {
-    const auto kernel = distill_stream_kernel<T, kSaved, kLag>;
+    const auto kernel = distill_stream_kernel<T, kMode>;
     // Clusters of 1 << i CTAs that the device holds at one time (its SMs come in groups, so it is fewer than its SMs
     // would make; one more would run after all others), 0: not looked up yet.
     static std::atomic<int> resident[64][4];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(GAR_ECUDA, "no current device");
-    const unsigned cluster = kLag ? 1u << p.log_cluster : 1u;
+    const unsigned cluster = kMode == kGradOnly ? 1u : 1u << p.log_cluster;
     std::atomic<int> &known = resident[dev & 63][p.log_cluster];
     int clusters = known.load(std::memory_order_relaxed);
     if (clusters == 0) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
         clusters = 1;
-        if (e == cudaSuccess && kLag) {
+        if (e == cudaSuccess && cluster > 1) {
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(cluster);
-            cfg.blockDim = dim3(kStreamThreads);
+            cfg.blockDim = dim3(stream_threads(kMode));
             cfg.dynamicSmemBytes = kSharedBytes;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -659,52 +697,50 @@ int launch_stream(const DistillParams &p, int64_t rows_at_once, size_t shared, c
         if (e != cudaSuccess || clusters < 1) return fail(GAR_ECUDA, "distill_stream_kernel: %s", cudaGetErrorString(e));
         known.store(clusters, std::memory_order_relaxed);
     }
-    if (!kLag || clusters > rows_at_once) clusters = static_cast<int>(rows_at_once);
-    return launch_early("distill_stream_kernel", kernel, dim3(static_cast<unsigned>(clusters) << p.log_cluster), kStreamThreads, shared,
-                        cluster, stream, p);
+    // (looked up for one CTA an SM, which is what rows of several CTAs get)
+    if (cluster == 1 || clusters > rows_at_once) clusters = static_cast<int>(rows_at_once);
+    return launch_early("distill_stream_kernel", kernel, dim3(static_cast<unsigned>(clusters) << p.log_cluster), stream_threads(kMode),
+                        shared, cluster, stream, p);
 }
 
-template <typename T, bool kSaved>
+template <typename T, int kMode>
 int launch(DistillParams &p, cudaStream_t stream) {
     const int64_t bytes = static_cast<int64_t>(p.vocab) * sizeof(T);
     const int slot = 12 * ((p.k + 3) & ~3);
     int tables = 32;
     while (tables < 2 * p.k) tables *= 2;
     tables *= 4 * kPrepare;
-    // Slots: eight up to 24 KB, else four (three rows' entries are in use where the gradient lags).
-    p.slots = slot * kMaxSlots <= 24576 ? kMaxSlots : 4;
+    p.slots = slot * kMaxSlots <= 24576 ? kMaxSlots : 4;  // eight up to 24 KB
     const int fixed = p.slots * slot + tables;
-    // The fewest CTAs a row whose parts fit the stages (two, or three where the gradient lags a row), and more while
+    // The fewest CTAs a row whose parts fit the stages (one a group works on, and one on its way), and more while
     // there are SMs without a row.
     const auto part = [&](int K) { return (ceil_div(bytes / 16, K) + 1) * 16; };
-    const auto fits = [&](int K, int room) { return (K > 1 && !kSaved ? 3 : 2) * part(K) + fixed <= room; };
+    const auto fits = [&](int K, int room) { return (kMode == kFused ? 3 : 2) * part(K) + fixed <= room; };
     int K = 1;
     while (K < kMaxCluster && !fits(K, kSharedBytes)) K *= 2;
     while (K < kMaxCluster && p.rows * K * 2 <= sm_count() && part(K) >= 8192) K *= 2;
-    if (bytes < kStreamBytes || !fits(K, kSharedBytes)) {
-        return launch_early("distill_row_kernel", distill_row_kernel<T, kSaved>, dim3(static_cast<unsigned>(p.rows)), kRowThreads, 0, 1,
-                            stream, p);
-    }
+    if (bytes < kStreamBytes || !fits(K, kSharedBytes))
+        return launch_early("distill_row_kernel", distill_row_kernel<T, kMode == kGradOnly>, dim3(static_cast<unsigned>(p.rows)),
+                            kRowThreads, 0, 1, stream, p);
     p.log_cluster = K == 8 ? 3 : K / 2;
     p.stage_bytes = static_cast<int32_t>(part(K));
-    const bool lag = K > 1 && !kSaved;
-    // two CTAs an SM where two find room for their stages: one's barriers hide behind the other's passes
-    const bool two = !lag && fits(K, kSharedBytes / 2 - 2048);
+    // two CTAs an SM where two find room for their stages
+    const bool two = (kMode == kGradOnly || K == 1) && fits(K, kSharedBytes / 2 - 2048);
     const int room = (two ? kSharedBytes / 2 - 2048 : kSharedBytes) - fixed;
     p.stages = room / p.stage_bytes < kMaxStages ? room / p.stage_bytes : kMaxStages;
     p.status = device_status();
     int64_t at_once = static_cast<int64_t>(sm_count()) * (two ? 2 : 1) / K;
     if (at_once > p.rows) at_once = p.rows;
-    const size_t shared = static_cast<size_t>(p.stages) * p.stage_bytes + fixed;
-    if constexpr (!kSaved)
-        if (lag) return launch_stream<T, false, true>(p, at_once, shared, stream);
-    return launch_stream<T, kSaved, false>(p, at_once, shared, stream);
+    return launch_stream<T, kMode>(p, at_once, static_cast<size_t>(p.stages) * p.stage_bytes + fixed, stream);
 }
 
 int run(DistillParams &p, int32_t dtype, cudaStream_t stream) {
     if (p.rows == 0) return GAR_OK;
-    if (dtype == GAR_F32) return p.lse_in ? launch<float, true>(p, stream) : launch<float, false>(p, stream);
-    return p.lse_in ? launch<uint16_t, true>(p, stream) : launch<uint16_t, false>(p, stream);
+    if (dtype == GAR_F32)
+        return p.lse_in ? launch<float, kGradOnly>(p, stream) : p.dz ? launch<float, kFused>(p, stream) : launch<float, kLossOnly>(p, stream);
+    return p.lse_in ? launch<uint16_t, kGradOnly>(p, stream)
+           : p.dz   ? launch<uint16_t, kFused>(p, stream)
+                    : launch<uint16_t, kLossOnly>(p, stream);
 }
 
 }  // namespace
