@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_c
 // vectors, in shared memory, as a pipeline of warps:
 //   one warp copies the CTA's part of the coming rows there (bulk copies, up to
 //   eight stages);
-//   kPrepare warps take turns preparing the coming rows' teacher entries
+//   three warps (or five) take turns preparing the coming rows' teacher entries
 //   (slots), a chain of dependent loads and reductions of microseconds a row;
 //   the first group passes over a row for the maximum and the sum of powers,
 //   which its CTAs send one another as one pair each;
@@ -228,8 +228,10 @@ __global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_c
 enum { kFused, kLossOnly, kGradOnly };
 constexpr int first_warps(int mode) { return mode == kGradOnly ? 0 : 8; }  // as many with the gradient as without: the same loss
 constexpr int second_warps(int mode) { return mode == kFused ? 8 : mode == kLossOnly ? 1 : 16; }
-constexpr int kPrepare = 3;
-constexpr int stream_threads(int mode) { return 32 * (first_warps(mode) + second_warps(mode) + 1 + kPrepare); }
+// fp32 logits for the loss alone go by so fast (5.5 to 6.8 TB/s) that three preparing warps hold them up (2048 x 131072, 128
+// entries: 251 us with three, 195 with five); elsewhere more only take issue slots (4096 x 50001 bf16: 144 us, 159 with five).
+constexpr int prepare_warps(int mode, size_t size) { return mode == kLossOnly && size == 4 ? 5 : 3; }
+constexpr int stream_threads(int mode, size_t size) { return 32 * (first_warps(mode) + second_warps(mode) + 1 + prepare_warps(mode, size)); }
 constexpr int kMaxStages = 8, kMaxSlots = 8, kMaxCluster = 8;
 // Exchanges under way.  A CTA's first group is at most kMaxStages rows ahead of its second; to send row i + n it has
 // seen its second group finish row i + n - kMaxStages, for which every CTA's first group sent that row and its second
@@ -323,10 +325,10 @@ __device__ __forceinline__ void bar_group(int id) {
 }
 
 template <typename T, int kMode>
-__global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kernel(const __grid_constant__ DistillParams p) {
+__global__ void __launch_bounds__(stream_threads(kMode, sizeof(T)), 2) distill_stream_kernel(const __grid_constant__ DistillParams p) {
     constexpr int n = 16 / sizeof(T);
     constexpr bool kSaved = kMode == kGradOnly;
-    constexpr int kFirst = first_warps(kMode), kSecond = second_warps(kMode), kMainWarps = kFirst + kSecond;
+    constexpr int kPrepare = prepare_warps(kMode, sizeof(T)), kFirst = first_warps(kMode), kSecond = second_warps(kMode), kMainWarps = kFirst + kSecond;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kMaxSlots + kMeets];
     __shared__ Header header[kMaxSlots];
@@ -684,7 +686,7 @@ int launch_stream(const DistillParams &p, int64_t rows_at_once, size_t shared, c
         if (e == cudaSuccess && cluster > 1) {
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(cluster);
-            cfg.blockDim = dim3(stream_threads(kMode));
+            cfg.blockDim = dim3(stream_threads(kMode, sizeof(T)));
             cfg.dynamicSmemBytes = kSharedBytes;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -699,7 +701,7 @@ int launch_stream(const DistillParams &p, int64_t rows_at_once, size_t shared, c
     }
     // (looked up for one CTA an SM, which is what rows of several CTAs get)
     if (cluster == 1 || clusters > rows_at_once) clusters = static_cast<int>(rows_at_once);
-    return launch_early("distill_stream_kernel", kernel, dim3(static_cast<unsigned>(clusters) << p.log_cluster), stream_threads(kMode),
+    return launch_early("distill_stream_kernel", kernel, dim3(static_cast<unsigned>(clusters) << p.log_cluster), stream_threads(kMode, sizeof(T)),
                         shared, cluster, stream, p);
 }
 
@@ -709,7 +711,7 @@ int launch(DistillParams &p, cudaStream_t stream) {
     const int slot = 12 * ((p.k + 3) & ~3);
     int tables = 32;
     while (tables < 2 * p.k) tables *= 2;
-    tables *= 4 * kPrepare;
+    tables *= 4 * prepare_warps(kMode, sizeof(T));
     p.slots = slot * kMaxSlots <= 24576 ? kMaxSlots : 4;  // eight up to 24 KB
     const int fixed = p.slots * slot + tables;
     // The fewest CTAs a row whose parts fit the stages (one a group works on, and one on its way), and more while
