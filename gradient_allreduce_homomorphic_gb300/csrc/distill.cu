@@ -110,102 +110,232 @@ struct Softmax {
     }
 };
 
-// ---------------------------------------------------------------- short rows
-constexpr int kRowThreads = 128;
+// ------------------------------------------------------------ a row's vectors
+template <typename T>
+struct Row {  // one row's split into head, vectors and tail
+    int32_t head, vectors, v0, v1;  // this CTA: vectors v0 .. v1
+    __device__ __forceinline__ Row(const T *z, int32_t vocab, int32_t rank, int32_t log_cluster) {
+        constexpr int32_t n = 16 / sizeof(T);
+        const int32_t off = static_cast<int32_t>((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / static_cast<int32_t>(sizeof(T));
+        head = off < vocab ? off : vocab;
+        vectors = (vocab - head) / n;
+        v0 = (vectors * rank) >> log_cluster;  // a row that is taken this way has fewer than 2^16 vectors
+        v1 = (vectors * (rank + 1)) >> log_cluster;
+    }
+    // Element of the i-th place outside the vectors, which are the first CTA's; -1 past the last.
+    __device__ __forceinline__ int32_t edge(int32_t i, int32_t vocab, int32_t rank) const {
+        const int32_t at = i < head ? i : i + vectors * static_cast<int32_t>(16 / sizeof(T));
+        return rank == 0 && at < vocab ? at : -1;
+    }
+    __device__ __forceinline__ bool holds(int32_t i, int32_t rank) const {
+        constexpr int32_t n = 16 / sizeof(T);
+        const int32_t v = i - head;
+        if (v < 0 || v >= vectors * n) return rank == 0;
+        return v >= v0 * n && v < v1 * n;
+    }
+};
 
-template <bool kMax>
-__device__ __forceinline__ float block_reduce(float v, float *scratch) {
-    v = kMax ? warp_max(v) : warp_sum(v);
-    __syncthreads();
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4 &g, float (&x)[16 / sizeof(T)]) {
+    if constexpr (sizeof(T) == 2) {
+        x[0] = bf16_lo(g.x), x[1] = bf16_hi(g.x), x[2] = bf16_lo(g.y), x[3] = bf16_hi(g.y);
+        x[4] = bf16_lo(g.z), x[5] = bf16_hi(g.z), x[6] = bf16_lo(g.w), x[7] = bf16_hi(g.w);
+    } else {
+        x[0] = __uint_as_float(g.x), x[1] = __uint_as_float(g.y);
+        x[2] = __uint_as_float(g.z), x[3] = __uint_as_float(g.w);
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&x)[16 / sizeof(T)]) {
+    if constexpr (sizeof(T) == 2)
+        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    else
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+
+template <int n>
+__device__ __forceinline__ float tree_max(const float (&x)[n]) {
+    float m[n / 2];
+#pragma unroll
+    for (int j = 0; j < n / 2; ++j) m[j] = fmaxf(x[j], x[j + n / 2]);
+    if constexpr (n == 2)
+        return m[0];
+    else
+        return tree_max(m);
+}
+template <int n>
+__device__ __forceinline__ float tree_sum(const float (&x)[n]) {
+    float m[n / 2];
+#pragma unroll
+    for (int j = 0; j < n / 2; ++j) m[j] = x[j] + x[j + n / 2];
+    if constexpr (n == 2)
+        return m[0];
+    else
+        return tree_sum(m);
+}
+
+// ---------------------------------------------------------------- short rows
+// A CTA holds its row in registers, kHold vectors a thread, so z is read once
+// and the maximum is known before the powers; the other rows' CTAs on the SM
+// hide its barriers.  Rows too long for the stages of eight CTAs (above 880 KB)
+// are taken here too, with kHold = 0: they are read from memory each time.
+constexpr int kRowThreads = 128, kRowHold = 8, kLongThreads = 1024;
+
+// Sums (or maxima) of both over the block.  The scratch is the call's own: one barrier.
+template <bool kMax, int kWarps>
+__device__ __forceinline__ float2 block_reduce(float2 v, float2 (&scratch)[kWarps]) {
+    v = kMax ? make_float2(warp_max(v.x), warp_max(v.y)) : make_float2(warp_sum(v.x), warp_sum(v.y));
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
     __syncthreads();
     v = scratch[0];
 #pragma unroll
-    for (int i = 1; i < kRowThreads / 32; ++i) v = kMax ? fmaxf(v, scratch[i]) : v + scratch[i];
+    for (int i = 1; i < kWarps; ++i) {
+        const float2 o = scratch[i];
+        v = kMax ? make_float2(fmaxf(v.x, o.x), fmaxf(v.y, o.y)) : make_float2(v.x + o.x, v.y + o.y);
+    }
     return v;
 }
 
-template <typename T, bool kSaved>
-__global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_constant__ DistillParams p) {
-    __shared__ float scratch[kRowThreads / 32];
+template <typename T, bool kSaved, int kHold>
+__global__ void __launch_bounds__(kHold ? kRowThreads : kLongThreads) distill_row_kernel(const __grid_constant__ DistillParams p) {
+    constexpr int n = 16 / sizeof(T), kThreads = kHold ? kRowThreads : kLongThreads;
+    __shared__ float2 scratch[3][kThreads / 32];
     __shared__ float top_p[kMaxTop], top_z[kMaxTop];
     __shared__ int32_t top_i[kMaxTop];
+    __shared__ uint32_t seen[((kHold * kThreads + 2) * n + 31) / 32];  // a bit for each element: entries that repeat one
+    __shared__ int repeated;
     const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x;
     const T *z = static_cast<const T *>(p.z) + row * p.ldz;
     T *dz = p.dz ? static_cast<T *>(p.dz) + row * p.lddz : nullptr;
+    const Row<T> part(z, p.vocab, 0, 0);
+    const int odd = part.edge(tid, p.vocab, 0);
+    if (kHold)
+        for (int i = tid; i * 32 < p.vocab; i += kThreads) seen[i] = 0;
+    if (tid == 0) repeated = kHold == 0;
     let_next_begin();
     after_previous();
+    uint4 held[kHold ? kHold : 1];
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+        const int i = tid + h * kThreads;
+        const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf: in no maximum and in no sum
+        held[h] = make_uint4(none, none, none, none);
+        if (i < part.vectors) held[h] = ld16(z + part.head + i * n);
+    }
+    // every vector of this thread's: f(which, its values)
+    const auto each = [&](auto &&f) {
+        float x[n];
+        if constexpr (kHold > 0) {
+#pragma unroll
+            for (int h = 0; h < kHold; ++h) {
+                unpack<T>(held[h], x);
+                f(tid + h * kThreads, x);
+            }
+        } else {
+#pragma unroll 2
+            for (int i = tid; i < part.vectors; i += kThreads) {
+                unpack<T>(*reinterpret_cast<const uint4 *>(z + part.head + static_cast<int64_t>(i) * n), x);
+                f(i, x);
+            }
+        }
+    };
+    const float z_odd = odd >= 0 ? load_f32(z + odd) : -INFINITY;
     const float w = p.weight ? p.weight[row] : 1.0f;
-    const int tid = threadIdx.x;
+    const float saved = kSaved ? p.lse_in[row] : 0.0f;
 
-    float tmax = -INFINITY;
-    for (int j = tid; j < p.k; j += kRowThreads) {
+    float2 top = make_float2(-INFINITY, z_odd);  // maxima of the entries' logits and of z
+    for (int j = tid; j < p.k; j += kThreads) {
         const int32_t i = p.index[row * p.k + j];
         const float t = p.teacher[row * p.k + j];
         const bool on = i >= 0 && i < p.vocab && !(t == -INFINITY);
         top_i[j] = on ? i : -1;
         top_p[j] = t;
         top_z[j] = on ? load_f32(z + i) : 0.0f;
-        if (on) tmax = fmaxf(tmax, t);
+        if (on) top.x = fmaxf(top.x, t);
     }
-    tmax = block_reduce<true>(tmax, scratch);
-    float tsum = 0.0f;
-    for (int j = tid; j < p.k; j += kRowThreads)
-        if (top_i[j] >= 0) tsum += entry_power(p, top_p[j], tmax).power;
-    tsum = block_reduce<false>(tsum, scratch);
-    if (w == 0.0f || tsum == 0.0f) {  // nothing to learn in this row
-        if (dz)
-            for (int v = tid; v < p.vocab; v += kRowThreads) store_f32(dz + v, 0.0f);
-        if (!kSaved && tid == 0) p.loss[row] = 0.0f, p.lse[row] = 0.0f;
-        return;
-    }
-    const float log_tsum = logf(tsum), c = kLog2e * p.inv_tau;
-    Softmax<kSaved> q;
-    bool empty = false;
-    if (kSaved) {
-        q.ref = 0.0f, q.c = p.inv_tau, q.sub = p.lse_in[row];
-        empty = q.sub == -INFINITY;
-    } else {
-        float m = -INFINITY;
-        for (int v = tid; v < p.vocab; v += kRowThreads) m = fmaxf(m, load_f32(z + v));
-        m = block_reduce<true>(m, scratch);
-        const float r = finite_or_0(m);
-        float s = 0.0f;
-        for (int v = tid; v < p.vocab; v += kRowThreads) s += pow2((load_f32(z + v) - r) * c);
-        s = block_reduce<false>(s, scratch);
-        empty = m == -INFINITY && s == 0.0f;
-        q.ref = r, q.c = c, q.sub = log2f(s);
-    }
-    float part = 0.0f;
-    for (int j = tid; j < p.k; j += kRowThreads) {
-        float pj = 0.0f;
-        if (top_i[j] >= 0) {
-            const Entry t = entry_power(p, top_p[j], tmax);
-            pj = t.power / tsum;
-            if (!(pj == 0.0f)) part += pj * (t.exponent - log_tsum - (top_z[j] - q.ref) * p.inv_tau);
-        }
-        top_p[j] = pj;
-    }
-    part = block_reduce<false>(part, scratch);
-    if (!kSaved && tid == 0) {
-        p.loss[row] = empty ? INFINITY : part + q.sub * kLn2;
-        p.lse[row] = empty ? -INFINITY : q.ref * p.inv_tau + q.sub * kLn2;
-    }
-    if (!dz) return;
-    const float g = w * p.inv_tau;
-    for (int v = tid; v < p.vocab; v += kRowThreads) store_f32(dz + v, empty ? 0.0f : g * q(load_f32(z + v)));
-    __syncthreads();
-    for (int j = tid; j < p.k; j += kRowThreads) {
+    const float c = kLog2e * p.inv_tau;
+    if (!kSaved) each([&](int, float(&x)[n]) { top.y = fmaxf(top.y, tree_max(x)); });
+    top = block_reduce<true>(top, scratch[0]);
+    const float tmax = top.x, r = finite_or_0(top.y);
+    float2 sum = make_float2(0.0f, 0.0f);  // of the entries' powers and of z's
+    for (int j = tid; j < p.k; j += kThreads) {
         const int32_t i = top_i[j];
         if (i < 0) continue;
-        float sum = 0.0f;
-        bool first = true;
-        for (int o = 0; o < p.k; ++o)
-            if (top_i[o] == i) {
-                if (o < j) first = false;
-                sum += top_p[o];
+        sum.x += entry_power(p, top_p[j], tmax).power;
+        if (kHold && dz && (atomicOr(seen + (i >> 5), 1u << (i & 31)) >> (i & 31) & 1)) repeated = 1;
+    }
+    if (!kSaved) {
+        sum.y = pow2((z_odd - r) * c);
+        each([&](int, float(&x)[n]) {
+#pragma unroll
+            for (int j = 0; j < n; ++j) x[j] = pow2((x[j] - r) * c);
+            sum.y += tree_sum(x);
+        });
+    }
+    sum = block_reduce<false>(sum, scratch[1]);
+    const bool live = w != 0.0f && sum.x != 0.0f;  // NaN: live, and it spreads
+    Softmax<kSaved> q{0.0f, 0.0f, kSaved ? p.inv_tau : c};
+    bool none;
+    if (kSaved)
+        q.sub = saved, none = saved == -INFINITY;
+    else
+        q.ref = r, q.sub = log2f(sum.y), none = top.y == -INFINITY && sum.y == 0.0f;
+    float2 cross = make_float2(0.0f, 0.0f);
+    if (live) {
+        const float log_tsum = logf(sum.x);
+        for (int j = tid; j < p.k; j += kThreads) {
+            float pj = 0.0f;
+            if (top_i[j] >= 0) {
+                const Entry t = entry_power(p, top_p[j], tmax);
+                pj = t.power / sum.x;
+                if (!(pj == 0.0f)) cross.x += pj * (t.exponent - log_tsum - (top_z[j] - q.ref) * p.inv_tau);
             }
-        if (first) store_f32(dz + i, g * ((empty ? 0.0f : q(top_z[j])) - sum));
+            top_p[j] = pj;
+        }
+    }
+    if (!kSaved) {
+        cross = block_reduce<false>(cross, scratch[2]);
+        if (tid == 0) {
+            p.loss[row] = !live ? 0.0f : none ? INFINITY : cross.x + q.sub * kLn2;
+            p.lse[row] = !live ? 0.0f : none ? -INFINITY : q.ref * p.inv_tau + q.sub * kLn2;
+        }
+    }
+    if (!dz) return;
+    const float g = live && !none ? w * p.inv_tau : 0.0f;
+    const bool zero = g == 0.0f;  // whatever z holds
+    T *out = dz + part.head;
+    const bool wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    if (odd >= 0) store_f32(dz + odd, zero ? 0.0f : g * q(z_odd));
+    each([&](int i, float(&x)[n]) {
+        if (i >= part.vectors) return;
+#pragma unroll
+        for (int j = 0; j < n; ++j) x[j] = zero ? 0.0f : g * q(x[j]);
+        T *at = out + static_cast<int64_t>(i) * n;
+        if (wide) {
+            st16(at, pack<T>(x));
+        } else {
+#pragma unroll
+            for (int j = 0; j < n; ++j) store_f32(at + j, x[j]);
+        }
+    });
+    if (!live) return;
+    __syncthreads();
+    for (int j = tid; j < p.k; j += kThreads) {  // dz at the entries, over what the pass stored there
+        const int32_t i = top_i[j];
+        if (i < 0) continue;
+        float pj = top_p[j];
+        if (repeated) {
+            pj = 0.0f;
+            bool earlier = false;
+            for (int o = 0; o < p.k; ++o)
+                if (top_i[o] == i) {
+                    earlier |= o < j;
+                    pj += top_p[o];
+                }
+            if (earlier) continue;
+        }
+        store_f32(dz + i, fmaf(-(w * p.inv_tau), pj, zero ? 0.0f : g * q(top_z[j])));
     }
 }
 
@@ -248,75 +378,12 @@ struct Header {
     float edge[16];  // the first CTA's logits outside the vectors (up to 14), in order
 };
 
-template <typename T>
-struct Row {  // one row's split into head, vectors and tail
-    int32_t head, vectors, v0, v1;  // this CTA: vectors v0 .. v1
-    __device__ __forceinline__ Row(const T *z, int32_t vocab, int32_t rank, int32_t log_cluster) {
-        constexpr int32_t n = 16 / sizeof(T);
-        const int32_t off = static_cast<int32_t>((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / static_cast<int32_t>(sizeof(T));
-        head = off < vocab ? off : vocab;
-        vectors = (vocab - head) / n;
-        v0 = (vectors * rank) >> log_cluster;  // a row that is taken this way has fewer than 2^16 vectors
-        v1 = (vectors * (rank + 1)) >> log_cluster;
-    }
-    // Element of the i-th place outside the vectors, which are the first CTA's; -1 past the last.
-    __device__ __forceinline__ int32_t edge(int32_t i, int32_t vocab, int32_t rank) const {
-        const int32_t at = i < head ? i : i + vectors * static_cast<int32_t>(16 / sizeof(T));
-        return rank == 0 && at < vocab ? at : -1;
-    }
-    __device__ __forceinline__ bool holds(int32_t i, int32_t rank) const {
-        constexpr int32_t n = 16 / sizeof(T);
-        const int32_t v = i - head;
-        if (v < 0 || v >= vectors * n) return rank == 0;
-        return v >= v0 * n && v < v1 * n;
-    }
-};
-
 // `bytes` (a multiple of 16) to shared memory, counted on the mbarrier.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     if (bytes > 0)
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                      "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
                      : "memory");
-}
-
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4 &g, float (&x)[16 / sizeof(T)]) {
-    if constexpr (sizeof(T) == 2) {
-        x[0] = bf16_lo(g.x), x[1] = bf16_hi(g.x), x[2] = bf16_lo(g.y), x[3] = bf16_hi(g.y);
-        x[4] = bf16_lo(g.z), x[5] = bf16_hi(g.z), x[6] = bf16_lo(g.w), x[7] = bf16_hi(g.w);
-    } else {
-        x[0] = __uint_as_float(g.x), x[1] = __uint_as_float(g.y);
-        x[2] = __uint_as_float(g.z), x[3] = __uint_as_float(g.w);
-    }
-}
-template <typename T>
-__device__ __forceinline__ uint4 pack(const float (&x)[16 / sizeof(T)]) {
-    if constexpr (sizeof(T) == 2)
-        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-    else
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-}
-
-template <int n>
-__device__ __forceinline__ float tree_max(const float (&x)[n]) {
-    float m[n / 2];
-#pragma unroll
-    for (int j = 0; j < n / 2; ++j) m[j] = fmaxf(x[j], x[j + n / 2]);
-    if constexpr (n == 2)
-        return m[0];
-    else
-        return tree_max(m);
-}
-template <int n>
-__device__ __forceinline__ float tree_sum(const float (&x)[n]) {
-    float m[n / 2];
-#pragma unroll
-    for (int j = 0; j < n / 2; ++j) m[j] = x[j] + x[j + n / 2];
-    if constexpr (n == 2)
-        return m[0];
-    else
-        return tree_sum(m);
 }
 
 template <int kThreads>
@@ -666,7 +733,7 @@ int check(const void *z, int32_t dtype, int64_t rows, int64_t vocab, int64_t ldz
     return GAR_OK;
 }
 
-constexpr int64_t kStreamBytes = 16384;
+constexpr int64_t kStreamBytes = kRowHold * kRowThreads * 16;
 constexpr int kSharedBytes = 220 * 1024;  // of a CTA that has the SM to itself, static shared memory taken off
 
 template <typename T, int kMode>
@@ -717,13 +784,21 @@ int launch(DistillParams &p, cudaStream_t stream) {
     // The fewest CTAs a row whose parts fit the stages (one a group works on, and one on its way), and more while
     // there are SMs without a row.
     const auto part = [&](int K) { return (ceil_div(bytes / 16, K) + 1) * 16; };
-    const auto fits = [&](int K, int room) { return (kMode == kFused ? 3 : 2) * part(K) + fixed <= room; };
+    int least = kMode == kFused && 3 * part(kMaxCluster) + fixed <= kSharedBytes ? 3 : 2;
+    const auto fits = [&](int K, int room) { return least * part(K) + fixed <= room; };
     int K = 1;
     while (K < kMaxCluster && !fits(K, kSharedBytes)) K *= 2;
     while (K < kMaxCluster && p.rows * K * 2 <= sm_count() && part(K) >= 8192) K *= 2;
-    if (bytes < kStreamBytes || !fits(K, kSharedBytes))
-        return launch_early("distill_row_kernel", distill_row_kernel<T, kMode == kGradOnly>, dim3(static_cast<unsigned>(p.rows)),
-                            kRowThreads, 0, 1, stream, p);
+    if (!fits(K, kSharedBytes))
+        return launch_early("distill_row_kernel", distill_row_kernel<T, kMode == kGradOnly, 0>, dim3(static_cast<unsigned>(p.rows)),
+                            kLongThreads, 0, 1, stream, p);
+    if (bytes < kStreamBytes) {
+        const auto kernel = bytes <= kRowThreads * 16      ? distill_row_kernel<T, kMode == kGradOnly, 1>
+                            : bytes <= kRowThreads * 2 * 16 ? distill_row_kernel<T, kMode == kGradOnly, 2>
+                            : bytes <= kRowThreads * 4 * 16 ? distill_row_kernel<T, kMode == kGradOnly, 4>
+                                                            : distill_row_kernel<T, kMode == kGradOnly, kRowHold>;
+        return launch_early("distill_row_kernel", kernel, dim3(static_cast<unsigned>(p.rows)), kRowThreads, 0, 1, stream, p);
+    }
     p.log_cluster = K == 8 ? 3 : K / 2;
     p.stage_bytes = static_cast<int32_t>(part(K));
     // two CTAs an SM where two find room for their stages

@@ -288,3 +288,30 @@ def test_offsets_beyond_32_bits(env):
     want = ref.distill(host, ih, th, 1.0, np.ones(5))
     close(loss[tail].cpu().numpy(), want[0], 1e-4, "loss")
     close(z[tail].float().cpu().numpy(), want[2], 2.0 ** -8 * np.abs(want[2]) + 1e-9, "dz")
+
+
+# rows that fill two stages of eight CTAs, and rows that no eight CTAs hold
+@pytest.mark.parametrize("vocab", [151937, 230003, 460001])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("mode", ["fused", "split", "place"])
+def test_very_long_rows(env, vocab, dtype, mode):
+    torch, g = env
+    z, index, teacher, weight = problem(5, vocab, 37, 12, repeat=True)
+    index[1, :] = vocab - 1
+    index[2, ::3] = vocab
+    weight[3] = 0.0
+    z[3] = np.inf
+    z[4, : vocab // 2] = -np.inf
+    check(torch, g, device(torch, z, dtype), index, teacher, weight, 1.3, mode)
+
+
+# short rows: each number of vectors a thread holds, one element to each side of it
+@pytest.mark.parametrize("vocab", [511, 512, 513, 1023, 1025, 2047, 2049, 4095, 4103, 8185, 8199])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("mode", ["fused", "split", "place"])
+def test_short_rows_at_every_length(env, vocab, dtype, mode):
+    torch, g = env
+    z, index, teacher, weight = problem(17, vocab, 19, 13, repeat=True)
+    index[1, :] = 0
+    index[2, :] = vocab - 1
+    check(torch, g, device(torch, z, dtype), index, teacher, weight, 0.9, mode)
