@@ -13,10 +13,13 @@
 // exact, and the product's rounding is relative to a small number.  A maximum
 // of -inf is replaced by 0 in the difference, which makes the powers 0.
 //
-// Bound by HBM: a row is read once and, with dz, written once.  Rows of at
-// least kStreamBytes go through shared memory (distill_stream_kernel); shorter
-// ones take one small CTA each, whose second and third reads hit L1 and L2
-// (distill_row_kernel).
+// Bound by HBM: a row is read once and, with dz, written once.  Short rows, or
+// few, are held in the registers of one CTA (distill_row_kernel); others go
+// through shared memory (distill_stream_kernel).  Loss and gradient in one call:
+// 4096 x 50001 bf16 144 us, 5.7 TB/s; 4096 x 50001 fp32 244 us, 6.7 TB/s;
+// 4096 x 4096 bf16 15.5 us, 4.3 TB/s (the rows' reductions); 8 x 32000 bf16 5 us
+// (one row's latency).  The loss alone of bf16 rows is bound by its pass's
+// instructions and powers: 4096 x 32768 62 us, 4.3 TB/s.
 #include <atomic>
 
 #include "common.cuh"
@@ -179,7 +182,6 @@ __device__ __forceinline__ float tree_sum(const float (&x)[n]) {
 // and the maximum is known before the powers; the other rows' CTAs on the SM
 // hide its barriers.  Rows too long for the stages of eight CTAs (above 880 KB)
 // are taken here too, with kHold = 0: they are read from memory each time.
-constexpr int kRowThreads = 128, kRowHold = 8, kLongThreads = 1024;
 
 // Sums (or maxima) of both over the block.  The scratch is the call's own: one barrier.
 template <bool kMax, int kWarps>
@@ -196,9 +198,9 @@ __device__ __forceinline__ float2 block_reduce(float2 v, float2 (&scratch)[kWarp
     return v;
 }
 
-template <typename T, bool kSaved, int kHold>
-__global__ void __launch_bounds__(kHold ? kRowThreads : kLongThreads) distill_row_kernel(const __grid_constant__ DistillParams p) {
-    constexpr int n = 16 / sizeof(T), kThreads = kHold ? kRowThreads : kLongThreads;
+template <typename T, bool kSaved, int kHold, int kThreads>
+__global__ void __launch_bounds__(kThreads) distill_row_kernel(const __grid_constant__ DistillParams p) {
+    constexpr int n = 16 / sizeof(T);
     __shared__ float2 scratch[3][kThreads / 32];
     __shared__ float top_p[kMaxTop], top_z[kMaxTop];
     __shared__ int32_t top_i[kMaxTop];
@@ -267,11 +269,20 @@ __global__ void __launch_bounds__(kHold ? kRowThreads : kLongThreads) distill_ro
     }
     if (!kSaved) {
         sum.y = pow2((z_odd - r) * c);
-        each([&](int, float(&x)[n]) {
+        const float rc = r * c;
+        if (sizeof(T) == 2 && fabsf(rc) <= kPlain) {
+            each([&](int, float(&x)[n]) {
 #pragma unroll
-            for (int j = 0; j < n; ++j) x[j] = pow2((x[j] - r) * c);
-            sum.y += tree_sum(x);
-        });
+                for (int j = 0; j < n; ++j) x[j] = pow2(fmaf(x[j], c, -rc));
+                sum.y += tree_sum(x);
+            });
+        } else {
+            each([&](int, float(&x)[n]) {
+#pragma unroll
+                for (int j = 0; j < n; ++j) x[j] = pow2((x[j] - r) * c);
+                sum.y += tree_sum(x);
+            });
+        }
     }
     sum = block_reduce<false>(sum, scratch[1]);
     const bool live = w != 0.0f && sum.x != 0.0f;  // NaN: live, and it spreads
@@ -307,18 +318,28 @@ __global__ void __launch_bounds__(kHold ? kRowThreads : kLongThreads) distill_ro
     T *out = dz + part.head;
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
     if (odd >= 0) store_f32(dz + odd, zero ? 0.0f : g * q(z_odd));
-    each([&](int i, float(&x)[n]) {
-        if (i >= part.vectors) return;
+    if (sizeof(T) == 2 && !kSaved && wide && g > 0.0f && fabsf(q.ref * c) <= kPlain) {
+        const float sub = fmaf(q.ref, c, q.sub) - log2f(g);  // g too goes into the exponent
+        each([&](int i, float(&x)[n]) {
+            if (i >= part.vectors) return;
 #pragma unroll
-        for (int j = 0; j < n; ++j) x[j] = zero ? 0.0f : g * q(x[j]);
-        T *at = out + static_cast<int64_t>(i) * n;
-        if (wide) {
-            st16(at, pack<T>(x));
-        } else {
+            for (int j = 0; j < n; ++j) x[j] = pow2(fmaf(x[j], c, -sub));
+            st16(out + static_cast<int64_t>(i) * n, pack<T>(x));
+        });
+    } else {
+        each([&](int i, float(&x)[n]) {
+            if (i >= part.vectors) return;
 #pragma unroll
-            for (int j = 0; j < n; ++j) store_f32(at + j, x[j]);
-        }
-    });
+            for (int j = 0; j < n; ++j) x[j] = zero ? 0.0f : g * q(x[j]);
+            T *at = out + static_cast<int64_t>(i) * n;
+            if (wide) {
+                st16(at, pack<T>(x));
+            } else {
+#pragma unroll
+                for (int j = 0; j < n; ++j) store_f32(at + j, x[j]);
+            }
+        });
+    }
     if (!live) return;
     __syncthreads();
     for (int j = tid; j < p.k; j += kThreads) {  // dz at the entries, over what the pass stored there
@@ -733,7 +754,6 @@ int check(const void *z, int32_t dtype, int64_t rows, int64_t vocab, int64_t ldz
     return GAR_OK;
 }
 
-constexpr int64_t kStreamBytes = kRowHold * kRowThreads * 16;
 constexpr int kSharedBytes = 220 * 1024;  // of a CTA that has the SM to itself, static shared memory taken off
 
 template <typename T, int kMode>
@@ -772,6 +792,12 @@ int launch_stream(const DistillParams &p, int64_t rows_at_once, size_t shared, c
                         shared, cluster, stream, p);
 }
 
+template <typename T, bool kSaved, int kHold, int kThreads>
+int launch_row(const DistillParams &p, cudaStream_t stream) {
+    return launch_early("distill_row_kernel", distill_row_kernel<T, kSaved, kHold, kThreads>, dim3(static_cast<unsigned>(p.rows)),
+                        kThreads, 0, 1, stream, p);
+}
+
 template <typename T, int kMode>
 int launch(DistillParams &p, cudaStream_t stream) {
     const int64_t bytes = static_cast<int64_t>(p.vocab) * sizeof(T);
@@ -789,15 +815,18 @@ int launch(DistillParams &p, cudaStream_t stream) {
     int K = 1;
     while (K < kMaxCluster && !fits(K, kSharedBytes)) K *= 2;
     while (K < kMaxCluster && p.rows * K * 2 <= sm_count() && part(K) >= 8192) K *= 2;
-    if (!fits(K, kSharedBytes))
-        return launch_early("distill_row_kernel", distill_row_kernel<T, kMode == kGradOnly, 0>, dim3(static_cast<unsigned>(p.rows)),
-                            kLongThreads, 0, 1, stream, p);
-    if (bytes < kStreamBytes) {
-        const auto kernel = bytes <= kRowThreads * 16      ? distill_row_kernel<T, kMode == kGradOnly, 1>
-                            : bytes <= kRowThreads * 2 * 16 ? distill_row_kernel<T, kMode == kGradOnly, 2>
-                            : bytes <= kRowThreads * 4 * 16 ? distill_row_kernel<T, kMode == kGradOnly, 4>
-                                                            : distill_row_kernel<T, kMode == kGradOnly, kRowHold>;
-        return launch_early("distill_row_kernel", kernel, dim3(static_cast<unsigned>(p.rows)), kRowThreads, 0, 1, stream, p);
+    // Rows in registers: up to 16 KB (4096 x 4096 bf16 15.5 us; through shared memory 30; 4096 x 8192 28 and 39), and while
+    // every row has an SM to itself, where latency counts, up to 64 KB (8 x 32000 bf16 5.0 us and 6.1; 150 x 16001 fp32 4.8
+    // and 10.6; but 8192 x 16384 bf16 133 and 93).  Fewer vectors a thread than eight cost more in barriers than they give.
+    constexpr bool kSaved = kMode == kGradOnly;
+    if (!fits(K, kSharedBytes)) return launch_row<T, kSaved, 0, 1024>(p, stream);
+    if (bytes <= 2048) return launch_row<T, kSaved, 1, 128>(p, stream);
+    if (bytes <= 4096) return launch_row<T, kSaved, 2, 128>(p, stream);
+    if (bytes <= 8192) return launch_row<T, kSaved, 4, 128>(p, stream);
+    if (bytes <= 16384) return launch_row<T, kSaved, 8, 128>(p, stream);
+    if (p.rows <= sm_count()) {
+        if (bytes <= 32768) return launch_row<T, kSaved, 8, 256>(p, stream);
+        if (bytes <= 65536) return launch_row<T, kSaved, 8, 512>(p, stream);
     }
     p.log_cluster = K == 8 ? 3 : K / 2;
     p.stage_bytes = static_cast<int32_t>(part(K));
