@@ -77,27 +77,51 @@ __device__ __forceinline__ int expert(int sub, int i) {
     return i / kRun * (kRun * L) + sub * kRun + i % kRun;
 }
 
-// A lane's logits of one token; -inf past the last expert.
+// A lane's logits of one token as they are stored, a run in each; -inf past the last expert.
+template <typename T, int V>
+using Runs = uint4[V * sizeof(T) / 16];
 template <typename T, int L, int V>
-__device__ __forceinline__ void load_token(const T *z, int sub, int experts, bool wide, float (&v)[V]) {
+__device__ __forceinline__ void load_runs(const T *z, int sub, int experts, bool wide, Runs<T, V> &g) {
     constexpr int kRun = 16 / sizeof(T);
 #pragma unroll
-    for (int r = 0; r < V; r += kRun) {
-        const int e0 = expert<T, L>(sub, r);
+    for (int r = 0; r < V / kRun; ++r) {
+        const int e0 = expert<T, L>(sub, r * kRun);
         if (wide && e0 + kRun <= experts) {
-            const uint4 g = *reinterpret_cast<const uint4 *>(z + e0);
-            if constexpr (sizeof(T) == 2) {
-                v[r] = bf16_lo(g.x), v[r + 1] = bf16_hi(g.x), v[r + 2] = bf16_lo(g.y), v[r + 3] = bf16_hi(g.y);
-                v[r + 4] = bf16_lo(g.z), v[r + 5] = bf16_hi(g.z), v[r + 6] = bf16_lo(g.w), v[r + 7] = bf16_hi(g.w);
-            } else {
-                v[r] = __uint_as_float(g.x), v[r + 1] = __uint_as_float(g.y);
-                v[r + 2] = __uint_as_float(g.z), v[r + 3] = __uint_as_float(g.w);
-            }
+            g[r] = *reinterpret_cast<const uint4 *>(z + e0);
         } else {
+            uint32_t x[4];
+            if constexpr (sizeof(T) == 2) {
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) v[r + j] = e0 + j < experts ? load_f32(z + e0 + j) : -INFINITY;
+                for (int j = 0; j < 4; ++j)
+                    x[j] = (e0 + 2 * j < experts ? z[e0 + 2 * j] : 0xFF80u) | (e0 + 2 * j + 1 < experts ? z[e0 + 2 * j + 1] : 0xFF80u) << 16;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = e0 + j < experts ? __float_as_uint(z[e0 + j]) : 0xFF800000u;
+            }
+            g[r] = make_uint4(x[0], x[1], x[2], x[3]);
         }
     }
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack_runs(const Runs<T, V> &g, float (&v)[V]) {
+    constexpr int kRun = 16 / sizeof(T);
+#pragma unroll
+    for (int r = 0; r < V / kRun; ++r) {
+        float *x = v + r * kRun;
+        if constexpr (sizeof(T) == 2) {
+            x[0] = bf16_lo(g[r].x), x[1] = bf16_hi(g[r].x), x[2] = bf16_lo(g[r].y), x[3] = bf16_hi(g[r].y);
+            x[4] = bf16_lo(g[r].z), x[5] = bf16_hi(g[r].z), x[6] = bf16_lo(g[r].w), x[7] = bf16_hi(g[r].w);
+        } else {
+            x[0] = __uint_as_float(g[r].x), x[1] = __uint_as_float(g[r].y);
+            x[2] = __uint_as_float(g[r].z), x[3] = __uint_as_float(g[r].w);
+        }
+    }
+}
+template <typename T, int L, int V>
+__device__ __forceinline__ void load_token(const T *z, int sub, int experts, bool wide, float (&v)[V]) {
+    Runs<T, V> g;
+    load_runs<T, L, V>(z, sub, experts, wide, g);
+    unpack_runs<T, V>(g, v);
 }
 template <typename T, int L, int V>
 __device__ __forceinline__ void store_token(T *dz, int sub, int experts, bool wide, const float (&v)[V]) {
@@ -273,18 +297,26 @@ __device__ __forceinline__ bool choose(const BalanceParams &p, int w, int64_t t,
     return some && sub == 0;
 }
 
-// Gradient of one warp's tokens; returns d_t in each lane that leads a group.
+// A lane's logits of token t (-inf where it does not count), and whether it does.
 template <typename T, int L, int V>
-__device__ __forceinline__ float gradient(const BalanceParams &p, int w, int64_t t, int sub, const float (&c)[V], float coef) {
-    const bool here = t < p.tokens;
-    bool live = here && (!p.has_valid || p.valid[w][t] != 0);
-    float v[V];
+__device__ __forceinline__ bool fetch(const BalanceParams &p, int w, int64_t t, int sub, Runs<T, V> &g) {
+    const bool live = t < p.tokens && (!p.has_valid || p.valid[w][t] != 0);
     if (live) {
-        load_token<T, L, V>(static_cast<const T *>(p.z[w]) + t * p.ldz, sub, p.experts, p.wide, v);
+        load_runs<T, L, V>(static_cast<const T *>(p.z[w]) + t * p.ldz, sub, p.experts, p.wide, g);
     } else {
+        constexpr uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = -INFINITY;
+        for (uint4 &r : g) r = make_uint4(none, none, none, none);
     }
+    return live;
+}
+// Gradient of one warp's tokens, from their logits; returns d_t in each lane that leads a group.
+template <typename T, int L, int V>
+__device__ __forceinline__ float gradient(const BalanceParams &p, int w, int64_t t, int sub, const Runs<T, V> &g, bool live,
+                                          const float (&c)[V], float coef) {
+    const bool here = t < p.tokens;
+    float v[V];
+    unpack_runs<T, V>(g, v);
     float m = v[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
@@ -405,7 +437,7 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_co
 }
 
 template <typename T, int L, int V>
-__global__ void __launch_bounds__(kThreads) balance_grad_kernel(const __grid_constant__ BalanceParams p) {
+__global__ void __launch_bounds__(kThreads, V == 32 ? 2 : 1) balance_grad_kernel(const __grid_constant__ BalanceParams p) {
     __shared__ int32_t all[kMaxExperts];
     __shared__ float dsum[kWarps];
     __shared__ int64_t isum[kWarps];
@@ -436,8 +468,16 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(const __grid_con
     // backwards: what the counting pass read last is still in L2
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps * kPerWarp;
     const int64_t own = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kPerWarp;
-    for (int64_t t0 = own + (p.tokens - 1 - own) / stride * stride; own < p.tokens && t0 >= 0; t0 -= stride)
-        sum += gradient<T, L, V>(p, w, t0 + lane / L, sub, c, coef);
+    int64_t t = own < p.tokens ? own + (p.tokens - 1 - own) / stride * stride : -1;
+    Runs<T, V> g, coming;
+    bool live = t >= 0 && fetch<T, L, V>(p, w, t + lane / L, sub, g), live_next = false;
+    for (; t >= 0; t -= stride) {  // the next tokens' logits on their way while these are worked on
+        if (t >= stride) live_next = fetch<T, L, V>(p, w, t - stride + lane / L, sub, coming);
+        sum += gradient<T, L, V>(p, w, t + lane / L, sub, g, live, c, coef);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(V * sizeof(T) / 16); ++i) g[i] = coming[i];
+        live = live_next;
+    }
     sum = group_sum<32>(sum);
     if (lane == 0) dsum[warp] = sum;
     __syncthreads();
@@ -523,7 +563,10 @@ __global__ void __launch_bounds__(kOneThreads) balance_one_kernel(const __grid_c
     float sum = 0.0f;
     for (int i = warp * C + rank; i < items; i += warps * C) {
         const int w = i / chunks;
-        sum += gradient<T, L, V>(p, w, static_cast<int64_t>(i - w * chunks) * kPerWarp + lane / L, sub, c, coef);
+        const int64_t t = static_cast<int64_t>(i - w * chunks) * kPerWarp + lane / L;
+        Runs<T, V> g;
+        const bool live = fetch<T, L, V>(p, w, t, sub, g);
+        sum += gradient<T, L, V>(p, w, t, sub, g, live, c, coef);
     }
     sum = group_sum<32>(sum);
     if (lane == 0) dsum[warp] = sum;
