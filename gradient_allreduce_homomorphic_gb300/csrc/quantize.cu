@@ -138,6 +138,13 @@ struct Patch<float> {
     }
 };
 
+// Two bf16 values times two powers of two: exact, or below 2^-126, whose code is 0 either way.
+__device__ __forceinline__ uint32_t scale2(uint32_t x, uint32_t f) {
+    uint32_t y;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f));
+    return y;
+}
+
 // The codes of one tile, both orders.  kBad: the tile has NaN or infinities;
 // fma(y, 0, y f) is y f for finite y and NaN else, whose code is the format's NaN.
 template <typename T, bool kE5M2, bool kBad>
@@ -151,6 +158,20 @@ __device__ __forceinline__ void emit(const QuantizeParams &p, const Patch<T> &v,
     if (p.qt) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+            if constexpr (sizeof(T) == 2 && !kBad) {  // two columns at a time, as they are held
+                if (j & 1) continue;
+                const uint32_t f = pack_bf16x2(inverse_scale(cbyte[j]), inverse_scale(cbyte[j + 1]));
+                uint32_t y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = scale2(v.w[i][j >> 1], f);
+                *reinterpret_cast<uint2 *>(&tile[(hl * 8 + j) * kTile + ((half ^ hl) << 3)]) =
+                    make_uint2(pack4<kE5M2>(bf16_lo(y[0]), bf16_lo(y[1]), bf16_lo(y[2]), bf16_lo(y[3])),
+                               pack4<kE5M2>(bf16_lo(y[4]), bf16_lo(y[5]), bf16_lo(y[6]), bf16_lo(y[7])));
+                *reinterpret_cast<uint2 *>(&tile[(hl * 8 + j + 1) * kTile + ((half ^ hl) << 3)]) =
+                    make_uint2(pack4<kE5M2>(bf16_hi(y[0]), bf16_hi(y[1]), bf16_hi(y[2]), bf16_hi(y[3])),
+                               pack4<kE5M2>(bf16_hi(y[4]), bf16_hi(y[5]), bf16_hi(y[6]), bf16_hi(y[7])));
+                continue;
+            }
             const float f = inverse_scale(cbyte[j]);
             uint2 w;
             w.x = pack4<kE5M2>(scaled(0, j, f), scaled(1, j, f), scaled(2, j, f), scaled(3, j, f));
@@ -170,8 +191,17 @@ __device__ __forceinline__ void emit(const QuantizeParams &p, const Patch<T> &v,
             const int64_t r = row0 + i;
             const float f = inverse_scale(rbyte[i]);
             uint2 w;
-            w.x = pack4<kE5M2>(scaled(i, 0, f), scaled(i, 1, f), scaled(i, 2, f), scaled(i, 3, f));
-            w.y = pack4<kE5M2>(scaled(i, 4, f), scaled(i, 5, f), scaled(i, 6, f), scaled(i, 7, f));
+            if constexpr (sizeof(T) == 2 && !kBad) {
+                const uint32_t ff = pack_bf16x2(f, f);
+                uint32_t y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = scale2(v.w[i][j], ff);
+                w.x = pack4<kE5M2>(bf16_lo(y[0]), bf16_hi(y[0]), bf16_lo(y[1]), bf16_hi(y[1]));
+                w.y = pack4<kE5M2>(bf16_lo(y[2]), bf16_hi(y[2]), bf16_lo(y[3]), bf16_hi(y[3]));
+            } else {
+                w.x = pack4<kE5M2>(scaled(i, 0, f), scaled(i, 1, f), scaled(i, 2, f), scaled(i, 3, f));
+                w.y = pack4<kE5M2>(scaled(i, 4, f), scaled(i, 5, f), scaled(i, 6, f), scaled(i, 7, f));
+            }
             if (r < p.rows) {
                 uint8_t *dst = p.q + r * p.ldq + col0;
                 if (left >= 8) {
@@ -198,8 +228,8 @@ __device__ __forceinline__ void emit(const QuantizeParams &p, const Patch<T> &v,
 // per tile tells) takes its maxima again without them.
 //
 // Bound by HBM traffic that a tile's phases (load, maxima, store) leave gaps in;
-// the SM's other tiles fill most of them.  16384 x 8192, both orders: bf16 105 us,
-// 5.1 TB/s (three CTAs an SM 108 us; 98 us with square blocks, which exchange less);
+// the SM's other tiles fill most of them.  16384 x 8192, both orders: bf16 103 us,
+// 5.2 TB/s (three CTAs an SM 106 us; 97 us with square blocks, which exchange less);
 // fp32 153 us, 5.3 TB/s.  Two orders by two launches would read x twice.
 template <typename T, bool kE5M2>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quantize_kernel(const __grid_constant__ QuantizeParams p) {
