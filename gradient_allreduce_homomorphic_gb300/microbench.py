@@ -17,7 +17,10 @@ table on a granularity-g grid), nmse, train_step, train_step_fused (one step
 of THC's training process over P workers: error feedback, rotation, range,
 non-uniform THC, inverse rotation, error-feedback update; separate calls, or
 the fused ones as training.TrainingStep runs them, the workers' chains over
---streams side streams).  Inputs are seeded N(0, 1) draws made on the device;
+--streams side streams), and the operators that a worker's gradients come from: fp8_quantize (--rows x --cols values,
+both orders), fp8_matmul (--rows x --cols, summed over --depth), distill and distill_split (--rows of --cols logits,
+--k teacher entries: loss and gradient in one call or two), balance (--P workers of --rows tokens and --cols experts,
+--k choices).  Inputs are seeded N(0, 1) draws made on the device;
 every size is chosen by the caller, so a case can be kept small enough for a
 profiler capture.  Prints one JSON line: time per call (CUDA events on the
 launching stream, after warm-up) and algorithmic GB/s.
@@ -51,7 +54,11 @@ def main(argv=None):
     ap.add_argument("--warmup", type=int, default=3)
     ap.add_argument("--dtype", default="f32")
     ap.add_argument("--g", type=int, default=0, help="granularity for the nuhc cases")
-    ap.add_argument("--k", type=int, default=64, help="partitions of the stream cases")
+    ap.add_argument("--k", type=int, default=64,
+                    help="partitions of the stream cases, teacher entries of distill, choices of balance")
+    ap.add_argument("--rows", type=int, default=4096)
+    ap.add_argument("--cols", type=int, default=8192)
+    ap.add_argument("--depth", type=int, default=2048, help="fp8_matmul: the summed axis")
     ap.add_argument("--streams", type=int, default=2,
                     help="train_step_fused: side streams the workers' chains go round-robin over")
     ap.add_argument("--flush", action="store_true",
@@ -61,6 +68,7 @@ def main(argv=None):
     torch.cuda.set_device(dev)
     g.load()
     P, N, b = a.P, a.N, a.b
+    flops = 0
     tdt = torch.float32 if a.dtype == "f32" else torch.bfloat16
     es = 4 if a.dtype == "f32" else 2
 
@@ -281,6 +289,50 @@ def main(argv=None):
         out = torch.empty(1, dtype=torch.int64, device=dev)
         fn = lambda: g.gar_checksum(w, out)  # noqa: E731
         nbytes = N * 4
+    elif a.case in ("fp8_quantize", "fp8_matmul", "distill", "distill_split", "balance"):
+        dt, size, rows, cols = tdt, es, a.rows, a.cols
+        if a.case == "fp8_quantize":
+            # algorithmic bytes: x read once, both orders' codes written, and their scales
+            x = torch.randn((rows, cols), device=dev).to(dt)
+            q, sc = g.fp8_matrix(rows, cols)
+            qt, st = g.fp8_matrix(cols, rows)
+            fn = lambda: g.gar_fp8_quantize(x, q, sc, qt, st)  # noqa: E731
+            nbytes = rows * cols * (size + 2) + sc.numel() + st.numel()
+        elif a.case == "fp8_matmul":
+            # algorithmic bytes: both operands read, the product written
+            qs = []
+            for r in (rows, cols):
+                q, sc = g.fp8_matrix(r, a.depth)
+                g.gar_fp8_quantize(torch.randn((r, a.depth), device=dev), q, sc)
+                qs += [q, sc]
+            d = torch.empty((rows, cols), dtype=dt, device=dev)
+            fn = lambda: g.gar_fp8_matmul(*qs, d)  # noqa: E731
+            nbytes = (rows + cols) * a.depth + rows * cols * size
+            flops = 2 * rows * cols * a.depth
+        elif a.case == "balance":
+            # algorithmic bytes: logits read once, their gradient and the choices written
+            zs = [torch.randn((rows, cols), device=dev).to(dt) for _ in range(P)]
+            choice = [torch.empty((rows, a.k), dtype=torch.int32, device=dev) for _ in range(P)]
+            counts = torch.empty((P, cols), dtype=torch.int32, device=dev)
+            loss = torch.empty(1, device=dev)
+            dzs = [torch.empty_like(z) for z in zs]
+            ws = torch.empty(g.gar_balance_workspace_bytes(P), dtype=torch.uint8, device=dev)
+            fn = lambda: g.gar_balance_loss(zs, a.k, 0.01, choice, counts, loss, ws, dz=dzs)  # noqa: E731
+            nbytes = P * rows * (2 * cols * size + 4 * a.k)
+        else:
+            # algorithmic bytes: logits read (twice in two calls), their gradient written
+            z = torch.randn((rows, cols), device=dev).to(dt)
+            dz = torch.empty_like(z)
+            index = torch.randint(0, cols, (rows, a.k), dtype=torch.int32, device=dev)
+            teacher = torch.randn((rows, a.k), device=dev)
+            loss, lse = torch.empty(rows, device=dev), torch.empty(rows, device=dev)
+            if a.case == "distill":
+                fn = lambda: g.gar_distill_loss(z, index, teacher, 1.0, loss, lse, dz=dz)  # noqa: E731
+            else:
+                def fn():
+                    g.gar_distill_loss(z, index, teacher, 1.0, loss, lse)
+                    g.gar_distill_grad(z, index, teacher, 1.0, lse, dz)
+            nbytes = rows * cols * size * (2 if a.case == "distill" else 3)
     else:
         raise SystemExit(f"unknown case {a.case}")
 
@@ -309,9 +361,10 @@ def main(argv=None):
         times.append(s.elapsed_time(e))
     launches = (g.gar_launch_count() - launches0) // max(a.iters, 1)
     ms = float(np.median(times))
+    rate = {"tflops": round(flops / (ms * 1e-3) / 1e12, 1)} if flops else {}
     print(json.dumps({"case": a.case, "P": P, "N": N, "b": b, "dtype": a.dtype, "ms": round(ms, 4),
                       "ms_min": round(float(np.min(times)), 4), "gbs": round(nbytes / (ms * 1e-3) / 1e9, 1),
-                      "bytes": int(nbytes), "launches_per_call": int(launches),
+                      "bytes": int(nbytes), **rate, "launches_per_call": int(launches),
                       "launches_total": int(g.gar_launch_count())}))
 
 
