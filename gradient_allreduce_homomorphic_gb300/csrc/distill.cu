@@ -33,8 +33,9 @@ namespace {
 constexpr int kMaxTop = 1024;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-// bf16 rows with |m c| up to this take (z - m) c as one fma of z, c and the rounded m c, which adds 2^-16 to an exponent
-// at most (2^-17 from rounding m c, as much from rounding the fma): a fraction 1.1e-5 of a probability.
+// bf16 rows with |m c| up to this take (z - m) c as one fma of z, c and the rounded m c.  That adds 2^-16 to an exponent
+// at most, in the sum (2^-17 from rounding m c, as much from rounding the fma: a fraction 1.1e-5 of it), and 2^-15 in the
+// gradient, whose subtrahend has the sum and the weight in it (2.1e-5, where rounding dz to bf16 takes 2e-3).
 constexpr float kPlain = 256.0f;
 
 struct DistillParams {
