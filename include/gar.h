@@ -2,7 +2,7 @@
  * gar.h -- C ABI of the GB300 gradient-averaging library (libgar.so).
  *
  * The library averages the gradients of P data-parallel workers whose
- * buffers all live in one GPU's HBM.  Three parts, each a hand-written
+ * buffers all live in one GPU's HBM.  Four parts, each a hand-written
  * sm_103a CUDA kernel family behind the calls below:
  *
  *   1. Tensor Fusion   -- many small gradient tensors packed into large
@@ -13,6 +13,11 @@
  *   3. Uniform THC     -- shared range, Philox-driven stochastic quantization
  *                         to b-bit indices, integer summation of the indices
  *                         without decompression, one decode to the average.
+ *   4. Worker operators -- what a language model's gradients come from before
+ *                         they are averaged: block-scaled 8-bit quantization
+ *                         and products on the tensor cores, distillation from
+ *                         a teacher's top logits, a router's choices and
+ *                         balance loss over all workers.
  *
  * Sources (cited by page title and section):
  *   [H] "Horovod: Fast and Easy Distributed Deep Learning in TensorFlow"
@@ -81,7 +86,7 @@ typedef enum { GAR_F8E4M3 = 0, GAR_F8E5M2 = 1 } gar_f8_format;
 /* Bits of the device status word (gar_sync_status). */
 typedef enum {
     GAR_STATUS_NONFINITE = 1, /* a THC range pass saw a NaN or an infinite input */
-    GAR_STATUS_TIMEOUT = 2    /* a wait inside gar_fp8_matmul ran out: its result is not valid */
+    GAR_STATUS_TIMEOUT = 2    /* a wait inside a kernel ran out (gar_sync_status): that call's result is not valid */
 } gar_device_status;
 typedef enum { GAR_SUM = 0, GAR_AVG = 1 } gar_op;
 
@@ -219,8 +224,10 @@ int gar_checksum(const uint32_t *d_words, int64_t n, uint64_t *d_out, gar_stream
  * range) saw a NaN or an infinite input; the range skips NaN and takes
  * infinities in, so the quantization of such a round is meaningless.  The
  * word is set to 0 when clear != 0.  Kernels queued on other streams may set
- * bits at any time.  No kernel of this library waits on a flag or a peer, so
- * there is no timeout condition to report.
+ * bits at any time.  GAR_STATUS_TIMEOUT: a wait for a copy or for another
+ * part of the same kernel (gar_fp8_matmul, gar_distill_loss,
+ * gar_distill_grad) ran out of its two seconds; the kernel ended all the same
+ * and its result is not valid.  No kernel waits for another kernel or a host.
  * Errors: GAR_EINVAL (status NULL), GAR_ECUDA. */
 int gar_sync_status(gar_stream_t stream, uint32_t *status, int32_t clear);
 
@@ -731,7 +738,9 @@ int gar_fp8_matmul(const uint8_t *a, int64_t lda, const uint8_t *a_scale, int32_
  *   loss, lse    device, out, [rows] fp32
  *   dz           device, out, of z's type, row stride lddz; NULL: loss only;
  *                may be z itself (same row stride)
- * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA. */
+ * loss and lse do not depend on whether dz is asked for, nor on timing.
+ * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA; on the device
+ * GAR_STATUS_TIMEOUT. */
 int gar_distill_loss(const void *z, int32_t dtype, int64_t rows, int64_t vocab, int64_t ldz, const int32_t *index,
                      const float *teacher, int32_t k, float tau, const float *weight, float *loss, float *lse,
                      void *dz, int64_t lddz, gar_stream_t stream);
