@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(stream_threads(kMode, sizeof(T)), 2) distill_s
                     const float *top_p = reinterpret_cast<const float *>(top_i + entries), *top_z = top_p + entries;
                     for (int j = tid; j < p.k; j += kThreads) {
                         const int32_t i = top_i[j];
-                        if (i < 0 || !part.holds(i, rank)) continue;
+                        if (i < 0 || i >= p.vocab || !part.holds(i, rank)) continue;  // (a slot that never came holds anything)
                         float sum = top_p[j];
                         if (h.repeated) {
                             sum = 0.0f;
