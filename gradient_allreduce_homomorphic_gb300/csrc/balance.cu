@@ -126,12 +126,6 @@ __device__ __forceinline__ void unpack_runs(const Runs<T, V> &g, float (&v)[V]) 
     }
 }
 template <typename T, int L, int V>
-__device__ __forceinline__ void load_token(const T *z, int sub, int experts, bool wide, float (&v)[V]) {
-    Runs<T, V> g;
-    load_runs<T, L, V>(z, sub, experts, wide, g);
-    unpack_runs<T, V>(g, v);
-}
-template <typename T, int L, int V>
 __device__ __forceinline__ void store_token(T *dz, int sub, int experts, bool wide, const float (&v)[V]) {
     constexpr int kRun = 16 / sizeof(T);
 #pragma unroll
@@ -270,21 +264,30 @@ __device__ __forceinline__ bool choose_by_bound(const float (&v)[32], const T *z
     return good;
 }
 
-// Choices of the tokens of one warp; adds to cnt (shared memory) and returns,
-// in each lane that leads a group, whether its token counts.
+// A lane's logits of token t (-inf where it does not count), and whether it does.
 template <typename T, int L, int V>
-__device__ __forceinline__ bool choose(const BalanceParams &p, int w, int64_t t, int sub, int lane, int32_t *cnt, uint64_t *list) {
-    const bool here = t < p.tokens, live = here && (!p.has_valid || p.valid[w][t] != 0);
+__device__ __forceinline__ bool fetch(const BalanceParams &p, int w, int64_t t, int sub, Runs<T, V> &g) {
+    const bool live = t < p.tokens && (!p.has_valid || p.valid[w][t] != 0);
+    if (live) {
+        load_runs<T, L, V>(static_cast<const T *>(p.z[w]) + t * p.ldz, sub, p.experts, p.wide, g);
+    } else {
+        constexpr uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+#pragma unroll
+        for (uint4 &r : g) r = make_uint4(none, none, none, none);
+    }
+    return live;
+}
+// Choices of the tokens of one warp, from their logits; adds to cnt (shared
+// memory) and returns, in each lane that leads a group, whether its token counts.
+template <typename T, int L, int V>
+__device__ __forceinline__ bool choose(const BalanceParams &p, int w, int64_t t, int sub, int lane, const Runs<T, V> &g, bool live,
+                                       int32_t *cnt, uint64_t *list) {
+    const bool here = t < p.tokens;
     int32_t *out = here ? p.choice[w] + t * p.k : nullptr;
     const T *z = static_cast<const T *>(p.z[w]) + (live ? t : 0) * p.ldz;
     float v[V];
-    if (live) {
-        load_token<T, L, V>(z, sub, p.experts, p.wide, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = -INFINITY;
-        for (int c = sub; here && c < p.k; c += L) out[c] = -1;
-    }
+    unpack_runs<T, V>(g, v);
+    for (int c = sub; here && !live && c < p.k; c += L) out[c] = -1;
     float m = v[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
@@ -305,19 +308,6 @@ __device__ __forceinline__ bool choose(const BalanceParams &p, int w, int64_t t,
     return some && sub == 0;
 }
 
-// A lane's logits of token t (-inf where it does not count), and whether it does.
-template <typename T, int L, int V>
-__device__ __forceinline__ bool fetch(const BalanceParams &p, int w, int64_t t, int sub, Runs<T, V> &g) {
-    const bool live = t < p.tokens && (!p.has_valid || p.valid[w][t] != 0);
-    if (live) {
-        load_runs<T, L, V>(static_cast<const T *>(p.z[w]) + t * p.ldz, sub, p.experts, p.wide, g);
-    } else {
-        constexpr uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
-#pragma unroll
-        for (uint4 &r : g) r = make_uint4(none, none, none, none);
-    }
-    return live;
-}
 // Gradient of one warp's tokens, from their logits; returns d_t in each lane that leads a group.
 template <typename T, int L, int V>
 __device__ __forceinline__ float gradient(const BalanceParams &p, int w, int64_t t, int sub, const Runs<T, V> &g, bool live,
@@ -390,7 +380,7 @@ __device__ __forceinline__ float centred(int32_t count, int64_t choices, int exp
 // counts; else the counts are zeroed by a kernel ahead and added with atomics
 // (integers: their order does not matter).  The counting kernel reads z before
 // it waits for the zeroing one, which lets it begin only once the kernels ahead
-// of both are done.
+// of both are done, and so does the gradient's kernel with its first tokens.
 __global__ void __launch_bounds__(kThreads) balance_zero_kernel(int32_t *counts, int n, uint32_t *seen, int workers) {
     after_previous();
     let_next_begin();
@@ -409,14 +399,30 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_co
     if (threadIdx.x == 0) seen = 0;
     __syncthreads();
     if (kTogether) {
-        let_next_begin();
         after_previous();
+        let_next_begin();
     }
     constexpr int kPerWarp = 32 / L;
     uint32_t mine = 0;
-    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kPerWarp; t0 < p.tokens;
-         t0 += static_cast<int64_t>(gridDim.x) * kWarps * kPerWarp)
-        mine += choose<T, L, V>(p, w, t0 + lane / L, sub, lane, cnt, list[L >= 4 && V == 32 ? warp : 0]);
+    int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kPerWarp + lane / L;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps * kPerWarp;
+    Runs<T, V> g;
+    if constexpr (V == 32) {
+        for (; t - lane / L < p.tokens; t += stride) {
+            const bool live = fetch<T, L, V>(p, w, t, sub, g);
+            mine += choose<T, L, V>(p, w, t, sub, lane, g, live, cnt, list[L >= 4 ? warp : 0]);
+        }
+    } else {  // few registers a token: the next tokens' logits come while these are worked on
+        Runs<T, V> coming;
+        bool live = fetch<T, L, V>(p, w, t, sub, g);
+        for (; t - lane / L < p.tokens; t += stride) {
+            const bool live_next = fetch<T, L, V>(p, w, t + stride, sub, coming);
+            mine += choose<T, L, V>(p, w, t, sub, lane, g, live, cnt, list[0]);
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(V * sizeof(T) / 16); ++i) g[i] = coming[i];
+            live = live_next;
+        }
+    }
     mine = __reduce_add_sync(0xFFFFFFFFu, mine);
     if (lane == 0 && mine) atomicAdd(&seen, mine);
     __syncthreads();
@@ -453,6 +459,13 @@ __global__ void __launch_bounds__(kThreads, V == 32 ? 2 : 1) balance_grad_kernel
     __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = blockIdx.y, sub = lane & (L - 1);
     let_next_begin();
+    constexpr int kPerWarp = 32 / L;
+    // backwards: what the counting pass read last is still in L2
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps * kPerWarp;
+    const int64_t own = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kPerWarp;
+    int64_t t = own < p.tokens ? own + (p.tokens - 1 - own) / stride * stride : -1;
+    Runs<T, V> g, coming;
+    bool live = t >= 0 && fetch<T, L, V>(p, w, t + lane / L, sub, g), live_next = false;
     after_previous();
     int64_t n = 0;
     for (int i = 0; i < p.P; ++i) n += p.seen[1 + i];
@@ -471,14 +484,7 @@ __global__ void __launch_bounds__(kThreads, V == 32 ? 2 : 1) balance_grad_kernel
         const int e = expert<T, L>(sub, i);
         c[i] = e < p.experts ? centred(all[e], choices, p.experts) : 0.0f;
     }
-    constexpr int kPerWarp = 32 / L;
     float sum = 0.0f;
-    // backwards: what the counting pass read last is still in L2
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps * kPerWarp;
-    const int64_t own = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kPerWarp;
-    int64_t t = own < p.tokens ? own + (p.tokens - 1 - own) / stride * stride : -1;
-    Runs<T, V> g, coming;
-    bool live = t >= 0 && fetch<T, L, V>(p, w, t + lane / L, sub, g), live_next = false;
     for (; t >= 0; t -= stride) {  // the next tokens' logits on their way while these are worked on
         if (t >= stride) live_next = fetch<T, L, V>(p, w, t - stride + lane / L, sub, coming);
         sum += gradient<T, L, V>(p, w, t + lane / L, sub, g, live, c, coef);
@@ -536,7 +542,10 @@ __global__ void __launch_bounds__(kOneThreads) balance_one_kernel(const __grid_c
     int64_t n = 0;
     for (int i = warp * C + rank; i < items; i += warps * C) {
         const int w = i / chunks;
-        n += choose<T, L, V>(p, w, static_cast<int64_t>(i - w * chunks) * kPerWarp + lane / L, sub, lane, cnt + w * E, nullptr);
+        const int64_t t = static_cast<int64_t>(i - w * chunks) * kPerWarp + lane / L;
+        Runs<T, V> g;
+        const bool live = fetch<T, L, V>(p, w, t, sub, g);
+        n += choose<T, L, V>(p, w, t, sub, lane, g, live, cnt + w * E, nullptr);
     }
     n = cta_count(n, isum);
     if (C > 1) {
