@@ -21,11 +21,10 @@
 // once, each load's wait would hold up the next (8 workers of 16384 tokens and
 // 256 bf16 experts: 93 us, 69 so).
 //
-// 8 x 16384 x 256 fp32, 8 choices: 86 us, of which the counting pass 40 (the
+// 8 x 16384 x 256 fp32, 8 choices: 84 us, of which the counting pass 40 (the
 // selection's instructions, 714 for a warp's four tokens, issued in 53 % of the
-// cycles) and the gradient 46 (HBM: 4.6 TB/s, its logits read a second
-// time).  Few tokens cost their launches: 4 x 2000 x 60 bf16 18 us a call, 64 x
-// 8 12 us, one launch.
+// cycles) and the gradient 44 (HBM: its logits read a second time).  Few tokens
+// cost their launches: 4 x 2000 x 60 bf16 18 us a call, 64 x 8 12 us, one launch.
 #include <algorithm>
 #include <atomic>
 
@@ -52,7 +51,7 @@ struct BalanceParams {
     const uint8_t *valid[GAR_MAX_WORKERS];
     int64_t tokens, ldz, lddz;
     int32_t P, experts, k, has_valid, has_grad;
-    int32_t wide, dwide; // whether rows of z, of dz may be accessed 16 bytes at a time
+    int32_t align, dalign;  // every row of z, of dz starts on that many bytes (2 to 16)
     float alpha;
     int32_t *counts;     // [P, experts]
     uint32_t *seen;      // workspace: CTAs done; each worker's tokens that count
@@ -88,26 +87,39 @@ __device__ __forceinline__ int expert(int sub, int i) {
 // A lane's logits of one token as they are stored, a run in each; -inf past the last expert.
 template <typename T, int V>
 using Runs = uint4[V * sizeof(T) / 16];
-template <typename T, int L, int V>
-__device__ __forceinline__ void load_runs(const T *z, int sub, int experts, bool wide, Runs<T, V> &g) {
-    constexpr int kRun = 16 / sizeof(T);
+// kWide: all rows start on 16 bytes.  Else (`align`: on how many they do), and
+// where the last expert cuts a run, it is accessed in the largest pieces that fit.
+template <typename T, int L, int V, bool kWide>
+__device__ __forceinline__ void load_runs(const T *z, int sub, int experts, int align, Runs<T, V> &g) {
+    constexpr int kRun = 16 / sizeof(T), kWord = 4 / sizeof(T);
 #pragma unroll
     for (int r = 0; r < V / kRun; ++r) {
         const int e0 = expert<T, L>(sub, r * kRun);
-        if (wide && e0 + kRun <= experts) {
+        if ((kWide || align == 16) && e0 + kRun <= experts) {
             g[r] = *reinterpret_cast<const uint4 *>(z + e0);
-        } else {
-            uint32_t x[4];
-            if constexpr (sizeof(T) == 2) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    x[j] = (e0 + 2 * j < experts ? z[e0 + 2 * j] : 0xFF80u) | (e0 + 2 * j + 1 < experts ? z[e0 + 2 * j + 1] : 0xFF80u) << 16;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = e0 + j < experts ? __float_as_uint(z[e0 + j]) : 0xFF800000u;
-            }
-            g[r] = make_uint4(x[0], x[1], x[2], x[3]);
+            continue;
         }
+        uint32_t x[4];
+#pragma unroll
+        for (int h = 0; h < 4; h += 2) {
+            const int e1 = e0 + h * kWord;
+            if (!kWide && align >= 8 && e1 + 2 * kWord <= experts) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(z + e1);
+                x[h] = u.x, x[h + 1] = u.y;
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int e = e1 + j * kWord;
+                if ((kWide || align >= 4) && e + kWord <= experts)
+                    x[h + j] = *reinterpret_cast<const uint32_t *>(z + e);
+                else if constexpr (sizeof(T) == 2)
+                    x[h + j] = (e < experts ? z[e] : 0xFF80u) | (e + 1 < experts ? z[e + 1] : 0xFF80u) << 16;
+                else
+                    x[h + j] = 0xFF800000u;
+            }
+        }
+        g[r] = make_uint4(x[0], x[1], x[2], x[3]);
     }
 }
 template <typename T, int V>
@@ -125,24 +137,41 @@ __device__ __forceinline__ void unpack_runs(const Runs<T, V> &g, float (&v)[V]) 
         }
     }
 }
-template <typename T, int L, int V>
-__device__ __forceinline__ void store_token(T *dz, int sub, int experts, bool wide, const float (&v)[V]) {
-    constexpr int kRun = 16 / sizeof(T);
+template <typename T, int L, int V, bool kWide>
+__device__ __forceinline__ void store_token(T *dz, int sub, int experts, int align, const float (&v)[V]) {
+    constexpr int kRun = 16 / sizeof(T), kWord = 4 / sizeof(T);
 #pragma unroll
     for (int r = 0; r < V; r += kRun) {
         const int e0 = expert<T, L>(sub, r);
-        if (wide && e0 + kRun <= experts) {
-            uint4 g;
-            if constexpr (sizeof(T) == 2)
-                g = make_uint4(pack_bf16x2(v[r], v[r + 1]), pack_bf16x2(v[r + 2], v[r + 3]), pack_bf16x2(v[r + 4], v[r + 5]),
-                               pack_bf16x2(v[r + 6], v[r + 7]));
-            else
-                g = make_uint4(__float_as_uint(v[r]), __float_as_uint(v[r + 1]), __float_as_uint(v[r + 2]), __float_as_uint(v[r + 3]));
-            st16(dz + e0, g);  // streaming: z, which is read again, is worth more in L2
-        } else {
+        uint32_t x[4];
 #pragma unroll
-            for (int j = 0; j < kRun; ++j)
-                if (e0 + j < experts) store_f32(dz + e0 + j, v[r + j]);
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (sizeof(T) == 2)
+                x[j] = pack_bf16x2(v[r + 2 * j], v[r + 2 * j + 1]);
+            else
+                x[j] = __float_as_uint(v[r + j]);
+        }
+        if ((kWide || align == 16) && e0 + kRun <= experts) {
+            st16(dz + e0, make_uint4(x[0], x[1], x[2], x[3]));  // streaming: z, which is read again, is worth more in L2
+            continue;
+        }
+#pragma unroll
+        for (int h = 0; h < 4; h += 2) {
+            const int e1 = e0 + h * kWord;
+            if (!kWide && align >= 8 && e1 + 2 * kWord <= experts) {
+                *reinterpret_cast<uint2 *>(dz + e1) = make_uint2(x[h], x[h + 1]);
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int e = e1 + j * kWord;
+                if ((kWide || align >= 4) && e + kWord <= experts) {
+                    *reinterpret_cast<uint32_t *>(dz + e) = x[h + j];
+                } else if constexpr (sizeof(T) == 2) {
+                    if (e < experts) dz[e] = static_cast<uint16_t>(x[h + j]);
+                    if (e + 1 < experts) dz[e + 1] = static_cast<uint16_t>(x[h + j] >> 16);
+                }
+            }
         }
     }
 }
@@ -265,11 +294,11 @@ __device__ __forceinline__ bool choose_by_bound(const float (&v)[32], const T *z
 }
 
 // A lane's logits of token t (-inf where it does not count), and whether it does.
-template <typename T, int L, int V>
+template <typename T, int L, int V, bool kWide>
 __device__ __forceinline__ bool fetch(const BalanceParams &p, int w, int64_t t, int sub, Runs<T, V> &g) {
     const bool live = t < p.tokens && (!p.has_valid || p.valid[w][t] != 0);
     if (live) {
-        load_runs<T, L, V>(static_cast<const T *>(p.z[w]) + t * p.ldz, sub, p.experts, p.wide, g);
+        load_runs<T, L, V, kWide>(static_cast<const T *>(p.z[w]) + t * p.ldz, sub, p.experts, p.align, g);
     } else {
         constexpr uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
 #pragma unroll
@@ -309,7 +338,7 @@ __device__ __forceinline__ bool choose(const BalanceParams &p, int w, int64_t t,
 }
 
 // Gradient of one warp's tokens, from their logits; returns d_t in each lane that leads a group.
-template <typename T, int L, int V>
+template <typename T, int L, int V, bool kWide>
 __device__ __forceinline__ float gradient(const BalanceParams &p, int w, int64_t t, int sub, const Runs<T, V> &g, bool live,
                                           const float (&c)[V], float coef) {
     const bool here = t < p.tokens;
@@ -341,7 +370,7 @@ __device__ __forceinline__ float gradient(const BalanceParams &p, int w, int64_t
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] *= fmaf(f, c[i], -fd);
-        store_token<T, L, V>(static_cast<T *>(p.dz[w]) + t * p.lddz, sub, p.experts, p.dwide, v);
+        store_token<T, L, V, kWide>(static_cast<T *>(p.dz[w]) + t * p.lddz, sub, p.experts, p.dalign, v);
     }
     return sub == 0 ? d : 0.0f;
 }
@@ -389,7 +418,7 @@ __global__ void __launch_bounds__(kThreads) balance_zero_kernel(int32_t *counts,
     if (i <= workers) seen[i] = 0;
 }
 
-template <typename T, int L, int V, bool kTogether>
+template <typename T, int L, int V, bool kTogether, bool kWide>
 __global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_constant__ BalanceParams p) {
     __shared__ int32_t cnt[kMaxExperts];
     __shared__ uint64_t list[L >= 4 && V == 32 ? kWarps : 1][32 / L * kList];
@@ -409,14 +438,14 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_co
     Runs<T, V> g;
     if constexpr (V == 32) {
         for (; t - lane / L < p.tokens; t += stride) {
-            const bool live = fetch<T, L, V>(p, w, t, sub, g);
+            const bool live = fetch<T, L, V, kWide>(p, w, t, sub, g);
             mine += choose<T, L, V>(p, w, t, sub, lane, g, live, cnt, list[L >= 4 ? warp : 0]);
         }
     } else {  // few registers a token: the next tokens' logits come while these are worked on
         Runs<T, V> coming;
-        bool live = fetch<T, L, V>(p, w, t, sub, g);
+        bool live = fetch<T, L, V, kWide>(p, w, t, sub, g);
         for (; t - lane / L < p.tokens; t += stride) {
-            const bool live_next = fetch<T, L, V>(p, w, t + stride, sub, coming);
+            const bool live_next = fetch<T, L, V, kWide>(p, w, t + stride, sub, coming);
             mine += choose<T, L, V>(p, w, t, sub, lane, g, live, cnt, list[0]);
 #pragma unroll
             for (int i = 0; i < static_cast<int>(V * sizeof(T) / 16); ++i) g[i] = coming[i];
@@ -450,7 +479,7 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_co
     }
 }
 
-template <typename T, int L, int V>
+template <typename T, int L, int V, bool kWide>
 __global__ void __launch_bounds__(kThreads, V == 32 ? 2 : 1) balance_grad_kernel(const __grid_constant__ BalanceParams p) {
     __shared__ int32_t all[kMaxExperts];
     __shared__ float dsum[kWarps];
@@ -465,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, V == 32 ? 2 : 1) balance_grad_kernel
     const int64_t own = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kPerWarp;
     int64_t t = own < p.tokens ? own + (p.tokens - 1 - own) / stride * stride : -1;
     Runs<T, V> g, coming;
-    bool live = t >= 0 && fetch<T, L, V>(p, w, t + lane / L, sub, g), live_next = false;
+    bool live = t >= 0 && fetch<T, L, V, kWide>(p, w, t + lane / L, sub, g), live_next = false;
     after_previous();
     int64_t n = 0;
     for (int i = 0; i < p.P; ++i) n += p.seen[1 + i];
@@ -486,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, V == 32 ? 2 : 1) balance_grad_kernel
     }
     float sum = 0.0f;
     for (; t >= 0; t -= stride) {  // the next tokens' logits on their way while these are worked on
-        if (t >= stride) live_next = fetch<T, L, V>(p, w, t - stride + lane / L, sub, coming);
-        sum += gradient<T, L, V>(p, w, t + lane / L, sub, g, live, c, coef);
+        if (t >= stride) live_next = fetch<T, L, V, kWide>(p, w, t - stride + lane / L, sub, coming);
+        sum += gradient<T, L, V, kWide>(p, w, t + lane / L, sub, g, live, c, coef);
 #pragma unroll
         for (int i = 0; i < static_cast<int>(V * sizeof(T) / 16); ++i) g[i] = coming[i];
         live = live_next;
@@ -521,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, V == 32 ? 2 : 1) balance_grad_kernel
 // Few tokens: everything in one cluster of up to 16 CTAs (one launch, and its
 // barriers, cost less than three launches).  The CTAs' counts and sums meet in
 // distributed shared memory; every CTA adds them in rank order.
-template <typename T, int L, int V>
+template <typename T, int L, int V, bool kWide>
 __global__ void __launch_bounds__(kOneThreads) balance_one_kernel(const __grid_constant__ BalanceParams p) {
     constexpr int threads = kOneThreads, warps = threads / 32;
     __shared__ int32_t cnt[kOneCounts];
@@ -544,7 +573,7 @@ __global__ void __launch_bounds__(kOneThreads) balance_one_kernel(const __grid_c
         const int w = i / chunks;
         const int64_t t = static_cast<int64_t>(i - w * chunks) * kPerWarp + lane / L;
         Runs<T, V> g;
-        const bool live = fetch<T, L, V>(p, w, t, sub, g);
+        const bool live = fetch<T, L, V, kWide>(p, w, t, sub, g);
         n += choose<T, L, V>(p, w, t, sub, lane, g, live, cnt + w * E, nullptr);
     }
     n = cta_count(n, isum);
@@ -582,8 +611,8 @@ __global__ void __launch_bounds__(kOneThreads) balance_one_kernel(const __grid_c
         const int w = i / chunks;
         const int64_t t = static_cast<int64_t>(i - w * chunks) * kPerWarp + lane / L;
         Runs<T, V> g;
-        const bool live = fetch<T, L, V>(p, w, t, sub, g);
-        sum += gradient<T, L, V>(p, w, t, sub, g, live, c, coef);
+        const bool live = fetch<T, L, V, kWide>(p, w, t, sub, g);
+        sum += gradient<T, L, V, kWide>(p, w, t, sub, g, live, c, coef);
     }
     sum = group_sum<32>(sum);
     if (lane == 0) dsum[warp] = sum;
@@ -633,8 +662,8 @@ bool wide_clusters(Kernel kernel, unsigned threads, std::atomic<int> *known) {
     return have == 1;
 }
 
-template <typename T, int L, int V>
-int launch(const BalanceParams &p, cudaStream_t stream) {
+template <typename T, int L, int V, bool kWide>
+int launch_as(const BalanceParams &p, cudaStream_t stream) {
     const unsigned P = static_cast<unsigned>(p.P);
     bool together = false;
     unsigned ctas = 1;
@@ -644,14 +673,14 @@ int launch(const BalanceParams &p, cudaStream_t stream) {
         // and 13.5 us; but a launch takes the host 3 us.)
         const int64_t items = ceil_div(p.tokens, int64_t{32 / L});  // of a worker
         if (items * p.P <= 16 * 16 * 2 && p.P * p.experts <= kOneCounts) {
-            const auto kernel = balance_one_kernel<T, L, V>;
+            const auto kernel = balance_one_kernel<T, L, V, kWide>;
             static std::atomic<int> known[64];
             while (ctas < 16 && items * p.P > static_cast<int64_t>(ctas) * 16 * 2) ctas *= 2;
             if (ctas == 16 && !wide_clusters(kernel, kOneThreads, known)) ctas = 8;
             return launch_early("balance_one_kernel", kernel, dim3(ctas), kOneThreads, 0, ctas, stream, p);
         }
         if (items <= 16 * kWarps * 4) {
-            const auto kernel = balance_count_kernel<T, L, V, true>;
+            const auto kernel = balance_count_kernel<T, L, V, true, kWide>;
             static std::atomic<int> known[64];
             while (ctas < 16 && items > static_cast<int64_t>(ctas) * kWarps) ctas *= 2;
             if (ctas == 16 && !wide_clusters(kernel, kThreads, known)) ctas = 8;
@@ -670,11 +699,19 @@ int launch(const BalanceParams &p, cudaStream_t stream) {
         if (int rc = launch_early("balance_zero_kernel", balance_zero_kernel, dim3(static_cast<unsigned>(ceil_div(std::max(n, p.P + 1), kThreads))),
                                   kThreads, 0, 1, stream, p.counts, n, p.seen, p.P))
             return rc;
-        if (int rc = launch_early("balance_count_kernel", balance_count_kernel<T, L, V, false>, dim3(blocks(V == 32 ? 3 : 6), P), kThreads, 0,
+        if (int rc = launch_early("balance_count_kernel", balance_count_kernel<T, L, V, false, kWide>, dim3(blocks(V == 32 ? 3 : 6), P), kThreads, 0,
                                   1, stream, p))
             return rc;
     }
-    return launch_early("balance_grad_kernel", balance_grad_kernel<T, L, V>, dim3(blocks(V == 32 ? 2 : 4), P), kThreads, 0, 1, stream, p);
+    return launch_early("balance_grad_kernel", balance_grad_kernel<T, L, V, kWide>, dim3(blocks(V == 32 ? 2 : 4), P), kThreads, 0, 1, stream, p);
+}
+
+// Kernels for aligned rows alone: 8 x 8192 x 512 fp32 83 us, 105 with the other pieces' code in
+// its way; 8 x 16384 x 250 fp32 (rows on 8 bytes) 104, element by element 123.
+template <typename T, int L, int V>
+int launch(const BalanceParams &p, cudaStream_t stream) {
+    if (p.align == 16 && p.dalign == 16) return launch_as<T, L, V, true>(p, stream);
+    return launch_as<T, L, V, false>(p, stream);
 }
 
 template <typename T>
@@ -691,11 +728,11 @@ int dispatch(const BalanceParams &p, cudaStream_t stream) {
     return launch<T, 32, 32>(p, stream);
 }
 
-// Whether every row of every worker starts on 16 bytes.
-bool wide_rows(const void *const *rows, int P, int64_t ld, int elem) {
-    bool good = ld * elem % 16 == 0;
-    for (int i = 0; i < P; ++i) good = good && aligned(rows[i], 16);
-    return good;
+// How many bytes every row of every worker starts on, 16 at most.
+int rows_align(const void *const *rows, int P, int64_t ld, int elem) {
+    uint64_t bits = static_cast<uint64_t>(ld) * elem | 16;
+    for (int i = 0; i < P; ++i) bits |= reinterpret_cast<uintptr_t>(rows[i]);
+    return static_cast<int>(bits & (~bits + 1));
 }
 
 }  // namespace
@@ -739,8 +776,8 @@ extern "C" int gar_balance_loss(const void *const *z, int32_t P, int64_t tokens,
     p.partial = static_cast<float *>(d_workspace);
     p.seen = reinterpret_cast<uint32_t *>(p.partial + kMaxBlocks);
     if (tokens > 0) {
-        p.wide = wide_rows(p.z, P, ldz, elem_bytes(dtype));
-        p.dwide = dz && wide_rows(p.dz, P, lddz, elem_bytes(dtype));
+        p.align = rows_align(p.z, P, ldz, elem_bytes(dtype));
+        p.dalign = dz ? rows_align(p.dz, P, lddz, elem_bytes(dtype)) : 16;
     }
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     return dtype == GAR_F32 ? dispatch<float>(p, stream) : dispatch<uint16_t>(p, stream);

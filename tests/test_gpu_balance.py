@@ -227,3 +227,30 @@ def test_back_to_back_calls_on_one_workspace(env):
         T, E = sets[i % 3][0].shape
         assert o[1].sum().item() == 2 * T
         assert torch.equal(o[1], outs[i % 3][1]) and torch.equal(o[2], outs[i % 3][2])
+
+
+# rows that start on 2, 4, 8 and 16 bytes (of z and of dz apart), their neighbours untouched; few tokens and many
+@pytest.mark.parametrize("E,T", [(13, 90), (60, 700), (60, 45000), (131, 300), (131, 22000)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_at_every_alignment(env, E, T, dtype):
+    torch, g = env
+    zs = device(torch, logits(1, T, E, 9), dtype)
+    base, k = None, 3
+    for lead, pad, dlead, dpad in ((0, 0, 0, 0), (0, 1, 1, 0), (2, 2, 0, 4), (4, 4, 2, 2), (8, 8, 8, 8), (1, 8, 8, 1)):
+        ld, dld = (E + 7) // 8 * 8 + pad + 8, (E + 7) // 8 * 8 + dpad + 8
+        z = torch.zeros((T, ld), device="cuda", dtype=zs[0].dtype)
+        z[:, lead:lead + E] = zs[0]
+        dz = torch.full((T, dld), 5.0, device="cuda", dtype=z.dtype)
+        choice = torch.full((T, k), 99, dtype=torch.int32, device="cuda")
+        counts, loss = torch.zeros((1, E), dtype=torch.int32, device="cuda"), torch.zeros(1, device="cuda")
+        ws = torch.zeros(g.gar_balance_workspace_bytes(1), dtype=torch.uint8, device="cuda")
+        g.gar_balance_loss([z[:, lead:lead + E]], k, 0.5, [choice], counts, loss, ws, dz=[dz[:, dlead:dlead + E]])
+        torch.cuda.synchronize()
+        got = choice, counts, dz[:, dlead:dlead + E].contiguous()
+        if base is None:
+            base = got
+            if T <= 700:
+                check(torch, g, zs, k)
+        for a, b in zip(got, base):  # the same values, whatever the pieces they were read in
+            assert torch.equal(a, b)
+        assert (dz[:, :dlead] == 5.0).all() and (dz[:, dlead + E:] == 5.0).all()
