@@ -53,6 +53,18 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
+// The words that start `bytes` (0 to 14, even) behind the start of w.
+template <int kWords>
+__device__ __forceinline__ void shift_words(const uint32_t (&w)[kWords + 4], uint32_t bytes, uint32_t (&out)[kWords]) {
+    uint32_t a[kWords + 2], b[kWords + 1];
+#pragma unroll
+    for (int j = 0; j < kWords + 2; ++j) a[j] = bytes & 8 ? w[j + 2] : w[j];
+#pragma unroll
+    for (int j = 0; j < kWords + 1; ++j) b[j] = bytes & 4 ? a[j + 1] : a[j];
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) out[j] = __funnelshift_r(b[j], b[j + 1], (bytes & 2) * 8);
+}
+
 // A thread's 8 rows x 8 columns of x as they are stored, and what both orders
 // need of them.  bf16 values stay packed (32 registers rather than 64): their
 // absolute values compare as unsigned 16-bit integers, two at a time.
@@ -66,6 +78,13 @@ struct Patch<uint16_t> {
     __device__ __forceinline__ void load(int i, const uint16_t *src) {
         const uint4 g = ld16(src);
         w[i][0] = g.x, w[i][1] = g.y, w[i][2] = g.z, w[i][3] = g.w;
+    }
+    // From any address, by the 16-byte lines that hold the values.
+    static constexpr int kLines = 2;
+    __device__ __forceinline__ void load_shifted(int i, const uint4 *line, uint32_t bytes) {
+        const uint4 g = ld16(line), h = ld16(line + 1);
+        const uint32_t x[8] = {g.x, g.y, g.z, g.w, h.x, h.y, h.z, h.w};
+        shift_words<4>(x, bytes, w[i]);
     }
     __device__ __forceinline__ void load_some(int i, const uint16_t *src, int64_t left) {
 #pragma unroll
@@ -113,6 +132,12 @@ struct Patch<float> {
         const uint4 g = ld16(src), h = ld16(src + 4);
         w[i][0] = g.x, w[i][1] = g.y, w[i][2] = g.z, w[i][3] = g.w;
         w[i][4] = h.x, w[i][5] = h.y, w[i][6] = h.z, w[i][7] = h.w;
+    }
+    static constexpr int kLines = 3;
+    __device__ __forceinline__ void load_shifted(int i, const uint4 *line, uint32_t bytes) {
+        const uint4 g = ld16(line), h = ld16(line + 1), k = ld16(line + 2);
+        const uint32_t x[12] = {g.x, g.y, g.z, g.w, h.x, h.y, h.z, h.w, k.x, k.y, k.z, k.w};
+        shift_words<8>(x, bytes, w[i]);
     }
     __device__ __forceinline__ void load_some(int i, const float *src, int64_t left) {
 #pragma unroll
@@ -247,8 +272,22 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quantize_ker
 #pragma unroll
         for (int i = 0; i < 8; ++i) v.load(i, x + i * p.ldx);
     } else {
+        // Rows that start anywhere: by whole lines of 16 bytes and shifts where the lines lie within x (8192 x 4095 bf16 42
+        // us, fp32 56; 48 and 66 value by value), else value by value.
+        const uintptr_t begin = reinterpret_cast<uintptr_t>(p.x);
+        const uintptr_t end = begin + static_cast<uintptr_t>((p.rows - 1) * p.ldx + p.cols) * sizeof(T);
+        const uintptr_t first = reinterpret_cast<uintptr_t>(x) & ~uintptr_t{15};
+        const uintptr_t last = reinterpret_cast<uintptr_t>(x + 7 * p.ldx) & ~uintptr_t{15};
+        if (row0 + 8 <= p.rows && left >= 8 && first >= begin && last + 16 * Patch<T>::kLines <= end) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v.load_some(i, x + i * p.ldx, row0 + i < p.rows ? left : 0);
+            for (int i = 0; i < 8; ++i) {
+                const uintptr_t at = reinterpret_cast<uintptr_t>(x + i * p.ldx);
+                v.load_shifted(i, reinterpret_cast<const uint4 *>(at & ~uintptr_t{15}), static_cast<uint32_t>(at & 15));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v.load_some(i, x + i * p.ldx, row0 + i < p.rows ? left : 0);
+        }
     }
     uint32_t rmax[8], cmax[8];
     v.template maxima<false>(rmax, cmax);

@@ -295,3 +295,16 @@ def test_offsets_beyond_32_bits(env):
     g.gar_fp8_quantize(xs, q, s)
     g.gar_fp8_matmul(q, s, r, t, x)
     check_product(torch, q[m - 200:], s[:, m - 200:], r, t, x[m - 200:])
+
+
+# rows that start anywhere in a line of 16 bytes, at both ends of the matrix and inside it
+@pytest.mark.parametrize("rows,cols", [(8, 8), (130, 263), (257, 129), (64, 1031)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lead,pad", [(0, 0), (0, 1), (1, 0), (3, 2), (5, 3), (7, 9)])
+def test_quantize_rows_that_start_anywhere(env, rows, cols, dtype, lead, pad):
+    torch, g = env
+    x = as_type(torch, values(rows, cols, 31), dtype)
+    flat = torch.full((rows * (cols + lead + pad),), float("nan"), device="cuda", dtype=x.dtype)
+    y = flat.view(rows, cols + lead + pad)[:, lead:lead + cols]
+    y.copy_(x)
+    check_quantize(torch, g, y, "e4m3", False)
