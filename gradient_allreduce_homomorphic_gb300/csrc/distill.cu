@@ -19,7 +19,7 @@
 // 4096 x 50001 bf16 144 us, 5.7 TB/s; 4096 x 50001 fp32 244 us, 6.7 TB/s;
 // 4096 x 4096 bf16 15.5 us, 4.3 TB/s (the rows' reductions); 8 x 32000 bf16 5 us
 // (one row's latency).  The loss alone of bf16 rows is bound by its pass's
-// instructions and powers: 4096 x 32768 62 us, 4.3 TB/s.
+// instructions and powers: 4096 x 32768 65 us, 4.1 TB/s (fp32 82 us, 6.6 TB/s).
 #include <atomic>
 
 #include "common.cuh"
@@ -49,7 +49,7 @@ struct DistillParams {
     float *loss, *lse;         // gar_distill_loss
     const float *lse_in;       // gar_distill_grad
     void *dz;                  // NULL: no gradient
-    int32_t stages, stage_bytes, slots, log_cluster;  // distill_stream_kernel
+    int32_t stages, stage_bytes, slots, log_cluster, log_parts;  // distill_stream_kernel
     unsigned int *status;
 };
 
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) distill_row_kernel(const __grid_cons
 // vectors, in shared memory, as a pipeline of warps:
 //   one warp copies the CTA's part of the coming rows there (bulk copies, up to
 //   eight stages);
-//   three warps (or five) take turns preparing the coming rows' teacher entries
+//   kPrepare warps take turns preparing the coming rows' teacher entries
 //   (slots), a chain of dependent loads and reductions of microseconds a row;
 //   the first group passes over a row for the maximum and the sum of powers,
 //   which its CTAs send one another as one pair each;
@@ -375,15 +375,14 @@ __global__ void __launch_bounds__(kThreads) distill_row_kernel(const __grid_cons
 // So copies, reductions and exchanges of some rows hide behind the passes over
 // others.  The elements before a row's first 16-byte boundary and after its last
 // one (a vocabulary of odd size) are the cluster's first CTA's; they come with the
-// teacher entries.  The loss alone leaves the second group one warp; the gradient
+// teacher entries.  The loss alone leaves the second group one warp, and takes the
+// parts of a row one after another where there are rows for all SMs; the gradient
 // alone, from a saved lse, needs no first group and no cluster.
 enum { kFused, kLossOnly, kGradOnly };
 constexpr int first_warps(int mode) { return mode == kGradOnly ? 0 : 8; }  // as many with the gradient as without: the same loss
 constexpr int second_warps(int mode) { return mode == kFused ? 8 : mode == kLossOnly ? 1 : 16; }
-// fp32 logits for the loss alone go by so fast (5.5 to 6.8 TB/s) that three preparing warps hold them up (2048 x 131072, 128
-// entries: 251 us with three, 195 with five); elsewhere more only take issue slots (4096 x 50001 bf16: 144 us, 159 with five).
-constexpr int prepare_warps(int mode, size_t size) { return mode == kLossOnly && size == 4 ? 5 : 3; }
-constexpr int stream_threads(int mode, size_t size) { return 32 * (first_warps(mode) + second_warps(mode) + 1 + prepare_warps(mode, size)); }
+constexpr int kPrepare = 3;  // more take issue slots: 4096 x 50001 bf16 144 us, 159 with five
+constexpr int stream_threads(int mode) { return 32 * (first_warps(mode) + second_warps(mode) + 1 + kPrepare); }
 constexpr int kMaxStages = 8, kMaxSlots = 8, kMaxCluster = 8;
 // Exchanges under way.  A CTA's first group is at most kMaxStages rows ahead of its second; to send row i + n it has
 // seen its second group finish row i + n - kMaxStages, for which every CTA's first group sent that row and its second
@@ -414,18 +413,23 @@ __device__ __forceinline__ void bar_group(int id) {
 }
 
 template <typename T, int kMode>
-__global__ void __launch_bounds__(stream_threads(kMode, sizeof(T)), 2) distill_stream_kernel(const __grid_constant__ DistillParams p) {
+__global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kernel(const __grid_constant__ DistillParams p) {
     constexpr int n = 16 / sizeof(T);
     constexpr bool kSaved = kMode == kGradOnly;
-    constexpr int kPrepare = prepare_warps(kMode, sizeof(T)), kFirst = first_warps(kMode), kSecond = second_warps(kMode), kMainWarps = kFirst + kSecond;
+    constexpr int kFirst = first_warps(kMode), kSecond = second_warps(kMode), kMainWarps = kFirst + kSecond;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kMaxSlots + kMeets];
     __shared__ Header header[kMaxSlots];
     __shared__ MaxSum partial[2][16];
+    __shared__ MaxSum of_warps[kMode == kLossOnly ? kMaxSlots : 1][kMaxCluster][8];
     __shared__ __align__(8) MaxSum pairs[kMeets][kMaxCluster];
     __shared__ int failed;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t K = 1u << p.log_cluster, rank = blockIdx.x & (K - 1);
+    const uint32_t own = kMode == kLossOnly ? 1u << (p.log_parts - p.log_cluster) : 1u;  // this CTA's parts of a row
+    // With the loss alone and no cluster, the second group's warp adds the first group's warps too, so that those need not
+    // meet after each part (4096 x 50001 bf16: 99 us, 108 where they do).
+    const bool apart = kMode == kLossOnly && K == 1;
     const int64_t first = blockIdx.x >> p.log_cluster, step = gridDim.x >> p.log_cluster;
     const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages, slot_full = empty + 8 * kMaxStages,
                    slot_empty = slot_full + 8 * kMaxSlots, met = slot_empty + 8 * kMaxSlots;
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(stream_threads(kMode, sizeof(T)), 2) distill_s
             mbar_init(slot_full + 8 * i, 1);
             mbar_init(slot_empty + 8 * i, kMainWarps);
         }
-        for (int i = 0; i < kMeets; ++i) mbar_init(met + 8 * i, 1);
+        for (int i = 0; i < kMeets; ++i) mbar_init(met + 8 * i, apart ? kFirst * own : 1);
         failed = 0;
         mbar_init_fence();
     }
@@ -458,13 +462,16 @@ __global__ void __launch_bounds__(stream_threads(kMode, sizeof(T)), 2) distill_s
             bool ok = true;
             for (int64_t row = first; row < p.rows; row += step) {
                 const T *z = static_cast<const T *>(p.z) + row * p.ldz;
-                const Row<T> part(z, p.vocab, rank, p.log_cluster);
-                const uint32_t bytes = static_cast<uint32_t>((part.v1 - part.v0) * 16);
-                if (!(ok = mbar_wait(empty + 8 * s, turn, &failed))) break;
-                mbar_expect_tx(full + 8 * s, bytes);
-                bulk_load(smem_u32(smem + s * p.stage_bytes), z + part.head + part.v0 * n, bytes, full + 8 * s);
-                issued = issued < S ? issued + 1 : S;
-                if (++s == S) s = 0, turn ^= 1;
+                for (uint32_t u = 0; u < own; ++u) {
+                    const Row<T> part(z, p.vocab, rank * own + u, p.log_parts);
+                    const uint32_t bytes = static_cast<uint32_t>((part.v1 - part.v0) * 16);
+                    if (!(ok = mbar_wait(empty + 8 * s, turn, &failed))) break;
+                    mbar_expect_tx(full + 8 * s, bytes);
+                    bulk_load(smem_u32(smem + s * p.stage_bytes), z + part.head + part.v0 * n, bytes, full + 8 * s);
+                    issued = issued < S ? issued + 1 : S;
+                    if (++s == S) s = 0, turn ^= 1;
+                }
+                if (!ok) break;
             }
             if (!ok)  // leave no copy in flight
                 for (; issued > 0; --issued) {
@@ -562,52 +569,61 @@ __global__ void __launch_bounds__(stream_threads(kMode, sizeof(T)), 2) distill_s
     } else if (warp < kFirst) {
         const float c = kLog2e * p.inv_tau;
         constexpr int kThreads = 32 * (kFirst > 0 ? kFirst : 1);
-        uint32_t s = 0, turn = 0, e = 0, eturn = 0, meet = 0;
+        uint32_t s = 0, turn = 0, e = 0, eturn = 0, meet = 0, flip = 0;
         for (int64_t row = first; row < p.rows; row += step) {
             const T *z = static_cast<const T *>(p.z) + row * p.ldz;
-            const Row<T> part(z, p.vocab, rank, p.log_cluster);
-            const uint4 *v = reinterpret_cast<const uint4 *>(smem + s * p.stage_bytes);
-            const int count = part.v1 - part.v0, odd = part.edge(threadIdx.x, p.vocab, rank);
             mbar_wait(slot_full + 8 * e, eturn, &failed);
             const bool live = header[e].live;
-            mbar_wait(full + 8 * s, turn, &failed);
-            MaxSum a{-INFINITY, 0.0f};
-            if (live) {
-                if (odd >= 0) a.m = header[e].edge[threadIdx.x], a.s = pow2((a.m - finite_or_0(a.m)) * c);
-                // two vectors at a time: a thread's maximum, powers and sum are chains of dependent instructions
-                for (int i = threadIdx.x; i < count; i += 2 * kThreads) {
-                    float x[2][n];
-                    unpack<T>(v[i], x[0]);
-                    unpack<T>(v[i + kThreads < count ? i + kThreads : i], x[1]);
-                    const float kept = i + kThreads < count ? 1.0f : 0.0f;  // of the second one's powers
-                    const float m = fmaxf(a.m, fmaxf(tree_max(x[0]), tree_max(x[1]))), r = finite_or_0(m);
-                    if (m > a.m) {  // a new maximum: seldom, after the first values
-                        a.s *= pow2((a.m - r) * c);
-                        a.m = m;
-                    }
-                    if (sizeof(T) == 2 && fabsf(r * c) <= kPlain) {
-                        const float rc = r * c;
+            for (uint32_t u = 0; u < own; ++u) {
+                const Row<T> part(z, p.vocab, rank * own + u, p.log_parts);
+                const uint4 *v = reinterpret_cast<const uint4 *>(smem + s * p.stage_bytes);
+                const int count = part.v1 - part.v0, odd = part.edge(threadIdx.x, p.vocab, rank * own + u);
+                mbar_wait(full + 8 * s, turn, &failed);
+                MaxSum a{-INFINITY, 0.0f};
+                if (live) {
+                    if (odd >= 0) a.m = header[e].edge[threadIdx.x], a.s = pow2((a.m - finite_or_0(a.m)) * c);
+                    // two vectors at a time: a thread's maximum, powers and sum are chains of dependent instructions
+                    for (int i = threadIdx.x; i < count; i += 2 * kThreads) {
+                        float x[2][n];
+                        unpack<T>(v[i], x[0]);
+                        unpack<T>(v[i + kThreads < count ? i + kThreads : i], x[1]);
+                        const float kept = i + kThreads < count ? 1.0f : 0.0f;  // of the second one's powers
+                        const float m = fmaxf(a.m, fmaxf(tree_max(x[0]), tree_max(x[1]))), r = finite_or_0(m);
+                        if (m > a.m) {  // a new maximum: seldom, after the first values
+                            a.s *= pow2((a.m - r) * c);
+                            a.m = m;
+                        }
+                        if (sizeof(T) == 2 && fabsf(r * c) <= kPlain) {
+                            const float rc = r * c;
 #pragma unroll
-                        for (int j = 0; j < n; ++j) x[0][j] = pow2(fmaf(x[0][j], c, -rc)), x[1][j] = pow2(fmaf(x[1][j], c, -rc));
-                    } else {
+                            for (int j = 0; j < n; ++j) x[0][j] = pow2(fmaf(x[0][j], c, -rc)), x[1][j] = pow2(fmaf(x[1][j], c, -rc));
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < n; ++j) x[0][j] = pow2((x[0][j] - r) * c), x[1][j] = pow2((x[1][j] - r) * c);
+                            for (int j = 0; j < n; ++j) x[0][j] = pow2((x[0][j] - r) * c), x[1][j] = pow2((x[1][j] - r) * c);
+                        }
+                        a.s += fmaf(kept, tree_sum(x[1]), tree_sum(x[0]));
                     }
-                    a.s += fmaf(kept, tree_sum(x[1]), tree_sum(x[0]));
                 }
-            }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(empty + 8 * s);
-                mbar_arrive(slot_empty + 8 * e);
-            }
-            if (live) {
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(empty + 8 * s);
+                    if (u == own - 1) mbar_arrive(slot_empty + 8 * e);
+                }
+                if (++s == S) s = 0, turn ^= 1;
+                if (!live) continue;
                 a = merge_lanes<32>(a, c);
-                if (lane == 0) partial[meet & 1][warp] = a;
+                if (apart) {
+                    if (lane == 0) {
+                        of_warps[kMode == kLossOnly ? meet % kMaxSlots : 0][u][warp] = a;
+                        mbar_arrive(met + 8 * (meet % kMeets));
+                    }
+                    continue;
+                }
+                if (lane == 0) partial[flip & 1][warp] = a;
                 bar_group<kThreads>(1);
                 if (warp == 0) {
                     const uint32_t at = meet % kMeets, bar = met + 8 * at;
-                    a = merge_lanes<(kFirst > 0 ? kFirst : 1)>(partial[meet & 1][lane & (kFirst > 0 ? kFirst - 1 : 0)], c);
+                    a = merge_lanes<(kFirst > 0 ? kFirst : 1)>(partial[flip & 1][lane & (kFirst > 0 ? kFirst - 1 : 0)], c);
                     if (K == 1) {
                         if (lane == 0) {
                             pairs[at][0] = a;
@@ -624,9 +640,9 @@ __global__ void __launch_bounds__(stream_threads(kMode, sizeof(T)), 2) distill_s
                                 : "memory");
                     }
                 }
-                ++meet;
+                ++flip;
             }
-            if (++s == S) s = 0, turn ^= 1;
+            if (live) ++meet;
             if (++e == E) e = 0, eturn ^= 1;
         }
     } else {
@@ -651,9 +667,17 @@ __global__ void __launch_bounds__(stream_threads(kMode, sizeof(T)), 2) distill_s
                 } else {
                     const uint32_t at = meet % kMeets;
                     mbar_wait(met + 8 * at, (meet / kMeets) & 1, &failed);
+                    MaxSum a{};
+                    if (apart) {
+                        for (uint32_t u = 0; u < own; ++u) {
+                            const MaxSum of_part = merge_lanes<8>(of_warps[kMode == kLossOnly ? meet % kMaxSlots : 0][u][lane & 7], c);
+                            a = u == 0 ? of_part : merge(a, of_part, c);
+                        }
+                    } else {
+                        a = pairs[at][0];
+                        for (uint32_t i = 1; i < K; ++i) a = merge(a, pairs[at][i], c);
+                    }
                     ++meet;
-                    MaxSum a = pairs[at][0];
-                    for (uint32_t i = 1; i < K; ++i) a = merge(a, pairs[at][i], c);
                     none = a.m == -INFINITY && a.s == 0.0f;
                     q.ref = finite_or_0(a.m), q.sub = log2f(a.s);
                     if (rank == 0 && tid == 0) {
@@ -774,7 +798,7 @@ int launch_stream(const DistillParams &p, int64_t rows_at_once, size_t shared, c
         if (e == cudaSuccess && cluster > 1) {
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(cluster);
-            cfg.blockDim = dim3(stream_threads(kMode, sizeof(T)));
+            cfg.blockDim = dim3(stream_threads(kMode));
             cfg.dynamicSmemBytes = kSharedBytes;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -789,7 +813,7 @@ int launch_stream(const DistillParams &p, int64_t rows_at_once, size_t shared, c
     }
     // (looked up for one CTA an SM, which is what rows of several CTAs get)
     if (cluster == 1 || clusters > rows_at_once) clusters = static_cast<int>(rows_at_once);
-    return launch_early("distill_stream_kernel", kernel, dim3(static_cast<unsigned>(clusters) << p.log_cluster), stream_threads(kMode, sizeof(T)),
+    return launch_early("distill_stream_kernel", kernel, dim3(static_cast<unsigned>(clusters) << p.log_cluster), stream_threads(kMode),
                         shared, cluster, stream, p);
 }
 
@@ -805,13 +829,13 @@ int launch(DistillParams &p, cudaStream_t stream) {
     const int slot = 12 * ((p.k + 3) & ~3);
     int tables = 32;
     while (tables < 2 * p.k) tables *= 2;
-    tables *= 4 * prepare_warps(kMode, sizeof(T));
+    tables *= 4 * kPrepare;
     p.slots = slot * kMaxSlots <= 24576 ? kMaxSlots : 4;  // eight up to 24 KB
     const int fixed = p.slots * slot + tables;
     // The fewest CTAs a row whose parts fit the stages (one a group works on, and one on its way), and more while
     // there are SMs without a row.
     const auto part = [&](int K) { return (ceil_div(bytes / 16, K) + 1) * 16; };
-    int least = kMode == kFused && 3 * part(kMaxCluster) + fixed <= kSharedBytes ? 3 : 2;
+    const int least = kMode != kGradOnly && 3 * part(kMaxCluster) + fixed <= kSharedBytes ? 3 : 2;
     const auto fits = [&](int K, int room) { return least * part(K) + fixed <= room; };
     int K = 1;
     while (K < kMaxCluster && !fits(K, kSharedBytes)) K *= 2;
@@ -829,14 +853,19 @@ int launch(DistillParams &p, cudaStream_t stream) {
         if (bytes <= 32768) return launch_row<T, kSaved, 8, 256>(p, stream);
         if (bytes <= 65536) return launch_row<T, kSaved, 8, 512>(p, stream);
     }
-    p.log_cluster = K == 8 ? 3 : K / 2;
+    p.log_cluster = p.log_parts = K == 8 ? 3 : K / 2;
+    // The loss alone needs no row whole: a CTA takes a row's parts in turn where there are rows for all SMs (clusters leave
+    // SMs free, and each of their CTAs prepares the entries: 2048 x 131072 fp32 with 128 entries 166 us, 195 by clusters).
+    // The parts are the fused call's, so the loss is the same bit for bit.
+    if (kMode == kLossOnly && p.rows >= sm_count()) p.log_cluster = 0;
+    const int cluster = 1 << p.log_cluster;
     p.stage_bytes = static_cast<int32_t>(part(K));
     // two CTAs an SM where two find room for their stages
-    const bool two = (kMode == kGradOnly || K == 1) && fits(K, kSharedBytes / 2 - 2048);
+    const bool two = (kMode == kGradOnly || cluster == 1) && fits(K, kSharedBytes / 2 - 2048);
     const int room = (two ? kSharedBytes / 2 - 2048 : kSharedBytes) - fixed;
     p.stages = room / p.stage_bytes < kMaxStages ? room / p.stage_bytes : kMaxStages;
     p.status = device_status();
-    int64_t at_once = static_cast<int64_t>(sm_count()) * (two ? 2 : 1) / K;
+    int64_t at_once = static_cast<int64_t>(sm_count()) * (two ? 2 : 1) / cluster;
     if (at_once > p.rows) at_once = p.rows;
     return launch_stream<T, kMode>(p, at_once, static_cast<size_t>(p.stages) * p.stage_bytes + fixed, stream);
 }

@@ -315,3 +315,27 @@ def test_short_rows_at_every_length(env, vocab, dtype, mode):
     index[1, :] = 0
     index[2, :] = vocab - 1
     check(torch, g, device(torch, z, dtype), index, teacher, weight, 0.9, mode)
+
+
+# the loss alone takes a row's parts as the call with the gradient does, wherever they run
+@pytest.mark.parametrize("rows,vocab,k", [(3, 50001, 9), (400, 50001, 40), (400, 36001, 300), (330, 131072, 64), (170, 151937, 200),
+                                          (160, 33000, 1024), (200, 8200, 5)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_loss_alone_is_the_same_bit_for_bit(env, rows, vocab, k, dtype):
+    torch, g = env
+    gen = torch.Generator(device="cuda").manual_seed(rows + vocab)
+    z = (torch.randn((rows, vocab), generator=gen, device="cuda") * 3).to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    z[1, : vocab // 2] = float("-inf")
+    z[2, 7] = float("inf")
+    index = torch.randint(-2, vocab + 2, (rows, k), generator=gen, device="cuda", dtype=torch.int32)
+    teacher = torch.randn((rows, k), generator=gen, device="cuda")
+    weight = (torch.rand(rows, generator=gen, device="cuda") > 0.1).float()
+    got = []
+    for dz in (torch.empty_like(z), None):
+        loss, lse = torch.full((rows,), 7.0, device="cuda"), torch.full((rows,), 7.0, device="cuda")
+        g.gar_distill_loss(z, index, teacher, 1.2, loss, lse, dz=dz, weight=weight)
+        got.append((loss, lse))
+    torch.cuda.synchronize()
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+    assert g.gar_sync_status() == 0
