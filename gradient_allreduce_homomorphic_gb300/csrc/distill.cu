@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kerne
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kMaxSlots + kMeets];
     __shared__ Header header[kMaxSlots];
     __shared__ MaxSum partial[2][16];
+    // (the first group is at most kMaxSlots rows ahead: a row's slot is free once the second group is done with it)
     __shared__ MaxSum of_warps[kMode == kLossOnly ? kMaxSlots : 1][kMaxCluster][8];
     __shared__ __align__(8) MaxSum pairs[kMeets][kMaxCluster];
     __shared__ int failed;
