@@ -21,9 +21,9 @@
 // once, each load's wait would hold up the next (8 workers of 16384 tokens and
 // 256 bf16 experts: 93 us, 69 so).
 //
-// 8 x 16384 x 256 fp32, 8 choices: 84 us, of which the counting pass 40 (the
+// 8 x 16384 x 256 fp32, 8 choices: 86 us, of which the counting pass 40 (the
 // selection's instructions, 714 for a warp's four tokens, issued in 53 % of the
-// cycles) and the gradient 44 (HBM: its logits read a second time).  Few tokens
+// cycles) and the gradient 46 (HBM: its logits read a second time).  Few tokens
 // cost their launches: 4 x 2000 x 60 bf16 18 us a call, 64 x 8 12 us, one launch.
 #include <algorithm>
 #include <atomic>
@@ -407,12 +407,13 @@ __device__ __forceinline__ float centred(int32_t count, int64_t choices, int exp
 // Two or three launches.  With kTogether, blockIdx.y's CTAs are one cluster,
 // which adds its counts in distributed shared memory and stores a worker's whole
 // counts; else the counts are zeroed by a kernel ahead and added with atomics
-// (integers: their order does not matter).  The counting kernel reads z before
-// it waits for the zeroing one, which lets it begin only once the kernels ahead
-// of both are done, and so does the gradient's kernel with its first tokens.
+// (integers: their order does not matter).  Each kernel waits for the one ahead
+// before it reads z too: that a kernel further ahead, which wrote z, has ended
+// orders the two, but only a wait of its own makes those writes visible to it
+// (8 x 16384 tokens of 64 fp32 experts 44 us, 41 with the first logits read ahead).
 __global__ void __launch_bounds__(kThreads) balance_zero_kernel(int32_t *counts, int n, uint32_t *seen, int workers) {
-    after_previous();
     let_next_begin();
+    after_previous();
     const int i = blockIdx.x * kThreads + threadIdx.x;
     if (i < n) counts[i] = 0;
     if (i <= workers) seen[i] = 0;
@@ -427,10 +428,8 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_co
     for (int e = threadIdx.x; e < p.experts; e += kThreads) cnt[e] = 0;
     if (threadIdx.x == 0) seen = 0;
     __syncthreads();
-    if (kTogether) {
-        after_previous();
-        let_next_begin();
-    }
+    let_next_begin();
+    after_previous();
     constexpr int kPerWarp = 32 / L;
     uint32_t mine = 0;
     int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kPerWarp + lane / L;
@@ -471,8 +470,6 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const __grid_co
         }
         cluster_barrier();  // no CTA leaves while another reads its shared memory
     } else {
-        let_next_begin();
-        after_previous();
         for (int e = threadIdx.x; e < p.experts; e += kThreads)
             if (cnt[e]) atomicAdd(&p.counts[w * p.experts + e], cnt[e]);
         if (threadIdx.x == 0 && seen) atomicAdd(p.seen + 1 + w, seen);
@@ -494,8 +491,8 @@ __global__ void __launch_bounds__(kThreads, V == 32 ? 2 : 1) balance_grad_kernel
     const int64_t own = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kPerWarp;
     int64_t t = own < p.tokens ? own + (p.tokens - 1 - own) / stride * stride : -1;
     Runs<T, V> g, coming;
-    bool live = t >= 0 && fetch<T, L, V, kWide>(p, w, t + lane / L, sub, g), live_next = false;
     after_previous();
+    bool live = t >= 0 && fetch<T, L, V, kWide>(p, w, t + lane / L, sub, g), live_next = false;
     int64_t n = 0;
     for (int i = 0; i < p.P; ++i) n += p.seen[1 + i];
     if (threadIdx.x == 0) coef = loss_scale(p, n);
@@ -707,7 +704,7 @@ int launch_as(const BalanceParams &p, cudaStream_t stream) {
 }
 
 // Kernels for aligned rows alone: 8 x 8192 x 512 fp32 83 us, 105 with the other pieces' code in
-// its way; 8 x 16384 x 250 fp32 (rows on 8 bytes) 104, element by element 123.
+// its way; 8 x 16384 x 250 fp32 (rows on 8 bytes) 107, element by element 123.
 template <typename T, int L, int V>
 int launch(const BalanceParams &p, cudaStream_t stream) {
     if (p.align == 16 && p.dalign == 16) return launch_as<T, L, V, true>(p, stream);

@@ -254,3 +254,53 @@ def test_rows_at_every_alignment(env, E, T, dtype):
         for a, b in zip(got, base):  # the same values, whatever the pieces they were read in
             assert torch.equal(a, b)
         assert (dz[:, :dlead] == 5.0).all() and (dz[:, dlead + E:] == 5.0).all()
+
+
+# the calls' one, two and three launches; in place (as a step that keeps one buffer of logits) and not
+@pytest.mark.parametrize("P,T,E", [(2, 300, 12), (2, 3000, 60), (1, 41000, 64), (2, 12000, 128), (1, 9000, 300)])
+@pytest.mark.parametrize("place", [False, True])
+def test_logits_rewritten_before_each_call(env, P, T, E, place):
+    """One buffer of logits, rewritten by the 8-bit product directly before each of a hundred calls without a wait of the
+    host: every call sees the new ones, as calls with the host waiting in between do."""
+    torch, g = env
+    gen = torch.Generator(device="cuda").manual_seed(77)
+    H, n, k = 128, 4, 4
+
+    def codes(rows):
+        q, s = g.fp8_matrix(rows, H)
+        g.gar_fp8_quantize(torch.randn((rows, H), generator=gen, device="cuda"), q, s)
+        return q, s
+
+    router, xs = codes(E), [[codes(T) for _ in range(P)] for _ in range(n)]
+    z = [torch.empty((T, E), device="cuda") for _ in range(P)]
+    ws = torch.empty(g.gar_balance_workspace_bytes(P), dtype=torch.uint8, device="cuda")
+
+    def outputs():
+        return ([torch.empty((T, k), dtype=torch.int32, device="cuda") for _ in range(P)],
+                torch.empty((P, E), dtype=torch.int32, device="cuda"), torch.empty(1, device="cuda"),
+                z if place else [torch.empty_like(a) for a in z])
+
+    def step(i, out, wait):
+        for w in range(P):
+            g.gar_fp8_matmul(*xs[i][w], *router, z[w])
+        if wait:
+            torch.cuda.synchronize()
+        g.gar_balance_loss(z, k, 0.5, *out[:3], ws, dz=out[3])
+
+    want = []
+    for i in range(n):
+        out = outputs()
+        step(i, out, True)
+        torch.cuda.synchronize()
+        want.append([t.clone() for part in out for t in (part if isinstance(part, list) else [part])])
+    outs = [outputs() for _ in range(n)]
+    for _ in range(100 // n):
+        for i in range(n):
+            step(i, outs[i], False)
+            if place:
+                outs[i] = outs[i][:3] + ([a.clone() for a in z],)  # its gradient, before the next product takes the buffer
+        torch.cuda.synchronize()
+        for i in range(n):
+            got = [t for part in outs[i] for t in (part if isinstance(part, list) else [part])]
+            assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+            outs[i] = outs[i][:3] + (z if place else outs[i][3],)
