@@ -255,6 +255,7 @@ class PtrTable:
         first = next((t for t in self.tensors if t is not None), None)
         self.numel = first.numel() if first is not None else 0
         self.first = first
+        self.checked = {}  # (shape, dtype) that every tensor was found to have -> their stride
 
     def __len__(self):
         return len(self.tensors)
@@ -803,17 +804,23 @@ def _worker_fits(t, name, shape, stride, dtype):
 
 def _workers(given, name, P, shape, dtype):
     """(pointers, row stride) of one tensor per worker, each of the given shape
-    and type and all of one row stride.  A PtrTable's tensors were put together
-    before: its first is looked at."""
+    and type and all of one row stride.  A PtrTable's tensors are looked at once
+    for each shape and type asked of them."""
     table = isinstance(given, PtrTable)
     tensors = given.tensors if table else given
     if len(tensors) != P:
         raise GarError(GAR_EINVAL, f"{name} has {len(tensors)} tensors, not {P}")
-    stride, ptrs = tensors[0].stride(), []
-    for t in tensors[:1] if table else tensors:
-        if t.dtype is not dtype or t.shape != shape or not t.is_cuda or t.stride() != stride:
-            _worker_fits(t, name, shape, stride, dtype)
-        ptrs.append(t.data_ptr())
+    stride = given.checked.get((shape, dtype)) if table else None
+    if stride is None:
+        if any(t is None for t in tensors):
+            raise GarError(GAR_EINVAL, f"{name} lacks a worker's tensor")
+        stride, ptrs = tensors[0].stride(), []
+        for t in tensors:
+            if t.dtype is not dtype or t.shape != shape or not t.is_cuda or t.stride() != stride:
+                _worker_fits(t, name, shape, stride, dtype)
+            ptrs.append(t.data_ptr())
+        if table:
+            given.checked[shape, dtype] = stride
     if stride[-1] != 1 and shape[-1] > 1:
         raise GarError(GAR_EINVAL, f"{name}: the elements of a row are not contiguous")
     return given.array if table else struct.pack(f"{P}Q", *ptrs), stride[0] if shape[0] > 1 else max(shape[-1], 1)

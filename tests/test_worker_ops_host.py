@@ -144,3 +144,68 @@ def test_reference_grid_is_the_format(fmt):
     np.testing.assert_array_equal(got, torch.from_numpy(mid).to(t).double().numpy())
     near = np.nextafter(mid, np.inf)
     np.testing.assert_array_equal(ref.round_to_format(near, fmt), v[1:])
+
+
+@pytest.fixture
+def binding(gar, monkeypatch):
+    """gar_balance_loss as it would be called with CUDA tensors, here with the host's: the library is not reached."""
+    torch = pytest.importorskip("torch")
+    calls = []
+
+    class Cuda(torch.Tensor):
+        is_cuda = True
+
+    monkeypatch.setattr(gar, "_call", lambda name, *a: calls.append(name))
+    monkeypatch.setattr(gar, "_stream", lambda stream: 0)
+
+    def tensor(*shape, dtype=torch.float32):
+        return torch.zeros(shape, dtype=dtype).as_subclass(Cuda)
+
+    def call(z, choice, k=2, tokens=6, experts=8, table=False, **more):
+        wrap = gar.pointer_table if table else list
+        P = len(z)
+        args = {n: None if v is None else wrap(v) for n, v in more.items()}
+        gar.gar_balance_loss(wrap(z), k, 0.1, wrap(choice), tensor(P, experts, dtype=torch.int32), tensor(1), tensor(1 << 15),
+                             **args)
+        return calls.pop()
+
+    def refused(*a, **more):
+        with pytest.raises(gar.GarError) as e:
+            call(*a, **more)
+        assert not calls
+        return e.value.status
+
+    return torch, tensor, call, refused
+
+
+@pytest.mark.parametrize("table", [False, True])
+def test_every_workers_tensor_is_checked(gar, binding, table):
+    torch, tensor, call, refused = binding
+    i32 = torch.int32
+    z, choice = [tensor(6, 8) for _ in range(3)], [tensor(6, 2, dtype=i32) for _ in range(3)]
+    dz, valid = [tensor(6, 8) for _ in range(3)], [tensor(6, dtype=torch.uint8) for _ in range(3)]
+    assert call(z, choice, table=table, dz=dz, valid=valid) == "gar_balance_loss"
+    assert call(z, choice, table=table, valid=[v.bool() for v in valid]) == "gar_balance_loss"
+    for bad in (tensor(5, 8), tensor(6, 7), tensor(6, 9)[:, :8], tensor(8, 6).t()):
+        assert refused(z[:2] + [bad], choice, table=table) == gar.GAR_EINVAL
+        assert refused(z, choice, table=table, dz=[dz[0], bad, dz[2]]) == gar.GAR_EINVAL
+    assert refused(z[:2] + [tensor(6, 8, dtype=torch.bfloat16)], choice, table=table) == gar.GAR_EDTYPE
+    assert refused(z, choice[:2] + [tensor(5, 2, dtype=i32)], table=table) == gar.GAR_EINVAL
+    assert refused(z, choice[:2] + [tensor(6, 2, dtype=torch.int64)], table=table) == gar.GAR_EDTYPE
+    assert refused(z, choice, table=table, valid=valid[:2] + [tensor(5, dtype=torch.uint8)]) == gar.GAR_EINVAL
+    assert refused(z, choice, table=table, valid=valid[:2] + [tensor(6)]) == gar.GAR_EDTYPE
+    assert refused(z, choice[:2], table=table) == gar.GAR_EINVAL
+
+
+def test_a_table_is_looked_at_once_per_shape_and_type(gar, binding):
+    torch, tensor, call, refused = binding
+    z, choice = [tensor(6, 8) for _ in range(2)], [tensor(6, 2, dtype=torch.int32) for _ in range(2)]
+    tz, tc = gar.pointer_table(z), gar.pointer_table(choice)
+    more = (tensor(2, 8, dtype=torch.int32), tensor(1), tensor(1 << 15))
+    for _ in range(2):
+        gar.gar_balance_loss(tz, 2, 0.1, tc, *more, dz=tz)
+    assert tz.checked == {((6, 8), torch.float32): (8, 1)} and tc.checked == {((6, 2), torch.int32): (2, 1)}
+    with pytest.raises(gar.GarError):  # another number of choices is another shape
+        gar.gar_balance_loss(tz, 3, 0.1, tc, *more, dz=tz)
+    with pytest.raises(gar.GarError):
+        gar.gar_balance_loss(tz, 2, 0.1, gar.pointer_table([choice[0], None], allow_none=True), *more)
