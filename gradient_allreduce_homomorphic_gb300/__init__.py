@@ -798,7 +798,8 @@ def _worker_fits(t, name, shape, stride, dtype):
         _dev(t)
     if t.dtype != dtype and not (dtype is _UINT8 and t.element_size() == 1):
         raise GarError(GAR_EDTYPE, f"{name} is {t.dtype}, not {dtype}")
-    if t.shape != shape or (t.stride() != stride and shape[0] > 1):
+    # one token's row stride means nothing, the stride of its elements does
+    if t.shape != shape or (t.stride() != stride if shape[0] > 1 else t.stride()[-1] != 1 and shape[-1] > 1):
         raise GarError(GAR_EINVAL, f"{name} has a tensor of shape {tuple(t.shape)}, not {shape}, or of another stride")
 
 

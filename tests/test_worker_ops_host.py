@@ -209,3 +209,20 @@ def test_a_table_is_looked_at_once_per_shape_and_type(gar, binding):
         gar.gar_balance_loss(tz, 3, 0.1, tc, *more, dz=tz)
     with pytest.raises(gar.GarError):
         gar.gar_balance_loss(tz, 2, 0.1, gar.pointer_table([choice[0], None], allow_none=True), *more)
+
+
+@pytest.mark.parametrize("table", [False, True])
+def test_one_token_of_strided_elements(gar, binding, table):
+    """A single token's row stride may differ between workers, the stride of its elements may not."""
+    torch, tensor, call, refused = binding
+    z, choice = [tensor(1, 8) for _ in range(2)], [tensor(1, 2, dtype=torch.int32) for _ in range(2)]
+    other = [z[0], tensor(1, 20)[:, 3:11]]
+    assert call(other, choice, table=table, dz=other) == "gar_balance_loss"
+    for place in (0, 1):
+        bad = list(z)
+        bad[place] = tensor(1, 16)[:, ::2]
+        assert refused(bad, choice, table=table) == gar.GAR_EINVAL
+        assert refused(z, choice, table=table, dz=bad) == gar.GAR_EINVAL
+        bad = list(choice)
+        bad[place] = tensor(1, 4, dtype=torch.int32)[:, ::2]
+        assert refused(z, bad, table=table) == gar.GAR_EINVAL
