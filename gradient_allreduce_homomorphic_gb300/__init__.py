@@ -832,7 +832,9 @@ def gar_balance_loss(z, k: int, alpha: float, choice, counts, loss, workspace, d
     [tokens, experts] logits, choice[w] [tokens, k] int32 out, counts [P,
     experts] int32 out, loss one fp32 out, dz[w] of z's type out (may be z[w]),
     valid[w] [tokens] uint8 or bool.  Lists or PtrTables."""
-    first = z.first if isinstance(z, PtrTable) else z[0]
+    first = z.first if isinstance(z, PtrTable) else z[0] if len(z) else None
+    if first is None:
+        raise GarError(GAR_EINVAL, "z has no worker's tensor")
     dtype = _code(first, _FLOATS, "z")
     P, (tokens, experts) = len(z), _two_dims(first, "z[0]")
     za, ldz = _workers(z, "z", P, (tokens, experts), first.dtype)

@@ -226,3 +226,8 @@ def test_one_token_of_strided_elements(gar, binding, table):
         bad = list(choice)
         bad[place] = tensor(1, 4, dtype=torch.int32)[:, ::2]
         assert refused(z, bad, table=table) == gar.GAR_EINVAL
+
+
+def test_no_workers(gar, binding):
+    torch, tensor, call, refused = binding
+    assert refused([], []) == refused([], [], table=True) == refused([None], [None]) == gar.GAR_EINVAL
