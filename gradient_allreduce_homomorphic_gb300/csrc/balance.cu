@@ -747,10 +747,10 @@ extern "C" int gar_balance_loss(const void *const *z, int32_t P, int64_t tokens,
                                 void *d_workspace, size_t workspace_bytes, gar_stream_t stream_) {
     if (P < 1 || P > GAR_MAX_WORKERS) return fail(GAR_EINVAL, "P=%d outside 1..%d", P, GAR_MAX_WORKERS);
     if (elem_bytes(dtype) < 0) return fail(GAR_EDTYPE, "unknown dtype %d", dtype);
-    if (tokens < 0 || tokens * P > 0x7FFFFFFF / kMaxChoices || experts < 1 || experts > kMaxExperts || k < 1 ||
+    if (tokens < 0 || tokens > 0x7FFFFFFF / kMaxChoices / P || experts < 1 || experts > kMaxExperts || k < 1 ||
         k > kMaxChoices || k > experts)
-        return fail(GAR_EINVAL, "tokens=%lld experts=%d (1..%d) k=%d (1..%d, at most the experts)",
-                    static_cast<long long>(tokens), experts, kMaxExperts, k, kMaxChoices);
+        return fail(GAR_EINVAL, "tokens=%lld (P tokens <= %d) experts=%d (1..%d) k=%d (1..%d, at most the experts)",
+                    static_cast<long long>(tokens), 0x7FFFFFFF / kMaxChoices, experts, kMaxExperts, k, kMaxChoices);
     if (!(alpha - alpha == 0.0f)) return fail(GAR_EINVAL, "alpha must be finite");
     if (!counts || !loss || !d_workspace || workspace_bytes < gar_balance_workspace_bytes(P))
         return fail(GAR_EINVAL, "NULL argument, or the workspace is too small");

@@ -768,6 +768,8 @@ size_t gar_balance_workspace_bytes(int32_t P);
  * than summed, pass P alpha.
  *   z            host array of P device pointers, tokens x experts fp32 or bf16
  *                (dtype), row stride ldz
+ *   tokens       of each worker; P tokens <= 2^26 - 1: all choices can be
+ *                counted in 32 bits
  *   experts, k   1 <= k <= min(32, experts), experts <= 1024
  *   valid        host array of P device pointers, [tokens] bytes (0: the token
  *                is padding); NULL: every token is valid

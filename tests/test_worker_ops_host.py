@@ -231,3 +231,16 @@ def test_one_token_of_strided_elements(gar, binding, table):
 def test_no_workers(gar, binding):
     torch, tensor, call, refused = binding
     assert refused([], []) == refused([], [], table=True) == refused([None], [None]) == gar.GAR_EINVAL
+
+
+@pytest.mark.parametrize("P", [1, 2, 8, 64])
+def test_balance_token_limit(gar, P):
+    """P tokens <= 2^26 - 1, also where their product does not fit 64 bits (2^63 and 2^64 at P = 64)."""
+    lib = gar.load()
+    table = (V * P)(*range(0x10000, 0x10000 * (P + 1), 0x10000))
+    for tokens in (1 << 26, ((1 << 26) - 1) // P + 1, 1 << 40, 1 << 57, 1 << 58, 1 << 62, (1 << 63) - 1):
+        status = lib.gar_balance_loss(table, P, tokens, 8, 8, 0, 2, None, 0.1, table, B, D, None, 0, V(0x10004), 1 << 16, NULL)
+        assert status == gar.GAR_EINVAL, tokens  # (the workspace is misaligned: nothing is launched whatever the count)
+    tokens = ((1 << 26) - 1) // P
+    assert lib.gar_balance_loss(table, P, tokens, 8, 8, 0, 2, None, 0.1, table, B, D, None, 0, V(0x10004), 1 << 16,
+                                NULL) == gar.GAR_EALIGN
