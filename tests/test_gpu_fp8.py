@@ -308,3 +308,24 @@ def test_quantize_rows_that_start_anywhere(env, rows, cols, dtype, lead, pad):
     y = flat.view(rows, cols + lead + pad)[:, lead:lead + cols]
     y.copy_(x)
     check_quantize(torch, g, y, "e4m3", False)
+
+
+def test_split_products_that_share_sms(env):
+    """Two streams of products whose k is split over clusters, two CTAs an SM: the same results as one after another."""
+    torch, g = env
+    sizes = [(16, 4096, 2048), (33, 2000, 4096), (64, 1024, 8192), (5, 700, 3000)]
+    ops = [(operand(torch, g, m, k, "e4m3", 31), operand(torch, g, n, k, "e4m3", 32)) for m, n, k in sizes]
+    want = []
+    for (m, n, _), (a, b) in zip(sizes, ops):
+        want.append(torch.empty((m, n), device="cuda"))
+        g.gar_fp8_matmul(*a, *b, want[-1])
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[torch.zeros_like(d) for d in want] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(50):
+        for s, (stream, outs) in enumerate(zip(streams, got)):
+            for j in (range(4) if s == 0 else (2, 0, 3, 1)):
+                g.gar_fp8_matmul(*ops[j][0], *ops[j][1], outs[j], stream=stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for outs in got for a, b in zip(outs, want)) and g.gar_sync_status() == 0
