@@ -138,6 +138,14 @@ __device__ __noinline__ void mbar_drain(uint32_t full, uint32_t stages, int issu
     }
 }
 
+// All products that the issuing warp sent off are done: tensor memory may be
+// given back.  A wait of its own limit, for a wait that ran out elsewhere lets all
+// others of the CTA pass.
+__device__ __forceinline__ void products_done(uint32_t bar) {
+    int given_up = 0;
+    mbar_wait(bar, 0, &given_up);
+}
+
 template <typename T, int TM>
 __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant__ CUtensorMap map_n,
                                                           const __grid_constant__ CUtensorMap map_m,
@@ -211,14 +219,15 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
 #pragma unroll
                 for (int k = 0; k < kKC / 32; ++k)
                     tc_mma_mxf8<1>(tmem, d + 2 * k, d + (S::kBytesA >> 4) + 2 * k, idesc, col, col + 4, c > c0 || k > 0);
-                tc_commit(empty + 8 * s);
-                if ((c & 3) == 3 || c == c1 - 1) tc_commit(sf_empty + 8 * (g % kScaleBufs));
+                tc_commit<1>(empty + 8 * s);
+                if ((c & 3) == 3 || c == c1 - 1) tc_commit<1>(sf_empty + 8 * (g % kScaleBufs));
             }
             __syncwarp();
             if (++s == S::kStages) s = 0, turn ^= 1;
         }
-        if (elect_one()) tc_commit(done);
+        if (elect_one()) tc_commit<1>(done);
         __syncwarp();
+        products_done(done);
     } else if (warp == 2) {
         const int j0 = c0 >> 2, groups = c0 < c1 ? ((c1 - 1) >> 2) - j0 + 1 : 0;
         for (int g = 0; g < groups; ++g) {
@@ -228,6 +237,7 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
             copy_scales_async(dst + 512, p.sa + static_cast<int64_t>(j0 + g) * p.M, m0, p.M, lane);
             copy_async_arrive(sf_full + 8 * b);
         }
+        copy_async_wait();
     }
     if (warp >= 4) {
         mbar_wait(done, 0, &failed);
@@ -329,7 +339,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                        const __grid_constant__ PairParams pp) {
     const MatmulParams &p = pp.mm;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kPairStages + 3 * kPairScaleBufs + 4];
+    __shared__ __align__(8) uint64_t bars[2 * kPairStages + 3 * kPairScaleBufs + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
     const uint32_t stage = pair_stage(pp.rows);
@@ -337,7 +347,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t scales = base + kPairStages * stage;
     const uint32_t full = smem_u32(bars), empty = full + 8 * kPairStages, sf_full = empty + 8 * kPairStages,
                    sf_empty = sf_full + 8 * kPairScaleBufs, acc_full = sf_empty + 8 * kPairScaleBufs,
-                   drained = acc_full + 16, sf_here = drained + 16;
+                   drained = acc_full + 16, sf_here = drained + 16, done = sf_here + 8 * kPairScaleBufs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_cta_rank();
     const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
@@ -356,6 +366,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(acc_full + 8 * i, 1);
             mbar_init(drained + 8 * i, 16);  // eight epilogue warps of each CTA
         }
+        mbar_init(done, 1);
         failed = 0;
         mbar_init_fence();
     }
@@ -442,6 +453,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
             }
         }
+        if (elect_one()) tc_commit<2>(done);  // here alone: the other CTA frees its half behind the cluster barrier below
+        __syncwarp();
+        products_done(done);
     } else if (warp == 2) {
         const int words = (p.chunks + 3) >> 2;
         uint32_t g = 0;
@@ -458,6 +472,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 copy_async_arrive(sf_here + 8 * b);
             }
         }
+        copy_async_wait();
     } else if (warp == 3) {
         // Passes on to the pair's first CTA that a group of scales is here.  Not the copying warp's work: a release to
         // the cluster waits for the thread's own copies under way.

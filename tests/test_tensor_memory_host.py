@@ -27,3 +27,17 @@ def test_permit_to_allocate_is_given_back_at_once():
     order = re.findall(r"tcgen05\.(alloc|relinquish_alloc_permit)\.(cta_group::\d)", body(text, "void tmem_alloc("))
     assert order == [(op, g) for g in ("cta_group::1", "cta_group::2") for op in ("alloc", "relinquish_alloc_permit")]
     assert "relinquish" not in body(text, "void tmem_free(")
+
+
+def test_tensor_memory_is_given_back_after_the_products():
+    """Also where a wait ran out and lets all others pass: the warp that sends off products ends with a commit behind
+    them and a wait of its own limit for it, and the warp that copies scales with a wait for its copies."""
+    text = source("matmul.cu")
+    for head in ("matmul_kernel(", "matmul_pair_kernel("):
+        kernel = body(text, head)
+        warps = re.split(r"if \(warp == (\d)[^)]*\) \{", kernel)
+        roles = dict(zip(warps[1::2], warps[2::2]))
+        assert re.search(r"tc_commit<\d>\(done\);\s*__syncwarp\(\);\s*products_done\(done\);\s*\} else $", roles["1"]), head
+        assert re.search(r"copy_async_wait\(\);\s*\}", roles["2"]), head
+    wait = body(text, "void products_done(")
+    assert "int given_up = 0;" in wait and "failed" not in wait
