@@ -574,7 +574,9 @@ __global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kerne
         for (int64_t row = first; row < p.rows; row += step) {
             const T *z = static_cast<const T *>(p.z) + row * p.ldz;
             mbar_wait(slot_full + 8 * e, eturn, &failed);
-            const bool live = header[e].live;
+            // One decision for the warp, and barriers that every row passes: after a wait that ran out the header may change
+            // as it is read.
+            const bool live = __any_sync(0xFFFFFFFFu, header[e].live != 0);
             for (uint32_t u = 0; u < own; ++u) {
                 const Row<T> part(z, p.vocab, rank * own + u, p.log_parts);
                 const uint4 *v = reinterpret_cast<const uint4 *>(smem + s * p.stage_bytes);
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kerne
                     if (u == own - 1) mbar_arrive(slot_empty + 8 * e);
                 }
                 if (++s == S) s = 0, turn ^= 1;
-                if (!live) continue;
+                if (!live && apart) continue;
                 a = merge_lanes<32>(a, c);
                 if (apart) {
                     if (lane == 0) {
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kerne
                 }
                 if (lane == 0) partial[flip & 1][warp] = a;
                 bar_group<kThreads>(1);
-                if (warp == 0) {
+                if (live && warp == 0) {
                     const uint32_t at = meet % kMeets, bar = met + 8 * at;
                     a = merge_lanes<(kFirst > 0 ? kFirst : 1)>(partial[flip & 1][lane & (kFirst > 0 ? kFirst - 1 : 0)], c);
                     if (K == 1) {
@@ -658,9 +660,10 @@ __global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kerne
             mbar_wait(slot_full + 8 * e, eturn, &failed);
             const Header &h = header[e];
             if (kMode != kLossOnly) mbar_wait(full + 8 * s, turn, &failed);
+            const bool live = __any_sync(0xFFFFFFFFu, h.live != 0);  // as in the first group
             Softmax<kSaved> q{0.0f, 0.0f, kSaved ? p.inv_tau : c};
             float g = 0.0f;
-            if (h.live) {
+            if (live) {
                 bool none;
                 if (kSaved) {
                     q.sub = p.lse_in[row];
@@ -731,8 +734,8 @@ __global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kerne
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + 8 * s);
-                if (h.live) {  // dz at the entries that this CTA's part holds, over what the pass stored there
-                    bar_group<kThreads>(2);
+                bar_group<kThreads>(2);
+                if (live) {  // dz at the entries that this CTA's part holds, over what the pass stored there
                     const int32_t *top_i = reinterpret_cast<const int32_t *>(slots + e * 12 * entries);
                     const float *top_p = reinterpret_cast<const float *>(top_i + entries), *top_z = top_p + entries;
                     for (int j = tid; j < p.k; j += kThreads) {
