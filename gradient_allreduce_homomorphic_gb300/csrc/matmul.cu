@@ -36,6 +36,10 @@ namespace {
 constexpr int kTN = 128;     // tile rows in tensor memory: columns of D
 constexpr int kKC = 128;     // k per chunk: one scale block, one swizzled line
 constexpr int kThreads = 256;
+// Chunks that an accumulator adds at most, for an fp32 result: the tensor core's additions round toward zero, so its error
+// grows with the number of k (measured against 64 bits, of the result: 2.6e-7 at 2048, 8e-7 at 8192 for values of mean 0;
+// 1.7e-6 at 8192, 7e-6 at 40000 for values with a mean, whose sums grow all along).
+constexpr int kSegment = 64;
 constexpr int kScaleBufs = 4;   // of scale words, one for each 512 k, in shared memory; tensor memory has two
 
 struct MatmulParams {
@@ -297,10 +301,8 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
 // lets the next tile's products start.  TM is chosen so that the tiles fill
 // the SMs' last wave (pair_rows below).
 //
-// With an fp32 result, k is cut into segments of at most 8192 whose sums are
-// added in fp32: the tensor core's additions round toward zero, so its error
-// grows with the number of k it adds (measured against 64 bits: 2.6e-7 of the
-// result at 2048, 8e-7 at 8192).
+// With an fp32 result, k is cut into segments of at most kSegment chunks, whose
+// sums are added in fp32.
 //
 // Bound by the tensor cores at the clock that the power limit leaves them:
 // 16384 x 4096 x 8192 to fp32 325 us, 3380 TFLOP/s (tensor pipe active in 85 %
@@ -312,7 +314,6 @@ constexpr int kPairStages = 6;
 constexpr int kPairScaleBuf = 512 * 3;
 constexpr int kPairScaleBufs = 8;
 constexpr int kPairScaleCols = 480;
-constexpr int kSegment = 64;  // chunks of 128 k
 
 struct PairParams {
     MatmulParams mm;
@@ -608,10 +609,11 @@ int resident_clusters(int splits) {
 // and K of 512 to 8192: 3.9 us, 0.33 for a chunk, 1.4 for the exchange of
 // partial tiles, and a wave more as often as the CTAs exceed the SMs.  So k is
 // split from 12 chunks on, down to four a CTA, as far as all clusters run at
-// one time.
+// one time.  Segments (kSegment) are launches of their own, each of which adds
+// to the one before's result.
 struct Plan {
     int64_t tiles, ns;
-    int splits;
+    int splits, segments;
 };
 template <typename T, int TM>
 int plan(const MatmulParams &p, Plan *out) {
@@ -625,24 +627,41 @@ int plan(const MatmulParams &p, Plan *out) {
         if (n < 1) return n;
         if (out->tiles <= n / Shape<TM>::kResident) out->splits = splits;
     }
-    out->ns = 3900 + 330 * ceil_div(p.chunks, int64_t{out->splits}) + (out->splits > 1 ? 1400 : 0) + (waves - 1) * (1500 + 330 * p.chunks);
+    out->segments = sizeof(T) == 2 ? 1 : static_cast<int>(std::max(ceil_div(p.chunks, int64_t{out->splits} * kSegment), int64_t{1}));
+    out->ns = out->segments * (3900 + (out->splits > 1 ? 1400 : 0)) + 330 * ceil_div(p.chunks, int64_t{out->splits}) +
+              (waves - 1) * (1500 * out->segments + 330 * p.chunks);
     return GAR_OK;
+}
+
+// Chunks of each of at most `segments` segments: whole scale words, four chunks each.
+int32_t segment_chunks(int32_t chunks, int32_t segments) {
+    return static_cast<int32_t>(std::max(ceil_div(ceil_div(chunks, segments), 4) * 4, int64_t{4}));
 }
 
 template <typename T, int TM>
 int launch(MatmulParams &p, const Plan &how, const uint8_t *a, int64_t lda, const uint8_t *b, int64_t ldb, int64_t K, cudaStream_t stream) {
     using S = Shape<TM>;
-    CUtensorMap map_n{}, map_m{};
-    if (K > 0) {
-        if (int rc = encode(&map_n, b, p.N, K, ldb, kTN)) return rc;
-        if (int rc = encode(&map_m, a, p.M, K, lda, TM)) return rc;
-    }
     p.tiles_n = static_cast<int32_t>(ceil_div(p.N, int64_t{kTN}));
     p.splits = how.splits;
     if (how.tiles * how.splits > 0x7FFFFFFF) return fail(GAR_EINVAL, "the product has too many tiles");
     p.idesc = p.idesc | mxf8_idesc(0, 0, kTN, TM);
-    return launch_early("matmul_kernel", matmul_kernel<T, TM>, dim3(static_cast<unsigned>(how.tiles * how.splits)), kThreads, S::kSmem,
-                        static_cast<unsigned>(p.splits), stream, map_n, map_m, p);
+    const int32_t chunks = p.chunks, step = segment_chunks(chunks, how.segments);
+    const uint32_t *const sa = p.sa, *const sb = p.sb;
+    for (int32_t c0 = 0; c0 == 0 || c0 < chunks; c0 += step) {
+        p.chunks = std::min(step, chunks - c0);
+        p.sa = sa + p.M * (c0 / 4), p.sb = sb + p.N * (c0 / 4);
+        if (c0 > 0) p.c = p.d, p.ldc = p.ldd;
+        CUtensorMap map_n{}, map_m{};
+        if (K > 0) {
+            const int64_t k0 = int64_t{kKC} * c0, k = std::min(int64_t{kKC} * p.chunks, K - k0);
+            if (int rc = encode(&map_n, b + k0, p.N, k, ldb, kTN)) return rc;
+            if (int rc = encode(&map_m, a + k0, p.M, k, lda, TM)) return rc;
+        }
+        if (int rc = launch_early("matmul_kernel", matmul_kernel<T, TM>, dim3(static_cast<unsigned>(how.tiles * how.splits)), kThreads,
+                                  S::kSmem, static_cast<unsigned>(p.splits), stream, map_n, map_m, p))
+            return rc;
+    }
+    return GAR_OK;
 }
 
 // The rows of a pair's tiles: the count that finishes soonest.  In clocks, as
@@ -696,8 +715,7 @@ int launch_pair(MatmulParams &mm, int pairs, const uint8_t *a, int64_t lda, cons
     p.tiles_m = ceil_div(mm.M, int64_t{p.rows});
     p.tiles = p.tiles_m * mm.tiles_n;
     p.segments = sizeof(T) == 2 ? 1 : static_cast<int32_t>(ceil_div(mm.chunks, kSegment));
-    // whole scale words per segment
-    p.seg_chunks = static_cast<int32_t>(ceil_div(ceil_div(mm.chunks, p.segments), 4) * 4);
+    p.seg_chunks = segment_chunks(mm.chunks, p.segments);
     p.segments = static_cast<int32_t>(ceil_div(mm.chunks, p.seg_chunks));
     CUtensorMap map_n{}, map_m{};
     if (int rc = encode(&map_n, b, mm.N, K, ldb, 128)) return rc;

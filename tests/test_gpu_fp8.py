@@ -329,3 +329,37 @@ def test_split_products_that_share_sms(env):
                 g.gar_fp8_matmul(*ops[j][0], *ops[j][1], outs[j], stream=stream)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for outs in got for a, b in zip(outs, want)) and g.gar_sync_status() == 0
+
+
+def product_error(torch, g, m, n, k, seed, addend):
+    """Relative error, in the norm, of an fp32 product of values with a mean, whose sums grow with k."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def codes(rows):
+        q, s = g.fp8_matrix(rows, k)
+        g.gar_fp8_quantize(torch.randn((rows, k), generator=gen, device="cuda") + 0.5, q, s)
+        return q, s
+
+    a, b = codes(m), codes(n)
+    want = decoded(torch, *a) @ decoded(torch, *b).t()
+    d, c = torch.empty((m, n), device="cuda"), None
+    if addend:
+        c = torch.randn((m, n), generator=gen, device="cuda") * k ** 0.5
+        want += c.double()
+        d.copy_(c)
+    g.gar_fp8_matmul(*a, *b, d, c=d if addend else None)  # the addend in place
+    again = torch.empty_like(d)
+    g.gar_fp8_matmul(*a, *b, again, c=c)
+    assert torch.equal(d, again)
+    return ((d.double() - want).norm() / want.norm()).item()
+
+
+@pytest.mark.parametrize("addend", [False, True])
+@pytest.mark.parametrize("m,n,k", [(256, 2048, 65536), (16, 300, 262144), (100, 130, 100001), (70, 5000, 40000)])
+def test_matmul_long_sums_of_few_tiles(env, m, n, k, addend):
+    """An accumulator of the tensor core adds 8192 k at most, so that its error, which grows with them where the sum does,
+    is that of a product with k = 8192 (one accumulator there: many tiles).  Beyond it, up to 32 parts are added in fp32
+    to nearest: 2^-24 sqrt(1/3) sqrt(sum of (j / 32)^2) = 1.2e-7 in the mean square."""
+    torch, g = env
+    one = product_error(torch, g, 2560, 2400, 8192, 34, False)
+    assert product_error(torch, g, m, n, k, 33, addend) <= 1.05 * one + 2.5e-7
