@@ -412,6 +412,12 @@ __device__ __forceinline__ void bar_group(int id) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
 }
 
+// Dynamic shared memory: of a CTA that has its SM to itself, and of each of two CTAs that share one (of_warps below is the
+// loss-only kernel's).
+constexpr int kSmBytes = 228 * 1024, kCtaBytes = 227 * 1024, kReserved = 1024;  // shared memory; a CTA's most; what each CTA costs besides
+constexpr int kSharedBytes = 220 * 1024;
+constexpr int two_room(int mode) { return kSharedBytes / 2 - 2048 - (mode == kLossOnly ? 1408 : 0); }
+
 template <typename T, int kMode>
 __global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kernel(const __grid_constant__ DistillParams p) {
     constexpr int n = 16 / sizeof(T);
@@ -425,6 +431,9 @@ __global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kerne
     __shared__ MaxSum of_warps[kMode == kLossOnly ? kMaxSlots : 1][kMaxCluster][8];
     __shared__ __align__(8) MaxSum pairs[kMeets][kMaxCluster];
     __shared__ int failed;
+    constexpr int kArrays = sizeof(bars) + sizeof(header) + sizeof(partial) + sizeof(of_warps) + sizeof(pairs) + sizeof(failed);
+    constexpr int kStatic = (kArrays + 127) / 128 * 128;  // the dynamic part behind them starts on 128 bytes
+    static_assert(kSharedBytes + kStatic <= kCtaBytes && 2 * (two_room(kMode) + kStatic + kReserved) <= kSmBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t K = 1u << p.log_cluster, rank = blockIdx.x & (K - 1);
     const uint32_t own = kMode == kLossOnly ? 1u << (p.log_parts - p.log_cluster) : 1u;  // this CTA's parts of a row
@@ -783,8 +792,6 @@ int check(const void *z, int32_t dtype, int64_t rows, int64_t vocab, int64_t ldz
     return GAR_OK;
 }
 
-constexpr int kSharedBytes = 220 * 1024;  // of a CTA that has the SM to itself, static shared memory taken off
-
 template <typename T, int kMode>
 int launch_stream(const DistillParams &p, int64_t rows_at_once, size_t shared, cudaStream_t stream) {
     const auto kernel = distill_stream_kernel<T, kMode>;
@@ -865,8 +872,8 @@ int launch(DistillParams &p, cudaStream_t stream) {
     const int cluster = 1 << p.log_cluster;
     p.stage_bytes = static_cast<int32_t>(part(K));
     // two CTAs an SM where two find room for their stages
-    const bool two = (kMode == kGradOnly || cluster == 1) && fits(K, kSharedBytes / 2 - 2048);
-    const int room = (two ? kSharedBytes / 2 - 2048 : kSharedBytes) - fixed;
+    const bool two = (kMode == kGradOnly || cluster == 1) && fits(K, two_room(kMode));
+    const int room = (two ? two_room(kMode) : kSharedBytes) - fixed;
     p.stages = room / p.stage_bytes < kMaxStages ? room / p.stage_bytes : kMaxStages;
     p.status = device_status();
     int64_t at_once = static_cast<int64_t>(sm_count()) * (two ? 2 : 1) / cluster;

@@ -339,3 +339,14 @@ def test_loss_alone_is_the_same_bit_for_bit(env, rows, vocab, k, dtype):
     for a, b in zip(*got):
         assert torch.equal(a.view(torch.int32), b.view(torch.int32))
     assert g.gar_sync_status() == 0
+
+
+# rows whose stages just fill, or just miss, the shared memory of two CTAs that share an SM
+@pytest.mark.parametrize("vocab,dtype", [(16900, "bf16"), (17000, "bf16"), (17100, "bf16"), (8450, "f32"), (8500, "f32"), (8550, "f32")])
+def test_rows_at_the_limit_of_two_ctas_an_sm(env, vocab, dtype):
+    torch, g = env
+    z, index, teacher, weight = problem(310, vocab, 64, 15, repeat=True)
+    zt = device(torch, z, dtype)
+    check(torch, g, zt, index, teacher, weight, 1.1, "fused")
+    check(torch, g, zt, index, teacher, weight, 1.1, "split")
+    assert g.gar_sync_status() == 0
