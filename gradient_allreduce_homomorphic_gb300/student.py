@@ -42,13 +42,20 @@ class StudentStep:
     P workers of ``tokens`` tokens each; k choices a token; alpha the balance
     loss's weight; tau the distillation's temperature.
 
-    After ``run(...)``: ``loss[w]`` the tokens' distillation losses, ``choice[w]``
-    and ``counts`` the router's choices, ``balance`` the balance loss, ``dx[w]``
-    the gradient of the hidden states, ``grads[w]`` the worker's flat gradient
-    (``head_grad[w]`` and ``router_grad[w]`` are views of it) and
-    ``averaging.ring_flat[w]`` / ``averaging.thc_flat`` its averages.  The
-    gradients are of the mean over workers of (distillation loss summed with
-    the tokens' weights) + balance loss.
+    The objective is F = (1 / P) sum over workers of D_w + alpha B, with D_w a
+    worker's distillation losses summed with its tokens' weights and B the
+    balance loss over all workers' tokens.  As the averages divide by P, each
+    worker's gradients are those of P F = sum of D_w + P alpha B, as far as
+    its own tokens go.  After ``run(...)``:
+
+      loss[w]            the tokens' distillation losses (without their weights)
+      choice[w], counts  the router's choices
+      balance            P alpha B: F is the workers' mean of D_w + balance / P
+      dx[w]              the gradient of P F over the worker's hidden states
+      grads[w]           the worker's share of P F's gradient over the weights, flat
+                         (head_grad[w] and router_grad[w] are views of it)
+      averaging          ring_flat[w] and thc_flat: the averages of grads, the
+                         gradient of F, exact and compressed
     """
 
     def __init__(self, head, router, *, workers: int, tokens: int, k: int = 2, alpha: float = 0.01, tau: float = 1.0,

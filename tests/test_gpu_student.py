@@ -115,3 +115,41 @@ def test_padding_tokens_do_not_count(env):
         assert torch.equal(a, b)
     assert torch.equal(outs[0][1], outs[1][1]) and torch.equal(outs[0][2], outs[1][2])
     assert outs[0][1][1].sum().item() == 100 * 2
+
+
+@pytest.mark.parametrize("P,T,H,V,E,k,weighted", [(1, 150, 200, 900, 12, 2, False), (3, 300, 256, 9001, 40, 4, True)])
+def test_reported_losses_and_gradient_of_the_hidden_states(env, P, T, H, V, E, k, weighted):
+    """What the class says of its results, in 64 bits: balance is P alpha B, dx the gradient of P F over the hidden states
+    (its router's share is checked apart, with a balance loss that outweighs the distillation)."""
+    torch, g = env
+    from gradient_allreduce_homomorphic_gb300.student import StudentStep
+
+    head, router, hidden, index, teacher = make(torch, P, T, H, V, E, 8, 64)
+    weight = valid = None
+    gen = torch.Generator(device="cuda").manual_seed(65)
+    if weighted:
+        weight = [torch.rand(T, generator=gen, device="cuda") / T for _ in range(P)]
+        valid = [(torch.rand(T, generator=gen, device="cuda") < 0.9).to(torch.uint8) for _ in range(P)]
+    for alpha in (0.5, 5000.0):
+        step = StudentStep(head, router, workers=P, tokens=T, k=k, alpha=alpha, tau=1.5)
+        step.run(1, hidden, index, teacher, weight, valid)
+        torch.cuda.synchronize()
+        x = [h.double().requires_grad_() for h in hidden]
+        W, R = head.double(), router.double()
+        on = [torch.ones(T, device="cuda").double() if valid is None else v.double() for v in valid or hidden]
+        n = sum(o.sum() for o in on)
+        D, mean_p = [], 0.0
+        for w in range(P):
+            logq = torch.log_softmax(x[w] @ W.t() / 1.5, 1).gather(1, index[w].long())
+            p = torch.softmax(teacher[w].double() / 1.5, 1)
+            share = torch.full((T,), 1.0 / T, device="cuda").double() if weight is None else weight[w].double()
+            D.append((share * (p * (torch.log(p) - logq)).sum(1)).sum())
+            mean_p = mean_p + (on[w][:, None] * torch.softmax(x[w] @ R.t(), 1)).sum(0) / n
+            losses = (share * step.loss[w].double()).sum().item()
+            assert abs(losses - D[w].item()) <= 0.05 * D[w].item()
+        B = E * ((step.counts.sum(0).double() / (k * n)) * mean_p).sum()
+        assert abs(step.balance.item() - P * alpha * B.item()) <= 0.02 * P * alpha * B.item()
+        (sum(D) / P + alpha * B).backward()
+        for w in range(P):
+            assert ((step.dx[w].double() - P * x[w].grad).norm() / (P * x[w].grad).norm()).item() <= 0.15
+    assert g.gar_sync_status() == 0
