@@ -783,6 +783,7 @@ int check(const void *z, int32_t dtype, int64_t rows, int64_t vocab, int64_t ldz
         return fail(GAR_EINVAL, "rows=%lld vocab=%lld k=%d (1 <= k <= %d)", static_cast<long long>(rows),
                     static_cast<long long>(vocab), k, kMaxTop);
     if (!(tau > 0.0f) || !(tau <= 3.0e38f)) return fail(GAR_EINVAL, "tau must be positive and finite");
+    if (!(kLog2e * (1.0f / tau) <= 3.4e38f)) return fail(GAR_EINVAL, "tau is too small: log2(e) / tau overflows, and equal logits would give NaN");
     if (rows == 0) return GAR_OK;
     if (!z || !index || !teacher) return fail(GAR_EINVAL, "NULL argument");
     if (ldz < vocab || (dz && lddz < vocab)) return fail(GAR_EINVAL, "a row stride is below the vocabulary");

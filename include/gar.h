@@ -735,6 +735,8 @@ int gar_fp8_matmul(const uint8_t *a, int64_t lda, const uint8_t *a_scale, int32_
  *   z            device, rows x vocab fp32 or bf16 (dtype), row stride ldz
  *   index        device, [rows, k] int32, 1 <= k <= 1024
  *   teacher      device, [rows, k] fp32 logits
+ *   tau          positive, such that log2(e) / tau is a finite fp32 (4.3e-39 on), up
+ *                to 3e38
  *   weight       device, [rows] fp32: the gradient of the total loss with
  *                respect to each row's (tau^2 / rows for the mean scaled by
  *                tau^2); NULL: 1

@@ -244,3 +244,14 @@ def test_balance_token_limit(gar, P):
     tokens = ((1 << 26) - 1) // P
     assert lib.gar_balance_loss(table, P, tokens, 8, 8, 0, 2, None, 0.1, table, B, D, None, 0, V(0x10004), 1 << 16,
                                 NULL) == gar.GAR_EALIGN
+
+
+@pytest.mark.parametrize("tau", [1e-45, 1e-39, 4e-39])
+def test_distill_refuses_a_temperature_without_a_reciprocal(gar, tau):
+    """log2(e) / tau would be infinite, and equal logits NaN."""
+    lib = gar.load()
+    odd = V(0x10002)  # misaligned, so that nothing is launched whatever the temperature
+    args = (A, 0, 3, 10, 10, odd, D, 2)
+    assert lib.gar_distill_loss(*args, tau, NULL, S, T, NULL, 0, NULL) == gar.GAR_EINVAL
+    assert lib.gar_distill_grad(*args, tau, NULL, S, T, 10, NULL) == gar.GAR_EINVAL
+    assert lib.gar_distill_loss(*args, 4.5e-39, NULL, S, T, NULL, 0, NULL) == gar.GAR_EALIGN
