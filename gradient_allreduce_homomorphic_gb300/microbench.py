@@ -18,7 +18,7 @@ of THC's training process over P workers: error feedback, rotation, range,
 non-uniform THC, inverse rotation, error-feedback update; separate calls, or
 the fused ones as training.TrainingStep runs them, the workers' chains over
 --streams side streams), and the operators that a worker's gradients come from: fp8_quantize (--rows x --cols values,
-both orders), fp8_matmul (--rows x --cols, summed over --depth), distill and distill_split (--rows of --cols logits,
+both orders), fp8_matmul (--rows x --cols, summed over --depth; --addend: added to another matrix), distill and distill_split (--rows of --cols logits,
 --k teacher entries: loss and gradient in one call or two), balance (--P workers of --rows tokens and --cols experts,
 --k choices).  Inputs are seeded N(0, 1) draws made on the device;
 every size is chosen by the caller, so a case can be kept small enough for a
@@ -59,6 +59,7 @@ def main(argv=None):
     ap.add_argument("--rows", type=int, default=4096)
     ap.add_argument("--cols", type=int, default=8192)
     ap.add_argument("--depth", type=int, default=2048, help="fp8_matmul: the summed axis")
+    ap.add_argument("--addend", action="store_true", help="fp8_matmul: add the product to a matrix of its size")
     ap.add_argument("--streams", type=int, default=2,
                     help="train_step_fused: side streams the workers' chains go round-robin over")
     ap.add_argument("--flush", action="store_true",
@@ -299,15 +300,16 @@ def main(argv=None):
             fn = lambda: g.gar_fp8_quantize(x, q, sc, qt, st)  # noqa: E731
             nbytes = rows * cols * (size + 2) + sc.numel() + st.numel()
         elif a.case == "fp8_matmul":
-            # algorithmic bytes: both operands read, the product written
+            # algorithmic bytes: both operands read, the product written, the addend read
             qs = []
             for r in (rows, cols):
                 q, sc = g.fp8_matrix(r, a.depth)
                 g.gar_fp8_quantize(torch.randn((r, a.depth), device=dev), q, sc)
                 qs += [q, sc]
             d = torch.empty((rows, cols), dtype=dt, device=dev)
-            fn = lambda: g.gar_fp8_matmul(*qs, d)  # noqa: E731
-            nbytes = (rows + cols) * a.depth + rows * cols * size
+            c = torch.randn((rows, cols), device=dev).to(dt) if a.addend else None
+            fn = lambda: g.gar_fp8_matmul(*qs, d, c=c)  # noqa: E731
+            nbytes = (rows + cols) * a.depth + rows * cols * size * (2 if a.addend else 1)
             flops = 2 * rows * cols * a.depth
         elif a.case == "balance":
             # algorithmic bytes: logits read once, their gradient and the choices written
