@@ -794,6 +794,8 @@ def gar_balance_workspace_bytes(P: int) -> int:
 
 def _worker_fits(t, name, shape, stride, dtype):
     """Whether one worker's tensor is as asked; what _workers' quick comparison turned down may still be."""
+    if t is None:
+        raise GarError(GAR_EINVAL, f"{name} lacks a worker's tensor")
     if not t.is_cuda:
         _dev(t)
     if t.dtype != dtype and not (dtype is _UINT8 and t.element_size() == 1):
@@ -813,11 +815,11 @@ def _workers(given, name, P, shape, dtype):
         raise GarError(GAR_EINVAL, f"{name} has {len(tensors)} tensors, not {P}")
     stride = given.checked.get((shape, dtype)) if table else None
     if stride is None:
-        if any(t is None for t in tensors):
-            raise GarError(GAR_EINVAL, f"{name} lacks a worker's tensor")
+        if tensors[0] is None:
+            _worker_fits(None, name, shape, None, dtype)
         stride, ptrs = tensors[0].stride(), []
         for t in tensors:
-            if t.dtype is not dtype or t.shape != shape or not t.is_cuda or t.stride() != stride:
+            if t is None or t.dtype is not dtype or t.shape != shape or not t.is_cuda or t.stride() != stride:
                 _worker_fits(t, name, shape, stride, dtype)
             ptrs.append(t.data_ptr())
         if table:

@@ -231,6 +231,9 @@ def test_one_token_of_strided_elements(gar, binding, table):
 def test_no_workers(gar, binding):
     torch, tensor, call, refused = binding
     assert refused([], []) == refused([], [], table=True) == refused([None], [None]) == gar.GAR_EINVAL
+    z, choice = [tensor(6, 8) for _ in range(2)], [tensor(6, 2, dtype=torch.int32) for _ in range(2)]
+    for bad in ([None, choice[1]], [choice[0], None]):
+        assert refused(z, bad) == gar.GAR_EINVAL
 
 
 @pytest.mark.parametrize("P", [1, 2, 8, 64])
