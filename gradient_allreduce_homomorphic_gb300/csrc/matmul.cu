@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads) matmul_kernel(const __grid_constant_
 //
 // Bound by the tensor cores at the clock that the power limit leaves them:
 // 16384 x 4096 x 8192 to fp32 325 us, 3380 TFLOP/s (tensor pipe active in 85 %
-// of the cycles, SM clock 1.70 GHz of 2.07), with an fp32 addend 364 us; 4096 x
+// of the cycles, SM clock 1.70 GHz of 2.07), with an fp32 addend 348 us; 4096 x
 // 8192 x 2048 to bf16 53 us, 2600 TFLOP/s (65 %: 16 chunks a tile leave its
 // beginning and the kernel's, 5.8 us, in sight).
 constexpr int kPairThreads = 384;  // warps 0-3 and 4-11 epilogue

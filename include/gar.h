@@ -728,8 +728,9 @@ int gar_fp8_matmul(const uint8_t *a, int64_t lda, const uint8_t *a_scale, int32_
  *   lse  = log sum_v exp(z_v / tau)
  *   loss = sum_j p_j (log p_j + lse - z_{index_j} / tau)
  *   dz_v = weight / tau * (exp(z_v / tau - lse) - sum of p_j with index_j = v)
- * An entry is present if its index lies in [0, vocab) and its logit is above
- * -inf; an index may occur more than once.  A row of weight 0 or without an
+ * An entry is present if its index lies in [0, vocab) and its logit is not -inf;
+ * an index may occur more than once, and a NaN logit makes the row's loss, and
+ * its gradient at the entries, NaN.  A row of weight 0 or without an
  * entry has loss 0, lse 0 and gradient 0, whatever its z.  A student
  * logit of -inf has probability 0 (loss +inf where the teacher gives it any).
  *   z            device, rows x vocab fp32 or bf16 (dtype), row stride ldz
@@ -743,7 +744,10 @@ int gar_fp8_matmul(const uint8_t *a, int64_t lda, const uint8_t *a_scale, int32_
  *   loss, lse    device, out, [rows] fp32
  *   dz           device, out, of z's type, row stride lddz; NULL: loss only;
  *                may be z itself (same row stride)
- * loss and lse do not depend on whether dz is asked for, nor on timing.
+ * loss and lse do not depend on whether dz is asked for, nor on timing.  Sums
+ * are fp32; of bf16 rows whose maximum / tau lies within 177 of 0 the powers'
+ * exponents are formed in one fma, which may put 1.1e-5 of the sum into lse and
+ * loss (2.1e-5 of it into dz, itself rounded to bf16).
  * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA; on the device
  * GAR_STATUS_TIMEOUT. */
 int gar_distill_loss(const void *z, int32_t dtype, int64_t rows, int64_t vocab, int64_t ldz, const int32_t *index,

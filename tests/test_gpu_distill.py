@@ -350,3 +350,24 @@ def test_rows_at_the_limit_of_two_ctas_an_sm(env, vocab, dtype):
     check(torch, g, zt, index, teacher, weight, 1.1, "fused")
     check(torch, g, zt, index, teacher, weight, 1.1, "split")
     assert g.gar_sync_status() == 0
+
+
+@pytest.mark.parametrize("rows,vocab", [(5, 900), (5, 40000), (300, 50001)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_teachers_nan_shows(env, rows, vocab, dtype):
+    """A NaN among a row's present entries makes its loss, and its gradient at the entries, NaN; absent ones (an index
+    outside the vocabulary) and rows without weight do not see it."""
+    torch, g = env
+    z, index, teacher, weight = problem(rows, vocab, 8, 16)
+    teacher[1, 2] = teacher[2, 3] = teacher[3, 0] = np.nan
+    index[2, 3] = -1
+    weight[3] = 0.0
+    zt = device(torch, z, dtype)
+    to = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    loss, lse, dz = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"), torch.empty_like(zt)
+    g.gar_distill_loss(zt, to(index), to(teacher), 1.0, loss, lse, dz=dz, weight=to(weight))
+    only = torch.arange(rows, device="cuda") == 1
+    assert torch.equal(torch.isnan(loss), only) and not torch.isnan(lse).any()
+    assert torch.equal(torch.isnan(dz).any(1), only)
+    assert torch.isnan(dz[1, torch.from_numpy(index[1].astype(np.int64)).cuda()]).all() and torch.isnan(dz[1]).sum().item() == 8
+    assert loss[3].item() == 0.0 and (dz[3] == 0).all()
