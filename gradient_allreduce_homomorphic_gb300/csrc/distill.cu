@@ -431,7 +431,9 @@ __global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kerne
     __shared__ MaxSum of_warps[kMode == kLossOnly ? kMaxSlots : 1][kMaxCluster][8];
     __shared__ __align__(8) MaxSum pairs[kMeets][kMaxCluster];
     __shared__ int failed;
-    constexpr int kArrays = sizeof(bars) + sizeof(header) + sizeof(partial) + sizeof(of_warps) + sizeof(pairs) + sizeof(failed);
+    __shared__ uint32_t exchanged;  // rows whose pairs this CTA's cluster exchanged
+    constexpr int kArrays =
+        sizeof(bars) + sizeof(header) + sizeof(partial) + sizeof(of_warps) + sizeof(pairs) + sizeof(failed) + sizeof(exchanged);
     constexpr int kStatic = (kArrays + 127) / 128 * 128;  // the dynamic part behind them starts on 128 bytes
     static_assert(kSharedBytes + kStatic <= kCtaBytes && 2 * (two_room(kMode) + kStatic + kReserved) <= kSmBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -657,6 +659,7 @@ __global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kerne
             if (live) ++meet;
             if (++e == E) e = 0, eturn ^= 1;
         }
+        if (threadIdx.x == 0) exchanged = meet;
     } else {
         const float c = kLog2e * p.inv_tau;
         constexpr int kThreads = 32 * kSecond;
@@ -772,7 +775,15 @@ __global__ void __launch_bounds__(stream_threads(kMode), 2) distill_stream_kerne
         }
     }
     __syncthreads();
-    if (exchange) cluster_barrier();  // no CTA leaves while another may write its pair
+    if (exchange) {
+        cluster_barrier();  // no CTA leaves while another may write its pair
+        // The second group has waited for every pair, unless a wait ran out: the last ones of each barrier may be on their way.
+        if (threadIdx.x == 0 && failed)
+            for (uint32_t at = 0; at < kMeets && at < exchanged; ++at) {
+                int given_up = 0;
+                mbar_wait(met + 8 * at, ((exchanged - 1 - at) / kMeets) & 1, &given_up);
+            }
+    }
     if (threadIdx.x == 0 && failed && p.status) atomicOr(p.status, static_cast<unsigned int>(GAR_STATUS_TIMEOUT));
 }
 

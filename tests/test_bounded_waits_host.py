@@ -49,3 +49,13 @@ def test_shared_flags_are_read_once_for_a_warp():
     body = kernel("distill.cu", "distill_stream_kernel(")
     reads = re.findall(r"[^\n]*\b(?:h|header\[e\])\.live\b(?!\s*=[^=])[^\n]*", body)
     assert len(reads) == 2 and all("__any_sync(0xFFFFFFFFu," in line for line in reads), reads
+
+
+def test_no_cta_of_a_cluster_leaves_before_its_pairs_have_come():
+    """A wait that ran out skips the second group's waits for them: behind the cluster barrier they are waited for with a
+    limit of their own."""
+    body = kernel("distill.cu", "distill_stream_kernel(")
+    assert "st.async" in body
+    end = body[body.rindex("__syncthreads();"):]
+    assert end.index("cluster_barrier();") < end.index("failed)") < end.index("int given_up = 0;") < end.index("mbar_wait(met + 8 * at,")
+    assert "&given_up" in end
