@@ -104,6 +104,10 @@ _SIGNATURES = {
     "gar_balance_workspace_bytes": (C.c_size_t, [_i32]),
     "gar_balance_loss": (C.c_int, [_vp, _i32, _i64, _i32, _i64, _i32, _i32, _vp, C.c_float, _vp, _vp, _vp, _vp, _i64,
                                    _vp, C.c_size_t, _vp]),
+    "gar_vocab_workspace_bytes": (C.c_size_t, [_i64, _i64, _i64, _i32]),
+    "gar_vocab_loss": (C.c_int, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "gar_vocab_grad": (C.c_int, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp,
+                                 _i64, _i32, _vp, C.c_size_t, _vp]),
 }
 
 
@@ -848,6 +852,62 @@ def gar_balance_loss(z, k: int, alpha: float, choice, counts, loss, workspace, d
     _call("gar_balance_loss", za, P, tokens, experts, ldz, dtype, k, va, alpha, ca,
           _vector(counts, "counts", _INT32, P * experts), _vector(loss, "loss", _FLOAT32, 1), da, lddz, _dev(workspace),
           workspace.numel() * workspace.element_size(), _stream(stream))
+
+
+# --------------------------------- the vocabulary layer's cross entropy
+def gar_vocab_workspace_bytes(rows: int, vocab: int, hidden: int, dw_dtype=None) -> int:
+    """Bytes for gar_vocab_loss and gar_vocab_grad; dw_dtype: torch.float32 or
+    bfloat16 (None: bfloat16)."""
+    if not _FLOATS:
+        _types()
+    if dw_dtype is not None and dw_dtype not in _FLOATS:
+        raise GarError(GAR_EDTYPE, f"dw is {dw_dtype}, not one of {', '.join(map(str, _FLOATS))}")
+    return int(load().gar_vocab_workspace_bytes(rows, vocab, hidden, GAR_BF16 if dw_dtype is None else _FLOATS[dw_dtype]))
+
+
+def _vocab_args(x, w, target, weight):
+    dtype = _code(x, _FLOATS, "x")
+    if w.dtype != x.dtype:
+        raise GarError(GAR_EDTYPE, f"w is {w.dtype}, x {x.dtype}")
+    rows, hidden = _two_dims(x, "x")
+    vocab = _two_dims(w, "w")[0]
+    xp, ldx = _matrix(x, "x", rows, hidden)
+    wp, ldw = _matrix(w, "w", vocab, hidden)
+    return rows, vocab, hidden, (xp, ldx, wp, ldw, dtype, _vector(target, "target", _INT32, rows),
+                                 None if weight is None else _vector(weight, "weight", _FLOAT32, rows), rows, vocab, hidden)
+
+
+def gar_vocab_loss(x, w, target, loss, lse, workspace, weight=None, stream=None):
+    """Cross entropy of a vocabulary layer, logits x w^T, without its logits: x
+    [rows, hidden] and w [vocab, hidden] bf16, target [rows] int32; loss and lse
+    [rows] fp32.  Rows with a target outside the vocabulary or weight 0 do not
+    count (0)."""
+    rows, _, _, head = _vocab_args(x, w, target, weight)
+    _call("gar_vocab_loss", *head, _vector(loss, "loss", _FLOAT32, rows), _vector(lse, "lse", _FLOAT32, rows),
+          _dev(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+
+
+def gar_vocab_grad(x, w, target, lse, dx, dw, workspace, weight=None, addend=None, stream=None):
+    """The gradient of sum(weight * loss) from the lse of gar_vocab_loss: dx
+    [rows, hidden] bf16 and dw [vocab, hidden] fp32 or bf16 (either may be None);
+    addend, of dw's type, is added to dw (it may be dw)."""
+    rows, vocab, hidden, head = _vocab_args(x, w, target, weight)
+    dxp = dwp = ap = None
+    lddx = lddw = lda = 0
+    dw_type = GAR_BF16
+    if dx is not None:
+        if dx.dtype != x.dtype:
+            raise GarError(GAR_EDTYPE, f"dx is {dx.dtype}, x {x.dtype}")
+        dxp, lddx = _matrix(dx, "dx", rows, hidden)
+    if dw is not None:
+        dw_type = _code(dw, _FLOATS, "dw")
+        dwp, lddw = _matrix(dw, "dw", vocab, hidden)
+    if addend is not None:
+        if dw is None or addend.dtype != dw.dtype:
+            raise GarError(GAR_EDTYPE, f"addend is {addend.dtype}, dw {None if dw is None else dw.dtype}")
+        ap, lda = _matrix(addend, "addend", vocab, hidden)
+    _call("gar_vocab_grad", *head, _vector(lse, "lse", _FLOAT32, rows), dxp, lddx, ap, lda, dwp, lddw, dw_type,
+          _dev(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
 
 
 __all__ = [n for n in dir() if n.startswith(("gar_", "GAR_"))] + ["GarError", "FusionPlan", "PtrTable", "load",

@@ -29,6 +29,7 @@
 #include "fp8.cuh"
 #include "launch.cuh"
 #include "tensorcore.cuh"
+#include "tensormap.cuh"
 
 namespace gar {
 namespace {
@@ -542,36 +543,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp == 1) tmem_free<2>(tmem, 512);
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static std::atomic<void *> fn{nullptr};
-    void *f = fn.load(std::memory_order_acquire);
-    if (!f) {
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            return nullptr;
-        fn.store(f, std::memory_order_release);
-    }
-    return reinterpret_cast<EncodeTiled>(f);
-}
-
 // Map of the codes [rows, K] (row stride ld bytes) in boxes of `box` rows x 128 bytes.
 int encode(CUtensorMap *map, const uint8_t *q, int64_t rows, int64_t K, int64_t ld, int box) {
-    EncodeTiled fn = encode_tiled();
-    if (!fn) return fail(GAR_ECUDA, "cuTensorMapEncodeTiled is not available");
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
-    const cuuint32_t boxes[2] = {kKC, static_cast<cuuint32_t>(box)};
-    const cuuint32_t elem[2] = {1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(q), dims, strides, boxes, elem,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(GAR_ECUDA, "cuTensorMapEncodeTiled: %d", static_cast<int>(r));
-    return GAR_OK;
+    return encode_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, rows, ld, kKC, box);
 }
 
 // Clusters of `splits` CTAs that the device holds at one time (its SMs come in

@@ -193,6 +193,20 @@ __device__ __forceinline__ void tc_mma_mxf8(uint32_t d, uint64_t a, uint64_t b, 
             "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
             : "memory");
 }
+// Instruction descriptor of a bf16 product with fp32 sums (m, n: the tile's rows
+// and columns; mn_a, mn_b: whether an operand lies with its rows, not k, along
+// the 128 bytes of a swizzled line).
+__host__ __device__ constexpr uint32_t bf16_idesc(uint32_t m, uint32_t n, uint32_t mn_a, uint32_t mn_b) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (mn_a << 15) | (mn_b << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+// By a CTA pair (cta_group::2).
+__device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 // 32 columns of this warp's 32 lanes (asynchronous until tc_wait_ld).
 __device__ __forceinline__ void tc_load32(float (&v)[32], uint32_t taddr) {
     uint32_t *r = reinterpret_cast<uint32_t *>(v);

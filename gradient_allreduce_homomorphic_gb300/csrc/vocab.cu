@@ -1,0 +1,696 @@
+// vocab.cu -- softmax cross entropy of a vocabulary layer without its logits:
+// gar_vocab_loss, gar_vocab_grad.
+//
+//   z[t][v] = sum_h x[t][h] w[v][h]              (bf16 operands, fp32 sums)
+//   lse[t]  = log sum_v exp z[t][v],  loss[t] = lse[t] - z[t][target[t]]
+//   g[t][v] = weight[t] (exp(z[t][v] - lse[t]) - [v = target[t]])
+//   dx = g w,   dw = g^T x (+ addend)
+//
+// The loss is one pass of tensor-core tiles whose epilogue keeps, per row, the
+// running maximum and sum over a run of vocabulary tiles; the runs' pairs are
+// joined by a second, small kernel.  The gradient goes piece by piece of the
+// vocabulary: the piece's logits again, g from them in the epilogue (bf16, in
+// the workspace), then the piece's rows of dw and its share of dx.  So a loss
+// and its gradient take four products where keeping the logits would take
+// three, and no more than a piece of g exists at a time.
+//
+// g is rounded to bf16 as an operand of the products: of a bf16 gradient that is
+// another error of the size of the result's own rounding.  An fp32 dw takes g as
+// the sum of two bf16 values (16 bits and more of it), a product of twice the
+// length, so that its error is what the fp32 sums leave.
+//
+// All products run on one kernel of persistent CTA pairs (cta_group::2): tiles
+// of 256 x 256, two accumulators in tensor memory, so that a tile's epilogue
+// overlaps the next one's products.  Operands are loaded as they lie: the
+// contraction runs along the rows of x and w for the logits, along their
+// columns for dw and dx, which the tensor core takes as "MN-major" operands;
+// nothing is transposed in memory.
+#include <algorithm>
+#include <atomic>
+#include <cfloat>
+
+#include "fp8.cuh"
+#include "launch.cuh"
+#include "tensorcore.cuh"
+#include "tensormap.cuh"
+
+namespace gar {
+namespace {
+
+constexpr int kTile = 256;    // rows and columns of a pair's tile
+constexpr int kK = 64;        // k per chunk: one swizzled line of bf16
+constexpr int kStages = 6;
+constexpr int kOperand = 128 * kK * 2;  // bytes of one operand of a stage, of each CTA
+constexpr int kStage = 2 * kOperand;
+constexpr int kThreads = 320;  // warp 0 loads, warp 1 issues products, warps 2-9 epilogue
+constexpr int kSmem = 1024 + kStages * kStage;
+// Chunks that an accumulator adds at most for an fp32 result: the tensor core's additions round toward zero, so a sum's
+// error grows with its length (8e-7 of the result at 8192 k).
+constexpr int kSegment = 8192 / kK;
+
+enum { kLoss, kGradient, kWeights, kInputs };
+
+struct VocabParams {
+    int64_t items;       // handed out in order
+    int64_t tiles_m;     // tiles along the lanes: rows of x (logits), hidden (dw, dx)
+    int64_t tiles_n;     // along the columns: vocabulary (logits, dw), rows of x (dx)
+    int32_t runs;        // a run: consecutive column tiles of one item
+    int32_t splits;      // parts of k (dx)
+    int32_t chunks;      // of 64 k, of one part of g
+    int32_t parts;       // of g: 1, or 2 along k (fp32 dw)
+    int64_t rows, hidden, vocab;
+    int64_t first, cols;  // the piece's columns
+    const int32_t *target;
+    const float *weight, *lse;
+    float2 *stats;       // [rows][2 runs]: maximum, sum
+    float *at_target;    // [rows]
+    uint16_t *g, *g_low;
+    int64_t ldg;
+    void *out;           // dw, dx or its partial sums
+    const void *addend;
+    int64_t ld_out, ld_addend, split_stride;
+    unsigned int *status;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Whether a row counts: a weight, and a target of the vocabulary.
+__device__ __forceinline__ bool counts(const int32_t *target, const float *weight, int64_t vocab, int64_t t) {
+    return target[t] >= 0 && target[t] < vocab && (!weight || weight[t] != 0.0f);
+}
+
+// After a wait ran out: the copies into the last `issued` stages before stage
+// s have to land before the CTA ends.
+__device__ __noinline__ void drain_stages(uint32_t full, int issued, uint32_t s, uint32_t turn) {
+    for (; issued > 0; --issued) {
+        if (s == 0) s = kStages, turn ^= 1;
+        --s;
+        int given_up = 0;
+        mbar_wait(full + 8 * s, turn ^ 1, &given_up);
+    }
+}
+
+// An item: tile m, column tiles n0 .. n1, chunks c0 .. c1.  Runs of 8 tiles of
+// rows by all column runs, so that the pairs at work share operands in L2.
+struct Item {
+    int64_t m, run, n0, n1;
+    int32_t c0, c1, split;
+};
+__device__ __forceinline__ Item item_of(const VocabParams &p, int64_t i) {
+    const int64_t tiles = p.tiles_m * p.runs;
+    Item it;
+    it.split = static_cast<int32_t>(i / tiles);
+    i -= it.split * tiles;
+    const int64_t per = 8 * static_cast<int64_t>(p.runs), group = i / per, in = i % per;
+    const int64_t wide = p.tiles_m - group * 8 < 8 ? p.tiles_m - group * 8 : 8;
+    it.m = group * 8 + in % wide;
+    it.run = in / wide;
+    it.n0 = p.tiles_n * it.run / p.runs, it.n1 = p.tiles_n * (it.run + 1) / p.runs;
+    const int64_t all = static_cast<int64_t>(p.chunks) * p.parts;
+    it.c0 = static_cast<int32_t>(all * it.split / p.splits), it.c1 = static_cast<int32_t>(all * (it.split + 1) / p.splits);
+    return it;
+}
+
+// 32 accumulator columns to rows 0 .. count of d (ld apart), c added where given.
+template <typename T>
+__device__ __forceinline__ void store_columns(const float (&v)[32], T *d, int64_t ld, const T *c, int64_t ldc, int count) {
+    if (c) {
+        float x[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = j < count ? load_f32(c + j * ldc) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < count) store_f32(d + j * ld, v[j] + x[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < count) store_f32(d + j * ld, v[j]);
+    }
+}
+
+// One epilogue warp's state over an item: a row's running maximum and sum (loss),
+// or what its gradient takes.
+struct Row {
+    float top, sum;     // kLoss
+    int32_t target;     // -1: none
+    float lse, weight;  // kGradient; a row that does not count has target -1 and weight 0
+};
+
+// 32 logits of a row (vocabulary columns col ..) into its running maximum and sum.
+__device__ __forceinline__ void take_logits(const VocabParams &p, float (&v)[32], Row &r, int64_t t, int64_t col) {
+    if (col + 32 > p.vocab) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (col + j >= p.vocab) v[j] = -INFINITY;
+    }
+    const int64_t at = r.target - col;
+    if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {
+        float z = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (at == j) z = v[j];
+        if (at >= 0 && at < 32) p.at_target[t] = z;
+    }
+    float top = r.top;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
+    float s[4] = {r.sum * exp2_fast((r.top - top) * kLog2e), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 32; ++j) s[j & 3] += exp2_fast((v[j] - top) * kLog2e);
+    r.top = top, r.sum = (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// The same logits to g; col counts from the piece's first column.
+template <bool kTwoParts>
+__device__ __forceinline__ void give_gradient(const VocabParams &p, float (&v)[32], const Row &r, int64_t t, int64_t col) {
+    const int64_t at = r.target - p.first - col;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = exp2_fast((v[j] - r.lse) * kLog2e);
+    if (__any_sync(0xFFFFFFFFu, r.target >= 0 && at >= 0 && at < 32)) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (r.target >= 0 && at == j) v[j] -= 1.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = r.target >= 0 ? v[j] * r.weight : 0.0f;
+    if (t >= p.rows) return;
+    uint4 *to = reinterpret_cast<uint4 *>(p.g + t * p.ldg + col);
+    uint4 *low = reinterpret_cast<uint4 *>(p.g_low + t * p.ldg + col);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t w[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = v[q * 8 + 2 * i], b = v[q * 8 + 2 * i + 1];
+            w[i] = pack_bf16x2(a, b);
+            if (kTwoParts) l[i] = pack_bf16x2(a - bf16_lo(w[i]), b - bf16_hi(w[i]));
+        }
+        to[q] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (kTwoParts) low[q] = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+}
+
+template <int kMode, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    vocab_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                         const __grid_constant__ CUtensorMap map_b2, const __grid_constant__ VocabParams p) {
+    constexpr bool kMnA = kMode == kWeights || kMode == kInputs, kMnB = kMode == kWeights;
+    constexpr uint32_t kIdesc = bf16_idesc(kTile, kTile, kMnA, kMnB);
+    // 16 k of a K-major operand are 32 bytes of each line; of an MN-major one two groups of eight lines of 128 bytes
+    constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
+    const int seg_chunks = kMode == kWeights && sizeof(T) == 4 ? kSegment : 0x7FFFFFFF;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int failed;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages, drained = acc_full + 16,
+                   done = drained + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_cta_rank();
+    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    let_next_begin();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * kStages; ++i) mbar_init(full + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(drained + 8 * i, 16);  // eight epilogue warps of each CTA
+        }
+        mbar_init(done, 1);
+        failed = 0;
+        mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc<2>(smem_u32(&tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();
+    tc_fence_after();
+    after_previous();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
+        const uint32_t lead_full = cluster_map(full, 0);
+        uint32_t s = 0, turn = 1;  // the first turn finds every stage free
+        int issued = 0;
+        bool ok = true;
+        for (int64_t i = first; i < p.items && ok; i += step) {
+            const Item it = item_of(p, i);
+            const int32_t a = static_cast<int32_t>(it.m * kTile + 128 * rank);
+            for (int64_t n = it.n0; n < it.n1 && ok; ++n) {
+                const int32_t b = static_cast<int32_t>(n * kTile + 128 * rank);
+                for (int32_t c = it.c0; c < it.c1; ++c) {
+                    if (!(ok = mbar_wait(empty + 8 * s, turn, &failed))) break;
+                    const uint32_t dst = base + s * kStage, bar = lead_full + 8 * s;
+                    const bool second = kMode == kWeights && c >= p.chunks;
+                    const int32_t k = (second ? c - p.chunks : c) * kK;
+                    const CUtensorMap *of_b = second ? &map_b2 : &map_b;
+                    if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * kStage);
+                    if (kMnA) {
+                        tma_load_2d_pair(dst, &map_a, bar, a, k);
+                        tma_load_2d_pair(dst + kOperand / 2, &map_a, bar, a + 64, k);
+                    } else {
+                        tma_load_2d_pair(dst, &map_a, bar, k, a);
+                    }
+                    if (kMnB) {
+                        tma_load_2d_pair(dst + kOperand, of_b, bar, b, k);
+                        tma_load_2d_pair(dst + kOperand + kOperand / 2, of_b, bar, b + 64, k);
+                    } else {
+                        tma_load_2d_pair(dst + kOperand, of_b, bar, k, b);
+                    }
+                    issued = issued < kStages ? issued + 1 : kStages;
+                    if (++s == kStages) s = 0, turn ^= 1;
+                }
+            }
+        }
+        // both CTAs' copies count on the first one's barriers; the other waits at the cluster barrier below
+        if (!ok && rank == 0) drain_stages(full, issued, s, turn);
+    } else if (warp == 1 && rank == 0) {
+        const uint64_t desc_a = smem_desc(base, kMnA ? kOperand / 2 : 16, 1024, 2);
+        const uint64_t desc_b = smem_desc(base + kOperand, kMnB ? kOperand / 2 : 16, 1024, 2);
+        uint32_t s = 0, turn = 0, seq = 0;
+        bool ready = false;  // whether the next stage was seen to be full already
+        for (int64_t i = first; i < p.items; i += step) {
+            const Item it = item_of(p, i);
+            for (int64_t n = it.n0; n < it.n1; ++n) {
+                for (int32_t c0 = it.c0; c0 < it.c1; ++seq) {
+                    const int32_t c1 = it.c1 - c0 > seg_chunks ? c0 + seg_chunks : it.c1;
+                    const uint32_t acc = tmem + (seq & 1) * kTile;
+                    if (seq >= 2) mbar_wait_cluster(drained + 8 * (seq & 1), ((seq - 2) >> 1) & 1, &failed);
+                    for (int32_t c = c0; c < c1; ++c) {
+                        if (!ready) mbar_wait(full + 8 * s, turn, &failed);
+                        tc_fence_after();
+                        const uint32_t next = s + 1 == kStages ? 0 : s + 1;
+                        ready = mbar_test(full + 8 * next, next ? turn : turn ^ 1);
+                        if (elect_one()) {
+                            const uint64_t da = desc_a + s * (kStage >> 4), db = desc_b + s * (kStage >> 4);
+#pragma unroll
+                            for (int k = 0; k < kK / 16; ++k)
+                                tc_mma_bf16_pair(acc, da + k * kStepA, db + k * kStepB, kIdesc, c > c0 || k > 0);
+                            tc_commit_pair(empty + 8 * s);
+                            if (c == c1 - 1) tc_commit_pair(acc_full + 8 * (seq & 1));
+                        }
+                        __syncwarp();
+                        s = next;
+                        if (s == 0) turn ^= 1;
+                    }
+                    c0 = c1;
+                }
+            }
+        }
+        if (elect_one()) tc_commit<2>(done);  // here alone: the other CTA frees its half behind the cluster barrier below
+        __syncwarp();
+        int given_up = 0;  // a wait of its own limit, for one that ran out elsewhere lets all others pass
+        mbar_wait(done, 0, &given_up);
+    } else if (warp >= 2) {
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t lead_drained = cluster_map(drained, 0);
+        uint32_t seq = 0;
+        for (int64_t i = first; i < p.items; i += step) {
+            const Item it = item_of(p, i);
+            const int64_t lane_at = it.m * kTile + 128 * rank + quarter * 32 + lane;
+            Row r{-FLT_MAX, 0.0f, -1, 0.0f, 0.0f};
+            if (kMode == kLoss && lane_at < p.rows) r.target = p.target[lane_at];
+            if (kMode == kGradient && lane_at < p.rows && counts(p.target, p.weight, p.vocab, lane_at)) {
+                r.target = p.target[lane_at];
+                r.lse = p.lse[lane_at], r.weight = p.weight ? p.weight[lane_at] : 1.0f;
+            }
+            for (int64_t n = it.n0; n < it.n1; ++n) {
+                for (int32_t c0 = it.c0; c0 < it.c1; ++seq) {
+                    const int32_t c1 = it.c1 - c0 > seg_chunks ? c0 + seg_chunks : it.c1;
+                    const uint32_t buf = seq & 1;
+                    mbar_wait(acc_full + 8 * buf, (seq >> 1) & 1, &failed);
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int j = half; j < kTile / 32; j += 2) {
+                        __syncwarp();
+                        float v[32];
+                        tc_load32(v, lanes + buf * kTile + j * 32);
+                        tc_wait_ld();
+                        if (j + 2 >= kTile / 32) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
+                        }
+                        const int64_t col = n * kTile + j * 32;
+                        if (kMode == kLoss) {
+                            if (col < p.vocab) take_logits(p, v, r, lane_at, col);
+                        } else if (kMode == kGradient) {
+                            give_gradient<sizeof(T) == 4>(p, v, r, lane_at, col);
+                        } else if (const int64_t left = (kMode == kWeights ? p.cols : p.rows) - col; lane_at < p.hidden && left > 0) {
+                            T *d = static_cast<T *>(p.out) + it.split * p.split_stride + col * p.ld_out + lane_at;
+                            const T *c = static_cast<const T *>(p.addend);
+                            int64_t ldc = p.ld_addend;
+                            if (c0 > it.c0) c = d, ldc = p.ld_out;
+                            else if (c) c += it.split * p.split_stride + col * ldc + lane_at;
+                            store_columns<T>(v, d, p.ld_out, c, ldc, left < 32 ? static_cast<int>(left) : 32);
+                        }
+                    }
+                    c0 = c1;
+                }
+            }
+            if (kMode == kLoss && lane_at < p.rows) {
+                p.stats[(lane_at * p.runs + it.run) * 2 + half] = make_float2(r.top, r.sum);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();
+    if (threadIdx.x == 0 && failed && p.status) atomicOr(p.status, static_cast<unsigned int>(GAR_STATUS_TIMEOUT));
+    if (warp == 1) tmem_free<2>(tmem, 512);
+}
+
+// A row's pairs (maximum, sum) joined, by one warp.
+__global__ void __launch_bounds__(256) vocab_join_kernel(const __grid_constant__ VocabParams p, float *loss, float *lse) {
+    let_next_begin();
+    after_previous();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (t >= p.rows) return;
+    if (!counts(p.target, p.weight, p.vocab, t)) {
+        if (lane == 0) loss[t] = 0.0f, lse[t] = 0.0f;
+        return;
+    }
+    const float2 *of = p.stats + t * p.runs * 2;
+    float top = -FLT_MAX, sum = 0.0f;
+    for (int i = lane; i < 2 * p.runs; i += 32) {
+        const float2 q = of[i];
+        const float m = fmaxf(top, q.x);
+        sum = sum * exp2_fast((top - m) * kLog2e) + q.y * exp2_fast((q.x - m) * kLog2e);
+        top = m;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, top, o), more = __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const float m = fmaxf(top, other);
+        sum = sum * exp2_fast((top - m) * kLog2e) + more * exp2_fast((other - m) * kLog2e);
+        top = m;
+    }
+    if (lane == 0) {
+        const float log_sum = logf(sum);
+        lse[t] = top + log_sum;
+        loss[t] = log_sum + (top - p.at_target[t]);
+    }
+}
+
+// x with the rows that do not count set to 0: an operand of dw, where a NaN or an
+// infinity in such a row would meet g's zeros.
+__global__ void __launch_bounds__(256)
+    vocab_live_rows_kernel(const uint16_t *x, int64_t ldx, const __grid_constant__ VocabParams p, uint16_t *to,
+                           int64_t ld_to) {
+    let_next_begin();
+    after_previous();
+    const int64_t t = blockIdx.x;
+    const bool live = counts(p.target, p.weight, p.vocab, t);
+    const int64_t pieces = p.hidden / 8;
+    for (int64_t i = threadIdx.x; i < pieces; i += 256)
+        reinterpret_cast<uint4 *>(to + t * ld_to)[i] =
+            live ? reinterpret_cast<const uint4 *>(x + t * ldx)[i] : make_uint4(0, 0, 0, 0);
+    for (int64_t h = pieces * 8 + threadIdx.x; h < p.hidden; h += 256) to[t * ld_to + h] = live ? x[t * ldx + h] : 0;
+}
+
+// dx from its partial sums, added in order.
+__global__ void __launch_bounds__(256) vocab_inputs_kernel(const float *part, const __grid_constant__ VocabParams p, uint16_t *dx, int64_t lddx) {
+    let_next_begin();
+    after_previous();
+    const int64_t n = p.rows * p.hidden;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+        float v = part[i];
+        for (int s = 1; s < p.splits; ++s) v += part[s * p.split_stride + i];
+        dx[i / p.hidden * lddx + i % p.hidden] = to_bf16(v);
+    }
+}
+
+// dw where no row is given: the addend, or 0.
+template <typename T>
+__global__ void __launch_bounds__(256) vocab_no_rows_kernel(const T *addend, int64_t ld_addend, T *dw, int64_t lddw, int64_t vocab, int64_t hidden) {
+    let_next_begin();
+    after_previous();
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < vocab * hidden; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t v = i / hidden, h = i % hidden;
+        dw[v * lddw + h] = addend ? addend[v * ld_addend + h] : T(0);
+    }
+}
+
+// ---------------------------------------------------------------------- host
+// Pairs of CTAs that the device holds at one time; looked up once.  < 1: an error, reported.
+template <int kMode, typename T>
+int resident_pairs() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return fail(GAR_ECUDA, "no current device");
+    int pairs = known[dev & 63].load(std::memory_order_relaxed);
+    if (pairs == 0) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        cudaError_t e = cudaFuncSetAttribute(vocab_product_kernel<kMode, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&pairs, vocab_product_kernel<kMode, T>, &cfg);
+        if (e != cudaSuccess || pairs < 1) return fail(GAR_ECUDA, "vocab_product_kernel: %s", cudaGetErrorString(e));
+        known[dev & 63].store(pairs, std::memory_order_relaxed);
+    }
+    return pairs;
+}
+
+template <int kMode, typename T>
+int launch(const VocabParams &p, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b2, cudaStream_t stream) {
+    const int pairs = resident_pairs<kMode, T>();
+    if (pairs < 1) return pairs;
+    const unsigned grid = 2 * static_cast<unsigned>(std::min(p.items, static_cast<int64_t>(pairs)));
+    return launch_early("vocab_product_kernel", vocab_product_kernel<kMode, T>, dim3(grid), kThreads, kSmem, 2, stream, a, b, b2, p);
+}
+
+int encode(CUtensorMap *map, const void *base, int64_t inner, int64_t outer, int64_t ld, int box_outer) {
+    return encode_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, ld * 2, kK, box_outer);
+}
+
+// Clocks of a chunk of 64 k, and of a tile's beginning and end that its neighbours do not hide.
+constexpr int64_t kChunkClocks = 520, kTileClocks = 500, kItemClocks = 2500;
+
+// Column runs of the loss pass: the count that leaves the pairs evenly busy.
+int32_t loss_runs(int64_t tiles_m, int64_t tiles_n, int64_t chunks, int64_t pairs) {
+    int64_t best = 0;
+    int32_t runs = 1;
+    for (int64_t r = 1; r <= std::min(tiles_n, std::max(int64_t{1}, 8 * pairs / tiles_m)); ++r) {
+        const int64_t clocks = ceil_div(tiles_m * r, pairs) * (ceil_div(tiles_n, r) * (chunks * kChunkClocks + kTileClocks) + kItemClocks);
+        if (r == 1 || clocks < best) best = clocks, runs = static_cast<int32_t>(r);
+    }
+    return runs;
+}
+
+// Parts of the vocabulary that dx's sums are cut into where its tiles are few.
+int32_t input_splits(int64_t tiles, int64_t chunks, int64_t pairs, int64_t elements) {
+    int64_t best = 0;
+    int32_t splits = 1;
+    for (int64_t s = 1; s <= 64 && chunks >= 4 * s; ++s) {
+        const int64_t clocks = ceil_div(tiles * s, pairs) * (ceil_div(chunks, s) * kChunkClocks + kItemClocks) +
+                               (s > 1 ? 4000 + s * elements * 8 / 3500 : 0);
+        if (s == 1 || clocks < best) best = clocks, splits = static_cast<int32_t>(s);
+    }
+    return splits;
+}
+
+constexpr int64_t kPieceBytes = int64_t{256} << 20;  // of g, at most (or 256 columns)
+
+struct Plan {
+    int64_t piece, pieces;   // columns of a piece, a multiple of the tile
+    int32_t runs, splits;
+    int64_t g, x, part, loss, grad;  // bytes
+};
+int64_t room(int64_t bytes) { return ceil_div(bytes, 256) * 256; }
+
+Plan plan_for(int64_t rows, int64_t vocab, int64_t hidden, int32_t dw_type) {
+    Plan p{};
+    const int64_t pairs = std::max(sm_count() / 2, 1), tiles_t = ceil_div(rows, int64_t{kTile}), tiles_h = ceil_div(hidden, int64_t{kTile});
+    const int64_t parts = dw_type == GAR_F32 ? 2 : 1;
+    const int64_t most = std::max(kPieceBytes / (std::max(rows, int64_t{1}) * 2 * parts) / kTile, int64_t{1}) * kTile;
+    p.pieces = ceil_div(vocab, most);
+    p.piece = ceil_div(ceil_div(vocab, p.pieces), int64_t{kTile}) * kTile;
+    p.pieces = ceil_div(vocab, p.piece);
+    p.runs = rows > 0 ? loss_runs(tiles_t, ceil_div(vocab, int64_t{kTile}), ceil_div(hidden, int64_t{kK}), pairs) : 1;
+    p.splits = rows > 0 ? input_splits(tiles_t * tiles_h, ceil_div(std::min(p.piece, vocab), int64_t{kK}), pairs, rows * hidden) : 1;
+    p.loss = room(rows * p.runs * 16) + room(rows * 4);
+    p.g = room(rows * p.piece * 2);
+    p.x = room(rows * ceil_div(hidden, 8) * 16);
+    p.part = p.splits > 1 || p.pieces > 1 ? room(rows * hidden * 4 * p.splits) : 0;
+    p.grad = p.g * parts + p.x + p.part;
+    return p;
+}
+
+int check(const void *x, int64_t ldx, const void *w, int64_t ldw, const int32_t *target, const float *weight, int64_t rows,
+          int64_t vocab, int64_t hidden, int32_t dtype) {
+    if (dtype != GAR_BF16) return fail(GAR_EDTYPE, "x and w have to be bf16, not dtype %d", dtype);
+    if (rows < 0 || vocab < 1 || hidden < 1 || rows > 0x7FFFFFFF - 1024 || vocab > 0x7FFFFFFF - 1024 || hidden > (1 << 20))
+        return fail(GAR_EINVAL, "rows=%lld vocab=%lld (from 1) hidden=%lld (1..2^20)", static_cast<long long>(rows),
+                    static_cast<long long>(vocab), static_cast<long long>(hidden));
+    if (rows == 0) return GAR_OK;
+    if (!x || !w || !target) return fail(GAR_EINVAL, "x, w or target is NULL");
+    if (ldx < hidden || ldw < hidden) return fail(GAR_EINVAL, "a row stride of x or w is below the hidden size");
+    if (!aligned(x, 16) || !aligned(w, 16) || ldx % 8 || ldw % 8)
+        return fail(GAR_EALIGN, "x, w and their row strides need 16-byte alignment");
+    if (!aligned(target, 4) || !aligned(weight, 4)) return fail(GAR_EALIGN, "target or weight is misaligned");
+    return GAR_OK;
+}
+
+// dw and the shares of dx of all pieces; T: dw's type.
+template <typename T>
+int gradient(VocabParams p, const Plan &how, const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t ldw, uint16_t *dx, int64_t lddx,
+             const T *addend, int64_t ld_addend, T *dw, int64_t lddw, uint8_t *workspace, cudaStream_t stream) {
+    const int64_t rows = p.rows, vocab = p.vocab, hidden = p.hidden, ld_live = ceil_div(hidden, 8) * 8;
+    constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
+    p.g = reinterpret_cast<uint16_t *>(workspace);
+    p.g_low = reinterpret_cast<uint16_t *>(workspace + how.g);
+    p.ldg = how.piece;
+    uint16_t *live = reinterpret_cast<uint16_t *>(workspace + kParts * how.g);
+    float *part = reinterpret_cast<float *>(workspace + kParts * how.g + how.x);
+    const int64_t tiles_t = ceil_div(rows, int64_t{kTile}), tiles_h = ceil_div(hidden, int64_t{kTile});
+    if (dw)
+        if (int rc = launch_early("vocab_live_rows_kernel", vocab_live_rows_kernel, dim3(static_cast<unsigned>(rows)), 256, 0, 1, stream, x,
+                                  ldx, p, live, ld_live))
+            return rc;
+    CUtensorMap rows_k{}, live_mn{};
+    if (int rc = encode(&rows_k, x, hidden, rows, ldx, 128)) return rc;
+    if (int rc = encode(&live_mn, live, hidden, rows, ld_live, 64)) return rc;
+    for (int64_t first = 0; first < vocab; first += how.piece) {
+        const int64_t cols = std::min(how.piece, vocab - first), tiles_v = ceil_div(cols, int64_t{kTile});
+        CUtensorMap w_k{}, w_mn{}, g_k{}, g_mn{}, low_mn{};
+        if (int rc = encode(&w_k, w + first * ldw, hidden, cols, ldw, 128)) return rc;
+        if (int rc = encode(&w_mn, w + first * ldw, hidden, cols, ldw, 64)) return rc;
+        if (int rc = encode(&g_k, p.g, cols, rows, p.ldg, 128)) return rc;
+        if (int rc = encode(&g_mn, p.g, cols, rows, p.ldg, 64)) return rc;
+        if (kParts == 2)
+            if (int rc = encode(&low_mn, p.g_low, cols, rows, p.ldg, 64)) return rc;
+        VocabParams q = p;
+        q.first = first, q.cols = cols;
+        q.tiles_m = tiles_t, q.tiles_n = tiles_v, q.runs = static_cast<int32_t>(tiles_v), q.splits = 1, q.parts = 1;
+        q.chunks = static_cast<int32_t>(ceil_div(hidden, int64_t{kK}));
+        q.items = q.tiles_m * q.runs;
+        if (int rc = launch<kGradient, T>(q, rows_k, w_k, w_k, stream)) return rc;
+        if (dw) {
+            q.tiles_m = tiles_h, q.tiles_n = tiles_v, q.runs = static_cast<int32_t>(tiles_v), q.parts = kParts;
+            q.chunks = static_cast<int32_t>(ceil_div(rows, int64_t{kK}));
+            q.items = q.tiles_m * q.runs;
+            q.out = dw + first * lddw, q.ld_out = lddw;
+            q.addend = addend ? addend + first * ld_addend : nullptr, q.ld_addend = ld_addend;
+            if (int rc = launch<kWeights, T>(q, live_mn, g_mn, kParts == 2 ? low_mn : g_mn, stream)) return rc;
+        }
+        if (dx) {
+            q.tiles_m = tiles_h, q.tiles_n = tiles_t, q.runs = static_cast<int32_t>(tiles_t), q.parts = 1, q.splits = how.splits;
+            q.chunks = static_cast<int32_t>(ceil_div(cols, int64_t{kK}));
+            q.items = q.tiles_m * q.runs * q.splits;
+            q.split_stride = rows * hidden;
+            q.out = part, q.ld_out = hidden;
+            q.addend = first > 0 ? part : nullptr, q.ld_addend = hidden;
+            if (how.part == 0) {
+                q.out = dx, q.ld_out = lddx;
+                if (int rc = launch<kInputs, uint16_t>(q, w_mn, g_k, g_k, stream)) return rc;
+            } else {
+                if (int rc = launch<kInputs, float>(q, w_mn, g_k, g_k, stream)) return rc;
+            }
+        }
+    }
+    if (dx && how.part > 0) {
+        p.splits = how.splits, p.split_stride = rows * hidden;
+        const int64_t blocks = std::min(ceil_div(rows * hidden, int64_t{1024}), static_cast<int64_t>(sm_count()) * 8);
+        return launch_early("vocab_inputs_kernel", vocab_inputs_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, 1, stream, part, p, dx,
+                            lddx);
+    }
+    return GAR_OK;
+}
+
+}  // namespace
+}  // namespace gar
+
+using namespace gar;
+
+extern "C" size_t gar_vocab_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden, int32_t dw_type) {
+    if (rows < 0 || vocab < 1 || hidden < 1 || elem_bytes(dw_type) < 0) return 0;
+    const Plan p = plan_for(rows, vocab, hidden, dw_type);
+    return static_cast<size_t>(std::max(std::max(p.loss, p.grad), int64_t{256}));
+}
+
+extern "C" int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target,
+                              const float *weight, int64_t rows, int64_t vocab, int64_t hidden, float *loss, float *lse,
+                              void *d_workspace, size_t workspace_bytes, gar_stream_t stream_) {
+    if (int rc = check(x, ldx, w, ldw, target, weight, rows, vocab, hidden, dtype)) return rc;
+    if (rows == 0) return GAR_OK;
+    const Plan how = plan_for(rows, vocab, hidden, GAR_BF16);
+    if (!loss || !lse || !d_workspace || workspace_bytes < static_cast<size_t>(how.loss))
+        return fail(GAR_EINVAL, "loss, lse or the workspace is NULL, or the workspace below %lld bytes", static_cast<long long>(how.loss));
+    if (!aligned(loss, 4) || !aligned(lse, 4) || !aligned(d_workspace, 256)) return fail(GAR_EALIGN, "loss, lse (4 bytes) or the workspace (256) is misaligned");
+    VocabParams p{};
+    p.rows = rows, p.vocab = vocab, p.hidden = hidden;
+    p.target = target, p.weight = weight;
+    p.tiles_m = ceil_div(rows, int64_t{kTile}), p.tiles_n = ceil_div(vocab, int64_t{kTile});
+    p.runs = how.runs, p.splits = 1, p.parts = 1, p.chunks = static_cast<int32_t>(ceil_div(hidden, int64_t{kK}));
+    p.items = p.tiles_m * p.runs;
+    p.stats = static_cast<float2 *>(d_workspace);
+    p.at_target = reinterpret_cast<float *>(static_cast<uint8_t *>(d_workspace) + room(rows * how.runs * 16));
+    p.status = device_status();
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    CUtensorMap a{}, b{};
+    if (int rc = encode(&a, x, hidden, rows, ldx, 128)) return rc;
+    if (int rc = encode(&b, w, hidden, vocab, ldw, 128)) return rc;
+    if (int rc = launch<kLoss, float>(p, a, b, b, stream)) return rc;
+    return launch_early("vocab_join_kernel", vocab_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, int64_t{8}))), 256, 0, 1, stream, p,
+                        loss, lse);
+}
+
+extern "C" int gar_vocab_grad(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target,
+                              const float *weight, int64_t rows, int64_t vocab, int64_t hidden, const float *lse, void *dx, int64_t lddx,
+                              const void *addend, int64_t ld_addend, void *dw, int64_t lddw, int32_t dw_type, void *d_workspace,
+                              size_t workspace_bytes, gar_stream_t stream_) {
+    if (int rc = check(x, ldx, w, ldw, target, weight, rows, vocab, hidden, dtype)) return rc;
+    const int size = elem_bytes(dw_type);
+    if (size < 0) return fail(GAR_EDTYPE, "unknown dtype %d of dw", dw_type);
+    if (!dx && !dw) return fail(GAR_EINVAL, "dx and dw are NULL");
+    if ((dx && dx == x) || (dw && dw == w)) return fail(GAR_EINVAL, "dx in place of x, or dw in place of w");
+    if (addend && !dw) return fail(GAR_EINVAL, "an addend without dw");
+    if (dw && (lddw < hidden || (addend && ld_addend < hidden))) return fail(GAR_EINVAL, "a row stride of dw or its addend is below the hidden size");
+    if (addend == dw && dw && ld_addend != lddw) return fail(GAR_EINVAL, "an addend in place of dw needs the same row stride");
+    if (!aligned(dw, size) || !aligned(addend, size)) return fail(GAR_EALIGN, "dw or its addend is misaligned");
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (rows == 0) {
+        if (!dw || (addend == dw)) return GAR_OK;
+        const unsigned blocks = static_cast<unsigned>(std::min(ceil_div(vocab * hidden, int64_t{1024}), static_cast<int64_t>(sm_count()) * 8));
+        return dw_type == GAR_F32
+                   ? launch_early("vocab_no_rows_kernel", vocab_no_rows_kernel<float>, dim3(blocks), 256, 0, 1, stream,
+                                  static_cast<const float *>(addend), ld_addend, static_cast<float *>(dw), lddw, vocab, hidden)
+                   : launch_early("vocab_no_rows_kernel", vocab_no_rows_kernel<uint16_t>, dim3(blocks), 256, 0, 1, stream,
+                                  static_cast<const uint16_t *>(addend), ld_addend, static_cast<uint16_t *>(dw), lddw, vocab, hidden);
+    }
+    if (dx && lddx < hidden) return fail(GAR_EINVAL, "the row stride of dx is below the hidden size");
+    const Plan how = plan_for(rows, vocab, hidden, dw_type);
+    if (!lse || !d_workspace || workspace_bytes < static_cast<size_t>(how.grad))
+        return fail(GAR_EINVAL, "lse or the workspace is NULL, or the workspace below %lld bytes", static_cast<long long>(how.grad));
+    if (!aligned(dx, 2) || !aligned(lse, 4) || !aligned(d_workspace, 256)) return fail(GAR_EALIGN, "dx, lse or the workspace (256 bytes) is misaligned");
+    VocabParams p{};
+    p.rows = rows, p.vocab = vocab, p.hidden = hidden;
+    p.target = target, p.weight = weight, p.lse = lse;
+    p.status = device_status();
+    const uint16_t *xh = static_cast<const uint16_t *>(x), *wh = static_cast<const uint16_t *>(w);
+    uint16_t *dxh = static_cast<uint16_t *>(dx);
+    uint8_t *ws = static_cast<uint8_t *>(d_workspace);
+    return dw_type == GAR_F32 ? gradient<float>(p, how, xh, ldx, wh, ldw, dxh, lddx, static_cast<const float *>(addend), ld_addend,
+                                                static_cast<float *>(dw), lddw, ws, stream)
+                              : gradient<uint16_t>(p, how, xh, ldx, wh, ldw, dxh, lddx, static_cast<const uint16_t *>(addend), ld_addend,
+                                                   static_cast<uint16_t *>(dw), lddw, ws, stream);
+}

@@ -796,6 +796,53 @@ int gar_balance_loss(const void *const *z, int32_t P, int64_t tokens, int32_t ex
                      float *loss, void *const *dz, int64_t lddz, void *d_workspace, size_t workspace_bytes,
                      gar_stream_t stream);
 
+/* Bytes of device workspace for gar_vocab_loss and gar_vocab_grad; dw_type: the
+ * type of dw (GAR_BF16 where dw is not asked for).  The gradient's holds a piece
+ * of the vocabulary's gradients, 256 MB of them at most (or rows x 256). */
+size_t gar_vocab_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden, int32_t dw_type);
+
+/* gar_vocab_loss -- softmax cross entropy of a vocabulary layer whose logits are
+ * never written.  For each row t of x,
+ *   z_tv   = sum_h x_th w_vh                     (bf16 values, fp32 sums)
+ *   lse_t  = log sum_v exp(z_tv)
+ *   loss_t = lse_t - z_{t, target_t}
+ * A row counts if its target lies in [0, vocab) and its weight is not 0; any other
+ * has loss 0 and lse 0, whatever its x.  A NaN or an infinity among a row's logits
+ * makes its loss NaN.  fp32 sums in tensor-core order (rounding toward zero within
+ * a product, 8e-7 of the result at hidden = 8192); the same bits in every run.
+ *   x, w         device, [rows, hidden] and [vocab, hidden] bf16 (dtype: GAR_BF16),
+ *                row strides ldx, ldw; 16-byte aligned, strides multiples of 8
+ *   target       device, [rows] int32
+ *   weight       device, [rows] fp32, here only for which rows count; NULL: all
+ *   loss, lse    device, out, [rows] fp32
+ *   d_workspace  device, 256-byte aligned, not shared with a concurrent call
+ * Sizes: rows >= 0, vocab >= 1, 1 <= hidden <= 2^20.
+ * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA; on the device
+ * GAR_STATUS_TIMEOUT. */
+int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target,
+                   const float *weight, int64_t rows, int64_t vocab, int64_t hidden, float *loss, float *lse,
+                   void *d_workspace, size_t workspace_bytes, gar_stream_t stream);
+
+/* gar_vocab_grad -- the gradient of sum_t weight_t loss_t, from the lse that
+ * gar_vocab_loss wrote for the same rows:
+ *   g_tv = weight_t (exp(z_tv - lse_t) - [v = target_t])   (0 where t does not count)
+ *   dx = g w,   dw = g^T x + addend
+ * The vocabulary is taken in pieces, their logits computed again.  g is rounded to
+ * bf16 for the products; for an fp32 dw it is the sum of two bf16 values (2^-17 of
+ * each g), at twice that product's cost.  Sums are fp32; of an fp32 dw none that
+ * the tensor cores form is over more than 8192 terms.
+ *   dx           device, out, [rows, hidden] bf16, row stride lddx, or NULL
+ *   dw           device, out, [vocab, hidden] fp32 or bf16 (dw_type), row stride
+ *                lddw, or NULL
+ *   addend       device, of dw's type, added before the rounding; NULL: none; may
+ *                be dw (same row stride)
+ * Outputs must not overlap x, w or one another.  With no rows dw is the addend or
+ * 0.  Other arguments and errors as for gar_vocab_loss. */
+int gar_vocab_grad(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target,
+                   const float *weight, int64_t rows, int64_t vocab, int64_t hidden, const float *lse, void *dx, int64_t lddx,
+                   const void *addend, int64_t ld_addend, void *dw, int64_t lddw, int32_t dw_type, void *d_workspace,
+                   size_t workspace_bytes, gar_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
