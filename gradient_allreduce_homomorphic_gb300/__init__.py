@@ -108,6 +108,18 @@ _SIGNATURES = {
     "gar_vocab_loss": (C.c_int, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, C.c_size_t, _vp]),
     "gar_vocab_grad": (C.c_int, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp,
                                  _i64, _i32, _vp, C.c_size_t, _vp]),
+    "gar_expert_rows": (_i64, [_i32, _i64, _i32, _i32, _i32, _i32]),
+    "gar_expert_workspace_bytes": (C.c_size_t, [_i32, _i64, _i32, _i32]),
+    "gar_expert_sort": (C.c_int, [_vp, _i32, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _vp, C.c_size_t, _vp]),
+    "gar_expert_gather": (C.c_int, [_vp, _i32, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _i64, _vp]),
+    "gar_expert_combine": (C.c_int, [_vp, _i64, _i64, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _i64, _vp]),
+    "gar_expert_combine_grad": (C.c_int, [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _i64,
+                                          _vp, _vp]),
+    "gar_expert_weights": (C.c_int, [_vp, _i32, _i64, _i32, _i64, _i32, _i32, _vp, _vp, _vp]),
+    "gar_expert_weights_grad": (C.c_int, [_vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _i64, _i32, _i32, _vp]),
+    "gar_grad_workspace_bytes": (C.c_size_t, [_i32, _i32]),
+    "gar_grad_norm": (C.c_int, [_vp, _i32, _vp, _vp, _i32, _vp, _vp, C.c_size_t, _vp]),
+    "gar_grad_clip": (C.c_int, [_vp, _vp, _i32, _vp, _vp, _i32, _i32, C.c_float, _vp, _vp, C.c_size_t, _vp]),
 }
 
 
@@ -828,7 +840,7 @@ def _workers(given, name, P, shape, dtype):
             ptrs.append(t.data_ptr())
         if table:
             given.checked[shape, dtype] = stride
-    if stride[-1] != 1 and shape[-1] > 1:
+    if stride[-1] != 1 and shape[-1] > 1 and shape[0] > 0:
         raise GarError(GAR_EINVAL, f"{name}: the elements of a row are not contiguous")
     return given.array if table else struct.pack(f"{P}Q", *ptrs), stride[0] if shape[0] > 1 else max(shape[-1], 1)
 
@@ -910,7 +922,179 @@ def gar_vocab_grad(x, w, target, lse, dx, dw, workspace, weight=None, addend=Non
           _dev(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
 
 
+# ------------------------------------------- tokens to experts and back
+def gar_expert_rows(P: int, tokens: int, k: int, experts: int, align: int = 1, capacity: int = 0) -> int:
+    """Rows of the experts' buffer that any choices of P workers' tokens fit in."""
+    rows = int(load().gar_expert_rows(P, tokens, k, experts, align, capacity))
+    if rows < 0:
+        raise GarError(GAR_EINVAL, f"P={P} tokens={tokens} k={k} experts={experts} align={align} capacity={capacity}")
+    return rows
+
+
+def gar_expert_workspace_bytes(P: int, tokens: int, k: int, experts: int) -> int:
+    return int(load().gar_expert_workspace_bytes(P, tokens, k, experts))
+
+
+def _first(given, name):
+    """The first worker's tensor, of two dimensions."""
+    t = given.first if isinstance(given, PtrTable) else given[0] if len(given) else None
+    if t is None:
+        raise GarError(GAR_EINVAL, f"{name} has no worker's tensor")
+    return t, *_two_dims(t, f"{name}[0]")
+
+
+def _per_choice(given, name, P, tokens, k, dtype):
+    """The pointers of one [tokens, k] tensor per worker, contiguous."""
+    table, ld = _workers(given, name, P, (tokens, k), dtype)
+    if ld != k:
+        raise GarError(GAR_EINVAL, f"{name} has to be contiguous")
+    return table
+
+
+def gar_expert_sort(choice, experts: int, position, source, offsets, workspace, align: int = 1, capacity: int = 0, stream=None):
+    """Rows of the pairs (worker, token, choice) sorted by expert: choice[w]
+    [tokens, k] int32 in, position[w] [tokens, k] int32, source [rows] int32 and
+    offsets [experts + 1] int32 out.  Each expert's rows are filled up to a
+    multiple of align, or are capacity rows, what is over them dropped."""
+    if not _FLOATS:
+        _types()
+    _, tokens, k = _first(choice, "choice")
+    P, rows = len(choice), source.numel()
+    _call("gar_expert_sort", _per_choice(choice, "choice", P, tokens, k, _INT32), P, tokens, k, experts, align, capacity,
+          _per_choice(position, "position", P, tokens, k, _INT32), _vector(source, "source", _INT32, rows), rows,
+          _vector(offsets, "offsets", _INT32, experts + 1), _dev(workspace), workspace.numel() * workspace.element_size(),
+          _stream(stream))
+
+
+def gar_expert_gather(x, position, source, y, weight=None, stream=None):
+    """y[position[w][t, j]] = x[w][t] (times weight[w][t, j]); an expert's rows
+    without a token become 0.  x[w] [tokens, hidden], y [rows, hidden]."""
+    first, tokens, hidden = _first(x, "x")
+    dtype, P, rows, k = _code(first, _FLOATS, "x"), len(x), source.numel(), _first(position, "position")[2]
+    if y.dtype != first.dtype:
+        raise GarError(GAR_EDTYPE, f"y is {y.dtype}, x {first.dtype}")
+    xa, ldx = _workers(x, "x", P, (tokens, hidden), first.dtype)
+    yp, ldy = _matrix(y, "y", rows, hidden)
+    wa = _per_choice(weight, "weight", P, tokens, k, _FLOAT32) if weight is not None else None
+    _call("gar_expert_gather", xa, P, tokens, hidden, ldx, dtype, k, _per_choice(position, "position", P, tokens, k, _INT32),
+          _vector(source, "source", _INT32, rows), rows, wa, yp, ldy, _stream(stream))
+
+
+def gar_expert_combine(y, position, out, weight=None, addend=None, stream=None):
+    """out[w][t] = addend[w][t] + sum_j weight[w][t, j] y[position[w][t, j]] (weight
+    None: 1; addend None: 0; it may be out)."""
+    first, tokens, hidden = _first(out, "out")
+    dtype, P, k = _code(first, _FLOATS, "out"), len(out), _first(position, "position")[2]
+    if y.dtype != first.dtype:
+        raise GarError(GAR_EDTYPE, f"y is {y.dtype}, out {first.dtype}")
+    rows = _two_dims(y, "y")[0]
+    yp, ldy = _matrix(y, "y", rows, hidden)
+    oa, ldo = _workers(out, "out", P, (tokens, hidden), first.dtype)
+    aa, lda = _workers(addend, "addend", P, (tokens, hidden), first.dtype) if addend is not None else (None, 0)
+    wa = _per_choice(weight, "weight", P, tokens, k, _FLOAT32) if weight is not None else None
+    _call("gar_expert_combine", yp, ldy, rows, P, tokens, hidden, dtype, k,
+          _per_choice(position, "position", P, tokens, k, _INT32), wa, aa, lda, oa, ldo, _stream(stream))
+
+
+def gar_expert_combine_grad(dout, y, position, source, weight, dy, dweight, stream=None):
+    """The gradient of gar_expert_combine: dy[position] = weight dout (rows without
+    a token 0), dweight[w][t, j] = <dout[w][t], y[position[w][t, j]]>; dy may be y."""
+    first, tokens, hidden = _first(dout, "dout")
+    dtype, P, rows, k = _code(first, _FLOATS, "dout"), len(dout), source.numel(), _first(position, "position")[2]
+    if y.dtype != first.dtype or dy.dtype != first.dtype:
+        raise GarError(GAR_EDTYPE, f"y is {y.dtype}, dy {dy.dtype}, dout {first.dtype}")
+    da, ldd = _workers(dout, "dout", P, (tokens, hidden), first.dtype)
+    yp, ldy = _matrix(y, "y", rows, hidden)
+    gp, ldg = _matrix(dy, "dy", rows, hidden)
+    _call("gar_expert_combine_grad", da, ldd, yp, ldy, P, tokens, hidden, dtype, k,
+          _per_choice(position, "position", P, tokens, k, _INT32), _vector(source, "source", _INT32, rows), rows,
+          _per_choice(weight, "weight", P, tokens, k, _FLOAT32), gp, ldg,
+          _per_choice(dweight, "dweight", P, tokens, k, _FLOAT32), _stream(stream))
+
+
+def gar_expert_weights(z, choice, weight, stream=None):
+    """weight[w][t, j]: the softmax over the token's chosen logits z[w][t, choice]
+    (a choice of -1 has weight 0)."""
+    first, tokens, experts = _first(z, "z")
+    dtype, P, k = _code(first, _FLOATS, "z"), len(z), _first(choice, "choice")[2]
+    za, ldz = _workers(z, "z", P, (tokens, experts), first.dtype)
+    _call("gar_expert_weights", za, P, tokens, experts, ldz, dtype, k, _per_choice(choice, "choice", P, tokens, k, _INT32),
+          _per_choice(weight, "weight", P, tokens, k, _FLOAT32), _stream(stream))
+
+
+def gar_expert_weights_grad(weight, dweight, choice, dz, accumulate: bool = False, stream=None):
+    """The gradient of gar_expert_weights over the router's logits: dz[w] [tokens,
+    experts], 0 where an expert was not chosen; accumulate: added to dz."""
+    first, tokens, experts = _first(dz, "dz")
+    dtype, P, k = _code(first, _FLOATS, "dz"), len(dz), _first(choice, "choice")[2]
+    da, ldd = _workers(dz, "dz", P, (tokens, experts), first.dtype)
+    _call("gar_expert_weights_grad", _per_choice(weight, "weight", P, tokens, k, _FLOAT32),
+          _per_choice(dweight, "dweight", P, tokens, k, _FLOAT32), P, tokens, experts, k,
+          _per_choice(choice, "choice", P, tokens, k, _INT32), da, ldd, dtype, 1 if accumulate else 0, _stream(stream))
+
+
+# ------------------------------------------------- gradient norm, clipping
+class GradTables:
+    """Host tables of P workers' gradient tensors, built once: grads[w][i], and the
+    tensors that the clipped ones go to (the same ones unless given)."""
+
+    def __init__(self, grads, out=None):
+        self.P = len(grads)
+        self.count = len(grads[0]) if self.P else 0
+        self.src = self._table(grads, "grads")
+        self.dst = self.src if out is None else self._table(out, "out")
+        first = self.src.tensors[:self.count]
+        self.dtype = np.array([_dtype_code(t) for t in first], np.int32)
+        self.numel = np.array([t.numel() for t in first], np.int64)
+        for name, table in (("grads", self.src), ("out", self.dst)):
+            for i, t in enumerate(table.tensors):
+                like = first[i % self.count]
+                if t.dtype != like.dtype:
+                    raise GarError(GAR_EDTYPE, f"{name}: tensor {i % self.count} is {t.dtype}, not {like.dtype}")
+                if t.numel() != like.numel() or not t.is_contiguous():
+                    raise GarError(GAR_EINVAL, f"{name}: tensor {i % self.count} is not contiguous, or not of {like.numel()} elements")
+
+    def _table(self, rows, name):
+        if not 1 <= self.P <= GAR_MAX_WORKERS or len(rows) != self.P or any(len(r) != self.count for r in rows):
+            raise GarError(GAR_EINVAL, f"{name}: {len(rows)} workers' lists, not all of {self.count} tensors")
+        return PtrTable([t for r in rows for t in r])
+
+
+def grad_tables(grads, out=None) -> GradTables:
+    return grads if isinstance(grads, GradTables) else GradTables(grads, out)
+
+
+def gar_grad_workspace_bytes(grads) -> int:
+    t = grad_tables(grads)
+    return int(load().gar_grad_workspace_bytes(t.P, t.count))
+
+
+def gar_grad_norm(grads, norm, workspace, stream=None):
+    """norm[w] = the 2-norm of worker w's gradient tensors grads[w][i] (lists, or
+    grad_tables), [P] fp32."""
+    t = grad_tables(grads)
+    _call("gar_grad_norm", t.src.array, t.P, t.numel.ctypes.data, t.dtype.ctypes.data, t.count,
+          _vector(norm, "norm", _float32(), t.P), _dev(workspace), workspace.numel() * workspace.element_size(),
+          _stream(stream))
+
+
+def gar_grad_clip(grads, max_norm: float, norm, workspace, out=None, shared: bool = False, stream=None):
+    """Each worker's gradients times min(1, max_norm / norm[w]), in place or to
+    out[w][i]; shared: by the norm of the first worker's, norm [1].  A norm that is
+    not finite leaves them as they are."""
+    t = grad_tables(grads, out)
+    _call("gar_grad_clip", t.src.array, t.dst.array, t.P, t.numel.ctypes.data, t.dtype.ctypes.data, t.count,
+          1 if shared else 0, max_norm, _vector(norm, "norm", _float32(), 1 if shared else t.P), _dev(workspace),
+          workspace.numel() * workspace.element_size(), _stream(stream))
+
+
+def _float32():
+    if _FLOAT32 is None:
+        _types()
+    return _FLOAT32
+
+
 __all__ = [n for n in dir() if n.startswith(("gar_", "GAR_"))] + ["GarError", "FusionPlan", "PtrTable", "load",
                                                                     "pointer_table", "fused_pointer_tables", "thc_plan_tables",
-                                                                    "fp8_matrix",
+                                                                    "fp8_matrix", "GradTables", "grad_tables",
                                                                     "Timeline", "timeline"]

@@ -843,6 +843,136 @@ int gar_vocab_grad(const void *x, int64_t ldx, const void *w, int64_t ldw, int32
                    const void *addend, int64_t ld_addend, void *dw, int64_t lddw, int32_t dw_type, void *d_workspace,
                    size_t workspace_bytes, gar_stream_t stream);
 
+/* Tokens sorted by the experts that a router chose, and back.  A pair is one of
+ * the k choices of one token of one worker, numbered (w tokens + t) k + j; P tokens
+ * k <= 2^30.  Tables of P pointers are host arrays.  [tokens, k] arrays are
+ * contiguous; choice is what gar_balance_loss writes (an entry outside [0, experts)
+ * is no choice; the same expert more than once is as many pairs). */
+
+/* Rows that any choices fit in: experts * capacity where capacity > 0, else
+ * P tokens k + experts (align - 1).  -1: an argument out of range. */
+int64_t gar_expert_rows(int32_t P, int64_t tokens, int32_t k, int32_t experts, int32_t align, int32_t capacity);
+
+/* Bytes of device workspace gar_expert_sort needs. */
+size_t gar_expert_workspace_bytes(int32_t P, int64_t tokens, int32_t k, int32_t experts);
+
+/* gar_expert_sort -- the row of each pair when all are sorted by expert, pairs of
+ * one expert in the order of their numbers.  With capacity 0 an expert's rows begin
+ * where the rows before end, their count rounded up to a multiple of align; with
+ * capacity > 0 (align 1) expert e has the rows e capacity .. (e + 1) capacity - 1
+ * and its pairs past the first `capacity` are dropped.
+ *   choice       P device pointers, [tokens, k] int32
+ *   experts      1..1024;  k 1..32
+ *   position     P device pointers, out, [tokens, k] int32: the pair's row, -1 for
+ *                none (no choice, or dropped)
+ *   source       device, out, [rows] int32: the row's pair; -1: a row of an expert
+ *                without a pair; -2: a row behind the last expert
+ *   rows         of source; at least gar_expert_rows(...)
+ *   offsets      device, out, [experts + 1] int32: first row of each expert, and the
+ *                end of the last
+ *   d_workspace  device, 4-byte aligned, not shared with a concurrent call
+ * Errors: GAR_EINVAL, GAR_EALIGN, GAR_ECUDA. */
+int gar_expert_sort(const int32_t *const *choice, int32_t P, int64_t tokens, int32_t k, int32_t experts, int32_t align,
+                    int32_t capacity, int32_t *const *position, int32_t *source, int64_t rows, int32_t *offsets,
+                    void *d_workspace, size_t workspace_bytes, gar_stream_t stream);
+
+/* gar_expert_gather -- y[position_tj] = x_t, or weight_tj x_t: each token's row to
+ * its experts' rows.  Rows whose source is -1 become 0, those whose source is -2
+ * stay as they are.  A position outside [0, rows) is none.
+ *   x            P device pointers, tokens x hidden fp32 or bf16 (dtype), row stride ldx
+ *   position, source, rows   as gar_expert_sort wrote them
+ *   weight       P device pointers, [tokens, k] fp32, or NULL (1: the rows are copies)
+ *   y            device, out, rows x hidden of x's type, row stride ldy
+ * The gradient over x (weight NULL) is gar_expert_combine of y's gradient without
+ * weights.
+ * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA. */
+int gar_expert_gather(const void *const *x, int32_t P, int64_t tokens, int64_t hidden, int64_t ldx, int32_t dtype, int32_t k,
+                      const int32_t *const *position, const int32_t *source, int64_t rows, const float *const *weight,
+                      void *y, int64_t ldy, gar_stream_t stream);
+
+/* gar_expert_combine -- out_t = sum_j weight_tj y[position_tj] + addend_t, each
+ * token's rows back to it: fp32 sums in the order of j, one rounding.  A choice
+ * without a row adds nothing (whatever its weight).
+ *   y            device, rows x hidden fp32 or bf16 (dtype), row stride ldy
+ *   weight       P device pointers, [tokens, k] fp32, or NULL (1)
+ *   addend       P device pointers, tokens x hidden of y's type, row stride
+ *                ld_addend, or NULL (0); an entry may be that of out
+ *   out          P device pointers, out, tokens x hidden of y's type, row stride ldo
+ * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA. */
+int gar_expert_combine(const void *y, int64_t ldy, int64_t rows, int32_t P, int64_t tokens, int64_t hidden, int32_t dtype,
+                       int32_t k, const int32_t *const *position, const float *const *weight, const void *const *addend,
+                       int64_t ld_addend, void *const *out, int64_t ldo, gar_stream_t stream);
+
+/* gar_expert_combine_grad -- the gradient of gar_expert_combine, in one pass over
+ * dout and y:
+ *   dy[position_tj] = weight_tj dout_t,   dweight_tj = sum_h dout_th y[position_tj]_h
+ * (the addend's gradient is dout).  dweight is 0 for a choice without a row; rows of
+ * dy whose source is -1 become 0, those whose source is -2 stay as they are.
+ *   dout         P device pointers, tokens x hidden fp32 or bf16 (dtype), row stride
+ *                ld_dout
+ *   y            device, rows x hidden of the same type, row stride ldy
+ *   dy           device, out, the same; may be y (same row stride)
+ *   dweight      P device pointers, out, [tokens, k] fp32
+ * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA. */
+int gar_expert_combine_grad(const void *const *dout, int64_t ld_dout, const void *y, int64_t ldy, int32_t P, int64_t tokens,
+                            int64_t hidden, int32_t dtype, int32_t k, const int32_t *const *position, const int32_t *source,
+                            int64_t rows, const float *const *weight, void *dy, int64_t lddy, float *const *dweight,
+                            gar_stream_t stream);
+
+/* gar_expert_weights -- the weights of each token's experts: the softmax over its
+ * chosen logits, weight_tj = exp(z_{t,choice_tj}) / sum_i exp(z_{t,choice_ti}); 0 for
+ * no choice, and for every choice of a token whose chosen logits are all -inf.
+ *   z            P device pointers, tokens x experts fp32 or bf16 (dtype), row stride ldz
+ *   choice       P device pointers, [tokens, k] int32
+ *   weight       P device pointers, out, [tokens, k] fp32
+ * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA. */
+int gar_expert_weights(const void *const *z, int32_t P, int64_t tokens, int32_t experts, int64_t ldz, int32_t dtype, int32_t k,
+                       const int32_t *const *choice, float *const *weight, gar_stream_t stream);
+
+/* gar_expert_weights_grad -- its gradient over the logits,
+ *   dz_{t,choice_tj} = weight_tj (dweight_tj - sum_i weight_ti dweight_ti)
+ * (summed where an expert was chosen more than once), 0 for experts that were not
+ * chosen.
+ *   dz           P device pointers, out, tokens x experts fp32 or bf16 (dtype), row
+ *                stride lddz
+ *   accumulate   0: dz is written; else the gradient is added to it (to that of
+ *                gar_balance_loss, say), experts that were not chosen stay as they are
+ * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA. */
+int gar_expert_weights_grad(const float *const *weight, const float *const *dweight, int32_t P, int64_t tokens, int32_t experts,
+                            int32_t k, const int32_t *const *choice, void *const *dz, int64_t lddz, int32_t dtype,
+                            int32_t accumulate, gar_stream_t stream);
+
+/* Bytes of device workspace gar_grad_norm and gar_grad_clip need. */
+size_t gar_grad_workspace_bytes(int32_t P, int32_t count);
+
+/* gar_grad_norm -- norm[w] = sqrt(sum over the worker's `count` tensors and their
+ * elements of g^2).  Squares are added sixteen at a time in fp32, these sums in fp64
+ * in a fixed order (within 3e-7 of the exact norm; the same bits in every run on a
+ * given GPU model).  No square overflows or vanishes: only a norm past fp32's largest
+ * value becomes infinite.  A NaN or an infinity among the gradients shows in the norm.
+ *   src          host, P * count device pointers: worker w's tensor i at w count + i
+ *   numel, dtype host, [count]: elements and type (fp32 or bf16) of tensor i, the same
+ *                for every worker
+ *   norm         device, out, [P] fp32
+ *   d_workspace  device, gar_grad_workspace_bytes(P, count) bytes, 8-byte aligned, not
+ *                shared with a concurrent call
+ * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA. */
+int gar_grad_norm(const void *const *src, int32_t P, const int64_t *numel, const int32_t *dtype, int32_t count, float *norm,
+                  void *d_workspace, size_t workspace_bytes, gar_stream_t stream);
+
+/* gar_grad_clip -- that norm, and dst = c src with c = max_norm / norm where norm >
+ * max_norm, else 1 (nothing is written where dst is src).  One fp32 product a value,
+ * rounded to its type.  A norm that is not finite leaves the gradients as they are
+ * (dst: copies) and raises GAR_STATUS_NONFINITE.
+ *   dst          host, P * count device pointers: where the clipped tensors go; each
+ *                src's own or apart from all of src
+ *   shared       not 0: every worker's tensors are scaled by the norm of worker 0's
+ *                (copies of one average); norm is then one fp32
+ *   max_norm     0 or more; infinity: no clipping
+ * Other arguments and errors as for gar_grad_norm. */
+int gar_grad_clip(const void *const *src, void *const *dst, int32_t P, const int64_t *numel, const int32_t *dtype, int32_t count,
+                  int32_t shared, float max_norm, float *norm, void *d_workspace, size_t workspace_bytes, gar_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

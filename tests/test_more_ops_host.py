@@ -116,3 +116,167 @@ def test_vocab_binding(gar, binding):
     assert refused(grad_of, x, w, target, lse, dx, dw, ws, addend=tensor(30, 64)) == gar.GAR_EDTYPE
     assert refused(grad_of, x, w, target, lse, dx, None, ws, addend=dw) == gar.GAR_EDTYPE
     assert refused(grad_of, x, w, target, lse, dx, tensor(31, 64), ws) == gar.GAR_EINVAL
+
+
+def tables(P, *places):
+    return [(V * P)(*[p + 0x100000 * i for i in range(P)]) for p in places]
+
+
+def test_expert_rows(gar):
+    f = gar.load().gar_expert_rows
+    assert f(2, 10, 3, 4, 1, 0) == 60 and f(2, 10, 3, 4, 128, 0) == 60 + 4 * 127 and f(2, 10, 3, 4, 1, 9) == 36
+    assert f(0, 1, 1, 1, 1, 0) == f(1, -1, 1, 1, 1, 0) == f(1, 1, 33, 1, 1, 0) == f(1, 1, 1, 1025, 1, 0) == f(1, 1, 1, 1, 0, 0) == -1
+    assert f(64, 1 << 62, 1, 1, 1, 0) == -1
+    with pytest.raises(gar.GarError):
+        gar.gar_expert_rows(1, 1, 0, 1)
+    assert gar.gar_expert_workspace_bytes(1, 10, 2, 8) > 0 and gar.gar_expert_workspace_bytes(65, 10, 2, 8) == 0
+
+
+def test_expert_sort_refusals(gar):
+    c, p = tables(2, 0x1000000, 0x2000000)
+
+    def call(choice=c, P=2, tokens=10, k=2, experts=4, align=1, capacity=0, position=p, source=S, rows=40, offsets=T, ws=U, n=1 << 20):
+        return gar.load().gar_expert_sort(choice, P, tokens, k, experts, align, capacity, position, source, rows, offsets, ws, n, NULL)
+
+    assert call(P=0) == call(P=65) == call(tokens=-1) == call(k=0) == call(k=33) == call(experts=0) == call(
+        experts=1025) == gar.GAR_EINVAL
+    assert call(align=0) == call(capacity=-1) == call(capacity=8, align=2) == call(rows=39) == call(align=8) == call(
+        rows=1 << 31) == gar.GAR_EINVAL
+    assert call(tokens=1 << 29, rows=(1 << 31) - 1) == call(tokens=1 << 62) == gar.GAR_EINVAL
+    assert call(choice=None) == call(position=None) == call(source=NULL) == call(offsets=NULL) == call(ws=NULL) == call(
+        n=10) == gar.GAR_EINVAL
+    assert call(choice=(V * 2)(0x1000, None)) == gar.GAR_EINVAL
+    assert call(choice=(V * 2)(0x1000, 0x1002)) == call(source=V(0x10001)) == call(ws=V(0x10002)) == gar.GAR_EALIGN
+
+
+def test_expert_move_refusals(gar):
+    x, pos, w, o = tables(2, 0x1000000, 0x2000000, 0x3000000, 0x4000000)
+    lib = gar.load()
+
+    def gather(x=x, P=2, tokens=10, hidden=16, ldx=16, dtype=0, k=2, position=pos, source=S, rows=40, weight=w, y=T, ldy=16):
+        return lib.gar_expert_gather(x, P, tokens, hidden, ldx, dtype, k, position, source, rows, weight, y, ldy, NULL)
+
+    def combine(y=T, ldy=16, rows=40, P=2, tokens=10, hidden=16, dtype=0, k=2, position=pos, weight=w, add=x, ldadd=16, out=o, ldo=16):
+        return lib.gar_expert_combine(y, ldy, rows, P, tokens, hidden, dtype, k, position, weight, add, ldadd, out, ldo, NULL)
+
+    def grad(dout=x, ldd=16, y=T, ldy=16, P=2, tokens=10, hidden=16, dtype=0, k=2, position=pos, source=S, rows=40, weight=w, dy=U,
+             lddy=16, dweight=o):
+        return lib.gar_expert_combine_grad(dout, ldd, y, ldy, P, tokens, hidden, dtype, k, position, source, rows, weight, dy, lddy,
+                                           dweight, NULL)
+
+    bad = (V * 2)(0x1000, None)
+    odd = (V * 2)(0x1000, 0x1002)
+    for f in (gather, combine, grad):
+        assert f(dtype=2) == gar.GAR_EDTYPE
+        assert f(P=0) == f(P=65) == f(tokens=-1) == f(hidden=0) == f(k=0) == f(k=33) == f(rows=-1) == f(rows=1 << 31) == gar.GAR_EINVAL
+        assert f(position=None) == f(position=bad) == f(weight=bad) == f(tokens=1 << 60) == gar.GAR_EINVAL
+        assert f(position=odd) == f(weight=odd) == gar.GAR_EALIGN
+    assert gather(ldx=15) == gather(ldy=15) == gather(x=bad) == gather(y=NULL) == gather(source=NULL) == gar.GAR_EINVAL
+    assert gather(x=odd) == gather(y=V(0x10002)) == gather(source=V(0x10001)) == gar.GAR_EALIGN
+    assert combine(ldy=15) == combine(ldo=15) == combine(ldadd=15) == combine(out=None) == combine(y=NULL) == gar.GAR_EINVAL
+    assert combine(add=o, ldadd=17) == combine(add=bad) == gar.GAR_EINVAL
+    assert combine(out=odd) == combine(add=odd) == gar.GAR_EALIGN
+    assert combine(tokens=0) == gar.GAR_OK
+    assert grad(ldd=15) == grad(ldy=15) == grad(lddy=15) == grad(weight=None) == grad(dweight=bad) == grad(dy=NULL) == grad(
+        source=NULL) == grad(dy=T, lddy=17) == gar.GAR_EINVAL
+    assert grad(dy=V(0x10001)) == grad(dout=odd) == grad(dweight=odd) == gar.GAR_EALIGN
+    assert gather(tokens=0, rows=0) == grad(tokens=0, rows=0) == gar.GAR_OK
+
+
+def test_expert_weights_refusals(gar):
+    z, c, w = tables(2, 0x1000000, 0x2000000, 0x3000000)
+    lib = gar.load()
+
+    def weights(z=z, P=2, tokens=10, experts=8, ldz=8, dtype=0, k=2, choice=c, weight=w):
+        return lib.gar_expert_weights(z, P, tokens, experts, ldz, dtype, k, choice, weight, NULL)
+
+    def grad(weight=w, dweight=w, P=2, tokens=10, experts=8, k=2, choice=c, z=z, ldz=8, dtype=0):
+        return lib.gar_expert_weights_grad(weight, dweight, P, tokens, experts, k, choice, z, ldz, dtype, 0, NULL)
+
+    bad, odd = (V * 2)(0x1000, None), (V * 2)(0x1000, 0x1002)
+    for f in (weights, grad):
+        assert f(dtype=3) == gar.GAR_EDTYPE
+        assert f(P=0) == f(experts=0) == f(experts=1025) == f(ldz=7) == f(k=0) == f(k=33) == f(tokens=-1) == gar.GAR_EINVAL
+        assert f(z=bad) == f(choice=bad) == f(weight=bad) == f(z=None) == f(choice=None) == f(weight=None) == gar.GAR_EINVAL
+        assert f(z=odd) == f(choice=odd) == f(weight=odd) == gar.GAR_EALIGN
+        assert f(tokens=0) == gar.GAR_OK
+    assert grad(dweight=bad) == gar.GAR_EINVAL
+
+
+def test_clip_refusals(gar):
+    lib = gar.load()
+    src, dst = (V * 4)(*range(0x1000, 0x5000, 0x1000)), (V * 4)(*range(0x11000, 0x15000, 0x1000))
+    numel, dtype = (C.c_int64 * 2)(10, 20), (C.c_int32 * 2)(0, 1)
+
+    def clip(src=src, dst=dst, P=2, numel=numel, dtype=dtype, count=2, shared=0, top=1.0, norm=S, ws=T, n=1 << 20):
+        return lib.gar_grad_clip(src, dst, P, numel, dtype, count, shared, top, norm, ws, n, NULL)
+
+    def norm(src=src, P=2, numel=numel, dtype=dtype, count=2, norm=S, ws=T, n=1 << 20):
+        return lib.gar_grad_norm(src, P, numel, dtype, count, norm, ws, n, NULL)
+
+    for f in (clip, norm):
+        assert f(P=0) == f(P=65) == f(count=-1) == f(src=None) == f(numel=None) == f(dtype=None) == f(norm=NULL) == f(
+            ws=NULL) == f(n=100) == gar.GAR_EINVAL
+        assert f(numel=(C.c_int64 * 2)(10, -1)) == f(src=(V * 4)(0x1000, 0x2000, None, 0x4000)) == gar.GAR_EINVAL
+        assert f(dtype=(C.c_int32 * 2)(0, 2)) == gar.GAR_EDTYPE
+        assert f(src=(V * 4)(0x1000, 0x2000, 0x3002, 0x4000)) == f(norm=V(0x10002)) == f(ws=V(0x10004)) == gar.GAR_EALIGN
+    assert clip(top=-1.0) == clip(top=float("nan")) == clip(dst=None) == gar.GAR_EINVAL
+    assert clip(dst=(V * 4)(0x1000, 0x2000, 0x3000, 0x4001)) == gar.GAR_EALIGN
+    assert lib.gar_grad_workspace_bytes(0, 5) == lib.gar_grad_workspace_bytes(1, -1) == 0
+
+
+def test_expert_binding(gar, binding):
+    torch, tensor, made, refused = binding
+    i32 = torch.int32
+    choice, position = ([tensor(6, 2, dtype=i32) for _ in range(3)] for _ in range(2))
+    source, offsets, ws = tensor(40, dtype=i32), tensor(5, dtype=i32), tensor(64)
+    x, weight, out = [tensor(6, 16) for _ in range(3)], [tensor(6, 2) for _ in range(3)], [tensor(6, 16) for _ in range(3)]
+    y, dy, dweight = tensor(40, 20)[:, 2:18], tensor(40, 16), [tensor(6, 2) for _ in range(3)]
+    z, dz = [tensor(6, 4) for _ in range(3)], [tensor(6, 4, dtype=torch.bfloat16) for _ in range(3)]
+    gar.gar_expert_sort(choice, 4, position, source, offsets, ws, align=2)
+    gar.gar_expert_gather(x, position, source, y, weight=weight)
+    gar.gar_expert_combine(y, position, out, weight=weight, addend=x)
+    gar.gar_expert_combine_grad(x, y, position, source, weight, dy, dweight)
+    gar.gar_expert_weights(z, choice, weight)
+    gar.gar_expert_weights_grad(weight, dweight, choice, dz)
+    assert [n for n, _ in made] == ["gar_expert_sort", "gar_expert_gather", "gar_expert_combine", "gar_expert_combine_grad",
+                                    "gar_expert_weights", "gar_expert_weights_grad"]
+    E, D = gar.GAR_EINVAL, gar.GAR_EDTYPE
+    assert refused(gar.gar_expert_sort, choice, 4, position[:2], source, offsets, ws) == E
+    assert refused(gar.gar_expert_sort, choice, 5, position, source, offsets, ws) == E
+    assert refused(gar.gar_expert_sort, choice, 4, [tensor(6, 4, dtype=i32)[:, ::2] for _ in range(3)], source, offsets, ws) == E
+    assert refused(gar.gar_expert_sort, choice, 4, weight, source, offsets, ws) == D
+    assert refused(gar.gar_expert_sort, [], 4, [], source, offsets, ws) == E
+    assert refused(gar.gar_expert_gather, x, position, source, tensor(39, 16)) == E
+    assert refused(gar.gar_expert_gather, x, position, source, tensor(40, 16, dtype=torch.bfloat16)) == D
+    assert refused(gar.gar_expert_gather, [tensor(6, 16, dtype=torch.float16)] * 3, position, source, y) == D
+    assert refused(gar.gar_expert_gather, x, position, source, y, weight=choice) == D
+    assert refused(gar.gar_expert_combine, tensor(40, 15), position, out) == E
+    assert refused(gar.gar_expert_combine, y, position, out, addend=x[:2]) == E
+    assert refused(gar.gar_expert_combine_grad, x, y, position, source, weight, tensor(40, 16, dtype=torch.bfloat16), dweight) == D
+    assert refused(gar.gar_expert_combine_grad, x, y, position, source, weight, dy, [tensor(6, 3) for _ in range(3)]) == E
+    assert refused(gar.gar_expert_weights, z, choice, [tensor(5, 2) for _ in range(3)]) == E
+    assert refused(gar.gar_expert_weights_grad, weight, dweight, choice, [tensor(7, 4) for _ in range(3)]) == E
+
+
+def test_clip_binding(gar, binding):
+    torch, tensor, made, refused = binding
+    grads = [[tensor(10, 3), tensor(7, dtype=torch.bfloat16)] for _ in range(2)]
+    out = [[tensor(30), tensor(7, dtype=torch.bfloat16)] for _ in range(2)]
+    norm, ws = tensor(2), tensor(1 << 14)
+    t = gar.grad_tables(grads, out)
+    assert t.P == 2 and t.count == 2 and list(t.numel) == [30, 7] and list(t.dtype) == [0, 1]
+    assert gar.grad_tables(t) is t and gar.gar_grad_workspace_bytes(t) == gar.gar_grad_workspace_bytes(grads)
+    gar.gar_grad_norm(grads, norm, ws)
+    gar.gar_grad_clip(t, 1.0, norm, ws)
+    gar.gar_grad_clip(grads, 1.0, tensor(1), ws, out=out, shared=True)
+    assert [n for n, _ in made] == ["gar_grad_norm", "gar_grad_clip", "gar_grad_clip"]
+    E, D = gar.GAR_EINVAL, gar.GAR_EDTYPE
+    assert refused(gar.gar_grad_clip, t, 1.0, tensor(1), ws) == refused(gar.gar_grad_clip, t, 1.0, norm, ws, shared=True) == E
+    assert refused(gar.gar_grad_norm, t, tensor(2, dtype=torch.float64), ws) == D
+    assert refused(gar.grad_tables, []) == refused(gar.grad_tables, [[tensor(3)], []]) == refused(gar.grad_tables, grads, out[:1]) == E
+    assert refused(gar.grad_tables, grads, [[tensor(31), out[0][1]], out[1]]) == E
+    assert refused(gar.grad_tables, [[tensor(4, 4)[:, ::2]]]) == E
+    assert refused(gar.grad_tables, grads, [[tensor(30, dtype=torch.bfloat16), out[0][1]], out[1]]) == D
+    assert refused(gar.grad_tables, [[tensor(3, dtype=torch.float16)]]) == D
+    assert refused(gar.grad_tables, [[torch.zeros(3)]]) == E
