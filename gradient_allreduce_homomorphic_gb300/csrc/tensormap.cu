@@ -26,18 +26,36 @@ EncodeTiled encode_tiled() {
 
 }  // namespace
 
-int encode_tile_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, int64_t inner, int64_t outer, int64_t stride,
-                    int box_inner, int box_outer) {
+namespace {
+
+int encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
+           const cuuint32_t *boxes, CUtensorMapSwizzle swizzle) {
     EncodeTiled fn = encode_tiled();
     if (!fn) return fail(GAR_ECUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint32_t elem[3] = {1, 1, 1};
+    const CUresult r = fn(map, type, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, strides, boxes, elem,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(GAR_ECUDA, "cuTensorMapEncodeTiled: %d", static_cast<int>(r));
+    return GAR_OK;
+}
+
+}  // namespace
+
+int encode_tile_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, int64_t inner, int64_t outer, int64_t stride,
+                    int box_inner, int box_outer, CUtensorMapSwizzle swizzle) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
     const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer)};
-    const cuuint32_t elem[2] = {1, 1};
-    const CUresult r = fn(map, type, 2, const_cast<void *>(base), dims, strides, boxes, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(GAR_ECUDA, "cuTensorMapEncodeTiled: %d", static_cast<int>(r));
-    return GAR_OK;
+    return encode(map, type, 2, base, dims, strides, boxes, swizzle);
+}
+
+int encode_column_map(CUtensorMap *map, CUtensorMapDataType type, int elem, const void *base, int64_t inner, int64_t outer,
+                      int64_t stride, int box_columns, int box_outer) {
+    const int wide = 128 / elem;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(wide), static_cast<cuuint64_t>(outer), static_cast<cuuint64_t>(inner / wide)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride), 128};
+    const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(wide), static_cast<cuuint32_t>(box_outer), static_cast<cuuint32_t>(box_columns)};
+    return encode(map, type, 3, base, dims, strides, boxes, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace gar

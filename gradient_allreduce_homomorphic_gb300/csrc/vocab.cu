@@ -37,13 +37,14 @@
 namespace gar {
 namespace {
 
-constexpr int kTile = 256;    // rows and columns of a pair's tile
+constexpr int kTile = 256;    // rows of a pair's tile, and its columns at most
 constexpr int kK = 64;        // k per chunk: one swizzled line of bf16
 constexpr int kStages = 6;
 constexpr int kOperand = 128 * kK * 2;  // bytes of one operand of a stage, of each CTA
 constexpr int kStage = 2 * kOperand;
 constexpr int kThreads = 320;  // warp 0 loads, warp 1 issues products, warps 2-9 epilogue
-constexpr int kSmem = 1024 + kStages * kStage;
+constexpr int kStaging = 8 * 4096;  // two tiles of 32 x 32 bf16 for each epilogue warp
+constexpr int kSmem = 1024 + kStages * kStage + kStaging;
 // Chunks that an accumulator adds at most for an fp32 result: the tensor core's additions round toward zero, so a sum's
 // error grows with its length (8e-7 of the result at 8192 k).
 constexpr int kSegment = 8192 / kK;
@@ -51,24 +52,27 @@ constexpr int kSegment = 8192 / kK;
 enum { kLoss, kGradient, kWeights, kInputs };
 
 struct VocabParams {
-    int64_t items;       // handed out in order
+    int64_t items;       // whole tiles or runs, handed out in order
     int64_t tiles_m;     // tiles along the lanes: rows of x (logits), hidden (dw, dx)
     int64_t tiles_n;     // along the columns: vocabulary (logits, dw), rows of x (dx)
+    int32_t tile_n;      // columns of a tile, a multiple of 32
     int32_t runs;        // a run: consecutive column tiles of one item
-    int32_t splits;      // parts of k (dx)
     int32_t chunks;      // of 64 k, of one part of g
     int32_t parts;       // of g: 1, or 2 along k (fp32 dw)
+    int32_t rest;        // dx: tiles behind the items, whose k is cut
+    int32_t splits;      // into as many parts
     int64_t rows, hidden, vocab;
     int64_t first, cols;  // the piece's columns
     const int32_t *target;
     const float *weight, *lse;
-    float2 *stats;       // [rows][2 runs]: maximum, sum
+    float2 *stats;       // [rows][2 runs]: maximum (times log2 e), sum
     float *at_target;    // [rows]
-    uint16_t *g, *g_low;
-    int64_t ldg;
-    void *out;           // dw, dx or its partial sums
+    void *out;           // dw or dx
     const void *addend;
-    int64_t ld_out, ld_addend, split_stride;
+    float *sum;          // dx: sums over the pieces [rows][hidden], where there are several
+    float *part;         // dx: sums over parts of k, [splits][rest] tiles of 256 x 256
+    int64_t ld_out, ld_addend;
+    int32_t last;        // dx: of the last piece
     unsigned int *status;
 };
 
@@ -77,7 +81,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Whether a row counts: a weight, and a target of the vocabulary.
 __device__ __forceinline__ bool counts(const int32_t *target, const float *weight, int64_t vocab, int64_t t) {
@@ -97,28 +101,38 @@ __device__ __noinline__ void drain_stages(uint32_t full, int issued, uint32_t s,
 
 // An item: tile m, column tiles n0 .. n1, chunks c0 .. c1.  Runs of 8 tiles of
 // rows by all column runs, so that the pairs at work share operands in L2.
+// Behind the items come the tiles of dx that would leave pairs without work, cut
+// along k: the first parts of all of them, then the second ones, so that the pairs
+// at work read the same k.
 struct Item {
     int64_t m, run, n0, n1;
-    int32_t c0, c1, split;
+    int32_t c0, c1;
+    int32_t slot;  // -1: all of k
 };
-__device__ __forceinline__ Item item_of(const VocabParams &p, int64_t i) {
-    const int64_t tiles = p.tiles_m * p.runs;
-    Item it;
-    it.split = static_cast<int32_t>(i / tiles);
-    i -= it.split * tiles;
+__device__ __forceinline__ void place_item(const VocabParams &p, int64_t i, Item &it) {
     const int64_t per = 8 * static_cast<int64_t>(p.runs), group = i / per, in = i % per;
     const int64_t wide = p.tiles_m - group * 8 < 8 ? p.tiles_m - group * 8 : 8;
     it.m = group * 8 + in % wide;
     it.run = in / wide;
     it.n0 = p.tiles_n * it.run / p.runs, it.n1 = p.tiles_n * (it.run + 1) / p.runs;
-    const int64_t all = static_cast<int64_t>(p.chunks) * p.parts;
-    it.c0 = static_cast<int32_t>(all * it.split / p.splits), it.c1 = static_cast<int32_t>(all * (it.split + 1) / p.splits);
+}
+__device__ __forceinline__ Item item_of(const VocabParams &p, int64_t i) {
+    Item it;
+    it.c0 = 0, it.c1 = p.chunks * p.parts, it.slot = -1;
+    if (i < p.items) {
+        place_item(p, i, it);
+        return it;
+    }
+    it.slot = static_cast<int32_t>(i - p.items);
+    const int64_t split = it.slot / p.rest;
+    place_item(p, p.items + it.slot % p.rest, it);
+    it.c0 = static_cast<int32_t>(p.chunks * split / p.splits), it.c1 = static_cast<int32_t>(p.chunks * (split + 1) / p.splits);
     return it;
 }
 
 // 32 accumulator columns to rows 0 .. count of d (ld apart), c added where given.
-template <typename T>
-__device__ __forceinline__ void store_columns(const float (&v)[32], T *d, int64_t ld, const T *c, int64_t ldc, int count) {
+template <typename T, typename C>
+__device__ __forceinline__ void store_columns(const float (&v)[32], T *d, int64_t ld, const C *c, int64_t ldc, int count) {
     if (c) {
         float x[32];
 #pragma unroll
@@ -133,15 +147,18 @@ __device__ __forceinline__ void store_columns(const float (&v)[32], T *d, int64_
     }
 }
 
-// One epilogue warp's state over an item: a row's running maximum and sum (loss),
-// or what its gradient takes.
+// A lane's row over an item: its running maximum and sum (loss), or what its
+// gradient takes.
 struct Row {
-    float top, sum;     // kLoss
-    int32_t target;     // -1: none
-    float lse, weight;  // kGradient; a row that does not count has target -1 and weight 0
+    float top, sum;            // kLoss
+    int32_t target;            // -1: the row does not count (gradient), or has none
+    float lse, lse2, weight;   // kGradient; lse2: times log2 e
 };
 
 // 32 logits of a row (vocabulary columns col ..) into its running maximum and sum.
+// Powers are of two, their exponents one fma each: z log2(e) less the maximum's,
+// whose rounding is the same in every term and in what is written, so that it
+// drops out.
 __device__ __forceinline__ void take_logits(const VocabParams &p, float (&v)[32], Row &r, int64_t t, int64_t col) {
     if (col + 32 > p.vocab) {
 #pragma unroll
@@ -156,51 +173,59 @@ __device__ __forceinline__ void take_logits(const VocabParams &p, float (&v)[32]
             if (at == j) z = v[j];
         if (at >= 0 && at < 32) p.at_target[t] = z;
     }
-    float top = r.top;
+    float m[4] = {r.top, v[0], v[1], v[2]};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
-    float s[4] = {r.sum * exp2_fast((r.top - top) * kLog2e), 0.0f, 0.0f, 0.0f};
+    for (int j = 3; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], v[j]);
+    const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), low = -top * kLog2e;
+    float s[4] = {r.sum * exp2_fast(fmaf(r.top, kLog2e, low)), 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) s[j & 3] += exp2_fast((v[j] - top) * kLog2e);
+    for (int j = 0; j < 32; ++j) s[j & 3] += exp2_fast(fmaf(v[j], kLog2e, low));
     r.top = top, r.sum = (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// The same logits to g; col counts from the piece's first column.
+// The same logits to g (col counts from the piece's first column), as bf16 pairs:
+// to `low` what `high` leaves of an fp32 value.  A bf16 g's exponent is one fma, which
+// may put 2^-24 of lse's size into it; that of a g of two parts is formed from z - lse.
 template <bool kTwoParts>
-__device__ __forceinline__ void give_gradient(const VocabParams &p, float (&v)[32], const Row &r, int64_t t, int64_t col) {
-    const int64_t at = r.target - p.first - col;
+__device__ __forceinline__ void give_gradient(const VocabParams &p, float (&v)[32], const Row &r, int64_t col, uint32_t (&high)[16],
+                                              uint32_t (&low)[16]) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = exp2_fast((v[j] - r.lse) * kLog2e);
-    if (__any_sync(0xFFFFFFFFu, r.target >= 0 && at >= 0 && at < 32)) {
+    for (int j = 0; j < 32; ++j) v[j] = exp2_fast(kTwoParts ? (v[j] - r.lse) * kLog2e : fmaf(v[j], kLog2e, -r.lse2));
+    const int64_t at = r.target - p.first - col;
+    if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-            if (r.target >= 0 && at == j) v[j] -= 1.0f;
+            if (at == j) v[j] -= 1.0f;
     }
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = r.target >= 0 ? v[j] * r.weight : 0.0f;
-    if (t >= p.rows) return;
-    uint4 *to = reinterpret_cast<uint4 *>(p.g + t * p.ldg + col);
-    uint4 *low = reinterpret_cast<uint4 *>(p.g_low + t * p.ldg + col);
+    for (int j = 0; j < 32; ++j) v[j] *= r.weight;
+    if (__any_sync(0xFFFFFFFFu, r.target < 0)) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        uint32_t w[4], l[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = v[q * 8 + 2 * i], b = v[q * 8 + 2 * i + 1];
-            w[i] = pack_bf16x2(a, b);
-            if (kTwoParts) l[i] = pack_bf16x2(a - bf16_lo(w[i]), b - bf16_hi(w[i]));
-        }
-        to[q] = make_uint4(w[0], w[1], w[2], w[3]);
-        if (kTwoParts) low[q] = make_uint4(l[0], l[1], l[2], l[3]);
+        for (int j = 0; j < 32; ++j) v[j] = r.target < 0 ? 0.0f : v[j];
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        high[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        if (kTwoParts) low[i] = pack_bf16x2(v[2 * i] - bf16_lo(high[i]), v[2 * i + 1] - bf16_hi(high[i]));
+    }
+}
+
+// A lane's row of a warp's 32 x 32 tile to shared memory, in the order of the
+// 64-byte swizzle (no two lanes of eight in the same banks).
+__device__ __forceinline__ void stage_row(uint32_t tile, int lane, const uint32_t (&w)[16]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)), "r"(w[4 * q]),
+                     "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
+                     : "memory");
 }
 
 template <int kMode, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                         const __grid_constant__ CUtensorMap map_b2, const __grid_constant__ VocabParams p) {
+                         const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_d,
+                         const __grid_constant__ VocabParams p) {
     constexpr bool kMnA = kMode == kWeights || kMode == kInputs, kMnB = kMode == kWeights;
-    constexpr uint32_t kIdesc = bf16_idesc(kTile, kTile, kMnA, kMnB);
     // 16 k of a K-major operand are 32 bytes of each line; of an MN-major one two groups of eight lines of 128 bytes
     constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
     const int seg_chunks = kMode == kWeights && sizeof(T) == 4 ? kSegment : 0x7FFFFFFF;
@@ -213,7 +238,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                    done = drained + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_cta_rank();
-    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1, items = p.items + static_cast<int64_t>(p.rest) * p.splits;
+    const int tile_n = kMnB ? kTile : p.tile_n;
 
     let_next_begin();
     if (threadIdx.x == 0) {
@@ -241,28 +267,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s = 0, turn = 1;  // the first turn finds every stage free
         int issued = 0;
         bool ok = true;
-        for (int64_t i = first; i < p.items && ok; i += step) {
+        for (int64_t i = first; i < items && ok; i += step) {
             const Item it = item_of(p, i);
             const int32_t a = static_cast<int32_t>(it.m * kTile + 128 * rank);
             for (int64_t n = it.n0; n < it.n1 && ok; ++n) {
-                const int32_t b = static_cast<int32_t>(n * kTile + 128 * rank);
+                const int32_t b = static_cast<int32_t>(n * tile_n + tile_n / 2 * rank);
                 for (int32_t c = it.c0; c < it.c1; ++c) {
                     if (!(ok = mbar_wait(empty + 8 * s, turn, &failed))) break;
                     const uint32_t dst = base + s * kStage, bar = lead_full + 8 * s;
                     const bool second = kMode == kWeights && c >= p.chunks;
                     const int32_t k = (second ? c - p.chunks : c) * kK;
-                    const CUtensorMap *of_b = second ? &map_b2 : &map_b;
-                    if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * kStage);
-                    if (kMnA) {
-                        tma_load_2d_pair(dst, &map_a, bar, a, k);
-                        tma_load_2d_pair(dst + kOperand / 2, &map_a, bar, a + 64, k);
+                    const CUtensorMap *of_b = second ? &map_c : &map_b;
+                    if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * kOperand + 2 * 64 * tile_n);
+                    if (kMode == kWeights) {  // the library's own copies: their rows are whole columns of 128 bytes
+                        tma_load_columns_pair(dst, &map_a, bar, a >> 6, k);
+                        tma_load_columns_pair(dst + kOperand, of_b, bar, b >> 6, k);
                     } else {
-                        tma_load_2d_pair(dst, &map_a, bar, k, a);
-                    }
-                    if (kMnB) {
-                        tma_load_2d_pair(dst + kOperand, of_b, bar, b, k);
-                        tma_load_2d_pair(dst + kOperand + kOperand / 2, of_b, bar, b + 64, k);
-                    } else {
+                        if (kMnA) {
+                            tma_load_2d_pair(dst, &map_a, bar, a, k);
+                            tma_load_2d_pair(dst + kOperand / 2, &map_a, bar, a + 64, k);
+                        } else {
+                            tma_load_2d_pair(dst, &map_a, bar, k, a);
+                        }
                         tma_load_2d_pair(dst + kOperand, of_b, bar, k, b);
                     }
                     issued = issued < kStages ? issued + 1 : kStages;
@@ -275,9 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1 && rank == 0) {
         const uint64_t desc_a = smem_desc(base, kMnA ? kOperand / 2 : 16, 1024, 2);
         const uint64_t desc_b = smem_desc(base + kOperand, kMnB ? kOperand / 2 : 16, 1024, 2);
+        const uint32_t idesc = bf16_idesc(kTile, static_cast<uint32_t>(tile_n), kMnA, kMnB);
         uint32_t s = 0, turn = 0, seq = 0;
         bool ready = false;  // whether the next stage was seen to be full already
-        for (int64_t i = first; i < p.items; i += step) {
+        for (int64_t i = first; i < items; i += step) {
             const Item it = item_of(p, i);
             for (int64_t n = it.n0; n < it.n1; ++n) {
                 for (int32_t c0 = it.c0; c0 < it.c1; ++seq) {
@@ -293,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint64_t da = desc_a + s * (kStage >> 4), db = desc_b + s * (kStage >> 4);
 #pragma unroll
                             for (int k = 0; k < kK / 16; ++k)
-                                tc_mma_bf16_pair(acc, da + k * kStepA, db + k * kStepB, kIdesc, c > c0 || k > 0);
+                                tc_mma_bf16_pair(acc, da + k * kStepA, db + k * kStepB, idesc, c > c0 || k > 0);
                             tc_commit_pair(empty + 8 * s);
                             if (c == c1 - 1) tc_commit_pair(acc_full + 8 * (seq & 1));
                         }
@@ -313,15 +340,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t lead_drained = cluster_map(drained, 0);
-        uint32_t seq = 0;
-        for (int64_t i = first; i < p.items; i += step) {
+        const uint32_t staging = base + kStages * kStage + (warp - 2) * 4096;
+        const int batches = tile_n / 32;
+        constexpr bool kTwoParts = sizeof(T) == 4;
+        uint32_t seq = 0, turn = 0;
+        for (int64_t i = first; i < items; i += step) {
             const Item it = item_of(p, i);
             const int64_t lane_at = it.m * kTile + 128 * rank + quarter * 32 + lane;
-            Row r{-FLT_MAX, 0.0f, -1, 0.0f, 0.0f};
+            Row r{-FLT_MAX / 2, 0.0f, -1, 0.0f, 0.0f, 0.0f};
             if (kMode == kLoss && lane_at < p.rows) r.target = p.target[lane_at];
             if (kMode == kGradient && lane_at < p.rows && counts(p.target, p.weight, p.vocab, lane_at)) {
                 r.target = p.target[lane_at];
-                r.lse = p.lse[lane_at], r.weight = p.weight ? p.weight[lane_at] : 1.0f;
+                r.lse = p.lse[lane_at], r.lse2 = r.lse * kLog2e, r.weight = p.weight ? p.weight[lane_at] : 1.0f;
             }
             for (int64_t n = it.n0; n < it.n1; ++n) {
                 for (int32_t c0 = it.c0; c0 < it.c1; ++seq) {
@@ -330,38 +360,68 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_wait(acc_full + 8 * buf, (seq >> 1) & 1, &failed);
                     __syncwarp();
                     tc_fence_after();
+                    if (half >= batches) {  // a tile of 32 columns has none for the second warps
+                        tc_fence_before();
+                        if (lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
+                    }
 #pragma unroll 1
-                    for (int j = half; j < kTile / 32; j += 2) {
+                    for (int j = half; j < batches; j += 2) {
                         __syncwarp();
                         float v[32];
                         tc_load32(v, lanes + buf * kTile + j * 32);
                         tc_wait_ld();
-                        if (j + 2 >= kTile / 32) {
+                        if (j + 2 >= batches) {
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
                         }
-                        const int64_t col = n * kTile + j * 32;
+                        const int64_t col = n * tile_n + j * 32;
                         if (kMode == kLoss) {
-                            if (col < p.vocab) take_logits(p, v, r, lane_at, col);
+                            if (col < p.vocab && lane_at - lane < p.rows) take_logits(p, v, r, lane_at, col);
                         } else if (kMode == kGradient) {
-                            give_gradient<sizeof(T) == 4>(p, v, r, lane_at, col);
-                        } else if (const int64_t left = (kMode == kWeights ? p.cols : p.rows) - col; lane_at < p.hidden && left > 0) {
-                            T *d = static_cast<T *>(p.out) + it.split * p.split_stride + col * p.ld_out + lane_at;
-                            const T *c = static_cast<const T *>(p.addend);
-                            int64_t ldc = p.ld_addend;
-                            if (c0 > it.c0) c = d, ldc = p.ld_out;
-                            else if (c) c += it.split * p.split_stride + col * ldc + lane_at;
-                            store_columns<T>(v, d, p.ld_out, c, ldc, left < 32 ? static_cast<int>(left) : 32);
+                            if (lane_at - lane >= p.rows || col >= p.cols) continue;  // all lanes: no row, or no column, of theirs
+                            uint32_t high[16], low[16];
+                            give_gradient<kTwoParts>(p, v, r, col, high, low);
+                            // two tiles take turns, or hold the two parts
+                            if (lane == 0) tma_store_wait_read<kTwoParts ? 0 : 1>();
+                            __syncwarp();
+                            const uint32_t tile = staging + (kTwoParts ? 0 : turn * 2048);
+                            stage_row(tile, lane, high);
+                            if (kTwoParts) stage_row(tile + 2048, lane, low);
+                            fence_async_shared();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_2d(&map_c, tile, static_cast<int32_t>(col), static_cast<int32_t>(lane_at));
+                                if (kTwoParts) tma_store_2d(&map_d, tile + 2048, static_cast<int32_t>(col), static_cast<int32_t>(lane_at));
+                                tma_store_commit();
+                            }
+                            turn ^= 1;
+                        } else if (kMode == kWeights) {
+                            if (const int64_t left = p.cols - col; lane_at < p.hidden && left > 0) {
+                                T *d = static_cast<T *>(p.out) + col * p.ld_out + lane_at;
+                                const T *c = c0 > it.c0 ? d : p.addend ? static_cast<const T *>(p.addend) + col * p.ld_addend + lane_at : nullptr;
+                                store_columns(v, d, p.ld_out, c, c0 > it.c0 ? p.ld_out : p.ld_addend, left < 32 ? static_cast<int>(left) : 32);
+                            }
+                        } else if (const int64_t left = p.rows - col; lane_at < p.hidden && left > 0) {
+                            const int count = left < 32 ? static_cast<int>(left) : 32;
+                            float *sum = p.sum + col * p.hidden + lane_at;
+                            const float *before = p.first > 0 ? sum : nullptr;
+                            if (it.slot >= 0)
+                                store_columns<float, float>(v, p.part + (static_cast<int64_t>(it.slot) * kTile + j * 32) * kTile + (lane_at & (kTile - 1)),
+                                                            kTile, nullptr, 0, count);
+                            else if (p.last)
+                                store_columns(v, static_cast<uint16_t *>(p.out) + col * p.ld_out + lane_at, p.ld_out, before, p.hidden, count);
+                            else
+                                store_columns(v, sum, p.hidden, before, p.hidden, count);
                         }
                     }
                     c0 = c1;
                 }
             }
-            if (kMode == kLoss && lane_at < p.rows) {
-                p.stats[(lane_at * p.runs + it.run) * 2 + half] = make_float2(r.top, r.sum);
-            }
+            if (kMode == kLoss && lane_at < p.rows)
+                p.stats[(lane_at * p.runs + it.run) * 2 + half] = make_float2(r.top * kLog2e, r.sum);
         }
+        if (kMode == kGradient && lane == 0) tma_store_wait();
     }
     __syncwarp();
     tc_fence_before();
@@ -387,49 +447,63 @@ __global__ void __launch_bounds__(256) vocab_join_kernel(const __grid_constant__
     for (int i = lane; i < 2 * p.runs; i += 32) {
         const float2 q = of[i];
         const float m = fmaxf(top, q.x);
-        sum = sum * exp2_fast((top - m) * kLog2e) + q.y * exp2_fast((q.x - m) * kLog2e);
+        sum = sum * exp2_fast(top - m) + q.y * exp2_fast(q.x - m);
         top = m;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float other = __shfl_xor_sync(0xFFFFFFFFu, top, o), more = __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         const float m = fmaxf(top, other);
-        sum = sum * exp2_fast((top - m) * kLog2e) + more * exp2_fast((other - m) * kLog2e);
+        sum = sum * exp2_fast(top - m) + more * exp2_fast(other - m);
         top = m;
     }
     if (lane == 0) {
-        const float log_sum = logf(sum);
-        lse[t] = top + log_sum;
-        loss[t] = log_sum + (top - p.at_target[t]);
+        const float log_sum = log2f(sum);
+        lse[t] = (top + log_sum) * kLn2;
+        loss[t] = (fmaf(-p.at_target[t], kLog2e, top) + log_sum) * kLn2;
     }
 }
 
-// x with the rows that do not count set to 0: an operand of dw, where a NaN or an
-// infinity in such a row would meet g's zeros.
+// x with the rows that do not count set to 0, its rows filled up to whole columns of
+// 64: an operand of dw, where a NaN or an infinity in such a row would meet g's zeros.
 __global__ void __launch_bounds__(256)
-    vocab_live_rows_kernel(const uint16_t *x, int64_t ldx, const __grid_constant__ VocabParams p, uint16_t *to,
-                           int64_t ld_to) {
+    vocab_live_rows_kernel(const uint16_t *x, int64_t ldx, const __grid_constant__ VocabParams p, uint16_t *to, int64_t ld_to) {
     let_next_begin();
     after_previous();
     const int64_t t = blockIdx.x;
     const bool live = counts(p.target, p.weight, p.vocab, t);
-    const int64_t pieces = p.hidden / 8;
+    const int64_t pieces = live ? p.hidden / 8 : 0;
     for (int64_t i = threadIdx.x; i < pieces; i += 256)
-        reinterpret_cast<uint4 *>(to + t * ld_to)[i] =
-            live ? reinterpret_cast<const uint4 *>(x + t * ldx)[i] : make_uint4(0, 0, 0, 0);
-    for (int64_t h = pieces * 8 + threadIdx.x; h < p.hidden; h += 256) to[t * ld_to + h] = live ? x[t * ldx + h] : 0;
+        reinterpret_cast<uint4 *>(to + t * ld_to)[i] = reinterpret_cast<const uint4 *>(x + t * ldx)[i];
+    for (int64_t h = pieces * 8 + threadIdx.x; h < ld_to; h += 256) to[t * ld_to + h] = live && h < p.hidden ? x[t * ldx + h] : 0;
 }
 
-// dx from its partial sums, added in order.
-__global__ void __launch_bounds__(256) vocab_inputs_kernel(const float *part, const __grid_constant__ VocabParams p, uint16_t *dx, int64_t lddx) {
+// The tiles of dx whose k was cut: the parts' sums added in order.  A CTA: two rows
+// of x of a tile, a column to each thread.
+__global__ void __launch_bounds__(kTile) vocab_inputs_kernel(const __grid_constant__ VocabParams p) {
     let_next_begin();
     after_previous();
-    const int64_t n = p.rows * p.hidden;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-        float v = part[i];
-        for (int s = 1; s < p.splits; ++s) v += part[s * p.split_stride + i];
-        dx[i / p.hidden * lddx + i % p.hidden] = to_bf16(v);
+    const int64_t tile = blockIdx.x / (p.tile_n / 2);
+    Item it;
+    place_item(p, p.items + tile, it);
+    const int64_t h = it.m * kTile + threadIdx.x, t0 = blockIdx.x % (p.tile_n / 2) * 2, t = it.n0 * p.tile_n + t0;
+    if (h >= p.hidden || t >= p.rows) return;
+    const bool two = t + 1 < p.rows;
+    const float *of = p.part + (tile * kTile + t0) * kTile + threadIdx.x;
+    const int64_t stride = static_cast<int64_t>(p.rest) * kTile * kTile;
+    float a = 0.0f, b = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < p.splits; ++i) {
+        a += of[i * stride];
+        if (two) b += of[i * stride + kTile];
     }
+    const auto give = [&](int64_t row, float v) {
+        if (p.first > 0) v += p.sum[row * p.hidden + h];
+        if (p.last) static_cast<uint16_t *>(p.out)[row * p.ld_out + h] = to_bf16(v);
+        else p.sum[row * p.hidden + h] = v;
+    };
+    give(t, a);
+    if (two) give(t + 1, b);
 }
 
 // dw where no row is given: the addend, or 0.
@@ -471,67 +545,109 @@ int resident_pairs() {
 }
 
 template <int kMode, typename T>
-int launch(const VocabParams &p, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b2, cudaStream_t stream) {
-    const int pairs = resident_pairs<kMode, T>();
-    if (pairs < 1) return pairs;
-    const unsigned grid = 2 * static_cast<unsigned>(std::min(p.items, static_cast<int64_t>(pairs)));
-    return launch_early("vocab_product_kernel", vocab_product_kernel<kMode, T>, dim3(grid), kThreads, kSmem, 2, stream, a, b, b2, p);
+int launch(const VocabParams &p, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &c, const CUtensorMap &d, cudaStream_t stream) {
+    const int resident = resident_pairs<kMode, T>();
+    if (resident < 1) return resident;
+    const int64_t pairs = std::min(p.items + static_cast<int64_t>(p.rest) * p.splits, static_cast<int64_t>(resident));
+    return launch_early("vocab_product_kernel", vocab_product_kernel<kMode, T>, dim3(2 * static_cast<unsigned>(pairs)), kThreads, kSmem, 2,
+                        stream, a, b, c, d, p);
 }
 
 int encode(CUtensorMap *map, const void *base, int64_t inner, int64_t outer, int64_t ld, int box_outer) {
     return encode_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, ld * 2, kK, box_outer);
 }
-
-// Clocks of a chunk of 64 k, and of a tile's beginning and end that its neighbours do not hide.
-constexpr int64_t kChunkClocks = 520, kTileClocks = 500, kItemClocks = 2500;
-
-// Column runs of the loss pass: the count that leaves the pairs evenly busy.
-int32_t loss_runs(int64_t tiles_m, int64_t tiles_n, int64_t chunks, int64_t pairs) {
-    int64_t best = 0;
-    int32_t runs = 1;
-    for (int64_t r = 1; r <= std::min(tiles_n, std::max(int64_t{1}, 8 * pairs / tiles_m)); ++r) {
-        const int64_t clocks = ceil_div(tiles_m * r, pairs) * (ceil_div(tiles_n, r) * (chunks * kChunkClocks + kTileClocks) + kItemClocks);
-        if (r == 1 || clocks < best) best = clocks, runs = static_cast<int32_t>(r);
-    }
-    return runs;
+int encode_columns(CUtensorMap *map, const void *base, int64_t inner, int64_t outer) {
+    return encode_column_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, inner, outer, inner * 2, 2, kK);
+}
+int encode_store(CUtensorMap *map, const void *base, int64_t inner, int64_t outer) {
+    return encode_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, inner * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// Parts of the vocabulary that dx's sums are cut into where its tiles are few.
-int32_t input_splits(int64_t tiles, int64_t chunks, int64_t pairs, int64_t elements) {
-    int64_t best = 0;
-    int32_t splits = 1;
-    for (int64_t s = 1; s <= 64 && chunks >= 4 * s; ++s) {
-        const int64_t clocks = ceil_div(tiles * s, pairs) * (ceil_div(chunks, s) * kChunkClocks + kItemClocks) +
-                               (s > 1 ? 4000 + s * elements * 8 / 3500 : 0);
-        if (s == 1 || clocks < best) best = clocks, splits = static_cast<int32_t>(s);
+// Clocks of a chunk of 64 k at 256 columns, of a tile's beginning and end that its
+// neighbours do not hide, and of an item's.
+constexpr int64_t kChunkClocks = 520, kTileClocks = 500, kItemClocks = 2500;
+int64_t tile_clocks(int64_t chunks, int64_t columns) { return chunks * std::max(kChunkClocks * columns / kTile, int64_t{300}) + kTileClocks; }
+
+// Columns of the logits' tiles, and the loss's runs of them: what leaves the pairs
+// evenly busy.
+struct Split {
+    int32_t columns, runs;
+};
+Split loss_split(int64_t tiles_m, int64_t vocab, int64_t chunks, int64_t pairs) {
+    Split best{kTile, 1};
+    int64_t least = -1;
+    for (int32_t columns = kTile; columns >= 128; columns -= 32) {
+        const int64_t tiles = ceil_div(vocab, int64_t{columns});
+        for (int64_t rounds = 1; rounds <= 4; ++rounds) {
+            const int64_t r = std::max(std::min(tiles, rounds * pairs / tiles_m), int64_t{1});
+            const int64_t clocks = ceil_div(tiles_m * r, pairs) * (ceil_div(tiles, r) * tile_clocks(chunks, columns) + kItemClocks);
+            if (least < 0 || clocks < least) least = clocks, best = {columns, static_cast<int32_t>(r)};
+        }
     }
-    return splits;
+    return best;
+}
+int32_t gradient_columns(int64_t tiles_m, int64_t cols, int64_t chunks, int64_t pairs) {
+    int32_t best = kTile;
+    int64_t least = -1;
+    for (int32_t columns = kTile; columns >= 128; columns -= 32) {
+        const int64_t clocks = ceil_div(tiles_m * ceil_div(cols, int64_t{columns}), pairs) * tile_clocks(chunks, columns);
+        if (least < 0 || clocks < least) least = clocks, best = columns;
+    }
+    return best;
+}
+
+// dx's tiles over the pairs: whole ones as often as all pairs have one, and the rest
+// cut along k where that is sooner than another round (each part costs its beginning,
+// the write and the addition of its sums).
+struct Rounds {
+    int64_t items;
+    int32_t rest, splits;
+};
+constexpr int kMaxParts = 2;  // tiles of partial sums, of each pair
+Rounds input_rounds(int64_t tiles, int64_t chunks, int64_t resident) {
+    const int64_t rest = tiles % resident;
+    int64_t least = chunks * kChunkClocks + kItemClocks, splits = 1;
+    for (int64_t s = 2; rest > 0 && s * 4 <= chunks && s * rest <= kMaxParts * resident; ++s) {
+        const int64_t clocks = ceil_div(rest * s, resident) * (ceil_div(chunks, s) * kChunkClocks + kItemClocks) + 4000 + s * rest * 150;
+        if (clocks < least) least = clocks, splits = s;
+    }
+    return splits == 1 ? Rounds{tiles, 0, 1} : Rounds{tiles - rest, static_cast<int32_t>(rest), static_cast<int32_t>(splits)};
 }
 
 constexpr int64_t kPieceBytes = int64_t{256} << 20;  // of g, at most (or 256 columns)
 
 struct Plan {
     int64_t piece, pieces;   // columns of a piece, a multiple of the tile
-    int32_t runs, splits;
-    int64_t g, x, part, loss, grad;  // bytes
+    Split split;
+    int64_t resident;        // pairs
+    int64_t g, x, sum, part, loss, grad;  // bytes
 };
 int64_t room(int64_t bytes) { return ceil_div(bytes, 256) * 256; }
+int64_t live_ld(int64_t hidden) { return ceil_div(hidden, kK) * kK; }
 
 Plan plan_for(int64_t rows, int64_t vocab, int64_t hidden, int32_t dw_type) {
     Plan p{};
-    const int64_t pairs = std::max(sm_count() / 2, 1), tiles_t = ceil_div(rows, int64_t{kTile}), tiles_h = ceil_div(hidden, int64_t{kTile});
+    const int64_t tiles_t = ceil_div(rows, int64_t{kTile});
     const int64_t parts = dw_type == GAR_F32 ? 2 : 1;
+    p.resident = std::max(sm_count() / 2, 1);
     const int64_t most = std::max(kPieceBytes / (std::max(rows, int64_t{1}) * 2 * parts) / kTile, int64_t{1}) * kTile;
     p.pieces = ceil_div(vocab, most);
     p.piece = ceil_div(ceil_div(vocab, p.pieces), int64_t{kTile}) * kTile;
     p.pieces = ceil_div(vocab, p.piece);
-    p.runs = rows > 0 ? loss_runs(tiles_t, ceil_div(vocab, int64_t{kTile}), ceil_div(hidden, int64_t{kK}), pairs) : 1;
-    p.splits = rows > 0 ? input_splits(tiles_t * tiles_h, ceil_div(std::min(p.piece, vocab), int64_t{kK}), pairs, rows * hidden) : 1;
-    p.loss = room(rows * p.runs * 16) + room(rows * 4);
+    p.split = {kTile, 1};
+    if (rows > 0) p.split = loss_split(tiles_t, vocab, ceil_div(hidden, int64_t{kK}), p.resident);
     p.g = room(rows * p.piece * 2);
-    p.x = room(rows * ceil_div(hidden, 8) * 16);
-    p.part = p.splits > 1 || p.pieces > 1 ? room(rows * hidden * 4 * p.splits) : 0;
-    p.grad = p.g * parts + p.x + p.part;
+    p.x = room(rows * live_ld(hidden) * 2);
+    p.loss = room(rows * p.split.runs * 16) + room(rows * 4) + p.x;
+    p.sum = p.pieces > 1 ? room(rows * hidden * 4) : 0;
+    if (rows > 0) {
+        const int64_t tile_t = std::min(ceil_div(rows, int64_t{32}) * 32, int64_t{kTile});
+        for (const int64_t cols : {std::min(p.piece, vocab), vocab - (p.pieces - 1) * p.piece}) {
+            const Rounds r = input_rounds(ceil_div(rows, tile_t) * ceil_div(hidden, int64_t{kTile}), ceil_div(cols, int64_t{kK}), p.resident);
+            p.part = std::max(p.part, static_cast<int64_t>(r.rest) * r.splits * kTile * kTile * 4);
+        }
+    }
+    p.grad = p.g * parts + p.x + p.sum + p.part;
     return p;
 }
 
@@ -550,68 +666,82 @@ int check(const void *x, int64_t ldx, const void *w, int64_t ldw, const int32_t 
     return GAR_OK;
 }
 
+int copy_live_rows(const VocabParams &p, const uint16_t *x, int64_t ldx, uint16_t *to, cudaStream_t stream) {
+    return launch_early("vocab_live_rows_kernel", vocab_live_rows_kernel, dim3(static_cast<unsigned>(p.rows)), 256, 0, 1, stream, x, ldx, p, to,
+                        live_ld(p.hidden));
+}
+// Rows of x that do not start on 128 bytes load at half the rate (two lines for each
+// one's 128 bytes): copied to such that do where the logits take long enough.
+bool copy_pays(const uint16_t *x, int64_t ldx, const VocabParams &p) {
+    return (!aligned(x, 128) || ldx % 64) && static_cast<double>(p.rows) * p.vocab * p.hidden > 2.5e10;
+}
+
 // dw and the shares of dx of all pieces; T: dw's type.
 template <typename T>
-int gradient(VocabParams p, const Plan &how, const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t ldw, uint16_t *dx, int64_t lddx,
+int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t ldw, uint16_t *dx, int64_t lddx,
              const T *addend, int64_t ld_addend, T *dw, int64_t lddw, uint8_t *workspace, cudaStream_t stream) {
-    const int64_t rows = p.rows, vocab = p.vocab, hidden = p.hidden, ld_live = ceil_div(hidden, 8) * 8;
+    const int64_t rows = p.rows, vocab = p.vocab, hidden = p.hidden, ld_live = live_ld(hidden);
     constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
-    p.g = reinterpret_cast<uint16_t *>(workspace);
-    p.g_low = reinterpret_cast<uint16_t *>(workspace + how.g);
-    p.ldg = how.piece;
-    uint16_t *live = reinterpret_cast<uint16_t *>(workspace + kParts * how.g);
-    float *part = reinterpret_cast<float *>(workspace + kParts * how.g + how.x);
+    const auto g = reinterpret_cast<uint16_t *>(workspace), g_low = reinterpret_cast<uint16_t *>(workspace + how.g);
+    const auto live = reinterpret_cast<uint16_t *>(workspace + kParts * how.g);
+    const auto sum = reinterpret_cast<float *>(workspace + kParts * how.g + how.x);
+    const auto part = reinterpret_cast<float *>(workspace + kParts * how.g + how.x + how.sum);
     const int64_t tiles_t = ceil_div(rows, int64_t{kTile}), tiles_h = ceil_div(hidden, int64_t{kTile});
-    if (dw)
-        if (int rc = launch_early("vocab_live_rows_kernel", vocab_live_rows_kernel, dim3(static_cast<unsigned>(rows)), 256, 0, 1, stream, x,
-                                  ldx, p, live, ld_live))
-            return rc;
-    CUtensorMap rows_k{}, live_mn{};
-    if (int rc = encode(&rows_k, x, hidden, rows, ldx, 128)) return rc;
-    if (int rc = encode(&live_mn, live, hidden, rows, ld_live, 64)) return rc;
+    CUtensorMap rows_k{}, live_mn{}, g_mn{}, low_mn{}, g_to{}, low_to{};
+    const bool copied = dw || copy_pays(x, ldx, p);
+    if (copied)
+        if (int rc = copy_live_rows(p, x, ldx, live, stream)) return rc;
+    if (int rc = encode(&rows_k, copied ? live : x, hidden, rows, copied ? ld_live : ldx, 128)) return rc;
+    if (dw) {
+        if (int rc = encode_columns(&live_mn, live, ld_live, rows)) return rc;
+    }
+    if (int rc = encode_columns(&g_mn, g, how.piece, rows)) return rc;
+    if (int rc = encode_store(&g_to, g, how.piece, rows)) return rc;
+    if (kParts == 2) {
+        if (int rc = encode_columns(&low_mn, g_low, how.piece, rows)) return rc;
+        if (int rc = encode_store(&low_to, g_low, how.piece, rows)) return rc;
+    } else {
+        low_mn = g_mn, low_to = g_to;
+    }
     for (int64_t first = 0; first < vocab; first += how.piece) {
-        const int64_t cols = std::min(how.piece, vocab - first), tiles_v = ceil_div(cols, int64_t{kTile});
-        CUtensorMap w_k{}, w_mn{}, g_k{}, g_mn{}, low_mn{};
-        if (int rc = encode(&w_k, w + first * ldw, hidden, cols, ldw, 128)) return rc;
-        if (int rc = encode(&w_mn, w + first * ldw, hidden, cols, ldw, 64)) return rc;
-        if (int rc = encode(&g_k, p.g, cols, rows, p.ldg, 128)) return rc;
-        if (int rc = encode(&g_mn, p.g, cols, rows, p.ldg, 64)) return rc;
-        if (kParts == 2)
-            if (int rc = encode(&low_mn, p.g_low, cols, rows, p.ldg, 64)) return rc;
+        const int64_t cols = std::min(how.piece, vocab - first);
         VocabParams q = p;
-        q.first = first, q.cols = cols;
-        q.tiles_m = tiles_t, q.tiles_n = tiles_v, q.runs = static_cast<int32_t>(tiles_v), q.splits = 1, q.parts = 1;
-        q.chunks = static_cast<int32_t>(ceil_div(hidden, int64_t{kK}));
-        q.items = q.tiles_m * q.runs;
-        if (int rc = launch<kGradient, T>(q, rows_k, w_k, w_k, stream)) return rc;
+        q.first = first, q.cols = cols, q.last = first + cols == vocab;
+        q.parts = 1, q.rest = 0, q.splits = 1;
+        {
+            CUtensorMap w_k{};
+            q.chunks = static_cast<int32_t>(ceil_div(hidden, int64_t{kK}));
+            q.tile_n = gradient_columns(tiles_t, cols, q.chunks, how.resident);
+            q.tiles_m = tiles_t, q.tiles_n = ceil_div(cols, int64_t{q.tile_n}), q.runs = static_cast<int32_t>(q.tiles_n);
+            q.items = q.tiles_m * q.runs;
+            if (int rc = encode(&w_k, w + first * ldw, hidden, cols, ldw, q.tile_n / 2)) return rc;
+            if (int rc = launch<kGradient, T>(q, rows_k, w_k, g_to, low_to, stream)) return rc;
+        }
         if (dw) {
-            q.tiles_m = tiles_h, q.tiles_n = tiles_v, q.runs = static_cast<int32_t>(tiles_v), q.parts = kParts;
+            q.tile_n = kTile;
+            q.tiles_m = tiles_h, q.tiles_n = ceil_div(cols, int64_t{kTile}), q.runs = static_cast<int32_t>(q.tiles_n), q.parts = kParts;
             q.chunks = static_cast<int32_t>(ceil_div(rows, int64_t{kK}));
             q.items = q.tiles_m * q.runs;
             q.out = dw + first * lddw, q.ld_out = lddw;
             q.addend = addend ? addend + first * ld_addend : nullptr, q.ld_addend = ld_addend;
-            if (int rc = launch<kWeights, T>(q, live_mn, g_mn, kParts == 2 ? low_mn : g_mn, stream)) return rc;
+            if (int rc = launch<kWeights, T>(q, live_mn, g_mn, low_mn, low_mn, stream)) return rc;
         }
         if (dx) {
-            q.tiles_m = tiles_h, q.tiles_n = tiles_t, q.runs = static_cast<int32_t>(tiles_t), q.parts = 1, q.splits = how.splits;
+            CUtensorMap w_mn{}, g_k{};
+            q.tile_n = static_cast<int32_t>(std::min(ceil_div(rows, int64_t{32}) * 32, int64_t{kTile}));
+            q.tiles_m = tiles_h, q.tiles_n = ceil_div(rows, int64_t{q.tile_n}), q.runs = static_cast<int32_t>(q.tiles_n), q.parts = 1;
             q.chunks = static_cast<int32_t>(ceil_div(cols, int64_t{kK}));
-            q.items = q.tiles_m * q.runs * q.splits;
-            q.split_stride = rows * hidden;
-            q.out = part, q.ld_out = hidden;
-            q.addend = first > 0 ? part : nullptr, q.ld_addend = hidden;
-            if (how.part == 0) {
-                q.out = dx, q.ld_out = lddx;
-                if (int rc = launch<kInputs, uint16_t>(q, w_mn, g_k, g_k, stream)) return rc;
-            } else {
-                if (int rc = launch<kInputs, float>(q, w_mn, g_k, g_k, stream)) return rc;
-            }
+            const Rounds rounds = input_rounds(q.tiles_m * q.tiles_n, q.chunks, how.resident);
+            q.items = rounds.items, q.rest = rounds.rest, q.splits = rounds.splits;
+            q.out = dx, q.ld_out = lddx, q.sum = sum, q.part = part;
+            if (int rc = encode(&w_mn, w + first * ldw, hidden, cols, ldw, kK)) return rc;
+            if (int rc = encode_tile_map(&g_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g, cols, rows, how.piece * 2, kK, q.tile_n / 2)) return rc;
+            if (int rc = launch<kInputs, uint16_t>(q, w_mn, g_k, g_k, g_k, stream)) return rc;
+            if (q.rest > 0)
+                if (int rc = launch_early("vocab_inputs_kernel", vocab_inputs_kernel, dim3(static_cast<unsigned>(q.rest * (q.tile_n / 2))), kTile, 0, 1,
+                                          stream, q))
+                    return rc;
         }
-    }
-    if (dx && how.part > 0) {
-        p.splits = how.splits, p.split_stride = rows * hidden;
-        const int64_t blocks = std::min(ceil_div(rows * hidden, int64_t{1024}), static_cast<int64_t>(sm_count()) * 8);
-        return launch_early("vocab_inputs_kernel", vocab_inputs_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, 1, stream, part, p, dx,
-                            lddx);
     }
     return GAR_OK;
 }
@@ -639,17 +769,24 @@ extern "C" int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t
     VocabParams p{};
     p.rows = rows, p.vocab = vocab, p.hidden = hidden;
     p.target = target, p.weight = weight;
-    p.tiles_m = ceil_div(rows, int64_t{kTile}), p.tiles_n = ceil_div(vocab, int64_t{kTile});
-    p.runs = how.runs, p.splits = 1, p.parts = 1, p.chunks = static_cast<int32_t>(ceil_div(hidden, int64_t{kK}));
+    p.tile_n = how.split.columns;
+    p.tiles_m = ceil_div(rows, int64_t{kTile}), p.tiles_n = ceil_div(vocab, int64_t{p.tile_n});
+    p.runs = how.split.runs, p.parts = 1, p.splits = 1, p.chunks = static_cast<int32_t>(ceil_div(hidden, int64_t{kK}));
     p.items = p.tiles_m * p.runs;
     p.stats = static_cast<float2 *>(d_workspace);
-    p.at_target = reinterpret_cast<float *>(static_cast<uint8_t *>(d_workspace) + room(rows * how.runs * 16));
+    p.at_target = reinterpret_cast<float *>(static_cast<uint8_t *>(d_workspace) + room(rows * how.split.runs * 16));
     p.status = device_status();
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const uint16_t *from = static_cast<const uint16_t *>(x);
+    if (copy_pays(from, ldx, p)) {
+        const auto live = reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(p.at_target) + room(rows * 4));
+        if (int rc = copy_live_rows(p, from, ldx, live, stream)) return rc;
+        from = live, ldx = live_ld(hidden);
+    }
     CUtensorMap a{}, b{};
-    if (int rc = encode(&a, x, hidden, rows, ldx, 128)) return rc;
-    if (int rc = encode(&b, w, hidden, vocab, ldw, 128)) return rc;
-    if (int rc = launch<kLoss, float>(p, a, b, b, stream)) return rc;
+    if (int rc = encode(&a, from, hidden, rows, ldx, 128)) return rc;
+    if (int rc = encode(&b, w, hidden, vocab, ldw, p.tile_n / 2)) return rc;
+    if (int rc = launch<kLoss, float>(p, a, b, b, b, stream)) return rc;
     return launch_early("vocab_join_kernel", vocab_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, int64_t{8}))), 256, 0, 1, stream, p,
                         loss, lse);
 }
