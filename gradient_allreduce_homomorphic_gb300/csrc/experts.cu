@@ -10,6 +10,7 @@
 // and ranks within it come from comparing 32 pairs at a time.  No atomic decides
 // an order, so the rows are the same in every run.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -21,6 +22,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 32;
 constexpr int kMaxBlocks = 192;  // of the sort
@@ -46,20 +49,20 @@ __device__ __forceinline__ int expert_of(const SortParams &p, int32_t i) {
     return e >= 0 && e < p.experts ? e : -1;
 }
 
-__global__ void __launch_bounds__(kThreads) expert_count_kernel(const __grid_constant__ SortParams p) {
+__global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const __grid_constant__ SortParams p) {
     __shared__ int32_t of[kMaxExperts];
-    for (int e = threadIdx.x; e < p.experts; e += kThreads) of[e] = 0;
+    for (int e = threadIdx.x; e < p.experts; e += kSortThreads) of[e] = 0;
     __syncthreads();
     let_next_begin();
     after_previous();
     const int64_t first = static_cast<int64_t>(blockIdx.x) * p.per_block;
     const int32_t end = static_cast<int32_t>(min(first + p.per_block, static_cast<int64_t>(p.pairs)));
-    for (int32_t i = static_cast<int32_t>(first) + threadIdx.x; i < end; i += kThreads) {
+    for (int32_t i = static_cast<int32_t>(first) + threadIdx.x; i < end; i += kSortThreads) {
         const int e = expert_of(p, i);
         if (e >= 0) atomicAdd(&of[e], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.experts; e += kThreads) p.counts[static_cast<int64_t>(blockIdx.x) * p.experts + e] = of[e];
+    for (int e = threadIdx.x; e < p.experts; e += kSortThreads) p.counts[static_cast<int64_t>(blockIdx.x) * p.experts + e] = of[e];
 }
 
 // Rows of an expert of n pairs, and how many of them hold one.
@@ -67,15 +70,16 @@ __device__ __forceinline__ int32_t rows_for(const SortParams &p, int32_t n) {
     return p.capacity > 0 ? p.capacity : (n + p.align - 1) / p.align * p.align;
 }
 
-__global__ void __launch_bounds__(kThreads) expert_place_kernel(const __grid_constant__ SortParams p) {
-    __shared__ int32_t total[kMaxExperts];   // pairs of each expert
-    __shared__ int32_t ahead[kMaxExperts];   // of the CTAs before this one
-    __shared__ int32_t start[kMaxExperts];   // first row
-    __shared__ int32_t cursor[kWarps][kMaxExperts];
-    __shared__ int32_t sums[kWarps];
+__global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const __grid_constant__ SortParams p) {
+    extern __shared__ int32_t shared[];
+    __shared__ int32_t sums[kSortWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = p.experts;
-    for (int e = threadIdx.x; e < E; e += kThreads) total[e] = ahead[e] = 0;
-    for (int i = threadIdx.x; i < kWarps * E; i += kThreads) cursor[i / E][i % E] = 0;
+    int32_t *const total = shared;          // pairs of each expert
+    int32_t *const ahead = shared + E;      // of the CTAs before this one
+    int32_t *const start = shared + 2 * E;  // first row
+    int32_t *const cursor = shared + 3 * E; // [warp][expert]: the next rank
+    for (int e = threadIdx.x; e < E; e += kSortThreads) total[e] = ahead[e] = 0;
+    for (int i = threadIdx.x; i < kSortWarps * E; i += kSortThreads) cursor[i] = 0;
     __syncthreads();
     let_next_begin();
     after_previous();
@@ -83,17 +87,18 @@ __global__ void __launch_bounds__(kThreads) expert_place_kernel(const __grid_con
     // this CTA's pairs, a run of them to each warp
     const int64_t begin = static_cast<int64_t>(blockIdx.x) * p.per_block;
     const int32_t end = static_cast<int32_t>(min(begin + p.per_block, static_cast<int64_t>(p.pairs)));
-    const int32_t run = p.per_block / kWarps, from = static_cast<int32_t>(begin) + warp * run;
+    const int32_t run = p.per_block / kSortWarps, from = static_cast<int32_t>(begin) + warp * run;
     const int32_t to = min(from + run, end);
     for (int32_t i = from + lane; i < to; i += 32) {
         const int e = expert_of(p, i);
-        if (e >= 0) atomicAdd(&cursor[warp][e], 1);
+        if (e >= 0) atomicAdd(&cursor[warp * E + e], 1);
     }
-    if (gridDim.x > 1) {  // counts of every CTA, an expert by kThreads / E threads
-        const int parts = E >= kThreads ? 1 : kThreads / E;
-        for (int i = threadIdx.x; i < E * parts; i += kThreads) {
+    if (gridDim.x > 1) {  // counts of every CTA, an expert by kSortThreads / E threads
+        const int parts = E >= kSortThreads ? 1 : kSortThreads / E;
+        for (int i = threadIdx.x; i < E * parts; i += kSortThreads) {
             const int e = i % E, part = i / E;
             int32_t all = 0, before = 0;
+#pragma unroll 8
             for (int b = part; b < static_cast<int>(gridDim.x); b += parts) {
                 const int32_t n = p.counts[static_cast<int64_t>(b) * E + e];
                 all += n;
@@ -105,14 +110,14 @@ __global__ void __launch_bounds__(kThreads) expert_place_kernel(const __grid_con
     }
     __syncthreads();
     if (gridDim.x == 1)
-        for (int e = threadIdx.x; e < E; e += kThreads) {
+        for (int e = threadIdx.x; e < E; e += kSortThreads) {
             int32_t n = 0;
-            for (int w = 0; w < kWarps; ++w) n += cursor[w][e];
+            for (int w = 0; w < kSortWarps; ++w) n += cursor[w * E + e];
             total[e] = n;
         }
     __syncthreads();
     // first rows: a scan over the experts, consecutive ones to each thread
-    const int each = (E + kThreads - 1) / kThreads, e0 = min(static_cast<int>(threadIdx.x) * each, E), e1 = min(e0 + each, E);
+    const int each = (E + kSortThreads - 1) / kSortThreads, e0 = min(static_cast<int>(threadIdx.x) * each, E), e1 = min(e0 + each, E);
     int32_t mine = 0;
     for (int e = e0; e < e1; ++e) mine += rows_for(p, total[e]);
     int32_t scan = mine;
@@ -126,14 +131,14 @@ __global__ void __launch_bounds__(kThreads) expert_place_kernel(const __grid_con
     int32_t row = scan - mine;
     for (int w = 0; w < warp; ++w) row += sums[w];
     int32_t used = 0;  // rows of all experts
-    for (int w = 0; w < kWarps; ++w) used += sums[w];
+    for (int w = 0; w < kSortWarps; ++w) used += sums[w];
     for (int e = e0; e < e1; ++e) {
         start[e] = row;
         if (blockIdx.x == 0) p.offsets[e] = row;
         int32_t n = ahead[e];  // ranks that each warp's pairs begin at
-        for (int w = 0; w < kWarps; ++w) {
-            const int32_t c = cursor[w][e];
-            cursor[w][e] = n;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int32_t c = cursor[w * E + e];
+            cursor[w * E + e] = n;
             n += c;
         }
         row += rows_for(p, total[e]);
@@ -146,11 +151,11 @@ __global__ void __launch_bounds__(kThreads) expert_place_kernel(const __grid_con
         const unsigned same = __match_any_sync(kAll, e);
         int32_t at = -1;
         if (e >= 0) {
-            const int32_t rank = cursor[warp][e] + __popc(same & ((1u << lane) - 1));
+            const int32_t rank = cursor[warp * E + e] + __popc(same & ((1u << lane) - 1));
             if (p.capacity == 0 || rank < p.capacity) at = start[e] + rank;
         }
         __syncwarp();
-        if (e >= 0 && (same >> lane) == 1u) cursor[warp][e] += __popc(same);  // the last of them
+        if (e >= 0 && (same >> lane) == 1u) cursor[warp * E + e] += __popc(same);  // the last of them
         __syncwarp();
         if (i < to) p.position[i / p.per_worker][i % p.per_worker] = at;
         if (at >= 0) p.source[at] = i;
@@ -158,10 +163,10 @@ __global__ void __launch_bounds__(kThreads) expert_place_kernel(const __grid_con
     // rows without a pair: -1 within an expert's rows, -2 behind the last expert
     for (int e = blockIdx.x; e < E; e += gridDim.x) {
         const int32_t n = rows_for(p, total[e]);
-        for (int32_t r = min(total[e], n) + threadIdx.x; r < n; r += kThreads) p.source[start[e] + r] = -1;
+        for (int32_t r = min(total[e], n) + threadIdx.x; r < n; r += kSortThreads) p.source[start[e] + r] = -1;
     }
-    for (int64_t r = used + static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; r < p.rows;
-         r += static_cast<int64_t>(gridDim.x) * kThreads)
+    for (int64_t r = used + static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x; r < p.rows;
+         r += static_cast<int64_t>(gridDim.x) * kSortThreads)
         p.source[r] = -2;
 }
 
@@ -177,50 +182,98 @@ struct MoveParams {
     void *to;                              // the experts' rows written
     int64_t tokens, items, rows, hidden;   // tokens of a worker; items: P tokens
     int64_t ldx, ldo, ldy, ldt;
+    int64_t segments;                      // of a row
     int32_t k;
+    int32_t share;                         // warps of a CTA that share a token: 1, 2, 4 or 8
     int32_t has_weight, has_addend;
 };
 
-// V elements of a row, as one load or store of their V * sizeof(T) bytes.
+// V elements of a row as loaded and stored at one time: 16 bytes, or one element.
 template <typename T, int V>
-struct Piece {
-    float v[V];
+struct Piece;
+template <>
+struct Piece<float, 4> {
+    uint4 q;
+};
+template <>
+struct Piece<uint16_t, 8> {
+    uint4 q;
+};
+template <typename T>
+struct Piece<T, 1> {
+    T q;
 };
 template <typename T, int V>
 __device__ __forceinline__ Piece<T, V> load_piece(const T *p) {
-    Piece<T, V> r;
-    if constexpr (sizeof(T) * V == 16) {
-        const uint4 q = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r.v[i] = __uint_as_float(w[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r.v[2 * i] = bf16_lo(w[i]), r.v[2 * i + 1] = bf16_hi(w[i]);
-        }
-    } else {
-        static_assert(V == 1);
-        r.v[0] = load_f32(p);
-    }
-    return r;
+    if constexpr (V > 1) return {ld16(p)};
+    else return {__ldcs(p)};
+}
+// The same where `on`, else zero.  Loads that carry their own condition stay ahead of
+// their uses: with a branch around each the compiler puts load and use together, one
+// row's after the other's (8 rows of 8 KB to each of 32768 tokens 1904 us, 495 with
+// one row at a time and more warps).
+__device__ __forceinline__ uint4 load16_if(const void *p, bool on) {
+    uint4 q;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(q.x), "=&r"(q.y), "=&r"(q.z), "=&r"(q.w)
+        : "l"(p), "r"(static_cast<int>(on)));
+    return q;
+}
+__device__ __forceinline__ float load_one_if(const float *p, bool on) {
+    float v;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.cs.f32 %0, [%1];\n\t}"
+                 : "=&f"(v)
+                 : "l"(p), "r"(static_cast<int>(on)));
+    return v;
+}
+__device__ __forceinline__ uint16_t load_one_if(const uint16_t *p, bool on) {
+    uint16_t v;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.cs.u16 %0, [%1];\n\t}"
+                 : "=&h"(v)
+                 : "l"(p), "r"(static_cast<int>(on)));
+    return v;
 }
 template <typename T, int V>
-__device__ __forceinline__ void store_piece(T *p, const Piece<T, V> &r) {
-    if constexpr (sizeof(T) * V == 16) {
-        uint32_t w[4];
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(r.v[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(r.v[2 * i], r.v[2 * i + 1]);
-        }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ Piece<T, V> load_piece_if(const T *p, bool on) {
+    if constexpr (V > 1) return {load16_if(p, on)};
+    else return {load_one_if(p, on)};
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_piece(T *p, Piece<T, V> r) {
+    if constexpr (V > 1) st16(p, r.q);
+    else __stcs(p, r.q);
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Piece<T, V> &r, float (&v)[V]) {
+    if constexpr (V == 1) {
+        v[0] = load_f32(&r.q);
     } else {
-        store_f32(p, r.v[0]);
+        const uint32_t w[4] = {r.q.x, r.q.y, r.q.z, r.q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (V == 4) v[i] = __uint_as_float(w[i]);
+            else v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+        }
     }
 }
+template <typename T, int V>
+__device__ __forceinline__ Piece<T, V> pack(const float (&v)[V]) {
+    Piece<T, V> r;
+    if constexpr (V == 1) store_f32(&r.q, v[0]);
+    else if constexpr (V == 4)
+        r.q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    else
+        r.q = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    return r;
+}
+
+// A row is cut into segments of U pieces of V elements for each lane; `share` warps
+// of a CTA take a token's segments in turn, and a lane has all its loads of a segment
+// (and of up to J of the token's rows) under way at one time.
+__host__ __device__ constexpr int pieces_of(int V, int J) { return V == 1 ? (J >= 8 ? 2 : 4) : (J >= 8 ? 1 : J >= 4 ? 2 : 4); }
 
 // The row of a token's choice `lane`, -1 for none.
 __device__ __forceinline__ int32_t row_of(const MoveParams &p, int64_t w, int64_t t, int lane) {
@@ -233,133 +286,233 @@ template <typename T, int V>
 __device__ __forceinline__ void clear_rows(const MoveParams &p, int64_t r0, int lane) {
     const int64_t r = r0 + lane;
     unsigned empty = __ballot_sync(kAll, r < p.rows && p.source[r < p.rows ? r : 0] == -1);
-    const Piece<T, V> zero{};
+    const float zero[V] = {};
     while (empty) {
         T *to = static_cast<T *>(p.to) + (r0 + __ffs(empty) - 1) * p.ldt;
         empty &= empty - 1;
         const int64_t whole = p.hidden / V * V;
-        for (int64_t h = lane * V; h < whole; h += 32 * V) store_piece<T, V>(to + h, zero);
+        for (int64_t h = lane * V; h < whole; h += 32 * V) store_piece<T, V>(to + h, pack<T, V>(zero));
         for (int64_t h = whole + lane; h < p.hidden; h += 32) store_f32(to + h, 0.0f);
     }
+}
+
+// A warp's token and segments.
+struct Place {
+    int64_t w, t, first;
+    bool on;
+};
+__device__ __forceinline__ Place place_of(const MoveParams &p) {
+    const int warp = threadIdx.x >> 5;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * (kWarps / p.share) + warp / p.share;
+    Place r;
+    r.on = at < p.items;
+    r.w = r.on ? at / p.tokens : 0, r.t = r.on ? at % p.tokens : 0, r.first = warp % p.share;
+    return r;
+}
+// The CTAs behind the tokens' clear rows.
+__device__ __forceinline__ int64_t clearing_cta(const MoveParams &p) {
+    return blockIdx.x - (p.items + kWarps / p.share - 1) / (kWarps / p.share);
 }
 
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) expert_gather_kernel(const __grid_constant__ MoveParams p) {
     let_next_begin();
     after_previous();
+    constexpr int U = pieces_of(V, 4);
     const int lane = threadIdx.x & 31;
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (at >= p.items) {
-        clear_rows<T, V>(p, (at - p.items) * 32, lane);
+    if (const int64_t c = clearing_cta(p); c >= 0) {
+        clear_rows<T, V>(p, (c * kWarps + (threadIdx.x >> 5)) * 32, lane);
         return;
     }
-    const int64_t w = at / p.tokens, t = at % p.tokens;
-    const T *x = static_cast<const T *>(p.x[w]) + t * p.ldx;
-    const int32_t row = row_of(p, w, t, lane);
-    const float weight = p.has_weight && lane < p.k ? p.weight[w][t * p.k + lane] : 1.0f;
-    const int64_t whole = p.hidden / V * V;
-    for (int64_t h0 = 0; h0 < p.hidden; h0 += 32 * V) {
-        const int64_t h = h0 + lane * V;
-        const bool in = h < whole;
-        Piece<T, V> v{};
-        if (in) v = load_piece<T, V>(x + h);
+    const Place at = place_of(p);
+    if (!at.on) return;
+    const T *x = static_cast<const T *>(p.x[at.w]) + at.t * p.ldx;
+    const int32_t row = row_of(p, at.w, at.t, lane);
+    const float weight = p.has_weight && lane < p.k ? p.weight[at.w][at.t * p.k + lane] : 1.0f;
+    for (int64_t s = at.first; s < p.segments; s += p.share) {
+        const int64_t h0 = s * (32 * U * V) + lane * V;
+        Piece<T, V> in[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (h0 + u * 32 * V + V <= p.hidden) in[u] = load_piece<T, V>(x + h0 + u * 32 * V);
         for (int j = 0; j < p.k; ++j) {
             const int32_t r = __shfl_sync(kAll, row, j);
             const float f = __shfl_sync(kAll, weight, j);
-            if (r < 0 || !in) continue;
-            Piece<T, V> o = v;
-            if (p.has_weight)
+            if (r < 0) continue;  // all lanes
+            T *to = static_cast<T *>(p.to) + r * p.ldt;
 #pragma unroll
-                for (int i = 0; i < V; ++i) o.v[i] *= f;
-            store_piece<T, V>(static_cast<T *>(p.to) + static_cast<int64_t>(r) * p.ldt + h, o);
+            for (int u = 0; u < U; ++u) {
+                const int64_t h = h0 + u * 32 * V;
+                if (h + V > p.hidden) {  // single elements behind the last whole piece
+                    if (V > 1)
+                        for (int64_t e = h; e < p.hidden; ++e) store_f32(to + e, p.has_weight ? load_f32(x + e) * f : load_f32(x + e));
+                    continue;
+                }
+                if (p.has_weight) {
+                    float v[V];
+                    unpack<T, V>(in[u], v);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[i] *= f;
+                    store_piece<T, V>(to + h, pack<T, V>(v));
+                } else {
+                    store_piece<T, V>(to + h, in[u]);
+                }
+            }
         }
-    }
-    for (int j = 0; j < p.k; ++j) {
-        const int32_t r = __shfl_sync(kAll, row, j);
-        const float f = __shfl_sync(kAll, weight, j);
-        if (r >= 0)
-            for (int64_t h = whole + lane; h < p.hidden; h += 32)
-                store_f32(static_cast<T *>(p.to) + static_cast<int64_t>(r) * p.ldt + h, p.has_weight ? load_f32(x + h) * f : load_f32(x + h));
     }
 }
 
-template <typename T, int V>
+// J rows of a token at a time (J >= k where k <= 8).
+template <typename T, int V, int J>
 __global__ void __launch_bounds__(kThreads) expert_combine_kernel(const __grid_constant__ MoveParams p) {
     let_next_begin();
     after_previous();
+    constexpr int U = pieces_of(V, J);
     const int lane = threadIdx.x & 31;
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (at >= p.items) return;
-    const int64_t w = at / p.tokens, t = at % p.tokens;
-    const T *add = p.has_addend ? static_cast<const T *>(p.x[w]) + t * p.ldx : nullptr;
-    T *out = static_cast<T *>(p.out[w]) + t * p.ldo;
-    const int32_t row = row_of(p, w, t, lane);
-    const float weight = p.has_weight && lane < p.k ? p.weight[w][t * p.k + lane] : 1.0f;
-    const auto take = [&](int64_t h, bool in, auto size) {
-        constexpr int N = decltype(size)::value;
-        Piece<T, N> sum{};
-        for (int j = 0; j < p.k; ++j) {
-            const int32_t r = __shfl_sync(kAll, row, j);
-            const float f = __shfl_sync(kAll, weight, j);
-            if (r < 0 || !in) continue;
-            const Piece<T, N> v = load_piece<T, N>(static_cast<const T *>(p.y) + static_cast<int64_t>(r) * p.ldy + h);
+    const Place at = place_of(p);
+    if (!at.on) return;
+    const T *add = p.has_addend ? static_cast<const T *>(p.x[at.w]) + at.t * p.ldx : nullptr;
+    T *out = static_cast<T *>(p.out[at.w]) + at.t * p.ldo;
+    const T *const y = static_cast<const T *>(p.y);
+    const int32_t row = row_of(p, at.w, at.t, lane);
+    const float weight = row < 0 ? 0.0f : p.has_weight ? p.weight[at.w][at.t * p.k + lane] : 1.0f;
+    for (int64_t s = at.first; s < p.segments; s += p.share) {
+        const int64_t h0 = s * (32 * U * V) + lane * V;
+        float sum[U][V];
+        Piece<T, V> a[U];
 #pragma unroll
-            for (int i = 0; i < N; ++i) sum.v[i] = fmaf(v.v[i], f, sum.v[i]);
-        }
-        if (!in) return;
-        if (add) {
-            const Piece<T, N> a = load_piece<T, N>(add + h);
+        for (int u = 0; u < U; ++u) {
+            a[u] = load_piece_if<T, V>(add + h0 + u * 32 * V, add && h0 + u * 32 * V + V <= p.hidden);
 #pragma unroll
-            for (int i = 0; i < N; ++i) sum.v[i] += a.v[i];
+            for (int i = 0; i < V; ++i) sum[u][i] = 0.0f;
         }
-        store_piece<T, N>(out + h, sum);
-    };
-    const int64_t whole = p.hidden / V * V;
-    for (int64_t h0 = 0; h0 < whole; h0 += 32 * V) take(h0 + lane * V, h0 + lane * V < whole, std::integral_constant<int, V>{});
-    for (int64_t h0 = whole; h0 < p.hidden; h0 += 32) take(h0 + lane, h0 + lane < p.hidden, std::integral_constant<int, 1>{});
+        for (int j0 = 0; j0 < p.k; j0 += J) {
+            Piece<T, V> in[J][U];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int32_t r = __shfl_sync(kAll, row, (j0 + j) & 31);  // lanes behind the choices hold -1
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    in[j][u] = load_piece_if<T, V>(y + r * p.ldy + h0 + u * 32 * V, r >= 0 && h0 + u * 32 * V + V <= p.hidden);
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float f = __shfl_sync(kAll, weight, (j0 + j) & 31);  // 0 for a choice without a row
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float v[V];
+                    unpack<T, V>(in[j][u], v);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum[u][i] = fmaf(v[i], f, sum[u][i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t h = h0 + u * 32 * V;
+            if (h + V <= p.hidden) {
+                if (add) {
+                    float v[V];
+                    unpack<T, V>(a[u], v);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum[u][i] += v[i];
+                }
+                store_piece<T, V>(out + h, pack<T, V>(sum[u]));
+            } else if (V > 1) {
+                for (int64_t e = h; e < p.hidden; ++e) {
+                    float v = 0.0f;
+                    for (int j = 0; j < p.k; ++j) {
+                        const int32_t r = p.position[at.w][at.t * p.k + j];
+                        if (r >= 0 && r < p.rows) v = fmaf(load_f32(y + r * p.ldy + e), p.has_weight ? p.weight[at.w][at.t * p.k + j] : 1.0f, v);
+                    }
+                    store_f32(out + e, add ? v + load_f32(add + e) : v);
+                }
+            }
+        }
+    }
 }
 
-template <typename T, int V>
+template <typename T, int V, int J>
 __global__ void __launch_bounds__(kThreads) expert_combine_grad_kernel(const __grid_constant__ MoveParams p) {
+    __shared__ float dots[kWarps][kMaxChoices];
     let_next_begin();
     after_previous();
-    const int lane = threadIdx.x & 31;
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (at >= p.items) {
-        clear_rows<T, V>(p, (at - p.items) * 32, lane);
+    constexpr int U = pieces_of(V, J);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (const int64_t c = clearing_cta(p); c >= 0) {
+        clear_rows<T, V>(p, (c * kWarps + warp) * 32, lane);
         return;
     }
-    const int64_t w = at / p.tokens, t = at % p.tokens;
-    const T *dout = static_cast<const T *>(p.x[w]) + t * p.ldx;
-    const int32_t row = row_of(p, w, t, lane);
-    const float weight = lane < p.k ? p.weight[w][t * p.k + lane] : 0.0f;
-    float mine = 0.0f;
-    for (int j = 0; j < p.k; ++j) {
-        const int32_t r = __shfl_sync(kAll, row, j);
-        const float f = __shfl_sync(kAll, weight, j);
-        if (r < 0) continue;
-        const T *y = static_cast<const T *>(p.y) + static_cast<int64_t>(r) * p.ldy;
-        T *to = static_cast<T *>(p.to) + static_cast<int64_t>(r) * p.ldt;
-        float dot = 0.0f;
-        const auto take = [&](int64_t h, auto size) {
-            constexpr int N = decltype(size)::value;
-            Piece<T, N> d = load_piece<T, N>(dout + h);
-            const Piece<T, N> v = load_piece<T, N>(y + h);
+    const Place at = place_of(p);
+    const T *const y = static_cast<const T *>(p.y);
+    T *const to = static_cast<T *>(p.to);
+    float mine = 0.0f;  // lane j: the product with row j so far
+    if (at.on) {
+        const T *dout = static_cast<const T *>(p.x[at.w]) + at.t * p.ldx;
+        const int32_t row = row_of(p, at.w, at.t, lane);
+        const float weight = lane < p.k ? p.weight[at.w][at.t * p.k + lane] : 0.0f;
+        for (int j0 = 0; j0 < p.k; j0 += J) {
+            int32_t to_row[J];
+            float dot[J];
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                dot = fmaf(d.v[i], v.v[i], dot);
-                d.v[i] *= f;
+            for (int j = 0; j < J; ++j) {
+                to_row[j] = __shfl_sync(kAll, row, (j0 + j) & 31);  // lanes behind the choices hold -1
+                dot[j] = 0.0f;
             }
-            store_piece<T, N>(to + h, d);
-        };
-        const int64_t whole = p.hidden / V * V;
-        for (int64_t h = lane * V; h < whole; h += 32 * V) take(h, std::integral_constant<int, V>{});
-        for (int64_t h = whole + lane; h < p.hidden; h += 32) take(h, std::integral_constant<int, 1>{});
+            for (int64_t s = at.first; s < p.segments; s += p.share) {
+                const int64_t h0 = s * (32 * U * V) + lane * V;
+                Piece<T, V> d[U], in[J][U];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
-        if (lane == j) mine = dot;
+                for (int u = 0; u < U; ++u) d[u] = load_piece_if<T, V>(dout + h0 + u * 32 * V, h0 + u * 32 * V + V <= p.hidden);
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        in[j][u] = load_piece_if<T, V>(y + to_row[j] * p.ldy + h0 + u * 32 * V, to_row[j] >= 0 && h0 + u * 32 * V + V <= p.hidden);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const float f = __shfl_sync(kAll, weight, (j0 + j) & 31);
+                    const int32_t r = to_row[j];
+                    if (r < 0) continue;  // all lanes
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int64_t h = h0 + u * 32 * V;
+                        if (h + V <= p.hidden) {
+                            float g[V], v[V];
+                            unpack<T, V>(d[u], g);
+                            unpack<T, V>(in[j][u], v);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) {
+                                dot[j] = fmaf(g[i], v[i], dot[j]);
+                                g[i] *= f;
+                            }
+                            store_piece<T, V>(to + r * p.ldt + h, pack<T, V>(g));
+                        } else if (V > 1) {
+                            for (int64_t e = h; e < p.hidden; ++e) {
+                                const float g = load_f32(dout + e);
+                                dot[j] = fmaf(g, load_f32(y + r * p.ldy + e), dot[j]);
+                                store_f32(to + r * p.ldt + e, g * f);
+                            }
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                float v = dot[j];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+                if (lane == j0 + j) mine = v;
+            }
+        }
     }
-    if (lane < p.k) p.dweight[w][t * p.k + lane] = mine;
+    if (p.share > 1) {  // the warps' shares, added in order
+        dots[warp][lane] = mine;
+        __syncthreads();
+        if (warp % p.share != 0) return;
+        for (int i = 1; i < p.share; ++i) mine += dots[warp + i][lane];
+    }
+    if (at.on && lane < p.k) p.dweight[at.w][at.t * p.k + lane] = mine;
 }
 
 // ------------------------------------------------ the chosen experts' weights
@@ -371,6 +524,7 @@ struct WeightParams {
     const float *dweight[GAR_MAX_WORKERS];
     int64_t tokens, items, ldz;
     int32_t experts, k, accumulate;
+    int32_t wide;  // dz's rows start on 16 bytes
 };
 
 // L lanes to a token (L >= k, a power of two), a choice to each.
@@ -428,7 +582,10 @@ __global__ void __launch_bounds__(kThreads) expert_weights_grad_kernel(const __g
         for (int i = 0; i < 32 / L; ++i) {
             if (first + i >= p.items) break;
             T *dz = static_cast<T *>(p.dz[(first + i) / p.tokens]) + (first + i) % p.tokens * p.ldz;
-            for (int e = lane; e < p.experts; e += 32) store_f32(dz + e, 0.0f);
+            constexpr int V = 16 / sizeof(T);
+            const int whole = p.wide ? p.experts / V * V : 0;
+            for (int e = lane * V; e < whole; e += 32 * V) *reinterpret_cast<uint4 *>(dz + e) = make_uint4(0, 0, 0, 0);
+            for (int e = whole + lane; e < p.experts; e += 32) store_f32(dz + e, 0.0f);
         }
         __syncwarp();
     }
@@ -477,17 +634,43 @@ int check_rows(const void *y, int64_t ld, int64_t rows, int64_t hidden, int elem
     return GAR_OK;
 }
 
+// The sort's shared memory at most, told to the runtime once.
+int allow_shared() {
+    static std::atomic<int> done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return fail(GAR_ECUDA, "no current device");
+    if (done[dev & 63].load(std::memory_order_relaxed)) return GAR_OK;
+    const cudaError_t e = cudaFuncSetAttribute(expert_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>((3 + kSortWarps) * kMaxExperts * sizeof(int32_t)));
+    if (e != cudaSuccess) return fail(GAR_ECUDA, "expert_place_kernel: %s", cudaGetErrorString(e));
+    done[dev & 63].store(1, std::memory_order_relaxed);
+    return GAR_OK;
+}
+
 enum { kGather, kCombine, kCombineGrad };
 template <typename T, int V>
-int launch_move(int which, const MoveParams &p, bool clears, cudaStream_t stream) {
-    const int64_t warps = p.items + (clears ? ceil_div(p.rows, int64_t{32}) : 0);
-    if (warps == 0) return GAR_OK;
-    const dim3 grid(static_cast<unsigned>(ceil_div(warps, int64_t{kWarps})));
-    if (which == kGather) return launch_early("expert_gather_kernel", expert_gather_kernel<T, V>, grid, kThreads, 0, 1, stream, p);
-    if (which == kCombine) return launch_early("expert_combine_kernel", expert_combine_kernel<T, V>, grid, kThreads, 0, 1, stream, p);
-    return launch_early("expert_combine_grad_kernel", expert_combine_grad_kernel<T, V>, grid, kThreads, 0, 1, stream, p);
+int launch_move(int which, MoveParams &p, bool clears, cudaStream_t stream) {
+    const auto go = [&](auto rows) {
+        constexpr int J = decltype(rows)::value;
+        p.segments = ceil_div(p.hidden, int64_t{32 * pieces_of(V, J) * V});
+        p.share = 1;
+        while (p.share < kWarps && p.share * 2 <= p.segments && p.items * p.share < sm_count() * int64_t{24}) p.share *= 2;
+        const int64_t ctas = ceil_div(p.items, int64_t{kWarps / p.share}) + (clears ? ceil_div(p.rows, int64_t{32 * kWarps}) : 0);
+        if (ctas == 0) return static_cast<int>(GAR_OK);
+        const dim3 grid(static_cast<unsigned>(ctas));
+        if (which == kCombine) return launch_early("expert_combine_kernel", expert_combine_kernel<T, V, J>, grid, kThreads, 0, 1, stream, p);
+        if (which == kCombineGrad)
+            return launch_early("expert_combine_grad_kernel", expert_combine_grad_kernel<T, V, J>, grid, kThreads, 0, 1, stream, p);
+        if constexpr (J == 4) return launch_early("expert_gather_kernel", expert_gather_kernel<T, V>, grid, kThreads, 0, 1, stream, p);
+        return static_cast<int>(GAR_OK);
+    };
+    if (which == kGather) return go(std::integral_constant<int, 4>{});
+    if (p.k <= 1) return go(std::integral_constant<int, 1>{});
+    if (p.k <= 2) return go(std::integral_constant<int, 2>{});
+    if (p.k <= 4) return go(std::integral_constant<int, 4>{});
+    return go(std::integral_constant<int, 8>{});
 }
-int launch_move_as(int which, int32_t dtype, bool wide, const MoveParams &p, bool clears, cudaStream_t stream) {
+int launch_move_as(int which, int32_t dtype, bool wide, MoveParams &p, bool clears, cudaStream_t stream) {
     if (dtype == GAR_F32) return wide ? launch_move<float, 4>(which, p, clears, stream) : launch_move<float, 1>(which, p, clears, stream);
     return wide ? launch_move<uint16_t, 8>(which, p, clears, stream) : launch_move<uint16_t, 1>(which, p, clears, stream);
 }
@@ -545,13 +728,17 @@ extern "C" int gar_expert_sort(const int32_t *const *choice, int32_t P, int64_t 
     p.experts = experts, p.align = align, p.capacity = capacity, p.rows = rows;
     p.source = source, p.offsets = offsets, p.counts = static_cast<int32_t *>(d_workspace);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    // one CTA, and one launch, for few pairs; 4096 pairs a CTA else, as far as the SMs go (262144 pairs of 256 experts, both
+    // launches: 2048 a CTA of 256 threads 41 us, for each CTA begins with all CTAs' counts)
     const int64_t most = std::min(sm_count(), kMaxBlocks);
-    const int64_t blocks = std::max(std::min(ceil_div(int64_t{p.pairs}, int64_t{2048}), most), int64_t{1});
-    p.per_block = static_cast<int32_t>(std::max(ceil_div(ceil_div(int64_t{p.pairs}, blocks), int64_t{kThreads}) * kThreads, int64_t{kThreads}));
+    const int64_t blocks = p.pairs <= 8192 ? 1 : std::min(ceil_div(int64_t{p.pairs}, int64_t{4096}), most);
+    p.per_block = static_cast<int32_t>(std::max(ceil_div(ceil_div(int64_t{p.pairs}, blocks), int64_t{kSortThreads}), int64_t{1}) * kSortThreads);
     const dim3 grid(static_cast<unsigned>(std::max(ceil_div(int64_t{p.pairs}, int64_t{p.per_block}), int64_t{1})));
+    const size_t shared = static_cast<size_t>(3 + kSortWarps) * experts * sizeof(int32_t);
+    if (int rc = allow_shared()) return rc;
     if (grid.x > 1)
-        if (int rc = launch_early("expert_count_kernel", expert_count_kernel, grid, kThreads, 0, 1, stream, p)) return rc;
-    return launch_early("expert_place_kernel", expert_place_kernel, grid, kThreads, 0, 1, stream, p);
+        if (int rc = launch_early("expert_count_kernel", expert_count_kernel, grid, kSortThreads, 0, 1, stream, p)) return rc;
+    return launch_early("expert_place_kernel", expert_place_kernel, grid, kSortThreads, shared, 1, stream, p);
 }
 
 extern "C" int gar_expert_gather(const void *const *x, int32_t P, int64_t tokens, int64_t hidden, int64_t ldx, int32_t dtype, int32_t k,
@@ -669,6 +856,7 @@ extern "C" int gar_expert_weights_grad(const float *const *weight, const float *
         p.weight[i] = const_cast<float *>(weight[i]);
     }
     p.tokens = tokens, p.items = P * tokens, p.ldz = lddz, p.experts = experts, p.k = k, p.accumulate = accumulate != 0;
+    p.wide = rows_on_16(p.dz, P, lddz, size);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     return dtype == GAR_F32 ? launch_weights<float>(true, p, stream) : launch_weights<uint16_t>(true, p, stream);
 }
