@@ -23,9 +23,13 @@ namespace gar {
 namespace {
 
 constexpr int kThreads = 256;
+// Tiles of 32 KB, 8 loads of a thread under way, handed out round the CTAs: 8 x 45M
+// values out of place 484 us; tiles of 16 KB and twice the CTAs 543, two batches of 8
+// to a tile 505, runs of tiles to each CTA 550.
 constexpr int kVecs = 8;                               // of 16 bytes, of a thread in a tile
+constexpr int kCtas = 4;                               // of an SM
 constexpr int64_t kTileBytes = kThreads * kVecs * 16;
-constexpr int kMaxSums = 1216;                         // partial sums of a worker and launch
+constexpr int kMaxSums = 2048;                         // partial sums of a worker and launch
 
 template <int NPTR, int NTENSOR>
 struct ClipParams {
@@ -34,7 +38,7 @@ struct ClipParams {
     int32_t sums, launches;  // partial sums of a worker in one launch; launches
     int32_t launch;
     float max_norm;
-    double *partial;         // [launches][norms][sums]
+    double *partial;         // [launches][norms][sums], each written by every call
     float *norm;
     unsigned int *status;
     int64_t tiles;           // of one worker
@@ -44,8 +48,9 @@ struct ClipParams {
     const void *src[NPTR];   // [tensor][worker]
     void *dst[NPTR];
 };
-using ClipSmall = ClipParams<96, 64>;
-using ClipLarge = ClipParams<1536, 320>;
+constexpr int kSmallPointers = 96, kSmallTensors = 64, kLargePointers = 1536, kLargeTensors = 320;
+using ClipSmall = ClipParams<kSmallPointers, kSmallTensors>;
+using ClipLarge = ClipParams<kLargePointers, kLargeTensors>;
 static_assert(sizeof(ClipSmall) <= 4096 && sizeof(ClipLarge) <= 32000, "parameters exceed the launch limit");
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -168,8 +173,9 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     after_previous();
     const int w = blockIdx.y;
     double sum = 0.0;
+    int i = tensor_of(p, blockIdx.x);
     for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x) {
-        const int i = tensor_of(p, t);
+        while (p.first[i + 1] <= t) ++i;
         const void *x = p.src[i * p.P + w];
         sum += p.dtype[i] == GAR_F32 ? tile_squares(static_cast<const float *>(x), p.numel[i], t - p.first[i])
                                      : tile_squares(static_cast<const uint16_t *>(x), p.numel[i], t - p.first[i]);
@@ -242,8 +248,9 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
         if (!finite && p.status) atomicOr(p.status, static_cast<unsigned int>(GAR_STATUS_NONFINITE));
     }
     const float c = finite && norm > p.max_norm ? p.max_norm / norm : 1.0f;
+    int i = tensor_of(p, p.tiles - 1 - blockIdx.x);
     for (int64_t t = p.tiles - 1 - blockIdx.x; t >= 0; t -= gridDim.x) {
-        const int i = tensor_of(p, t);
+        while (p.first[i] > t) --i;
         const void *x = p.src[i * p.P + w];
         void *y = p.dst[i * p.P + w];
         if (c == 1.0f && x == y) continue;  // stays as it is
@@ -254,22 +261,23 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
 
 // ---------------------------------------------------------------------- host
 int tensors_per_launch(int P, int pointers, int tensors) { return std::max(1, std::min(tensors, pointers / P)); }
-bool is_small(int P, int32_t count) { return count <= tensors_per_launch(P, 96, 64) && static_cast<int64_t>(P) * count <= 96; }
+bool is_small(int P, int32_t count) { return count <= kSmallTensors && static_cast<int64_t>(P) * count <= kSmallPointers; }
 int32_t launches_for(int P, int32_t count) {
-    return is_small(P, count) ? 1 : static_cast<int32_t>(std::max(ceil_div(count, int64_t{tensors_per_launch(P, 1536, 320)}), int64_t{1}));
+    return static_cast<int32_t>(std::max(ceil_div(count, int64_t{tensors_per_launch(P, kLargePointers, kLargeTensors)}), int64_t{1}));
 }
 
 template <typename Params>
 int run(const void *const *src, void *const *dst, int32_t P, const int64_t *numel, const int32_t *dtype, int32_t count, int32_t norms,
-        float max_norm, float *norm, double *partial, int per_launch, bool scale, cudaStream_t stream) {
+        float max_norm, float *norm, double *partial, bool small, bool scale, cudaStream_t stream) {
     Params p;
-    p.P = P, p.norms = norms, p.max_norm = max_norm, p.norm = norm, p.partial = partial, p.status = device_status();
-    p.launches = static_cast<int32_t>(std::max(ceil_div(count, int64_t{per_launch}), int64_t{1}));
-    // as many CTAs as fit the SMs at one time, the workers' together
-    const int resident = std::min(sm_count() * 4, kMaxSums);
-    p.sums = std::max(1, resident / norms);
-    const auto fill = [&](int32_t l) {
-        p.launch = l;
+    p.norms = norms, p.max_norm = max_norm, p.norm = norm, p.partial = partial, p.status = device_status();
+    p.launches = small ? 1 : launches_for(norms, count);
+    // as many CTAs as the SMs hold at one time, the workers' together
+    int64_t tiles = 0;
+    for (int32_t i = 0; i < count; ++i) tiles += ceil_div(numel[i] * elem_bytes(dtype[i]), kTileBytes);
+    p.sums = static_cast<int32_t>(std::max(std::min(tiles, int64_t{std::min(sm_count() * kCtas, kMaxSums) / norms}), int64_t{1}));
+    const auto fill = [&](int32_t l, int32_t workers, int32_t per_launch) {
+        p.launch = l, p.P = workers;
         const int32_t i0 = l * per_launch;
         p.count = std::min(per_launch, count - i0);
         p.tiles = 0;
@@ -277,24 +285,26 @@ int run(const void *const *src, void *const *dst, int32_t P, const int64_t *nume
             p.numel[i] = numel[i0 + i], p.dtype[i] = dtype[i0 + i];
             p.first[i] = p.tiles;
             p.tiles += ceil_div(numel[i0 + i] * elem_bytes(dtype[i0 + i]), kTileBytes);
-            for (int w = 0; w < P; ++w) {
-                p.src[i * P + w] = src[static_cast<int64_t>(w) * count + i0 + i];
-                p.dst[i * P + w] = dst ? dst[static_cast<int64_t>(w) * count + i0 + i] : nullptr;
+            for (int w = 0; w < workers; ++w) {
+                p.src[i * workers + w] = src[static_cast<int64_t>(w) * count + i0 + i];
+                p.dst[i * workers + w] = dst ? dst[static_cast<int64_t>(w) * count + i0 + i] : nullptr;
             }
         }
         p.first[p.count] = p.tiles;
     };
+    const auto tensors = [&](int32_t workers) { return small ? std::max(count, 1) : tensors_per_launch(workers, kLargePointers, kLargeTensors); };
     for (int32_t l = 0; l < p.launches; ++l) {
-        fill(l);
+        fill(l, norms, tensors(norms));
+        // every launch writes all its sums: a CTA without a tile 0
         if (int rc = launch_early("grad_norm_kernel", grad_norm_kernel<Params>, dim3(static_cast<unsigned>(p.sums), static_cast<unsigned>(norms)),
                                   kThreads, 0, 1, stream, p))
             return rc;
     }
     if (!scale)
         return launch_early("grad_norm_final_kernel", grad_norm_final_kernel<Params>, dim3(static_cast<unsigned>(norms)), kThreads, 0, 1, stream, p);
-    for (int32_t l = p.launches - 1; l >= 0; --l) {
-        fill(l);
-        const int64_t blocks = std::max(std::min(p.tiles, int64_t{std::max(1, resident / P)}), int64_t{1});
+    for (int32_t l = (small ? 1 : launches_for(P, count)) - 1; l >= 0; --l) {
+        fill(l, P, tensors(P));
+        const int64_t blocks = std::max(std::min(p.tiles, int64_t{std::max(1, sm_count() * kCtas / P)}), int64_t{1});
         if (int rc = launch_early("grad_scale_kernel", grad_scale_kernel<Params>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(P)),
                                   kThreads, 0, 1, stream, p))
             return rc;
@@ -324,8 +334,8 @@ int start(const void *const *src, void *const *dst, int32_t P, const int64_t *nu
     double *partial = static_cast<double *>(d_workspace);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     if (is_small(P, count))
-        return run<ClipSmall>(src, dst, P, numel, dtype, count, norms, max_norm, norm, partial, std::max(count, 1), scale, stream);
-    return run<ClipLarge>(src, dst, P, numel, dtype, count, norms, max_norm, norm, partial, tensors_per_launch(P, 1536, 320), scale, stream);
+        return run<ClipSmall>(src, dst, P, numel, dtype, count, norms, max_norm, norm, partial, true, scale, stream);
+    return run<ClipLarge>(src, dst, P, numel, dtype, count, norms, max_norm, norm, partial, false, scale, stream);
 }
 
 }  // namespace

@@ -527,7 +527,9 @@ struct WeightParams {
     int32_t wide;  // dz's rows start on 16 bytes
 };
 
-// L lanes to a token (L >= k, a power of two), a choice to each.
+// L lanes to a token (L >= k, a power of two), a choice to each.  Bound by the 32-byte
+// sectors of the logits, one for each choice: four tokens of a lane under way at one
+// time are no faster.
 template <typename T, int L>
 __global__ void __launch_bounds__(kThreads) expert_weights_kernel(const __grid_constant__ WeightParams p) {
     let_next_begin();
@@ -540,10 +542,10 @@ __global__ void __launch_bounds__(kThreads) expert_weights_kernel(const __grid_c
     const bool on = c >= 0 && c < p.experts;
     const float z = on ? load_f32(static_cast<const T *>(p.z[w]) + t * p.ldz + c) : -INFINITY;
     float top = z;
-    bool nan = z != z;  // the maximum passes over a NaN
+    const bool nan = z != z;  // the maximum passes over a NaN
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-    float e = top == -INFINITY && !nan ? 0.0f : expf(z - top);
+    const float e = top == -INFINITY && !nan ? 0.0f : expf(z - top);
     float sum = e;
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
@@ -557,6 +559,17 @@ __global__ void __launch_bounds__(kThreads) expert_weights_grad_kernel(const __g
     const int lane = threadIdx.x & 31, j = lane & (L - 1);
     const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * (32 / L);
     const int64_t at = first + lane / L;
+    // zeros first: they wait for nothing that is read
+    if (!p.accumulate) {
+        for (int i = 0; i < 32 / L; ++i) {
+            if (first + i >= p.items) break;
+            T *dz = static_cast<T *>(p.dz[(first + i) / p.tokens]) + (first + i) % p.tokens * p.ldz;
+            constexpr int V = 16 / sizeof(T);
+            const int whole = p.wide ? p.experts / V * V : 0;
+            for (int e = lane * V; e < whole; e += 32 * V) *reinterpret_cast<uint4 *>(dz + e) = make_uint4(0, 0, 0, 0);
+            for (int e = whole + lane; e < p.experts; e += 32) store_f32(dz + e, 0.0f);
+        }
+    }
     const bool mine = at < p.items && j < p.k;
     const int64_t w = mine ? at / p.tokens : 0, t = mine ? at % p.tokens : 0;
     const int c0 = mine ? p.choice[w][t * p.k + j] : -1;
@@ -578,17 +591,7 @@ __global__ void __launch_bounds__(kThreads) expert_weights_grad_kernel(const __g
             if (i < j) leads = false;
         }
     }
-    if (!p.accumulate) {
-        for (int i = 0; i < 32 / L; ++i) {
-            if (first + i >= p.items) break;
-            T *dz = static_cast<T *>(p.dz[(first + i) / p.tokens]) + (first + i) % p.tokens * p.ldz;
-            constexpr int V = 16 / sizeof(T);
-            const int whole = p.wide ? p.experts / V * V : 0;
-            for (int e = lane * V; e < whole; e += 32 * V) *reinterpret_cast<uint4 *>(dz + e) = make_uint4(0, 0, 0, 0);
-            for (int e = whole + lane; e < p.experts; e += 32) store_f32(dz + e, 0.0f);
-        }
-        __syncwarp();
-    }
+    if (!p.accumulate) __syncwarp();
     if (leads) {
         T *dz = static_cast<T *>(p.dz[w]) + t * p.ldz + c;
         store_f32(dz, p.accumulate ? load_f32(dz) + sum : sum);
