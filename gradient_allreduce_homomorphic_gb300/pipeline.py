@@ -15,6 +15,8 @@ The step runs every row of the path through the library's entry points:
      its sums taken inside step 3 (one more read of the exact   gar_nmse_combine
      average), then combined (nmse="separate": one pass over    (gar_nmse)
      both averages at the end)
+  5. with max_norm: both averages clipped to it, each by its    gar_grad_clip
+     own norm over all tensors, in place
 
 Overlap ([R] "8. Compute-Communication Overlapping & Gradient Bucketing"):
 fusion buffers are the buckets.  The ring runs on one stream, bucket after
@@ -33,10 +35,10 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (GAR_AVG, gar_fused_allreduce_range, gar_fusion_plan, gar_nmse, gar_nmse_combine,
-               gar_nmse_workspace_bytes, gar_thc_allreduce_fused_plan, gar_thc_allreduce_fused_plan_nmse,
+from . import (GAR_AVG, gar_fused_allreduce_range, gar_fusion_plan, gar_grad_clip, gar_grad_workspace_bytes, gar_nmse,
+               gar_nmse_combine, gar_nmse_workspace_bytes, gar_thc_allreduce_fused_plan, gar_thc_allreduce_fused_plan_nmse,
                gar_thc_plan_nmse_workspace_bytes, gar_thc_words, fused_pointer_tables, pointer_table,
-               thc_plan_tables)
+               grad_tables, thc_plan_tables)
 
 STAGES = ("ring", "thc", "nmse")
 
@@ -59,10 +61,13 @@ class AveragingStep:
     worker's copy) and ``thc_flat`` (the compressed average); their padding
     stays zero, so an NMSE over the flat buffers equals the NMSE over the
     tensors.  ``packed[w][b]`` holds worker w's wire vector of fusion buffer
-    b, ``mM[b]`` that buffer's range, ``nmse`` the step's NMSE."""
+    b, ``mM[b]`` that buffer's range, ``nmse`` the step's NMSE (of the averages
+    before they are clipped).  With max_norm the averages are scaled by min(1,
+    max_norm / norm): ``norm`` holds the exact one's norm, ``thc_norm`` the
+    compressed one's (left as they are where it is not finite)."""
 
     def __init__(self, grads, sizes, offsets=None, *, b: int = 4, capacity_bytes: int = 64 << 20,
-                 align_bytes: int = 16, nmse: str = "fused"):
+                 align_bytes: int = 16, nmse: str = "fused", max_norm=None):
         import torch
 
         if nmse not in ("separate", "fused"):
@@ -113,6 +118,13 @@ class AveragingStep:
                 "ref": pointer_table(self.ring[0][rows]),  # NMSE reference: the exact (ring) average
                 "ev": torch.cuda.Event(),
             })
+        self.max_norm = None if max_norm is None else float(max_norm)
+        if max_norm is not None:
+            if not self.max_norm >= 0:
+                raise ValueError(f"max_norm must be 0 or more, not {max_norm!r}")
+            self.norm, self.thc_norm = torch.zeros(1, device=dev), torch.zeros(1, device=dev)
+            self.clip = grad_tables(self.ring), grad_tables([self.thc])
+            self.ws_clip = torch.empty(max(gar_grad_workspace_bytes(t) for t in self.clip), dtype=torch.uint8, device=dev)
         self.stream_ring = torch.cuda.Stream(device=dev)
         self.stream_thc = torch.cuda.Stream(device=dev)
         self._host = None
@@ -141,6 +153,11 @@ class AveragingStep:
             gar_nmse_combine(self.pairs, self.nmse, stream=stream)
         else:
             gar_nmse(self.ring_flat[0], self.thc_flat, self.nmse, self.ws_nmse, stream=stream)
+
+    def _clip(self, stream):
+        if self.max_norm is not None:
+            for tables, norm in zip(self.clip, (self.norm, self.thc_norm)):
+                gar_grad_clip(tables, self.max_norm, norm, self.ws_clip, shared=True, stream=stream)
 
     def algorithmic_bytes(self):
         """HBM bytes each stage must move per step (the roofline's numerator)."""
@@ -193,6 +210,7 @@ class AveragingStep:
         mark("nmse", 0, main)
         self._nmse(main)
         mark("nmse", 1, main)
+        self._clip(main)
 
     # ------------------------------------------------------ from the host
     def setup_host(self, n_h2d: int = 2):
@@ -240,6 +258,8 @@ class AveragingStep:
         h = self._host
         if h is None:
             raise RuntimeError("call setup_host() first")
+        if self.max_norm is not None:
+            raise RuntimeError("clipping needs the norm of all buckets, and a bucket's averages leave for the host before it is known")
         main = torch.cuda.current_stream(self.device)
         plan = gar_fusion_plan(self.sizes, self.dtype, self.capacity, self.align)
         n_in = len(h["h2d"])
