@@ -43,7 +43,7 @@ constexpr int kStages = 6;
 constexpr int kOperand = 128 * kK * 2;  // bytes of one operand of a stage, of each CTA
 constexpr int kStage = 2 * kOperand;
 constexpr int kThreads = 320;  // warp 0 loads, warp 1 issues products, warps 2-9 epilogue
-constexpr int kStaging = 8 * 4096;  // two tiles of 32 x 32 bf16 for each epilogue warp
+constexpr int kStaging = 8 * 4096;  // for each epilogue warp two tiles of 32 x 32 bf16, or one of fp32
 constexpr int kSmem = 1024 + kStages * kStage + kStaging;
 // Chunks that an accumulator adds at most for an fp32 result: the tensor core's additions round toward zero, so a sum's
 // error grows with its length (8e-7 of the result at 8192 k).
@@ -53,8 +53,8 @@ enum { kLoss, kGradient, kWeights, kInputs };
 
 struct VocabParams {
     int64_t items;       // whole tiles or runs, handed out in order
-    int64_t tiles_m;     // tiles along the lanes: rows of x (logits), hidden (dw, dx)
-    int64_t tiles_n;     // along the columns: vocabulary (logits, dw), rows of x (dx)
+    int64_t tiles_m;     // tiles along the lanes: rows of x (logits), vocabulary (dw), hidden (dx)
+    int64_t tiles_n;     // along the columns: vocabulary (logits), hidden (dw), rows of x (dx)
     int32_t tile_n;      // columns of a tile, a multiple of 32
     int32_t runs;        // a run: consecutive column tiles of one item
     int32_t chunks;      // of 64 k, of one part of g
@@ -73,6 +73,7 @@ struct VocabParams {
     float *part;         // dx: sums over parts of k, [splits][rest] tiles of 256 x 256
     int64_t ld_out, ld_addend;
     int32_t last;        // dx: of the last piece
+    int32_t by_tma;      // dw: its tiles are stored by TMA
     unsigned int *status;
 };
 
@@ -220,6 +221,33 @@ __device__ __forceinline__ void stage_row(uint32_t tile, int lane, const uint32_
                      : "memory");
 }
 
+// The same of 32 fp32 values, in the order of the 128-byte swizzle.
+__device__ __forceinline__ uint32_t staged(uint32_t tile, int row, int quad) { return tile + row * 128 + ((quad ^ (row & 7)) << 4); }
+__device__ __forceinline__ void stage_row(uint32_t tile, int lane, const float (&v)[32]) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(staged(tile, lane, q)), "f"(v[4 * q]), "f"(v[4 * q + 1]),
+                     "f"(v[4 * q + 2]), "f"(v[4 * q + 3])
+                     : "memory");
+}
+// A staged tile's rows one after another, a column to each lane: what TMA does not
+// store (rows that do not start on 16 bytes, an addend, a sum's later parts).
+template <typename T>
+__device__ __forceinline__ void store_rows(uint32_t tile, int lane, T *d, int64_t ld, const T *c, int64_t ldc, int rows, bool on) {
+#pragma unroll 1
+    for (int i0 = 0; i0 < rows; i0 += 16) {
+        float x[16];  // all under way before the first store
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = c && on && i0 + i < rows ? load_f32(c + (i0 + i) * ldc + lane) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(staged(tile, i0 + i, lane >> 2) + (lane & 3) * 4) : "memory");
+            if (on && i0 + i < rows) store_f32(d + (i0 + i) * ld + lane, c ? v + x[i] : v);
+        }
+    }
+}
+
 template <int kMode, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -238,8 +266,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                    done = drained + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_cta_rank();
-    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1, items = p.items + static_cast<int64_t>(p.rest) * p.splits;
-    const int tile_n = kMnB ? kTile : p.tile_n;
+    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int64_t items = p.items + static_cast<int64_t>(p.rest) * p.splits;
+    const int tile_n = p.tile_n;
 
     let_next_begin();
     if (threadIdx.x == 0) {
@@ -277,11 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t dst = base + s * kStage, bar = lead_full + 8 * s;
                     const bool second = kMode == kWeights && c >= p.chunks;
                     const int32_t k = (second ? c - p.chunks : c) * kK;
-                    const CUtensorMap *of_b = second ? &map_c : &map_b;
                     if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * kOperand + 2 * 64 * tile_n);
                     if (kMode == kWeights) {  // the library's own copies: their rows are whole columns of 128 bytes
-                        tma_load_columns_pair(dst, &map_a, bar, a >> 6, k);
-                        tma_load_columns_pair(dst + kOperand, of_b, bar, b >> 6, k);
+                        tma_load_columns_pair(dst, second ? &map_c : &map_a, bar, a >> 6, k);
+                        tma_load_columns_pair(dst + kOperand, &map_b, bar, b >> 6, k);
                     } else {
                         if (kMnA) {
                             tma_load_2d_pair(dst, &map_a, bar, a, k);
@@ -289,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             tma_load_2d_pair(dst, &map_a, bar, k, a);
                         }
-                        tma_load_2d_pair(dst + kOperand, of_b, bar, k, b);
+                        tma_load_2d_pair(dst + kOperand, &map_b, bar, k, b);
                     }
                     issued = issued < kStages ? issued + 1 : kStages;
                     if (++s == kStages) s = 0, turn ^= 1;
@@ -397,10 +425,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             turn ^= 1;
                         } else if (kMode == kWeights) {
-                            if (const int64_t left = p.cols - col; lane_at < p.hidden && left > 0) {
-                                T *d = static_cast<T *>(p.out) + col * p.ld_out + lane_at;
-                                const T *c = c0 > it.c0 ? d : p.addend ? static_cast<const T *>(p.addend) + col * p.ld_addend + lane_at : nullptr;
-                                store_columns(v, d, p.ld_out, c, c0 > it.c0 ? p.ld_out : p.ld_addend, left < 32 ? static_cast<int>(left) : 32);
+                            const int64_t row0 = lane_at - lane, left = p.cols - row0;
+                            if (left <= 0 || col >= p.hidden) continue;  // all lanes
+                            const uint32_t tile = staging + (kTwoParts ? 0 : turn * 2048);
+                            if (p.by_tma && c1 - c0 == it.c1 - it.c0) {
+                                if (lane == 0) tma_store_wait_read<kTwoParts ? 0 : 1>();
+                                __syncwarp();
+                                if constexpr (kTwoParts) {
+                                    stage_row(tile, lane, v);
+                                } else {
+                                    uint32_t w[16];
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+                                    stage_row(tile, lane, w);
+                                }
+                                fence_async_shared();
+                                __syncwarp();
+                                if (lane == 0) {
+                                    tma_store_2d(&map_d, tile, static_cast<int32_t>(col), static_cast<int32_t>(row0));
+                                    tma_store_commit();
+                                }
+                                turn ^= 1;
+                            } else {
+                                stage_row(staging, lane, v);
+                                __syncwarp();
+                                T *d = static_cast<T *>(p.out) + row0 * p.ld_out + col;
+                                const T *c = c0 > it.c0 ? d : p.addend ? static_cast<const T *>(p.addend) + row0 * p.ld_addend + col : nullptr;
+                                store_rows(staging, lane, d, p.ld_out, c, c0 > it.c0 ? p.ld_out : p.ld_addend, left < 32 ? static_cast<int>(left) : 32,
+                                           col + lane < p.hidden);
                             }
                         } else if (const int64_t left = p.rows - col; lane_at < p.hidden && left > 0) {
                             const int count = left < 32 ? static_cast<int>(left) : 32;
@@ -421,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kMode == kLoss && lane_at < p.rows)
                 p.stats[(lane_at * p.runs + it.run) * 2 + half] = make_float2(r.top * kLog2e, r.sum);
         }
-        if (kMode == kGradient && lane == 0) tma_store_wait();
+        if ((kMode == kGradient || kMode == kWeights) && lane == 0) tma_store_wait();
     }
     __syncwarp();
     tc_fence_before();
@@ -556,8 +608,8 @@ int launch(const VocabParams &p, const CUtensorMap &a, const CUtensorMap &b, con
 int encode(CUtensorMap *map, const void *base, int64_t inner, int64_t outer, int64_t ld, int box_outer) {
     return encode_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, ld * 2, kK, box_outer);
 }
-int encode_columns(CUtensorMap *map, const void *base, int64_t inner, int64_t outer) {
-    return encode_column_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, inner, outer, inner * 2, 2, kK);
+int encode_columns(CUtensorMap *map, const void *base, int64_t inner, int64_t outer, int columns) {
+    return encode_column_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, inner, outer, inner * 2, columns, kK);
 }
 int encode_store(CUtensorMap *map, const void *base, int64_t inner, int64_t outer) {
     return encode_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, inner * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
@@ -689,16 +741,17 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
     const int64_t tiles_t = ceil_div(rows, int64_t{kTile}), tiles_h = ceil_div(hidden, int64_t{kTile});
     CUtensorMap rows_k{}, live_mn{}, g_mn{}, low_mn{}, g_to{}, low_to{};
     const bool copied = dw || copy_pays(x, ldx, p);
+    const int weights_n = hidden <= 128 ? 128 : kTile;  // columns of dw's tiles
     if (copied)
         if (int rc = copy_live_rows(p, x, ldx, live, stream)) return rc;
     if (int rc = encode(&rows_k, copied ? live : x, hidden, rows, copied ? ld_live : ldx, 128)) return rc;
     if (dw) {
-        if (int rc = encode_columns(&live_mn, live, ld_live, rows)) return rc;
+        if (int rc = encode_columns(&live_mn, live, ld_live, rows, weights_n / 128)) return rc;
     }
-    if (int rc = encode_columns(&g_mn, g, how.piece, rows)) return rc;
+    if (int rc = encode_columns(&g_mn, g, how.piece, rows, 2)) return rc;
     if (int rc = encode_store(&g_to, g, how.piece, rows)) return rc;
     if (kParts == 2) {
-        if (int rc = encode_columns(&low_mn, g_low, how.piece, rows)) return rc;
+        if (int rc = encode_columns(&low_mn, g_low, how.piece, rows, 2)) return rc;
         if (int rc = encode_store(&low_to, g_low, how.piece, rows)) return rc;
     } else {
         low_mn = g_mn, low_to = g_to;
@@ -718,13 +771,21 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
             if (int rc = launch<kGradient, T>(q, rows_k, w_k, g_to, low_to, stream)) return rc;
         }
         if (dw) {
-            q.tile_n = kTile;
-            q.tiles_m = tiles_h, q.tiles_n = ceil_div(cols, int64_t{kTile}), q.runs = static_cast<int32_t>(q.tiles_n), q.parts = kParts;
-            q.chunks = static_cast<int32_t>(ceil_div(rows, int64_t{kK}));
+            CUtensorMap to{};
+            q.tile_n = weights_n;
+            q.tiles_m = ceil_div(cols, int64_t{kTile}), q.tiles_n = ceil_div(hidden, int64_t{weights_n}), q.runs = static_cast<int32_t>(q.tiles_n);
+            q.chunks = static_cast<int32_t>(ceil_div(rows, int64_t{kK})), q.parts = kParts;
             q.items = q.tiles_m * q.runs;
             q.out = dw + first * lddw, q.ld_out = lddw;
             q.addend = addend ? addend + first * ld_addend : nullptr, q.ld_addend = ld_addend;
-            if (int rc = launch<kWeights, T>(q, live_mn, g_mn, low_mn, low_mn, stream)) return rc;
+            q.by_tma = !addend && aligned(q.out, 16) && lddw * sizeof(T) % 16 == 0;
+            if (q.by_tma) {
+                if (int rc = encode_tile_map(&to, kParts == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q.out, hidden,
+                                             cols, lddw * static_cast<int64_t>(sizeof(T)), 32, 32,
+                                             kParts == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+                    return rc;
+            }
+            if (int rc = launch<kWeights, T>(q, g_mn, live_mn, low_mn, to, stream)) return rc;
         }
         if (dx) {
             CUtensorMap w_mn{}, g_k{};
