@@ -272,6 +272,8 @@ class PtrTable:
         self.numel = first.numel() if first is not None else 0
         self.first = first
         self.checked = {}  # (shape, dtype) that every tensor was found to have -> their stride
+        self.last = None   # (P, shape, dtype) asked of them last, and what _workers said
+        self.size = tuple(first.shape) if first is not None and first.dim() == 2 else None
 
     def __len__(self):
         return len(self.tensors)
@@ -826,6 +828,8 @@ def _workers(given, name, P, shape, dtype):
     and type and all of one row stride.  A PtrTable's tensors are looked at once
     for each shape and type asked of them."""
     table = isinstance(given, PtrTable)
+    if table and given.last is not None and given.last[0] == (P, shape, dtype):
+        return given.last[1]
     tensors = given.tensors if table else given
     if len(tensors) != P:
         raise GarError(GAR_EINVAL, f"{name} has {len(tensors)} tensors, not {P}")
@@ -842,7 +846,10 @@ def _workers(given, name, P, shape, dtype):
             given.checked[shape, dtype] = stride
     if stride[-1] != 1 and shape[-1] > 1 and shape[0] > 0:
         raise GarError(GAR_EINVAL, f"{name}: the elements of a row are not contiguous")
-    return given.array if table else struct.pack(f"{P}Q", *ptrs), stride[0] if shape[0] > 1 else max(shape[-1], 1)
+    found = given.array if table else struct.pack(f"{P}Q", *ptrs), stride[0] if shape[0] > 1 else max(shape[-1], 1)
+    if table:
+        given.last = (P, shape, dtype), found
+    return found
 
 
 def gar_balance_loss(z, k: int, alpha: float, choice, counts, loss, workspace, dz=None, valid=None, stream=None):
@@ -937,10 +944,15 @@ def gar_expert_workspace_bytes(P: int, tokens: int, k: int, experts: int) -> int
 
 def _first(given, name):
     """The first worker's tensor, of two dimensions."""
-    t = given.first if isinstance(given, PtrTable) else given[0] if len(given) else None
+    if isinstance(given, PtrTable):
+        if given.size is not None:
+            return given.first, *given.size
+        t = given.first
+    else:
+        t = given[0] if len(given) else None
     if t is None:
         raise GarError(GAR_EINVAL, f"{name} has no worker's tensor")
-    return t, *_two_dims(t, f"{name}[0]")
+    return t, *_two_dims(t, name)
 
 
 def _per_choice(given, name, P, tokens, k, dtype):
@@ -1046,6 +1058,10 @@ class GradTables:
         first = self.src.tensors[:self.count]
         self.dtype = np.array([_dtype_code(t) for t in first], np.int32)
         self.numel = np.array([t.numel() for t in first], np.int64)
+        self.host = self.numel.ctypes.data, self.dtype.ctypes.data
+        places = [t.data_ptr() for t in self.dst.tensors if t.numel()]
+        if len(set(places)) < len(places):
+            raise GarError(GAR_EINVAL, "the same tensor stands twice in the lists: it would be scaled twice")
         for name, table in (("grads", self.src), ("out", self.dst)):
             for i, t in enumerate(table.tensors):
                 like = first[i % self.count]
@@ -1073,7 +1089,7 @@ def gar_grad_norm(grads, norm, workspace, stream=None):
     """norm[w] = the 2-norm of worker w's gradient tensors grads[w][i] (lists, or
     grad_tables), [P] fp32."""
     t = grad_tables(grads)
-    _call("gar_grad_norm", t.src.array, t.P, t.numel.ctypes.data, t.dtype.ctypes.data, t.count,
+    _call("gar_grad_norm", t.src.array, t.P, *t.host, t.count,
           _vector(norm, "norm", _float32(), t.P), _dev(workspace), workspace.numel() * workspace.element_size(),
           _stream(stream))
 
@@ -1083,7 +1099,7 @@ def gar_grad_clip(grads, max_norm: float, norm, workspace, out=None, shared: boo
     out[w][i]; shared: by the norm of the first worker's, norm [1].  A norm that is
     not finite leaves them as they are."""
     t = grad_tables(grads, out)
-    _call("gar_grad_clip", t.src.array, t.dst.array, t.P, t.numel.ctypes.data, t.dtype.ctypes.data, t.count,
+    _call("gar_grad_clip", t.src.array, t.dst.array, t.P, *t.host, t.count,
           1 if shared else 0, max_norm, _vector(norm, "norm", _float32(), 1 if shared else t.P), _dev(workspace),
           workspace.numel() * workspace.element_size(), _stream(stream))
 

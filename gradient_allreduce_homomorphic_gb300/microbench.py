@@ -20,7 +20,10 @@ the fused ones as training.TrainingStep runs them, the workers' chains over
 --streams side streams), and the operators that a worker's gradients come from: fp8_quantize (--rows x --cols values,
 both orders), fp8_matmul (--rows x --cols, summed over --depth; --addend: added to another matrix), distill and distill_split (--rows of --cols logits,
 --k teacher entries: loss and gradient in one call or two), balance (--P workers of --rows tokens and --cols experts,
---k choices).  Inputs are seeded N(0, 1) draws made on the device;
+--k choices), vocab and vocab_grad (the cross entropy of --rows over --cols vocabulary entries, --depth hidden, bf16; its
+gradient with dw of --dtype, --addend), expert_sort, expert_gather, expert_combine, expert_combine_grad, expert_weights
+and expert_weights_grad (--P workers of --rows tokens, --cols experts, --k choices, --depth hidden), grad_norm and grad_clip
+(--P workers' --N values as 300 tensors, out of place).  Inputs are seeded N(0, 1) draws made on the device;
 every size is chosen by the caller, so a case can be kept small enough for a
 profiler capture.  Prints one JSON line: time per call (CUDA events on the
 launching stream, after warm-up) and algorithmic GB/s.
@@ -55,11 +58,11 @@ def main(argv=None):
     ap.add_argument("--dtype", default="f32")
     ap.add_argument("--g", type=int, default=0, help="granularity for the nuhc cases")
     ap.add_argument("--k", type=int, default=64,
-                    help="partitions of the stream cases, teacher entries of distill, choices of balance")
+                    help="partitions of the stream cases, teacher entries of distill, choices of balance and the experts")
     ap.add_argument("--rows", type=int, default=4096)
     ap.add_argument("--cols", type=int, default=8192)
-    ap.add_argument("--depth", type=int, default=2048, help="fp8_matmul: the summed axis")
-    ap.add_argument("--addend", action="store_true", help="fp8_matmul: add the product to a matrix of its size")
+    ap.add_argument("--depth", type=int, default=2048, help="fp8_matmul: the summed axis; vocab, experts: the hidden size")
+    ap.add_argument("--addend", action="store_true", help="fp8_matmul, vocab_grad: add the product to a matrix of its size")
     ap.add_argument("--streams", type=int, default=2,
                     help="train_step_fused: side streams the workers' chains go round-robin over")
     ap.add_argument("--flush", action="store_true",
@@ -335,6 +338,74 @@ def main(argv=None):
                     g.gar_distill_loss(z, index, teacher, 1.0, loss, lse)
                     g.gar_distill_grad(z, index, teacher, 1.0, lse, dz)
             nbytes = rows * cols * size * (2 if a.case == "distill" else 3)
+    elif a.case in ("vocab", "vocab_grad"):
+        # algorithmic bytes: x and w read, dx and dw written; the gradient's flops as it computes them (the logits
+        # again, and an fp32 dw from two parts)
+        rows, cols, H = a.rows, a.cols, a.depth
+        x = torch.randn((rows, H), device=dev).bfloat16()
+        w = (torch.randn((cols, H), device=dev) * 2 / H ** 0.5).bfloat16()
+        target = torch.randint(0, cols, (rows,), dtype=torch.int32, device=dev)
+        loss, lse = torch.empty(rows, device=dev), torch.empty(rows, device=dev)
+        dx, dw = torch.empty_like(x), torch.empty((cols, H), dtype=tdt, device=dev)
+        add = torch.randn((cols, H), device=dev).to(tdt) if a.addend else None
+        ws = torch.empty(g.gar_vocab_workspace_bytes(rows, cols, H, tdt), dtype=torch.uint8, device=dev)
+        g.gar_vocab_loss(x, w, target, loss, lse, ws)
+        if a.case == "vocab":
+            fn = lambda: g.gar_vocab_loss(x, w, target, loss, lse, ws)  # noqa: E731
+            nbytes, flops = (rows + cols) * H * 2, 2 * rows * cols * H
+        else:
+            fn = lambda: g.gar_vocab_grad(x, w, target, lse, dx, dw, ws, addend=add)  # noqa: E731
+            nbytes = (rows + cols) * H * 2 + rows * H * 2 + cols * H * es * (2 if a.addend else 1)
+            flops = (6 if es == 2 else 8) * rows * cols * H
+    elif a.case in ("expert_sort", "expert_gather", "expert_combine", "expert_combine_grad", "expert_weights",
+                    "expert_weights_grad"):
+        # P workers of --rows tokens, --cols experts, --k choices, --depth hidden; algorithmic bytes: each token's row
+        # and each of its experts' rows once
+        T, E, k, H = a.rows, a.cols, a.k, a.depth
+        choice = [torch.rand((T, E), device=dev).topk(k, dim=1).indices.int() for _ in range(P)]
+        rows = g.gar_expert_rows(P, T, k, E)
+        position = [torch.empty((T, k), dtype=torch.int32, device=dev) for _ in range(P)]
+        source, offsets = (torch.empty(n, dtype=torch.int32, device=dev) for n in (rows, E + 1))
+        ws = torch.empty(g.gar_expert_workspace_bytes(P, T, k, E), dtype=torch.uint8, device=dev)
+        choice, position = g.pointer_table(choice), g.pointer_table(position)
+        per_choice = lambda: g.pointer_table([torch.rand((T, k), device=dev) for _ in range(P)])  # noqa: E731
+        weight, dweight = per_choice(), per_choice()
+        g.gar_expert_sort(choice, E, position, source, offsets, ws)
+        if a.case == "expert_sort":
+            fn = lambda: g.gar_expert_sort(choice, E, position, source, offsets, ws)  # noqa: E731
+            nbytes = 12 * rows
+        elif a.case.startswith("expert_weights"):
+            z = g.pointer_table([torch.randn((T, E), device=dev).to(tdt) for _ in range(P)])
+            if a.case == "expert_weights":
+                fn = lambda: g.gar_expert_weights(z, choice, weight)  # noqa: E731
+                nbytes = rows * (8 + 32)  # a sector of each chosen logit
+            else:
+                fn = lambda: g.gar_expert_weights_grad(weight, dweight, choice, z)  # noqa: E731
+                nbytes = rows * 12 + P * T * E * es
+        else:
+            x = g.pointer_table([torch.randn((T, H), device=dev).to(tdt) for _ in range(P)])
+            out = g.pointer_table([torch.empty((T, H), device=dev, dtype=tdt) for _ in range(P)])
+            y, dy = (torch.randn((rows, H), device=dev).to(tdt) for _ in range(2))
+            if a.case == "expert_gather":
+                fn = lambda: g.gar_expert_gather(x, position, source, y)  # noqa: E731
+            elif a.case == "expert_combine":
+                fn = lambda: g.gar_expert_combine(y, position, out, weight=weight)  # noqa: E731
+            else:
+                fn = lambda: g.gar_expert_combine_grad(x, y, position, source, weight, dy, dweight)  # noqa: E731
+            nbytes = (P * T + rows * (2 if a.case == "expert_combine_grad" else 1)) * H * es
+    elif a.case in ("grad_norm", "grad_clip"):
+        # P workers' N values as 300 tensors, out of place; algorithmic bytes: one read, and one write
+        cuts = np.linspace(0, N, 301).astype(np.int64) // 8 * 8
+        src, dst = bufs(N, P, tdt), bufs(N, P, tdt, seed=500)
+        views = [[[t[int(p):int(q)] for p, q in zip(cuts, cuts[1:])] for t in ts] for ts in (src, dst)]
+        tables = g.grad_tables(*views)
+        norm = torch.empty(P, device=dev)
+        ws = torch.empty(g.gar_grad_workspace_bytes(tables), dtype=torch.uint8, device=dev)
+        if a.case == "grad_norm":
+            fn = lambda: g.gar_grad_norm(tables, norm, ws)  # noqa: E731
+        else:
+            fn = lambda: g.gar_grad_clip(tables, 1e-3, norm, ws)  # noqa: E731
+        nbytes = P * N * es * (1 if a.case == "grad_norm" else 2)
     else:
         raise SystemExit(f"unknown case {a.case}")
 

@@ -17,7 +17,10 @@
  *                         they are averaged: block-scaled 8-bit quantization
  *                         and products on the tensor cores, distillation from
  *                         a teacher's top logits, a router's choices and
- *                         balance loss over all workers.
+ *                         balance loss over all workers, tokens sorted by
+ *                         expert and back, a vocabulary layer's cross entropy
+ *                         without its logits; and what follows the average:
+ *                         the global norm and clipping.
  *
  * Sources (cited by page title and section):
  *   [H] "Horovod: Fast and Easy Distributed Deep Learning in TensorFlow"
@@ -85,7 +88,7 @@ typedef enum { GAR_F8E4M3 = 0, GAR_F8E5M2 = 1 } gar_f8_format;
 
 /* Bits of the device status word (gar_sync_status). */
 typedef enum {
-    GAR_STATUS_NONFINITE = 1, /* a THC range pass saw a NaN or an infinite input */
+    GAR_STATUS_NONFINITE = 1, /* a THC range pass saw a NaN or an infinite input, or clipping a norm that is not finite */
     GAR_STATUS_TIMEOUT = 2    /* a wait inside a kernel ran out (gar_sync_status): that call's result is not valid */
 } gar_device_status;
 typedef enum { GAR_SUM = 0, GAR_AVG = 1 } gar_op;
@@ -836,8 +839,8 @@ int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t ldw, int32
  *                lddw, or NULL
  *   addend       device, of dw's type, added before the rounding; NULL: none; may
  *                be dw (same row stride)
- * Outputs must not overlap x, w or one another.  With no rows dw is the addend or
- * 0.  Other arguments and errors as for gar_vocab_loss. */
+ * A row that did not count when lse was written must not count now.  Outputs must
+ * not overlap x, w or one another.  With no rows dw is the addend or 0.  Other arguments and errors as for gar_vocab_loss. */
 int gar_vocab_grad(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target,
                    const float *weight, int64_t rows, int64_t vocab, int64_t hidden, const float *lse, void *dx, int64_t lddx,
                    const void *addend, int64_t ld_addend, void *dw, int64_t lddw, int32_t dw_type, void *d_workspace,
@@ -897,7 +900,8 @@ int gar_expert_gather(const void *const *x, int32_t P, int64_t tokens, int64_t h
  *   weight       P device pointers, [tokens, k] fp32, or NULL (1)
  *   addend       P device pointers, tokens x hidden of y's type, row stride
  *                ld_addend, or NULL (0); an entry may be that of out
- *   out          P device pointers, out, tokens x hidden of y's type, row stride ldo
+ *   out          P device pointers, out, tokens x hidden of y's type, row stride ldo,
+ *                apart from y
  * Errors: GAR_EINVAL, GAR_EDTYPE, GAR_EALIGN, GAR_ECUDA. */
 int gar_expert_combine(const void *y, int64_t ldy, int64_t rows, int32_t P, int64_t tokens, int64_t hidden, int32_t dtype,
                        int32_t k, const int32_t *const *position, const float *const *weight, const void *const *addend,
@@ -964,8 +968,8 @@ int gar_grad_norm(const void *const *src, int32_t P, const int64_t *numel, const
  * max_norm, else 1 (nothing is written where dst is src).  One fp32 product a value,
  * rounded to its type.  A norm that is not finite leaves the gradients as they are
  * (dst: copies) and raises GAR_STATUS_NONFINITE.
- *   dst          host, P * count device pointers: where the clipped tensors go; each
- *                src's own or apart from all of src
+ *   dst          host, P * count device pointers: where the clipped tensors go, no
+ *                two of them overlapping; each src's own or apart from all of src
  *   shared       not 0: every worker's tensors are scaled by the norm of worker 0's
  *                (copies of one average); norm is then one fp32
  *   max_norm     0 or more; infinity: no clipping

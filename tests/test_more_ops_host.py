@@ -277,6 +277,9 @@ def test_clip_binding(gar, binding):
     assert refused(gar.grad_tables, []) == refused(gar.grad_tables, [[tensor(3)], []]) == refused(gar.grad_tables, grads, out[:1]) == E
     assert refused(gar.grad_tables, grads, [[tensor(31), out[0][1]], out[1]]) == E
     assert refused(gar.grad_tables, [[tensor(4, 4)[:, ::2]]]) == E
+    same = tensor(8)
+    assert refused(gar.grad_tables, [[same, same]]) == refused(gar.grad_tables, [[tensor(8)], [tensor(8)]], [[same], [same]]) == E
+    gar.grad_tables([[same, same]], [[tensor(8), tensor(8)]])  # read twice, written apart
     assert refused(gar.grad_tables, grads, [[tensor(30, dtype=torch.bfloat16), out[0][1]], out[1]]) == D
     assert refused(gar.grad_tables, [[tensor(3, dtype=torch.float16)]]) == D
     assert refused(gar.grad_tables, [[torch.zeros(3)]]) == E
