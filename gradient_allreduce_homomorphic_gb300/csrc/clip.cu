@@ -42,9 +42,11 @@ struct ClipParams {
     float *norm;
     unsigned int *status;
     int64_t tiles;           // of one worker
-    int64_t numel[NTENSOR];
-    int64_t first[NTENSOR + 1];  // tile
-    int32_t dtype[NTENSOR];
+    struct Tensor {
+        int64_t first;  // tile
+        int64_t numel : 62;
+        int64_t bf16 : 2;
+    } tensor[NTENSOR + 1];   // one more, for its first tile
     const void *src[NPTR];   // [tensor][worker]
     void *dst[NPTR];
 };
@@ -74,7 +76,7 @@ __device__ __forceinline__ int tensor_of(const P &p, int64_t tile) {
     int lo = 0, hi = p.count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.first[mid] <= tile) lo = mid;
+        if (p.tensor[mid].first <= tile) lo = mid;
         else hi = mid - 1;
     }
     return lo;
@@ -157,11 +159,13 @@ __device__ __forceinline__ double tile_squares(const T *x, int64_t n, int64_t i)
         unpack<T>(q[k], v + (k * V) % 16);
         if ((k + 1) * V % 16 == 0) sum += squares(v);
     }
+    const int64_t rest = r.body + vecs * V;
+    if (r.begin == r.body && rest == r.end) return sum;  // whole lines alone (fp64 is dear: no additions of nothing)
     float one[1] = {0.0f};
     if (static_cast<int64_t>(threadIdx.x) < r.body - r.begin) one[0] = load_f32(x + r.begin + threadIdx.x);
     sum += squares(one);
     one[0] = 0.0f;
-    const int64_t tail = r.body + vecs * V + threadIdx.x;
+    const int64_t tail = rest + threadIdx.x;
     if (tail < r.end) one[0] = load_f32(x + tail);
     return sum + squares(one);
 }
@@ -175,10 +179,10 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     double sum = 0.0;
     int i = tensor_of(p, blockIdx.x);
     for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x) {
-        while (p.first[i + 1] <= t) ++i;
+        while (p.tensor[i + 1].first <= t) ++i;
         const void *x = p.src[i * p.P + w];
-        sum += p.dtype[i] == GAR_F32 ? tile_squares(static_cast<const float *>(x), p.numel[i], t - p.first[i])
-                                     : tile_squares(static_cast<const uint16_t *>(x), p.numel[i], t - p.first[i]);
+        const int64_t n = p.tensor[i].numel, at = t - p.tensor[i].first;
+        sum += p.tensor[i].bf16 ? tile_squares(static_cast<const uint16_t *>(x), n, at) : tile_squares(static_cast<const float *>(x), n, at);
     }
     sum = block_sum(sum, of_warps);
     if (threadIdx.x == 0) p.partial[(static_cast<int64_t>(p.launch) * p.norms + w) * p.sums + blockIdx.x] = sum;
@@ -250,12 +254,13 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
     const float c = finite && norm > p.max_norm ? p.max_norm / norm : 1.0f;
     int i = tensor_of(p, p.tiles - 1 - blockIdx.x);
     for (int64_t t = p.tiles - 1 - blockIdx.x; t >= 0; t -= gridDim.x) {
-        while (p.first[i] > t) --i;
+        while (p.tensor[i].first > t) --i;
         const void *x = p.src[i * p.P + w];
         void *y = p.dst[i * p.P + w];
         if (c == 1.0f && x == y) continue;  // stays as it is
-        if (p.dtype[i] == GAR_F32) scale_tile(static_cast<const float *>(x), static_cast<float *>(y), p.numel[i], t - p.first[i], c);
-        else scale_tile(static_cast<const uint16_t *>(x), static_cast<uint16_t *>(y), p.numel[i], t - p.first[i], c);
+        const int64_t n = p.tensor[i].numel, at = t - p.tensor[i].first;
+        if (p.tensor[i].bf16) scale_tile(static_cast<const uint16_t *>(x), static_cast<uint16_t *>(y), n, at, c);
+        else scale_tile(static_cast<const float *>(x), static_cast<float *>(y), n, at, c);
     }
 }
 
@@ -282,15 +287,16 @@ int run(const void *const *src, void *const *dst, int32_t P, const int64_t *nume
         p.count = std::min(per_launch, count - i0);
         p.tiles = 0;
         for (int32_t i = 0; i < p.count; ++i) {
-            p.numel[i] = numel[i0 + i], p.dtype[i] = dtype[i0 + i];
-            p.first[i] = p.tiles;
+            p.tensor[i].first = p.tiles;
+            p.tensor[i].numel = numel[i0 + i];
+            p.tensor[i].bf16 = dtype[i0 + i] == GAR_BF16;
             p.tiles += ceil_div(numel[i0 + i] * elem_bytes(dtype[i0 + i]), kTileBytes);
             for (int w = 0; w < workers; ++w) {
                 p.src[i * workers + w] = src[static_cast<int64_t>(w) * count + i0 + i];
                 p.dst[i * workers + w] = dst ? dst[static_cast<int64_t>(w) * count + i0 + i] : nullptr;
             }
         }
-        p.first[p.count] = p.tiles;
+        p.tensor[p.count].first = p.tiles;
     };
     const auto tensors = [&](int32_t workers) { return small ? std::max(count, 1) : tensors_per_launch(workers, kLargePointers, kLargeTensors); };
     for (int32_t l = 0; l < p.launches; ++l) {

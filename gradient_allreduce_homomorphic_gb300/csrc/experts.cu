@@ -24,6 +24,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kEach = 8;                           // pairs of a lane under way at one time
+constexpr int kSortChunk = kSortThreads * kEach;   // pairs that a CTA holds in registers
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 32;
 constexpr int kMaxBlocks = 192;  // of the sort
@@ -36,7 +38,7 @@ struct SortParams {
     int32_t *position[GAR_MAX_WORKERS];
     int32_t per_worker;  // pairs of a worker
     int32_t pairs;       // of all
-    int32_t per_block;   // a multiple of kThreads
+    int32_t per_block;   // a multiple of kSortThreads
     int32_t experts, align, capacity;
     int64_t rows;
     int32_t *source, *offsets;
@@ -49,6 +51,15 @@ __device__ __forceinline__ int expert_of(const SortParams &p, int32_t i) {
     return e >= 0 && e < p.experts ? e : -1;
 }
 
+// kEach pairs of a lane, 32 apart.
+__device__ __forceinline__ void experts_of(const SortParams &p, int32_t from, int32_t end, int lane, int (&e)[kEach]) {
+#pragma unroll
+    for (int m = 0; m < kEach; ++m) {
+        const int32_t i = from + m * 32 + lane;
+        e[m] = i < end ? expert_of(p, i) : -1;
+    }
+}
+
 __global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const __grid_constant__ SortParams p) {
     __shared__ int32_t of[kMaxExperts];
     for (int e = threadIdx.x; e < p.experts; e += kSortThreads) of[e] = 0;
@@ -57,9 +68,13 @@ __global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const __grid
     after_previous();
     const int64_t first = static_cast<int64_t>(blockIdx.x) * p.per_block;
     const int32_t end = static_cast<int32_t>(min(first + p.per_block, static_cast<int64_t>(p.pairs)));
-    for (int32_t i = static_cast<int32_t>(first) + threadIdx.x; i < end; i += kSortThreads) {
-        const int e = expert_of(p, i);
-        if (e >= 0) atomicAdd(&of[e], 1);
+    const int32_t run = p.per_block / kSortWarps, from = static_cast<int32_t>(first) + (threadIdx.x >> 5) * run, to = min(from + run, end);
+    for (int32_t at = from; at < to; at += 32 * kEach) {
+        int e[kEach];
+        experts_of(p, at, to, threadIdx.x & 31, e);
+#pragma unroll
+        for (int m = 0; m < kEach; ++m)
+            if (e[m] >= 0) atomicAdd(&of[e[m]], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < p.experts; e += kSortThreads) p.counts[static_cast<int64_t>(blockIdx.x) * p.experts + e] = of[e];
@@ -89,9 +104,12 @@ __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const __grid
     const int32_t end = static_cast<int32_t>(min(begin + p.per_block, static_cast<int64_t>(p.pairs)));
     const int32_t run = p.per_block / kSortWarps, from = static_cast<int32_t>(begin) + warp * run;
     const int32_t to = min(from + run, end);
-    for (int32_t i = from + lane; i < to; i += 32) {
-        const int e = expert_of(p, i);
-        if (e >= 0) atomicAdd(&cursor[warp * E + e], 1);
+    int of[kEach];  // of the last 256 pairs: all of them, unless a CTA has more than a chunk
+    for (int32_t at = from; at < to; at += 32 * kEach) {
+        experts_of(p, at, to, lane, of);
+#pragma unroll
+        for (int m = 0; m < kEach; ++m)
+            if (of[m] >= 0) atomicAdd(&cursor[warp * E + of[m]], 1);
     }
     if (gridDim.x > 1) {  // counts of every CTA, an expert by kSortThreads / E threads
         const int parts = E >= kSortThreads ? 1 : kSortThreads / E;
@@ -145,26 +163,32 @@ __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const __grid
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) p.offsets[E] = used;
     __syncthreads();
-    for (int32_t i0 = from; i0 < to; i0 += 32) {
-        const int32_t i = i0 + lane;
-        const int e = i < to ? expert_of(p, i) : -1;
-        const unsigned same = __match_any_sync(kAll, e);
-        int32_t at = -1;
-        if (e >= 0) {
-            const int32_t rank = cursor[warp * E + e] + __popc(same & ((1u << lane) - 1));
-            if (p.capacity == 0 || rank < p.capacity) at = start[e] + rank;
+    for (int32_t i0 = from; i0 < to; i0 += 32 * kEach) {
+        if (run > 32 * kEach) experts_of(p, i0, to, lane, of);
+#pragma unroll
+        for (int m = 0; m < kEach; ++m) {
+            if (i0 + m * 32 >= to) break;  // all lanes
+            const int32_t i = i0 + m * 32 + lane;
+            const int e = of[m];
+            const unsigned same = __match_any_sync(kAll, e);
+            int32_t at = -1;
+            if (e >= 0) {
+                const int32_t rank = cursor[warp * E + e] + __popc(same & ((1u << lane) - 1));
+                if (p.capacity == 0 || rank < p.capacity) at = start[e] + rank;
+            }
+            __syncwarp();
+            if (e >= 0 && (same >> lane) == 1u) cursor[warp * E + e] += __popc(same);  // the last of them
+            __syncwarp();
+            if (i < to) p.position[i / p.per_worker][i % p.per_worker] = at;
+            if (at >= 0) p.source[at] = i;
         }
-        __syncwarp();
-        if (e >= 0 && (same >> lane) == 1u) cursor[warp * E + e] += __popc(same);  // the last of them
-        __syncwarp();
-        if (i < to) p.position[i / p.per_worker][i % p.per_worker] = at;
-        if (at >= 0) p.source[at] = i;
     }
-    // rows without a pair: -1 within an expert's rows, -2 behind the last expert
-    for (int e = blockIdx.x; e < E; e += gridDim.x) {
-        const int32_t n = rows_for(p, total[e]);
-        for (int32_t r = min(total[e], n) + threadIdx.x; r < n; r += kSortThreads) p.source[start[e] + r] = -1;
-    }
+    // rows without a pair: -1 within an expert's rows (a warp to each), -2 behind the last expert
+    if (p.align > 1 || p.capacity > 0)
+        for (int e = blockIdx.x * kSortWarps + warp; e < E; e += gridDim.x * kSortWarps) {
+            const int32_t end_row = e + 1 < E ? start[e + 1] : used;
+            for (int32_t r = start[e] + min(total[e], end_row - start[e]) + lane; r < end_row; r += 32) p.source[r] = -1;
+        }
     for (int64_t r = used + static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x; r < p.rows;
          r += static_cast<int64_t>(gridDim.x) * kSortThreads)
         p.source[r] = -2;
@@ -731,10 +755,9 @@ extern "C" int gar_expert_sort(const int32_t *const *choice, int32_t P, int64_t 
     p.experts = experts, p.align = align, p.capacity = capacity, p.rows = rows;
     p.source = source, p.offsets = offsets, p.counts = static_cast<int32_t *>(d_workspace);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    // one CTA, and one launch, for few pairs; 4096 pairs a CTA else, as far as the SMs go (262144 pairs of 256 experts, both
-    // launches: 2048 a CTA of 256 threads 41 us, for each CTA begins with all CTAs' counts)
+    // 4096 pairs a CTA, held in registers, as far as the SMs go; one CTA needs no launch for the counts
     const int64_t most = std::min(sm_count(), kMaxBlocks);
-    const int64_t blocks = p.pairs <= 8192 ? 1 : std::min(ceil_div(int64_t{p.pairs}, int64_t{4096}), most);
+    const int64_t blocks = std::max(std::min(ceil_div(int64_t{p.pairs}, int64_t{kSortChunk}), most), int64_t{1});
     p.per_block = static_cast<int32_t>(std::max(ceil_div(ceil_div(int64_t{p.pairs}, blocks), int64_t{kSortThreads}), int64_t{1}) * kSortThreads);
     const dim3 grid(static_cast<unsigned>(std::max(ceil_div(int64_t{p.pairs}, int64_t{p.per_block}), int64_t{1})));
     const size_t shared = static_cast<size_t>(3 + kSortWarps) * experts * sizeof(int32_t);
