@@ -60,17 +60,6 @@ __device__ __forceinline__ double warp_sum(double v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
-// The CTA's sum, in every thread.
-__device__ __forceinline__ double block_sum(double v, double *of_warps) {
-    v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0) of_warps[threadIdx.x >> 5] = v;
-    __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) s += of_warps[i];
-    return s;
-}
-
 template <typename P>
 __device__ __forceinline__ int tensor_of(const P &p, int64_t tile) {
     int lo = 0, hi = p.count - 1;
@@ -172,7 +161,7 @@ __device__ __forceinline__ double tile_squares(const T *x, int64_t n, int64_t i)
 
 template <typename P>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ P p) {
-    __shared__ double of_warps[kThreads / 32];
+    __shared__ double of_warp[kThreads / 32];
     let_next_begin();
     after_previous();
     const int w = blockIdx.y;
@@ -184,25 +173,35 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
         const int64_t n = p.tensor[i].numel, at = t - p.tensor[i].first;
         sum += p.tensor[i].bf16 ? tile_squares(static_cast<const uint16_t *>(x), n, at) : tile_squares(static_cast<const float *>(x), n, at);
     }
-    sum = block_sum(sum, of_warps);
-    if (threadIdx.x == 0) p.partial[(static_cast<int64_t>(p.launch) * p.norms + w) * p.sums + blockIdx.x] = sum;
+    sum = warp_sum(sum);
+    if ((threadIdx.x & 31) == 0) of_warp[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int k = 1; k < kThreads / 32; ++k) sum += of_warp[k];
+    p.partial[(static_cast<int64_t>(p.launch) * p.norms + w) * p.sums + blockIdx.x] = sum;
 }
 
-// Worker w's norm from all partial sums.
+// Worker w's norm from all partial sums, by one warp: fp64 in every thread of the
+// CTAs that scale took longer than the scaling of small tensors.
 template <typename P>
-__device__ __forceinline__ float norm_of(const P &p, int w, double *of_warps) {
-    double sum = 0.0;
-    for (int l = 0; l < p.launches; ++l)
-        for (int i = threadIdx.x; i < p.sums; i += kThreads) sum += p.partial[(static_cast<int64_t>(l) * p.norms + w) * p.sums + i];
-    return static_cast<float>(sqrt(block_sum(sum, of_warps)));
+__device__ __forceinline__ float norm_of(const P &p, int w) {
+    const int lane = threadIdx.x & 31;
+    double sum[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int l = 0; l < p.launches; ++l) {
+        const double *of = p.partial + (static_cast<int64_t>(l) * p.norms + w) * p.sums;
+        for (int i = lane; i < p.sums; i += 128)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + 32 * k < p.sums) sum[k] += of[i + 32 * k];
+    }
+    return static_cast<float>(sqrt(warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]))));
 }
 
 template <typename P>
-__global__ void __launch_bounds__(kThreads) grad_norm_final_kernel(const __grid_constant__ P p) {
-    __shared__ double of_warps[kThreads / 32];
+__global__ void __launch_bounds__(32) grad_norm_final_kernel(const __grid_constant__ P p) {
     let_next_begin();
     after_previous();
-    const float norm = norm_of(p, blockIdx.x, of_warps);
+    const float norm = norm_of(p, blockIdx.x);
     if (threadIdx.x == 0) p.norm[blockIdx.x] = norm;
 }
 
@@ -241,17 +240,23 @@ __device__ __forceinline__ void scale_tile(const T *x, T *y, int64_t n, int64_t 
 
 template <typename P>
 __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ P p) {
-    __shared__ double of_warps[kThreads / 32];
+    __shared__ float scale;
     let_next_begin();
     after_previous();
     const int w = blockIdx.y, of = p.norms == 1 ? 0 : w;
-    const float norm = norm_of(p, of, of_warps);
-    const bool finite = norm < INFINITY;  // false for NaN too
-    if (blockIdx.x == 0 && threadIdx.x == 0 && of == w && p.launch == 0) {
-        p.norm[w] = norm;
-        if (!finite && p.status) atomicOr(p.status, static_cast<unsigned int>(GAR_STATUS_NONFINITE));
+    if (threadIdx.x < 32) {
+        const float norm = norm_of(p, of);
+        const bool finite = norm < INFINITY;  // false for NaN too
+        if (threadIdx.x == 0) {
+            scale = finite && norm > p.max_norm ? p.max_norm / norm : 1.0f;
+            if (blockIdx.x == 0 && of == w && p.launch == 0) {
+                p.norm[w] = norm;
+                if (!finite && p.status) atomicOr(p.status, static_cast<unsigned int>(GAR_STATUS_NONFINITE));
+            }
+        }
     }
-    const float c = finite && norm > p.max_norm ? p.max_norm / norm : 1.0f;
+    __syncthreads();
+    const float c = scale;
     int i = tensor_of(p, p.tiles - 1 - blockIdx.x);
     for (int64_t t = p.tiles - 1 - blockIdx.x; t >= 0; t -= gridDim.x) {
         while (p.tensor[i].first > t) --i;
@@ -277,10 +282,14 @@ int run(const void *const *src, void *const *dst, int32_t P, const int64_t *nume
     Params p;
     p.norms = norms, p.max_norm = max_norm, p.norm = norm, p.partial = partial, p.status = device_status();
     p.launches = small ? 1 : launches_for(norms, count);
-    // as many CTAs as the SMs hold at one time, the workers' together
     int64_t tiles = 0;
     for (int32_t i = 0; i < count; ++i) tiles += ceil_div(numel[i] * elem_bytes(dtype[i]), kTileBytes);
-    p.sums = static_cast<int32_t>(std::max(std::min(tiles, int64_t{std::min(sm_count() * kCtas, kMaxSums) / norms}), int64_t{1}));
+    // a CTA to each tile while they are few, else as many as the SMs hold at one time, the workers' together
+    const auto ctas = [&](int64_t of_worker, int32_t workers, int64_t few) {
+        const int64_t held = std::max(std::min(sm_count() * kCtas, kMaxSums) / workers, 1);
+        return static_cast<int32_t>(std::max(of_worker * workers <= few ? of_worker : std::min(of_worker, held), int64_t{1}));
+    };
+    p.sums = ctas(tiles, norms, kMaxSums);
     const auto fill = [&](int32_t l, int32_t workers, int32_t per_launch) {
         p.launch = l, p.P = workers;
         const int32_t i0 = l * per_launch;
@@ -307,10 +316,10 @@ int run(const void *const *src, void *const *dst, int32_t P, const int64_t *nume
             return rc;
     }
     if (!scale)
-        return launch_early("grad_norm_final_kernel", grad_norm_final_kernel<Params>, dim3(static_cast<unsigned>(norms)), kThreads, 0, 1, stream, p);
+        return launch_early("grad_norm_final_kernel", grad_norm_final_kernel<Params>, dim3(static_cast<unsigned>(norms)), 32, 0, 1, stream, p);
     for (int32_t l = (small ? 1 : launches_for(P, count)) - 1; l >= 0; --l) {
         fill(l, P, tensors(P));
-        const int64_t blocks = std::max(std::min(p.tiles, int64_t{std::max(1, sm_count() * kCtas / P)}), int64_t{1});
+        const int32_t blocks = ctas(p.tiles, P, 4 * sm_count() * kCtas);
         if (int rc = launch_early("grad_scale_kernel", grad_scale_kernel<Params>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(P)),
                                   kThreads, 0, 1, stream, p))
             return rc;
