@@ -39,12 +39,11 @@ namespace {
 
 constexpr int kTile = 256;    // rows of a pair's tile, and its columns at most
 constexpr int kK = 64;        // k per chunk: one swizzled line of bf16
-constexpr int kStages = 6;
-constexpr int kOperand = 128 * kK * 2;  // bytes of one operand of a stage, of each CTA
-constexpr int kStage = 2 * kOperand;
+constexpr int kMaxStages = 16;
+constexpr int kOperand = 128 * kK * 2;  // bytes of 128 rows of an operand of a stage
 constexpr int kThreads = 320;  // warp 0 loads, warp 1 issues products, warps 2-9 epilogue
 constexpr int kStaging = 8 * 4096;  // for each epilogue warp two tiles of 32 x 32 bf16, or one of fp32
-constexpr int kSmem = 1024 + kStages * kStage + kStaging;
+constexpr int kShared = 224 * 1024, kSmem = 1024 + kShared;
 // Chunks that an accumulator adds at most for an fp32 result: the tensor core's additions round toward zero, so a sum's
 // error grows with its length (8e-7 of the result at 8192 k).
 constexpr int kSegment = 8192 / kK;
@@ -56,6 +55,10 @@ struct VocabParams {
     int64_t tiles_m;     // tiles along the lanes: rows of x (logits), vocabulary (dw), hidden (dx)
     int64_t tiles_n;     // along the columns: vocabulary (logits), hidden (dw), rows of x (dx)
     int32_t tile_n;      // columns of a tile, a multiple of 32
+    // What a stage holds: a_rows rows of operand A in each CTA (in the first alone where `second` is 0) and tile_n / 2 of B.
+    // Few rows of x are few rows of A, and more stages: what the tensor core finds in the place of the other rows goes to
+    // rows of the result that nobody reads.
+    int32_t a_rows, second, stages;
     int32_t runs;        // a run: consecutive column tiles of one item
     int32_t chunks;      // of 64 k, of one part of g
     int32_t parts;       // of g: 1, or 2 along k (fp32 dw)
@@ -74,6 +77,7 @@ struct VocabParams {
     int64_t ld_out, ld_addend;
     int32_t last;        // dx: of the last piece
     int32_t by_tma;      // dw: its tiles are stored by TMA
+    int32_t by_16;       // dw: it and its addend in pieces of 16 bytes
     unsigned int *status;
 };
 
@@ -91,9 +95,9 @@ __device__ __forceinline__ bool counts(const int32_t *target, const float *weigh
 
 // After a wait ran out: the copies into the last `issued` stages before stage
 // s have to land before the CTA ends.
-__device__ __noinline__ void drain_stages(uint32_t full, int issued, uint32_t s, uint32_t turn) {
+__device__ __noinline__ void drain_stages(uint32_t full, uint32_t stages, int issued, uint32_t s, uint32_t turn) {
     for (; issued > 0; --issued) {
-        if (s == 0) s = kStages, turn ^= 1;
+        if (s == 0) s = stages, turn ^= 1;
         --s;
         int given_up = 0;
         mbar_wait(full + 8 * s, turn ^ 1, &given_up);
@@ -230,8 +234,44 @@ __device__ __forceinline__ void stage_row(uint32_t tile, int lane, const float (
                      "f"(v[4 * q + 2]), "f"(v[4 * q + 3])
                      : "memory");
 }
-// A staged tile's rows one after another, a column to each lane: what TMA does not
-// store (rows that do not start on 16 bytes, an addend, a sum's later parts).
+// A staged tile in pieces of 16 bytes of its rows, an addend's pieces (loaded before
+// the tile's sums were there) added to it.
+template <typename T>
+constexpr int kTilePieces = 32 * 32 * sizeof(T) / 16 / 32;  // of a lane
+template <typename T>
+__device__ __forceinline__ void load_pieces(uint4 (&x)[kTilePieces<T>], int lane, const T *c, int64_t ldc, int rows, int64_t cols) {
+    constexpr int kPerRow = 32 * sizeof(T) / 16, V = 16 / sizeof(T);
+#pragma unroll
+    for (int q = 0; q < kTilePieces<T>; ++q) {
+        const int row = (q * 32 + lane) / kPerRow, e = (q * 32 + lane) % kPerRow * V;
+        x[q] = c && row < rows && e < cols ? ld16(c + row * ldc + e) : make_uint4(0, 0, 0, 0);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_pieces(uint32_t tile, int lane, T *d, int64_t ld, const uint4 (&x)[kTilePieces<T>], int rows, int64_t cols) {
+    constexpr int kPerRow = 32 * sizeof(T) / 16, V = 16 / sizeof(T);
+#pragma unroll
+    for (int q = 0; q < kTilePieces<T>; ++q) {
+        const int row = (q * 32 + lane) / kPerRow, e = (q * 32 + lane) % kPerRow * V;
+        const uint32_t w[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v[4 * i]), "=f"(v[4 * i + 1]), "=f"(v[4 * i + 2]), "=f"(v[4 * i + 3])
+                         : "r"(staged(tile, row, e / 4 + i))
+                         : "memory");
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (V == 4) o[i] = __float_as_uint(v[i] + __uint_as_float(w[i]));
+            else o[i] = pack_bf16x2(v[2 * i] + bf16_lo(w[i]), v[2 * i + 1] + bf16_hi(w[i]));
+        }
+        if (row < rows && e < cols) *reinterpret_cast<uint4 *>(d + row * ld + e) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+// A staged tile's rows one after another, a column to each lane: rows that do not
+// start on 16 bytes.
 template <typename T>
 __device__ __forceinline__ void store_rows(uint32_t tile, int lane, T *d, int64_t ld, const T *c, int64_t ldc, int rows, bool on) {
 #pragma unroll 1
@@ -258,21 +298,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
     const int seg_chunks = kMode == kWeights && sizeof(T) == 4 ? kSegment : 0x7FFFFFFF;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages, drained = acc_full + 16,
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages, acc_full = empty + 8 * kMaxStages, drained = acc_full + 16,
                    done = drained + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_cta_rank();
     const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
     const int64_t items = p.items + static_cast<int64_t>(p.rest) * p.splits;
     const int tile_n = p.tile_n;
+    const uint32_t stages = p.stages, a_bytes = p.a_rows * kK * 2, stage = a_bytes + tile_n * kK;
 
     let_next_begin();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2 * kStages; ++i) mbar_init(full + 8 * i, 1);
+        for (int i = 0; i < 2 * kMaxStages; ++i) mbar_init(full + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
             mbar_init(drained + 8 * i, 16);  // eight epilogue warps of each CTA
@@ -303,32 +344,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t b = static_cast<int32_t>(n * tile_n + tile_n / 2 * rank);
                 for (int32_t c = it.c0; c < it.c1; ++c) {
                     if (!(ok = mbar_wait(empty + 8 * s, turn, &failed))) break;
-                    const uint32_t dst = base + s * kStage, bar = lead_full + 8 * s;
+                    const uint32_t dst = base + s * stage, bar = lead_full + 8 * s;
                     const bool second = kMode == kWeights && c >= p.chunks;
                     const int32_t k = (second ? c - p.chunks : c) * kK;
-                    if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * kOperand + 2 * 64 * tile_n);
+                    if (rank == 0) mbar_expect_tx(full + 8 * s, a_bytes * (1 + p.second) + 2 * tile_n * kK);
                     if (kMode == kWeights) {  // the library's own copies: their rows are whole columns of 128 bytes
                         tma_load_columns_pair(dst, second ? &map_c : &map_a, bar, a >> 6, k);
-                        tma_load_columns_pair(dst + kOperand, &map_b, bar, b >> 6, k);
+                        tma_load_columns_pair(dst + a_bytes, &map_b, bar, b >> 6, k);
                     } else {
                         if (kMnA) {
                             tma_load_2d_pair(dst, &map_a, bar, a, k);
                             tma_load_2d_pair(dst + kOperand / 2, &map_a, bar, a + 64, k);
-                        } else {
+                        } else if (rank == 0 || p.second) {
                             tma_load_2d_pair(dst, &map_a, bar, k, a);
                         }
-                        tma_load_2d_pair(dst + kOperand, &map_b, bar, k, b);
+                        tma_load_2d_pair(dst + a_bytes, &map_b, bar, k, b);
                     }
-                    issued = issued < kStages ? issued + 1 : kStages;
-                    if (++s == kStages) s = 0, turn ^= 1;
+                    issued = issued < static_cast<int>(stages) ? issued + 1 : static_cast<int>(stages);
+                    if (++s == stages) s = 0, turn ^= 1;
                 }
             }
         }
         // both CTAs' copies count on the first one's barriers; the other waits at the cluster barrier below
-        if (!ok && rank == 0) drain_stages(full, issued, s, turn);
+        if (!ok && rank == 0) drain_stages(full, stages, issued, s, turn);
     } else if (warp == 1 && rank == 0) {
         const uint64_t desc_a = smem_desc(base, kMnA ? kOperand / 2 : 16, 1024, 2);
-        const uint64_t desc_b = smem_desc(base + kOperand, kMnB ? kOperand / 2 : 16, 1024, 2);
+        const uint64_t desc_b = smem_desc(base + a_bytes, kMnB ? kOperand / 2 : 16, 1024, 2);
         const uint32_t idesc = bf16_idesc(kTile, static_cast<uint32_t>(tile_n), kMnA, kMnB);
         uint32_t s = 0, turn = 0, seq = 0;
         bool ready = false;  // whether the next stage was seen to be full already
@@ -342,10 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int32_t c = c0; c < c1; ++c) {
                         if (!ready) mbar_wait(full + 8 * s, turn, &failed);
                         tc_fence_after();
-                        const uint32_t next = s + 1 == kStages ? 0 : s + 1;
+                        const uint32_t next = s + 1 == stages ? 0 : s + 1;
                         ready = mbar_test(full + 8 * next, next ? turn : turn ^ 1);
                         if (elect_one()) {
-                            const uint64_t da = desc_a + s * (kStage >> 4), db = desc_b + s * (kStage >> 4);
+                            const uint64_t da = desc_a + s * (stage >> 4), db = desc_b + s * (stage >> 4);
 #pragma unroll
                             for (int k = 0; k < kK / 16; ++k)
                                 tc_mma_bf16_pair(acc, da + k * kStepA, db + k * kStepB, idesc, c > c0 || k > 0);
@@ -368,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t lead_drained = cluster_map(drained, 0);
-        const uint32_t staging = base + kStages * kStage + (warp - 2) * 4096;
+        const uint32_t staging = base + kShared - kStaging + (warp - 2) * 4096;
         const int batches = tile_n / 32;
         constexpr bool kTwoParts = sizeof(T) == 4;
         uint32_t seq = 0, turn = 0;
@@ -381,10 +422,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 r.target = p.target[lane_at];
                 r.lse = p.lse[lane_at], r.lse2 = r.lse * kLog2e, r.weight = p.weight ? p.weight[lane_at] : 1.0f;
             }
+            // dw: the pieces that are added to the tile of batch j: the addend's, or of the sum so far
+            uint4 pieces[kTilePieces<T>];
+            const auto fetch_pieces = [&](int64_t n, int j, bool later) {
+                const int64_t row0 = lane_at - lane, left = p.cols - row0, col = n * tile_n + j * 32;
+                const T *c = later ? static_cast<const T *>(p.out) + row0 * p.ld_out + col
+                                   : p.addend ? static_cast<const T *>(p.addend) + row0 * p.ld_addend + col : nullptr;
+                load_pieces(pieces, lane, c, later ? p.ld_out : p.ld_addend, left < 32 ? static_cast<int>(left) : 32, p.hidden - col);
+            };
             for (int64_t n = it.n0; n < it.n1; ++n) {
                 for (int32_t c0 = it.c0; c0 < it.c1; ++seq) {
                     const int32_t c1 = it.c1 - c0 > seg_chunks ? c0 + seg_chunks : it.c1;
                     const uint32_t buf = seq & 1;
+                    if (kMode == kWeights && p.by_16) fetch_pieces(n, half, c0 > it.c0);
                     mbar_wait(acc_full + 8 * buf, (seq >> 1) & 1, &failed);
                     __syncwarp();
                     tc_fence_after();
@@ -446,6 +496,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     tma_store_commit();
                                 }
                                 turn ^= 1;
+                            } else if (p.by_16) {
+                                stage_row(staging, lane, v);
+                                __syncwarp();
+                                uint4 mine[kTilePieces<T>];
+#pragma unroll
+                                for (int q = 0; q < kTilePieces<T>; ++q) mine[q] = pieces[q];
+                                if (j + 2 < batches) fetch_pieces(n, j + 2, c0 > it.c0);
+                                store_pieces(staging, lane, static_cast<T *>(p.out) + row0 * p.ld_out + col, p.ld_out, mine,
+                                             left < 32 ? static_cast<int>(left) : 32, p.hidden - col);
                             } else {
                                 stage_row(staging, lane, v);
                                 __syncwarp();
@@ -605,6 +664,16 @@ int launch(const VocabParams &p, const CUtensorMap &a, const CUtensorMap &b, con
                         stream, a, b, c, d, p);
 }
 
+// The stages of a product whose first operand has `rows` rows along its summed axis
+// (0: lies the other way, always 128).
+void lay_out(VocabParams *p, int64_t rows, bool staging) {
+    p->a_rows = rows > 0 && rows < 128 ? static_cast<int32_t>(ceil_div(rows, int64_t{8}) * 8) : 128;
+    p->second = rows == 0 || rows > 128;
+    const int stage = (p->a_rows + p->tile_n / 2) * kK * 2;
+    // the last stage's 128 rows of A, as the tensor core reads them, lie in the shared memory too
+    p->stages = std::min((kShared - (staging ? kStaging : 0) - std::max(stage, kOperand)) / stage + 1, kMaxStages);
+}
+
 int encode(CUtensorMap *map, const void *base, int64_t inner, int64_t outer, int64_t ld, int box_outer) {
     return encode_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, ld * 2, kK, box_outer);
 }
@@ -744,7 +813,10 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
     const int weights_n = hidden <= 128 ? 128 : kTile;  // columns of dw's tiles
     if (copied)
         if (int rc = copy_live_rows(p, x, ldx, live, stream)) return rc;
-    if (int rc = encode(&rows_k, copied ? live : x, hidden, rows, copied ? ld_live : ldx, 128)) return rc;
+    VocabParams of_rows = p;
+    of_rows.tile_n = kTile;
+    lay_out(&of_rows, rows, true);
+    if (int rc = encode(&rows_k, copied ? live : x, hidden, rows, copied ? ld_live : ldx, of_rows.a_rows)) return rc;
     if (dw) {
         if (int rc = encode_columns(&live_mn, live, ld_live, rows, weights_n / 128)) return rc;
     }
@@ -768,6 +840,7 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
             q.tiles_m = tiles_t, q.tiles_n = ceil_div(cols, int64_t{q.tile_n}), q.runs = static_cast<int32_t>(q.tiles_n);
             q.items = q.tiles_m * q.runs;
             if (int rc = encode(&w_k, w + first * ldw, hidden, cols, ldw, q.tile_n / 2)) return rc;
+            lay_out(&q, rows, true);
             if (int rc = launch<kGradient, T>(q, rows_k, w_k, g_to, low_to, stream)) return rc;
         }
         if (dw) {
@@ -778,6 +851,8 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
             q.items = q.tiles_m * q.runs;
             q.out = dw + first * lddw, q.ld_out = lddw;
             q.addend = addend ? addend + first * ld_addend : nullptr, q.ld_addend = ld_addend;
+            q.by_16 = aligned(q.out, 16) && lddw * sizeof(T) % 16 == 0 && hidden * sizeof(T) % 16 == 0 &&
+                      (!addend || (aligned(q.addend, 16) && ld_addend * sizeof(T) % 16 == 0));
             q.by_tma = !addend && aligned(q.out, 16) && lddw * sizeof(T) % 16 == 0;
             if (q.by_tma) {
                 if (int rc = encode_tile_map(&to, kParts == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q.out, hidden,
@@ -785,6 +860,7 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
                                              kParts == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
                     return rc;
             }
+            lay_out(&q, 0, true);
             if (int rc = launch<kWeights, T>(q, g_mn, live_mn, low_mn, to, stream)) return rc;
         }
         if (dx) {
@@ -797,6 +873,7 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
             q.out = dx, q.ld_out = lddx, q.sum = sum, q.part = part;
             if (int rc = encode(&w_mn, w + first * ldw, hidden, cols, ldw, kK)) return rc;
             if (int rc = encode_tile_map(&g_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g, cols, rows, how.piece * 2, kK, q.tile_n / 2)) return rc;
+            lay_out(&q, 0, false);
             if (int rc = launch<kInputs, uint16_t>(q, w_mn, g_k, g_k, g_k, stream)) return rc;
             if (q.rest > 0)
                 if (int rc = launch_early("vocab_inputs_kernel", vocab_inputs_kernel, dim3(static_cast<unsigned>(q.rest * (q.tile_n / 2))), kTile, 0, 1,
@@ -845,7 +922,8 @@ extern "C" int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t
         from = live, ldx = live_ld(hidden);
     }
     CUtensorMap a{}, b{};
-    if (int rc = encode(&a, from, hidden, rows, ldx, 128)) return rc;
+    lay_out(&p, rows, false);
+    if (int rc = encode(&a, from, hidden, rows, ldx, p.a_rows)) return rc;
     if (int rc = encode(&b, w, hidden, vocab, ldw, p.tile_n / 2)) return rc;
     if (int rc = launch<kLoss, float>(p, a, b, b, b, stream)) return rc;
     return launch_early("vocab_join_kernel", vocab_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, int64_t{8}))), 256, 0, 1, stream, p,
