@@ -685,9 +685,13 @@ int encode_store(CUtensorMap *map, const void *base, int64_t inner, int64_t oute
 }
 
 // Clocks of a chunk of 64 k at 256 columns, of a tile's beginning and end that its
-// neighbours do not hide, and of an item's.
+// neighbours do not hide, and of an item's.  A chunk of fewer columns is held by its
+// loads: 128 rows of x and half the columns of w at 63 bytes a clock for each SM; by
+// DRAM's 24 where x is a single tile of rows, for then w is read once.
 constexpr int64_t kChunkClocks = 520, kTileClocks = 500, kItemClocks = 2500;
-int64_t tile_clocks(int64_t chunks, int64_t columns) { return chunks * std::max(kChunkClocks * columns / kTile, int64_t{300}) + kTileClocks; }
+int64_t tile_clocks(int64_t chunks, int64_t columns, int64_t tiles_m) {
+    return chunks * (tiles_m == 1 ? columns * 27 / 10 : kChunkClocks * (kTile + columns) / (2 * kTile)) + kTileClocks;
+}
 
 // Columns of the logits' tiles, and the loss's runs of them: what leaves the pairs
 // evenly busy.
@@ -701,7 +705,7 @@ Split loss_split(int64_t tiles_m, int64_t vocab, int64_t chunks, int64_t pairs) 
         const int64_t tiles = ceil_div(vocab, int64_t{columns});
         for (int64_t rounds = 1; rounds <= 4; ++rounds) {
             const int64_t r = std::max(std::min(tiles, rounds * pairs / tiles_m), int64_t{1});
-            const int64_t clocks = ceil_div(tiles_m * r, pairs) * (ceil_div(tiles, r) * tile_clocks(chunks, columns) + kItemClocks);
+            const int64_t clocks = ceil_div(tiles_m * r, pairs) * (ceil_div(tiles, r) * tile_clocks(chunks, columns, tiles_m) + kItemClocks);
             if (least < 0 || clocks < least) least = clocks, best = {columns, static_cast<int32_t>(r)};
         }
     }
@@ -711,7 +715,7 @@ int32_t gradient_columns(int64_t tiles_m, int64_t cols, int64_t chunks, int64_t 
     int32_t best = kTile;
     int64_t least = -1;
     for (int32_t columns = kTile; columns >= 128; columns -= 32) {
-        const int64_t clocks = ceil_div(tiles_m * ceil_div(cols, int64_t{columns}), pairs) * tile_clocks(chunks, columns);
+        const int64_t clocks = ceil_div(tiles_m * ceil_div(cols, int64_t{columns}), pairs) * tile_clocks(chunks, columns, tiles_m);
         if (least < 0 || clocks < least) least = clocks, best = columns;
     }
     return best;
