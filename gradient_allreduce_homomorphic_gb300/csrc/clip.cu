@@ -10,6 +10,10 @@
 // the first pass has left in L2.  The tables of tensors travel as kernel
 // parameters; a long list takes several launches of each pass.
 //
+// Bound by HBM: the norms of 8 x 45M fp32 values 229 us (6.3 TB/s); by one norm, out
+// of place, 482 us (35 for the norm of one worker's, scaling at 6.3 TB/s).  12 small
+// tensors 8.8 us a call, the two launches' host time.
+//
 // Squares are summed sixteen at a time in fp32 before an fp64 addition (fp64 runs
 // at 1/64 of the fp32 rate here).  Sixteen whose sum comes near either end of
 // fp32's range are squared again in fp64.

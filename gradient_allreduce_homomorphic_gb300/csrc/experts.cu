@@ -8,7 +8,12 @@
 // Every CTA takes a run of pairs; counts by CTA come from a first launch (none
 // where one CTA holds all pairs), sums over the CTAs ahead give its first ranks,
 // and ranks within it come from comparing 32 pairs at a time.  No atomic decides
-// an order, so the rows are the same in every run.
+// an order, so the rows are the same in every run.  262144 pairs of 256 experts 25 us
+// in two launches, 2048 pairs of 64 experts 6 us in one: chains of dependent loads.
+//
+// Moving rows is bound by HBM: 8 x 4096 tokens to 8 experts each, 4096 bf16, 371 us
+// there (6.5 TB/s; each token's row read once), 379 us back (6.4 TB/s), 706 us for the
+// gradient of that (6.5 TB/s: dy and dweight from one read of dout and y).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -681,6 +686,9 @@ int launch_move(int which, MoveParams &p, bool clears, cudaStream_t stream) {
         constexpr int J = decltype(rows)::value;
         p.segments = ceil_div(p.hidden, int64_t{32 * pieces_of(V, J) * V});
         p.share = 1;
+        // few tokens: a warp alone would take a row's segments one after another (4 x 501 x 4 x 1001 fp32, both calls: 82 us with
+        // a warp to each, 29 with up to eight); many: a warp reads its token's positions once (8 x 4096 x 4 x 4096 bf16 the
+        // gradient 522 us with eight to each, 453 with one)
         while (p.share < kWarps && p.share * 2 <= p.segments && p.items * p.share < sm_count() * int64_t{24}) p.share *= 2;
         const int64_t ctas = ceil_div(p.items, int64_t{kWarps / p.share}) + (clears ? ceil_div(p.rows, int64_t{32 * kWarps}) : 0);
         if (ctas == 0) return static_cast<int>(GAR_OK);
