@@ -78,13 +78,11 @@ __device__ __forceinline__ int tensor_of(const P &p, int64_t tile) {
 // The squares of n values (16 or fewer), in fp64.
 template <int N>
 __device__ __forceinline__ double squares(const float (&x)[N]) {
-    float s[N];
+    constexpr int kChains = N < 4 ? N : 4;
+    float s[kChains];
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = x[i] * x[i];
-#pragma unroll
-    for (int w = N / 2; w > 0; w /= 2)
-#pragma unroll
-        for (int i = 0; i < w; ++i) s[i] += s[i + w];
+    for (int i = 0; i < N; ++i) s[i % kChains] = i < kChains ? x[i] * x[i] : fmaf(x[i], x[i], s[i % kChains]);
+    if constexpr (kChains == 4) s[0] = (s[0] + s[1]) + (s[2] + s[3]);
     if (s[0] > 1e-24f && s[0] < 1e38f) return s[0];
     uint32_t any = 0;
 #pragma unroll
@@ -138,13 +136,18 @@ __device__ __forceinline__ double tile_squares(const T *x, int64_t n, int64_t i)
     const Range r = tile_range(x, n, i);
     double sum = 0.0;
     if (r.begin >= r.end) return sum;
-    const int64_t vecs = (r.end - r.body) / V;
+    const int vecs = static_cast<int>((r.end - r.body) / V);
     const uint4 *from = reinterpret_cast<const uint4 *>(x + r.body);
     uint4 q[kVecs];
+    if (vecs == kVecs * kThreads) {
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-        const int64_t at = k * kThreads + threadIdx.x;
-        q[k] = at < vecs ? from[at] : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < kVecs; ++k) q[k] = from[k * kThreads + threadIdx.x];
+    } else {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            const int at = k * kThreads + threadIdx.x;
+            q[k] = at < vecs ? from[at] : make_uint4(0, 0, 0, 0);
+        }
     }
     float v[16];
 #pragma unroll
@@ -218,18 +221,18 @@ __device__ __forceinline__ void scale_tile(const T *x, T *y, int64_t n, int64_t 
         for (int64_t e = r.begin + threadIdx.x; e < r.end; e += kThreads) store_f32(y + e, load_f32(x + e) * c);
         return;
     }
-    const int64_t vecs = (r.end - r.body) / V;
+    const int vecs = static_cast<int>((r.end - r.body) / V);
     const uint4 *from = reinterpret_cast<const uint4 *>(x + r.body);
     uint4 *to = reinterpret_cast<uint4 *>(y + r.body);
     uint4 q[kVecs];
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-        const int64_t at = k * kThreads + threadIdx.x;
+        const int at = k * kThreads + threadIdx.x;
         if (at < vecs) q[k] = from[at];
     }
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-        const int64_t at = k * kThreads + threadIdx.x;
+        const int at = k * kThreads + threadIdx.x;
         if (at >= vecs) continue;
         float v[V];
         unpack<T>(q[k], v);

@@ -168,6 +168,8 @@ struct Row {
 };
 
 // 32 logits of a row (vocabulary columns col ..) into its running maximum and sum.
+// They never leave registers within a run, and a lane is a row, so no lane asks
+// another.
 // Powers are of two, their exponents one fma each: z log2(e) less the maximum's,
 // whose rounding is the same in every term and in what is written, so that it
 // drops out.
@@ -195,10 +197,6 @@ __device__ __forceinline__ void take_logits(const VocabParams &p, float (&v)[32]
     r.top = top, r.sum = (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// A row's maximum and sum never leave registers within a run, and a lane is a row, so
-// no lane asks another; 128 columns of a tile for each of eight warps take about a
-// quarter of the products' time at hidden = 1024 and overlap them.
-//
 // The same logits to g (col counts from the piece's first column), as bf16 pairs:
 // to `low` what `high` leaves of an fp32 value.  A bf16 g's exponent is one fma, which
 // may put 2^-24 of lse's size into it; that of a g of two parts is formed from z - lse.

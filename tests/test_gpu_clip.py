@@ -1,7 +1,7 @@
 """Global gradient norm and clipping against sums in 64 bits.
 
-Tolerances: a square and four pairwise sums round in fp32 (5 2^-24 of the sum of
-squares, half of that in the norm), the norm once more: 4 2^-24.  A clipped value is
+Tolerances: four squares added by fma and two pairwise sums round in fp32 (6 2^-24 of
+the sum of squares, half of that in the norm), the norm once more: 4 2^-24.  A clipped value is
 the product with c = max_norm / norm (one quotient, the norm's error) and one rounding
 to its type."""
 import math
