@@ -49,7 +49,7 @@ constexpr int kK = 64;        // k per chunk: one swizzled line of bf16
 constexpr int kMaxStages = 16;
 constexpr int kOperand = 128 * kK * 2;  // bytes of 128 rows of an operand of a stage
 constexpr int kThreads = 320;  // warp 0 loads, warp 1 issues products, warps 2-9 epilogue
-constexpr int kStaging = 8 * 4096;  // for each epilogue warp two tiles of 32 x 32 bf16, or one of fp32
+constexpr int kStaging = 8 * 4096;  // for each epilogue warp a tile of 32 x 64 bf16, two of 32 x 32, or one of 32 x 32 fp32
 constexpr int kShared = 224 * 1024, kSmem = 1024 + kShared;
 // Chunks that an accumulator adds at most for an fp32 result: the tensor core's additions round toward zero, so a sum's
 // error grows with its length (8e-7 of the result at 8192 k).
@@ -85,6 +85,10 @@ struct VocabParams {
     int32_t last;        // dx: of the last piece
     int32_t by_tma;      // dw: its tiles are stored by TMA
     int32_t by_16;       // dw: it and its addend in pieces of 16 bytes
+    // logits of the gradient: x, to be copied to `live` on the way (NULL: not)
+    const uint16_t *x;
+    uint16_t *live;
+    int64_t ldx, ld_live;
     unsigned int *status;
 };
 
@@ -297,6 +301,26 @@ __device__ __forceinline__ void store_rows(uint32_t tile, int lane, T *d, int64_
     }
 }
 
+// The same of 32 bf16 values, the first (u = 0) or second half of a row of 64.
+__device__ __forceinline__ void stage_half_row(uint32_t tile, int lane, int u, const uint32_t (&w)[16]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(staged(tile, lane, 4 * u + q)), "r"(w[4 * q]), "r"(w[4 * q + 1]),
+                     "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
+                     : "memory");
+}
+
+// A row of x to `live`, 0 if it does not count, filled up to whole columns of 64: an
+// operand of dw, where a NaN or an infinity in such a row would meet g's zeros.
+__device__ __forceinline__ void copy_live_row(const VocabParams &p, int64_t t, int thread, int threads) {
+    const bool live = counts(p.target, p.weight, p.vocab, t);
+    const uint16_t *from = p.x + t * p.ldx;
+    uint16_t *to = p.live + t * p.ld_live;
+    const int64_t pieces = live ? p.hidden / 8 : 0;
+    for (int64_t i = thread; i < pieces; i += threads) reinterpret_cast<uint4 *>(to)[i] = reinterpret_cast<const uint4 *>(from)[i];
+    for (int64_t h = pieces * 8 + thread; h < p.ld_live; h += threads) to[h] = live && h < p.hidden ? from[h] : 0;
+}
+
 template <int kMode, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -421,7 +445,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t staging = base + kShared - kStaging + (warp - 2) * 4096;
         const int batches = tile_n / 32;
         constexpr bool kTwoParts = sizeof(T) == 4;
-        uint32_t seq = 0, turn = 0;
+        // bf16 tiles leave in rows of 128 bytes, 64 columns at a time: TMA takes a row's 64 bytes as long as 128
+        const bool wide = !kTwoParts && (kMode == kGradient || (kMode == kWeights && p.by_tma));
+        uint32_t seq = 0;
+        if (kMode == kGradient && p.live)  // while the first tiles are on their way
+            for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + warp - 2; t < p.rows; t += static_cast<int64_t>(gridDim.x) * 8)
+                copy_live_row(p, t, lane, 32);
         for (int64_t i = first; i < items; i += step) {
             const Item it = item_of(p, i);
             const int64_t lane_at = it.m * kTile + 128 * rank + quarter * 32 + lane;
@@ -451,8 +480,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_before();
                         if (lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
                     }
+                    if (wide) {
 #pragma unroll 1
-                    for (int j = half; j < batches; j += 2) {
+                        for (int q = half; q < batches / 2; q += 2) {
+                            const int64_t col = n * tile_n + q * 64, row0 = lane_at - lane;
+                            const bool on = kMode == kGradient ? row0 < p.rows && col < p.cols : row0 < p.cols && col < p.hidden;  // all lanes
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                __syncwarp();
+                                float v[32];
+                                tc_load32(v, lanes + buf * kTile + q * 64 + u * 32);
+                                tc_wait_ld();
+                                if (u == 1 && q + 2 >= batches / 2) {
+                                    tc_fence_before();
+                                    __syncwarp();
+                                    if (lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
+                                }
+                                if (!on) continue;
+                                uint32_t w[16], none[16];
+                                if (kMode == kGradient) {
+                                    give_gradient<false>(p, v, r, col + u * 32, w, none);
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+                                }
+                                if (u == 0) {  // the tile before has left
+                                    if (lane == 0) tma_store_wait_read<0>();
+                                    __syncwarp();
+                                }
+                                stage_half_row(staging, lane, u, w);
+                            }
+                            if (on) {
+                                fence_async_shared();
+                                __syncwarp();
+                                if (lane == 0) {
+                                    tma_store_2d(kMode == kGradient ? &map_c : &map_d, staging, static_cast<int32_t>(col), static_cast<int32_t>(row0));
+                                    tma_store_commit();
+                                }
+                            }
+                        }
+                    }
+#pragma unroll 1
+                    for (int j = half; j < batches && !wide; j += 2) {
                         __syncwarp();
                         float v[32];
                         tc_load32(v, lanes + buf * kTile + j * 32);
@@ -469,42 +538,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (lane_at - lane >= p.rows || col >= p.cols) continue;  // all lanes: no row, or no column, of theirs
                             uint32_t high[16], low[16];
                             give_gradient<kTwoParts>(p, v, r, col, high, low);
-                            // two tiles take turns, or hold the two parts
-                            if (lane == 0) tma_store_wait_read<kTwoParts ? 0 : 1>();
+                            if (lane == 0) tma_store_wait_read<0>();
                             __syncwarp();
-                            const uint32_t tile = staging + (kTwoParts ? 0 : turn * 2048);
-                            stage_row(tile, lane, high);
-                            if (kTwoParts) stage_row(tile + 2048, lane, low);
+                            stage_row(staging, lane, high);
+                            stage_row(staging + 2048, lane, low);
                             fence_async_shared();
                             __syncwarp();
                             if (lane == 0) {
-                                tma_store_2d(&map_c, tile, static_cast<int32_t>(col), static_cast<int32_t>(lane_at));
-                                if (kTwoParts) tma_store_2d(&map_d, tile + 2048, static_cast<int32_t>(col), static_cast<int32_t>(lane_at));
+                                tma_store_2d(&map_c, staging, static_cast<int32_t>(col), static_cast<int32_t>(lane_at));
+                                tma_store_2d(&map_d, staging + 2048, static_cast<int32_t>(col), static_cast<int32_t>(lane_at));
                                 tma_store_commit();
                             }
-                            turn ^= 1;
                         } else if (kMode == kWeights) {
                             const int64_t row0 = lane_at - lane, left = p.cols - row0;
                             if (left <= 0 || col >= p.hidden) continue;  // all lanes
-                            const uint32_t tile = staging + (kTwoParts ? 0 : turn * 2048);
                             if (p.by_tma && c1 - c0 == it.c1 - it.c0) {
-                                if (lane == 0) tma_store_wait_read<kTwoParts ? 0 : 1>();
+                                if (lane == 0) tma_store_wait_read<0>();
                                 __syncwarp();
-                                if constexpr (kTwoParts) {
-                                    stage_row(tile, lane, v);
-                                } else {
-                                    uint32_t w[16];
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-                                    stage_row(tile, lane, w);
-                                }
+                                stage_row(staging, lane, v);
                                 fence_async_shared();
                                 __syncwarp();
                                 if (lane == 0) {
-                                    tma_store_2d(&map_d, tile, static_cast<int32_t>(col), static_cast<int32_t>(row0));
+                                    tma_store_2d(&map_d, staging, static_cast<int32_t>(col), static_cast<int32_t>(row0));
                                     tma_store_commit();
                                 }
-                                turn ^= 1;
                             } else if (p.by_16) {
                                 stage_row(staging, lane, v);
                                 __syncwarp();
@@ -584,18 +641,11 @@ __global__ void __launch_bounds__(256) vocab_join_kernel(const __grid_constant__
     }
 }
 
-// x with the rows that do not count set to 0, its rows filled up to whole columns of
-// 64: an operand of dw, where a NaN or an infinity in such a row would meet g's zeros.
-__global__ void __launch_bounds__(256)
-    vocab_live_rows_kernel(const uint16_t *x, int64_t ldx, const __grid_constant__ VocabParams p, uint16_t *to, int64_t ld_to) {
+// x to `live` alone: the logits take it from there.
+__global__ void __launch_bounds__(256) vocab_live_rows_kernel(const __grid_constant__ VocabParams p) {
     let_next_begin();
     after_previous();
-    const int64_t t = blockIdx.x;
-    const bool live = counts(p.target, p.weight, p.vocab, t);
-    const int64_t pieces = live ? p.hidden / 8 : 0;
-    for (int64_t i = threadIdx.x; i < pieces; i += 256)
-        reinterpret_cast<uint4 *>(to + t * ld_to)[i] = reinterpret_cast<const uint4 *>(x + t * ldx)[i];
-    for (int64_t h = pieces * 8 + threadIdx.x; h < ld_to; h += 256) to[t * ld_to + h] = live && h < p.hidden ? x[t * ldx + h] : 0;
+    copy_live_row(p, blockIdx.x, threadIdx.x, 256);
 }
 
 // The tiles of dx whose k was cut: the parts' sums added in order (6 us for 64 x
@@ -613,7 +663,7 @@ __global__ void __launch_bounds__(kTile) vocab_inputs_kernel(const __grid_consta
     const float *of = p.part + (tile * kTile + t0) * kTile + threadIdx.x;
     const int64_t stride = static_cast<int64_t>(p.rest) * kTile * kTile;
     float a = 0.0f, b = 0.0f;
-#pragma unroll 8
+#pragma unroll 16
     for (int i = 0; i < p.splits; ++i) {
         a += of[i * stride];
         if (two) b += of[i * stride + kTile];
@@ -690,8 +740,13 @@ int encode(CUtensorMap *map, const void *base, int64_t inner, int64_t outer, int
 int encode_columns(CUtensorMap *map, const void *base, int64_t inner, int64_t outer, int columns) {
     return encode_column_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, inner, outer, inner * 2, columns, kK);
 }
-int encode_store(CUtensorMap *map, const void *base, int64_t inner, int64_t outer) {
-    return encode_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, inner * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+// Tiles of 32 rows as the epilogue stores them: of a bf16 matrix, of one of two parts (ld in elements), of fp32.
+int encode_store(CUtensorMap *map, const void *base, int64_t inner, int64_t outer, int64_t ld, bool wide) {
+    return encode_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, ld * 2, wide ? 64 : 32, 32,
+                           wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+int encode_store_f32(CUtensorMap *map, const void *base, int64_t inner, int64_t outer, int64_t ld) {
+    return encode_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, inner, outer, ld * 4, 32, 32);
 }
 
 // Clocks of a chunk of 64 k at 256 columns, of a tile's beginning and end that its
@@ -724,7 +779,7 @@ Split loss_split(int64_t tiles_m, int64_t vocab, int64_t chunks, int64_t pairs) 
 int32_t gradient_columns(int64_t tiles_m, int64_t cols, int64_t chunks, int64_t pairs) {
     int32_t best = kTile;
     int64_t least = -1;
-    for (int32_t columns = kTile; columns >= 128; columns -= 32) {
+    for (int32_t columns = kTile; columns >= 128; columns -= 64) {  // g leaves in tiles of 64 columns
         const int64_t clocks = ceil_div(tiles_m * ceil_div(cols, int64_t{columns}), pairs) * tile_clocks(chunks, columns, tiles_m);
         if (least < 0 || clocks < least) least = clocks, best = columns;
     }
@@ -801,9 +856,9 @@ int check(const void *x, int64_t ldx, const void *w, int64_t ldw, const int32_t 
     return GAR_OK;
 }
 
-int copy_live_rows(const VocabParams &p, const uint16_t *x, int64_t ldx, uint16_t *to, cudaStream_t stream) {
-    return launch_early("vocab_live_rows_kernel", vocab_live_rows_kernel, dim3(static_cast<unsigned>(p.rows)), 256, 0, 1, stream, x, ldx, p, to,
-                        live_ld(p.hidden));
+int copy_live_rows(VocabParams p, const uint16_t *x, int64_t ldx, uint16_t *to, cudaStream_t stream) {
+    p.x = x, p.ldx = ldx, p.live = to, p.ld_live = live_ld(p.hidden);
+    return launch_early("vocab_live_rows_kernel", vocab_live_rows_kernel, dim3(static_cast<unsigned>(p.rows)), 256, 0, 1, stream, p);
 }
 // Rows of x that do not start on 128 bytes load at half the rate (two lines for each
 // one's 128 bytes): copied to such that do where the logits take long enough.
@@ -823,7 +878,7 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
     const auto part = reinterpret_cast<float *>(workspace + kParts * how.g + how.x + how.sum);
     const int64_t tiles_t = ceil_div(rows, int64_t{kTile}), tiles_h = ceil_div(hidden, int64_t{kTile});
     CUtensorMap rows_k{}, live_mn{}, g_mn{}, low_mn{}, g_to{}, low_to{};
-    const bool copied = dw || copy_pays(x, ldx, p);
+    const bool copied = copy_pays(x, ldx, p);
     const int weights_n = hidden <= 128 ? 128 : kTile;  // columns of dw's tiles
     if (copied)
         if (int rc = copy_live_rows(p, x, ldx, live, stream)) return rc;
@@ -835,10 +890,10 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
         if (int rc = encode_columns(&live_mn, live, ld_live, rows, weights_n / 128)) return rc;
     }
     if (int rc = encode_columns(&g_mn, g, how.piece, rows, 2)) return rc;
-    if (int rc = encode_store(&g_to, g, how.piece, rows)) return rc;
+    if (int rc = encode_store(&g_to, g, how.piece, rows, how.piece, kParts == 1)) return rc;
     if (kParts == 2) {
         if (int rc = encode_columns(&low_mn, g_low, how.piece, rows, 2)) return rc;
-        if (int rc = encode_store(&low_to, g_low, how.piece, rows)) return rc;
+        if (int rc = encode_store(&low_to, g_low, how.piece, rows, how.piece, false)) return rc;
     } else {
         low_mn = g_mn, low_to = g_to;
     }
@@ -855,6 +910,7 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
             q.items = q.tiles_m * q.runs;
             if (int rc = encode(&w_k, w + first * ldw, hidden, cols, ldw, q.tile_n / 2)) return rc;
             lay_out(&q, rows, true);
+            if (dw && !copied && first == 0) q.x = x, q.ldx = ldx, q.live = live, q.ld_live = ld_live;
             if (int rc = launch<kGradient, T>(q, rows_k, w_k, g_to, low_to, stream)) return rc;
         }
         if (dw) {
@@ -869,9 +925,7 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
                       (!addend || (aligned(q.addend, 16) && ld_addend * sizeof(T) % 16 == 0));
             q.by_tma = !addend && aligned(q.out, 16) && lddw * sizeof(T) % 16 == 0;
             if (q.by_tma) {
-                if (int rc = encode_tile_map(&to, kParts == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q.out, hidden,
-                                             cols, lddw * static_cast<int64_t>(sizeof(T)), 32, 32,
-                                             kParts == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+                if (int rc = kParts == 2 ? encode_store_f32(&to, q.out, hidden, cols, lddw) : encode_store(&to, q.out, hidden, cols, lddw, true))
                     return rc;
             }
             lay_out(&q, 0, true);
