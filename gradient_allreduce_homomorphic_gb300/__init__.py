@@ -266,7 +266,10 @@ class PtrTable:
 
     def __init__(self, tensors, allow_none: bool = False):
         self.tensors = list(tensors)
-        ptrs = [(_dev(t) if t is not None else None) if allow_none else _dev(t) for t in self.tensors]
+        if allow_none:
+            ptrs = [_dev(t) if t is not None else None for t in self.tensors]
+        else:
+            ptrs = [t.data_ptr() if t.is_cuda else _dev(t) for t in self.tensors]
         self.array = (C.c_void_p * len(ptrs))(*ptrs)
         first = next((t for t in self.tensors if t is not None), None)
         self.numel = first.numel() if first is not None else 0
@@ -1056,19 +1059,18 @@ class GradTables:
         self.src = self._table(grads, "grads")
         self.dst = self.src if out is None else self._table(out, "out")
         first = self.src.tensors[:self.count]
+        types, sizes = [t.dtype for t in first], [t.numel() for t in first]
         self.dtype = np.array([_dtype_code(t) for t in first], np.int32)
-        self.numel = np.array([t.numel() for t in first], np.int64)
+        self.numel = np.array(sizes, np.int64)
         self.host = self.numel.ctypes.data, self.dtype.ctypes.data
-        places = [t.data_ptr() for t in self.dst.tensors if t.numel()]
+        for name, table in (("grads", self.src),) if out is None else (("grads", self.src), ("out", self.dst)):
+            if [t.dtype for t in table.tensors] != types * self.P:
+                raise GarError(GAR_EDTYPE, f"{name}: a tensor is not of the type of the first worker's")
+            if [t.numel() for t in table.tensors] != sizes * self.P or not all([t.is_contiguous() for t in table.tensors]):
+                raise GarError(GAR_EINVAL, f"{name}: a tensor is not contiguous, or not of the size of the first worker's")
+        places = [p for p, n in zip(self.dst.array, sizes * self.P) if n]
         if len(set(places)) < len(places):
             raise GarError(GAR_EINVAL, "the same tensor stands twice in the lists: it would be scaled twice")
-        for name, table in (("grads", self.src), ("out", self.dst)):
-            for i, t in enumerate(table.tensors):
-                like = first[i % self.count]
-                if t.dtype != like.dtype:
-                    raise GarError(GAR_EDTYPE, f"{name}: tensor {i % self.count} is {t.dtype}, not {like.dtype}")
-                if t.numel() != like.numel() or not t.is_contiguous():
-                    raise GarError(GAR_EINVAL, f"{name}: tensor {i % self.count} is not contiguous, or not of {like.numel()} elements")
 
     def _table(self, rows, name):
         if not 1 <= self.P <= GAR_MAX_WORKERS or len(rows) != self.P or any(len(r) != self.count for r in rows):
