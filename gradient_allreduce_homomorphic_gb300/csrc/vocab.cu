@@ -75,7 +75,7 @@ struct VocabParams {
     int64_t first, cols;  // the piece's columns
     const int32_t *target;
     const float *weight, *lse;
-    float2 *stats;       // [rows][2 runs]: maximum (times log2 e), sum
+    float2 *stats;       // [rows][2 runs]: maximum, sum
     float *at_target;    // [rows]
     void *out;           // dw or dx
     const void *addend;
@@ -97,7 +97,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 // Whether a row counts: a weight, and a target of the vocabulary.
 __device__ __forceinline__ bool counts(const int32_t *target, const float *weight, int64_t vocab, int64_t t) {
@@ -168,15 +168,14 @@ __device__ __forceinline__ void store_columns(const float (&v)[32], T *d, int64_
 struct Row {
     float top, sum;            // kLoss
     int32_t target;            // -1: the row does not count (gradient), or has none
-    float lse, lse2, weight;   // kGradient; lse2: times log2 e
+    float lse, weight;         // kGradient
 };
 
 // 32 logits of a row (vocabulary columns col ..) into its running maximum and sum.
 // They never leave registers within a run, and a lane is a row, so no lane asks
 // another.
-// Powers are of two, their exponents one fma each: z log2(e) less the maximum's,
-// whose rounding is the same in every term and in what is written, so that it
-// drops out.
+// Exponents are formed from z - maximum, not from z log2(e) in one fma: a loss near
+// 0 (the target's logit is the maximum, the rest far below) keeps its digits.
 __device__ __forceinline__ void take_logits(const VocabParams &p, float (&v)[32], Row &r, int64_t t, int64_t col) {
     if (col + 32 > p.vocab) {
 #pragma unroll
@@ -194,21 +193,20 @@ __device__ __forceinline__ void take_logits(const VocabParams &p, float (&v)[32]
     float m[4] = {r.top, v[0], v[1], v[2]};
 #pragma unroll
     for (int j = 3; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], v[j]);
-    const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), low = -top * kLog2e;
-    float s[4] = {r.sum * exp2_fast(fmaf(r.top, kLog2e, low)), 0.0f, 0.0f, 0.0f};
+    const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    float s[4] = {r.sum * exp2_fast((r.top - top) * kLog2e), 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) s[j & 3] += exp2_fast(fmaf(v[j], kLog2e, low));
+    for (int j = 0; j < 32; ++j) s[j & 3] += exp2_fast((v[j] - top) * kLog2e);
     r.top = top, r.sum = (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 // The same logits to g (col counts from the piece's first column), as bf16 pairs:
-// to `low` what `high` leaves of an fp32 value.  A bf16 g's exponent is one fma, which
-// may put 2^-24 of lse's size into it; that of a g of two parts is formed from z - lse.
+// to `low` what `high` leaves of an fp32 value.
 template <bool kTwoParts>
 __device__ __forceinline__ void give_gradient(const VocabParams &p, float (&v)[32], const Row &r, int64_t col, uint32_t (&high)[16],
                                               uint32_t (&low)[16]) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = exp2_fast(kTwoParts ? (v[j] - r.lse) * kLog2e : fmaf(v[j], kLog2e, -r.lse2));
+    for (int j = 0; j < 32; ++j) v[j] = exp2_fast((v[j] - r.lse) * kLog2e);
     const int64_t at = r.target - p.first - col;
     if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {
 #pragma unroll
@@ -356,6 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init_fence();
     }
     if (warp == 1) tmem_alloc<2>(smem_u32(&tmem_slot), 512);
+    if (warp == 2 && lane == 0) {  // parameters, not global memory: ahead of the wait
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
+        if (kMode == kGradient || kMode == kWeights) tma_prefetch_map(&map_c), tma_prefetch_map(&map_d);
+    }
     tc_fence_before();
     __syncthreads();
     cluster_barrier();
@@ -364,8 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = tmem_slot;
 
     if (warp == 0 && lane == 0) {
-        tma_prefetch_map(&map_a);
-        tma_prefetch_map(&map_b);
         const uint32_t lead_full = cluster_map(full, 0);
         uint32_t s = 0, turn = 1;  // the first turn finds every stage free
         int issued = 0;
@@ -454,11 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int64_t i = first; i < items; i += step) {
             const Item it = item_of(p, i);
             const int64_t lane_at = it.m * kTile + 128 * rank + quarter * 32 + lane;
-            Row r{-FLT_MAX / 2, 0.0f, -1, 0.0f, 0.0f, 0.0f};
+            Row r{-FLT_MAX, 0.0f, -1, 0.0f, 0.0f};
             if (kMode == kLoss && lane_at < p.rows) r.target = p.target[lane_at];
             if (kMode == kGradient && lane_at < p.rows && counts(p.target, p.weight, p.vocab, lane_at)) {
                 r.target = p.target[lane_at];
-                r.lse = p.lse[lane_at], r.lse2 = r.lse * kLog2e, r.weight = p.weight ? p.weight[lane_at] : 1.0f;
+                r.lse = p.lse[lane_at], r.weight = p.weight ? p.weight[lane_at] : 1.0f;
             }
             // dw: the pieces that are added to the tile of batch j: the addend's, or of the sum so far
             uint4 pieces[kTilePieces<T>];
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (kMode == kLoss && lane_at < p.rows)
-                p.stats[(lane_at * p.runs + it.run) * 2 + half] = make_float2(r.top * kLog2e, r.sum);
+                p.stats[(lane_at * p.runs + it.run) * 2 + half] = make_float2(r.top, r.sum);
         }
         if ((kMode == kGradient || kMode == kWeights) && lane == 0) tma_store_wait();
     }
@@ -624,20 +625,20 @@ __global__ void __launch_bounds__(256) vocab_join_kernel(const __grid_constant__
     for (int i = lane; i < 2 * p.runs; i += 32) {
         const float2 q = of[i];
         const float m = fmaxf(top, q.x);
-        sum = sum * exp2_fast(top - m) + q.y * exp2_fast(q.x - m);
+        sum = sum * exp2_fast((top - m) * kLog2e) + q.y * exp2_fast((q.x - m) * kLog2e);
         top = m;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float other = __shfl_xor_sync(0xFFFFFFFFu, top, o), more = __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         const float m = fmaxf(top, other);
-        sum = sum * exp2_fast(top - m) + more * exp2_fast(other - m);
+        sum = sum * exp2_fast((top - m) * kLog2e) + more * exp2_fast((other - m) * kLog2e);
         top = m;
     }
     if (lane == 0) {
-        const float log_sum = log2f(sum);
-        lse[t] = (top + log_sum) * kLn2;
-        loss[t] = (fmaf(-p.at_target[t], kLog2e, top) + log_sum) * kLn2;
+        const float log_sum = logf(sum);
+        lse[t] = top + log_sum;
+        loss[t] = (top - p.at_target[t]) + log_sum;
     }
 }
 

@@ -243,6 +243,22 @@ def test_large_and_small_logits(env, scale):
     check(torch, g, Problem(torch, 200, 1500, 128, seed=7, scale=scale), torch.float32)
 
 
+def test_a_vocabulary_of_one_and_sure_targets(env):
+    """Loss and gradient 0 exactly where the target has all the probability, however large its logit."""
+    torch, g = env
+    p = Problem(torch, 40, 1, 64, seed=12, scale=30.0)
+    for t in run(torch, g, p, torch.bfloat16)[::2]:
+        assert bool((t == 0).all())
+    q = Problem(torch, 40, 300, 64, seed=12, masked=0.0, weighted=False)
+    q.w.zero_()
+    q.w[7] = 4.0
+    q.x.copy_(q.x.abs() + 1)  # z = 4 sum |x| + 256 for entry 7, 0 for all others
+    q.target.fill_(7)
+    loss, lse, dx, dw = run(torch, g, q, torch.float32)
+    assert bool((loss == 0).all()) and bool((dx == 0).all()) and bool((dw[7] == 0).all())
+    assert bool((lse == (q.x.double() @ q.w.double()[7]).float()).all())
+
+
 def test_rows_far_apart(env):
     """Offsets past 2^31 elements in w and dw."""
     torch, g = env
