@@ -811,8 +811,9 @@ size_t gar_vocab_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden, in
  *   loss_t = lse_t - z_{t, target_t}
  * A row counts if its target lies in [0, vocab) and its weight is not 0; any other
  * has loss 0 and lse 0, whatever its x.  A NaN or an infinity among a row's logits
- * makes its loss NaN.  fp32 sums in tensor-core order (rounding toward zero within
- * a product, 8e-7 of the result at hidden = 8192); the same bits in every run.
+ * makes its loss NaN.  Sums are fp32; the tensor cores' additions round toward zero
+ * (2e-6 of lse at hidden = 4096).  Exponents are formed from z less the maximum, so a
+ * loss near 0 keeps its digits.  The same bits in every run.
  *   x, w         device, [rows, hidden] and [vocab, hidden] bf16 (dtype: GAR_BF16),
  *                row strides ldx, ldw; 16-byte aligned, strides multiples of 8
  *   target       device, [rows] int32
@@ -831,8 +832,9 @@ int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t ldw, int32
  *   g_tv = weight_t (exp(z_tv - lse_t) - [v = target_t])   (0 where t does not count)
  *   dx = g w,   dw = g^T x + addend
  * The vocabulary is taken in pieces, their logits computed again.  g is rounded to
- * bf16 for the products; for an fp32 dw it is the sum of two bf16 values (2^-17 of
- * each g), at twice that product's cost.  Sums are fp32; of an fp32 dw none that
+ * bf16 for the products (a bf16 dx or dw is 2.4e-3 from the exact one in the 2-norm, its
+ * own rounding 1.7e-3 of it); for an fp32 dw it is the sum of two bf16 values (2^-17 of
+ * each g; 4e-6 in the 2-norm), at twice that product's cost.  Sums are fp32; of an fp32 dw none that
  * the tensor cores form is over more than 8192 terms.
  *   dx           device, out, [rows, hidden] bf16, row stride lddx, or NULL
  *   dw           device, out, [vocab, hidden] fp32 or bf16 (dw_type), row stride
