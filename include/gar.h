@@ -801,7 +801,8 @@ int gar_balance_loss(const void *const *z, int32_t P, int64_t tokens, int32_t ex
 
 /* Bytes of device workspace for gar_vocab_loss and gar_vocab_grad; dw_type: the
  * type of dw (GAR_BF16 where dw is not asked for).  The gradient's holds a piece
- * of the vocabulary's gradients, 256 MB of them at most (or rows x 256). */
+ * of the vocabulary's g, 256 MB of it at most (512 for an fp32 dw; or rows x 256),
+ * and where there are several the fp32 sums of dx. */
 size_t gar_vocab_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden, int32_t dw_type);
 
 /* gar_vocab_loss -- softmax cross entropy of a vocabulary layer whose logits are
