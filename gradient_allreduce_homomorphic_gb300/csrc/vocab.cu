@@ -27,11 +27,12 @@
 // nothing is transposed in memory.
 //
 // Bound by the tensor cores at the clock that the power limit leaves: 4096 x 16384
-// x 4096 the loss 299 us (1840 TFLOP/s, tensor pipe active in 97 % of the cycles,
-// SM clock 1.77 GHz of 2.07), logits and g 288, dw 283, dx 276 us (94 to 96 %); 4096 x
-// 131072 x 4096 loss and gradient 10.2 ms one after another (1725 TFLOP/s).  With few
-// rows bound by the read of w: the loss of 16 x 131072 x 1024 54 us (5.0 TB/s), of 64
-// x 32000 x 1024 18.7 us, 6 of them the kernel's beginning and end.
+// x 4096 the loss 303 us (1810 TFLOP/s, tensor pipe active in 97 % of the cycles,
+// SM clock 1.75 GHz of 2.07), logits and g 295, dw 288, dx 280 us (93 to 96 %); 4096 x
+// 131072 x 4096 loss and gradient 10.3 ms one after another (1710 TFLOP/s; 2.2 and 6.9
+// in short runs).  With few rows bound by the read of w: the loss of 16 x 131072 x 1024
+// 55 us (4.8 TB/s), of 64 x 32000 x 1024 18.9 us, 6 of them the kernel's beginning and
+// end.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
