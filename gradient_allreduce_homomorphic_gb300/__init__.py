@@ -1079,7 +1079,11 @@ class GradTables:
 
 
 def grad_tables(grads, out=None) -> GradTables:
-    return grads if isinstance(grads, GradTables) else GradTables(grads, out)
+    if isinstance(grads, GradTables):
+        if out is not None:
+            raise GarError(GAR_EINVAL, "the tables say where the clipped tensors go: out is for lists")
+        return grads
+    return GradTables(grads, out)
 
 
 def gar_grad_workspace_bytes(grads) -> int:
@@ -1098,8 +1102,8 @@ def gar_grad_norm(grads, norm, workspace, stream=None):
 
 def gar_grad_clip(grads, max_norm: float, norm, workspace, out=None, shared: bool = False, stream=None):
     """Each worker's gradients times min(1, max_norm / norm[w]), in place or to
-    out[w][i]; shared: by the norm of the first worker's, norm [1].  A norm that is
-    not finite leaves them as they are."""
+    out[w][i] (tables: to what they were built with); shared: by the norm of the
+    first worker's, norm [1].  A norm that is not finite leaves them as they are."""
     t = grad_tables(grads, out)
     _call("gar_grad_clip", t.src.array, t.dst.array, t.P, *t.host, t.count,
           1 if shared else 0, max_norm, _vector(norm, "norm", _float32(), 1 if shared else t.P), _dev(workspace),

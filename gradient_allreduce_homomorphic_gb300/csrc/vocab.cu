@@ -650,33 +650,34 @@ __global__ void __launch_bounds__(256) vocab_live_rows_kernel(const __grid_const
     copy_live_row(p, blockIdx.x, threadIdx.x, 256);
 }
 
-// The tiles of dx whose k was cut: the parts' sums added in order (6 us for 64 x
-// 1024 of 19 parts; HBM or L2 bound beyond).  A CTA: two rows
-// of x of a tile, a column to each thread.
+// The tiles of dx whose k was cut: the parts' sums added in order.  A CTA: four rows
+// of x of a tile, four columns to each thread.
 __global__ void __launch_bounds__(kTile) vocab_inputs_kernel(const __grid_constant__ VocabParams p) {
     let_next_begin();
     after_previous();
-    const int64_t tile = blockIdx.x / (p.tile_n / 2);
+    const int64_t tile = blockIdx.x / (p.tile_n / 4);
     Item it;
     place_item(p, p.items + tile, it);
-    const int64_t h = it.m * kTile + threadIdx.x, t0 = blockIdx.x % (p.tile_n / 2) * 2, t = it.n0 * p.tile_n + t0;
+    const int64_t at = threadIdx.x % 64 * 4, t0 = blockIdx.x % (p.tile_n / 4) * 4 + threadIdx.x / 64;
+    const int64_t h = it.m * kTile + at, t = it.n0 * p.tile_n + t0;
     if (h >= p.hidden || t >= p.rows) return;
-    const bool two = t + 1 < p.rows;
-    const float *of = p.part + (tile * kTile + t0) * kTile + threadIdx.x;
-    const int64_t stride = static_cast<int64_t>(p.rest) * kTile * kTile;
-    float a = 0.0f, b = 0.0f;
-#pragma unroll 16
+    const float4 *of = reinterpret_cast<const float4 *>(p.part + (tile * kTile + t0) * kTile + at);
+    const int64_t stride = static_cast<int64_t>(p.rest) * kTile * kTile / 4;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
     for (int i = 0; i < p.splits; ++i) {
-        a += of[i * stride];
-        if (two) b += of[i * stride + kTile];
+        const float4 a = of[i * stride];
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
     }
-    const auto give = [&](int64_t row, float v) {
-        if (p.first > 0) v += p.sum[row * p.hidden + h];
-        if (p.last) static_cast<uint16_t *>(p.out)[row * p.ld_out + h] = to_bf16(v);
-        else p.sum[row * p.hidden + h] = v;
-    };
-    give(t, a);
-    if (two) give(t + 1, b);
+    float *sum = p.sum + t * p.hidden + h;
+    uint16_t *out = static_cast<uint16_t *>(p.out) + t * p.ld_out + h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (h + i >= p.hidden) break;
+        if (p.first > 0) v[i] += sum[i];
+        if (!p.last) sum[i] = v[i];
+        else out[i] = to_bf16(v[i]);
+    }
 }
 
 // dw where no row is given: the addend, or 0.
@@ -950,7 +951,7 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
             lay_out(&q, 0, false);
             if (int rc = launch<kInputs, uint16_t>(q, w_mn, g_k, g_k, g_k, stream)) return rc;
             if (q.rest > 0)
-                if (int rc = launch_early("vocab_inputs_kernel", vocab_inputs_kernel, dim3(static_cast<unsigned>(q.rest * (q.tile_n / 2))), kTile, 0, 1,
+                if (int rc = launch_early("vocab_inputs_kernel", vocab_inputs_kernel, dim3(static_cast<unsigned>(q.rest * (q.tile_n / 4))), kTile, 0, 1,
                                           stream, q))
                     return rc;
         }

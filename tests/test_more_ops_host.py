@@ -277,6 +277,7 @@ def test_clip_binding(gar, binding):
     assert refused(gar.grad_tables, []) == refused(gar.grad_tables, [[tensor(3)], []]) == refused(gar.grad_tables, grads, out[:1]) == E
     assert refused(gar.grad_tables, grads, [[tensor(31), out[0][1]], out[1]]) == E
     assert refused(gar.grad_tables, [[tensor(4, 4)[:, ::2]]]) == E
+    assert refused(gar.gar_grad_clip, t, 1.0, norm, ws, out=out) == E
     same = tensor(8)
     assert refused(gar.grad_tables, [[same, same]]) == refused(gar.grad_tables, [[tensor(8)], [tensor(8)]], [[same], [same]]) == E
     gar.grad_tables([[same, same]], [[tensor(8), tensor(8)]])  # read twice, written apart
