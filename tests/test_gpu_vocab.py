@@ -354,3 +354,28 @@ def test_other_stream_and_captured_graph(env):
     for a, b in zip(want, (loss, lse, dx, dw)):
         assert torch.equal(a, b)
     assert np.isfinite(loss.sum().item())
+
+
+def test_two_calls_at_once(env):
+    """Calls on two streams, each with its workspace, beside 8-bit products on a third."""
+    torch, g = env
+    problems = [Problem(torch, 700, 9001, 256, seed=20), Problem(torch, 40, 30001, 512, seed=21)]
+    want = [run(torch, g, p, torch.float32) for p in problems]
+    a, sa = g.fp8_matrix(300, 2048)
+    b, sb = g.fp8_matrix(1000, 2048)
+    for m, s in ((a, sa), (b, sb)):
+        g.gar_fp8_quantize(torch.randn(m.shape, generator=problems[0].gen, device="cuda"), m, s)
+    product, other = torch.empty((300, 1000), device="cuda"), torch.empty((300, 1000), device="cuda")
+    g.gar_fp8_matmul(a, sa, b, sb, product)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    made = [(outputs(torch, p, torch.float32), workspace(torch, g, p, torch.float32)) for p in problems]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for p, (o, ws), s in zip(problems, made, streams):
+            g.gar_vocab_loss(p.x, p.w, p.target, o[0], o[1], ws, weight=p.weight, stream=s)
+            g.gar_vocab_grad(p.x, p.w, p.target, o[1], o[2], o[3], ws, weight=p.weight, stream=s)
+        g.gar_fp8_matmul(a, sa, b, sb, other, stream=streams[2])
+    torch.cuda.synchronize()
+    assert g.gar_sync_status() == 0 and torch.equal(product, other)
+    for w, (o, _) in zip(want, made):
+        assert all(torch.equal(x, y) for x, y in zip(w, o))
