@@ -7,8 +7,10 @@
 //   dx = g w,   dw = g^T x (+ addend)
 //
 // The loss is one pass of tensor-core tiles whose epilogue keeps, per row, the
-// running maximum and sum over a run of vocabulary tiles; the runs' pairs are
-// joined by a second, small kernel.  The gradient goes piece by piece of the
+// running maximum and sum of all logits but the target's over a run of vocabulary
+// tiles; the runs' pairs are joined by a second, small kernel.  With r the sum's
+// logarithm the loss is log(1 + exp(r - z[target])): near 0, where the target has
+// almost all of the probability, the rest is a sum of its own and keeps its digits.  The gradient goes piece by piece of the
 // vocabulary: the piece's logits again, g from them in the epilogue (bf16, in
 // the workspace), then the piece's rows of dw and its share of dx.  So a loss
 // and its gradient take four products where keeping the logits would take
@@ -167,16 +169,17 @@ __device__ __forceinline__ void store_columns(const float (&v)[32], T *d, int64_
 // A lane's row over an item: its running maximum and sum (loss), or what its
 // gradient takes.
 struct Row {
-    float top, sum;            // kLoss
+    float top, sum, low;       // kLoss: sum + low
     int32_t target;            // -1: the row does not count (gradient), or has none
     float lse, weight;         // kGradient
 };
 
-// 32 logits of a row (vocabulary columns col ..) into its running maximum and sum.
-// They never leave registers within a run, and a lane is a row, so no lane asks
-// another.
-// Exponents are formed from z - maximum, not from z log2(e) in one fma: a loss near
-// 0 (the target's logit is the maximum, the rest far below) keeps its digits.
+// 32 logits of a row (vocabulary columns col ..) into its running maximum and sum,
+// the target's apart.  They never leave registers within a run, and a lane is a row,
+// so no lane asks another.
+// Exponents are formed from z - maximum, not from z log2(e) in one fma, which would
+// lose digits with z.  A run may add thousands of batches, each of them less than half a
+// step of a sum that one large term has set: what an addition rounds away is kept (`low`).
 __device__ __forceinline__ void take_logits(const VocabParams &p, float (&v)[32], Row &r, int64_t t, int64_t col) {
     if (col + 32 > p.vocab) {
 #pragma unroll
@@ -190,15 +193,22 @@ __device__ __forceinline__ void take_logits(const VocabParams &p, float (&v)[32]
         for (int j = 0; j < 32; ++j)
             if (at == j) z = v[j];
         if (at >= 0 && at < 32) p.at_target[t] = z;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (at == j) v[j] = -INFINITY;
     }
     float m[4] = {r.top, v[0], v[1], v[2]};
 #pragma unroll
     for (int j = 3; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], v[j]);
     const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-    float s[4] = {r.sum * exp2_fast((r.top - top) * kLog2e), 0.0f, 0.0f, 0.0f};
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < 32; ++j) s[j & 3] += exp2_fast((v[j] - top) * kLog2e);
-    r.top = top, r.sum = (s[0] + s[1]) + (s[2] + s[3]);
+    const float batch = (s[0] + s[1]) + (s[2] + s[3]), scale = exp2_fast((r.top - top) * kLog2e), before = __fmul_rn(r.sum, scale);
+    const float sum = __fadd_rn(before, batch), added = __fsub_rn(sum, before);
+    const float lost = __fadd_rn(__fsub_rn(before, __fsub_rn(sum, added)), __fsub_rn(batch, added));  // exactly: sum + lost = before + batch
+    r.low = fmaf(r.low, scale, lost);
+    r.top = top, r.sum = sum;
 }
 
 // The same logits to g (col counts from the piece's first column), as bf16 pairs:
@@ -456,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int64_t i = first; i < items; i += step) {
             const Item it = item_of(p, i);
             const int64_t lane_at = it.m * kTile + 128 * rank + quarter * 32 + lane;
-            Row r{-FLT_MAX, 0.0f, -1, 0.0f, 0.0f};
+            Row r{-FLT_MAX, 0.0f, 0.0f, -1, 0.0f, 0.0f};
             if (kMode == kLoss && lane_at < p.rows) r.target = p.target[lane_at];
             if (kMode == kGradient && lane_at < p.rows && counts(p.target, p.weight, p.vocab, lane_at)) {
                 r.target = p.target[lane_at];
@@ -598,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (kMode == kLoss && lane_at < p.rows)
-                p.stats[(lane_at * p.runs + it.run) * 2 + half] = make_float2(r.top, r.sum);
+                p.stats[(lane_at * p.runs + it.run) * 2 + half] = make_float2(r.top, r.sum + r.low);
         }
         if ((kMode == kGradient || kMode == kWeights) && lane == 0) tma_store_wait();
     }
@@ -637,9 +647,11 @@ __global__ void __launch_bounds__(256) vocab_join_kernel(const __grid_constant__
         top = m;
     }
     if (lane == 0) {
-        const float log_sum = logf(sum);
-        lse[t] = top + log_sum;
-        loss[t] = (top - p.at_target[t]) + log_sum;
+        const float z = p.at_target[t], d = (top - z) + logf(sum);
+        float of_row = d > 0.0f ? d + log1pf(expf(-d)) : log1pf(expf(d));
+        float whole = z >= top ? z + of_row : top + logf(sum + expf(z - top));
+        if (!(z < INFINITY)) of_row = whole = z - z;  // NaN
+        loss[t] = of_row, lse[t] = whole;
     }
 }
 

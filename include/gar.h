@@ -813,8 +813,10 @@ size_t gar_vocab_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden, in
  * A row counts if its target lies in [0, vocab) and its weight is not 0; any other
  * has loss 0 and lse 0, whatever its x.  A NaN or an infinity among a row's logits
  * makes its loss NaN.  Sums are fp32; the tensor cores' additions round toward zero
- * (2e-6 of lse at hidden = 4096).  Exponents are formed from z less the maximum, so a
- * loss near 0 keeps its digits.  The same bits in every run.
+ * (2e-6 of lse at hidden = 4096).  The target's logit is kept apart from the sum over the
+ * others, r = log sum_{v != target} exp(z_tv), and loss_t = log(1 + exp(r - z_{t, target})):
+ * of a loss near 0 too the sums take no more than 1e-5 of itself, as far as the
+ * logits are exact.  The same bits in every run.
  *   x, w         device, [rows, hidden] and [vocab, hidden] bf16 (dtype: GAR_BF16),
  *                row strides ldx, ldw; 16-byte aligned, strides multiples of 8
  *   target       device, [rows] int32
