@@ -108,6 +108,8 @@ _SIGNATURES = {
     "gar_vocab_loss": (C.c_int, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, C.c_size_t, _vp]),
     "gar_vocab_grad": (C.c_int, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp,
                                  _i64, _i32, _vp, C.c_size_t, _vp]),
+    "gar_vocab_grad_with_loss": (C.c_int, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp,
+                                           _i64, _vp, _i64, _i32, _vp, C.c_size_t, _vp]),
     "gar_expert_rows": (_i64, [_i32, _i64, _i32, _i32, _i32, _i32]),
     "gar_expert_workspace_bytes": (C.c_size_t, [_i32, _i64, _i32, _i32]),
     "gar_expert_sort": (C.c_int, [_vp, _i32, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _vp, C.c_size_t, _vp]),
@@ -909,11 +911,7 @@ def gar_vocab_loss(x, w, target, loss, lse, workspace, weight=None, stream=None)
           _dev(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
 
 
-def gar_vocab_grad(x, w, target, lse, dx, dw, workspace, weight=None, addend=None, stream=None):
-    """The gradient of sum(weight * loss) from the lse of gar_vocab_loss: dx
-    [rows, hidden] bf16 and dw [vocab, hidden] fp32 or bf16 (either may be None);
-    addend, of dw's type, is added to dw (it may be dw)."""
-    rows, vocab, hidden, head = _vocab_args(x, w, target, weight)
+def _vocab_outputs(x, dx, dw, addend, rows, vocab, hidden, workspace, stream):
     dxp = dwp = ap = None
     lddx = lddw = lda = 0
     dw_type = GAR_BF16
@@ -928,8 +926,26 @@ def gar_vocab_grad(x, w, target, lse, dx, dw, workspace, weight=None, addend=Non
         if dw is None or addend.dtype != dw.dtype:
             raise GarError(GAR_EDTYPE, f"addend is {addend.dtype}, dw {None if dw is None else dw.dtype}")
         ap, lda = _matrix(addend, "addend", vocab, hidden)
-    _call("gar_vocab_grad", *head, _vector(lse, "lse", _FLOAT32, rows), dxp, lddx, ap, lda, dwp, lddw, dw_type,
-          _dev(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    return (dxp, lddx, ap, lda, dwp, lddw, dw_type, _dev(workspace), workspace.numel() * workspace.element_size(),
+            _stream(stream))
+
+
+def gar_vocab_grad(x, w, target, lse, dx, dw, workspace, weight=None, addend=None, stream=None):
+    """The gradient of sum(weight * loss) from the lse of gar_vocab_loss: dx
+    [rows, hidden] bf16 and dw [vocab, hidden] fp32 or bf16 (either may be None);
+    addend, of dw's type, is added to dw (it may be dw).  lse alone does not hold
+    the share of a target that is all but sure (gar_vocab_grad_with_loss)."""
+    rows, vocab, hidden, head = _vocab_args(x, w, target, weight)
+    tail = _vocab_outputs(x, dx, dw, addend, rows, vocab, hidden, workspace, stream)
+    _call("gar_vocab_grad", *head, _vector(lse, "lse", _FLOAT32, rows), *tail)
+
+
+def gar_vocab_grad_with_loss(x, w, target, loss, lse, dx, dw, workspace, weight=None, addend=None, stream=None):
+    """The same gradient from the loss and lse of gar_vocab_loss: each target's share
+    keeps its digits, however small its loss."""
+    rows, vocab, hidden, head = _vocab_args(x, w, target, weight)
+    tail = _vocab_outputs(x, dx, dw, addend, rows, vocab, hidden, workspace, stream)
+    _call("gar_vocab_grad_with_loss", *head, _vector(loss, "loss", _FLOAT32, rows), _vector(lse, "lse", _FLOAT32, rows), *tail)
 
 
 # ------------------------------------------- tokens to experts and back

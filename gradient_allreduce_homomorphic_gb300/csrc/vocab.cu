@@ -1,5 +1,5 @@
 // vocab.cu -- softmax cross entropy of a vocabulary layer without its logits:
-// gar_vocab_loss, gar_vocab_grad.
+// gar_vocab_loss, gar_vocab_grad, gar_vocab_grad_with_loss.
 //
 //   z[t][v] = sum_h x[t][h] w[v][h]              (bf16 operands, fp32 sums)
 //   lse[t]  = log sum_v exp z[t][v],  loss[t] = lse[t] - z[t][target[t]]
@@ -77,7 +77,7 @@ struct VocabParams {
     int64_t rows, hidden, vocab;
     int64_t first, cols;  // the piece's columns
     const int32_t *target;
-    const float *weight, *lse;
+    const float *weight, *loss, *lse;  // loss NULL: not given
     float2 *stats;       // [rows][2 runs]: maximum, sum
     float *at_target;    // [rows]
     void *out;           // dw or dx
@@ -172,6 +172,7 @@ struct Row {
     float top, sum, low;       // kLoss: sum + low
     int32_t target;            // -1: the row does not count (gradient), or has none
     float lse, weight;         // kGradient
+    float sure;                // p - 1 of the target
 };
 
 // 32 logits of a row (vocabulary columns col ..) into its running maximum and sum,
@@ -212,7 +213,9 @@ __device__ __forceinline__ void take_logits(const VocabParams &p, float (&v)[32]
 }
 
 // The same logits to g (col counts from the piece's first column), as bf16 pairs:
-// to `low` what `high` leaves of an fp32 value.
+// to `low` what `high` leaves of an fp32 value.  The target's p - 1 comes from its loss
+// where that is given, exp(-loss) - 1: formed from p, it would lose its digits where p is
+// near 1, and half a step of lse is as much (a target at 100, lse 100 + 4e-7: nothing left).
 template <bool kTwoParts>
 __device__ __forceinline__ void give_gradient(const VocabParams &p, float (&v)[32], const Row &r, int64_t col, uint32_t (&high)[16],
                                               uint32_t (&low)[16]) {
@@ -222,7 +225,7 @@ __device__ __forceinline__ void give_gradient(const VocabParams &p, float (&v)[3
     if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-            if (at == j) v[j] -= 1.0f;
+            if (at == j) v[j] = p.loss ? r.sure : v[j] - 1.0f;
     }
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= r.weight;
@@ -466,11 +469,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int64_t i = first; i < items; i += step) {
             const Item it = item_of(p, i);
             const int64_t lane_at = it.m * kTile + 128 * rank + quarter * 32 + lane;
-            Row r{-FLT_MAX, 0.0f, 0.0f, -1, 0.0f, 0.0f};
+            Row r{-FLT_MAX, 0.0f, 0.0f, -1, 0.0f, 0.0f, 0.0f};
             if (kMode == kLoss && lane_at < p.rows) r.target = p.target[lane_at];
             if (kMode == kGradient && lane_at < p.rows && counts(p.target, p.weight, p.vocab, lane_at)) {
                 r.target = p.target[lane_at];
                 r.lse = p.lse[lane_at], r.weight = p.weight ? p.weight[lane_at] : 1.0f;
+                if (p.loss) r.sure = expm1f(-p.loss[lane_at]);
             }
             // dw: the pieces that are added to the tile of batch j: the addend's, or of the sum so far
             uint4 pieces[kTilePieces<T>];
@@ -1017,10 +1021,10 @@ extern "C" int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t
                         loss, lse);
 }
 
-extern "C" int gar_vocab_grad(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target,
-                              const float *weight, int64_t rows, int64_t vocab, int64_t hidden, const float *lse, void *dx, int64_t lddx,
-                              const void *addend, int64_t ld_addend, void *dw, int64_t lddw, int32_t dw_type, void *d_workspace,
-                              size_t workspace_bytes, gar_stream_t stream_) {
+namespace {
+int vocab_grad(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target, const float *weight,
+               int64_t rows, int64_t vocab, int64_t hidden, const float *loss, const float *lse, void *dx, int64_t lddx, const void *addend,
+               int64_t ld_addend, void *dw, int64_t lddw, int32_t dw_type, void *d_workspace, size_t workspace_bytes, gar_stream_t stream_) {
     if (int rc = check(x, ldx, w, ldw, target, weight, rows, vocab, hidden, dtype)) return rc;
     const int size = elem_bytes(dw_type);
     if (size < 0) return fail(GAR_EDTYPE, "unknown dtype %d of dw", dw_type);
@@ -1047,7 +1051,7 @@ extern "C" int gar_vocab_grad(const void *x, int64_t ldx, const void *w, int64_t
     if (!aligned(dx, 2) || !aligned(lse, 4) || !aligned(d_workspace, 256)) return fail(GAR_EALIGN, "dx, lse or the workspace (256 bytes) is misaligned");
     VocabParams p{};
     p.rows = rows, p.vocab = vocab, p.hidden = hidden;
-    p.target = target, p.weight = weight, p.lse = lse;
+    p.target = target, p.weight = weight, p.loss = loss, p.lse = lse;
     p.status = device_status();
     const uint16_t *xh = static_cast<const uint16_t *>(x), *wh = static_cast<const uint16_t *>(w);
     uint16_t *dxh = static_cast<uint16_t *>(dx);
@@ -1056,4 +1060,23 @@ extern "C" int gar_vocab_grad(const void *x, int64_t ldx, const void *w, int64_t
                                                 static_cast<float *>(dw), lddw, ws, stream)
                               : gradient<uint16_t>(p, how, xh, ldx, wh, ldw, dxh, lddx, static_cast<const uint16_t *>(addend), ld_addend,
                                                    static_cast<uint16_t *>(dw), lddw, ws, stream);
+}
+}  // namespace
+
+extern "C" int gar_vocab_grad(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target,
+                              const float *weight, int64_t rows, int64_t vocab, int64_t hidden, const float *lse, void *dx, int64_t lddx,
+                              const void *addend, int64_t ld_addend, void *dw, int64_t lddw, int32_t dw_type, void *d_workspace,
+                              size_t workspace_bytes, gar_stream_t stream) {
+    return vocab_grad(x, ldx, w, ldw, dtype, target, weight, rows, vocab, hidden, nullptr, lse, dx, lddx, addend, ld_addend, dw, lddw,
+                      dw_type, d_workspace, workspace_bytes, stream);
+}
+
+extern "C" int gar_vocab_grad_with_loss(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target,
+                                        const float *weight, int64_t rows, int64_t vocab, int64_t hidden, const float *loss,
+                                        const float *lse, void *dx, int64_t lddx, const void *addend, int64_t ld_addend, void *dw,
+                                        int64_t lddw, int32_t dw_type, void *d_workspace, size_t workspace_bytes, gar_stream_t stream) {
+    if (rows > 0 && !loss) return fail(GAR_EINVAL, "loss is NULL");
+    if (!aligned(loss, 4)) return fail(GAR_EALIGN, "loss is misaligned");
+    return vocab_grad(x, ldx, w, ldw, dtype, target, weight, rows, vocab, hidden, loss, lse, dx, lddx, addend, ld_addend, dw, lddw,
+                      dw_type, d_workspace, workspace_bytes, stream);
 }

@@ -20,7 +20,7 @@ Per step:
   4. per worker: its tokens sorted by expert, their rows;        gar_expert_sort, gar_expert_gather
      per expert its rows' product; the rows back to the tokens   gar_fp8_quantize, gar_fp8_matmul
      with weights and X added (h, bf16)                          gar_expert_combine
-  5. per worker: the vocabulary layer's loss, its gradient       gar_vocab_loss, gar_vocab_grad
+  5. per worker: the vocabulary layer's loss, its gradient       gar_vocab_loss, gar_vocab_grad_with_loss
      over h (dX so far) and over W (fp32, into the worker's
      flat gradient buffer)
   6. per worker: the gradient over the rows and the weights;     gar_expert_combine_grad
@@ -42,8 +42,8 @@ import numpy as np
 
 from . import (fp8_matrix, gar_balance_loss, gar_balance_workspace_bytes, gar_expert_combine, gar_expert_combine_grad,
                gar_expert_gather, gar_expert_rows, gar_expert_sort, gar_expert_weights, gar_expert_weights_grad,
-               gar_expert_workspace_bytes, gar_fp8_matmul, gar_fp8_quantize, gar_vocab_grad, gar_vocab_loss,
-               gar_vocab_workspace_bytes, pointer_table)
+               gar_expert_workspace_bytes, gar_fp8_matmul, gar_fp8_quantize, gar_vocab_grad_with_loss,
+               gar_vocab_loss, gar_vocab_workspace_bytes, pointer_table)
 from .pipeline import AveragingStep, flat_offsets
 
 
@@ -153,8 +153,8 @@ class LanguageStep:
                 gar_fp8_matmul(*self.rows8[e][:2], *self.expert8[e][:2], self.ys[at])
             gar_expert_combine(self.ys, position, [self.h[w]], weight=share, addend=[hidden[w]])
             gar_vocab_loss(self.h[w], self.head, target[w], self.loss[w], self.lse[w], self.workspace, weight=weight[w])
-            gar_vocab_grad(self.h[w], self.head, target[w], self.lse[w], self.dx[w], self.head_grad[w], self.workspace,
-                           weight=weight[w])
+            gar_vocab_grad_with_loss(self.h[w], self.head, target[w], self.loss[w], self.lse[w], self.dx[w], self.head_grad[w],
+                                     self.workspace, weight=weight[w])
             gar_expert_combine_grad([self.dx[w]], self.ys, position, self.source, share, self.ys, dshare)  # over the rows
             for e, at in enumerate(rows):
                 gar_fp8_quantize(self.ys[at], drows, drows_s, drows_t, drows_ts)

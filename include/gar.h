@@ -845,11 +845,23 @@ int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t ldw, int32
  *   addend       device, of dw's type, added before the rounding; NULL: none; may
  *                be dw (same row stride)
  * A row that did not count when lse was written must not count now.  Outputs must
- * not overlap x, w or one another.  With no rows dw is the addend or 0.  Other arguments and errors as for gar_vocab_loss. */
+ * not overlap x, w or one another.  With no rows dw is the addend or 0.  Other arguments and errors as for gar_vocab_loss.
+ * exp(z - lse) is off by what lse's own rounding leaves, 2^-24 |lse| of itself (4e-6 at
+ * 64 .. 128).  Of the target's g that is not a part of it but of 1: a sure target's, its
+ * loss near 0, loses its digits, and one of 1e-6 is lost at an lse near 100.
+ * gar_vocab_grad_with_loss keeps them. */
 int gar_vocab_grad(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target,
                    const float *weight, int64_t rows, int64_t vocab, int64_t hidden, const float *lse, void *dx, int64_t lddx,
                    const void *addend, int64_t ld_addend, void *dw, int64_t lddw, int32_t dw_type, void *d_workspace,
                    size_t workspace_bytes, gar_stream_t stream);
+
+/* gar_vocab_grad_with_loss -- the same gradient, from the losses too, so that the
+ * target's g, -weight_t (1 - exp(-loss_t)), keeps its digits also where the target is all but sure.
+ *   loss         device, [rows] fp32, what gar_vocab_loss wrote beside lse */
+int gar_vocab_grad_with_loss(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target,
+                             const float *weight, int64_t rows, int64_t vocab, int64_t hidden, const float *loss, const float *lse,
+                             void *dx, int64_t lddx, const void *addend, int64_t ld_addend, void *dw, int64_t lddw, int32_t dw_type,
+                             void *d_workspace, size_t workspace_bytes, gar_stream_t stream);
 
 /* Tokens sorted by the experts that a router chose, and back.  A pair is one of
  * the k choices of one token of one worker, numbered (w tokens + t) k + j; P tokens

@@ -9,7 +9,10 @@ Tolerances, u = 2^-24:
          30 joins of pairs at most, 7 u each: under 260 u
   d      its logarithm (2 u of it), the maxima's difference and their sum: 4 u |d|
   loss   log1p(exp(d)): relative to exp(d) the above and 8 u; no more of the loss
-  lse    the loss's absolute error or the above, and 2 u of itself"""
+  g      of the target: the loss's, and 8 u for exp(-loss) - 1 and its weight; of the others:
+         lse's absolute error, its rounding u |lse|, 2^-22 and 4 u log2(e) |z - lse|
+  dw     g as two bf16 values 2^-16, 2 u a term of the sum (2 for each row)
+  dx     g as a bf16 value and the result 2^-8, 2 u a term of the sum  lse    the loss's absolute error or the above, and 2 u of itself"""
 import math
 
 import pytest
@@ -79,3 +82,57 @@ def test_a_sure_mistake(env, rows):
     want = whole - z[9].item()
     assert (lse.double() - whole).abs().max().item() <= 260 * U + 4 * U * whole
     assert (loss.double() - want).abs().max().item() <= 260 * U + 8 * U * want
+
+
+@pytest.mark.parametrize("dw_type", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 300])
+@pytest.mark.parametrize("sure,others,vocab", CASES)
+def test_gradients_of_sure_targets(env, sure, others, vocab, rows, dw_type):
+    """The target's share, of 1e-7 to 1e-2, and with it g's sum of 0 over the vocabulary."""
+    torch, g = env
+    x, w, z, rest = problem(torch, rows, sure, others, vocab)
+    target, loss, lse, ws = loss_of(torch, g, x, w, 7)
+    weight = torch.full((rows,), 1.0 / 1024, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty(w.shape, dtype=torch.float32 if dw_type == "f32" else torch.bfloat16, device="cuda")
+    g.gar_vocab_grad_with_loss(x, w, target, loss, lse, dx, dw, ws, weight=weight)
+    torch.cuda.synchronize()
+    d = rest - z[7].item()
+    want_loss = math.log1p(math.exp(d))
+    want = torch.exp(z - (z[7] + want_loss)) / 1024
+    want[7] = math.expm1(-want_loss) / 1024
+    of_loss = (260 + 4 * abs(d) + 2 * math.log(vocab) + 8) * U
+    rel = torch.full_like(z, of_loss * want_loss + 2 * U * (z[7].item() + want_loss) + 2 ** -22)
+    rel += 4 * U * 1.4426950408889634 * (z - z[7] - want_loss).abs() + 4 * U
+    rel[7] = of_loss + 8 * U
+    parts, half = (2 ** -16, U) if dw_type == "f32" else (2 ** -8, 2 ** -8)
+    got = dw[:, 0].double()
+    assert ((got - rows * want).abs() <= 1.02 * (rel + parts + half + 4 * U * rows) * rows * want.abs()).all()
+    tol = ((1.02 * rel + 2 ** -8 + 2 * U * vocab) * want.abs()) @ w.double().abs() * 1.02
+    want_dx = want @ w.double()
+    assert ((dx.double() - want_dx).abs() <= tol + 2 ** -8 * want_dx.abs()).all()
+
+
+def test_losses_given_or_not(env):
+    """Where no target is sure the losses change nothing but the target's entry, by lse's rounding; rows that do not
+    count and NaN among the losses stay theirs."""
+    torch, g = env
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    x = torch.randn((200, 96), generator=gen, device="cuda").bfloat16()
+    w = (torch.randn((1000, 96), generator=gen, device="cuda") * 0.2).bfloat16()
+    target = torch.randint(0, 1000, (200,), generator=gen, device="cuda").int()
+    target[::7] = -100
+    x[5] = float("inf")
+    loss, lse = torch.empty(200, device="cuda"), torch.empty(200, device="cuda")
+    ws = torch.empty(g.gar_vocab_workspace_bytes(200, 1000, 96, torch.bfloat16), dtype=torch.uint8, device="cuda")
+    g.gar_vocab_loss(x, w, target, loss, lse, ws)
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    g.gar_vocab_grad(x, w, target, lse, a, None, ws)
+    g.gar_vocab_grad_with_loss(x, w, target, loss, lse, b, None, ws)
+    torch.cuda.synchronize()
+    assert bool((b[::7] == 0).all()) and bool(b[5].isnan().all()) and bool(loss[5].isnan())
+    rest = torch.arange(200, device="cuda") != 5
+    g64 = torch.softmax(x[rest].double() @ w.double().t(), 1)
+    g64.scatter_add_(1, target[rest].clamp(min=0).long()[:, None], -torch.ones((199, 1), dtype=torch.float64, device="cuda"))
+    size = g64.abs() @ w.double().abs()  # both: g's rounding and the result's, sums, and lse's error far below them
+    assert ((a[rest].double() - b[rest].double()).abs() <= (4 * 2 ** -8 + 1e-3) * size).all()
