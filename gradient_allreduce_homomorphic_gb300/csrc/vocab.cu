@@ -59,6 +59,9 @@ constexpr int kShared = 224 * 1024, kSmem = 1024 + kShared;
 constexpr int kSegment = 8192 / kK;
 
 enum { kLoss, kGradient, kWeights, kInputs };
+// A gradient with its losses given is a kernel of its own: the load among the exponents costs 32 registers, and the
+// bf16 gradient of 4096 x 131072 x 64 without it 831 us instead of 845.
+enum { kPlain, kSure };
 
 struct VocabParams {
     int64_t items;       // whole tiles or runs, handed out in order
@@ -172,7 +175,6 @@ struct Row {
     float top, sum, low;       // kLoss: sum + low
     int32_t target;            // -1: the row does not count (gradient), or has none
     float lse, weight;         // kGradient
-    float sure;                // p - 1 of the target
 };
 
 // 32 logits of a row (vocabulary columns col ..) into its running maximum and sum,
@@ -216,16 +218,23 @@ __device__ __forceinline__ void take_logits(const VocabParams &p, float (&v)[32]
 // to `low` what `high` leaves of an fp32 value.  The target's p - 1 comes from its loss
 // where that is given, exp(-loss) - 1: formed from p, it would lose its digits where p is
 // near 1, and half a step of lse is as much (a target at 100, lse 100 + 4e-7: nothing left).
-template <bool kTwoParts>
-__device__ __forceinline__ void give_gradient(const VocabParams &p, float (&v)[32], const Row &r, int64_t col, uint32_t (&high)[16],
-                                              uint32_t (&low)[16]) {
+template <bool kTwoParts, int kForm>
+__device__ __forceinline__ void give_gradient(const VocabParams &p, float (&v)[32], const Row &r, int64_t t, int64_t col,
+                                              uint32_t (&high)[16], uint32_t (&low)[16]) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = exp2_fast((v[j] - r.lse) * kLog2e);
     const int64_t at = r.target - p.first - col;
-    if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {
+    if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {  // once for a row
+        if (kForm == kSure) {
+            const float sure = at >= 0 && at < 32 ? expm1f(-p.loss[t]) : 0.0f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (at == j) v[j] = p.loss ? r.sure : v[j] - 1.0f;
+            for (int j = 0; j < 32; ++j)
+                if (at == j) v[j] = sure;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (at == j) v[j] -= 1.0f;
+        }
     }
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= r.weight;
@@ -333,7 +342,7 @@ __device__ __forceinline__ void copy_live_row(const VocabParams &p, int64_t t, i
     for (int64_t h = pieces * 8 + thread; h < p.ld_live; h += threads) to[h] = live && h < p.hidden ? from[h] : 0;
 }
 
-template <int kMode, typename T>
+template <int kMode, typename T, int kForm = kPlain>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                          const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_d,
@@ -469,12 +478,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int64_t i = first; i < items; i += step) {
             const Item it = item_of(p, i);
             const int64_t lane_at = it.m * kTile + 128 * rank + quarter * 32 + lane;
-            Row r{-FLT_MAX, 0.0f, 0.0f, -1, 0.0f, 0.0f, 0.0f};
+            Row r{-FLT_MAX, 0.0f, 0.0f, -1, 0.0f, 0.0f};
             if (kMode == kLoss && lane_at < p.rows) r.target = p.target[lane_at];
             if (kMode == kGradient && lane_at < p.rows && counts(p.target, p.weight, p.vocab, lane_at)) {
                 r.target = p.target[lane_at];
                 r.lse = p.lse[lane_at], r.weight = p.weight ? p.weight[lane_at] : 1.0f;
-                if (p.loss) r.sure = expm1f(-p.loss[lane_at]);
             }
             // dw: the pieces that are added to the tile of batch j: the addend's, or of the sum so far
             uint4 pieces[kTilePieces<T>];
@@ -515,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (!on) continue;
                                 uint32_t w[16], none[16];
                                 if (kMode == kGradient) {
-                                    give_gradient<false>(p, v, r, col + u * 32, w, none);
+                                    give_gradient<false, kForm>(p, v, r, lane_at, col + u * 32, w, none);
                                 } else {
 #pragma unroll
                                     for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
@@ -553,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else if (kMode == kGradient) {
                             if (lane_at - lane >= p.rows || col >= p.cols) continue;  // all lanes: no row, or no column, of theirs
                             uint32_t high[16], low[16];
-                            give_gradient<kTwoParts>(p, v, r, col, high, low);
+                            give_gradient<kTwoParts, kForm>(p, v, r, lane_at, col, high, low);
                             if (lane == 0) tma_store_wait_read<0>();
                             __syncwarp();
                             stage_row(staging, lane, high);
@@ -709,7 +717,7 @@ __global__ void __launch_bounds__(256) vocab_no_rows_kernel(const T *addend, int
 
 // ---------------------------------------------------------------------- host
 // Pairs of CTAs that the device holds at one time; looked up once.  < 1: an error, reported.
-template <int kMode, typename T>
+template <int kMode, typename T, int kForm>
 int resident_pairs() {
     static std::atomic<int> known[64];
     int dev = 0;
@@ -726,20 +734,20 @@ int resident_pairs() {
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        cudaError_t e = cudaFuncSetAttribute(vocab_product_kernel<kMode, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&pairs, vocab_product_kernel<kMode, T>, &cfg);
+        cudaError_t e = cudaFuncSetAttribute(vocab_product_kernel<kMode, T, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&pairs, vocab_product_kernel<kMode, T, kForm>, &cfg);
         if (e != cudaSuccess || pairs < 1) return fail(GAR_ECUDA, "vocab_product_kernel: %s", cudaGetErrorString(e));
         known[dev & 63].store(pairs, std::memory_order_relaxed);
     }
     return pairs;
 }
 
-template <int kMode, typename T>
+template <int kMode, typename T, int kForm = kPlain>
 int launch(const VocabParams &p, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &c, const CUtensorMap &d, cudaStream_t stream) {
-    const int resident = resident_pairs<kMode, T>();
+    const int resident = resident_pairs<kMode, T, kForm>();
     if (resident < 1) return resident;
     const int64_t pairs = std::min(p.items + static_cast<int64_t>(p.rest) * p.splits, static_cast<int64_t>(resident));
-    return launch_early("vocab_product_kernel", vocab_product_kernel<kMode, T>, dim3(2 * static_cast<unsigned>(pairs)), kThreads, kSmem, 2,
+    return launch_early("vocab_product_kernel", vocab_product_kernel<kMode, T, kForm>, dim3(2 * static_cast<unsigned>(pairs)), kThreads, kSmem, 2,
                         stream, a, b, c, d, p);
 }
 
@@ -934,7 +942,9 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
             if (int rc = encode(&w_k, w + first * ldw, hidden, cols, ldw, q.tile_n / 2)) return rc;
             lay_out(&q, rows, true);
             if (dw && !copied && first == 0) q.x = x, q.ldx = ldx, q.live = live, q.ld_live = ld_live;
-            if (int rc = launch<kGradient, T>(q, rows_k, w_k, g_to, low_to, stream)) return rc;
+            if (int rc = q.loss ? launch<kGradient, T, kSure>(q, rows_k, w_k, g_to, low_to, stream)
+                                : launch<kGradient, T>(q, rows_k, w_k, g_to, low_to, stream))
+                return rc;
         }
         if (dw) {
             CUtensorMap to{};
