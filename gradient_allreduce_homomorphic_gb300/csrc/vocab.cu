@@ -189,16 +189,14 @@ __device__ __forceinline__ void take_logits(const VocabParams &p, float (&v)[32]
         for (int j = 0; j < 32; ++j)
             if (col + j >= p.vocab) v[j] = -INFINITY;
     }
-    const int64_t at = r.target - col;
-    if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {
+    const int64_t behind = r.target - col;
+    const int at = behind >= 0 && behind < 32 ? static_cast<int>(behind) : -1;
+    if (__any_sync(0xFFFFFFFFu, at >= 0)) {
         float z = 0.0f;
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-            if (at == j) z = v[j];
-        if (at >= 0 && at < 32) p.at_target[t] = z;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (at == j) v[j] = -INFINITY;
+            if (at == j) z = v[j], v[j] = -INFINITY;
+        if (at >= 0) p.at_target[t] = z;
     }
     float m[4] = {r.top, v[0], v[1], v[2]};
 #pragma unroll
