@@ -47,6 +47,13 @@
 namespace gar {
 namespace {
 
+enum { kLoss, kGradient, kWeights, kInputs };
+// A gradient with its losses given is a kernel of its own: the load among the exponents costs 32 registers, and the
+// bf16 gradient of 4096 x 131072 x 64 without it 831 us instead of 845.  So are the products whose sums are longer than a
+// segment: the products of a tile all go to one accumulator, the sum of its segments so far lies in the place of the
+// other, and no epilogue overlaps the next products.
+enum { kPlain, kSure, kLong };
+
 constexpr int kTile = 256;    // rows of a pair's tile, and its columns at most
 constexpr int kK = 64;        // k per chunk: one swizzled line of bf16
 constexpr int kMaxStages = 16;
@@ -54,14 +61,14 @@ constexpr int kOperand = 128 * kK * 2;  // bytes of 128 rows of an operand of a 
 constexpr int kThreads = 320;  // warp 0 loads, warp 1 issues products, warps 2-9 epilogue
 constexpr int kStaging = 8 * 4096;  // for each epilogue warp a tile of 32 x 64 bf16, two of 32 x 32, or one of 32 x 32 fp32
 constexpr int kShared = 224 * 1024, kSmem = 1024 + kShared;
-// Chunks that an accumulator adds at most for an fp32 result: the tensor core's additions round toward zero, so a sum's
-// error grows with its length (8e-7 of the result at 8192 k).
-constexpr int kSegment = 8192 / kK;
+// Chunks that an accumulator adds at most.  The tensor core's additions round toward zero, so the error of a sum of
+// one sign grows with its length: 3e-5 of it at 8192 k, which an fp32 dw and logits are held to, 1.6e-4 at 32768, beside
+// the 2e-3 of bf16's own rounding (uncut: lse 6e-3 at 2^20 k, a bf16 dw of 4M rows 2.6e-2).  Longer sums are added up by
+// the epilogue: those of an fp32 dw in dw itself, the others in tensor memory (kLong: loss of 2048 x 32000 x 16384 1270 us,
+// 1170 uncut; its bf16 gradient within 2 % of uncut).
+template <int kMode, typename T>
+constexpr int kSegment = (kMode == kInputs || (kMode == kWeights && sizeof(T) == 2) ? 32768 : 8192) / kK;
 
-enum { kLoss, kGradient, kWeights, kInputs };
-// A gradient with its losses given is a kernel of its own: the load among the exponents costs 32 registers, and the
-// bf16 gradient of 4096 x 131072 x 64 without it 831 us instead of 845.
-enum { kPlain, kSure };
 
 struct VocabParams {
     int64_t items;       // whole tiles or runs, handed out in order
@@ -223,7 +230,7 @@ __device__ __forceinline__ void give_gradient(const VocabParams &p, float (&v)[3
     for (int j = 0; j < 32; ++j) v[j] = exp2_fast((v[j] - r.lse) * kLog2e);
     const int64_t at = r.target - p.first - col;
     if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {  // once for a row
-        if (kForm == kSure) {
+        if (kForm == kSure || (kForm == kLong && p.loss)) {
             const float sure = at >= 0 && at < 32 ? expm1f(-p.loss[t]) : 0.0f;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -340,7 +347,7 @@ __device__ __forceinline__ void copy_live_row(const VocabParams &p, int64_t t, i
     for (int64_t h = pieces * 8 + thread; h < p.ld_live; h += threads) to[h] = live && h < p.hidden ? from[h] : 0;
 }
 
-template <int kMode, typename T, int kForm = kPlain>
+template <int kMode, typename T, int kForm>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                          const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_d,
@@ -348,7 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool kMnA = kMode == kWeights || kMode == kInputs, kMnB = kMode == kWeights;
     // 16 k of a K-major operand are 32 bytes of each line; of an MN-major one two groups of eight lines of 128 bytes
     constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
-    const int seg_chunks = kMode == kWeights && sizeof(T) == 4 ? kSegment : 0x7FFFFFFF;
+    constexpr bool kThroughOut = kMode == kWeights && sizeof(T) == 4;  // segments are added up in dw itself
+    constexpr int seg_chunks = kThroughOut || kForm == kLong ? kSegment<kMode, T> : 0x7FFFFFFF;
+    constexpr uint32_t kBack = kForm == kLong ? 1 : 2;  // accumulators in use
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
     __shared__ uint32_t tmem_slot;
@@ -433,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int64_t n = it.n0; n < it.n1; ++n) {
                 for (int32_t c0 = it.c0; c0 < it.c1; ++seq) {
                     const int32_t c1 = it.c1 - c0 > seg_chunks ? c0 + seg_chunks : it.c1;
-                    const uint32_t acc = tmem + (seq & 1) * kTile;
-                    if (seq >= 2) mbar_wait_cluster(drained + 8 * (seq & 1), ((seq - 2) >> 1) & 1, &failed);
+                    const uint32_t acc = tmem + (kForm == kLong ? 0 : (seq & 1) * kTile);
+                    if (seq >= kBack) mbar_wait_cluster(drained + 8 * ((seq - kBack) & 1), ((seq - kBack) >> 1) & 1, &failed);
                     for (int32_t c = c0; c < c1; ++c) {
                         if (!ready) mbar_wait(full + 8 * s, turn, &failed);
                         tc_fence_after();
@@ -493,14 +502,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int64_t n = it.n0; n < it.n1; ++n) {
                 for (int32_t c0 = it.c0; c0 < it.c1; ++seq) {
                     const int32_t c1 = it.c1 - c0 > seg_chunks ? c0 + seg_chunks : it.c1;
-                    const uint32_t buf = seq & 1;
-                    if (kMode == kWeights && p.by_16) fetch_pieces(n, half, c0 > it.c0);
+                    const uint32_t buf = seq & 1, from = lanes + (kForm == kLong ? 0 : buf * kTile), so_far = lanes + kTile;
+                    const bool later = kThroughOut && c0 > it.c0;
+                    if (kMode == kWeights && p.by_16 && (kThroughOut || c1 == it.c1)) fetch_pieces(n, half, later);
                     mbar_wait(acc_full + 8 * buf, (seq >> 1) & 1, &failed);
                     __syncwarp();
                     tc_fence_after();
                     if (half >= batches) {  // a tile of 32 columns has none for the second warps
                         tc_fence_before();
                         if (lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
+                    }
+                    // 32 columns of the tile's sums
+                    const auto load_columns = [&](float (&v)[32], int column) {
+                        tc_load32(v, from + column);
+                        if (kForm == kLong && c0 > it.c0) {
+                            float more[32];
+                            tc_load32(more, so_far + column);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] += more[e];
+                        } else {
+                            tc_wait_ld();
+                        }
+                    };
+                    if (kForm == kLong && c1 < it.c1) {  // each column by the warp that takes the whole sum's
+#pragma unroll 1
+                        for (int j = 0; j < batches; ++j) {
+                            if (((wide ? j >> 1 : j) & 1) != half) continue;
+                            float v[32];
+                            load_columns(v, j * 32);
+                            tc_store32(so_far + j * 32, v);
+                        }
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (half < batches && lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
+                        c0 = c1;
+                        continue;
                     }
                     if (wide) {
 #pragma unroll 1
@@ -511,8 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int u = 0; u < 2; ++u) {
                                 __syncwarp();
                                 float v[32];
-                                tc_load32(v, lanes + buf * kTile + q * 64 + u * 32);
-                                tc_wait_ld();
+                                load_columns(v, q * 64 + u * 32);
                                 if (u == 1 && q + 2 >= batches / 2) {
                                     tc_fence_before();
                                     __syncwarp();
@@ -546,8 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = half; j < batches && !wide; j += 2) {
                         __syncwarp();
                         float v[32];
-                        tc_load32(v, lanes + buf * kTile + j * 32);
-                        tc_wait_ld();
+                        load_columns(v, j * 32);
                         if (j + 2 >= batches) {
                             tc_fence_before();
                             __syncwarp();
@@ -574,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else if (kMode == kWeights) {
                             const int64_t row0 = lane_at - lane, left = p.cols - row0;
                             if (left <= 0 || col >= p.hidden) continue;  // all lanes
-                            if (p.by_tma && c1 - c0 == it.c1 - it.c0) {
+                            if (p.by_tma && (!kThroughOut || c1 - c0 == it.c1 - it.c0)) {
                                 if (lane == 0) tma_store_wait_read<0>();
                                 __syncwarp();
                                 stage_row(staging, lane, v);
@@ -590,15 +626,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 uint4 mine[kTilePieces<T>];
 #pragma unroll
                                 for (int q = 0; q < kTilePieces<T>; ++q) mine[q] = pieces[q];
-                                if (j + 2 < batches) fetch_pieces(n, j + 2, c0 > it.c0);
+                                if (j + 2 < batches) fetch_pieces(n, j + 2, later);
                                 store_pieces(staging, lane, static_cast<T *>(p.out) + row0 * p.ld_out + col, p.ld_out, mine,
                                              left < 32 ? static_cast<int>(left) : 32, p.hidden - col);
                             } else {
                                 stage_row(staging, lane, v);
                                 __syncwarp();
                                 T *d = static_cast<T *>(p.out) + row0 * p.ld_out + col;
-                                const T *c = c0 > it.c0 ? d : p.addend ? static_cast<const T *>(p.addend) + row0 * p.ld_addend + col : nullptr;
-                                store_rows(staging, lane, d, p.ld_out, c, c0 > it.c0 ? p.ld_out : p.ld_addend, left < 32 ? static_cast<int>(left) : 32,
+                                const T *c = later ? d : p.addend ? static_cast<const T *>(p.addend) + row0 * p.ld_addend + col : nullptr;
+                                store_rows(staging, lane, d, p.ld_out, c, later ? p.ld_out : p.ld_addend, left < 32 ? static_cast<int>(left) : 32,
                                            col + lane < p.hidden);
                             }
                         } else if (const int64_t left = p.rows - col; lane_at < p.hidden && left > 0) {
@@ -740,13 +776,25 @@ int resident_pairs() {
     return pairs;
 }
 
-template <int kMode, typename T, int kForm = kPlain>
+template <int kMode, typename T, int kForm>
 int launch(const VocabParams &p, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &c, const CUtensorMap &d, cudaStream_t stream) {
     const int resident = resident_pairs<kMode, T, kForm>();
     if (resident < 1) return resident;
     const int64_t pairs = std::min(p.items + static_cast<int64_t>(p.rest) * p.splits, static_cast<int64_t>(resident));
     return launch_early("vocab_product_kernel", vocab_product_kernel<kMode, T, kForm>, dim3(2 * static_cast<unsigned>(pairs)), kThreads, kSmem, 2,
                         stream, a, b, c, d, p);
+}
+
+// The product by the kernel that its sums' length and (gradient) the losses ask for.
+template <int kMode, typename T>
+int launch_form(const VocabParams &p, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &c, const CUtensorMap &d,
+                cudaStream_t stream) {
+    const int64_t longest = p.items > 0 ? static_cast<int64_t>(p.chunks) * p.parts : ceil_div(p.chunks, int64_t{p.splits});
+    if constexpr (kMode != kWeights || sizeof(T) == 2)
+        if (longest > kSegment<kMode, T>) return launch<kMode, T, kLong>(p, a, b, c, d, stream);
+    if constexpr (kMode == kGradient)
+        if (p.loss) return launch<kMode, T, kSure>(p, a, b, c, d, stream);
+    return launch<kMode, T, kPlain>(p, a, b, c, d, stream);
 }
 
 // The stages of a product whose first operand has `rows` rows along its summed axis
@@ -940,9 +988,7 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
             if (int rc = encode(&w_k, w + first * ldw, hidden, cols, ldw, q.tile_n / 2)) return rc;
             lay_out(&q, rows, true);
             if (dw && !copied && first == 0) q.x = x, q.ldx = ldx, q.live = live, q.ld_live = ld_live;
-            if (int rc = q.loss ? launch<kGradient, T, kSure>(q, rows_k, w_k, g_to, low_to, stream)
-                                : launch<kGradient, T>(q, rows_k, w_k, g_to, low_to, stream))
-                return rc;
+            if (int rc = launch_form<kGradient, T>(q, rows_k, w_k, g_to, low_to, stream)) return rc;
         }
         if (dw) {
             CUtensorMap to{};
@@ -960,7 +1006,7 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
                     return rc;
             }
             lay_out(&q, 0, true);
-            if (int rc = launch<kWeights, T>(q, g_mn, live_mn, low_mn, to, stream)) return rc;
+            if (int rc = launch_form<kWeights, T>(q, g_mn, live_mn, low_mn, to, stream)) return rc;
         }
         if (dx) {
             CUtensorMap w_mn{}, g_k{};
@@ -973,7 +1019,7 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
             if (int rc = encode(&w_mn, w + first * ldw, hidden, cols, ldw, kK)) return rc;
             if (int rc = encode_tile_map(&g_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g, cols, rows, how.piece * 2, kK, q.tile_n / 2)) return rc;
             lay_out(&q, 0, false);
-            if (int rc = launch<kInputs, uint16_t>(q, w_mn, g_k, g_k, g_k, stream)) return rc;
+            if (int rc = launch_form<kInputs, uint16_t>(q, w_mn, g_k, g_k, g_k, stream)) return rc;
             if (q.rest > 0)
                 if (int rc = launch_early("vocab_inputs_kernel", vocab_inputs_kernel, dim3(static_cast<unsigned>(q.rest * (q.tile_n / 4))), kTile, 0, 1,
                                           stream, q))
@@ -1024,7 +1070,7 @@ extern "C" int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t
     lay_out(&p, rows, false);
     if (int rc = encode(&a, from, hidden, rows, ldx, p.a_rows)) return rc;
     if (int rc = encode(&b, w, hidden, vocab, ldw, p.tile_n / 2)) return rc;
-    if (int rc = launch<kLoss, float>(p, a, b, b, b, stream)) return rc;
+    if (int rc = launch_form<kLoss, float>(p, a, b, b, b, stream)) return rc;
     return launch_early("vocab_join_kernel", vocab_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, int64_t{8}))), 256, 0, 1, stream, p,
                         loss, lse);
 }

@@ -812,8 +812,10 @@ size_t gar_vocab_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden, in
  *   loss_t = lse_t - z_{t, target_t}
  * A row counts if its target lies in [0, vocab) and its weight is not 0; any other
  * has loss 0 and lse 0, whatever its x.  A NaN or an infinity among a row's logits
- * makes its loss NaN.  Sums are fp32; the tensor cores' additions round toward zero
- * (2e-6 of lse at hidden = 4096).  The target's logit is kept apart from the sum over the
+ * makes its loss NaN.  Sums are fp32; the tensor cores' additions round toward zero,
+ * so that a logit whose products are all of one sign is 1e-5 of itself too small at hidden =
+ * 4096 and 3e-5 from 8192 on, where it is the sum of several (2e-6 of lse at 4096 for
+ * products of both signs).  The target's logit is kept apart from the sum over the
  * others, r = log sum_{v != target} exp(z_tv), and loss_t = log(1 + exp(r - z_{t, target})):
  * of a loss near 0 too the sums take no more than 1e-5 of itself, as far as the
  * logits are exact.  The same bits in every run.
@@ -837,8 +839,9 @@ int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t ldw, int32
  * The vocabulary is taken in pieces, their logits computed again.  g is rounded to
  * bf16 for the products (a bf16 dx or dw is 2.4e-3 from the exact one in the 2-norm, its
  * own rounding 1.7e-3 of it); for an fp32 dw it is the sum of two bf16 values (2^-17 of
- * each g; 4e-6 in the 2-norm), at twice that product's cost.  Sums are fp32; of an fp32 dw none that
- * the tensor cores form is over more than 8192 terms.
+ * each g; 4e-6 in the 2-norm where g x has both signs), at twice that product's cost.  Sums are fp32,
+ * those that the tensor cores form over no more than 8192 terms of an fp32 dw (of one
+ * sign: 3e-5 of it too small) and 32768 of dx and a bf16 dw (1.6e-4).
  *   dx           device, out, [rows, hidden] bf16, row stride lddx, or NULL
  *   dw           device, out, [vocab, hidden] fp32 or bf16 (dw_type), row stride
  *                lddw, or NULL
