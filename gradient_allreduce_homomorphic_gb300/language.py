@@ -105,6 +105,7 @@ class LanguageStep:
         self.xs, self.ys = (torch.empty((rows, hidden), dtype=bf16, device=dev) for _ in range(2))
         self.h, self.dx = each(tokens, hidden, dtype=bf16), each(tokens, hidden, dtype=bf16)
         self.loss, self.lse = each(tokens), each(tokens)
+        self._even = torch.full((tokens,), 1.0 / max(tokens, 1), device=dev)  # the weights where none are given
         self.workspace = torch.empty(max(gar_balance_workspace_bytes(workers), gar_expert_workspace_bytes(1, tokens, k, E),
                                          gar_vocab_workspace_bytes(tokens, vocab, hidden, torch.float32)), dtype=torch.uint8,
                                      device=dev)
@@ -127,8 +128,6 @@ class LanguageStep:
         be finite: the 8-bit products meet them with zeros.  seed keys the
         compressed average's draws."""
         if weight is None:
-            if not hasattr(self, "_even"):
-                self._even = self.torch.full((self.tokens,), 1.0 / self.tokens, device=self.head.device)
             weight = [self._even] * self.P
         t, C = self._tables, self.capacity
         gar_fp8_quantize(self.router, *self.router8, square=True)
