@@ -79,6 +79,7 @@ class StudentStep:
         self.r = [torch.empty((tokens, experts), device=dev) for _ in range(workers)]
         self.loss = [torch.empty(tokens, device=dev) for _ in range(workers)]
         self.lse = torch.empty(tokens, device=dev)
+        self._even = torch.full((tokens,), 1.0 / max(tokens, 1), device=dev)  # the weights where none are given
         self.choice = [torch.empty((tokens, k), dtype=torch.int32, device=dev) for _ in range(workers)]
         self.counts = torch.empty((workers, experts), dtype=torch.int32, device=dev)
         self.balance = torch.empty(1, device=dev)
@@ -99,8 +100,6 @@ class StudentStep:
         None: 1 / tokens each); valid[w] [tokens] uint8, the tokens that the
         router counts (None: all).  seed keys the compressed average's draws."""
         if weight is None:
-            if not hasattr(self, "_even"):
-                self._even = self.torch.full((self.tokens,), 1.0 / self.tokens, device=self.head.device)
             weight = [self._even] * self.P
         gar_fp8_quantize(self.head, *self.head8, square=True)
         gar_fp8_quantize(self.router, *self.router8, square=True)

@@ -40,3 +40,14 @@ def test_language_step(env):
     captured_then_eager(torch, lambda: LanguageStep(head, router, experts, workers=2, tokens=200),
                         lambda s: s.run(5, hidden, target), lambda s: [*s.loss, *s.dx, *s.head_grad, *s.router_grad])
     assert g.gar_sync_status() == 0
+
+
+def test_student_step(env):
+    torch, g = env
+    import test_gpu_student
+    from gradient_allreduce_homomorphic_gb300.student import StudentStep
+
+    head, router, hidden, index, teacher = test_gpu_student.make(torch, 2, 150, 200, 900, 12, 8, 91)
+    captured_then_eager(torch, lambda: StudentStep(head, router, workers=2, tokens=150),
+                        lambda s: s.run(5, hidden, index, teacher), lambda s: [*s.loss, *s.dx, *s.head_grad, *s.router_grad])
+    assert g.gar_sync_status() == 0
