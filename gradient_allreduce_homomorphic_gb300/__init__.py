@@ -1067,13 +1067,14 @@ def gar_expert_weights_grad(weight, dweight, choice, dz, accumulate: bool = Fals
 # ------------------------------------------------- gradient norm, clipping
 class GradTables:
     """Host tables of P workers' gradient tensors, built once: grads[w][i], and the
-    tensors that the clipped ones go to (the same ones unless given)."""
+    tensors that the clipped ones go to (the same ones unless given).  With norm_only
+    they go nowhere (gar_grad_norm), and a tensor may stand in the lists more than once."""
 
-    def __init__(self, grads, out=None):
+    def __init__(self, grads, out=None, norm_only: bool = False):
         self.P = len(grads)
         self.count = len(grads[0]) if self.P else 0
         self.src = self._table(grads, "grads")
-        self.dst = self.src if out is None else self._table(out, "out")
+        self.dst = None if norm_only else self.src if out is None else self._table(out, "out")
         first = self.src.tensors[:self.count]
         types, sizes = [t.dtype for t in first], [t.numel() for t in first]
         self.dtype = np.array([_dtype_code(t) for t in first], np.int32)
@@ -1084,7 +1085,7 @@ class GradTables:
                 raise GarError(GAR_EDTYPE, f"{name}: a tensor is not of the type of the first worker's")
             if [t.numel() for t in table.tensors] != sizes * self.P or not all([t.is_contiguous() for t in table.tensors]):
                 raise GarError(GAR_EINVAL, f"{name}: a tensor is not contiguous, or not of the size of the first worker's")
-        places = [p for p, n in zip(self.dst.array, sizes * self.P) if n]
+        places = [] if norm_only else [p for p, n in zip(self.dst.array, sizes * self.P) if n]
         if len(set(places)) < len(places):
             raise GarError(GAR_EINVAL, "the same tensor stands twice in the lists: it would be scaled twice")
 
@@ -1094,23 +1095,21 @@ class GradTables:
         return PtrTable([t for r in rows for t in r])
 
 
-def grad_tables(grads, out=None) -> GradTables:
-    if isinstance(grads, GradTables):
-        if out is not None:
-            raise GarError(GAR_EINVAL, "the tables say where the clipped tensors go: out is for lists")
-        return grads
-    return GradTables(grads, out)
+def grad_tables(grads, out=None, norm_only: bool = False) -> GradTables:
+    if out is not None and (norm_only or isinstance(grads, GradTables)):
+        raise GarError(GAR_EINVAL, "out is for lists of tensors to be clipped: tables say where theirs go, a norm writes none")
+    return grads if isinstance(grads, GradTables) else GradTables(grads, out, norm_only)
 
 
 def gar_grad_workspace_bytes(grads) -> int:
-    t = grad_tables(grads)
+    t = grad_tables(grads, norm_only=True)
     return int(load().gar_grad_workspace_bytes(t.P, t.count))
 
 
 def gar_grad_norm(grads, norm, workspace, stream=None):
     """norm[w] = the 2-norm of worker w's gradient tensors grads[w][i] (lists, or
-    grad_tables), [P] fp32."""
-    t = grad_tables(grads)
+    grad_tables), [P] fp32.  A tensor that stands twice counts twice."""
+    t = grad_tables(grads, norm_only=True)
     _call("gar_grad_norm", t.src.array, t.P, *t.host, t.count,
           _vector(norm, "norm", _float32(), t.P), _dev(workspace), workspace.numel() * workspace.element_size(),
           _stream(stream))
@@ -1121,6 +1120,8 @@ def gar_grad_clip(grads, max_norm: float, norm, workspace, out=None, shared: boo
     out[w][i] (tables: to what they were built with); shared: by the norm of the
     first worker's, norm [1].  A norm that is not finite leaves them as they are."""
     t = grad_tables(grads, out)
+    if t.dst is None:
+        raise GarError(GAR_EINVAL, "the tables are for the norm alone")
     _call("gar_grad_clip", t.src.array, t.dst.array, t.P, *t.host, t.count,
           1 if shared else 0, max_norm, _vector(norm, "norm", _float32(), 1 if shared else t.P), _dev(workspace),
           workspace.numel() * workspace.element_size(), _stream(stream))
