@@ -733,10 +733,11 @@ int launch_weights(bool grad, const WeightParams &p, cudaStream_t stream) {
 using namespace gar;
 
 extern "C" int64_t gar_expert_rows(int32_t P, int64_t tokens, int32_t k, int32_t experts, int32_t align, int32_t capacity) {
-    if (P < 1 || P > GAR_MAX_WORKERS || tokens < 0 || tokens > kMaxPairs / P || k < 1 || k > kMaxChoices || experts < 1 ||
-        experts > kMaxExperts || align < 1 || capacity < 0)
+    if (P < 1 || P > GAR_MAX_WORKERS || k < 1 || k > kMaxChoices || tokens < 0 || tokens > kMaxPairs / k / P || experts < 1 ||
+        experts > kMaxExperts || align < 1 || capacity < 0 || (capacity > 0 && align != 1))
         return -1;
-    return sort_rows(P * tokens * k, experts, align, capacity);
+    const int64_t rows = sort_rows(P * tokens * k, experts, align, capacity);
+    return rows <= 0x7FFFFFFF ? rows : -1;
 }
 
 extern "C" size_t gar_expert_workspace_bytes(int32_t P, int64_t tokens, int32_t k, int32_t experts) {

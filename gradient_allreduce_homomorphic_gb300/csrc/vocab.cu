@@ -917,10 +917,14 @@ Plan plan_for(int64_t rows, int64_t vocab, int64_t hidden, int32_t dw_type) {
     return p;
 }
 
+bool sizes_fit(int64_t rows, int64_t vocab, int64_t hidden) {
+    return rows >= 0 && vocab >= 1 && hidden >= 1 && rows <= 0x7FFFFFFF - 1024 && vocab <= 0x7FFFFFFF - 1024 && hidden <= (1 << 20);
+}
+
 int check(const void *x, int64_t ldx, const void *w, int64_t ldw, const int32_t *target, const float *weight, int64_t rows,
           int64_t vocab, int64_t hidden, int32_t dtype) {
     if (dtype != GAR_BF16) return fail(GAR_EDTYPE, "x and w have to be bf16, not dtype %d", dtype);
-    if (rows < 0 || vocab < 1 || hidden < 1 || rows > 0x7FFFFFFF - 1024 || vocab > 0x7FFFFFFF - 1024 || hidden > (1 << 20))
+    if (!sizes_fit(rows, vocab, hidden))
         return fail(GAR_EINVAL, "rows=%lld vocab=%lld (from 1) hidden=%lld (1..2^20)", static_cast<long long>(rows),
                     static_cast<long long>(vocab), static_cast<long long>(hidden));
     if (rows == 0) return GAR_OK;
@@ -1035,7 +1039,7 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
 using namespace gar;
 
 extern "C" size_t gar_vocab_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden, int32_t dw_type) {
-    if (rows < 0 || vocab < 1 || hidden < 1 || elem_bytes(dw_type) < 0) return 0;
+    if (!sizes_fit(rows, vocab, hidden) || elem_bytes(dw_type) < 0) return 0;
     const Plan p = plan_for(rows, vocab, hidden, dw_type);
     return static_cast<size_t>(std::max(std::max(p.loss, p.grad), int64_t{256}));
 }

@@ -802,7 +802,7 @@ int gar_balance_loss(const void *const *z, int32_t P, int64_t tokens, int32_t ex
 /* Bytes of device workspace for gar_vocab_loss and gar_vocab_grad; dw_type: the
  * type of dw (GAR_BF16 where dw is not asked for).  The gradient's holds a piece
  * of the vocabulary's g, 256 MB of it at most (512 for an fp32 dw; or rows x 256),
- * and where there are several the fp32 sums of dx. */
+ * and where there are several the fp32 sums of dx.  0: sizes that these refuse. */
 size_t gar_vocab_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden, int32_t dw_type);
 
 /* gar_vocab_loss -- softmax cross entropy of a vocabulary layer whose logits are
@@ -873,7 +873,7 @@ int gar_vocab_grad_with_loss(const void *x, int64_t ldx, const void *w, int64_t 
  * is no choice; the same expert more than once is as many pairs). */
 
 /* Rows that any choices fit in: experts * capacity where capacity > 0, else
- * P tokens k + experts (align - 1).  -1: an argument out of range. */
+ * P tokens k + experts (align - 1).  -1: arguments that gar_expert_sort refuses. */
 int64_t gar_expert_rows(int32_t P, int64_t tokens, int32_t k, int32_t experts, int32_t align, int32_t capacity);
 
 /* Bytes of device workspace gar_expert_sort needs. */
