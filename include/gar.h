@@ -811,9 +811,9 @@ size_t gar_vocab_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden, in
  *   lse_t  = log sum_v exp(z_tv)
  *   loss_t = lse_t - z_{t, target_t}
  * A row counts if its target lies in [0, vocab) and its weight is not 0; any other
- * has loss 0 and lse 0, whatever its x.  A NaN or an infinity among a row's logits
- * makes its loss NaN.  Sums are fp32; the tensor cores' additions round toward zero,
- * so that a logit whose products are all of one sign is 1e-5 of itself too small at hidden =
+ * has loss 0 and lse 0, whatever its x.  A NaN or +infinity among a row's logits
+ * makes its loss NaN; one of -infinity has probability 0, and as the target's makes the
+ * loss +infinity.  Sums are fp32; the tensor cores' additions round toward zero, so that a logit whose products are all of one sign is 1e-5 of itself too small at hidden =
  * 4096 and 3e-5 from 8192 on, where it is the sum of several (2e-6 of lse at 4096 for
  * products of both signs).  The target's logit is kept apart from the sum over the
  * others, r = log sum_{v != target} exp(z_tv), and loss_t = log(1 + exp(r - z_{t, target})):

@@ -136,3 +136,39 @@ def test_losses_given_or_not(env):
     g64.scatter_add_(1, target[rest].clamp(min=0).long()[:, None], -torch.ones((199, 1), dtype=torch.float64, device="cuda"))
     size = g64.abs() @ w.double().abs()  # both: g's rounding and the result's, sums, and lse's error far below them
     assert ((a[rest].double() - b[rest].double()).abs() <= (4 * 2 ** -8 + 1e-3) * size).all()
+
+
+def test_logits_of_minus_infinity(env):
+    """Probability 0: the loss of another target is as if the entry were not there, its own is +inf; its share of dw is
+    -weight x where it is the target and 0 elsewhere."""
+    torch, g = env
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(4)
+    x = torch.randn((300, 64), generator=gen, device="cuda").abs().add_(0.5).bfloat16()
+    w = (torch.randn((900, 64), generator=gen, device="cuda") * 0.2).bfloat16()
+    gone = [3, 700]
+    w[gone, 5] = float("-inf")
+    target = torch.randint(4, 700, (300,), generator=gen, device="cuda").int()
+    target[::9] = 700
+    lost = target == 700
+    loss, lse = torch.empty(300, device="cuda"), torch.empty(300, device="cuda")
+    ws = torch.empty(g.gar_vocab_workspace_bytes(300, 900, 64, torch.float32), dtype=torch.uint8, device="cuda")
+    g.gar_vocab_loss(x, w, target, loss, lse, ws)
+    kept = torch.ones(900, dtype=torch.bool, device="cuda")
+    kept[gone] = False
+    z = x.double() @ w.double()[kept].t()
+    size = x.double().abs() @ w.double()[kept].abs().t()
+    ez = 2 * U * 64 * size.amax(1)
+    want = torch.logsumexp(z, 1)
+    tol = 2 * ez + 260 * U + 8 * U * (1 + want.abs())
+    assert ((lse.double() - want).abs() <= tol).all() and bool((loss[lost] == float("inf")).all())
+    place = torch.cumsum(kept, 0)[target.long()] - 1
+    of_row = want - z.gather(1, place[:, None])[:, 0]
+    assert ((loss.double() - of_row).abs() <= tol + 2 * ez + 8 * U * of_row)[~lost].all()
+    for grad in (lambda dw: g.gar_vocab_grad(x, w, target, lse, None, dw, ws),
+                 lambda dw: g.gar_vocab_grad_with_loss(x, w, target, loss, lse, None, dw, ws)):
+        dw = torch.empty((900, 64), device="cuda")
+        grad(dw)
+        want_dw = -x[lost].double().sum(0)
+        assert bool(torch.isfinite(dw).all()) and bool((dw[3] == 0).all())
+        assert ((dw[700].double() - want_dw).abs() <= (2 ** -16 + 2 * U * 600) * want_dw.abs()).all()
