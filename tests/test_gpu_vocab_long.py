@@ -155,3 +155,41 @@ def test_dx_of_a_long_vocabulary(env):
     want, size = G @ some, G.abs() @ some
     tol = (2 ** -8 + 1e-5 + 2 * U * 32768 + 8 * U) * size + 2 ** -8 * want.abs()
     assert ((dx[:, ::61].double() - want).abs() <= tol).all() and bool((dx[7] == 0).all())
+
+
+@pytest.mark.parametrize("addend", ["none", "given", "in place"])
+@pytest.mark.parametrize("hidden,pad", [(64, 0), (61, 0), (64, 3), (72, 8)])
+def test_segments_of_an_fp32_dw(env, hidden, pad, addend):
+    """More than 4096 rows (two parts of g each): the first segment takes the addend, the later ones what is in dw; rows of
+    dw on 16 bytes and off them, a last tile that is not full."""
+    torch, g = env
+    gen, rows, vocab = of(torch, 5), 9001, 300
+    x = torch.randn((rows, (hidden + 7) // 8 * 8), generator=gen, device="cuda").add_(0.25).bfloat16()[:, :hidden]
+    w = (torch.randn((vocab, (hidden + 7) // 8 * 8), generator=gen, device="cuda") * 0.2).bfloat16()[:, :hidden]
+    target = torch.randint(0, vocab, (rows,), generator=gen, device="cuda").int()
+    target[::11] = -1
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    whole = torch.full((vocab, hidden + pad), 7.0, device="cuda")
+    dw, add = whole[:, :hidden], None
+    before = torch.randn((vocab, hidden), generator=gen, device="cuda")
+    if addend == "given":
+        add = before.clone()
+    elif addend == "in place":
+        dw.copy_(before)
+        add = dw
+    ws = workspace(torch, g, rows, vocab, hidden, torch.float32)
+    g.gar_vocab_loss(x, w, target, loss, lse, ws)
+    g.gar_vocab_grad(x, w, target, lse, None, dw, ws, addend=add)
+    torch.cuda.synchronize()
+    assert g.gar_sync_status() == 0 and bool((whole[:, hidden:] == 7).all())
+    X, on = x.double(), (target >= 0)[:, None]
+    G = torch.softmax(X @ w.double().t(), 1)
+    at = target.long().clamp(min=0)[:, None]
+    G.scatter_add_(1, at, -torch.ones_like(at, dtype=torch.float64))
+    G *= on
+    want = G.t() @ X + (before.double() if add is not None else 0.0)
+    # of each term: g's parts, its exponential's error and lse's (below 1e-5); a segment's sum; the segments'
+    tol = (2 ** -16 + 1e-5 + 2 * U * 8192) * (G.abs().t() @ X.abs()) + 8 * U * (want.abs() + before.double().abs() + 1)
+    assert ((dw.double() - want).abs() <= tol).all()
+    if addend != "in place":  # and as closely as random signs allow: a segment left out or taken twice shows
+        assert (dw.double() - want).norm() <= 1e-4 * (want - (before.double() if add is not None else 0.0)).norm()
