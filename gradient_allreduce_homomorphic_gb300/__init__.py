@@ -109,7 +109,7 @@ _SIGNATURES = {
     "gar_vocab_grad": (C.c_int, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp,
                                  _i64, _i32, _vp, C.c_size_t, _vp]),
     "gar_vocab_grad_with_loss": (C.c_int, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp,
-                                           _i64, _vp, _i64, _i32, _vp, C.c_size_t, _vp]),
+                                           _i64, _vp, _i64, _i32, _i32, _vp, C.c_size_t, _vp]),
     "gar_expert_rows": (_i64, [_i32, _i64, _i32, _i32, _i32, _i32]),
     "gar_expert_workspace_bytes": (C.c_size_t, [_i32, _i64, _i32, _i32]),
     "gar_expert_sort": (C.c_int, [_vp, _i32, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _vp, C.c_size_t, _vp]),
@@ -926,8 +926,7 @@ def _vocab_outputs(x, dx, dw, addend, rows, vocab, hidden, workspace, stream):
         if dw is None or addend.dtype != dw.dtype:
             raise GarError(GAR_EDTYPE, f"addend is {addend.dtype}, dw {None if dw is None else dw.dtype}")
         ap, lda = _matrix(addend, "addend", vocab, hidden)
-    return (dxp, lddx, ap, lda, dwp, lddw, dw_type, _dev(workspace), workspace.numel() * workspace.element_size(),
-            _stream(stream))
+    return (dxp, lddx, ap, lda, dwp, lddw, dw_type), (_dev(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
 
 
 def gar_vocab_grad(x, w, target, lse, dx, dw, workspace, weight=None, addend=None, stream=None):
@@ -936,16 +935,18 @@ def gar_vocab_grad(x, w, target, lse, dx, dw, workspace, weight=None, addend=Non
     addend, of dw's type, is added to dw (it may be dw).  lse alone does not hold
     the share of a target that is all but sure (gar_vocab_grad_with_loss)."""
     rows, vocab, hidden, head = _vocab_args(x, w, target, weight)
-    tail = _vocab_outputs(x, dx, dw, addend, rows, vocab, hidden, workspace, stream)
-    _call("gar_vocab_grad", *head, _vector(lse, "lse", _FLOAT32, rows), *tail)
+    out, tail = _vocab_outputs(x, dx, dw, addend, rows, vocab, hidden, workspace, stream)
+    _call("gar_vocab_grad", *head, _vector(lse, "lse", _FLOAT32, rows), *out, *tail)
 
 
-def gar_vocab_grad_with_loss(x, w, target, loss, lse, dx, dw, workspace, weight=None, addend=None, stream=None):
+def gar_vocab_grad_with_loss(x, w, target, loss, lse, dx, dw, workspace, weight=None, addend=None, parts: int = 0, stream=None):
     """The same gradient from the loss and lse of gar_vocab_loss: each target's share
-    keeps its digits, however small its loss."""
+    keeps its digits, however small its loss.  parts=2: dx and a bf16 dw too from
+    all of g's bits, at twice their products' cost (the workspace of an fp32 dw)."""
     rows, vocab, hidden, head = _vocab_args(x, w, target, weight)
-    tail = _vocab_outputs(x, dx, dw, addend, rows, vocab, hidden, workspace, stream)
-    _call("gar_vocab_grad_with_loss", *head, _vector(loss, "loss", _FLOAT32, rows), _vector(lse, "lse", _FLOAT32, rows), *tail)
+    out, tail = _vocab_outputs(x, dx, dw, addend, rows, vocab, hidden, workspace, stream)
+    _call("gar_vocab_grad_with_loss", *head, _vector(loss, "loss", _FLOAT32, rows), _vector(lse, "lse", _FLOAT32, rows), *out, parts,
+          *tail)
 
 
 # ------------------------------------------- tokens to experts and back

@@ -17,9 +17,12 @@
 // three, and no more than a piece of g exists at a time.
 //
 // g is rounded to bf16 as an operand of the products: of a bf16 gradient that is
-// another error of the size of the result's own rounding.  An fp32 dw takes g as
+// another error of the size of the result's own rounding (dx and a bf16 dw 2.4e-3 from
+// the exact ones in the 2-norm, 1.7e-3 of it their own).  An fp32 dw takes g as
 // the sum of two bf16 values (16 bits and more of it), a product of twice the
-// length, so that its error is what the fp32 sums leave.
+// length, so that its error is what the fp32 sums leave; a caller who asks for them
+// (parts) has the same of dx and a bf16 dw, which then are the exact ones rounded but
+// for one value in thousands.
 //
 // All products run on one kernel of persistent CTA pairs (cta_group::2): tiles
 // of 256 x 256, two accumulators in tensor memory, so that a tile's epilogue
@@ -81,7 +84,7 @@ struct VocabParams {
     int32_t a_rows, second, stages;
     int32_t runs;        // a run: consecutive column tiles of one item
     int32_t chunks;      // of 64 k, of one part of g
-    int32_t parts;       // of g: 1, or 2 along k (fp32 dw)
+    int32_t parts;       // of g: 1, or 2 along k
     int32_t rest;        // dx: tiles behind the items, whose k is cut
     int32_t splits;      // into as many parts
     int64_t rows, hidden, vocab;
@@ -155,7 +158,8 @@ __device__ __forceinline__ Item item_of(const VocabParams &p, int64_t i) {
     it.slot = static_cast<int32_t>(i - p.items);
     const int64_t split = it.slot / p.rest;
     place_item(p, p.items + it.slot % p.rest, it);
-    it.c0 = static_cast<int32_t>(p.chunks * split / p.splits), it.c1 = static_cast<int32_t>(p.chunks * (split + 1) / p.splits);
+    const int64_t chunks = static_cast<int64_t>(p.chunks) * p.parts;
+    it.c0 = static_cast<int32_t>(chunks * split / p.splits), it.c1 = static_cast<int32_t>(chunks * (split + 1) / p.splits);
     return it;
 }
 
@@ -409,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int32_t c = it.c0; c < it.c1; ++c) {
                     if (!(ok = mbar_wait(empty + 8 * s, turn, &failed))) break;
                     const uint32_t dst = base + s * stage, bar = lead_full + 8 * s;
-                    const bool second = kMode == kWeights && c >= p.chunks;
+                    const bool second = (kMode == kWeights || kMode == kInputs) && c >= p.chunks;
                     const int32_t k = (second ? c - p.chunks : c) * kK;
                     if (rank == 0) mbar_expect_tx(full + 8 * s, a_bytes * (1 + p.second) + 2 * tile_n * kK);
                     if (kMode == kWeights) {  // the library's own copies: their rows are whole columns of 128 bytes
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else if (rank == 0 || p.second) {
                             tma_load_2d_pair(dst, &map_a, bar, k, a);
                         }
-                        tma_load_2d_pair(dst + a_bytes, &map_b, bar, k, b);
+                        tma_load_2d_pair(dst + a_bytes, kMode == kInputs && second ? &map_c : &map_b, bar, k, b);
                     }
                     issued = issued < static_cast<int>(stages) ? issued + 1 : static_cast<int>(stages);
                     if (++s == stages) s = 0, turn ^= 1;
@@ -789,7 +793,7 @@ int launch(const VocabParams &p, const CUtensorMap &a, const CUtensorMap &b, con
 template <int kMode, typename T>
 int launch_form(const VocabParams &p, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &c, const CUtensorMap &d,
                 cudaStream_t stream) {
-    const int64_t longest = p.items > 0 ? static_cast<int64_t>(p.chunks) * p.parts : ceil_div(p.chunks, int64_t{p.splits});
+    const int64_t longest = p.items > 0 ? static_cast<int64_t>(p.chunks) * p.parts : ceil_div(static_cast<int64_t>(p.chunks) * p.parts, int64_t{p.splits});
     if constexpr (kMode != kWeights || sizeof(T) == 2)
         if (longest > kSegment<kMode, T>) return launch<kMode, T, kLong>(p, a, b, c, d, stream);
     if constexpr (kMode == kGradient)
@@ -891,10 +895,10 @@ struct Plan {
 int64_t room(int64_t bytes) { return ceil_div(bytes, 256) * 256; }
 int64_t live_ld(int64_t hidden) { return ceil_div(hidden, kK) * kK; }
 
-Plan plan_for(int64_t rows, int64_t vocab, int64_t hidden, int32_t dw_type) {
+// parts: room for so many of g.
+Plan plan_for(int64_t rows, int64_t vocab, int64_t hidden, int64_t parts) {
     Plan p{};
     const int64_t tiles_t = ceil_div(rows, int64_t{kTile});
-    const int64_t parts = dw_type == GAR_F32 ? 2 : 1;
     p.resident = std::max(sm_count() / 2, 1);
     const int64_t most = std::max(kPieceBytes / (std::max(rows, int64_t{1}) * 2) / kTile, int64_t{1}) * kTile;
     p.pieces = ceil_div(vocab, most);
@@ -909,8 +913,10 @@ Plan plan_for(int64_t rows, int64_t vocab, int64_t hidden, int32_t dw_type) {
     if (rows > 0) {
         const int64_t tile_t = std::min(ceil_div(rows, int64_t{32}) * 32, int64_t{kTile});
         for (const int64_t cols : {std::min(p.piece, vocab), vocab - (p.pieces - 1) * p.piece}) {
-            const Rounds r = input_rounds(ceil_div(rows, tile_t) * ceil_div(hidden, int64_t{kTile}), ceil_div(cols, int64_t{kK}), p.resident);
-            p.part = std::max(p.part, static_cast<int64_t>(r.rest) * r.splits * kTile * kTile * 4);
+            for (int64_t of_dx = 1; of_dx <= parts; ++of_dx) {
+                const Rounds r = input_rounds(ceil_div(rows, tile_t) * ceil_div(hidden, int64_t{kTile}), ceil_div(cols, int64_t{kK}) * of_dx, p.resident);
+                p.part = std::max(p.part, static_cast<int64_t>(r.rest) * r.splits * kTile * kTile * 4);
+            }
         }
     }
     p.grad = p.g * parts + p.x + p.sum + p.part;
@@ -947,16 +953,16 @@ bool copy_pays(const uint16_t *x, int64_t ldx, const VocabParams &p) {
     return (!aligned(x, 128) || ldx % 64) && static_cast<double>(p.rows) * p.vocab * p.hidden > 2.5e10;
 }
 
-// dw and the shares of dx of all pieces; T: dw's type.
+// dw and the shares of dx of all pieces; T: dw's type; parts: bf16 values that g is taken as, 0: two for an fp32 dw, else one.
 template <typename T>
 int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t ldw, uint16_t *dx, int64_t lddx,
-             const T *addend, int64_t ld_addend, T *dw, int64_t lddw, uint8_t *workspace, cudaStream_t stream) {
+             const T *addend, int64_t ld_addend, T *dw, int64_t lddw, int parts, uint8_t *workspace, cudaStream_t stream) {
     const int64_t rows = p.rows, vocab = p.vocab, hidden = p.hidden, ld_live = live_ld(hidden);
-    constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
+    const int in_g = sizeof(T) == 4 || parts == 2 ? 2 : 1;
     const auto g = reinterpret_cast<uint16_t *>(workspace), g_low = reinterpret_cast<uint16_t *>(workspace + how.g);
-    const auto live = reinterpret_cast<uint16_t *>(workspace + kParts * how.g);
-    const auto sum = reinterpret_cast<float *>(workspace + kParts * how.g + how.x);
-    const auto part = reinterpret_cast<float *>(workspace + kParts * how.g + how.x + how.sum);
+    const auto live = reinterpret_cast<uint16_t *>(workspace + in_g * how.g);
+    const auto sum = reinterpret_cast<float *>(workspace + in_g * how.g + how.x);
+    const auto part = reinterpret_cast<float *>(workspace + in_g * how.g + how.x + how.sum);
     const int64_t tiles_t = ceil_div(rows, int64_t{kTile}), tiles_h = ceil_div(hidden, int64_t{kTile});
     CUtensorMap rows_k{}, live_mn{}, g_mn{}, low_mn{}, g_to{}, low_to{};
     const bool copied = copy_pays(x, ldx, p);
@@ -971,8 +977,8 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
         if (int rc = encode_columns(&live_mn, live, ld_live, rows, weights_n / 128)) return rc;
     }
     if (int rc = encode_columns(&g_mn, g, how.piece, rows, 2)) return rc;
-    if (int rc = encode_store(&g_to, g, how.piece, rows, how.piece, kParts == 1)) return rc;
-    if (kParts == 2) {
+    if (int rc = encode_store(&g_to, g, how.piece, rows, how.piece, in_g == 1)) return rc;
+    if (in_g == 2) {
         if (int rc = encode_columns(&low_mn, g_low, how.piece, rows, 2)) return rc;
         if (int rc = encode_store(&low_to, g_low, how.piece, rows, how.piece, false)) return rc;
     } else {
@@ -992,13 +998,15 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
             if (int rc = encode(&w_k, w + first * ldw, hidden, cols, ldw, q.tile_n / 2)) return rc;
             lay_out(&q, rows, true);
             if (dw && !copied && first == 0) q.x = x, q.ldx = ldx, q.live = live, q.ld_live = ld_live;
-            if (int rc = launch_form<kGradient, T>(q, rows_k, w_k, g_to, low_to, stream)) return rc;
+            if (int rc = in_g == 2 ? launch_form<kGradient, float>(q, rows_k, w_k, g_to, low_to, stream)
+                                   : launch_form<kGradient, uint16_t>(q, rows_k, w_k, g_to, low_to, stream))
+                return rc;
         }
         if (dw) {
             CUtensorMap to{};
             q.tile_n = weights_n;
             q.tiles_m = ceil_div(cols, int64_t{kTile}), q.tiles_n = ceil_div(hidden, int64_t{weights_n}), q.runs = static_cast<int32_t>(q.tiles_n);
-            q.chunks = static_cast<int32_t>(ceil_div(rows, int64_t{kK})), q.parts = kParts;
+            q.chunks = static_cast<int32_t>(ceil_div(rows, int64_t{kK})), q.parts = in_g;
             q.items = q.tiles_m * q.runs;
             q.out = dw + first * lddw, q.ld_out = lddw;
             q.addend = addend ? addend + first * ld_addend : nullptr, q.ld_addend = ld_addend;
@@ -1006,24 +1014,27 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
                       (!addend || (aligned(q.addend, 16) && ld_addend * sizeof(T) % 16 == 0));
             q.by_tma = !addend && aligned(q.out, 16) && lddw * sizeof(T) % 16 == 0;
             if (q.by_tma) {
-                if (int rc = kParts == 2 ? encode_store_f32(&to, q.out, hidden, cols, lddw) : encode_store(&to, q.out, hidden, cols, lddw, true))
+                if (int rc = sizeof(T) == 4 ? encode_store_f32(&to, q.out, hidden, cols, lddw) : encode_store(&to, q.out, hidden, cols, lddw, true))
                     return rc;
             }
             lay_out(&q, 0, true);
             if (int rc = launch_form<kWeights, T>(q, g_mn, live_mn, low_mn, to, stream)) return rc;
         }
         if (dx) {
-            CUtensorMap w_mn{}, g_k{};
+            CUtensorMap w_mn{}, g_k{}, low_k{};
             q.tile_n = static_cast<int32_t>(std::min(ceil_div(rows, int64_t{32}) * 32, int64_t{kTile}));
-            q.tiles_m = tiles_h, q.tiles_n = ceil_div(rows, int64_t{q.tile_n}), q.runs = static_cast<int32_t>(q.tiles_n), q.parts = 1;
+            q.tiles_m = tiles_h, q.tiles_n = ceil_div(rows, int64_t{q.tile_n}), q.runs = static_cast<int32_t>(q.tiles_n), q.parts = parts == 2 ? 2 : 1;
             q.chunks = static_cast<int32_t>(ceil_div(cols, int64_t{kK}));
-            const Rounds rounds = input_rounds(q.tiles_m * q.tiles_n, q.chunks, how.resident);
+            const Rounds rounds = input_rounds(q.tiles_m * q.tiles_n, static_cast<int64_t>(q.chunks) * q.parts, how.resident);
             q.items = rounds.items, q.rest = rounds.rest, q.splits = rounds.splits;
             q.out = dx, q.ld_out = lddx, q.sum = sum, q.part = part;
             if (int rc = encode(&w_mn, w + first * ldw, hidden, cols, ldw, kK)) return rc;
             if (int rc = encode_tile_map(&g_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g, cols, rows, how.piece * 2, kK, q.tile_n / 2)) return rc;
+            low_k = g_k;
+            if (q.parts == 2)
+                if (int rc = encode_tile_map(&low_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g_low, cols, rows, how.piece * 2, kK, q.tile_n / 2)) return rc;
             lay_out(&q, 0, false);
-            if (int rc = launch_form<kInputs, uint16_t>(q, w_mn, g_k, g_k, g_k, stream)) return rc;
+            if (int rc = launch_form<kInputs, uint16_t>(q, w_mn, g_k, low_k, low_k, stream)) return rc;
             if (q.rest > 0)
                 if (int rc = launch_early("vocab_inputs_kernel", vocab_inputs_kernel, dim3(static_cast<unsigned>(q.rest * (q.tile_n / 4))), kTile, 0, 1,
                                           stream, q))
@@ -1040,7 +1051,7 @@ using namespace gar;
 
 extern "C" size_t gar_vocab_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden, int32_t dw_type) {
     if (!sizes_fit(rows, vocab, hidden) || elem_bytes(dw_type) < 0) return 0;
-    const Plan p = plan_for(rows, vocab, hidden, dw_type);
+    const Plan p = plan_for(rows, vocab, hidden, dw_type == GAR_F32 ? 2 : 1);
     return static_cast<size_t>(std::max(std::max(p.loss, p.grad), int64_t{256}));
 }
 
@@ -1049,7 +1060,7 @@ extern "C" int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t
                               void *d_workspace, size_t workspace_bytes, gar_stream_t stream_) {
     if (int rc = check(x, ldx, w, ldw, target, weight, rows, vocab, hidden, dtype)) return rc;
     if (rows == 0) return GAR_OK;
-    const Plan how = plan_for(rows, vocab, hidden, GAR_BF16);
+    const Plan how = plan_for(rows, vocab, hidden, 1);
     if (!loss || !lse || !d_workspace || workspace_bytes < static_cast<size_t>(how.loss))
         return fail(GAR_EINVAL, "loss, lse or the workspace is NULL, or the workspace below %lld bytes", static_cast<long long>(how.loss));
     if (!aligned(loss, 4) || !aligned(lse, 4) || !aligned(d_workspace, 256)) return fail(GAR_EALIGN, "loss, lse (4 bytes) or the workspace (256) is misaligned");
@@ -1082,7 +1093,8 @@ extern "C" int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t
 namespace {
 int vocab_grad(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target, const float *weight,
                int64_t rows, int64_t vocab, int64_t hidden, const float *loss, const float *lse, void *dx, int64_t lddx, const void *addend,
-               int64_t ld_addend, void *dw, int64_t lddw, int32_t dw_type, void *d_workspace, size_t workspace_bytes, gar_stream_t stream_) {
+               int64_t ld_addend, void *dw, int64_t lddw, int32_t dw_type, int32_t parts, void *d_workspace, size_t workspace_bytes,
+               gar_stream_t stream_) {
     if (int rc = check(x, ldx, w, ldw, target, weight, rows, vocab, hidden, dtype)) return rc;
     const int size = elem_bytes(dw_type);
     if (size < 0) return fail(GAR_EDTYPE, "unknown dtype %d of dw", dw_type);
@@ -1103,7 +1115,7 @@ int vocab_grad(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t d
                                   static_cast<const uint16_t *>(addend), ld_addend, static_cast<uint16_t *>(dw), lddw, vocab, hidden);
     }
     if (dx && lddx < hidden) return fail(GAR_EINVAL, "the row stride of dx is below the hidden size");
-    const Plan how = plan_for(rows, vocab, hidden, dw_type);
+    const Plan how = plan_for(rows, vocab, hidden, dw_type == GAR_F32 || parts == 2 ? 2 : 1);
     if (!lse || !d_workspace || workspace_bytes < static_cast<size_t>(how.grad))
         return fail(GAR_EINVAL, "lse or the workspace is NULL, or the workspace below %lld bytes", static_cast<long long>(how.grad));
     if (!aligned(dx, 2) || !aligned(lse, 4) || !aligned(d_workspace, 256)) return fail(GAR_EALIGN, "dx, lse or the workspace (256 bytes) is misaligned");
@@ -1115,9 +1127,9 @@ int vocab_grad(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t d
     uint16_t *dxh = static_cast<uint16_t *>(dx);
     uint8_t *ws = static_cast<uint8_t *>(d_workspace);
     return dw_type == GAR_F32 ? gradient<float>(p, how, xh, ldx, wh, ldw, dxh, lddx, static_cast<const float *>(addend), ld_addend,
-                                                static_cast<float *>(dw), lddw, ws, stream)
+                                                static_cast<float *>(dw), lddw, parts, ws, stream)
                               : gradient<uint16_t>(p, how, xh, ldx, wh, ldw, dxh, lddx, static_cast<const uint16_t *>(addend), ld_addend,
-                                                   static_cast<uint16_t *>(dw), lddw, ws, stream);
+                                                   static_cast<uint16_t *>(dw), lddw, parts, ws, stream);
 }
 }  // namespace
 
@@ -1126,15 +1138,18 @@ extern "C" int gar_vocab_grad(const void *x, int64_t ldx, const void *w, int64_t
                               const void *addend, int64_t ld_addend, void *dw, int64_t lddw, int32_t dw_type, void *d_workspace,
                               size_t workspace_bytes, gar_stream_t stream) {
     return vocab_grad(x, ldx, w, ldw, dtype, target, weight, rows, vocab, hidden, nullptr, lse, dx, lddx, addend, ld_addend, dw, lddw,
-                      dw_type, d_workspace, workspace_bytes, stream);
+                      dw_type, 0, d_workspace, workspace_bytes, stream);
 }
 
 extern "C" int gar_vocab_grad_with_loss(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target,
                                         const float *weight, int64_t rows, int64_t vocab, int64_t hidden, const float *loss,
                                         const float *lse, void *dx, int64_t lddx, const void *addend, int64_t ld_addend, void *dw,
-                                        int64_t lddw, int32_t dw_type, void *d_workspace, size_t workspace_bytes, gar_stream_t stream) {
+                                        int64_t lddw, int32_t dw_type, int32_t parts, void *d_workspace, size_t workspace_bytes,
+                                        gar_stream_t stream) {
+    if (parts < 0 || parts > 2 || (parts == 1 && dw && dw_type == GAR_F32))
+        return fail(GAR_EINVAL, "parts=%d: 0, 1 (not of an fp32 dw) or 2", parts);
     if (rows > 0 && !loss) return fail(GAR_EINVAL, "loss is NULL");
     if (!aligned(loss, 4)) return fail(GAR_EALIGN, "loss is misaligned");
     return vocab_grad(x, ldx, w, ldw, dtype, target, weight, rows, vocab, hidden, loss, lse, dx, lddx, addend, ld_addend, dw, lddw,
-                      dw_type, d_workspace, workspace_bytes, stream);
+                      dw_type, parts, d_workspace, workspace_bytes, stream);
 }

@@ -800,7 +800,7 @@ int gar_balance_loss(const void *const *z, int32_t P, int64_t tokens, int32_t ex
                      gar_stream_t stream);
 
 /* Bytes of device workspace for gar_vocab_loss and gar_vocab_grad; dw_type: the
- * type of dw (GAR_BF16 where dw is not asked for).  The gradient's holds a piece
+ * type of dw (GAR_BF16 where dw is not asked for; GAR_F32 for two parts of g).  The gradient's holds a piece
  * of the vocabulary's g, 256 MB of it at most (512 for an fp32 dw; or rows x 256),
  * and where there are several the fp32 sums of dx.  0: sizes that these refuse. */
 size_t gar_vocab_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden, int32_t dw_type);
@@ -860,11 +860,16 @@ int gar_vocab_grad(const void *x, int64_t ldx, const void *w, int64_t ldw, int32
 
 /* gar_vocab_grad_with_loss -- the same gradient, from the losses too, so that the
  * target's g, -weight_t (1 - exp(-loss_t)), keeps its digits also where the target is all but sure.
- *   loss         device, [rows] fp32, what gar_vocab_loss wrote beside lse */
+ *   loss         device, [rows] fp32, what gar_vocab_loss wrote beside lse
+ *   parts        bf16 values whose sum g is taken as.  0: as in gar_vocab_grad, one for dx
+ *                and a bf16 dw, two for an fp32 dw.  2: two for all of them, each at twice
+ *                that product's cost: dx and a bf16 dw are then the exact ones
+ *                rounded but for one value in thousands (the workspace of an fp32 dw).
+ *                1: one (not for an fp32 dw) */
 int gar_vocab_grad_with_loss(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target,
                              const float *weight, int64_t rows, int64_t vocab, int64_t hidden, const float *loss, const float *lse,
                              void *dx, int64_t lddx, const void *addend, int64_t ld_addend, void *dw, int64_t lddw, int32_t dw_type,
-                             void *d_workspace, size_t workspace_bytes, gar_stream_t stream);
+                             int32_t parts, void *d_workspace, size_t workspace_bytes, gar_stream_t stream);
 
 /* Tokens sorted by the experts that a router chose, and back.  A pair is one of
  * the k choices of one token of one worker, numbered (w tokens + t) k + j; P tokens
