@@ -53,8 +53,9 @@ namespace {
 enum { kLoss, kGradient, kWeights, kInputs };
 // A gradient with its losses given is a kernel of its own: the load among the exponents costs 32 registers, and the
 // bf16 gradient of 4096 x 131072 x 64 without it 831 us instead of 845.  So are the products whose sums are longer than a
-// segment: the products of a tile all go to one accumulator, the sum of its segments so far lies in the place of the
-// other, and no epilogue overlaps the next products.
+// segment: these all go to one accumulator, and the sum of a tile's segments lies in the place of the other.  An
+// accumulator is handed back once it is read, and a tile's end is taken from the sum, so that the products wait for
+// little more than the reading.
 enum { kPlain, kSure, kLong };
 
 constexpr int kTile = 256;    // rows of a pair's tile, and its columns at most
@@ -64,13 +65,16 @@ constexpr int kOperand = 128 * kK * 2;  // bytes of 128 rows of an operand of a 
 constexpr int kThreads = 320;  // warp 0 loads, warp 1 issues products, warps 2-9 epilogue
 constexpr int kStaging = 8 * 4096;  // for each epilogue warp a tile of 32 x 64 bf16, two of 32 x 32, or one of 32 x 32 fp32
 constexpr int kShared = 224 * 1024, kSmem = 1024 + kShared;
-// Chunks that an accumulator adds at most.  The tensor core's additions round toward zero, so the error of a sum of
-// one sign grows with its length: 3e-5 of it at 8192 k, which an fp32 dw and logits are held to, 1.6e-4 at 32768, beside
-// the 2e-3 of bf16's own rounding (uncut: lse 6e-3 at 2^20 k, a bf16 dw of 4M rows 2.6e-2).  Longer sums are added up by
-// the epilogue: those of an fp32 dw in dw itself, the others in tensor memory (kLong: loss of 2048 x 32000 x 16384 1270 us,
-// 1170 uncut; its bf16 gradient within 2 % of uncut).
+// Chunks that an accumulator adds at most.  The tensor core's additions round toward zero, so that a sum of one sign, or
+// one with a large term ahead, is too small by what grows with its length: 3e-5 of it at 8192 k, which logits are held
+// to; 1.6e-4 at 32768, beside the 2e-3 of a bf16 result's own rounding (uncut: lse 6e-3 at 2^20 k, a bf16 dw of 4M rows
+// 2.6e-2); 3e-6 at 2048, of an fp32 dw (of 4096 rows, random signs, 1.3e-5 in the 2-norm uncut, 3.6e-6 so; at 1024 2.9e-6).
+// Longer sums are added up by the epilogue in tensor memory (kLong): an fp32 gradient of 4096 x 131072 x 4096 takes 10.6 ms,
+// 10.2 uncut (10.8 with segments of 1024), the loss of 2048 x 32000 x 16384 1260 us, 1220 uncut.  Of two parts of g the
+// low one goes first, when the sums are small: it needs no more segments than a bf16 result.
 template <int kMode, typename T>
-constexpr int kSegment = (kMode == kInputs || (kMode == kWeights && sizeof(T) == 2) ? 32768 : 8192) / kK;
+constexpr int kSegment = (kMode == kWeights && sizeof(T) == 4 ? 2048 : kMode == kWeights || kMode == kInputs ? 32768 : 8192) / kK;
+constexpr int kLowSegment = 32768 / kK;
 
 
 struct VocabParams {
@@ -359,8 +363,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool kMnA = kMode == kWeights || kMode == kInputs, kMnB = kMode == kWeights;
     // 16 k of a K-major operand are 32 bytes of each line; of an MN-major one two groups of eight lines of 128 bytes
     constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
-    constexpr bool kThroughOut = kMode == kWeights && sizeof(T) == 4;  // segments are added up in dw itself
-    constexpr int seg_chunks = kThroughOut || kForm == kLong ? kSegment<kMode, T> : 0x7FFFFFFF;
+    // where the accumulator ends that begins at chunk c
+    const auto segment_end = [&](int32_t c, int32_t end) {
+        if (kForm != kLong) return end;
+        const bool low = p.parts == 2 && c < p.chunks;
+        const int32_t most = low ? kLowSegment : kSegment<kMode, T>, stop = low && p.chunks < end ? p.chunks : end;
+        return stop - c > most ? c + most : stop;
+    };
     constexpr uint32_t kBack = kForm == kLong ? 1 : 2;  // accumulators in use
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
@@ -413,11 +422,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int32_t c = it.c0; c < it.c1; ++c) {
                     if (!(ok = mbar_wait(empty + 8 * s, turn, &failed))) break;
                     const uint32_t dst = base + s * stage, bar = lead_full + 8 * s;
-                    const bool second = (kMode == kWeights || kMode == kInputs) && c >= p.chunks;
-                    const int32_t k = (second ? c - p.chunks : c) * kK;
+                    const bool low = (kMode == kWeights || kMode == kInputs) && p.parts == 2 && c < p.chunks;
+                    const int32_t k = ((kMode == kWeights || kMode == kInputs) && p.parts == 2 && !low ? c - p.chunks : c) * kK;
                     if (rank == 0) mbar_expect_tx(full + 8 * s, a_bytes * (1 + p.second) + 2 * tile_n * kK);
                     if (kMode == kWeights) {  // the library's own copies: their rows are whole columns of 128 bytes
-                        tma_load_columns_pair(dst, second ? &map_c : &map_a, bar, a >> 6, k);
+                        tma_load_columns_pair(dst, low ? &map_c : &map_a, bar, a >> 6, k);
                         tma_load_columns_pair(dst + a_bytes, &map_b, bar, b >> 6, k);
                     } else {
                         if (kMnA) {
@@ -426,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else if (rank == 0 || p.second) {
                             tma_load_2d_pair(dst, &map_a, bar, k, a);
                         }
-                        tma_load_2d_pair(dst + a_bytes, kMode == kInputs && second ? &map_c : &map_b, bar, k, b);
+                        tma_load_2d_pair(dst + a_bytes, kMode == kInputs && low ? &map_c : &map_b, bar, k, b);
                     }
                     issued = issued < static_cast<int>(stages) ? issued + 1 : static_cast<int>(stages);
                     if (++s == stages) s = 0, turn ^= 1;
@@ -445,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Item it = item_of(p, i);
             for (int64_t n = it.n0; n < it.n1; ++n) {
                 for (int32_t c0 = it.c0; c0 < it.c1; ++seq) {
-                    const int32_t c1 = it.c1 - c0 > seg_chunks ? c0 + seg_chunks : it.c1;
+                    const int32_t c1 = segment_end(c0, it.c1);
                     const uint32_t acc = tmem + (kForm == kLong ? 0 : (seq & 1) * kTile);
                     if (seq >= kBack) mbar_wait_cluster(drained + 8 * ((seq - kBack) & 1), ((seq - kBack) >> 1) & 1, &failed);
                     for (int32_t c = c0; c < c1; ++c) {
@@ -495,20 +504,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 r.target = p.target[lane_at];
                 r.lse = p.lse[lane_at], r.weight = p.weight ? p.weight[lane_at] : 1.0f;
             }
-            // dw: the pieces that are added to the tile of batch j: the addend's, or of the sum so far
+            // dw: the addend's pieces of batch j of the tile
             uint4 pieces[kTilePieces<T>];
-            const auto fetch_pieces = [&](int64_t n, int j, bool later) {
+            const auto fetch_pieces = [&](int64_t n, int j) {
                 const int64_t row0 = lane_at - lane, left = p.cols - row0, col = n * tile_n + j * 32;
-                const T *c = later ? static_cast<const T *>(p.out) + row0 * p.ld_out + col
-                                   : p.addend ? static_cast<const T *>(p.addend) + row0 * p.ld_addend + col : nullptr;
-                load_pieces(pieces, lane, c, later ? p.ld_out : p.ld_addend, left < 32 ? static_cast<int>(left) : 32, p.hidden - col);
+                const T *c = p.addend ? static_cast<const T *>(p.addend) + row0 * p.ld_addend + col : nullptr;
+                load_pieces(pieces, lane, c, p.ld_addend, left < 32 ? static_cast<int>(left) : 32, p.hidden - col);
             };
             for (int64_t n = it.n0; n < it.n1; ++n) {
                 for (int32_t c0 = it.c0; c0 < it.c1; ++seq) {
-                    const int32_t c1 = it.c1 - c0 > seg_chunks ? c0 + seg_chunks : it.c1;
-                    const uint32_t buf = seq & 1, from = lanes + (kForm == kLong ? 0 : buf * kTile), so_far = lanes + kTile;
-                    const bool later = kThroughOut && c0 > it.c0;
-                    if (kMode == kWeights && p.by_16 && (kThroughOut || c1 == it.c1)) fetch_pieces(n, half, later);
+                    const int32_t c1 = segment_end(c0, it.c1);
+                    const uint32_t buf = seq & 1, so_far = lanes + kTile, from = kForm == kLong ? so_far : lanes + buf * kTile;
+                    if (kMode == kWeights && kForm != kLong && p.by_16) fetch_pieces(n, half);
                     mbar_wait(acc_full + 8 * buf, (seq >> 1) & 1, &failed);
                     __syncwarp();
                     tc_fence_after();
@@ -516,34 +523,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_before();
                         if (lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
                     }
-                    // 32 columns of the tile's sums
-                    const auto load_columns = [&](float (&v)[32], int column) {
-                        tc_load32(v, from + column);
-                        if (kForm == kLong && c0 > it.c0) {
-                            float more[32];
-                            tc_load32(more, so_far + column);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] += more[e];
-                        } else {
-                            tc_wait_ld();
-                        }
-                    };
-                    if (kForm == kLong && c1 < it.c1) {  // each column by the warp that takes the whole sum's
+                    if (kForm == kLong && half < batches) {  // each column by the warp that takes the whole sum's
 #pragma unroll 1
-                        for (int j = 0; j < batches; ++j) {
-                            if (((wide ? j >> 1 : j) & 1) != half) continue;
-                            float v[32];
-                            load_columns(v, j * 32);
-                            tc_store32(so_far + j * 32, v);
+                        for (int u = 0; u < 2; ++u) {  // two batches at a time: registers
+                            float v[2][32];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) tc_load32(v[i], lanes + (wide ? 2 * half + 4 * u + i : half + 4 * u + 2 * i) * 32);
+                            tc_wait_ld();
+                            if (u == 1) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t to = so_far + (wide ? 2 * half + 4 * u + i : half + 4 * u + 2 * i) * 32;
+                                if (c0 > it.c0) {
+                                    float more[32];
+                                    tc_load32(more, to);
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) v[i][e] += more[e];
+                                }
+                                tc_store32(to, v[i]);
+                            }
                         }
                         tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (half < batches && lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
+                    }
+                    if (kForm == kLong && c1 < it.c1) {
                         c0 = c1;
                         continue;
                     }
+                    if (kMode == kWeights && kForm == kLong && p.by_16) fetch_pieces(n, half);  // registers: only now
                     if (wide) {
 #pragma unroll 1
                         for (int q = half; q < batches / 2; q += 2) {
@@ -553,8 +564,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int u = 0; u < 2; ++u) {
                                 __syncwarp();
                                 float v[32];
-                                load_columns(v, q * 64 + u * 32);
-                                if (u == 1 && q + 2 >= batches / 2) {
+                                tc_load32(v, from + q * 64 + u * 32);
+                                tc_wait_ld();
+                                if (kForm != kLong && u == 1 && q + 2 >= batches / 2) {
                                     tc_fence_before();
                                     __syncwarp();
                                     if (lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
@@ -587,8 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = half; j < batches && !wide; j += 2) {
                         __syncwarp();
                         float v[32];
-                        load_columns(v, j * 32);
-                        if (j + 2 >= batches) {
+                        tc_load32(v, from + j * 32);
+                        tc_wait_ld();
+                        if (kForm != kLong && j + 2 >= batches) {
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive_cluster(lead_drained + 8 * buf);
@@ -614,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else if (kMode == kWeights) {
                             const int64_t row0 = lane_at - lane, left = p.cols - row0;
                             if (left <= 0 || col >= p.hidden) continue;  // all lanes
-                            if (p.by_tma && (!kThroughOut || c1 - c0 == it.c1 - it.c0)) {
+                            if (p.by_tma) {
                                 if (lane == 0) tma_store_wait_read<0>();
                                 __syncwarp();
                                 stage_row(staging, lane, v);
@@ -630,15 +643,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 uint4 mine[kTilePieces<T>];
 #pragma unroll
                                 for (int q = 0; q < kTilePieces<T>; ++q) mine[q] = pieces[q];
-                                if (j + 2 < batches) fetch_pieces(n, j + 2, later);
+                                if (j + 2 < batches) fetch_pieces(n, j + 2);
                                 store_pieces(staging, lane, static_cast<T *>(p.out) + row0 * p.ld_out + col, p.ld_out, mine,
                                              left < 32 ? static_cast<int>(left) : 32, p.hidden - col);
                             } else {
                                 stage_row(staging, lane, v);
                                 __syncwarp();
                                 T *d = static_cast<T *>(p.out) + row0 * p.ld_out + col;
-                                const T *c = later ? d : p.addend ? static_cast<const T *>(p.addend) + row0 * p.ld_addend + col : nullptr;
-                                store_rows(staging, lane, d, p.ld_out, c, later ? p.ld_out : p.ld_addend, left < 32 ? static_cast<int>(left) : 32,
+                                const T *c = p.addend ? static_cast<const T *>(p.addend) + row0 * p.ld_addend + col : nullptr;
+                                store_rows(staging, lane, d, p.ld_out, c, p.ld_addend, left < 32 ? static_cast<int>(left) : 32,
                                            col + lane < p.hidden);
                             }
                         } else if (const int64_t left = p.rows - col; lane_at < p.hidden && left > 0) {
@@ -793,9 +806,9 @@ int launch(const VocabParams &p, const CUtensorMap &a, const CUtensorMap &b, con
 template <int kMode, typename T>
 int launch_form(const VocabParams &p, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &c, const CUtensorMap &d,
                 cudaStream_t stream) {
-    const int64_t longest = p.items > 0 ? static_cast<int64_t>(p.chunks) * p.parts : ceil_div(static_cast<int64_t>(p.chunks) * p.parts, int64_t{p.splits});
-    if constexpr (kMode != kWeights || sizeof(T) == 2)
-        if (longest > kSegment<kMode, T>) return launch<kMode, T, kLong>(p, a, b, c, d, stream);
+    const int64_t of_split = ceil_div(static_cast<int64_t>(p.chunks) * p.parts, int64_t{p.splits});
+    const int64_t longest = p.items > 0 ? p.chunks : std::min(int64_t{p.chunks}, of_split);
+    if (longest > kSegment<kMode, T>) return launch<kMode, T, kLong>(p, a, b, c, d, stream);
     if constexpr (kMode == kGradient)
         if (p.loss) return launch<kMode, T, kSure>(p, a, b, c, d, stream);
     return launch<kMode, T, kPlain>(p, a, b, c, d, stream);

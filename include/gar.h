@@ -839,9 +839,9 @@ int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t ldw, int32
  * The vocabulary is taken in pieces, their logits computed again.  g is rounded to
  * bf16 for the products (a bf16 dx or dw is 2.4e-3 from the exact one in the 2-norm, its
  * own rounding 1.7e-3 of it); for an fp32 dw it is the sum of two bf16 values (2^-17 of
- * each g; 4e-6 in the 2-norm where g x has both signs), at twice that product's cost.  Sums are fp32,
- * those that the tensor cores form over no more than 8192 terms of an fp32 dw (of one
- * sign: 3e-5 of it too small) and 32768 of dx and a bf16 dw (1.6e-4).
+ * each g; 4e-6 in the 2-norm), at twice that product's cost.  Sums are fp32, those that the
+ * tensor cores form over no more than 2048 rows of an fp32 dw (of one sign: 3e-6 of it too
+ * small) and 32768 terms of dx and a bf16 dw (1.6e-4).
  *   dx           device, out, [rows, hidden] bf16, row stride lddx, or NULL
  *   dw           device, out, [vocab, hidden] fp32 or bf16 (dw_type), row stride
  *                lddw, or NULL

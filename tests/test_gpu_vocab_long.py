@@ -193,3 +193,27 @@ def test_segments_of_an_fp32_dw(env, hidden, pad, addend):
     assert ((dw.double() - want).abs() <= tol).all()
     if addend != "in place":  # and as closely as random signs allow: a segment left out or taken twice shows
         assert (dw.double() - want).norm() <= 1e-4 * (want - (before.double() if add is not None else 0.0)).norm()
+
+
+@pytest.mark.parametrize("rows", [4096, 16384])
+def test_small_terms_behind_a_large_one_of_an_fp32_dw(env, rows):
+    """Row 0 with weight 1, all others with 7/8 2^-27, all their logits 0 and their x 1: every term of a dw that is no
+    target's is positive, 2^-8 and 7/8 2^-35.  16 of the small ones are below one step of the large one and are lost behind
+    it, but in its accumulator alone, 2048 rows: rounding toward zero, no sum of positive terms falls below a part of it.
+    So what is missing is at most those 2047 terms; the exponentials' 2^-21 and the additions' 4 u besides."""
+    torch, g = env
+    x = torch.ones((rows, 64), device="cuda").bfloat16()
+    w = torch.zeros((256, 64), device="cuda").bfloat16()
+    target = torch.full((rows,), 5, dtype=torch.int32, device="cuda")
+    small = 0.875 * 2.0 ** -27
+    weight = torch.full((rows,), small, device="cuda")
+    weight[0] = 1.0
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    dw = torch.empty((256, 64), device="cuda")
+    ws = workspace(torch, g, rows, 256, 64, torch.float32)
+    g.gar_vocab_loss(x, w, target, loss, lse, ws, weight=weight)
+    g.gar_vocab_grad(x, w, target, lse, None, dw, ws, weight=weight)
+    torch.cuda.synchronize()
+    want = (1.0 + (rows - 1) * small) / 256
+    got = torch.cat([dw[:5], dw[6:]]).double()
+    assert (got - want).abs().max().item() <= (2047 * small + 2.0 ** -21 + 4 * U) / 256
