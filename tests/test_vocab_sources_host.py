@@ -51,14 +51,17 @@ def test_no_loop_ends_early_for_a_wait():
 
 
 def test_every_segment_hands_its_accumulator_back_once():
-    """Each way through an epilogue's turn has one arrival for the products that wait for it: a half without columns, a
-    segment of a longer sum, the two orders of the last one."""
+    """Each way through an epilogue's turn has one arrival for the products that wait for it: a half without columns; a
+    segment of a longer sum, behind the second of its two reads; the last batch else, in either order of batches."""
     text = roles()["2"]
     arrivals = [m.start() for m in re.finditer(r"mbar_arrive_cluster\(lead_drained \+ 8 \* buf\);", text)]
     heads = [" ".join(conditions(text, at)) for at in arrivals]
     assert len(arrivals) == 4
     assert "half >= batches" in heads[0]
-    assert "kForm == kLong && c1 < it.c1" in heads[1] and "half < batches" in text[arrivals[1] - 60:arrivals[1]]
-    assert "u == 1 && q + 2 >= batches / 2" in heads[2] and "j + 2 >= batches" in heads[3]
-    between = text[arrivals[1]:arrivals[2]]
-    assert between.index("c0 = c1;") < between.index("continue;")
+    assert "kForm == kLong && half < batches" in heads[1] and "u == 1" in heads[1]
+    assert "kForm != kLong && u == 1 && q + 2 >= batches / 2" in heads[2]
+    assert "kForm != kLong && j + 2 >= batches" in heads[3]
+    for at in arrivals:  # what was read has arrived
+        assert text.rindex("tc_fence_before();", 0, at) > text.rindex("tc_fence_after();", 0, at)
+    for at in arrivals[1:]:
+        assert text.rindex("tc_wait_ld();", 0, at) > text.rindex("tc_load32(", 0, at)
