@@ -69,9 +69,9 @@ constexpr int kShared = 224 * 1024, kSmem = 1024 + kShared;
 // one with a large term ahead, is too small by what grows with its length: 3e-5 of it at 8192 k, which logits are held
 // to; 1.6e-4 at 32768, beside the 2e-3 of a bf16 result's own rounding (uncut: lse 6e-3 at 2^20 k, a bf16 dw of 4M rows
 // 2.6e-2); 3e-6 at 2048, of an fp32 dw (of 4096 rows, random signs, 1.3e-5 in the 2-norm uncut, 3.6e-6 so; at 1024 2.9e-6).
-// Longer sums are added up by the epilogue in tensor memory (kLong): an fp32 gradient of 4096 x 131072 x 4096 takes 10.6 ms,
-// 10.2 uncut (10.8 with segments of 1024), the loss of 2048 x 32000 x 16384 1260 us, 1220 uncut.  Of two parts of g the
-// low one goes first, when the sums are small: it needs no more segments than a bf16 result.
+// Longer sums are added up by the epilogue in tensor memory (kLong): an fp32 gradient of 4096 x 131072 x 4096 takes 10.5 ms,
+// 10.3 uncut, the loss of 2048 x 32000 x 16384 1260 us, 1220 uncut.  Of two parts of g the
+// low one goes first, while the sum is small: its chunks count no more than those of a bf16 result.
 template <int kMode, typename T>
 constexpr int kSegment = (kMode == kWeights && sizeof(T) == 4 ? 2048 : kMode == kWeights || kMode == kInputs ? 32768 : 8192) / kK;
 constexpr int kLowSegment = 32768 / kK;
@@ -366,9 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // where the accumulator ends that begins at chunk c
     const auto segment_end = [&](int32_t c, int32_t end) {
         if (kForm != kLong) return end;
-        const bool low = p.parts == 2 && c < p.chunks;
-        const int32_t most = low ? kLowSegment : kSegment<kMode, T>, stop = low && p.chunks < end ? p.chunks : end;
-        return stop - c > most ? c + most : stop;
+        int32_t stop = c + kSegment<kMode, T>;
+        if (p.parts == 2 && c < p.chunks) stop = p.chunks - c > kLowSegment ? c + kLowSegment : p.chunks + kSegment<kMode, T>;
+        return stop < end ? stop : end;
     };
     constexpr uint32_t kBack = kForm == kLong ? 1 : 2;  // accumulators in use
     extern __shared__ uint8_t raw[];
