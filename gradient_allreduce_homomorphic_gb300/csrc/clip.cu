@@ -219,7 +219,8 @@ __device__ __forceinline__ void scale_tile(const T *x, T *y, int64_t n, int64_t 
     constexpr int V = 16 / sizeof(T);
     const Range r = tile_range(x, n, i);
     if (r.begin >= r.end) return;
-    if ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) & 15) {  // no 16-byte line in common
+    // no 16-byte line in common: element by element (one tensor of 45M values, with its norm, fp32 330 us for 94, bf16 268 for 54)
+    if ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) & 15) {
         for (int64_t e = r.begin + threadIdx.x; e < r.end; e += kThreads) store_f32(y + e, load_f32(x + e) * c);
         return;
     }

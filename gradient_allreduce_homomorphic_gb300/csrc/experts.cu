@@ -13,7 +13,9 @@
 //
 // Moving rows is bound by HBM: 8 x 4096 tokens to 8 experts each, 4096 bf16, 371 us
 // there (6.5 TB/s; each token's row read once), 379 us back (6.4 TB/s), 706 us for the
-// gradient of that (6.5 TB/s: dy and dweight from one read of dout and y).
+// gradient of that (6.5 TB/s: dy and dweight from one read of dout and y).  Rows that do
+// not start on 16 bytes go element by element: to 4 experts each, 4095 bf16, 399 us there
+// (4096: 207), 592 back (212), 565 for the gradient (359).
 #include <algorithm>
 #include <atomic>
 #include <cmath>

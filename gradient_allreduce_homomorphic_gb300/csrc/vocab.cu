@@ -10,11 +10,11 @@
 // running maximum and sum of all logits but the target's over a run of vocabulary
 // tiles; the runs' pairs are joined by a second, small kernel.  With r the sum's
 // logarithm the loss is log(1 + exp(r - z[target])): near 0, where the target has
-// almost all of the probability, the rest is a sum of its own and keeps its digits.  The gradient goes piece by piece of the
-// vocabulary: the piece's logits again, g from them in the epilogue (bf16, in
-// the workspace), then the piece's rows of dw and its share of dx.  So a loss
-// and its gradient take four products where keeping the logits would take
-// three, and no more than a piece of g exists at a time.
+// almost all of the probability, the rest is a sum of its own and keeps its digits.
+// The gradient goes piece by piece of the vocabulary: the piece's logits again, g from
+// them in the epilogue (bf16, in the workspace), then the piece's rows of dw and its
+// share of dx.  So a loss and its gradient take four products where keeping the logits
+// would take three, and no more than a piece of g exists at a time.
 //
 // g is rounded to bf16 as an operand of the products: of a bf16 gradient that is
 // another error of the size of the result's own rounding (dx and a bf16 dw 2.4e-3 from
@@ -22,7 +22,7 @@
 // the sum of two bf16 values (16 bits and more of it), a product of twice the
 // length, so that its error is what the fp32 sums leave; a caller who asks for them
 // (parts) has the same of dx and a bf16 dw, which then are the exact ones rounded but
-// for one value in thousands.
+// for one value in some hundreds.
 //
 // All products run on one kernel of persistent CTA pairs (cta_group::2): tiles
 // of 256 x 256, two accumulators in tensor memory, so that a tile's epilogue
@@ -32,12 +32,13 @@
 // nothing is transposed in memory.
 //
 // Bound by the tensor cores at the clock that the power limit leaves: 4096 x 16384
-// x 4096 the loss 303 us (1810 TFLOP/s, tensor pipe active in 97 % of the cycles,
-// SM clock 1.75 GHz of 2.07), logits and g 295, dw 288, dx 280 us (93 to 96 %); 4096 x
-// 131072 x 4096 loss and gradient 10.3 ms one after another (1710 TFLOP/s; 2.2 and 6.9
-// in short runs).  With few rows bound by the read of w: the loss of 16 x 131072 x 1024
-// 55 us (4.8 TB/s), of 64 x 32000 x 1024 18.9 us, 6 of them the kernel's beginning and
-// end.
+// x 4096 the loss 297 us (1850 TFLOP/s, tensor pipe active in 97 % of the cycles,
+// SM clock 1.76 GHz of 2.07), logits and g 285, dw 280 (fp32: 612), dx 274 us (92 to 95 %;
+// fp32 dw 86); 4096 x 131072 x 4096 loss and gradient 10.2 ms one after another (1720
+// TFLOP/s).  With few rows bound by the read of w: the loss of 16 x 131072 x 1024 53 us
+// (5.0 TB/s), of 64 x 32000 x 1024 19.1 us, 6 of them the kernel's beginning and end; the
+// gradient of 16 x 131072 x 1024 190 us reads w twice (119 us of bytes).  With few chunks a
+// tile bound by the exponents: the loss of 4096 x 131072 x 64 214 us, 36 of them products.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -70,12 +71,11 @@ constexpr int kShared = 224 * 1024, kSmem = 1024 + kShared;
 // to; 1.6e-4 at 32768, beside the 2e-3 of a bf16 result's own rounding (uncut: lse 6e-3 at 2^20 k, a bf16 dw of 4M rows
 // 2.6e-2); 3e-6 at 2048, of an fp32 dw (of 4096 rows, random signs, 1.3e-5 in the 2-norm uncut, 3.6e-6 so; at 1024 2.9e-6).
 // Longer sums are added up by the epilogue in tensor memory (kLong): an fp32 gradient of 4096 x 131072 x 4096 takes 10.5 ms,
-// 10.3 uncut, the loss of 2048 x 32000 x 16384 1260 us, 1220 uncut.  Of two parts of g the
-// low one goes first, while the sum is small: its chunks count no more than those of a bf16 result.
+// 10.3 uncut, the loss of 2048 x 32000 x 16384 1220 us, 1160 uncut.  Of two parts of g the low one goes first, while the
+// sum is small: its chunks count no more than those of a bf16 result.
 template <int kMode, typename T>
 constexpr int kSegment = (kMode == kWeights && sizeof(T) == 4 ? 2048 : kMode == kWeights || kMode == kInputs ? 32768 : 8192) / kK;
 constexpr int kLowSegment = 32768 / kK;
-
 
 struct VocabParams {
     int64_t items;       // whole tiles or runs, handed out in order
@@ -961,7 +961,7 @@ int copy_live_rows(VocabParams p, const uint16_t *x, int64_t ldx, uint16_t *to, 
 }
 // Rows of x that do not start on 128 bytes load at half the rate (two lines for each
 // one's 128 bytes): copied to such that do where the logits take long enough (loss of
-// 1003 x 50001 x 1000 103 us, 78 with the copy's 4; it pays from about 25 GFLOP).
+// 1003 x 50001 x 1000 103 us, 78 with the copy's 4; it pays from about 50 GFLOP).
 bool copy_pays(const uint16_t *x, int64_t ldx, const VocabParams &p) {
     return (!aligned(x, 128) || ldx % 64) && static_cast<double>(p.rows) * p.vocab * p.hidden > 2.5e10;
 }

@@ -848,7 +848,8 @@ int gar_vocab_loss(const void *x, int64_t ldx, const void *w, int64_t ldw, int32
  *   addend       device, of dw's type, added before the rounding; NULL: none; may
  *                be dw (same row stride)
  * A row that did not count when lse was written must not count now.  Outputs must
- * not overlap x, w or one another.  With no rows dw is the addend or 0.  Other arguments and errors as for gar_vocab_loss.
+ * not overlap x, w or one another.  With no rows dw is the addend or 0.  Other
+ * arguments and errors as for gar_vocab_loss.
  * exp(z - lse) is off by what lse's own rounding leaves, 2^-24 |lse| of itself (4e-6 at
  * 64 .. 128).  Of the target's g that is not a part of it but of 1: a sure target's, its
  * loss near 0, loses its digits, and one of 1e-6 is lost at an lse near 100.
@@ -864,7 +865,7 @@ int gar_vocab_grad(const void *x, int64_t ldx, const void *w, int64_t ldw, int32
  *   parts        bf16 values whose sum g is taken as.  0: as in gar_vocab_grad, one for dx
  *                and a bf16 dw, two for an fp32 dw.  2: two for all of them, each at twice
  *                that product's cost: dx and a bf16 dw are then the exact ones
- *                rounded but for one value in thousands (the workspace of an fp32 dw).
+ *                rounded but for one value in some hundreds (the workspace of an fp32 dw).
  *                1: one (not for an fp32 dw) */
 int gar_vocab_grad_with_loss(const void *x, int64_t ldx, const void *w, int64_t ldw, int32_t dtype, const int32_t *target,
                              const float *weight, int64_t rows, int64_t vocab, int64_t hidden, const float *loss, const float *lse,
