@@ -1025,7 +1025,8 @@ int gradient(const VocabParams &p, const Plan &how, const uint16_t *x, int64_t l
             q.addend = addend ? addend + first * ld_addend : nullptr, q.ld_addend = ld_addend;
             q.by_16 = aligned(q.out, 16) && lddw * sizeof(T) % 16 == 0 && hidden * sizeof(T) % 16 == 0 &&
                       (!addend || (aligned(q.addend, 16) && ld_addend * sizeof(T) % 16 == 0));
-            q.by_tma = !addend && aligned(q.out, 16) && lddw * sizeof(T) % 16 == 0;
+            // a tile that ends inside 16 bytes of a row is not TMA's: it writes them whole, past the row's end
+            q.by_tma = !addend && aligned(q.out, 16) && lddw * sizeof(T) % 16 == 0 && hidden * sizeof(T) % 16 == 0;
             if (q.by_tma) {
                 if (int rc = sizeof(T) == 4 ? encode_store_f32(&to, q.out, hidden, cols, lddw) : encode_store(&to, q.out, hidden, cols, lddw, true))
                     return rc;
